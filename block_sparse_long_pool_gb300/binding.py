@@ -29,6 +29,7 @@ SPARSE_ERR_CUDA = -3
 SPARSE_ERR_TIMEOUT = -4
 SPARSE_ERR_NOT_READY = -5
 SPARSE_ERR_BAD_INDEX = -6
+SPARSE_ERR_NO_PAGES = -7
 SPARSE_ATTN_BLOCKS_READY = 1
 SPARSE_ATTN_STREAM_K = 2
 SPARSE_ATTN_TENSOR_MEMORY = 16
@@ -67,6 +68,11 @@ SIGNATURES = {
     "sparse_nsa_compress": (_I, [_P, _P, _LL, _I, _I, _LL, _I, _I, _I, _P, _P, _I, _P]),
     "sparse_nsa_select": (_I, [_P, _P, _I, _I, _I, _P, _I, _I, _I, _I, _F, _I, _I, _I, _P, _P, _I, _P, _P]),
     "sparse_decode_attn_nsa_workspace_size": (_SZ, [_I, _I, _I]),
+    "sparse_page_plan": (_I, [_P, _P, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P]),
+    "sparse_paged_append_f8": (_I, [_P, _P, _I, _I, _P, _P, _LL, _LL, _P, _I, _P, _I, _I, _P, _P, _P, _P]),
+    "sparse_paged_decode_attn_f8": (_I, [_P, _P, _P, _I, _P, _I, _P, _P, _I, _P, _I, _I, _I, _F, _P, _P, _P, _SZ,
+                                         _P, _P]),
+    "sparse_paged_decode_attn_f8_workspace_size": (_SZ, [_I, _I, _I]),
 }
 
 
@@ -466,3 +472,146 @@ def sparse_prefill_select(F, ktil, seq_len, n_init: int, n_local: int, k: int, i
     rc = load().sparse_prefill_select(_ptr(F), T_cap, _ptr(ktil), N_cap, _ptr(seq_len), B, H_kv, n_init, n_local, k,
                                       _ptr(idx_out), _ptr(count_out), k_tot, _ptr(status), _stream(stream))
     _check(rc, "sparse_prefill_select")
+
+
+# ---------------------------------------------------------------- the paged 8-bit cache
+
+_F8 = torch.float8_e4m3fn
+
+
+def _on(dev, **tensors):
+    """Every tensor on ``dev``: (tensor, dtype, shape) each, or None."""
+    for name, spec in tensors.items():
+        if spec is None:
+            continue
+        t, dtype, shape = spec
+        if isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.shape == shape and t.is_contiguous():
+            continue
+        _need(t, name, dtype, shape=shape)
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _call(name, dev, stream, *args):
+    """The C entry point on ``dev``, which need not be the current device."""
+    fn = getattr(load(), name)
+    if dev.index == torch.cuda.current_device():
+        rc = fn(*args, stream.cuda_stream if stream is not None else torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream.cuda_stream if stream is not None else torch.cuda.current_stream().cuda_stream)
+    _check(rc, name)
+
+
+def _device_of(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _status_spec(status):
+    return None if status is None else (status, torch.int32, (1,))
+
+
+def sparse_page_plan(seq_len, n_new, block_table, free_pages, n_free, cu_new, start, seq_len_out, n_free_out, slot_map,
+                     tok_req, tok_pos, status=None, stream=None):
+    """Block tables and slot maps on the GPU, all int32: requests of seq_len [B] tokens get
+    n_new [B] more (negative: the request ends and its pages are returned); pages go from
+    the list free_pages [n_pages] (the first n_free [1]) into block_table [B][max_blocks].
+    Writes cu_new [B + 1], start [B] (-1: not granted), seq_len_out [B], n_free_out [1] (the
+    last two may be seq_len and n_free themselves) and slot_map, tok_req, tok_pos [n_tok]."""
+    dev = _device_of(block_table, "block_table")
+    i32 = torch.int32
+    B, max_blocks = block_table.shape
+    n_pages, n_tok = free_pages.numel(), slot_map.numel()
+    _on(dev, block_table=(block_table, i32, (B, max_blocks)), seq_len=(seq_len, i32, (B,)), n_new=(n_new, i32, (B,)),
+        free_pages=(free_pages, i32, (n_pages,)), n_free=(n_free, i32, (1,)), cu_new=(cu_new, i32, (B + 1,)),
+        start=(start, i32, (B,)), seq_len_out=(seq_len_out, i32, (B,)), n_free_out=(n_free_out, i32, (1,)),
+        slot_map=(slot_map, i32, (n_tok,)), tok_req=(tok_req, i32, (n_tok,)), tok_pos=(tok_pos, i32, (n_tok,)),
+        status=_status_spec(status))
+    _call("sparse_page_plan", dev, stream, seq_len.data_ptr(), n_new.data_ptr(), B, block_table.data_ptr(), max_blocks,
+          free_pages.data_ptr(), n_pages, n_free.data_ptr(), cu_new.data_ptr(), start.data_ptr(), seq_len_out.data_ptr(),
+          n_free_out.data_ptr(), slot_map.data_ptr(), tok_req.data_ptr(), tok_pos.data_ptr(), n_tok, _addr(status))
+
+
+def _new_rows(t, name, dev, n_tok, H_kv):
+    """Token stride of k_new / v_new [n_tok][H_kv][128], whose tokens may be apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.shape != (n_tok, H_kv, D):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n_tok, H_kv, D)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    step, head, dim = t.stride()
+    if dim != 1 or (head != D and H_kv > 1):
+        raise ValueError(f"{name}: the values of a token must be contiguous")
+    return step if n_tok > 1 else max(step - step % 8, H_kv * D)
+
+
+def sparse_paged_append_f8(kv_pages, kv_scale, k_new, v_new, slot_map, ktil=None, tok_req=None, tok_pos=None,
+                           status=None, stream=None):
+    """Round k_new / v_new [n_tok][H_kv][128] bf16 (parts of wider rows are taken as they are)
+    to e4m3 and write them to slot_map [n_tok] of kv_pages [n_pages][H_kv][2][64][128]
+    (torch.float8_e4m3fn), with kv_scale [n_pages][H_kv][2] fp32; with ktil
+    [B][H_kv][N_cap][128], tok_req and tok_pos [n_tok], update the compressed keys."""
+    dev = _device_of(kv_pages, "kv_pages")
+    n_pages, H_kv = kv_pages.shape[:2]
+    n_tok = slot_map.numel()
+    i32 = torch.int32
+    _on(dev, kv_pages=(kv_pages, _F8, (n_pages, H_kv, 2, BLK, D)), kv_scale=(kv_scale, torch.float32, (n_pages, H_kv, 2)),
+        slot_map=(slot_map, i32, (n_tok,)), status=_status_spec(status))
+    ks, vs = _new_rows(k_new, "k_new", dev, n_tok, H_kv), _new_rows(v_new, "v_new", dev, n_tok, H_kv)
+    B = N_cap = 0
+    if ktil is not None:
+        if tok_req is None or tok_pos is None:
+            raise ValueError("ktil needs tok_req and tok_pos")
+        B, N_cap = ktil.shape[0], ktil.shape[2]
+        _on(dev, ktil=(ktil, torch.float32, (B, H_kv, N_cap, D)), tok_req=(tok_req, i32, (n_tok,)),
+            tok_pos=(tok_pos, i32, (n_tok,)))
+    _call("sparse_paged_append_f8", dev, stream, kv_pages.data_ptr(), kv_scale.data_ptr(), n_pages, H_kv, k_new.data_ptr(),
+          v_new.data_ptr(), ks, vs, slot_map.data_ptr(), n_tok, _addr(ktil), B, N_cap, _addr(tok_req), _addr(tok_pos),
+          _addr(status))
+
+
+def sparse_paged_decode_attn_f8_workspace_size(B: int, H_q: int, H_kv: int) -> int:
+    """Bytes of the workspace of sparse_paged_decode_attn_f8 (0: invalid sizes)."""
+    return int(load().sparse_paged_decode_attn_f8_workspace_size(B, H_q, H_kv))
+
+
+def paged_workspace(B: int, H_q: int, H_kv: int, device="cuda"):
+    """A zeroed workspace tensor for sparse_paged_decode_attn_f8."""
+    with torch.cuda.device(device):
+        n = sparse_paged_decode_attn_f8_workspace_size(B, H_q, H_kv)
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def sparse_paged_decode_attn_f8(Q, kv_pages, kv_scale, block_table, seq_len, O, workspace, blk_idx=None, count=None,
+                                lse=None, scale: float = 0.0, status=None, stream=None):
+    """O [B][H_q][128] = attention of Q over the pages that block_table [B][max_blocks] names:
+    every block of each request's seq_len [B] tokens, or the logical blocks blk_idx
+    [B][H_kv][k_tot] with count [B][H_kv]."""
+    dev = _device_of(kv_pages, "kv_pages")
+    n_pages, H_kv = kv_pages.shape[:2]
+    B, max_blocks = block_table.shape
+    H_q = Q.shape[1]
+    i32, f32, b16 = torch.int32, torch.float32, torch.bfloat16
+    k_tot = 0
+    if blk_idx is not None:
+        if count is None:
+            raise ValueError("blk_idx needs count")
+        k_tot = blk_idx.shape[2]
+        _on(dev, blk_idx=(blk_idx, i32, (B, H_kv, k_tot)), count=(count, i32, (B, H_kv)))
+    _on(dev, Q=(Q, b16, (B, H_q, D)), kv_pages=(kv_pages, _F8, (n_pages, H_kv, 2, BLK, D)),
+        kv_scale=(kv_scale, f32, (n_pages, H_kv, 2)), block_table=(block_table, i32, (B, max_blocks)),
+        seq_len=(seq_len, i32, (B,)), O=(O, b16, (B, H_q, D)), workspace=(workspace, torch.uint8, (workspace.numel(),)),
+        lse=None if lse is None else (lse, f32, (B, H_q)), status=_status_spec(status))
+    _call("sparse_paged_decode_attn_f8", dev, stream, Q.data_ptr(), kv_pages.data_ptr(), kv_scale.data_ptr(), n_pages,
+          block_table.data_ptr(), max_blocks, _addr(blk_idx), _addr(count), k_tot, seq_len.data_ptr(), B, H_q, H_kv,
+          float(scale), O.data_ptr(), _addr(lse), workspace.data_ptr(), workspace.numel(), _addr(status))

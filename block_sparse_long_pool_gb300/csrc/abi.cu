@@ -179,6 +179,8 @@ SPARSE_API const char *sparse_status_string(int status)
         return "staging slot not marked ready";
     case SPARSE_ERR_BAD_INDEX:
         return "block id outside the cache (skipped)";
+    case SPARSE_ERR_NO_PAGES:
+        return "a request got no pages";
     default:
         return "unknown status";
     }

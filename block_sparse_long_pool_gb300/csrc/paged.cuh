@@ -1,0 +1,66 @@
+// paged.cuh -- what the paged 8-bit cache's kernels share: e4m3 conversions and the launch.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace {
+
+constexpr int kMaxPages = 1 << 25;   // 64 * page fits an int32 slot
+
+// Two fp32 values to e4m3, round to nearest even, beyond +-448 to +-448, NaN to NaN; `lo`
+// in the low byte.
+__device__ __forceinline__ uint32_t f8x2_pack(float lo, float hi)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t f8x4_pack(float a, float b, float c, float d)
+{
+    return f8x2_pack(a, b) | (f8x2_pack(c, d) << 16);
+}
+
+// Two e4m3 values to f16 (exact: e4m3 has fewer exponents and mantissa bits).
+__device__ __forceinline__ uint32_t f8x2_to_f16x2(uint32_t x)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(x)));
+    return r;
+}
+
+__device__ __forceinline__ float2 f8x2_to_float2(uint32_t x)
+{
+    const uint32_t h = f8x2_to_f16x2(x);
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
+// Four e4m3 values times `ratio`, rounded again.
+__device__ __forceinline__ uint32_t f8x4_scaled(uint32_t w, float ratio)
+{
+    const float2 a = f8x2_to_float2(w), b = f8x2_to_float2(w >> 16);
+    return f8x4_pack(a.x * ratio, a.y * ratio, b.x * ratio, b.y * ratio);
+}
+
+// One launch of a kernel that takes one parameter struct, with programmatic stream
+// serialization: it may be scheduled while the kernel before it drains.
+template <typename Params>
+cudaError_t launch_pdl(const void *kern, dim3 grid, int threads, int smem, const Params *prm, void *stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void *args[] = {const_cast<Params *>(prm)};
+    return cudaLaunchKernelExC(&cfg, kern, args);
+}
+
+}  // namespace

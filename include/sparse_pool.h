@@ -46,7 +46,8 @@ enum {
     SPARSE_ERR_CUDA = -3,          /* a CUDA runtime call failed                       */
     SPARSE_ERR_TIMEOUT = -4,       /* device: a bounded wait gave up                   */
     SPARSE_ERR_NOT_READY = -5,     /* device: a staging slot was not marked ready      */
-    SPARSE_ERR_BAD_INDEX = -6      /* device: a block id outside the cache was skipped */
+    SPARSE_ERR_BAD_INDEX = -6,     /* device: a block id outside the cache was skipped */
+    SPARSE_ERR_NO_PAGES = -7       /* device: a request got no pages (see sparse_page_plan) */
 };
 
 /* Message for a status code (static storage). */
@@ -544,6 +545,119 @@ SPARSE_API int sparse_gather_offloaded(const uint16_t *k_host, const uint16_t *v
                                        int k_tot, int B, int H_kv, uint16_t *k_ring,
                                        uint16_t *v_ring, unsigned *ready_flag, int n_ctas,
                                        int *status, void *stream);
+
+/*
+ * The paged 8-bit cache: three calls that serve requests of their own lengths from one
+ * pool of pages.  The notes have no counterpart; block size, head dimension, compressed
+ * keys and block lists are those of the calls above, so sparse_select_topk and the other
+ * selectors run on it unchanged.
+ *   page         64 tokens of every KV head: kv_pages [n_pages][H_kv][2][64][128] e4m3
+ *                (0: keys, 1: values), one byte an element.
+ *   kv_scale     [n_pages][H_kv][2] fp32: the element's value is e4m3 * scale.
+ *   block table  [B][max_blocks] int32: the page that holds block j (tokens 64 j ..
+ *                64 j + 63) of request b.
+ *   slot         64 * page + row: the place of one token's rows.
+ * A step is sparse_page_plan, then per layer sparse_paged_append_f8, a selector (or none),
+ * and sparse_paged_decode_attn_f8.  All three are launched with programmatic stream
+ * serialization and wait for the kernel before them on the stream before reading anything.
+ */
+
+/*
+ * sparse_page_plan -- block tables and slot maps from request lengths, on the device.
+ * Request b holds seq_len[b] tokens and gets n_new[b] more in this step (0: none); a
+ * negative n_new[b] ends the request.  In this order:
+ *   1. the pages of ended requests (blocks [0, ceil(seq_len / 64))) go onto the end of the
+ *      free list, by request and block; with them the list holds F pages.  The request's
+ *      length becomes 0; its table row is left as it was.
+ *   2. cu_new[b] = the sum of max(n_new, 0) of the requests before b: request b's new tokens
+ *      are rows [cu_new[b], cu_new[b + 1]) of this step's packed rows.
+ *   3. request b needs ceil((seq_len + n_new) / 64) - ceil(seq_len / 64) pages.  It is
+ *      granted if its tokens fit the table (64 max_blocks) and the rows (cu_new[b + 1] <=
+ *      n_tok) and, where it needs pages, the needs up to and including its own (of the
+ *      requests that fit) are at most F.  Pages are taken from the end of the list in
+ *      request and block order and written to the block table.  A request that is not
+ *      granted keeps its length and gets nothing; status reports SPARSE_ERR_NO_PAGES.
+ *   4. row t of a granted request b gets tok_req = b, tok_pos = its position, slot_map = its
+ *      slot; every other row (of requests not granted, and past cu_new[B]) gets -1 in all
+ *      three, which sparse_paged_append_f8 skips.
+ * The result does not depend on timing: no atomics, and pages go out in a fixed order.
+ *   seq_len, n_new   [B] int32.       block_table  [B][max_blocks] int32, entries added.
+ *   free_pages       [n_pages] int32, the first *n_free are the list; entries added.
+ *   n_free           one int32.       cu_new       [B + 1] int32, written.
+ *   start            [B] int32, written: the position of the first new token (the length
+ *                    before the step), 0 for an ended request, -1 for one not granted.
+ *   seq_len_out      [B] int32, n_free_out one int32, written; each may be the buffer that
+ *                    it replaces (seq_len, n_free), for a step captured into a graph.
+ *   slot_map, tok_req, tok_pos  [n_tok] int32, written.
+ *   status           a length outside [0, 64 max_blocks] (the request is not granted; an
+ *                    ended one returns no pages), an *n_free outside [0, n_pages] (clamped),
+ *                    more pages returned than the list holds (dropped) or a page id outside
+ *                    [0, n_pages) (its rows get slot -1) is reported as SPARSE_ERR_BAD_INDEX.
+ * B <= 4096; n_pages and max_blocks <= 2^25; cu_new saturates at 2^31 - 1.
+ */
+SPARSE_API int sparse_page_plan(const int *seq_len, const int *n_new, int B, int *block_table, int max_blocks,
+                                int *free_pages, int n_pages, const int *n_free, int *cu_new, int *start,
+                                int *seq_len_out, int *n_free_out, int *slot_map, int *tok_req, int *tok_pos,
+                                int n_tok, int *status, void *stream);
+
+/*
+ * sparse_paged_append_f8 -- sparse_pool_append for the paged cache: the rows of n_tok tokens
+ * are rounded to e4m3 and written to their slots, with one scale for each (page, head, K or
+ * V), and the compressed keys of the touched blocks are kept.
+ * The tokens of a page are consecutive rows of the call with consecutive slots (as
+ * sparse_page_plan lays them out), at most one such run a page and call; a run that starts
+ * at row r of its page continues the r rows there.  For each head, and for K and V:
+ *   s     = 2^e, e >= -120 the least with max |x| <= 448 * 2^e over the run's finite values;
+ *   scale = s if r = 0, else max(old scale, s);
+ *   new rows  e4m3(x / scale), rounded to nearest even; infinities and NaN become NaN;
+ *   old rows  where the scale grew, e4m3(old * (old scale / scale)): with the power-of-two
+ *             scales that this call writes, exact but for values that become subnormal.
+ * Bytes of the page past the run are left as they were.
+ *   k_new, v_new  [n_tok][H_kv][128] bf16; a token's H_kv * 128 values are contiguous and
+ *                 tokens are k_stride / v_stride elements apart (>= H_kv * 128, a multiple
+ *                 of 8), so both may be parts of one projection's rows.
+ *   slot_map      [n_tok] int32; negative: the row is skipped.  A page past n_pages is
+ *                 skipped and reported (SPARSE_ERR_BAD_INDEX).
+ *   ktil          [B][H_kv][N_cap][128] fp32, or NULL (then B, N_cap, tok_req and tok_pos
+ *                 are not used): the mean of the block's bf16 keys as in sparse_pool_append,
+ *                 for block tok_pos / 64 of request tok_req of the run's first row; a run
+ *                 whose request or block is outside is left out and reported.
+ */
+SPARSE_API int sparse_paged_append_f8(uint8_t *kv_pages, float *kv_scale, int n_pages, int H_kv,
+                                      const uint16_t *k_new, const uint16_t *v_new, long long k_stride,
+                                      long long v_stride, const int *slot_map, int n_tok, float *ktil, int B,
+                                      int N_cap, const int *tok_req, const int *tok_pos, int *status,
+                                      void *stream);
+
+/*
+ * sparse_paged_decode_attn_f8 -- sparse_decode_attn over the paged cache.  For every query
+ * head h of pair p = (b, floor(h/G)):
+ *     O[b][h] = sum_t softmax_t(scale * q_h . (ks k_t)) (vs v_t)
+ * over the tokens t < seq_len[b] of the listed blocks, k_t and v_t the e4m3 rows and ks, vs
+ * the scales of their page.
+ *   blk_idx      [B*H_kv][k_tot] int32 logical block ids with count [B*H_kv] (as
+ *                sparse_select_topk writes them), or NULL: every block of every request
+ *                (count and k_tot are then not used).
+ *   Q, O, lse, scale, seq_len  as for sparse_decode_attn: a row with no token gets O = 0 and
+ *                lse = -inf.
+ *   workspace    sparse_paged_decode_attn_f8_workspace_size() bytes, 16-byte aligned, all
+ *                zero before the first call that uses it; every call leaves its counters
+ *                zero again.  Calls that share a workspace must not run at the same time.
+ * Rows past seq_len in a request's last page are never used, whatever bytes they hold.
+ * Listed blocks are expected to be distinct.  A block past the request's length adds
+ * nothing.  A negative block or one past max_blocks, a page outside [0, n_pages), a count
+ * outside [0, k_tot] (clamped) and a length past 64 max_blocks (clamped) are reported as
+ * SPARSE_ERR_BAD_INDEX; such a block is left out.  The result does not depend on timing.
+ * G = H_q / H_kv <= 16, B * H_kv <= 65535, k_tot <= 2^25.
+ */
+SPARSE_API int sparse_paged_decode_attn_f8(const uint16_t *Q, const uint8_t *kv_pages, const float *kv_scale,
+                                           int n_pages, const int *block_table, int max_blocks,
+                                           const int *blk_idx, const int *count, int k_tot, const int *seq_len,
+                                           int B, int H_q, int H_kv, float scale, uint16_t *O, float *lse,
+                                           void *workspace, size_t workspace_bytes, int *status, void *stream);
+
+/* Bytes of the sparse_paged_decode_attn_f8 workspace on the current device; 0 if the sizes are invalid. */
+SPARSE_API size_t sparse_paged_decode_attn_f8_workspace_size(int B, int H_q, int H_kv);
 
 #ifdef __cplusplus
 }
