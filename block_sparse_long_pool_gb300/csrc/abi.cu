@@ -158,6 +158,25 @@ int make_kv_tensor_map(CUtensorMap *map, const void *base, long long rows_per_pa
     return SPARSE_OK;
 }
 
+int make_page_tensor_map(CUtensorMap *map, const void *base, long long tiles)
+{
+    std::call_once(g_encode_once, load_encoder);
+    if (g_encode == nullptr)
+        return fail(SPARSE_ERR_CUDA, "cuTensorMapEncodeTiled unavailable (%s)",
+                    cudaGetErrorString(g_encode_err));
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(sp::kD), static_cast<cuuint64_t>(sp::kBlk),
+                                static_cast<cuuint64_t>(tiles)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(sp::kD), static_cast<cuuint64_t>(sp::kD) * sp::kBlk};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(sp::kD), static_cast<cuuint32_t>(sp::kBlk), 2};
+    const cuuint32_t elem_strides[3] = {1, 1, 1};
+    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box,
+                          elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(SPARSE_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
+    return SPARSE_OK;
+}
+
 }  // namespace sp_host
 
 extern "C" {

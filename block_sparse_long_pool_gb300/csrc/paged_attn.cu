@@ -1,8 +1,23 @@
 // paged_attn.cu -- decode attention over the paged 8-bit cache.
 //
-// One CTA per (request, query head): each of its 4 warps takes every fourth token, a lane
-// 4 of the 128 dims, with a running maximum and sum; the warps' states are merged at the
-// end.
+// Work.  The items are the (pair, listed block) tiles, 16 KB each: 64 rows of keys and 64 of
+// values, one byte an element, adjacent in memory.  A persistent grid takes equal ranges
+// of the flattened item list (its length is known on the device only: every CTA sums the
+// counts itself), so requests of very different lengths load the SMs evenly.  A pair whose
+// items lie in several CTAs is merged by the CTA that finishes it last, in CTA order.
+//
+// Per CTA: warp 4 resolves items to pages, 32 at a time (list -> block table -> scales), and
+// streams tiles with one TMA load each into a ring; warps 0..3 own 16 tokens of every tile.
+//   S^T = K Q^T and O^T += V^T P^T run on mma.m16n8k16 in f16: every e4m3 value is an f16
+// value, so the tiles are converted without rounding, two elements an instruction.  Q rows
+// are scaled to f16's range by a power of two of their own.  Which 16 of the 128 dims make
+// a k-step, and which rows an m-tile, is free as long as both operands agree: lanes take
+// whole 16-byte chunks of the swizzled tile, without bank conflicts.
+//   The scales of a page: ks multiplies its scores.  vs is folded into the weights' exponent,
+// p_o = 2^(s + log2 vs - mo) with a running maximum mo of its own (scores are in log2
+// units), so that a weight rounded to f16 (11 bits) keeps its precision whatever the pages'
+// scales are; the row sum l uses the fp32 weights 2^(s - m).
+#include <limits.h>
 #include <math.h>
 
 #include "common.cuh"
@@ -12,11 +27,54 @@ namespace {
 
 using namespace sp;
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 4;                         // consumer warps
+constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kTile = kBlk * kD;                  // keys (or values) of a block: 8 KB
+constexpr int kStageBytes = 2 * kTile;
+constexpr int kCtasPerSm = 2;
+constexpr int kStride = kD + 4;                   // floats a row of the warps' states
+constexpr int kMeta = 64;                         // item records: 32 being written + the ring's
+constexpr float kWeightBits = 12.f;               // weights reach 2^12: f16 holds them down to 2^-24
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kMinItems = 2;                      // items a CTA takes at least
+
+// What the consumers need to know of an item.
+struct Item {
+    float ks;          // key scale
+    float log2_vs;     // value scale
+    int rows;          // valid rows, 0: nothing to do
+    int pair;
+    long long start;   // the pair's first item
+    int n;             // the pair's items
+    int last;          // the CTA's last item of the pair
+};
+static_assert(sizeof(Item) == 32, "two 16-byte loads");
+
+template <int NT>
+constexpr int stages()
+{
+    return NT == 1 ? 5 : 4;
+}
+
+template <int NT>
+struct Smem {
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kBars = stages<NT>() * kStageBytes;
+    static constexpr int kItems = kBars + 128;
+    static constexpr int kWo = kItems + kMeta * 32;                          // [4][kRows][kStride]
+    static constexpr int kStat = kWo + kWarps * kRows * kStride * 4;         // m, l, mo [4][kRows], weights
+    static constexpr int kBytes = kStat + 6 * kWarps * kRows * 4 + 1024;     // + alignment
+};
+
+// One partial state in the workspace: O [kRows][128], then m, l, mo [kRows].
+template <int NT>
+constexpr int part_floats()
+{
+    return 8 * NT * kD + 3 * 8 * NT;
+}
 
 struct PagedAttnParams {
     const uint16_t *Q;
-    const uint8_t *kv_pages;
     const float *kv_scale;
     const int *block_table;
     const int *blk_idx;
@@ -25,99 +83,603 @@ struct PagedAttnParams {
     uint16_t *O;
     float *lse;
     int *status;
+    int *arrivals;     // [pairs], zero between calls
+    float *parts;      // [2 * CTAs][part_floats]
     float scale_log2;
     int n_pages;
     int max_blocks;
     int k_tot;
+    int B;
     int H_q;
     int H_kv;
+    int G;
 };
 
-__global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const PagedAttnParams p)
+// Blocks of request b (a length outside its table is clamped).
+__device__ __forceinline__ int request_blocks(const PagedAttnParams &p, int b, bool *bad)
 {
-    __shared__ float s_o[kWarps][kD], s_m[kWarps], s_l[kWarps];
+    const long long len = p.seq_len[b], cap = static_cast<long long>(p.max_blocks) * kBlk;
+    if (len < 0 || len > cap)
+        *bad = true;
+    return len <= 0 ? 0 : static_cast<int>((min(len, cap) + kBlk - 1) / kBlk);
+}
+
+// Items of a pair.
+__device__ __forceinline__ int pair_items(const PagedAttnParams &p, int pair, bool *bad)
+{
+    if (p.blk_idx == nullptr)
+        return request_blocks(p, pair / p.H_kv, bad);
+    const int n = p.count[pair];
+    if (n < 0 || n > p.k_tot)
+        *bad = true;
+    return n < 0 ? 0 : min(n, p.k_tot);
+}
+
+// The CTA whose range [N c / C, N (c + 1) / C) holds an item.
+__device__ __forceinline__ int cta_of(long long item, long long N, long long C)
+{
+    long long c = item * C / N;
+    while (N * (c + 1) / C <= item)
+        ++c;
+    while (N * c / C > item)
+        --c;
+    return static_cast<int>(c);
+}
+
+// Workspace slot of a CTA's state of a pair: 2c if the pair began before the CTA's range
+// (it can only be the range's first), else 2c + 1 (only its last pair goes on after it).
+__device__ __forceinline__ long long part_slot(int c, long long pair_start, long long N, long long C)
+{
+    return 2LL * c + (pair_start < N * c / C ? 0 : 1);
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// The pair's queries as mma B fragments (row g8 of each n-tile, dims 32 t4 + 4 ks ..+3 for
+// k-step ks), scaled by a power of two to just below f16's largest value, and what undoes
+// it, times the softmax scale, for the rows 2 t4 + {0, 1} whose scores this lane holds.
+template <int NT>
+struct Query {
+    uint32_t b[NT][8][2];
+    float mul[NT][2];
+
+    __device__ __forceinline__ void load(const PagedAttnParams &p, int pair, int lane)
+    {
+        const int g8 = lane >> 2, t4 = lane & 3;
+        const int bb = pair / p.H_kv, g = pair % p.H_kv;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int row = nt * 8 + g8;
+            uint4 x[4] = {};
+            if (row < p.G) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    p.Q + (static_cast<size_t>(bb) * p.H_q + static_cast<size_t>(g) * p.G + row) * kD + 32 * t4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[i] = src[i];
+            }
+            float f[32], amax = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    f[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+                    f[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                amax = fmaxf(amax, fabsf(f[i]));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            // the exponent of the row's largest value becomes 14
+            const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+            const float down = __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23) * p.scale_log2;
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+                b[nt][ks][0] = pack_f16x2(f[4 * ks] * up, f[4 * ks + 1] * up);
+                b[nt][ks][1] = pack_f16x2(f[4 * ks + 2] * up, f[4 * ks + 3] * up);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                mul[nt][h] = __shfl_sync(0xffffffffu, down, (2 * t4 + h) * 4);
+        }
+    }
+};
+
+// A warp's online-softmax state: rows 2 t4 + {0, 1} of every n-tile.  acc[mt][nt] holds dims
+// 16 g8 + 2 mt + {0, 1} (elements 0/1 and 2/3) of those rows, in units of 2^mo.
+template <int NT>
+struct State {
+    float m[NT][2], mo[NT][2], l[NT][2], acc[8][NT][4];
+
+    __device__ __forceinline__ void reset()
+    {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                m[nt][h] = mo[nt][h] = -INFINITY;
+                l[nt][h] = 0.f;
+            }
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[mt][nt][i] = 0.f;
+    }
+};
+
+// One warp over tokens [16 w, 16 w + 16) of a tile, `rows` of the tile's 64 valid.
+template <int NT>
+__device__ __forceinline__ void attend(State<NT> &st, const Query<NT> &q, uint32_t tile, const Item &item, int w, int lane)
+{
+    const int g8 = lane >> 2, t4 = lane & 3;
+    // keys: tokens g8 and g8 + 8, 16-byte chunks 2 t4 and 2 t4 + 1 (dims 32 t4 .. 32 t4 + 31)
+    const uint32_t k0 = tile + (w * 16 + g8) * kD;
+    const uint32_t c0 = static_cast<uint32_t>((2 * t4) ^ g8) << 4, c1 = static_cast<uint32_t>((2 * t4 + 1) ^ g8) << 4;
+    uint32_t ka[8], kb[8];
+    *reinterpret_cast<uint4 *>(ka) = lds_v4(k0 + c0);
+    *reinterpret_cast<uint4 *>(ka + 4) = lds_v4(k0 + c1);
+    *reinterpret_cast<uint4 *>(kb) = lds_v4(k0 + 8 * kD + c0);
+    *reinterpret_cast<uint4 *>(kb + 4) = lds_v4(k0 + 8 * kD + c1);
+    float s[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            s[nt][i] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) {
+        const uint32_t a[4] = {f8x2_to_f16x2(ka[ks]), f8x2_to_f16x2(kb[ks]), f8x2_to_f16x2(ka[ks] >> 16),
+                               f8x2_to_f16x2(kb[ks] >> 16)};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            mma_f16(s[nt], a, q.b[nt][ks][0], q.b[nt][ks][1]);
+    }
+    // values: tokens 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9, chunk g8 (dims 16 g8 .. 16 g8 + 15)
+    const uint32_t v0 = tile + kTile + (w * 16 + 2 * t4) * kD;
+    const uint32_t d0 = static_cast<uint32_t>(g8 ^ (2 * t4)) << 4, d1 = static_cast<uint32_t>(g8 ^ (2 * t4 + 1)) << 4;
+    uint32_t v[4][4];
+    *reinterpret_cast<uint4 *>(v[0]) = lds_v4(v0 + d0);
+    *reinterpret_cast<uint4 *>(v[1]) = lds_v4(v0 + kD + d1);
+    *reinterpret_cast<uint4 *>(v[2]) = lds_v4(v0 + 8 * kD + d0);
+    *reinterpret_cast<uint4 *>(v[3]) = lds_v4(v0 + 9 * kD + d1);
+    const int left = item.rows - w * 16;   // valid tokens of the warp's 16
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            s[nt][i] *= item.ks * q.mul[nt][i & 1];
+    if (left < 16) {
+        // the request ends in this tile: what lies behind it may be any bytes
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (g8 + (i >> 1) * 8 >= left)
+                    s[nt][i] = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (2 * t4 + (i & 1) + (i >> 1) * 8 >= left)
+                v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0u;
+    }
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        float alpha[2], po[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float mx = fmaxf(s[nt][h], s[nt][h + 2]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float m_new = fmaxf(st.m[nt][h], mx);
+            const float mo_new = fmaxf(st.mo[nt][h], mx + item.log2_vs - kWeightBits);
+            const float m_use = m_new == -INFINITY ? 0.f : m_new;
+            const float mo_use = mo_new == -INFINITY ? 0.f : mo_new;
+            st.l[nt][h] = st.l[nt][h] * ex2_approx(st.m[nt][h] - m_use) + ex2_approx(s[nt][h] - m_use) +
+                          ex2_approx(s[nt][h + 2] - m_use);
+            alpha[h] = ex2_approx(st.mo[nt][h] - mo_use);
+            const float shift = item.log2_vs - mo_use;
+            po[h] = ex2_approx(s[nt][h] + shift);
+            po[h + 2] = ex2_approx(s[nt][h + 2] + shift);
+            st.m[nt][h] = m_new;
+            st.mo[nt][h] = mo_new;
+        }
+        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    st.acc[mt][nt][i] *= alpha[i & 1];
+        }
+        pb[nt][0] = movmatrix_trans(pack_f16x2(po[0], po[1]));
+        pb[nt][1] = movmatrix_trans(pack_f16x2(po[2], po[3]));
+    }
+#pragma unroll
+    for (int wi = 0; wi < 4; ++wi) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            // bytes 2x, 2x + 1 of the word: dims 4 wi + 2 x and + 1 of two tokens side by side
+            const uint32_t sel = x == 0 ? 0x5140u : 0x7362u;
+            const uint32_t ab = __byte_perm(v[0][wi], v[1][wi], sel), cd = __byte_perm(v[2][wi], v[3][wi], sel);
+            const uint32_t a[4] = {f8x2_to_f16x2(ab), f8x2_to_f16x2(ab >> 16), f8x2_to_f16x2(cd), f8x2_to_f16x2(cd >> 16)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                mma_f16(st.acc[2 * wi + x][nt], a, pb[nt][0], pb[nt][1]);
+        }
+    }
+}
+
+// Four adjacent output dims of one row, from its unnormalised O (units of 2^mo), m, l.
+__device__ __forceinline__ void write_out(const PagedAttnParams &p, int pair, int row, int d, float4 o, float m, float l,
+                                          float mo)
+{
+    const size_t at = (static_cast<size_t>(pair / p.H_kv) * p.H_q + static_cast<size_t>(pair % p.H_kv) * p.G + row);
+    const float f = l > 0.f ? exp2f(mo - m) / l : l == 0.f ? 0.f : l;   // l NaN: the row is NaN
+    if (l == 0.f)
+        o = make_float4(0.f, 0.f, 0.f, 0.f);
+    *reinterpret_cast<uint2 *>(p.O + at * kD + d) = make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
+    if (d == 0 && p.lse != nullptr)
+        p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    paged_attn_kernel(const __grid_constant__ CUtensorMap map, const PagedAttnParams p)
+{
+    constexpr int ROWS = 8 * NT;
+    constexpr int STAGES = stages<NT>();
+    constexpr int PART = part_floats<NT>();
+    using S = Smem<NT>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ long long s_sum[kWarps + 2];
+    __shared__ long long s_start;
+    __shared__ int s_unit, s_last;
+    const uint32_t base_s = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t *base = smem_raw + (base_s - smem_u32(smem_raw));
+    Item *items = reinterpret_cast<Item *>(base + S::kItems);
+    const uint32_t full = base_s + S::kBars, empty = full + 8 * STAGES, meet = empty + 8 * STAGES;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(full + 8 * i, 2);          // the load's expect_tx, and the item record
+            mbar_init(empty + 8 * i, kWarps);
+        }
+        mbar_init(meet, kWarps);
+        fence_barrier_init();
+    }
+    if (tid == kWarps * 32)
+        prefetch_tensormap(&map);
     griddep_wait();
     griddep_launch_dependents();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int b = blockIdx.x / p.H_q, h = blockIdx.x % p.H_q;
-    const int g = h / (p.H_q / p.H_kv);
-    const size_t pair = static_cast<size_t>(b) * p.H_kv + g;
-    const uint2 qb = *reinterpret_cast<const uint2 *>(p.Q + static_cast<size_t>(blockIdx.x) * kD + 4 * lane);
-    const float2 q0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&qb.x));
-    const float2 q1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&qb.y));
-    long long len = p.seq_len[b];
-    const long long cap = static_cast<long long>(p.max_blocks) * kBlk;
-    bool bad = len < 0 || len > cap;
-    len = len < 0 ? 0 : len > cap ? cap : len;
-    const int nb = static_cast<int>((len + kBlk - 1) / kBlk);
-    int n = nb;
-    if (p.blk_idx != nullptr) {
-        n = p.count[pair];
-        bad |= n < 0 || n > p.k_tot;
-        n = n < 0 ? 0 : n > p.k_tot ? p.k_tot : n;
-    }
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < n; ++i) {
-        const int blk = p.blk_idx != nullptr ? p.blk_idx[pair * p.k_tot + i] : i;
-        if (blk < 0 || blk >= p.max_blocks) {
-            bad = true;
-            continue;
-        }
-        if (blk >= nb)
-            continue;
-        const int page = p.block_table[static_cast<size_t>(b) * p.max_blocks + blk];
-        if (page < 0 || page >= p.n_pages) {
-            bad = true;
-            continue;
-        }
-        const size_t unit = (static_cast<size_t>(page) * p.H_kv + g) * 2;
-        const float ks = p.kv_scale[unit] * p.scale_log2, vs = p.kv_scale[unit + 1];
-        const int rows = static_cast<int>(min(len - static_cast<long long>(blk) * kBlk, static_cast<long long>(kBlk)));
-        for (int r = warp; r < rows; r += kWarps) {
-            const uint8_t *at = p.kv_pages + unit * (kBlk * kD) + r * kD + 4 * lane;
-            const uint32_t kw = *reinterpret_cast<const uint32_t *>(at);
-            const uint32_t vw = *reinterpret_cast<const uint32_t *>(at + kBlk * kD);
-            const float2 k0 = f8x2_to_float2(kw), k1 = f8x2_to_float2(kw >> 16);
-            float s = q0.x * k0.x + q0.y * k0.y + q1.x * k1.x + q1.y * k1.y;
-#pragma unroll
-            for (int x = 16; x > 0; x >>= 1)
-                s += __shfl_xor_sync(0xffffffffu, s, x);
-            s *= ks;
-            const float m_new = fmaxf(m, s);
-            const float a = exp2f(m - m_new), pr = exp2f(s - m_new);
-            m = m_new;
-            l = l * a + pr;
-            const float pv = pr * vs;
-            const float2 v0 = f8x2_to_float2(vw), v1 = f8x2_to_float2(vw >> 16);
-            o.x = o.x * a + pv * v0.x;
-            o.y = o.y * a + pv * v0.y;
-            o.z = o.z * a + pv * v1.x;
-            o.w = o.w * a + pv * v1.y;
-        }
-    }
-    if (bad && threadIdx.x == 0)
+
+    // ---- items before each unit (a request where every block is attended over, else a pair)
+    const bool all = p.blk_idx == nullptr;
+    const int units = all ? p.B : p.B * p.H_kv;
+    const int weight = all ? p.H_kv : 1;
+    const int per = (units + kThreads - 1) / kThreads;
+    const int u0 = min(units, tid * per), u1 = min(units, u0 + per);
+    bool bad = false;
+    long long mine = 0;
+    for (int u = u0; u < u1; ++u)
+        mine += static_cast<long long>(pair_items(p, u * weight, &bad)) * weight;
+    if (bad && blockIdx.x == 0)
         report(p.status, SPARSE_ERR_BAD_INDEX);
-    *reinterpret_cast<float4 *>(&s_o[warp][4 * lane]) = o;
-    if (lane == 0) {
-        s_m[warp] = m;
-        s_l[warp] = l;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o)
+            incl += v;
+    }
+    if (lane == 31)
+        s_sum[warp] = incl;
+    __syncthreads();
+    long long N = 0;
+#pragma unroll
+    for (int w = 0; w <= kWarps; ++w) {
+        if (w < warp)
+            incl += s_sum[w];
+        N += s_sum[w];
+    }
+    const long long C = max(1LL, min(static_cast<long long>(gridDim.x), (N + kMinItems - 1) / kMinItems));
+    const int c = static_cast<int>(blockIdx.x);
+    const long long lo = c < C ? N * c / C : N, hi = c < C ? N * (c + 1) / C : N;
+    if (lo < hi && incl - mine <= lo && lo < incl) {
+        long long at = incl - mine;
+        int u = u0;
+        for (; u < u1 - 1; ++u) {
+            const long long n = static_cast<long long>(pair_items(p, u * weight, &bad)) * weight;
+            if (at + n > lo)
+                break;
+            at += n;
+        }
+        s_unit = u;
+        s_start = at;
     }
     __syncthreads();
-    float M = -INFINITY, L = 0.f, acc = 0.f;
+
+    if (warp == kWarps) {
+        // ------------------------------------------------------------ producer
+        if (lo >= hi)
+            return;
+        int pair = s_unit;             // the pair that holds item `at`, and its first item
+        long long start = s_start;
+        if (all) {
+            const int n = pair_items(p, s_unit * weight, &bad);
+            const int h = static_cast<int>((lo - start) / n);
+            pair = s_unit * weight + h;
+            start += static_cast<long long>(h) * n;
+        }
+        const int pairs = p.B * p.H_kv;
+        const uint64_t pol = policy_evict_first();
+        long long at = lo;             // next item
+        int it = 0;                    // its number in the CTA
+        bool stop = false, wrong = false;
+        while (at < hi && pair < pairs && !stop) {
+            // the next 32 pairs' items and where they start
+            const int n = pair + lane < pairs ? pair_items(p, pair + lane, &bad) : 0;
+            long long end = n;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-        M = fmaxf(M, s_m[w]);
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long v = __shfl_up_sync(0xffffffffu, end, o);
+                if (lane >= o)
+                    end += v;
+            }
+            end += start;
+            const long long upto = min(hi, __shfl_sync(0xffffffffu, end, 31));
+            const int take = static_cast<int>(min(32LL, upto - at));
+            // lane j resolves item at + j: the first of the 32 pairs that ends after it
+            int k = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        const float f = s_l[w] > 0.f ? exp2f(s_m[w] - M) : 0.f;
-        L += f * s_l[w];
-        acc += f * s_o[w][threadIdx.x];
+            for (int step = 16; step > 0; step >>= 1)
+                if (__shfl_sync(0xffffffffu, end, k + step - 1) <= at + lane)
+                    k += step;
+            k = min(k, 31);
+            Item item;
+            item.pair = pair + k;
+            item.n = __shfl_sync(0xffffffffu, n, k);
+            item.start = __shfl_sync(0xffffffffu, end, k) - item.n;
+            item.rows = 0;
+            item.last = at + lane + 1 == hi || at + lane + 1 == item.start + item.n;
+            int unit = 0;
+            float2 sc = make_float2(1.f, 1.f);
+            if (lane < take) {
+                const int b = item.pair / p.H_kv, i = static_cast<int>(at + lane - item.start);
+                const int blk = all ? i : p.blk_idx[static_cast<size_t>(item.pair) * p.k_tot + i];
+                const long long rows = min(static_cast<long long>(p.seq_len[b]), static_cast<long long>(p.max_blocks) * kBlk) -
+                                       static_cast<long long>(blk) * kBlk;
+                if (blk < 0 || blk >= p.max_blocks) {
+                    wrong = true;
+                } else if (rows > 0) {
+                    const int page = p.block_table[static_cast<size_t>(b) * p.max_blocks + blk];
+                    if (page < 0 || page >= p.n_pages) {
+                        wrong = true;
+                    } else {
+                        item.rows = static_cast<int>(min(rows, static_cast<long long>(kBlk)));
+                        unit = page * p.H_kv + item.pair % p.H_kv;
+                        sc = *reinterpret_cast<const float2 *>(p.kv_scale + 2 * static_cast<size_t>(unit));
+                    }
+                }
+            }
+            // the ring is empty at first: those loads go out before the scales are here
+            const int ahead = it == 0 ? min(take, STAGES) : 0;
+            for (int j = 0; j < ahead; ++j) {
+                const int u = __shfl_sync(0xffffffffu, unit, j), rows = __shfl_sync(0xffffffffu, item.rows, j);
+                if (lane == 0) {
+                    if (rows > 0) {
+                        mbar_arrive_expect_tx(full + 8 * j, kStageBytes);
+                        tma_load_3d(base_s + j * kStageBytes, &map, full + 8 * j, 0, 0, 2 * u, pol);
+                    } else {
+                        mbar_arrive(full + 8 * j);
+                    }
+                }
+            }
+            item.ks = sc.x;
+            item.log2_vs = log2f(sc.y);
+            if (lane < take)
+                items[(it + lane) % kMeta] = item;
+            __syncwarp();
+            for (int j = 0; j < take && !stop; ++j) {
+                const int u = __shfl_sync(0xffffffffu, unit, j), rows = __shfl_sync(0xffffffffu, item.rows, j);
+                const int stage = (it + j) % STAGES, use = (it + j) / STAGES;
+                if (lane == 0) {
+                    if (j >= ahead) {
+                        if (use > 0 && !mbar_wait(empty + 8 * stage, (use - 1) & 1, kWaitNs)) {
+                            report(p.status, SPARSE_ERR_TIMEOUT);
+                            stop = true;
+                        } else if (rows > 0) {
+                            mbar_arrive_expect_tx(full + 8 * stage, kStageBytes);
+                            tma_load_3d(base_s + stage * kStageBytes, &map, full + 8 * stage, 0, 0, 2 * u, pol);
+                        } else {
+                            mbar_arrive(full + 8 * stage);
+                        }
+                    }
+                    if (!stop)
+                        mbar_arrive(full + 8 * stage);   // the item record
+                }
+                stop = __shfl_sync(0xffffffffu, stop ? 1 : 0, 0) != 0;
+            }
+            at += take;
+            it += take;
+            // the pair that holds the next item
+            const unsigned open = __ballot_sync(0xffffffffu, end > at);
+            const int skip = open != 0u ? __ffs(static_cast<int>(open)) - 1 : 32;
+            start = skip == 32 ? __shfl_sync(0xffffffffu, end, 31) : __shfl_sync(0xffffffffu, end - n, skip);
+            pair += skip;
+        }
+        if (__any_sync(0xffffffffu, wrong) && lane == 0)
+            report(p.status, SPARSE_ERR_BAD_INDEX);
+        return;
     }
-    const __nv_bfloat16 ob = __float2bfloat16_rn(L > 0.f ? acc / L : 0.f);
-    p.O[static_cast<size_t>(blockIdx.x) * kD + threadIdx.x] = *reinterpret_cast<const uint16_t *>(&ob);
-    if (p.lse != nullptr && threadIdx.x == 0)
-        p.lse[blockIdx.x] = L > 0.f ? (M + log2f(L)) * 0.69314718055994530942f : -INFINITY;
+
+    // ---------------------------------------------------------------- consumers
+    // the consumer warps meet; false where one of them gave up (it leaves, and so do the others)
+    int meetings = 0;
+    auto sync = [&] {
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(meet);
+        return __all_sync(0xffffffffu, mbar_wait(meet, meetings++ & 1, 2 * kWaitNs)) != 0;
+    };
+    // rows of pairs without items, shared out over the CTAs
+    for (int pair = c + static_cast<int>(gridDim.x) * warp; pair < p.B * p.H_kv; pair += static_cast<int>(gridDim.x) * kWarps)
+        if (pair_items(p, pair, &bad) == 0)
+            for (int row = 0; row < p.G; ++row)
+                write_out(p, pair, row, 4 * lane, make_float4(0.f, 0.f, 0.f, 0.f), 0.f, 0.f, 0.f);
+
+    float *wo = reinterpret_cast<float *>(base + S::kWo);
+    float *wm = reinterpret_cast<float *>(base + S::kStat);   // [4][ROWS] each: m, l, mo
+    float *wl = wm + kWarps * ROWS, *wmo = wl + kWarps * ROWS;
+    Query<NT> q;
+    State<NT> st;
+    st.reset();
+    int of_pair = -1;
+    const int n_items = static_cast<int>(hi - lo);
+    for (int it = 0; it < n_items; ++it) {
+        const int stage = it % STAGES;
+        if (!__all_sync(0xffffffffu, mbar_wait(full + 8 * stage, (it / STAGES) & 1, kWaitNs))) {
+            if (lane == 0)
+                report(p.status, SPARSE_ERR_TIMEOUT);
+            return;
+        }
+        const Item item = items[it % kMeta];
+        if (item.pair != of_pair) {
+            of_pair = item.pair;
+            q.load(p, of_pair, lane);
+            st.reset();
+        }
+        if (item.rows > warp * 16)
+            attend<NT>(st, q, base_s + stage * kStageBytes, item, warp, lane);
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(empty + 8 * stage);
+        if (!item.last)
+            continue;
+
+        // ---- the CTA's state of the pair: the 4 warps' states merged
+        const int g8 = lane >> 2, t4 = lane & 3;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int row = nt * 8 + 2 * t4 + h;
+                float l = st.l[nt][h];
+                l += __shfl_xor_sync(0xffffffffu, l, 4);
+                l += __shfl_xor_sync(0xffffffffu, l, 8);
+                l += __shfl_xor_sync(0xffffffffu, l, 16);
+                if (g8 == 0) {
+                    wm[warp * ROWS + row] = st.m[nt][h];
+                    wl[warp * ROWS + row] = l;
+                    wmo[warp * ROWS + row] = st.mo[nt][h];
+                }
+                float *dst = wo + (warp * ROWS + row) * kStride + 16 * g8;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<float4 *>(dst + 4 * i) =
+                        make_float4(st.acc[2 * i][nt][h], st.acc[2 * i][nt][h + 2], st.acc[2 * i + 1][nt][h],
+                                    st.acc[2 * i + 1][nt][h + 2]);
+            }
+        if (!sync())
+            return;
+        const bool whole = item.start >= lo && item.start + item.n <= hi;
+        float *part = p.parts + part_slot(c, item.start, N, C) * PART;
+        for (int e = tid; e < p.G * (kD / 4); e += kWarps * 32) {
+            const int row = e / (kD / 4), d = 4 * (e % (kD / 4));
+            float m = -INFINITY, mo = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                m = fmaxf(m, wm[w * ROWS + row]);
+                mo = fmaxf(mo, wmo[w * ROWS + row]);
+            }
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float lw = wl[w * ROWS + row];
+                l += lw == 0.f ? 0.f : lw * exp2f(wm[w * ROWS + row] - m);
+                const float f = wmo[w * ROWS + row] == -INFINITY ? 0.f : exp2f(wmo[w * ROWS + row] - mo);
+                const float4 x = *reinterpret_cast<const float4 *>(wo + (w * ROWS + row) * kStride + d);
+                o.x = fmaf(f, x.x, o.x);
+                o.y = fmaf(f, x.y, o.y);
+                o.z = fmaf(f, x.z, o.z);
+                o.w = fmaf(f, x.w, o.w);
+            }
+            if (whole) {
+                write_out(p, item.pair, row, d, o, m, l, mo);
+            } else {
+                *reinterpret_cast<float4 *>(part + row * kD + d) = o;
+                if (d == 0) {
+                    part[ROWS * kD + row] = m;
+                    part[ROWS * kD + ROWS + row] = l;
+                    part[ROWS * kD + 2 * ROWS + row] = mo;
+                }
+            }
+        }
+        if (!whole) {
+            // ---- the pair's last CTA merges the CTAs' states, in their order
+            __threadfence();
+            if (!sync())
+                return;
+            const int c0 = cta_of(item.start, N, C), c1 = cta_of(item.start + item.n - 1, N, C);
+            if (tid == 0) {
+                const int prev = atomicAdd(p.arrivals + item.pair, 1);
+                s_last = prev == c1 - c0;
+                if (prev == c1 - c0) {
+                    p.arrivals[item.pair] = 0;   // for the next call
+                    __threadfence();
+                }
+            }
+            if (!sync())
+                return;
+            if (s_last) {
+                for (int e = tid; e < p.G * (kD / 4); e += kWarps * 32) {
+                    const int row = e / (kD / 4), d = 4 * (e % (kD / 4));
+                    float m = -INFINITY, mo = -INFINITY, l = 0.f;
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int x = c0; x <= c1; ++x) {
+                        const float *src = p.parts + part_slot(x, item.start, N, C) * PART;
+                        const float mx = __ldcg(src + ROWS * kD + row), lx = __ldcg(src + ROWS * kD + ROWS + row),
+                                    mox = __ldcg(src + ROWS * kD + 2 * ROWS + row);
+                        const float4 ox = __ldcg(reinterpret_cast<const float4 *>(src + row * kD + d));
+                        const float m_new = fmaxf(m, mx), mo_new = fmaxf(mo, mox);
+                        const float a = m == -INFINITY ? 0.f : exp2f(m - m_new), ax = mx == -INFINITY ? 0.f : exp2f(mx - m_new);
+                        const float b = mo == -INFINITY ? 0.f : exp2f(mo - mo_new),
+                                    bx = mox == -INFINITY ? 0.f : exp2f(mox - mo_new);
+                        l = (l == 0.f ? 0.f : l * a) + (lx == 0.f ? 0.f : lx * ax);
+                        o.x = o.x * b + ox.x * bx;
+                        o.y = o.y * b + ox.y * bx;
+                        o.z = o.z * b + ox.z * bx;
+                        o.w = o.w * b + ox.w * bx;
+                        m = m_new;
+                        mo = mo_new;
+                    }
+                    write_out(p, item.pair, row, d, o, m, l, mo);
+                }
+            }
+        }
+        if (!sync())   // wo, the statistics and s_last are free again
+            return;
+    }
 }
 
 bool sizes_ok(int B, int H_q, int H_kv)
@@ -126,13 +688,48 @@ bool sizes_ok(int B, int H_q, int H_kv)
            static_cast<long long>(B) * H_kv <= 65535;
 }
 
+// Workspace: an arrival count a pair, then two partial states a CTA.
+size_t counter_bytes(long long pairs)
+{
+    return (static_cast<size_t>(pairs) * sizeof(int) + 255) & ~static_cast<size_t>(255);
+}
+
+size_t workspace_bytes_of(int B, int H_q, int H_kv, int sm_count)
+{
+    const size_t part = H_q / H_kv <= 8 ? part_floats<1>() : part_floats<2>();
+    return counter_bytes(static_cast<long long>(B) * H_kv) + 2ull * kCtasPerSm * sm_count * part * sizeof(float);
+}
+
+template <int NT>
+int launch(const PagedAttnParams &p, const CUtensorMap &map, const sp_host::DeviceInfo &dev, const char *name, void *stream)
+{
+    const void *kern = reinterpret_cast<const void *>(paged_attn_kernel<NT>);
+    static int configured[64];
+    const int rc = sp_host::configure_kernel(kern, Smem<NT>::kBytes, dev.device, configured);
+    if (rc != SPARSE_OK)
+        return rc;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(kCtasPerSm * dev.sm_count));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Smem<NT>::kBytes;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void *args[] = {const_cast<CUtensorMap *>(&map), const_cast<PagedAttnParams *>(&p)};
+    return sp_host::cuda_status(cudaLaunchKernelExC(&cfg, kern, args), name);
+}
+
 }  // namespace
 
 extern "C" SPARSE_API size_t sparse_paged_decode_attn_f8_workspace_size(int B, int H_q, int H_kv)
 {
-    if (!sizes_ok(B, H_q, H_kv))
+    sp_host::DeviceInfo dev;
+    if (!sizes_ok(B, H_q, H_kv) || sp_host::device_info(&dev) != SPARSE_OK)
         return 0;
-    return 256;
+    return workspace_bytes_of(B, H_q, H_kv, dev.sm_count);
 }
 
 extern "C" SPARSE_API int sparse_paged_decode_attn_f8(const uint16_t *Q, const uint8_t *kv_pages, const float *kv_scale,
@@ -163,16 +760,34 @@ extern "C" SPARSE_API int sparse_paged_decode_attn_f8(const uint16_t *Q, const u
     const size_t need = sparse_paged_decode_attn_f8_workspace_size(B, H_q, H_kv);
     if (workspace_bytes < need)
         return fail(SPARSE_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", name, workspace_bytes, need);
-    const float s = scale == 0.f ? 1.f / sqrtf(static_cast<float>(kD)) : scale;
-    const PagedAttnParams p{Q, kv_pages, kv_scale, block_table, blk_idx, count, seq_len, O, lse, status,
-                            s * 1.44269504088896340736f, n_pages, max_blocks, k_tot, H_q, H_kv};
+    if (2LL * n_pages * H_kv > INT_MAX)
+        return fail(SPARSE_ERR_UNSUPPORTED, "%s: n_pages * H_kv = %lld > 2^30", name, static_cast<long long>(n_pages) * H_kv);
     sp_host::DeviceInfo dev;
-    static int configured[64];
+    CUtensorMap map;
     int rc = sp_host::device_info(&dev);
     if (rc == SPARSE_OK)
-        rc = sp_host::configure_kernel(reinterpret_cast<const void *>(paged_attn_kernel), 0, dev.device, configured);
+        rc = sp_host::make_page_tensor_map(&map, kv_pages, 2LL * n_pages * H_kv);
     if (rc != SPARSE_OK)
         return rc;
-    return sp_host::cuda_status(launch_pdl(reinterpret_cast<const void *>(paged_attn_kernel),
-                                           dim3(static_cast<unsigned>(B) * H_q), kWarps * 32, 0, &p, stream), name);
+    const float s = scale == 0.f ? 1.f / sqrtf(static_cast<float>(kD)) : scale;
+    const PagedAttnParams p{Q,
+                            kv_scale,
+                            block_table,
+                            blk_idx,
+                            count,
+                            seq_len,
+                            O,
+                            lse,
+                            status,
+                            static_cast<int *>(workspace),
+                            reinterpret_cast<float *>(static_cast<char *>(workspace) + counter_bytes(static_cast<long long>(B) * H_kv)),
+                            s * 1.44269504088896340736f,   // log2(e): scores are exponentiated base 2
+                            n_pages,
+                            max_blocks,
+                            k_tot,
+                            B,
+                            H_q,
+                            H_kv,
+                            H_q / H_kv};
+    return p.G <= 8 ? launch<1>(p, map, dev, name, stream) : launch<2>(p, map, dev, name, stream);
 }
