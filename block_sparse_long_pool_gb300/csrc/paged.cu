@@ -18,6 +18,9 @@ using namespace sp;
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanMaxB = 4096;
 constexpr int kPlanPer = kPlanMaxB / kPlanThreads;   // requests a thread scans, at most
+constexpr int kRowThreads = 256;
+constexpr int kRowsPerCta = 4096;
+constexpr int kRowsOneCta = 4096;   // rows that the planning CTA writes itself
 
 struct PlanParams {
     const int *seq_len;
@@ -77,7 +80,88 @@ __device__ __forceinline__ int saturate(long long v)
     return v > INT_MAX ? INT_MAX : static_cast<int>(v);
 }
 
-__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParams p)
+// Pages that a granted request took.
+__device__ __forceinline__ int pages_taken(const int *cu, const int *first, int b)
+{
+    const int st = first[b];
+    return st < 0 ? 0 : (st + (cu[b + 1] - cu[b]) + kBlk - 1) / kBlk - (st + kBlk - 1) / kBlk;
+}
+
+// Rows [t0, t0 + n) (t0 a multiple of 4): four rows a thread, stored as one 16-byte word.
+// The first row's request comes from a binary search, the next rows' from a step.  A new
+// block's page is read from the free list and entered into the table by the row that
+// starts the block.
+__device__ __forceinline__ void plan_rows(const PlanParams &p, const int *cu, const int *first, const int *npre, int F,
+                                          int t0, int n)
+{
+    const int total = cu[p.B];
+    for (int i = 4 * static_cast<int>(threadIdx.x); i < n; i += 4 * static_cast<int>(blockDim.x)) {
+        int slot[4], req[4], pos[4];
+        int b = 0;
+        if (t0 + i < total) {
+            int hi = p.B - 1;
+            while (b < hi) {
+                const int mid = (b + hi) >> 1;
+                if (cu[mid + 1] > t0 + i)
+                    hi = mid;
+                else
+                    b = mid + 1;
+            }
+        }
+        int page = -1, of = -1;   // the page of block `of` of request b
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int t = t0 + i + j;
+            slot[j] = req[j] = pos[j] = -1;
+            if (t < total && i + j < n) {
+                while (cu[b + 1] <= t) {
+                    ++b;
+                    of = -1;
+                }
+                const int st = first[b];
+                if (st >= 0) {
+                    req[j] = b;
+                    pos[j] = st + t - cu[b];
+                    const int blk = pos[j] / kBlk;
+                    if (blk != of) {
+                        of = blk;
+                        const int used = (st + kBlk - 1) / kBlk;
+                        const size_t at = static_cast<size_t>(b) * p.max_blocks + blk;
+                        if (blk < used) {
+                            page = p.block_table[at];
+                        } else {
+                            page = p.free_pages[F - 1 - (npre[b] + blk - used)];
+                            if (pos[j] % kBlk == 0)
+                                p.block_table[at] = page;
+                        }
+                        if (page < 0 || page >= p.n_pages) {
+                            report(p.status, SPARSE_ERR_BAD_INDEX);
+                            page = -1;
+                        }
+                    }
+                    if (page >= 0)
+                        slot[j] = page * kBlk + pos[j] % kBlk;
+                }
+            }
+        }
+        const int t = t0 + i;
+        if (t + 3 < p.n_tok) {
+            *reinterpret_cast<int4 *>(p.slot_map + t) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+            *reinterpret_cast<int4 *>(p.tok_req + t) = make_int4(req[0], req[1], req[2], req[3]);
+            *reinterpret_cast<int4 *>(p.tok_pos + t) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+                if (t + j < p.n_tok) {
+                    p.slot_map[t + j] = slot[j];
+                    p.tok_req[t + j] = req[j];
+                    p.tok_pos[t + j] = pos[j];
+                }
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParams p, int with_rows)
 {
     extern __shared__ int plan_smem[];
     __shared__ long long red[33];
@@ -90,7 +174,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
     griddep_launch_dependents();
 
     const int tid = threadIdx.x;
-    const int per = (p.B + kPlanThreads - 1) / kPlanThreads;
+    const int per = (p.B + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x);
     long long len[kPlanPer], add[kPlanPer];
     bool ends[kPlanPer], sound[kPlanPer];
     long long s_rel = 0, s_add = 0;
@@ -186,53 +270,54 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
         p.n_free_out[0] = F - static_cast<int>(all_taken);
     if (all_rel > 0) {
         // returned pages: a warp takes a request, its lanes the request's blocks
-        for (int b = tid >> 5; b < p.B; b += kPlanThreads / 32)
+        for (int b = tid >> 5; b < p.B; b += static_cast<int>(blockDim.x) / 32)
             for (int j = tid & 31; j < rel[b]; j += 32)
                 if (static_cast<long long>(F0) + relpre[b] + j < p.n_pages)
                     p.free_pages[F0 + relpre[b] + j] = p.block_table[static_cast<size_t>(b) * p.max_blocks + j];
         __syncthreads();
     }
-    // rows: the request by binary search, then its page from the table or the free list
-    for (int t = tid; t < p.n_tok; t += kPlanThreads) {
-        int slot = -1, req = -1, pos = -1;
-        if (t < cu[p.B]) {
-            int lo = 0, hi = p.B - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (cu[mid + 1] > t)
-                    hi = mid;
-                else
-                    lo = mid + 1;
-            }
-            const int st = first[lo];
-            if (st >= 0) {
-                req = lo;
-                pos = st + t - cu[lo];
-                const int blk = pos / kBlk, used = (st + kBlk - 1) / kBlk;
-                const size_t at = static_cast<size_t>(lo) * p.max_blocks + blk;
-                int page;
-                if (blk < used) {
-                    page = p.block_table[at];
-                } else {
-                    page = p.free_pages[F - 1 - (npre[lo] + blk - used)];
-                    if (pos % kBlk == 0)   // a block past the used ones starts with a new token
-                        p.block_table[at] = page;
-                }
-                if (page >= 0 && page < p.n_pages)
-                    slot = page * kBlk + pos % kBlk;
-                else
-                    report(p.status, SPARSE_ERR_BAD_INDEX);
-            }
-        }
-        p.slot_map[t] = slot;
-        p.tok_req[t] = req;
-        p.tok_pos[t] = pos;
+    if (with_rows)
+        plan_rows(p, cu, first, npre, F, 0, p.n_tok);
+}
+
+// Steps with many rows: the grid writes them after page_plan_kernel, whose outputs give it
+// all it needs (F = what is left on the list and what was taken).
+__global__ void __launch_bounds__(kRowThreads) page_rows_kernel(const PlanParams p)
+{
+    extern __shared__ int plan_smem[];
+    __shared__ long long red[33];
+    int *cu = plan_smem;          // [B + 1]
+    int *first = cu + p.B + 1;    // [B]
+    int *npre = first + p.B;      // [B]
+    griddep_wait();
+    griddep_launch_dependents();
+    const int tid = threadIdx.x;
+    for (int b = tid; b <= p.B; b += kRowThreads) {
+        cu[b] = p.cu_new[b];
+        if (b < p.B)
+            first[b] = p.start[b];
     }
+    __syncthreads();
+    const int per = (p.B + kRowThreads - 1) / kRowThreads;
+    const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+    int mine = 0;
+    for (int b = b0; b < b1; ++b)
+        mine += pages_taken(cu, first, b);
+    long long all;
+    int o = static_cast<int>(block_scan(mine, red, &all)) - mine;
+    for (int b = b0; b < b1; ++b) {
+        npre[b] = o;
+        o += pages_taken(cu, first, b);
+    }
+    __syncthreads();
+    const int t0 = static_cast<int>(blockIdx.x) * kRowsPerCta;
+    plan_rows(p, cu, first, npre, p.n_free_out[0] + static_cast<int>(all), t0, min(p.n_tok - t0, kRowsPerCta));
 }
 
 // ---------------------------------------------------------------- append
 
 constexpr int kAppendThreads = 256;
+constexpr int kShort = 2;       // rows of a run that one warp appends
 constexpr int kMinExp = -120;   // least exponent of a scale: its reciprocal is a normal fp32 value
 
 struct PagedAppendParams {
@@ -265,120 +350,293 @@ __device__ __forceinline__ float pow2_scale(float amax)
     return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const PagedAppendParams p)
+// The largest absolute value of 8 bf16 values, packed in pairs; NaN does not count.
+__device__ __forceinline__ __nv_bfloat162 amax8(const uint4 &x, __nv_bfloat162 m)
 {
-    __shared__ float s_amax[8];
-    __shared__ float red[8][kD + 4];
-    griddep_wait();
-    griddep_launch_dependents();
-    const int tid = threadIdx.x;
-    const int kv = tid >> 7;             // 0: keys, 1: values
-    const int r0 = (tid & 127) >> 4;     // row phase 0..7
-    const int c = tid & 15;              // dims 8c .. 8c+7
-    const int head = blockIdx.y;
-    const int t_end = min(p.n_tok, (static_cast<int>(blockIdx.x) + 1) * p.window);
-    for (int t = static_cast<int>(blockIdx.x) * p.window; t < t_end; ++t) {
-        // does a run start at row t, and how many rows has it?
-        const int slot = p.slot_map[t];
-        if (slot < 0)
-            continue;
-        const int off = slot % kBlk, page = slot / kBlk;
-        if (off != 0 && t > 0 && p.slot_map[t - 1] == slot - 1)
-            continue;
-        if (page >= p.n_pages) {
-            if (tid == 0)
-                report(p.status, SPARSE_ERR_BAD_INDEX);
-            continue;
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t a = w[j] & 0x7fff7fffu;
+        m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162 *>(&a));
+    }
+    return m;
+}
+
+__device__ __forceinline__ float larger_of(__nv_bfloat162 m)
+{
+    const float2 f = __bfloat1622float2(m);
+    return fmaxf(f.x, f.y);
+}
+
+// As amax8, infinities left out too.
+__device__ __forceinline__ float finite_amax8(const uint4 &x, float m)
+{
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t u = (h ? w[j] & 0xffff0000u : w[j] << 16) & 0x7fffffffu;
+            m = fmaxf(m, u < 0x7f800000u ? __uint_as_float(u) : 0.f);
         }
-        int n = 1;
-        while (n < kBlk - off && t + n < p.n_tok && p.slot_map[t + n] == slot + n)
-            ++n;
-        const uint16_t *src = (kv ? p.v_new + static_cast<size_t>(t) * p.v_stride
-                                  : p.k_new + static_cast<size_t>(t) * p.k_stride) + head * kD + c * 8;
-        const long long stride = kv ? p.v_stride : p.k_stride;
-        uint4 x[8];
-        float amax = 0.f, sum[8];
+    return m;
+}
+
+// 8 bf16 values times `inv` as e4m3; `inf`: infinities may be among them, and become NaN.
+__device__ __forceinline__ uint2 round8(const uint4 &x, float inv, bool inf)
+{
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f[2 * j] = __uint_as_float(w[j] << 16);
+        f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+    if (inf) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            f[j] += f[j] - f[j];   // x - x: 0, or NaN for infinities and NaN
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        f[j] *= inv;
+    return make_uint2(f8x4_pack(f[0], f[1], f[2], f[3]), f8x4_pack(f[4], f[5], f[6], f[7]));
+}
+
+__device__ __forceinline__ void add8(float (&sum)[8], const uint4 &x)
+{
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        sum[2 * j] += __uint_as_float(w[j] << 16);
+        sum[2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
+    }
+}
+
+// Rows [0, off) of a tile at a larger scale; this thread's rows r0, r0 + step, ... and 8 dims.
+__device__ __forceinline__ void rescale_rows(uint8_t *dst, int r0, int step, int off, float ratio)
+{
+    for (int r = r0; r < off; r += step) {
+        uint2 *at = reinterpret_cast<uint2 *>(dst + r * kD);
+        uint2 w = *at;
+        w.x = f8x4_scaled(w.x, ratio);
+        w.y = f8x4_scaled(w.y, ratio);
+        *at = w;
+    }
+}
+
+// The compressed key row of the run that starts at row t, or null.
+__device__ __forceinline__ float *ktil_row(const PagedAppendParams &p, int t, int head, bool first_thread)
+{
+    if (p.ktil == nullptr)
+        return nullptr;
+    const int b = p.tok_req[t], j = p.tok_pos[t] >> 6;
+    if (b < 0 || b >= p.B || j < 0 || j >= p.N_cap) {
+        if (first_thread)
+            report(p.status, SPARSE_ERR_BAD_INDEX);
+        return nullptr;
+    }
+    return p.ktil + ((static_cast<size_t>(b) * p.H_kv + head) * p.N_cap + j) * kD;
+}
+
+// A run of at most kShort rows by one warp: lanes 0..15 take the keys, 16..31 the values,
+// 8 dims each.
+__device__ __forceinline__ void append_short(const PagedAppendParams &p, int t, int slot, int n, int head, int lane)
+{
+    const int kv = lane >> 4, c = lane & 15;
+    const int page = slot / kBlk, off = slot % kBlk;
+    const size_t unit = (static_cast<size_t>(page) * p.H_kv + head) * 2 + kv;
+    const uint16_t *src = (kv ? p.v_new + static_cast<size_t>(t) * p.v_stride
+                              : p.k_new + static_cast<size_t>(t) * p.k_stride) + head * kD + c * 8;
+    const long long stride = kv ? p.v_stride : p.k_stride;
+    uint4 x[kShort];
+#pragma unroll
+    for (int r = 0; r < kShort; ++r)
+        x[r] = r < n ? *reinterpret_cast<const uint4 *>(src + r * stride) : make_uint4(0, 0, 0, 0);
+    const float old = off > 0 ? p.kv_scale[unit] : 0.f;
+    float *kt = ktil_row(p, t, head, lane == 0);
+    float4 k0 = make_float4(0.f, 0.f, 0.f, 0.f), k1 = k0;
+    if (kt != nullptr && kv == 0 && off > 0) {
+        k0 = *reinterpret_cast<const float4 *>(kt + 8 * c);
+        k1 = *reinterpret_cast<const float4 *>(kt + 8 * c + 4);
+    }
+    __nv_bfloat162 m2 = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < kShort; ++r)
+        m2 = amax8(x[r], m2);
+    float amax = larger_of(m2);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const bool inf = __any_sync(0xffffffffu, isinf(amax));
+    if (inf) {
+        amax = 0.f;
+#pragma unroll
+        for (int r = 0; r < kShort; ++r)
+            amax = finite_amax8(x[r], amax);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1)
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    }
+    const float need = pow2_scale(amax);
+    const float scale = off > 0 && old > need ? old : need;
+    const float inv = 1.f / scale;
+    uint8_t *dst = p.kv_pages + unit * (kBlk * kD) + c * 8;
+    if (off > 0 && old != scale)
+        rescale_rows(dst, 0, 1, off, old * inv);
+#pragma unroll
+    for (int r = 0; r < kShort; ++r)
+        if (r < n)
+            *reinterpret_cast<uint2 *>(dst + (off + r) * kD) = round8(x[r], inv, inf);
+    if (c == 0)
+        p.kv_scale[unit] = scale;
+    if (kt != nullptr && kv == 0) {
+        const float was = static_cast<float>(off), now = static_cast<float>(off + n);
+        float sum[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             sum[i] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = r0 + 8 * i;
-            x[i] = make_uint4(0, 0, 0, 0);
-            if (r < n)
-                x[i] = *reinterpret_cast<const uint4 *>(src + r * stride);
-            const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&x[i]);
+        for (int r = 0; r < kShort; ++r)
+            add8(sum, x[r]);
+        *reinterpret_cast<float4 *>(kt + 8 * c) = make_float4((k0.x * was + sum[0]) / now, (k0.y * was + sum[1]) / now,
+                                                              (k0.z * was + sum[2]) / now, (k0.w * was + sum[3]) / now);
+        *reinterpret_cast<float4 *>(kt + 8 * c + 4) = make_float4((k1.x * was + sum[4]) / now, (k1.y * was + sum[5]) / now,
+                                                                  (k1.z * was + sum[6]) / now, (k1.w * was + sum[7]) / now);
+    }
+}
+
+// A run by the whole CTA: 16 threads cover a row of keys or values, 8 rows of each a pass,
+// and all of the run's rows are in registers between the maximum and the rounding.
+__device__ __forceinline__ void append_long(const PagedAppendParams &p, int t, int slot, int n, int head, float *s_amax,
+                                            float (*red)[kD + 4])
+{
+    const int tid = threadIdx.x;
+    const int kv = tid >> 7;             // 0: keys, 1: values
+    const int r0 = (tid & 127) >> 4;     // row phase 0..7
+    const int c = tid & 15;              // dims 8c .. 8c+7
+    const int page = slot / kBlk, off = slot % kBlk;
+    const size_t unit = (static_cast<size_t>(page) * p.H_kv + head) * 2 + kv;
+    const uint16_t *src = (kv ? p.v_new + static_cast<size_t>(t) * p.v_stride
+                              : p.k_new + static_cast<size_t>(t) * p.k_stride) + head * kD + c * 8;
+    const long long stride = kv ? p.v_stride : p.k_stride;
+    uint4 x[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 f = __bfloat1622float2(h[j]);
-                const float a = fabsf(f.x), b = fabsf(f.y);
-                amax = fmaxf(amax, a <= 3.4e38f ? a : 0.f);
-                amax = fmaxf(amax, b <= 3.4e38f ? b : 0.f);
-                sum[2 * j] += f.x;
-                sum[2 * j + 1] += f.y;
-            }
-        }
+    for (int i = 0; i < 8; ++i)
+        x[i] = r0 + 8 * i < n ? *reinterpret_cast<const uint4 *>(src + (r0 + 8 * i) * stride) : make_uint4(0, 0, 0, 0);
+    const float old = off > 0 ? p.kv_scale[unit] : 0.f;
+    float *kt = tid < kD ? ktil_row(p, t, head, tid == 0) : nullptr;
+    const float before = kt != nullptr && off > 0 ? kt[tid] : 0.f;
+    __nv_bfloat162 m2 = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        m2 = amax8(x[i], m2);
+    float amax = larger_of(m2);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if ((tid & 31) == 0)
+        s_amax[tid >> 5] = amax;
+    if (kv == 0) {
+        float sum[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            sum[i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            add8(sum, x[i]);
+        *reinterpret_cast<float4 *>(&red[r0][8 * c]) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+        *reinterpret_cast<float4 *>(&red[r0][8 * c + 4]) = make_float4(sum[4], sum[5], sum[6], sum[7]);
+    }
+    __syncthreads();
+    amax = fmaxf(fmaxf(s_amax[4 * kv], s_amax[4 * kv + 1]), fmaxf(s_amax[4 * kv + 2], s_amax[4 * kv + 3]));
+    const bool inf = __syncthreads_or(isinf(amax)) != 0;
+    if (inf) {
+        amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            amax = finite_amax8(x[i], amax);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         if ((tid & 31) == 0)
             s_amax[tid >> 5] = amax;
-        if (kv == 0)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                red[r0][8 * c + i] = sum[i];
-        const size_t unit = (static_cast<size_t>(page) * p.H_kv + head) * 2 + kv;
-        const float old = off > 0 ? p.kv_scale[unit] : 0.f;
         __syncthreads();
         amax = fmaxf(fmaxf(s_amax[4 * kv], s_amax[4 * kv + 1]), fmaxf(s_amax[4 * kv + 2], s_amax[4 * kv + 3]));
-        const float need = pow2_scale(amax);
-        const float scale = off > 0 && old > need ? old : need;
-        const float inv = 1.f / scale;
-        uint8_t *dst = p.kv_pages + unit * (kBlk * kD) + c * 8;
-        if (off > 0 && old != scale) {
-            const float ratio = old * inv;
-            for (int r = r0; r < off; r += 8) {
-                uint2 *at = reinterpret_cast<uint2 *>(dst + r * kD);
-                uint2 w = *at;
-                w.x = f8x4_scaled(w.x, ratio);
-                w.y = f8x4_scaled(w.y, ratio);
-                *at = w;
-            }
-        }
+    }
+    const float need = pow2_scale(amax);
+    const float scale = off > 0 && old > need ? old : need;
+    const float inv = 1.f / scale;
+    uint8_t *dst = p.kv_pages + unit * (kBlk * kD) + c * 8;
+    if (off > 0 && old != scale)
+        rescale_rows(dst, r0, 8, off, old * inv);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = r0 + 8 * i;
-            if (r < n) {
-                const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&x[i]);
-                float2 f[4];
+    for (int i = 0; i < 8; ++i)
+        if (r0 + 8 * i < n)
+            *reinterpret_cast<uint2 *>(dst + (off + r0 + 8 * i) * kD) = round8(x[i], inv, inf);
+    if ((tid & 127) == 0)
+        p.kv_scale[unit] = scale;
+    if (kt != nullptr) {
+        float sum = 0.f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    f[j] = __bfloat1622float2(h[j]);
-                    f[j].x = fmaf(f[j].x, inv, f[j].x - f[j].x);   // x - x: 0, or NaN for infinities and NaN
-                    f[j].y = fmaf(f[j].y, inv, f[j].y - f[j].y);
-                }
-                *reinterpret_cast<uint2 *>(dst + (off + r) * kD) =
-                    make_uint2(f8x4_pack(f[0].x, f[0].y, f[1].x, f[1].y), f8x4_pack(f[2].x, f[2].y, f[3].x, f[3].y));
-            }
-        }
-        if ((tid & 127) == 0)
-            p.kv_scale[unit] = scale;
-        if (p.ktil != nullptr && tid < kD) {
-            const int b = p.tok_req[t], j = p.tok_pos[t] >> 6;
-            if (b < 0 || b >= p.B || j < 0 || j >= p.N_cap) {
-                if (tid == 0)
-                    report(p.status, SPARSE_ERR_BAD_INDEX);
-            } else {
-                float s = 0.f;
+        for (int r = 0; r < 8; ++r)
+            sum += red[r][tid];
+        kt[tid] = (before * static_cast<float>(off) + sum) / static_cast<float>(off + n);
+    }
+    __syncthreads();   // s_amax and red are free again; every thread has read the old scale
+}
+
+__global__ void __launch_bounds__(kAppendThreads, 3) paged_append_kernel(const PagedAppendParams p)
+{
+    __shared__ float s_amax[8];
+    __shared__ __align__(16) float red[8][kD + 4];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int head = static_cast<int>(blockIdx.x) % p.H_kv;
+    const int t0 = (static_cast<int>(blockIdx.x) / p.H_kv) * p.window;
+    // row i of the window and the 64 behind it: lane `lane` holds rows 32 k + lane.  A run
+    // goes on at row i where the slot is the next of the same page.
+    int slot[4];
+    unsigned goes_on[4];
 #pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    s += red[r][tid];
-                float *kt = p.ktil + ((static_cast<size_t>(b) * p.H_kv + head) * p.N_cap + j) * kD + tid;
-                const float prev = off > 0 ? *kt * static_cast<float>(off) : 0.f;
-                *kt = (prev + s) / static_cast<float>(off + n);
-            }
+    for (int k = 0; k < 4; ++k) {
+        const int i = 32 * k + lane, t = t0 + i;
+        slot[k] = i < p.window + kBlk && t < p.n_tok ? p.slot_map[t] : -1;
+    }
+    const int prev0 = t0 > 0 ? p.slot_map[t0 - 1] : -1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        int prev = __shfl_up_sync(0xffffffffu, slot[k], 1);
+        const int edge = k == 0 ? prev0 : __shfl_sync(0xffffffffu, slot[k > 0 ? k - 1 : 0], 31);
+        if (lane == 0)
+            prev = edge;
+        goes_on[k] = __ballot_sync(0xffffffffu, slot[k] >= 0 && slot[k] % kBlk != 0 && prev == slot[k] - 1);
+    }
+    const uint64_t on_lo = goes_on[0] | static_cast<uint64_t>(goes_on[1]) << 32;
+    const uint64_t on_hi = goes_on[2] | static_cast<uint64_t>(goes_on[3]) << 32;
+    const uint64_t held = __ballot_sync(0xffffffffu, slot[0] >= 0) |
+                          static_cast<uint64_t>(__ballot_sync(0xffffffffu, slot[1] >= 0)) << 32;
+    uint64_t leads = held & ~on_lo;
+    if (p.window < 64)
+        leads &= (1ull << p.window) - 1;
+    // long runs by the CTA, one after another; a short one by a warp
+    int short_no = 0;
+    while (leads != 0) {
+        const int i = __ffsll(static_cast<long long>(leads)) - 1;
+        leads &= leads - 1;
+        const int at = __shfl_sync(0xffffffffu, i < 32 ? slot[0] : slot[1], i & 31);
+        // rows behind i that go on: the bits from i + 1 of the 128
+        const uint64_t rest = i == 63 ? on_hi : (on_lo >> (i + 1)) | (on_hi << (63 - i));
+        const int n = 1 + (~rest == 0 ? 63 : __ffsll(static_cast<long long>(~rest)) - 1);
+        if (at / kBlk >= p.n_pages) {
+            if (threadIdx.x == 0)
+                report(p.status, SPARSE_ERR_BAD_INDEX);
+        } else if (n > kShort) {
+            append_long(p, t0 + i, at, n, head, s_amax, red);
+        } else if (short_no++ % (kAppendThreads / 32) == warp) {
+            append_short(p, t0 + i, at, n, head, lane);
         }
-        __syncthreads();   // s_amax and red are free again; every thread has read the old scale
     }
 }
 
@@ -405,21 +663,34 @@ extern "C" SPARSE_API int sparse_page_plan(const int *seq_len, const int *n_new,
                     n_pages, n_tok);
     if (B > kPlanMaxB)
         return fail(SPARSE_ERR_UNSUPPORTED, "%s: B=%d > %d", name, B, kPlanMaxB);
-    if (n_pages > kMaxPages || max_blocks > kMaxPages)
-        return fail(SPARSE_ERR_UNSUPPORTED, "%s: n_pages=%d or max_blocks=%d > %d", name, n_pages, max_blocks, kMaxPages);
+    if (n_pages > kMaxPages || max_blocks > kMaxPages || n_tok > kMaxRows)
+        return fail(SPARSE_ERR_UNSUPPORTED, "%s: n_pages=%d or max_blocks=%d > %d, or n_tok=%d > %d", name, n_pages,
+                    max_blocks, kMaxPages, n_tok, kMaxRows);
     const PlanParams p{seq_len,    n_new,    block_table, free_pages, n_free, cu_new, start,      seq_len_out,
                        n_free_out, slot_map, tok_req,     tok_pos,    status, B,      max_blocks, n_pages, n_tok};
-    const int smem = (5 * B + 1) * static_cast<int>(sizeof(int));
     sp_host::DeviceInfo dev;
-    static int configured[64];
+    static int configured[2][64];
     int rc = sp_host::device_info(&dev);
     if (rc == SPARSE_OK)
         rc = sp_host::configure_kernel(reinterpret_cast<const void *>(page_plan_kernel),
-                                       (5 * kPlanMaxB + 1) * static_cast<int>(sizeof(int)), dev.device, configured);
+                                       (5 * kPlanMaxB + 1) * static_cast<int>(sizeof(int)), dev.device, configured[0]);
+    if (rc == SPARSE_OK)
+        rc = sp_host::configure_kernel(reinterpret_cast<const void *>(page_rows_kernel),
+                                       (3 * kPlanMaxB + 1) * static_cast<int>(sizeof(int)), dev.device, configured[1]);
     if (rc != SPARSE_OK)
         return rc;
-    return sp_host::cuda_status(
-        launch_pdl(reinterpret_cast<const void *>(page_plan_kernel), dim3(1), kPlanThreads, smem, &p, stream), name);
+    // four requests a thread at most, and four rows where the planning CTA writes them
+    const int with_rows = n_tok <= kRowsOneCta;
+    int threads = 128;
+    while (threads < kPlanThreads && (4 * threads < B || (with_rows && 4 * threads < n_tok)))
+        threads *= 2;
+    rc = sp_host::cuda_status(launch_pdl(reinterpret_cast<const void *>(page_plan_kernel), dim3(1), threads,
+                                         (5 * B + 1) * static_cast<int>(sizeof(int)), stream, p, with_rows), name);
+    if (rc != SPARSE_OK || with_rows)
+        return rc;
+    const unsigned ctas = (static_cast<unsigned>(n_tok) + kRowsPerCta - 1) / kRowsPerCta;
+    return sp_host::cuda_status(launch_pdl(reinterpret_cast<const void *>(page_rows_kernel), dim3(ctas), kRowThreads,
+                                           (3 * B + 1) * static_cast<int>(sizeof(int)), stream, p), name);
 }
 
 extern "C" SPARSE_API int sparse_paged_append_f8(uint8_t *kv_pages, float *kv_scale, int n_pages, int H_kv,
@@ -443,9 +714,10 @@ extern "C" SPARSE_API int sparse_paged_append_f8(uint8_t *kv_pages, float *kv_sc
     if (k_stride < width || v_stride < width || k_stride % 8 != 0 || v_stride % 8 != 0)
         return fail(SPARSE_ERR_INVALID_ARG, "%s: token strides %lld, %lld: at least %lld and a multiple of 8", name,
                     k_stride, v_stride, width);
-    if (n_pages > kMaxPages || H_kv > 65535)
-        return fail(SPARSE_ERR_UNSUPPORTED, "%s: n_pages=%d > %d or H_kv=%d > 65535", name, n_pages, kMaxPages, H_kv);
-    int window = 1;
+    if (n_pages > kMaxPages || H_kv > 65535 || n_tok > kMaxRows)
+        return fail(SPARSE_ERR_UNSUPPORTED, "%s: n_pages=%d > %d, H_kv=%d > 65535 or n_tok=%d > %d", name, n_pages, kMaxPages,
+                    H_kv, n_tok, kMaxRows);
+    int window = 8;
     sp_host::DeviceInfo dev;
     static int configured[64];
     int rc = sp_host::device_info(&dev);
@@ -453,11 +725,15 @@ extern "C" SPARSE_API int sparse_paged_append_f8(uint8_t *kv_pages, float *kv_sc
         rc = sp_host::configure_kernel(reinterpret_cast<const void *>(paged_append_kernel), 0, dev.device, configured);
     if (rc != SPARSE_OK)
         return rc;
-    while (window < kBlk && static_cast<long long>(n_tok) * H_kv > 16LL * dev.sm_count * window)
+    // rows a CTA looks over: with 8, every warp has a row of a decode step; more, up to a
+    // block's 64, once that alone makes over 8 CTAs an SM (prompts have a run in 64 rows)
+    while (window < kBlk && static_cast<long long>(n_tok) * H_kv > 8LL * dev.sm_count * window)
         window *= 2;
     const PagedAppendParams p{kv_pages, kv_scale, k_new, v_new, slot_map, ktil, tok_req, tok_pos, status, k_stride, v_stride,
                               n_pages, H_kv, n_tok, window, B, N_cap};
-    const dim3 grid((static_cast<unsigned>(n_tok) + window - 1) / window, static_cast<unsigned>(H_kv));
-    return sp_host::cuda_status(
-        launch_pdl(reinterpret_cast<const void *>(paged_append_kernel), grid, kAppendThreads, 0, &p, stream), name);
+    const long long ctas = (static_cast<long long>(n_tok) + window - 1) / window * H_kv;
+    if (ctas > INT_MAX)
+        return fail(SPARSE_ERR_UNSUPPORTED, "%s: n_tok=%d rows of %d heads in one call", name, n_tok, H_kv);
+    return sp_host::cuda_status(launch_pdl(reinterpret_cast<const void *>(paged_append_kernel),
+                                           dim3(static_cast<unsigned>(ctas)), kAppendThreads, 0, stream, p), name);
 }

@@ -8,6 +8,7 @@
 namespace {
 
 constexpr int kMaxPages = 1 << 25;   // 64 * page fits an int32 slot
+constexpr int kMaxRows = 1 << 30;    // rows of one call
 
 // Two fp32 values to e4m3, round to nearest even, beyond +-448 to +-448, NaN to NaN; `lo`
 // in the low byte.
@@ -44,10 +45,10 @@ __device__ __forceinline__ uint32_t f8x4_scaled(uint32_t w, float ratio)
     return f8x4_pack(a.x * ratio, a.y * ratio, b.x * ratio, b.y * ratio);
 }
 
-// One launch of a kernel that takes one parameter struct, with programmatic stream
-// serialization: it may be scheduled while the kernel before it drains.
-template <typename Params>
-cudaError_t launch_pdl(const void *kern, dim3 grid, int threads, int smem, const Params *prm, void *stream)
+// One launch with programmatic stream serialization: the kernel may be scheduled while the
+// one before it drains.
+template <typename... Args>
+cudaError_t launch_pdl(const void *kern, dim3 grid, int threads, int smem, void *stream, const Args &...args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -59,8 +60,8 @@ cudaError_t launch_pdl(const void *kern, dim3 grid, int threads, int smem, const
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    void *args[] = {const_cast<Params *>(prm)};
-    return cudaLaunchKernelExC(&cfg, kern, args);
+    void *list[] = {const_cast<void *>(static_cast<const void *>(&args))...};
+    return cudaLaunchKernelExC(&cfg, kern, list);
 }
 
 }  // namespace

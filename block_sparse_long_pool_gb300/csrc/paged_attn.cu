@@ -708,18 +708,9 @@ int launch(const PagedAttnParams &p, const CUtensorMap &map, const sp_host::Devi
     const int rc = sp_host::configure_kernel(kern, Smem<NT>::kBytes, dev.device, configured);
     if (rc != SPARSE_OK)
         return rc;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(kCtasPerSm * dev.sm_count));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Smem<NT>::kBytes;
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    void *args[] = {const_cast<CUtensorMap *>(&map), const_cast<PagedAttnParams *>(&p)};
-    return sp_host::cuda_status(cudaLaunchKernelExC(&cfg, kern, args), name);
+    return sp_host::cuda_status(
+        launch_pdl(kern, dim3(static_cast<unsigned>(kCtasPerSm * dev.sm_count)), kThreads, Smem<NT>::kBytes, stream, map, p),
+        name);
 }
 
 }  // namespace

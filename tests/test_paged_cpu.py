@@ -35,6 +35,8 @@ ATTN = dict(Q=FAKE, pages=FAKE, scale=FAKE, n_pages=32, table=FAKE, max_blocks=8
     ("sparse_page_plan", PLAN, {"B": 4097}, UNSUPPORTED),
     ("sparse_page_plan", PLAN, {"n_pages": (1 << 25) + 1}, UNSUPPORTED),
     ("sparse_page_plan", PLAN, {"max_blocks": (1 << 25) + 1}, UNSUPPORTED),
+    ("sparse_page_plan", PLAN, {"n_tok": (1 << 30) + 1}, UNSUPPORTED),
+    ("sparse_paged_append_f8", APPEND, {"n_tok": (1 << 30) + 1}, UNSUPPORTED),
     *[("sparse_paged_append_f8", APPEND, {x: None}, INVALID) for x in ("pages", "scale", "k", "v", "slot", "req", "pos")],
     *[("sparse_paged_append_f8", APPEND, {x: ODD}, INVALID) for x in ("pages", "scale", "k", "v", "slot", "ktil", "req", "pos")],
     *[("sparse_paged_append_f8", APPEND, {x: 0}, INVALID) for x in ("n_pages", "H", "n_tok", "B", "N_cap")],
