@@ -479,43 +479,52 @@ def sparse_prefill_select(F, ktil, seq_len, n_init: int, n_local: int, k: int, i
 _F8 = torch.float8_e4m3fn
 
 
-def _on(dev, **tensors):
-    """Every tensor on ``dev``: (tensor, dtype, shape) each, or None."""
-    for name, spec in tensors.items():
-        if spec is None:
-            continue
-        t, dtype, shape = spec
-        if isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.shape == shape and t.is_contiguous():
-            continue
+# The calls of this cache are short: a decode step's plan or append takes a few microseconds
+# on the device.  So their arguments are checked in one pass of plain comparisons, and what
+# is wrong is looked for (_explain) only when something is.
+
+
+def _sound(idx, specs) -> bool:
+    """Whether every (tensor, dtype, shape) is contiguous on device ``idx``."""
+    try:
+        for t, dtype, shape in specs:
+            if t.dtype is not dtype or t.shape != shape or t.get_device() != idx or not t.is_contiguous():
+                return False
+    except AttributeError:   # not a tensor
+        return False
+    return True
+
+
+def _explain(idx, names, specs):
+    for name, (t, dtype, shape) in zip(names, specs):
         _need(t, name, dtype, shape=shape)
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+        if t.get_device() != idx:
+            raise ValueError(f"{name} is on {t.device}, expected device {idx}")
 
 
-def _call(name, dev, stream, *args):
-    """The C entry point on ``dev``, which need not be the current device."""
-    fn = getattr(load(), name)
-    if dev.index == torch.cuda.current_device():
-        rc = fn(*args, stream.cuda_stream if stream is not None else torch.cuda.current_stream().cuda_stream)
+def _call(fn, name, idx, stream, *args):
+    """The C entry point on device ``idx``, which need not be the current one."""
+    if idx == torch._C._cuda_getDevice():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(idx) if stream is None else stream.cuda_stream)
     else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, stream.cuda_stream if stream is not None else torch.cuda.current_stream().cuda_stream)
-    _check(rc, name)
+        with torch.cuda.device(idx):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(idx) if stream is None else stream.cuda_stream)
+    if rc != SPARSE_OK:
+        _check(rc, name)
 
 
-def _device_of(t, name):
+def _device_index(t, name) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+    return t.get_device()
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _status_spec(status):
-    return None if status is None else (status, torch.int32, (1,))
+def _tensors(*named):
+    for name, t in named:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
 
 
 def sparse_page_plan(seq_len, n_new, block_table, free_pages, n_free, cu_new, start, seq_len_out, n_free_out, slot_map,
@@ -525,21 +534,28 @@ def sparse_page_plan(seq_len, n_new, block_table, free_pages, n_free, cu_new, st
     the list free_pages [n_pages] (the first n_free [1]) into block_table [B][max_blocks].
     Writes cu_new [B + 1], start [B] (-1: not granted), seq_len_out [B], n_free_out [1] (the
     last two may be seq_len and n_free themselves) and slot_map, tok_req, tok_pos [n_tok]."""
-    dev = _device_of(block_table, "block_table")
+    idx = _device_index(block_table, "block_table")
+    _tensors(("free_pages", free_pages), ("slot_map", slot_map))
     i32 = torch.int32
     B, max_blocks = block_table.shape
     n_pages, n_tok = free_pages.numel(), slot_map.numel()
-    _on(dev, block_table=(block_table, i32, (B, max_blocks)), seq_len=(seq_len, i32, (B,)), n_new=(n_new, i32, (B,)),
-        free_pages=(free_pages, i32, (n_pages,)), n_free=(n_free, i32, (1,)), cu_new=(cu_new, i32, (B + 1,)),
-        start=(start, i32, (B,)), seq_len_out=(seq_len_out, i32, (B,)), n_free_out=(n_free_out, i32, (1,)),
-        slot_map=(slot_map, i32, (n_tok,)), tok_req=(tok_req, i32, (n_tok,)), tok_pos=(tok_pos, i32, (n_tok,)),
-        status=_status_spec(status))
-    _call("sparse_page_plan", dev, stream, seq_len.data_ptr(), n_new.data_ptr(), B, block_table.data_ptr(), max_blocks,
-          free_pages.data_ptr(), n_pages, n_free.data_ptr(), cu_new.data_ptr(), start.data_ptr(), seq_len_out.data_ptr(),
-          n_free_out.data_ptr(), slot_map.data_ptr(), tok_req.data_ptr(), tok_pos.data_ptr(), n_tok, _addr(status))
+    per_request, one, rows = (B,), (1,), (n_tok,)
+    specs = [(block_table, i32, (B, max_blocks)), (seq_len, i32, per_request), (n_new, i32, per_request),
+             (free_pages, i32, (n_pages,)), (n_free, i32, one), (cu_new, i32, (B + 1,)), (start, i32, per_request),
+             (seq_len_out, i32, per_request), (n_free_out, i32, one), (slot_map, i32, rows), (tok_req, i32, rows),
+             (tok_pos, i32, rows)]
+    if status is not None:
+        specs.append((status, i32, one))
+    if not _sound(idx, specs):
+        _explain(idx, ("block_table", "seq_len", "n_new", "free_pages", "n_free", "cu_new", "start", "seq_len_out",
+                       "n_free_out", "slot_map", "tok_req", "tok_pos", "status"), specs)
+    _call((_lib or load()).sparse_page_plan, "sparse_page_plan", idx, stream, seq_len.data_ptr(), n_new.data_ptr(), B,
+          block_table.data_ptr(), max_blocks, free_pages.data_ptr(), n_pages, n_free.data_ptr(), cu_new.data_ptr(),
+          start.data_ptr(), seq_len_out.data_ptr(), n_free_out.data_ptr(), slot_map.data_ptr(), tok_req.data_ptr(),
+          tok_pos.data_ptr(), n_tok, None if status is None else status.data_ptr())
 
 
-def _new_rows(t, name, dev, n_tok, H_kv):
+def _token_stride(t, name, idx, n_tok, H_kv):
     """Token stride of k_new / v_new [n_tok][H_kv][128], whose tokens may be apart."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -547,12 +563,12 @@ def _new_rows(t, name, dev, n_tok, H_kv):
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     if t.shape != (n_tok, H_kv, D):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n_tok, H_kv, D)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.get_device() != idx:
+        raise ValueError(f"{name} is on {t.device}, expected device {idx}")
     step, head, dim = t.stride()
     if dim != 1 or (head != D and H_kv > 1):
         raise ValueError(f"{name}: the values of a token must be contiguous")
-    return step if n_tok > 1 else max(step - step % 8, H_kv * D)
+    return step if n_tok > 1 else H_kv * D   # one token: its stride is not used
 
 
 def sparse_paged_append_f8(kv_pages, kv_scale, k_new, v_new, slot_map, ktil=None, tok_req=None, tok_pos=None,
@@ -561,23 +577,35 @@ def sparse_paged_append_f8(kv_pages, kv_scale, k_new, v_new, slot_map, ktil=None
     to e4m3 and write them to slot_map [n_tok] of kv_pages [n_pages][H_kv][2][64][128]
     (torch.float8_e4m3fn), with kv_scale [n_pages][H_kv][2] fp32; with ktil
     [B][H_kv][N_cap][128], tok_req and tok_pos [n_tok], update the compressed keys."""
-    dev = _device_of(kv_pages, "kv_pages")
+    idx = _device_index(kv_pages, "kv_pages")
+    _tensors(("slot_map", slot_map))
     n_pages, H_kv = kv_pages.shape[:2]
     n_tok = slot_map.numel()
-    i32 = torch.int32
-    _on(dev, kv_pages=(kv_pages, _F8, (n_pages, H_kv, 2, BLK, D)), kv_scale=(kv_scale, torch.float32, (n_pages, H_kv, 2)),
-        slot_map=(slot_map, i32, (n_tok,)), status=_status_spec(status))
-    ks, vs = _new_rows(k_new, "k_new", dev, n_tok, H_kv), _new_rows(v_new, "v_new", dev, n_tok, H_kv)
+    i32, f32, rows = torch.int32, torch.float32, (n_tok,)
+    ks, vs = _token_stride(k_new, "k_new", idx, n_tok, H_kv), _token_stride(v_new, "v_new", idx, n_tok, H_kv)
+    specs = [(kv_pages, _F8, (n_pages, H_kv, 2, BLK, D)), (kv_scale, f32, (n_pages, H_kv, 2)), (slot_map, i32, rows)]
+    names = ["kv_pages", "kv_scale", "slot_map"]
     B = N_cap = 0
+    kt = req = pos = st = None
     if ktil is not None:
         if tok_req is None or tok_pos is None:
             raise ValueError("ktil needs tok_req and tok_pos")
-        B, N_cap = ktil.shape[0], ktil.shape[2]
-        _on(dev, ktil=(ktil, torch.float32, (B, H_kv, N_cap, D)), tok_req=(tok_req, i32, (n_tok,)),
-            tok_pos=(tok_pos, i32, (n_tok,)))
-    _call("sparse_paged_append_f8", dev, stream, kv_pages.data_ptr(), kv_scale.data_ptr(), n_pages, H_kv, k_new.data_ptr(),
-          v_new.data_ptr(), ks, vs, slot_map.data_ptr(), n_tok, _addr(ktil), B, N_cap, _addr(tok_req), _addr(tok_pos),
-          _addr(status))
+        _tensors(("ktil", ktil))
+        B, _, N_cap, _ = ktil.shape
+        specs += [(ktil, f32, (B, H_kv, N_cap, D)), (tok_req, i32, rows), (tok_pos, i32, rows)]
+        names += ["ktil", "tok_req", "tok_pos"]
+    if status is not None:
+        specs.append((status, i32, (1,)))
+        names.append("status")
+    if not _sound(idx, specs):
+        _explain(idx, names, specs)
+    if status is not None:
+        st = status.data_ptr()
+    if ktil is not None:
+        kt, req, pos = ktil.data_ptr(), tok_req.data_ptr(), tok_pos.data_ptr()
+    _call((_lib or load()).sparse_paged_append_f8, "sparse_paged_append_f8", idx, stream, kv_pages.data_ptr(),
+          kv_scale.data_ptr(), n_pages, H_kv, k_new.data_ptr(), v_new.data_ptr(), ks, vs, slot_map.data_ptr(), n_tok, kt, B,
+          N_cap, req, pos, st)
 
 
 def sparse_paged_decode_attn_f8_workspace_size(B: int, H_q: int, H_kv: int) -> int:
@@ -597,21 +625,40 @@ def sparse_paged_decode_attn_f8(Q, kv_pages, kv_scale, block_table, seq_len, O, 
     """O [B][H_q][128] = attention of Q over the pages that block_table [B][max_blocks] names:
     every block of each request's seq_len [B] tokens, or the logical blocks blk_idx
     [B][H_kv][k_tot] with count [B][H_kv]."""
-    dev = _device_of(kv_pages, "kv_pages")
+    idx = _device_index(kv_pages, "kv_pages")
+    _tensors(("Q", Q), ("block_table", block_table), ("workspace", workspace))
     n_pages, H_kv = kv_pages.shape[:2]
     B, max_blocks = block_table.shape
     H_q = Q.shape[1]
     i32, f32, b16 = torch.int32, torch.float32, torch.bfloat16
+    ws_bytes = workspace.numel()
+    specs = [(kv_pages, _F8, (n_pages, H_kv, 2, BLK, D)), (kv_scale, f32, (n_pages, H_kv, 2)), (Q, b16, (B, H_q, D)),
+             (O, b16, (B, H_q, D)), (block_table, i32, (B, max_blocks)), (seq_len, i32, (B,)),
+             (workspace, torch.uint8, (ws_bytes,))]
+    names = ["kv_pages", "kv_scale", "Q", "O", "block_table", "seq_len", "workspace"]
     k_tot = 0
+    blocks = counts = lse_at = st = None
     if blk_idx is not None:
         if count is None:
             raise ValueError("blk_idx needs count")
+        _tensors(("blk_idx", blk_idx), ("count", count))
         k_tot = blk_idx.shape[2]
-        _on(dev, blk_idx=(blk_idx, i32, (B, H_kv, k_tot)), count=(count, i32, (B, H_kv)))
-    _on(dev, Q=(Q, b16, (B, H_q, D)), kv_pages=(kv_pages, _F8, (n_pages, H_kv, 2, BLK, D)),
-        kv_scale=(kv_scale, f32, (n_pages, H_kv, 2)), block_table=(block_table, i32, (B, max_blocks)),
-        seq_len=(seq_len, i32, (B,)), O=(O, b16, (B, H_q, D)), workspace=(workspace, torch.uint8, (workspace.numel(),)),
-        lse=None if lse is None else (lse, f32, (B, H_q)), status=_status_spec(status))
-    _call("sparse_paged_decode_attn_f8", dev, stream, Q.data_ptr(), kv_pages.data_ptr(), kv_scale.data_ptr(), n_pages,
-          block_table.data_ptr(), max_blocks, _addr(blk_idx), _addr(count), k_tot, seq_len.data_ptr(), B, H_q, H_kv,
-          float(scale), O.data_ptr(), _addr(lse), workspace.data_ptr(), workspace.numel(), _addr(status))
+        specs += [(blk_idx, i32, (B, H_kv, k_tot)), (count, i32, (B, H_kv))]
+        names += ["blk_idx", "count"]
+    if lse is not None:
+        specs.append((lse, f32, (B, H_q)))
+        names.append("lse")
+    if status is not None:
+        specs.append((status, i32, (1,)))
+        names.append("status")
+    if not _sound(idx, specs):
+        _explain(idx, names, specs)
+    if blk_idx is not None:
+        blocks, counts = blk_idx.data_ptr(), count.data_ptr()
+    if lse is not None:
+        lse_at = lse.data_ptr()
+    if status is not None:
+        st = status.data_ptr()
+    _call((_lib or load()).sparse_paged_decode_attn_f8, "sparse_paged_decode_attn_f8", idx, stream, Q.data_ptr(),
+          kv_pages.data_ptr(), kv_scale.data_ptr(), n_pages, block_table.data_ptr(), max_blocks, blocks, counts, k_tot,
+          seq_len.data_ptr(), B, H_q, H_kv, scale, O.data_ptr(), lse_at, workspace.data_ptr(), ws_bytes, st)

@@ -19,8 +19,8 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanMaxB = 4096;
 constexpr int kPlanPer = kPlanMaxB / kPlanThreads;   // requests a thread scans, at most
 constexpr int kRowThreads = 256;
-constexpr int kRowsPerCta = 4096;
-constexpr int kRowsOneCta = 4096;   // rows that the planning CTA writes itself
+constexpr int kRowsPerCta = 1024;
+constexpr int kRowsOneCta = 1024;   // rows that the planning CTA writes itself
 
 struct PlanParams {
     const int *seq_len;
@@ -87,71 +87,68 @@ __device__ __forceinline__ int pages_taken(const int *cu, const int *first, int 
     return st < 0 ? 0 : (st + (cu[b + 1] - cu[b]) + kBlk - 1) / kBlk - (st + kBlk - 1) / kBlk;
 }
 
-// Rows [t0, t0 + n) (t0 a multiple of 4): four rows a thread, stored as one 16-byte word.
-// The first row's request comes from a binary search, the next rows' from a step.  A new
-// block's page is read from the free list and entered into the table by the row that
-// starts the block.
+// Rows [t0, t0 + n), R of them (1 or 4, t0 a multiple of R) a thread and pass: the first
+// row's request by binary search, the next rows' by steps from it; then the pages, whose
+// loads are in flight together; then the three entries, as words of R.  A new block's page
+// comes from the free list and is entered into the table by the row that starts the block.
+template <int R>
 __device__ __forceinline__ void plan_rows(const PlanParams &p, const int *cu, const int *first, const int *npre, int F,
                                           int t0, int n)
 {
     const int total = cu[p.B];
-    for (int i = 4 * static_cast<int>(threadIdx.x); i < n; i += 4 * static_cast<int>(blockDim.x)) {
-        int slot[4], req[4], pos[4];
+    for (int i = R * static_cast<int>(threadIdx.x); i < n; i += R * static_cast<int>(blockDim.x)) {
+        const int t = t0 + i;
         int b = 0;
-        if (t0 + i < total) {
+        if (t < total) {
             int hi = p.B - 1;
             while (b < hi) {
                 const int mid = (b + hi) >> 1;
-                if (cu[mid + 1] > t0 + i)
+                if (cu[mid + 1] > t)
                     hi = mid;
                 else
                     b = mid + 1;
             }
         }
-        int page = -1, of = -1;   // the page of block `of` of request b
+        int slot[R], req[R], pos[R], page[R];
+        const int *from[R];
+        int *to[R];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int t = t0 + i + j;
-            slot[j] = req[j] = pos[j] = -1;
-            if (t < total && i + j < n) {
-                while (cu[b + 1] <= t) {
+        for (int j = 0; j < R; ++j) {
+            req[j] = pos[j] = -1;
+            from[j] = to[j] = nullptr;
+            if (t + j < total && i + j < n) {
+                while (cu[b + 1] <= t + j)
                     ++b;
-                    of = -1;
-                }
                 const int st = first[b];
                 if (st >= 0) {
                     req[j] = b;
-                    pos[j] = st + t - cu[b];
-                    const int blk = pos[j] / kBlk;
-                    if (blk != of) {
-                        of = blk;
-                        const int used = (st + kBlk - 1) / kBlk;
-                        const size_t at = static_cast<size_t>(b) * p.max_blocks + blk;
-                        if (blk < used) {
-                            page = p.block_table[at];
-                        } else {
-                            page = p.free_pages[F - 1 - (npre[b] + blk - used)];
-                            if (pos[j] % kBlk == 0)
-                                p.block_table[at] = page;
-                        }
-                        if (page < 0 || page >= p.n_pages) {
-                            report(p.status, SPARSE_ERR_BAD_INDEX);
-                            page = -1;
-                        }
-                    }
-                    if (page >= 0)
-                        slot[j] = page * kBlk + pos[j] % kBlk;
+                    pos[j] = st + t + j - cu[b];
+                    const int blk = pos[j] / kBlk, used = (st + kBlk - 1) / kBlk;
+                    int *at = p.block_table + static_cast<size_t>(b) * p.max_blocks + blk;
+                    from[j] = blk < used ? at : p.free_pages + (F - 1 - (npre[b] + blk - used));
+                    to[j] = blk >= used && pos[j] % kBlk == 0 ? at : nullptr;
                 }
             }
         }
-        const int t = t0 + i;
-        if (t + 3 < p.n_tok) {
-            *reinterpret_cast<int4 *>(p.slot_map + t) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-            *reinterpret_cast<int4 *>(p.tok_req + t) = make_int4(req[0], req[1], req[2], req[3]);
-            *reinterpret_cast<int4 *>(p.tok_pos + t) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+            page[j] = from[j] != nullptr ? *from[j] : -1;
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            if (to[j] != nullptr)
+                *to[j] = page[j];
+            const bool ok = page[j] >= 0 && page[j] < p.n_pages;
+            if (from[j] != nullptr && !ok)
+                report(p.status, SPARSE_ERR_BAD_INDEX);
+            slot[j] = ok ? page[j] * kBlk + pos[j] % kBlk : -1;
+        }
+        if (R == 4 && t + 3 < p.n_tok) {
+            *reinterpret_cast<int4 *>(p.slot_map + t) = make_int4(slot[0], slot[R > 1 ? 1 : 0], slot[R > 2 ? 2 : 0], slot[R - 1]);
+            *reinterpret_cast<int4 *>(p.tok_req + t) = make_int4(req[0], req[R > 1 ? 1 : 0], req[R > 2 ? 2 : 0], req[R - 1]);
+            *reinterpret_cast<int4 *>(p.tok_pos + t) = make_int4(pos[0], pos[R > 1 ? 1 : 0], pos[R > 2 ? 2 : 0], pos[R - 1]);
         } else {
 #pragma unroll
-            for (int j = 0; j < 3; ++j)
+            for (int j = 0; j < R; ++j)
                 if (t + j < p.n_tok) {
                     p.slot_map[t + j] = slot[j];
                     p.tok_req[t + j] = req[j];
@@ -168,13 +165,12 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
     int *cu = plan_smem;                 // [B + 1]
     int *first = cu + p.B + 1;           // [B] start, -1: not granted
     int *npre = first + p.B;             // [B] pages granted before the request's own
-    int *rel = npre + p.B;               // [B] pages returned
-    int *relpre = rel + p.B;             // [B] pages returned before the request's own
+    int *relpre = npre + p.B;            // [B] pages returned before the request's own
     griddep_wait();
     griddep_launch_dependents();
 
     const int tid = threadIdx.x;
-    const int per = (p.B + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x);
+    const int per = (p.B + kPlanThreads - 1) / kPlanThreads;
     long long len[kPlanPer], add[kPlanPer];
     bool ends[kPlanPer], sound[kPlanPer];
     long long s_rel = 0, s_add = 0;
@@ -229,12 +225,9 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
                 if (fits[i])
                     need[i] = (len[i] + add[i] + kBlk - 1) / kBlk - (len[i] + kBlk - 1) / kBlk;
                 s_need += need[i];
-                rel[b] = 0;
-                if (ends[i] && sound[i]) {
-                    rel[b] = static_cast<int>((len[i] + kBlk - 1) / kBlk);
-                    relpre[b] = saturate(o_rel);
-                    o_rel += rel[b];
-                }
+                relpre[b] = saturate(o_rel);   // the last of equal ones holds the pages
+                if (ends[i] && sound[i])
+                    o_rel += (len[i] + kBlk - 1) / kBlk;
             }
         }
     }
@@ -269,15 +262,23 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
     if (tid == 0)
         p.n_free_out[0] = F - static_cast<int>(all_taken);
     if (all_rel > 0) {
-        // returned pages: a warp takes a request, its lanes the request's blocks
-        for (int b = tid >> 5; b < p.B; b += static_cast<int>(blockDim.x) / 32)
-            for (int j = tid & 31; j < rel[b]; j += 32)
-                if (static_cast<long long>(F0) + relpre[b] + j < p.n_pages)
-                    p.free_pages[F0 + relpre[b] + j] = p.block_table[static_cast<size_t>(b) * p.max_blocks + j];
+        // returned pages, one a thread: its request by binary search
+        const int end = static_cast<int>(min(all_rel, static_cast<long long>(p.n_pages - F0)));
+        for (int i = tid; i < end; i += kPlanThreads) {
+            int b = 0, hi = p.B - 1;
+            while (b < hi) {
+                const int mid = (b + hi + 1) >> 1;
+                if (relpre[mid] <= i)
+                    b = mid;
+                else
+                    hi = mid - 1;
+            }
+            p.free_pages[F0 + i] = p.block_table[static_cast<size_t>(b) * p.max_blocks + i - relpre[b]];
+        }
         __syncthreads();
     }
     if (with_rows)
-        plan_rows(p, cu, first, npre, F, 0, p.n_tok);
+        plan_rows<1>(p, cu, first, npre, F, 0, p.n_tok);
 }
 
 // Steps with many rows: the grid writes them after page_plan_kernel, whose outputs give it
@@ -311,12 +312,13 @@ __global__ void __launch_bounds__(kRowThreads) page_rows_kernel(const PlanParams
     }
     __syncthreads();
     const int t0 = static_cast<int>(blockIdx.x) * kRowsPerCta;
-    plan_rows(p, cu, first, npre, p.n_free_out[0] + static_cast<int>(all), t0, min(p.n_tok - t0, kRowsPerCta));
+    plan_rows<4>(p, cu, first, npre, p.n_free_out[0] + static_cast<int>(all), t0, min(p.n_tok - t0, kRowsPerCta));
 }
 
 // ---------------------------------------------------------------- append
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
+constexpr int kAhead = 4;       // CTAs an SM ahead whose rows a CTA brings into L2
 constexpr int kShort = 2;       // rows of a run that one warp appends
 constexpr int kMinExp = -120;   // least exponent of a scale: its reciprocal is a normal fp32 value
 
@@ -338,6 +340,7 @@ struct PagedAppendParams {
     int window;
     int B;
     int N_cap;
+    int ahead;
 };
 
 // The least power of two s >= 2^kMinExp with amax <= 448 s: 448 = 1.75 * 2^8, so the
@@ -506,15 +509,14 @@ __device__ __forceinline__ void append_short(const PagedAppendParams &p, int t, 
     }
 }
 
-// A run by the whole CTA: 16 threads cover a row of keys or values, 8 rows of each a pass,
+// A run's keys (kv = 0) or values by the whole CTA: 16 threads cover a row, 8 rows a pass,
 // and all of the run's rows are in registers between the maximum and the rounding.
-__device__ __forceinline__ void append_long(const PagedAppendParams &p, int t, int slot, int n, int head, float *s_amax,
-                                            float (*red)[kD + 4])
+__device__ __forceinline__ void append_long(const PagedAppendParams &p, int t, int slot, int n, int head, int kv,
+                                            float *s_amax, float (*red)[kD + 4])
 {
     const int tid = threadIdx.x;
-    const int kv = tid >> 7;             // 0: keys, 1: values
-    const int r0 = (tid & 127) >> 4;     // row phase 0..7
-    const int c = tid & 15;              // dims 8c .. 8c+7
+    const int r0 = tid >> 4;     // row phase 0..7
+    const int c = tid & 15;      // dims 8c .. 8c+7
     const int page = slot / kBlk, off = slot % kBlk;
     const size_t unit = (static_cast<size_t>(page) * p.H_kv + head) * 2 + kv;
     const uint16_t *src = (kv ? p.v_new + static_cast<size_t>(t) * p.v_stride
@@ -525,7 +527,7 @@ __device__ __forceinline__ void append_long(const PagedAppendParams &p, int t, i
     for (int i = 0; i < 8; ++i)
         x[i] = r0 + 8 * i < n ? *reinterpret_cast<const uint4 *>(src + (r0 + 8 * i) * stride) : make_uint4(0, 0, 0, 0);
     const float old = off > 0 ? p.kv_scale[unit] : 0.f;
-    float *kt = tid < kD ? ktil_row(p, t, head, tid == 0) : nullptr;
+    float *kt = kv == 0 ? ktil_row(p, t, head, tid == 0) : nullptr;
     const float before = kt != nullptr && off > 0 ? kt[tid] : 0.f;
     __nv_bfloat162 m2 = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
@@ -537,7 +539,7 @@ __device__ __forceinline__ void append_long(const PagedAppendParams &p, int t, i
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     if ((tid & 31) == 0)
         s_amax[tid >> 5] = amax;
-    if (kv == 0) {
+    if (kt != nullptr) {
         float sum[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -549,9 +551,10 @@ __device__ __forceinline__ void append_long(const PagedAppendParams &p, int t, i
         *reinterpret_cast<float4 *>(&red[r0][8 * c + 4]) = make_float4(sum[4], sum[5], sum[6], sum[7]);
     }
     __syncthreads();
-    amax = fmaxf(fmaxf(s_amax[4 * kv], s_amax[4 * kv + 1]), fmaxf(s_amax[4 * kv + 2], s_amax[4 * kv + 3]));
-    const bool inf = __syncthreads_or(isinf(amax)) != 0;
+    amax = fmaxf(fmaxf(s_amax[0], s_amax[1]), fmaxf(s_amax[2], s_amax[3]));
+    const bool inf = isinf(amax);   // the same for all threads
     if (inf) {
+        __syncthreads();   // s_amax has been read
         amax = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -562,7 +565,7 @@ __device__ __forceinline__ void append_long(const PagedAppendParams &p, int t, i
         if ((tid & 31) == 0)
             s_amax[tid >> 5] = amax;
         __syncthreads();
-        amax = fmaxf(fmaxf(s_amax[4 * kv], s_amax[4 * kv + 1]), fmaxf(s_amax[4 * kv + 2], s_amax[4 * kv + 3]));
+        amax = fmaxf(fmaxf(s_amax[0], s_amax[1]), fmaxf(s_amax[2], s_amax[3]));
     }
     const float need = pow2_scale(amax);
     const float scale = off > 0 && old > need ? old : need;
@@ -574,7 +577,7 @@ __device__ __forceinline__ void append_long(const PagedAppendParams &p, int t, i
     for (int i = 0; i < 8; ++i)
         if (r0 + 8 * i < n)
             *reinterpret_cast<uint2 *>(dst + (off + r0 + 8 * i) * kD) = round8(x[i], inv, inf);
-    if ((tid & 127) == 0)
+    if (tid == 0)
         p.kv_scale[unit] = scale;
     if (kt != nullptr) {
         float sum = 0.f;
@@ -586,15 +589,30 @@ __device__ __forceinline__ void append_long(const PagedAppendParams &p, int t, i
     __syncthreads();   // s_amax and red are free again; every thread has read the old scale
 }
 
-__global__ void __launch_bounds__(kAppendThreads, 3) paged_append_kernel(const PagedAppendParams p)
+// CTA (window, head, K or V): the runs that start in the window.  Of the window's short
+// runs, which a warp appends whole, the K and the V CTA take four in turn.
+__global__ void __launch_bounds__(kAppendThreads, 8) paged_append_kernel(const PagedAppendParams p)
 {
-    __shared__ float s_amax[8];
+    __shared__ float s_amax[4];
     __shared__ __align__(16) float red[8][kD + 4];
     griddep_wait();
     griddep_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int head = static_cast<int>(blockIdx.x) % p.H_kv;
-    const int t0 = (static_cast<int>(blockIdx.x) / p.H_kv) * p.window;
+    const int kv = static_cast<int>(blockIdx.x) & 1;
+    const int head = static_cast<int>(blockIdx.x >> 1) % p.H_kv;
+    const int t0 = (static_cast<int>(blockIdx.x >> 1) / p.H_kv) * p.window;
+    if (static_cast<long long>(blockIdx.x) + p.ahead < gridDim.x) {
+        // rows that a CTA of the next wave reads, into L2
+        const int bx = static_cast<int>(blockIdx.x) + p.ahead;
+        const int r = threadIdx.x >> 1, half = threadIdx.x & 1;
+        const int t = ((bx >> 1) / p.H_kv) * p.window + r;
+        if (r < p.window && t < p.n_tok) {
+            const uint16_t *at = ((bx & 1) ? p.v_new + static_cast<size_t>(t) * p.v_stride
+                                           : p.k_new + static_cast<size_t>(t) * p.k_stride) +
+                                 ((bx >> 1) % p.H_kv) * kD + 64 * half;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+        }
+    }
     // row i of the window and the 64 behind it: lane `lane` holds rows 32 k + lane.  A run
     // goes on at row i where the slot is the next of the same page.
     int slot[4];
@@ -620,7 +638,6 @@ __global__ void __launch_bounds__(kAppendThreads, 3) paged_append_kernel(const P
     uint64_t leads = held & ~on_lo;
     if (p.window < 64)
         leads &= (1ull << p.window) - 1;
-    // long runs by the CTA, one after another; a short one by a warp
     int short_no = 0;
     while (leads != 0) {
         const int i = __ffsll(static_cast<long long>(leads)) - 1;
@@ -633,9 +650,11 @@ __global__ void __launch_bounds__(kAppendThreads, 3) paged_append_kernel(const P
             if (threadIdx.x == 0)
                 report(p.status, SPARSE_ERR_BAD_INDEX);
         } else if (n > kShort) {
-            append_long(p, t0 + i, at, n, head, s_amax, red);
-        } else if (short_no++ % (kAppendThreads / 32) == warp) {
-            append_short(p, t0 + i, at, n, head, lane);
+            append_long(p, t0 + i, at, n, head, kv, s_amax, red);
+        } else {
+            if (short_no % 8 == 4 * kv + warp)
+                append_short(p, t0 + i, at, n, head, lane);
+            ++short_no;
         }
     }
 }
@@ -673,19 +692,15 @@ extern "C" SPARSE_API int sparse_page_plan(const int *seq_len, const int *n_new,
     int rc = sp_host::device_info(&dev);
     if (rc == SPARSE_OK)
         rc = sp_host::configure_kernel(reinterpret_cast<const void *>(page_plan_kernel),
-                                       (5 * kPlanMaxB + 1) * static_cast<int>(sizeof(int)), dev.device, configured[0]);
+                                       (4 * kPlanMaxB + 1) * static_cast<int>(sizeof(int)), dev.device, configured[0]);
     if (rc == SPARSE_OK)
         rc = sp_host::configure_kernel(reinterpret_cast<const void *>(page_rows_kernel),
                                        (3 * kPlanMaxB + 1) * static_cast<int>(sizeof(int)), dev.device, configured[1]);
     if (rc != SPARSE_OK)
         return rc;
-    // four requests a thread at most, and four rows where the planning CTA writes them
     const int with_rows = n_tok <= kRowsOneCta;
-    int threads = 128;
-    while (threads < kPlanThreads && (4 * threads < B || (with_rows && 4 * threads < n_tok)))
-        threads *= 2;
-    rc = sp_host::cuda_status(launch_pdl(reinterpret_cast<const void *>(page_plan_kernel), dim3(1), threads,
-                                         (5 * B + 1) * static_cast<int>(sizeof(int)), stream, p, with_rows), name);
+    rc = sp_host::cuda_status(launch_pdl(reinterpret_cast<const void *>(page_plan_kernel), dim3(1), kPlanThreads,
+                                         (4 * B + 1) * static_cast<int>(sizeof(int)), stream, p, with_rows), name);
     if (rc != SPARSE_OK || with_rows)
         return rc;
     const unsigned ctas = (static_cast<unsigned>(n_tok) + kRowsPerCta - 1) / kRowsPerCta;
@@ -730,8 +745,8 @@ extern "C" SPARSE_API int sparse_paged_append_f8(uint8_t *kv_pages, float *kv_sc
     while (window < kBlk && static_cast<long long>(n_tok) * H_kv > 8LL * dev.sm_count * window)
         window *= 2;
     const PagedAppendParams p{kv_pages, kv_scale, k_new, v_new, slot_map, ktil, tok_req, tok_pos, status, k_stride, v_stride,
-                              n_pages, H_kv, n_tok, window, B, N_cap};
-    const long long ctas = (static_cast<long long>(n_tok) + window - 1) / window * H_kv;
+                              n_pages, H_kv, n_tok, window, B, N_cap, kAhead * dev.sm_count};
+    const long long ctas = (static_cast<long long>(n_tok) + window - 1) / window * H_kv * 2;
     if (ctas > INT_MAX)
         return fail(SPARSE_ERR_UNSUPPORTED, "%s: n_tok=%d rows of %d heads in one call", name, n_tok, H_kv);
     return sp_host::cuda_status(launch_pdl(reinterpret_cast<const void *>(paged_append_kernel),
