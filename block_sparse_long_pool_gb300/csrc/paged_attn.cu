@@ -3,11 +3,12 @@
 // Work.  The items are the (pair, listed block) tiles, 16 KB each: 64 rows of keys and 64 of
 // values, one byte an element, adjacent in memory.  A persistent grid takes equal ranges
 // of the flattened item list (its length is known on the device only: every CTA sums the
-// counts itself), so requests of very different lengths load the SMs evenly.  A pair whose
-// items lie in several CTAs is merged by the CTA that finishes it last, in CTA order.
+// counts itself), in which a pair also counts as kPairCost items: its queries are loaded
+// and its state is merged.  So requests of very different lengths load the SMs evenly.  A
+// pair whose items lie in several CTAs is merged by the one that finishes last, in CTA order.
 //
-// Per CTA: warp 4 resolves items to pages, 32 at a time (list -> block table -> scales), and
-// streams tiles with one TMA load each into a ring; warps 0..3 own 16 tokens of every tile.
+// Per CTA: warp 3 resolves items to pages, 32 at a time (list -> block table -> scales), and
+// streams tiles with one TMA load each into a ring of 6; warps 0..2 take whole tiles in turn.
 //   S^T = K Q^T and O^T += V^T P^T run on mma.m16n8k16 in f16: every e4m3 value is an f16
 // value, so the tiles are converted without rounding, two elements an instruction.  Q rows
 // are scaled to f16's range by a power of two of their own.  Which 16 of the 128 dims make
@@ -27,43 +28,57 @@ namespace {
 
 using namespace sp;
 
-constexpr int kWarps = 4;                         // consumer warps
+constexpr int kWarps = 3;                         // consumer warps
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kTile = kBlk * kD;                  // keys (or values) of a block: 8 KB
 constexpr int kStageBytes = 2 * kTile;
 constexpr int kCtasPerSm = 2;
 constexpr int kStride = kD + 4;                   // floats a row of the warps' states
-constexpr int kMeta = 64;                         // item records: 32 being written + the ring's
+constexpr int kMeta = 64;                         // item and part records: 32 being written + the ring's
 constexpr float kWeightBits = 12.f;               // weights reach 2^12: f16 holds them down to 2^-24
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr int kMinItems = 2;                      // items a CTA takes at least
+#ifndef MINI
+#define MINI 4
+#define PCOST 4
+#endif
+constexpr int kMinItems = MINI;                   // a CTA's range at least
+constexpr int kPairCost = PCOST;                  // what a pair costs beside its items, in items
+constexpr int kDirect = 32;                       // partial states that are merged in one go
+constexpr int kGroup = 16;                        // CTAs whose states are merged first where there are more
 
-// What the consumers need to know of an item.
+// What the warp that takes an item needs to know of it.
 struct Item {
     float ks;          // key scale
     float log2_vs;     // value scale
     int rows;          // valid rows, 0: nothing to do
-    int pair;
-    long long start;   // the pair's first item
-    int n;             // the pair's items
-    int last;          // the CTA's last item of the pair
+    int part;          // the CTA's part of a pair that it belongs to (kEnd: no more items)
 };
-static_assert(sizeof(Item) == 32, "two 16-byte loads");
+static_assert(sizeof(Item) == 16, "one 16-byte load");
+constexpr int kEnd = 0x40000000;   // added to the number of parts
 
-template <int NT>
-constexpr int stages()
-{
-    return NT == 1 ? 5 : 4;
-}
+// The CTA's items of one pair.
+struct Part {
+    long long start;   // where the pair's items start in the flattened list
+    int n;             // the pair's items
+    int pair;
+};
+static_assert(sizeof(Part) == 16, "one 16-byte load");
+
+// Tiles in flight: a multiple of the consumer warps, so that a stage always belongs to the
+// same warp, which waits for each of its fills in turn (a wait by parity tells only
+// neighbouring fills apart).
+constexpr int kStages = 6;
+static_assert(kStages % kWarps == 0, "a stage belongs to one warp");
 
 template <int NT>
 struct Smem {
     static constexpr int kRows = 8 * NT;
-    static constexpr int kBars = stages<NT>() * kStageBytes;
+    static constexpr int kBars = kStages * kStageBytes;
     static constexpr int kItems = kBars + 128;
-    static constexpr int kWo = kItems + kMeta * 32;                          // [4][kRows][kStride]
-    static constexpr int kStat = kWo + kWarps * kRows * kStride * 4;         // m, l, mo [4][kRows], weights
-    static constexpr int kBytes = kStat + 6 * kWarps * kRows * 4 + 1024;     // + alignment
+    static constexpr int kParts = kItems + kMeta * 16;
+    static constexpr int kWo = kParts + kMeta * 16;                          // [kWarps][8][kStride]
+    static constexpr int kStat = kWo + kWarps * 8 * kStride * 4;             // m, l, mo [kWarps][kRows]
+    static constexpr int kBytes = kStat + 3 * kWarps * kRows * 4 + 1024;     // + alignment
 };
 
 // One partial state in the workspace: O [kRows][128], then m, l, mo [kRows].
@@ -83,7 +98,7 @@ struct PagedAttnParams {
     uint16_t *O;
     float *lse;
     int *status;
-    int *arrivals;     // [pairs], zero between calls
+    int *arrivals;     // [pairs], then [2 * groups of CTAs]; zero between calls
     float *parts;      // [2 * CTAs][part_floats]
     float scale_log2;
     int n_pages;
@@ -115,22 +130,28 @@ __device__ __forceinline__ int pair_items(const PagedAttnParams &p, int pair, bo
     return n < 0 ? 0 : min(n, p.k_tot);
 }
 
-// The CTA whose range [N c / C, N (c + 1) / C) holds an item.
-__device__ __forceinline__ int cta_of(long long item, long long N, long long C)
+// Its length in the flattened list.
+__device__ __forceinline__ long long pair_length(int n)
 {
-    long long c = item * C / N;
-    while (N * (c + 1) / C <= item)
+    return n > 0 ? static_cast<long long>(n) + kPairCost : 0;
+}
+
+// The CTA whose range [N c / C, N (c + 1) / C) holds a place of the list.
+__device__ __forceinline__ int cta_of(long long at, long long N, long long C)
+{
+    long long c = at * C / N;
+    while (N * (c + 1) / C <= at)
         ++c;
-    while (N * c / C > item)
+    while (N * c / C > at)
         --c;
     return static_cast<int>(c);
 }
 
-// Workspace slot of a CTA's state of a pair: 2c if the pair began before the CTA's range
-// (it can only be the range's first), else 2c + 1 (only its last pair goes on after it).
-__device__ __forceinline__ long long part_slot(int c, long long pair_start, long long N, long long C)
+// Workspace slot of CTA c's state of a pair whose items begin in CTA c0: a CTA has at most
+// one pair that began before it, and one that goes on after it.
+__device__ __forceinline__ int part_slot(int c, int c0)
 {
-    return 2LL * c + (pair_start < N * c / C ? 0 : 1);
+    return 2 * c + (c == c0 ? 1 : 0);
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -149,8 +170,9 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
 }
 
 // The pair's queries as mma B fragments (row g8 of each n-tile, dims 32 t4 + 4 ks ..+3 for
-// k-step ks), scaled by a power of two to just below f16's largest value, and what undoes
-// it, times the softmax scale, for the rows 2 t4 + {0, 1} whose scores this lane holds.
+// k-step ks), scaled by a power of two to just below f16's largest value (negated where the
+// softmax scale is negative), and what undoes it, times the softmax scale, for the rows
+// 2 t4 + {0, 1} whose scores this lane holds.
 template <int NT>
 struct Query {
     uint32_t b[NT][8][2];
@@ -188,8 +210,8 @@ struct Query {
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
             // the exponent of the row's largest value becomes 14
             const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
-            const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
-            const float down = __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23) * p.scale_log2;
+            const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23), p.scale_log2);
+            const float down = __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23) * fabsf(p.scale_log2);
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
                 b[nt][ks][0] = pack_f16x2(f[4 * ks] * up, f[4 * ks + 1] * up);
@@ -227,80 +249,77 @@ struct State {
     }
 };
 
-// One warp over tokens [16 w, 16 w + 16) of a tile, `rows` of the tile's 64 valid.
+// One warp over a tile, `rows` (1..64) of its tokens valid.
 template <int NT>
-__device__ __forceinline__ void attend(State<NT> &st, const Query<NT> &q, uint32_t tile, const Item &item, int w, int lane)
+__device__ __forceinline__ void attend(State<NT> &st, const Query<NT> &q, uint32_t tile, float ks_scale, float log2_vs,
+                                       int rows, int lane)
 {
     const int g8 = lane >> 2, t4 = lane & 3;
-    // keys: tokens g8 and g8 + 8, 16-byte chunks 2 t4 and 2 t4 + 1 (dims 32 t4 .. 32 t4 + 31)
-    const uint32_t k0 = tile + (w * 16 + g8) * kD;
+    // scores: m-tile mt holds tokens 16 mt + g8 and + 8 (elements 0/1 and 2/3)
+    float s[4][NT][4];
+    const uint32_t k0 = tile + g8 * kD;
     const uint32_t c0 = static_cast<uint32_t>((2 * t4) ^ g8) << 4, c1 = static_cast<uint32_t>((2 * t4 + 1) ^ g8) << 4;
-    uint32_t ka[8], kb[8];
-    *reinterpret_cast<uint4 *>(ka) = lds_v4(k0 + c0);
-    *reinterpret_cast<uint4 *>(ka + 4) = lds_v4(k0 + c1);
-    *reinterpret_cast<uint4 *>(kb) = lds_v4(k0 + 8 * kD + c0);
-    *reinterpret_cast<uint4 *>(kb + 4) = lds_v4(k0 + 8 * kD + c1);
-    float s[NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            s[nt][i] = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks) {
-        const uint32_t a[4] = {f8x2_to_f16x2(ka[ks]), f8x2_to_f16x2(kb[ks]), f8x2_to_f16x2(ka[ks] >> 16),
-                               f8x2_to_f16x2(kb[ks] >> 16)};
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-            mma_f16(s[nt], a, q.b[nt][ks][0], q.b[nt][ks][1]);
-    }
-    // values: tokens 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9, chunk g8 (dims 16 g8 .. 16 g8 + 15)
-    const uint32_t v0 = tile + kTile + (w * 16 + 2 * t4) * kD;
-    const uint32_t d0 = static_cast<uint32_t>(g8 ^ (2 * t4)) << 4, d1 = static_cast<uint32_t>(g8 ^ (2 * t4 + 1)) << 4;
-    uint32_t v[4][4];
-    *reinterpret_cast<uint4 *>(v[0]) = lds_v4(v0 + d0);
-    *reinterpret_cast<uint4 *>(v[1]) = lds_v4(v0 + kD + d1);
-    *reinterpret_cast<uint4 *>(v[2]) = lds_v4(v0 + 8 * kD + d0);
-    *reinterpret_cast<uint4 *>(v[3]) = lds_v4(v0 + 9 * kD + d1);
-    const int left = item.rows - w * 16;   // valid tokens of the warp's 16
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            s[nt][i] *= item.ks * q.mul[nt][i & 1];
-    if (left < 16) {
-        // the request ends in this tile: what lies behind it may be any bytes
+    for (int mt = 0; mt < 4; ++mt) {
+        // 16-byte chunks 2 t4 and 2 t4 + 1: dims 32 t4 .. 32 t4 + 31
+        uint32_t ka[8], kb[8];
+        *reinterpret_cast<uint4 *>(ka) = lds_v4(k0 + mt * 16 * kD + c0);
+        *reinterpret_cast<uint4 *>(ka + 4) = lds_v4(k0 + mt * 16 * kD + c1);
+        *reinterpret_cast<uint4 *>(kb) = lds_v4(k0 + mt * 16 * kD + 8 * kD + c0);
+        *reinterpret_cast<uint4 *>(kb + 4) = lds_v4(k0 + mt * 16 * kD + 8 * kD + c1);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (g8 + (i >> 1) * 8 >= left)
-                    s[nt][i] = -INFINITY;
+                s[mt][nt][i] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (2 * t4 + (i & 1) + (i >> 1) * 8 >= left)
-                v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0u;
+        for (int ks = 0; ks < 8; ++ks) {
+            const uint32_t a[4] = {f8x2_to_f16x2(ka[ks]), f8x2_to_f16x2(kb[ks]), f8x2_to_f16x2(ka[ks] >> 16),
+                                   f8x2_to_f16x2(kb[ks] >> 16)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                mma_f16(s[mt][nt], a, q.b[nt][ks][0], q.b[nt][ks][1]);
+        }
     }
-    uint32_t pb[NT][2];
+    uint32_t pb[4][NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        float alpha[2], po[4];
+        float mul[2], alpha[2];
+        mul[0] = ks_scale * q.mul[nt][0];
+        mul[1] = ks_scale * q.mul[nt][1];
+        if (rows < kBlk) {
+            // the request ends in this tile: what lies behind it may be any bytes
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    s[mt][nt][i] = 16 * mt + g8 + (i >> 1) * 8 < rows ? s[mt][nt][i] * mul[i & 1] : -INFINITY;
+            mul[0] = mul[1] = 1.f;
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            float mx = fmaxf(s[nt][h], s[nt][h + 2]);
+            float mx = fmaxf(s[0][nt][h], s[0][nt][h + 2]);
+#pragma unroll
+            for (int mt = 1; mt < 4; ++mt)
+                mx = fmaxf(mx, fmaxf(s[mt][nt][h], s[mt][nt][h + 2]));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float m_new = fmaxf(st.m[nt][h], mx);
-            const float mo_new = fmaxf(st.mo[nt][h], mx + item.log2_vs - kWeightBits);
-            const float m_use = m_new == -INFINITY ? 0.f : m_new;
-            const float mo_use = mo_new == -INFINITY ? 0.f : mo_new;
-            st.l[nt][h] = st.l[nt][h] * ex2_approx(st.m[nt][h] - m_use) + ex2_approx(s[nt][h] - m_use) +
-                          ex2_approx(s[nt][h + 2] - m_use);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) * mul[h];
+            const float m_new = fmaxf(st.m[nt][h], mx), mo_new = fmaxf(st.mo[nt][h], mx + log2_vs - kWeightBits);
+            const float m_use = m_new == -INFINITY ? 0.f : m_new, mo_use = mo_new == -INFINITY ? 0.f : mo_new;
+            float l = st.l[nt][h] * ex2_approx(st.m[nt][h] - m_use);
             alpha[h] = ex2_approx(st.mo[nt][h] - mo_use);
-            const float shift = item.log2_vs - mo_use;
-            po[h] = ex2_approx(s[nt][h] + shift);
-            po[h + 2] = ex2_approx(s[nt][h + 2] + shift);
+            // from units of 2^m to 2^mo; the bound is only reached by weights below 2^-100
+            const float to_o = ex2_approx(fminf(log2_vs + (m_use - mo_use), 112.f));
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                for (int i = h; i < 4; i += 2) {
+                    const float w = ex2_approx(fmaf(s[mt][nt][i], mul[h], -m_use));
+                    l += w;
+                    s[mt][nt][i] = w * to_o;
+                }
+            st.l[nt][h] = l;
             st.m[nt][h] = m_new;
             st.mo[nt][h] = mo_new;
         }
@@ -311,20 +330,41 @@ __device__ __forceinline__ void attend(State<NT> &st, const Query<NT> &q, uint32
                 for (int i = 0; i < 4; ++i)
                     st.acc[mt][nt][i] *= alpha[i & 1];
         }
-        pb[nt][0] = movmatrix_trans(pack_f16x2(po[0], po[1]));
-        pb[nt][1] = movmatrix_trans(pack_f16x2(po[2], po[3]));
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+            pb[mt][nt][0] = movmatrix_trans(pack_f16x2(s[mt][nt][0], s[mt][nt][1]));
+            pb[mt][nt][1] = movmatrix_trans(pack_f16x2(s[mt][nt][2], s[mt][nt][3]));
+        }
     }
+    // values, 16 tokens a step: tokens 2 t4, 2 t4 + 1, + 8, + 9, chunk g8 (dims 16 g8 ..+15)
+    const uint32_t v0 = tile + kTile + 2 * t4 * kD;
+    const uint32_t d0 = static_cast<uint32_t>(g8 ^ (2 * t4)) << 4, d1 = static_cast<uint32_t>(g8 ^ (2 * t4 + 1)) << 4;
 #pragma unroll
-    for (int wi = 0; wi < 4; ++wi) {
+    for (int kt = 0; kt < 4; ++kt) {
+        uint32_t v[4][4];
+        *reinterpret_cast<uint4 *>(v[0]) = lds_v4(v0 + kt * 16 * kD + d0);
+        *reinterpret_cast<uint4 *>(v[1]) = lds_v4(v0 + kt * 16 * kD + kD + d1);
+        *reinterpret_cast<uint4 *>(v[2]) = lds_v4(v0 + kt * 16 * kD + 8 * kD + d0);
+        *reinterpret_cast<uint4 *>(v[3]) = lds_v4(v0 + kt * 16 * kD + 9 * kD + d1);
+        if (rows < kBlk) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            // bytes 2x, 2x + 1 of the word: dims 4 wi + 2 x and + 1 of two tokens side by side
-            const uint32_t sel = x == 0 ? 0x5140u : 0x7362u;
-            const uint32_t ab = __byte_perm(v[0][wi], v[1][wi], sel), cd = __byte_perm(v[2][wi], v[3][wi], sel);
-            const uint32_t a[4] = {f8x2_to_f16x2(ab), f8x2_to_f16x2(ab >> 16), f8x2_to_f16x2(cd), f8x2_to_f16x2(cd >> 16)};
+            for (int i = 0; i < 4; ++i)
+                if (16 * kt + 2 * t4 + (i & 1) + (i >> 1) * 8 >= rows)
+                    v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0u;
+        }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                mma_f16(st.acc[2 * wi + x][nt], a, pb[nt][0], pb[nt][1]);
+        for (int wi = 0; wi < 4; ++wi) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                // bytes 2x, 2x + 1 of the word: dims 4 wi + 2 x and + 1 of two tokens side by side
+                const uint32_t sel = x == 0 ? 0x5140u : 0x7362u;
+                const uint32_t ab = __byte_perm(v[0][wi], v[1][wi], sel), cd = __byte_perm(v[2][wi], v[3][wi], sel);
+                const uint32_t a[4] = {f8x2_to_f16x2(ab), f8x2_to_f16x2(ab >> 16), f8x2_to_f16x2(cd),
+                                       f8x2_to_f16x2(cd >> 16)};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma_f16(st.acc[2 * wi + x][nt], a, pb[kt][nt][0], pb[kt][nt][1]);
+            }
         }
     }
 }
@@ -342,28 +382,236 @@ __device__ __forceinline__ void write_out(const PagedAttnParams &p, int pair, in
         p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
 }
 
+// The states of CTAs first, first + step, ... (n of them, at most kDirect; all but the first
+// at multiples of `step`) of a pair, merged in that order: into O, or (to >= 0) into the
+// workspace's slot `to`.  The consumer threads all call it; w holds 4 * kDirect * ROWS floats.
+template <int NT, typename Sync>
+__device__ __forceinline__ bool merge_parts(const PagedAttnParams &p, int pair, int c0, int first, int n, int step, int to,
+                                            float *w, int tid, Sync sync)
+{
+    constexpr int ROWS = 8 * NT;
+    constexpr int PART = part_floats<NT>();
+    float *wm = w, *wl = wm + kDirect * ROWS, *wmo = wl + kDirect * ROWS, *row_stat = wmo + kDirect * ROWS;
+    auto slot = [&](int j) { return part_slot(j == 0 ? first : (first / step + j) * step, c0); };
+    for (int e = tid; e < n * ROWS; e += kWarps * 32) {
+        const float *src = p.parts + static_cast<size_t>(slot(e / ROWS)) * PART + ROWS * kD + e % ROWS;
+        if (e % ROWS < p.G) {
+            wm[e] = __ldcg(src);
+            wl[e] = __ldcg(src + ROWS);
+            wmo[e] = __ldcg(src + 2 * ROWS);
+        }
+    }
+    if (!sync())
+        return false;
+    if (tid < p.G) {
+        float m = -INFINITY, mo = -INFINITY, l = 0.f;
+        for (int j = 0; j < n; ++j) {
+            m = fmaxf(m, wm[j * ROWS + tid]);
+            mo = fmaxf(mo, wmo[j * ROWS + tid]);
+        }
+        for (int j = 0; j < n; ++j) {
+            const float lj = wl[j * ROWS + tid], moj = wmo[j * ROWS + tid];
+            l += lj == 0.f ? 0.f : lj * exp2f(wm[j * ROWS + tid] - m);
+            wmo[j * ROWS + tid] = moj == -INFINITY ? 0.f : exp2f(moj - mo);   // O's weight
+        }
+        row_stat[tid] = m;
+        row_stat[ROWS + tid] = l;
+        row_stat[2 * ROWS + tid] = mo;
+    }
+    if (!sync())
+        return false;
+    float *dst = p.parts + static_cast<size_t>(to < 0 ? 0 : to) * PART;
+    for (int e = tid; e < p.G * (kD / 4); e += kWarps * 32) {
+        const int row = e / (kD / 4), d = 4 * (e % (kD / 4));
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j0 = 0; j0 < n; j0 += 16) {
+            float4 x[16];
+#pragma unroll
+            for (int u = 0; u < 16; ++u)
+                x[u] = j0 + u < n ? __ldcg(reinterpret_cast<const float4 *>(
+                                        p.parts + static_cast<size_t>(slot(j0 + u)) * PART + row * kD + d))
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+                const float f = j0 + u < n ? wmo[(j0 + u) * ROWS + row] : 0.f;
+                o.x = fmaf(f, x[u].x, o.x);
+                o.y = fmaf(f, x[u].y, o.y);
+                o.z = fmaf(f, x[u].z, o.z);
+                o.w = fmaf(f, x[u].w, o.w);
+            }
+        }
+        const float m = row_stat[row], l = row_stat[ROWS + row], mo = row_stat[2 * ROWS + row];
+        if (to < 0) {
+            write_out(p, pair, row, d, o, m, l, mo);
+        } else {
+            // slot `to` is one of those read, each element by the thread that writes it; its
+            // statistics were read before the barriers
+            *reinterpret_cast<float4 *>(dst + row * kD + d) = o;
+            if (d == 0) {
+                dst[ROWS * kD + row] = m;
+                dst[ROWS * kD + ROWS + row] = l;
+                dst[ROWS * kD + 2 * ROWS + row] = mo;
+            }
+        }
+    }
+    return true;
+}
+
+// The CTA's part of a pair: its 4 warps' states merged, and written out, or left in the
+// workspace for the last of the pair's CTAs to merge.  All consumer threads call it.
+template <int NT, typename Sync>
+__device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const State<NT> &st, const Part &of, int c, long long lo,
+                                            long long hi, long long N, long long C, uint8_t *base, int *s_last, int warp,
+                                            int lane, Sync sync)
+{
+    constexpr int ROWS = 8 * NT;
+    constexpr int PART = part_floats<NT>();
+    using S = Smem<NT>;
+    const int tid = warp * 32 + lane, pairs = p.B * p.H_kv;
+    float *wo = reinterpret_cast<float *>(base + S::kWo);
+    float *wm = reinterpret_cast<float *>(base + S::kStat);   // [4][ROWS] each: m, l, mo
+    float *wl = wm + kWarps * ROWS, *wmo = wl + kWarps * ROWS;
+    const int g8 = lane >> 2, t4 = lane & 3;
+    const bool whole = of.start >= lo && of.start + of.n <= hi;
+    const int c0 = whole ? c : cta_of(of.start, N, C), c1 = whole ? c : cta_of(of.start + of.n - 1, N, C);
+    float *part = p.parts + static_cast<size_t>(part_slot(c, c0)) * PART;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        if (nt > 0 && !sync())   // wo is free again
+            return false;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int row = 2 * t4 + h;
+            float l = st.l[nt][h];
+            l += __shfl_xor_sync(0xffffffffu, l, 4);
+            l += __shfl_xor_sync(0xffffffffu, l, 8);
+            l += __shfl_xor_sync(0xffffffffu, l, 16);
+            if (g8 == 0) {
+                wm[warp * ROWS + nt * 8 + row] = st.m[nt][h];
+                wl[warp * ROWS + nt * 8 + row] = l;
+                wmo[warp * ROWS + nt * 8 + row] = st.mo[nt][h];
+            }
+            float *dst = wo + (warp * 8 + row) * kStride + 16 * g8;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<float4 *>(dst + 4 * i) =
+                    make_float4(st.acc[2 * i][nt][h], st.acc[2 * i][nt][h + 2], st.acc[2 * i + 1][nt][h],
+                                st.acc[2 * i + 1][nt][h + 2]);
+        }
+        if (!sync())
+            return false;
+        for (int e = tid; e < min(8, p.G - nt * 8) * (kD / 4); e += kWarps * 32) {
+            const int r8 = e / (kD / 4), row = nt * 8 + r8, d = 4 * (e % (kD / 4));
+            float m = -INFINITY, mo = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                m = fmaxf(m, wm[w * ROWS + row]);
+                mo = fmaxf(mo, wmo[w * ROWS + row]);
+            }
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float lw = wl[w * ROWS + row];
+                l += lw == 0.f ? 0.f : lw * exp2f(wm[w * ROWS + row] - m);
+                const float f = wmo[w * ROWS + row] == -INFINITY ? 0.f : exp2f(wmo[w * ROWS + row] - mo);
+                const float4 x = *reinterpret_cast<const float4 *>(wo + (w * 8 + r8) * kStride + d);
+                o.x = fmaf(f, x.x, o.x);
+                o.y = fmaf(f, x.y, o.y);
+                o.z = fmaf(f, x.z, o.z);
+                o.w = fmaf(f, x.w, o.w);
+            }
+            if (whole) {
+                write_out(p, of.pair, row, d, o, m, l, mo);
+            } else {
+                *reinterpret_cast<float4 *>(part + row * kD + d) = o;
+                if (d == 0) {
+                    part[ROWS * kD + row] = m;
+                    part[ROWS * kD + ROWS + row] = l;
+                    part[ROWS * kD + 2 * ROWS + row] = mo;
+                }
+            }
+        }
+    }
+    // ---- the states of a pair's CTAs, merged by the last of them; where they are many,
+    // by the last of each kGroup neighbours first
+    int *count_of = p.arrivals + of.pair;
+    int expect = c1 - c0 + 1, first = c0, step = 1;
+    if (c1 > c0 && expect > kDirect) {
+        const int g = c / kGroup, g_first = max(c0, g * kGroup), g_n = min(c1, g * kGroup + kGroup - 1) - g_first + 1;
+        // at most two such pairs meet a group: one from before it, one that starts in it
+        int *group_count = p.arrivals + pairs + 2 * g + (c0 < g * kGroup ? 0 : 1);
+        __threadfence();
+        if (!sync())
+            return false;
+        if (tid == 0) {
+            const int prev = atomicAdd(group_count, 1);
+            if (prev == g_n - 1)
+                *group_count = 0;   // for the next call
+            *s_last = prev == g_n - 1;
+            __threadfence();
+        }
+        if (!sync())
+            return false;
+        if (*s_last) {
+            if (!merge_parts<NT>(p, of.pair, c0, g_first, g_n, 1, part_slot(g_first, c0), wo, tid, sync))
+                return false;
+            expect = c1 / kGroup - c0 / kGroup + 1;
+            step = kGroup;
+        } else {
+            expect = 0;   // this CTA's part is done
+        }
+    }
+    if (c1 > c0 && expect > 0) {
+        __threadfence();
+        if (!sync())
+            return false;
+        if (tid == 0) {
+            const int prev = atomicAdd(count_of, 1);
+            if (prev == expect - 1)
+                *count_of = 0;
+            *s_last = prev == expect - 1;
+            __threadfence();
+        }
+        if (!sync())
+            return false;
+        if (*s_last && !merge_parts<NT>(p, of.pair, c0, first, expect, step, -1, wo, tid, sync))
+            return false;
+    }
+    return true;
+}
+
+// A wait ran out: report it, and stay for longer than any load in flight takes to land in
+// this CTA's shared memory.
+__device__ __forceinline__ void give_up(const PagedAttnParams &p, int lane)
+{
+    if (lane == 0)
+        report(p.status, SPARSE_ERR_TIMEOUT);
+    for (int i = 0; i < 16; ++i)
+        __nanosleep(1000000);
+}
+
 template <int NT>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     paged_attn_kernel(const __grid_constant__ CUtensorMap map, const PagedAttnParams p)
 {
     constexpr int ROWS = 8 * NT;
-    constexpr int STAGES = stages<NT>();
-    constexpr int PART = part_floats<NT>();
     using S = Smem<NT>;
+    static_assert((3 * kDirect + 3) * ROWS <= kWarps * 8 * kStride, "the merge's weights fit the warps' states");
     extern __shared__ uint8_t smem_raw[];
-    __shared__ long long s_sum[kWarps + 2];
+    __shared__ long long s_sum[kWarps + 1];
     __shared__ long long s_start;
-    __shared__ int s_unit, s_last;
+    __shared__ int s_pair, s_n, s_last;
     const uint32_t base_s = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *base = smem_raw + (base_s - smem_u32(smem_raw));
     Item *items = reinterpret_cast<Item *>(base + S::kItems);
-    const uint32_t full = base_s + S::kBars, empty = full + 8 * STAGES, meet = empty + 8 * STAGES;
+    Part *parts = reinterpret_cast<Part *>(base + S::kParts);
+    const uint32_t full = base_s + S::kBars, empty = full + 8 * kStages, meet = empty + 8 * kStages;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
-        for (int i = 0; i < STAGES; ++i) {
+        for (int i = 0; i < kStages; ++i) {
             mbar_init(full + 8 * i, 2);          // the load's expect_tx, and the item record
-            mbar_init(empty + 8 * i, kWarps);
+            mbar_init(empty + 8 * i, 1);         // the warp that took the tile
         }
         mbar_init(meet, kWarps);
         fence_barrier_init();
@@ -373,16 +621,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     griddep_wait();
     griddep_launch_dependents();
 
-    // ---- items before each unit (a request where every block is attended over, else a pair)
+    // ---- length before each unit (a request where every block is attended over, else a pair)
     const bool all = p.blk_idx == nullptr;
-    const int units = all ? p.B : p.B * p.H_kv;
-    const int weight = all ? p.H_kv : 1;
+    const int pairs = p.B * p.H_kv;
+    const int units = all ? p.B : pairs;
+    const int heads = all ? p.H_kv : 1;
     const int per = (units + kThreads - 1) / kThreads;
     const int u0 = min(units, tid * per), u1 = min(units, u0 + per);
     bool bad = false;
     long long mine = 0;
     for (int u = u0; u < u1; ++u)
-        mine += static_cast<long long>(pair_items(p, u * weight, &bad)) * weight;
+        mine += pair_length(pair_items(p, u * heads, &bad)) * heads;
     if (bad && blockIdx.x == 0)
         report(p.status, SPARSE_ERR_BAD_INDEX);
     long long incl = mine;
@@ -406,40 +655,37 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     const int c = static_cast<int>(blockIdx.x);
     const long long lo = c < C ? N * c / C : N, hi = c < C ? N * (c + 1) / C : N;
     if (lo < hi && incl - mine <= lo && lo < incl) {
+        // the pair that holds `lo`
         long long at = incl - mine;
-        int u = u0;
-        for (; u < u1 - 1; ++u) {
-            const long long n = static_cast<long long>(pair_items(p, u * weight, &bad)) * weight;
-            if (at + n > lo)
+        int u = u0, n = 0;
+        for (; u < u1; ++u) {
+            n = pair_items(p, u * heads, &bad);
+            if (at + pair_length(n) * heads > lo)
                 break;
-            at += n;
+            at += pair_length(n) * heads;
         }
-        s_unit = u;
-        s_start = at;
+        const int h = all ? static_cast<int>((lo - at) / pair_length(n)) : 0;
+        s_pair = u * heads + h;
+        s_start = at + h * pair_length(n);
+        s_n = n;
     }
     __syncthreads();
+    // no items: an empty range, or one within what a pair costs beside its items
+    const bool idle = lo >= hi || s_start + kPairCost >= hi;
 
     if (warp == kWarps) {
         // ------------------------------------------------------------ producer
-        if (lo >= hi)
+        if (idle)
             return;
-        int pair = s_unit;             // the pair that holds item `at`, and its first item
-        long long start = s_start;
-        if (all) {
-            const int n = pair_items(p, s_unit * weight, &bad);
-            const int h = static_cast<int>((lo - start) / n);
-            pair = s_unit * weight + h;
-            start += static_cast<long long>(h) * n;
-        }
-        const int pairs = p.B * p.H_kv;
+        int pair = s_pair;
+        long long start = s_start;     // where this pair starts in the list
         const uint64_t pol = policy_evict_first();
-        long long at = lo;             // next item
-        int it = 0;                    // its number in the CTA
+        int it = 0, part = 0;          // the CTA's next item and part
         bool stop = false, wrong = false;
-        while (at < hi && pair < pairs && !stop) {
-            // the next 32 pairs' items and where they start
+        while (start < hi && pair < pairs && !stop) {
+            // the next 32 pairs, one a lane: items [a, a + cnt) of the pair are the CTA's
             const int n = pair + lane < pairs ? pair_items(p, pair + lane, &bad) : 0;
-            long long end = n;
+            long long end = pair_length(n);
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const long long v = __shfl_up_sync(0xffffffffu, end, o);
@@ -447,89 +693,113 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     end += v;
             }
             end += start;
-            const long long upto = min(hi, __shfl_sync(0xffffffffu, end, 31));
-            const int take = static_cast<int>(min(32LL, upto - at));
-            // lane j resolves item at + j: the first of the 32 pairs that ends after it
-            int k = 0;
+            const long long first = end - n;   // the pair's items start here
+            const int a = static_cast<int>(max(0LL, min(static_cast<long long>(n), lo - first)));
+            const int cnt = max(0, static_cast<int>(min(static_cast<long long>(n), hi - first)) - a);
+            int upto = cnt;
 #pragma unroll
-            for (int step = 16; step > 0; step >>= 1)
-                if (__shfl_sync(0xffffffffu, end, k + step - 1) <= at + lane)
-                    k += step;
-            k = min(k, 31);
-            Item item;
-            item.pair = pair + k;
-            item.n = __shfl_sync(0xffffffffu, n, k);
-            item.start = __shfl_sync(0xffffffffu, end, k) - item.n;
-            item.rows = 0;
-            item.last = at + lane + 1 == hi || at + lane + 1 == item.start + item.n;
-            int unit = 0;
-            float2 sc = make_float2(1.f, 1.f);
-            if (lane < take) {
-                const int b = item.pair / p.H_kv, i = static_cast<int>(at + lane - item.start);
-                const int blk = all ? i : p.blk_idx[static_cast<size_t>(item.pair) * p.k_tot + i];
-                const long long rows = min(static_cast<long long>(p.seq_len[b]), static_cast<long long>(p.max_blocks) * kBlk) -
-                                       static_cast<long long>(blk) * kBlk;
-                if (blk < 0 || blk >= p.max_blocks) {
-                    wrong = true;
-                } else if (rows > 0) {
-                    const int page = p.block_table[static_cast<size_t>(b) * p.max_blocks + blk];
-                    if (page < 0 || page >= p.n_pages) {
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o)
+                    upto += v;
+            }
+            const int total = __shfl_sync(0xffffffffu, upto, 31);
+            const unsigned has = __ballot_sync(0xffffffffu, cnt > 0);
+            const int my_part = part + __popc(has & ((1u << lane) - 1));
+            if (cnt > 0)
+                parts[my_part % kMeta] = Part{first, n, pair + lane};
+            for (int done = 0; done < total && !stop; done += 32) {
+                // lane j resolves item done + j: of the first pair whose count reaches past it
+                const int take = min(32, total - done);
+                int k = 0;
+#pragma unroll
+                for (int half = 16; half > 0; half >>= 1)
+                    if (__shfl_sync(0xffffffffu, upto, k + half - 1) <= done + lane)
+                        k += half;
+                const int in_pair = done + lane - (__shfl_sync(0xffffffffu, upto, k) - __shfl_sync(0xffffffffu, cnt, k));
+                const int i = __shfl_sync(0xffffffffu, a, k) + in_pair;
+                Item item;
+                item.rows = 0;
+                item.part = __shfl_sync(0xffffffffu, my_part, k);
+                const int of = pair + k;
+                int unit = 0;
+                float2 sc = make_float2(1.f, 1.f);
+                if (lane < take) {
+                    const int b = of / p.H_kv;
+                    const int blk = all ? i : p.blk_idx[static_cast<size_t>(of) * p.k_tot + i];
+                    const long long rows = min(static_cast<long long>(p.seq_len[b]), static_cast<long long>(p.max_blocks) * kBlk) -
+                                           static_cast<long long>(blk) * kBlk;
+                    if (blk < 0 || blk >= p.max_blocks) {
                         wrong = true;
-                    } else {
-                        item.rows = static_cast<int>(min(rows, static_cast<long long>(kBlk)));
-                        unit = page * p.H_kv + item.pair % p.H_kv;
-                        sc = *reinterpret_cast<const float2 *>(p.kv_scale + 2 * static_cast<size_t>(unit));
-                    }
-                }
-            }
-            // the ring is empty at first: those loads go out before the scales are here
-            const int ahead = it == 0 ? min(take, STAGES) : 0;
-            for (int j = 0; j < ahead; ++j) {
-                const int u = __shfl_sync(0xffffffffu, unit, j), rows = __shfl_sync(0xffffffffu, item.rows, j);
-                if (lane == 0) {
-                    if (rows > 0) {
-                        mbar_arrive_expect_tx(full + 8 * j, kStageBytes);
-                        tma_load_3d(base_s + j * kStageBytes, &map, full + 8 * j, 0, 0, 2 * u, pol);
-                    } else {
-                        mbar_arrive(full + 8 * j);
-                    }
-                }
-            }
-            item.ks = sc.x;
-            item.log2_vs = log2f(sc.y);
-            if (lane < take)
-                items[(it + lane) % kMeta] = item;
-            __syncwarp();
-            for (int j = 0; j < take && !stop; ++j) {
-                const int u = __shfl_sync(0xffffffffu, unit, j), rows = __shfl_sync(0xffffffffu, item.rows, j);
-                const int stage = (it + j) % STAGES, use = (it + j) / STAGES;
-                if (lane == 0) {
-                    if (j >= ahead) {
-                        if (use > 0 && !mbar_wait(empty + 8 * stage, (use - 1) & 1, kWaitNs)) {
-                            report(p.status, SPARSE_ERR_TIMEOUT);
-                            stop = true;
-                        } else if (rows > 0) {
-                            mbar_arrive_expect_tx(full + 8 * stage, kStageBytes);
-                            tma_load_3d(base_s + stage * kStageBytes, &map, full + 8 * stage, 0, 0, 2 * u, pol);
+                    } else if (rows > 0) {
+                        const int page = p.block_table[static_cast<size_t>(b) * p.max_blocks + blk];
+                        if (page < 0 || page >= p.n_pages) {
+                            wrong = true;
                         } else {
-                            mbar_arrive(full + 8 * stage);
+                            item.rows = static_cast<int>(min(rows, static_cast<long long>(kBlk)));
+                            unit = page * p.H_kv + of % p.H_kv;
+                            sc = *reinterpret_cast<const float2 *>(p.kv_scale + 2 * static_cast<size_t>(unit));
                         }
                     }
-                    if (!stop)
-                        mbar_arrive(full + 8 * stage);   // the item record
                 }
-                stop = __shfl_sync(0xffffffffu, stop ? 1 : 0, 0) != 0;
+                // the ring is empty at first: those loads go out before the scales are here
+                const int ahead = it == 0 ? min(take, kStages) : 0;
+                for (int j = 0; j < ahead; ++j) {
+                    const int u = __shfl_sync(0xffffffffu, unit, j), rows = __shfl_sync(0xffffffffu, item.rows, j);
+                    if (lane == 0) {
+                        if (rows > 0) {
+                            mbar_arrive_expect_tx(full + 8 * j, kStageBytes);
+                            tma_load_3d(base_s + j * kStageBytes, &map, full + 8 * j, 0, 0, 2 * u, pol);
+                        } else {
+                            mbar_arrive(full + 8 * j);
+                        }
+                    }
+                }
+                item.ks = sc.x;
+                item.log2_vs = log2f(sc.y);
+                if (lane < take)
+                    items[(it + lane) % kMeta] = item;
+                __syncwarp();
+                for (int j = 0; j < take && !stop; ++j) {
+                    const int u = __shfl_sync(0xffffffffu, unit, j), rows = __shfl_sync(0xffffffffu, item.rows, j);
+                    const int stage = (it + j) % kStages, use = (it + j) / kStages;
+                    if (lane == 0) {
+                        if (j >= ahead) {
+                            if (use > 0 && !mbar_wait(empty + 8 * stage, (use - 1) & 1, kWaitNs)) {
+                                stop = true;
+                            } else if (rows > 0) {
+                                mbar_arrive_expect_tx(full + 8 * stage, kStageBytes);
+                                tma_load_3d(base_s + stage * kStageBytes, &map, full + 8 * stage, 0, 0, 2 * u, pol);
+                            } else {
+                                mbar_arrive(full + 8 * stage);
+                            }
+                        }
+                        if (!stop)
+                            mbar_arrive(full + 8 * stage);   // the item record
+                    }
+                    stop = __shfl_sync(0xffffffffu, stop ? 1 : 0, 0) != 0;
+                }
+                it += take;
             }
-            at += take;
-            it += take;
-            // the pair that holds the next item
-            const unsigned open = __ballot_sync(0xffffffffu, end > at);
-            const int skip = open != 0u ? __ffs(static_cast<int>(open)) - 1 : 32;
-            start = skip == 32 ? __shfl_sync(0xffffffffu, end, 31) : __shfl_sync(0xffffffffu, end - n, skip);
-            pair += skip;
+            start = __shfl_sync(0xffffffffu, end, 31);
+            pair += 32;
+            part += __popc(has);
+        }
+        // each consumer warp gets an item that ends it
+        for (int j = 0; j < kWarps && lane == 0 && !stop; ++j, ++it) {
+            const int stage = it % kStages, use = it / kStages;
+            if (use > 0 && !mbar_wait(empty + 8 * stage, (use - 1) & 1, kWaitNs)) {
+                stop = true;
+                break;
+            }
+            items[it % kMeta] = Item{1.f, 0.f, 0, part + kEnd};
+            mbar_arrive(full + 8 * stage);
+            mbar_arrive(full + 8 * stage);
         }
         if (__any_sync(0xffffffffu, wrong) && lane == 0)
             report(p.status, SPARSE_ERR_BAD_INDEX);
+        if (__any_sync(0xffffffffu, stop))
+            give_up(p, lane);
         return;
     }
 
@@ -543,142 +813,48 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         return __all_sync(0xffffffffu, mbar_wait(meet, meetings++ & 1, 2 * kWaitNs)) != 0;
     };
     // rows of pairs without items, shared out over the CTAs
-    for (int pair = c + static_cast<int>(gridDim.x) * warp; pair < p.B * p.H_kv; pair += static_cast<int>(gridDim.x) * kWarps)
+    for (int pair = c + static_cast<int>(gridDim.x) * warp; pair < pairs; pair += static_cast<int>(gridDim.x) * kWarps)
         if (pair_items(p, pair, &bad) == 0)
             for (int row = 0; row < p.G; ++row)
                 write_out(p, pair, row, 4 * lane, make_float4(0.f, 0.f, 0.f, 0.f), 0.f, 0.f, 0.f);
+    if (idle)
+        return;
 
-    float *wo = reinterpret_cast<float *>(base + S::kWo);
-    float *wm = reinterpret_cast<float *>(base + S::kStat);   // [4][ROWS] each: m, l, mo
-    float *wl = wm + kWarps * ROWS, *wmo = wl + kWarps * ROWS;
     Query<NT> q;
     State<NT> st;
     st.reset();
-    int of_pair = -1;
-    const int n_items = static_cast<int>(hi - lo);
-    for (int it = 0; it < n_items; ++it) {
-        const int stage = it % STAGES;
-        if (!__all_sync(0xffffffffu, mbar_wait(full + 8 * stage, (it / STAGES) & 1, kWaitNs))) {
-            if (lane == 0)
-                report(p.status, SPARSE_ERR_TIMEOUT);
+    int part = 0, q_part = -1;
+    for (int it = warp;; it += kWarps) {
+        const int stage = it % kStages;
+        if (!__all_sync(0xffffffffu, mbar_wait(full + 8 * stage, (it / kStages) & 1, kWaitNs))) {
+            give_up(p, lane);
             return;
         }
         const Item item = items[it % kMeta];
-        if (item.pair != of_pair) {
-            of_pair = item.pair;
-            q.load(p, of_pair, lane);
+        const int next = item.part & ~kEnd;
+        // the parts before the item's are complete once every warp has come this far
+        for (; part < next; ++part) {
+            const Part of = parts[part % kMeta];
+            bool ok = finish_part<NT>(p, st, of, c, lo, hi, N, C, base, &s_last, warp, lane, sync);
             st.reset();
+            ok = ok && sync();   // shared memory is free again
+            if (!ok) {
+                give_up(p, lane);
+                return;
+            }
         }
-        if (item.rows > warp * 16)
-            attend<NT>(st, q, base_s + stage * kStageBytes, item, warp, lane);
+        if (item.part & kEnd)
+            return;
+        if (item.rows > 0) {
+            if (part != q_part) {
+                q_part = part;
+                q.load(p, parts[part % kMeta].pair, lane);
+            }
+            attend<NT>(st, q, base_s + stage * kStageBytes, item.ks, item.log2_vs, item.rows, lane);
+        }
         __syncwarp();
         if (lane == 0)
             mbar_arrive(empty + 8 * stage);
-        if (!item.last)
-            continue;
-
-        // ---- the CTA's state of the pair: the 4 warps' states merged
-        const int g8 = lane >> 2, t4 = lane & 3;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int row = nt * 8 + 2 * t4 + h;
-                float l = st.l[nt][h];
-                l += __shfl_xor_sync(0xffffffffu, l, 4);
-                l += __shfl_xor_sync(0xffffffffu, l, 8);
-                l += __shfl_xor_sync(0xffffffffu, l, 16);
-                if (g8 == 0) {
-                    wm[warp * ROWS + row] = st.m[nt][h];
-                    wl[warp * ROWS + row] = l;
-                    wmo[warp * ROWS + row] = st.mo[nt][h];
-                }
-                float *dst = wo + (warp * ROWS + row) * kStride + 16 * g8;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<float4 *>(dst + 4 * i) =
-                        make_float4(st.acc[2 * i][nt][h], st.acc[2 * i][nt][h + 2], st.acc[2 * i + 1][nt][h],
-                                    st.acc[2 * i + 1][nt][h + 2]);
-            }
-        if (!sync())
-            return;
-        const bool whole = item.start >= lo && item.start + item.n <= hi;
-        float *part = p.parts + part_slot(c, item.start, N, C) * PART;
-        for (int e = tid; e < p.G * (kD / 4); e += kWarps * 32) {
-            const int row = e / (kD / 4), d = 4 * (e % (kD / 4));
-            float m = -INFINITY, mo = -INFINITY, l = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                m = fmaxf(m, wm[w * ROWS + row]);
-                mo = fmaxf(mo, wmo[w * ROWS + row]);
-            }
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float lw = wl[w * ROWS + row];
-                l += lw == 0.f ? 0.f : lw * exp2f(wm[w * ROWS + row] - m);
-                const float f = wmo[w * ROWS + row] == -INFINITY ? 0.f : exp2f(wmo[w * ROWS + row] - mo);
-                const float4 x = *reinterpret_cast<const float4 *>(wo + (w * ROWS + row) * kStride + d);
-                o.x = fmaf(f, x.x, o.x);
-                o.y = fmaf(f, x.y, o.y);
-                o.z = fmaf(f, x.z, o.z);
-                o.w = fmaf(f, x.w, o.w);
-            }
-            if (whole) {
-                write_out(p, item.pair, row, d, o, m, l, mo);
-            } else {
-                *reinterpret_cast<float4 *>(part + row * kD + d) = o;
-                if (d == 0) {
-                    part[ROWS * kD + row] = m;
-                    part[ROWS * kD + ROWS + row] = l;
-                    part[ROWS * kD + 2 * ROWS + row] = mo;
-                }
-            }
-        }
-        if (!whole) {
-            // ---- the pair's last CTA merges the CTAs' states, in their order
-            __threadfence();
-            if (!sync())
-                return;
-            const int c0 = cta_of(item.start, N, C), c1 = cta_of(item.start + item.n - 1, N, C);
-            if (tid == 0) {
-                const int prev = atomicAdd(p.arrivals + item.pair, 1);
-                s_last = prev == c1 - c0;
-                if (prev == c1 - c0) {
-                    p.arrivals[item.pair] = 0;   // for the next call
-                    __threadfence();
-                }
-            }
-            if (!sync())
-                return;
-            if (s_last) {
-                for (int e = tid; e < p.G * (kD / 4); e += kWarps * 32) {
-                    const int row = e / (kD / 4), d = 4 * (e % (kD / 4));
-                    float m = -INFINITY, mo = -INFINITY, l = 0.f;
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int x = c0; x <= c1; ++x) {
-                        const float *src = p.parts + part_slot(x, item.start, N, C) * PART;
-                        const float mx = __ldcg(src + ROWS * kD + row), lx = __ldcg(src + ROWS * kD + ROWS + row),
-                                    mox = __ldcg(src + ROWS * kD + 2 * ROWS + row);
-                        const float4 ox = __ldcg(reinterpret_cast<const float4 *>(src + row * kD + d));
-                        const float m_new = fmaxf(m, mx), mo_new = fmaxf(mo, mox);
-                        const float a = m == -INFINITY ? 0.f : exp2f(m - m_new), ax = mx == -INFINITY ? 0.f : exp2f(mx - m_new);
-                        const float b = mo == -INFINITY ? 0.f : exp2f(mo - mo_new),
-                                    bx = mox == -INFINITY ? 0.f : exp2f(mox - mo_new);
-                        l = (l == 0.f ? 0.f : l * a) + (lx == 0.f ? 0.f : lx * ax);
-                        o.x = o.x * b + ox.x * bx;
-                        o.y = o.y * b + ox.y * bx;
-                        o.z = o.z * b + ox.z * bx;
-                        o.w = o.w * b + ox.w * bx;
-                        m = m_new;
-                        mo = mo_new;
-                    }
-                    write_out(p, item.pair, row, d, o, m, l, mo);
-                }
-            }
-        }
-        if (!sync())   // wo, the statistics and s_last are free again
-            return;
     }
 }
 
@@ -688,16 +864,17 @@ bool sizes_ok(int B, int H_q, int H_kv)
            static_cast<long long>(B) * H_kv <= 65535;
 }
 
-// Workspace: an arrival count a pair, then two partial states a CTA.
-size_t counter_bytes(long long pairs)
+// Workspace: an arrival count a pair, two a group of CTAs, then two partial states a CTA.
+size_t counter_bytes(long long pairs, int sm_count)
 {
-    return (static_cast<size_t>(pairs) * sizeof(int) + 255) & ~static_cast<size_t>(255);
+    const long long groups = (kCtasPerSm * sm_count + kGroup - 1) / kGroup;
+    return (static_cast<size_t>(pairs + 2 * groups) * sizeof(int) + 255) & ~static_cast<size_t>(255);
 }
 
 size_t workspace_bytes_of(int B, int H_q, int H_kv, int sm_count)
 {
     const size_t part = H_q / H_kv <= 8 ? part_floats<1>() : part_floats<2>();
-    return counter_bytes(static_cast<long long>(B) * H_kv) + 2ull * kCtasPerSm * sm_count * part * sizeof(float);
+    return counter_bytes(static_cast<long long>(B) * H_kv, sm_count) + 2ull * kCtasPerSm * sm_count * part * sizeof(float);
 }
 
 template <int NT>
@@ -771,7 +948,7 @@ extern "C" SPARSE_API int sparse_paged_decode_attn_f8(const uint16_t *Q, const u
                             lse,
                             status,
                             static_cast<int *>(workspace),
-                            reinterpret_cast<float *>(static_cast<char *>(workspace) + counter_bytes(static_cast<long long>(B) * H_kv)),
+                            reinterpret_cast<float *>(static_cast<char *>(workspace) + counter_bytes(static_cast<long long>(B) * H_kv, dev.sm_count)),
                             s * 1.44269504088896340736f,   // log2(e): scores are exponentiated base 2
                             n_pages,
                             max_blocks,

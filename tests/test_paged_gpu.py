@@ -456,6 +456,34 @@ def test_attn_is_repeatable_and_runs_on_another_stream():
         assert torch.equal(x.O, first[0]) and torch.equal(x.lse, first[1])
 
 
+def test_attn_many_calls_of_a_full_grid():
+    """Every SM busy, ranges that begin and end inside a pair's list: the same bits each time,
+    equal to the plain implementation for a few pairs."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    B, H, G, k, max_blocks, n_pages = 8, 8, 8, 67, 300, 900
+    pages = (torch.randn((n_pages, H, 2, BLK, D), generator=g, device=DEV) * 64).clamp(-448, 448).to(F8)
+    scale = torch.full((n_pages, H, 2), 2.0 ** -6, device=DEV)
+    table = torch.randint(0, n_pages, (B, max_blocks), generator=g, device=DEV, dtype=torch.int32)
+    lens = i32([max_blocks * BLK - 7 * b for b in range(B)])
+    idx = torch.rand((B, H, max_blocks), generator=g, device=DEV).argsort(2)[:, :, :k].sort(2).values.to(torch.int32)
+    count = torch.randint(k // 2, k + 1, (B, H), generator=g, device=DEV, dtype=torch.int32)
+    Q = torch.randn((B, H * G, D), generator=g, device=DEV).to(torch.bfloat16)
+    a = Attn(B, H * G, H)
+    for i in range(100):
+        binding.sparse_paged_decode_attn_f8(Q, pages, scale, table, lens, a.O, a.ws, blk_idx=idx, count=count, lse=a.lse,
+                                            status=a.status)
+        if i == 0:
+            first = a.O.clone(), a.lse.clone()
+    torch.cuda.synchronize()
+    assert a.status.item() == 0 and torch.equal(a.O, first[0]) and torch.equal(a.lse, first[1])
+    for b in (0, 5):
+        rows = slice(b, b + 1)
+        want = ref.attn(ref.f64(Q[rows]), ref.f8_values(pages), ref.f64(scale), table[rows].cpu().numpy(),
+                        lens[rows].cpu().numpy(), idx[rows].cpu().numpy(), count[rows].cpu().numpy())
+        ref.assert_attn(a.O[rows], a.lse[rows], want, k * BLK)
+
+
 # ---------------------------------------------------------------- together
 
 
