@@ -38,7 +38,7 @@ constexpr int kMeta = 64;                         // item and part records: 32 b
 constexpr float kWeightBits = 12.f;               // weights reach 2^12: f16 holds them down to 2^-24
 constexpr uint64_t kWaitNs = 2000000000ull;
 #ifndef MINI
-#define MINI 4
+#define MINI 6
 #define PCOST 4
 #endif
 constexpr int kMinItems = MINI;                   // a CTA's range at least
@@ -136,15 +136,11 @@ __device__ __forceinline__ long long pair_length(int n)
     return n > 0 ? static_cast<long long>(n) + kPairCost : 0;
 }
 
-// The CTA whose range [N c / C, N (c + 1) / C) holds a place of the list.
-__device__ __forceinline__ int cta_of(long long at, long long N, long long C)
+// The CTA whose range [c per, (c + 1) per) holds a place of the list.
+__device__ __forceinline__ int cta_of(long long at, long long per)
 {
-    long long c = at * C / N;
-    while (N * (c + 1) / C <= at)
-        ++c;
-    while (N * c / C > at)
-        --c;
-    return static_cast<int>(c);
+    return ((at | per) >> 32) == 0 ? static_cast<int>(static_cast<uint32_t>(at) / static_cast<uint32_t>(per))
+                                   : static_cast<int>(at / per);
 }
 
 // Workspace slot of CTA c's state of a pair whose items begin in CTA c0: a CTA has at most
@@ -403,54 +399,80 @@ __device__ __forceinline__ bool merge_parts(const PagedAttnParams &p, int pair, 
     }
     if (!sync())
         return false;
-    if (tid < p.G) {
-        float m = -INFINITY, mo = -INFINITY, l = 0.f;
-        for (int j = 0; j < n; ++j) {
-            m = fmaxf(m, wm[j * ROWS + tid]);
-            mo = fmaxf(mo, wmo[j * ROWS + tid]);
+    // a warp takes a row, a lane a state
+    for (int row = tid >> 5; row < p.G; row += kWarps) {
+        const int lane = tid & 31, e = lane * ROWS + row;
+        const bool in = lane < n;
+        const float mj = in ? wm[e] : -INFINITY, lj = in ? wl[e] : 0.f, moj = in ? wmo[e] : -INFINITY;
+        float m = mj, mo = moj;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            mo = fmaxf(mo, __shfl_xor_sync(0xffffffffu, mo, o));
         }
-        for (int j = 0; j < n; ++j) {
-            const float lj = wl[j * ROWS + tid], moj = wmo[j * ROWS + tid];
-            l += lj == 0.f ? 0.f : lj * exp2f(wm[j * ROWS + tid] - m);
-            wmo[j * ROWS + tid] = moj == -INFINITY ? 0.f : exp2f(moj - mo);   // O's weight
+        float l = lj == 0.f ? 0.f : lj * exp2f(mj - m);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            l += __shfl_xor_sync(0xffffffffu, l, o);
+        if (in)
+            wmo[e] = moj == -INFINITY ? 0.f : exp2f(moj - mo);   // O's weight
+        if (lane == 0) {
+            row_stat[row] = m;
+            row_stat[ROWS + row] = l;
+            row_stat[2 * ROWS + row] = mo;
         }
-        row_stat[tid] = m;
-        row_stat[ROWS + tid] = l;
-        row_stat[2 * ROWS + tid] = mo;
     }
     if (!sync())
         return false;
     float *dst = p.parts + static_cast<size_t>(to < 0 ? 0 : to) * PART;
-    for (int e = tid; e < p.G * (kD / 4); e += kWarps * 32) {
-        const int row = e / (kD / 4), d = 4 * (e % (kD / 4));
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int j0 = 0; j0 < n; j0 += 16) {
-            float4 x[16];
+    const int items = p.G * (kD / 4);
+    // kPer items (a row's four dims) of kStep states a thread in flight
+    constexpr int kPer = 3, kStep = 8;
+    for (int e0 = tid; e0 < items; e0 += kPer * kWarps * 32) {
+        float4 o[kPer];
 #pragma unroll
-            for (int u = 0; u < 16; ++u)
-                x[u] = j0 + u < n ? __ldcg(reinterpret_cast<const float4 *>(
-                                        p.parts + static_cast<size_t>(slot(j0 + u)) * PART + row * kD + d))
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < kPer; ++i)
+            o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j0 = 0; j0 < n; j0 += kStep) {
+            float4 x[kStep][kPer];
 #pragma unroll
-            for (int u = 0; u < 16; ++u) {
-                const float f = j0 + u < n ? wmo[(j0 + u) * ROWS + row] : 0.f;
-                o.x = fmaf(f, x[u].x, o.x);
-                o.y = fmaf(f, x[u].y, o.y);
-                o.z = fmaf(f, x[u].z, o.z);
-                o.w = fmaf(f, x[u].w, o.w);
+            for (int u = 0; u < kStep; ++u) {
+                // an item's place in a state is its number
+                const float4 *src = reinterpret_cast<const float4 *>(p.parts + static_cast<size_t>(slot(j0 + u)) * PART);
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    x[u][i] = j0 + u < n && e0 + i * kWarps * 32 < items ? __ldcg(src + e0 + i * kWarps * 32) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
+#pragma unroll
+            for (int u = 0; u < kStep; ++u)
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    const int row = min(e0 + i * kWarps * 32, items - 1) / (kD / 4);
+                    const float f = j0 + u < n ? wmo[(j0 + u) * ROWS + row] : 0.f;
+                    o[i].x = fmaf(f, x[u][i].x, o[i].x);
+                    o[i].y = fmaf(f, x[u][i].y, o[i].y);
+                    o[i].z = fmaf(f, x[u][i].z, o[i].z);
+                    o[i].w = fmaf(f, x[u][i].w, o[i].w);
+                }
         }
-        const float m = row_stat[row], l = row_stat[ROWS + row], mo = row_stat[2 * ROWS + row];
-        if (to < 0) {
-            write_out(p, pair, row, d, o, m, l, mo);
-        } else {
-            // slot `to` is one of those read, each element by the thread that writes it; its
-            // statistics were read before the barriers
-            *reinterpret_cast<float4 *>(dst + row * kD + d) = o;
-            if (d == 0) {
-                dst[ROWS * kD + row] = m;
-                dst[ROWS * kD + ROWS + row] = l;
-                dst[ROWS * kD + 2 * ROWS + row] = mo;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int e = e0 + i * kWarps * 32;
+            if (e >= items)
+                break;
+            const int row = e / (kD / 4), d = 4 * (e % (kD / 4));
+            const float m = row_stat[row], l = row_stat[ROWS + row], mo = row_stat[2 * ROWS + row];
+            if (to < 0) {
+                write_out(p, pair, row, d, o[i], m, l, mo);
+            } else {
+                // slot `to` is one of those read, each element by the thread that writes it;
+                // its statistics were read before the barriers
+                *reinterpret_cast<float4 *>(dst + row * kD + d) = o[i];
+                if (d == 0) {
+                    dst[ROWS * kD + row] = m;
+                    dst[ROWS * kD + ROWS + row] = l;
+                    dst[ROWS * kD + 2 * ROWS + row] = mo;
+                }
             }
         }
     }
@@ -461,7 +483,7 @@ __device__ __forceinline__ bool merge_parts(const PagedAttnParams &p, int pair, 
 // workspace for the last of the pair's CTAs to merge.  All consumer threads call it.
 template <int NT, typename Sync>
 __device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const State<NT> &st, const Part &of, int c, long long lo,
-                                            long long hi, long long N, long long C, uint8_t *base, int *s_last, int warp,
+                                            long long hi, long long len, uint8_t *base, int *s_last, int warp,
                                             int lane, Sync sync)
 {
     constexpr int ROWS = 8 * NT;
@@ -473,7 +495,7 @@ __device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const Stat
     float *wl = wm + kWarps * ROWS, *wmo = wl + kWarps * ROWS;
     const int g8 = lane >> 2, t4 = lane & 3;
     const bool whole = of.start >= lo && of.start + of.n <= hi;
-    const int c0 = whole ? c : cta_of(of.start, N, C), c1 = whole ? c : cta_of(of.start + of.n - 1, N, C);
+    const int c0 = whole ? c : cta_of(of.start, len), c1 = whole ? c : cta_of(of.start + of.n - 1, len);
     float *part = p.parts + static_cast<size_t>(part_slot(c, c0)) * PART;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -651,9 +673,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             incl += s_sum[w];
         N += s_sum[w];
     }
-    const long long C = max(1LL, min(static_cast<long long>(gridDim.x), (N + kMinItems - 1) / kMinItems));
+    const long long even = (N >> 31) == 0 ? (static_cast<uint32_t>(N) + gridDim.x - 1) / gridDim.x
+                                          : (N + gridDim.x - 1) / gridDim.x;
+    const long long len = max(static_cast<long long>(kMinItems), even);   // a CTA's range
     const int c = static_cast<int>(blockIdx.x);
-    const long long lo = c < C ? N * c / C : N, hi = c < C ? N * (c + 1) / C : N;
+    const long long lo = min(N, c * len), hi = min(N, lo + len);
     if (lo < hi && incl - mine <= lo && lo < incl) {
         // the pair that holds `lo`
         long long at = incl - mine;
@@ -664,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 break;
             at += pair_length(n) * heads;
         }
-        const int h = all ? static_cast<int>((lo - at) / pair_length(n)) : 0;
+        const int h = all ? cta_of(lo - at, pair_length(n)) : 0;
         s_pair = u * heads + h;
         s_start = at + h * pair_length(n);
         s_n = n;
@@ -677,22 +701,29 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         // ------------------------------------------------------------ producer
         if (idle)
             return;
-        int pair = s_pair;
-        long long start = s_start;     // where this pair starts in the list
         const uint64_t pol = policy_evict_first();
         int it = 0, part = 0;          // the CTA's next item and part
         bool stop = false, wrong = false;
+        // first the pair that holds `lo`, then 32 pairs at a time, one a lane: their counts
+        // are loaded a step ahead
+        int pair = s_pair, n = lane == 0 ? s_n : 0;
+        long long start = s_start;     // where this group of pairs starts in the list
+        int group = 1;
         while (start < hi && pair < pairs && !stop) {
-            // the next 32 pairs, one a lane: items [a, a + cnt) of the pair are the CTA's
-            const int n = pair + lane < pairs ? pair_items(p, pair + lane, &bad) : 0;
+            const int n_next = pair + group + lane < pairs ? pair_items(p, pair + group + lane, &bad) : 0;
             long long end = pair_length(n);
+            if (group > 1) {
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long v = __shfl_up_sync(0xffffffffu, end, o);
-                if (lane >= o)
-                    end += v;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long v = __shfl_up_sync(0xffffffffu, end, o);
+                    if (lane >= o)
+                        end += v;
+                }
+            } else {
+                end = __shfl_sync(0xffffffffu, end, 0);
             }
             end += start;
+            // items [a, a + cnt) of the lane's pair are the CTA's
             const long long first = end - n;   // the pair's items start here
             const int a = static_cast<int>(max(0LL, min(static_cast<long long>(n), lo - first)));
             const int cnt = max(0, static_cast<int>(min(static_cast<long long>(n), hi - first)) - a);
@@ -782,8 +813,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 it += take;
             }
             start = __shfl_sync(0xffffffffu, end, 31);
-            pair += 32;
+            pair += group;
             part += __popc(has);
+            group = 32;
+            n = n_next;
         }
         // each consumer warp gets an item that ends it
         for (int j = 0; j < kWarps && lane == 0 && !stop; ++j, ++it) {
@@ -823,35 +856,49 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     Query<NT> q;
     State<NT> st;
     st.reset();
-    int part = 0, q_part = -1;
-    for (int it = warp;; it += kWarps) {
+    // While the first tiles travel: the first pair's queries, and a pass (`warm`) over whatever
+    // the stage holds, which brings the loop's code into the instruction cache; its result is
+    // dropped.
+    int part = 0, q_part = 0;
+    q.load(p, s_pair, lane);
+    bool warm = true;
+#pragma unroll 1
+    for (int it = warp;;) {
         const int stage = it % kStages;
-        if (!__all_sync(0xffffffffu, mbar_wait(full + 8 * stage, (it / kStages) & 1, kWaitNs))) {
-            give_up(p, lane);
-            return;
-        }
-        const Item item = items[it % kMeta];
-        const int next = item.part & ~kEnd;
-        // the parts before the item's are complete once every warp has come this far
-        for (; part < next; ++part) {
-            const Part of = parts[part % kMeta];
-            bool ok = finish_part<NT>(p, st, of, c, lo, hi, N, C, base, &s_last, warp, lane, sync);
-            st.reset();
-            ok = ok && sync();   // shared memory is free again
-            if (!ok) {
+        Item item{1.f, 0.f, kBlk, 0};
+        if (!warm) {
+            if (!__all_sync(0xffffffffu, mbar_wait(full + 8 * stage, (it / kStages) & 1, kWaitNs))) {
                 give_up(p, lane);
                 return;
             }
-        }
-        if (item.part & kEnd)
-            return;
-        if (item.rows > 0) {
-            if (part != q_part) {
+            item = items[it % kMeta];
+            const int next = item.part & ~kEnd;
+            // the parts before the item's are complete once every warp has come this far
+            for (; part < next; ++part) {
+                const Part of = parts[part % kMeta];
+                bool ok = finish_part<NT>(p, st, of, c, lo, hi, len, base, &s_last, warp, lane, sync);
+                st.reset();
+                ok = ok && sync();   // shared memory is free again
+                if (!ok) {
+                    give_up(p, lane);
+                    return;
+                }
+            }
+            if (item.part & kEnd)
+                return;
+            if (part != q_part && item.rows > 0) {
                 q_part = part;
                 q.load(p, parts[part % kMeta].pair, lane);
             }
-            attend<NT>(st, q, base_s + stage * kStageBytes, item.ks, item.log2_vs, item.rows, lane);
         }
+        if (item.rows > 0)
+            attend<NT>(st, q, base_s + stage * kStageBytes, item.ks, item.log2_vs, item.rows, lane);
+        if (warm) {
+            warm = false;
+            st.reset();
+            continue;
+        }
+        it += kWarps;
         __syncwarp();
         if (lane == 0)
             mbar_arrive(empty + 8 * stage);
