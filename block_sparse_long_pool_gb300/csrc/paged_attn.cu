@@ -58,9 +58,10 @@ constexpr int kEnd = 0x40000000;   // added to the number of parts
 
 // The CTA's items of one pair.
 struct Part {
-    long long start;   // where the pair's items start in the flattened list
+    int start;         // where the pair's items start in the flattened list
     int n;             // the pair's items
     int pair;
+    int unused;
 };
 static_assert(sizeof(Part) == 16, "one 16-byte load");
 
@@ -110,37 +111,28 @@ struct PagedAttnParams {
     int G;
 };
 
-// Blocks of request b (a length outside its table is clamped).
-__device__ __forceinline__ int request_blocks(const PagedAttnParams &p, int b, bool *bad)
+// Tokens of request b (a length outside its table is clamped).
+__device__ __forceinline__ int request_len(const PagedAttnParams &p, int b, bool *bad)
 {
-    const long long len = p.seq_len[b], cap = static_cast<long long>(p.max_blocks) * kBlk;
-    if (len < 0 || len > cap)
-        *bad = true;
-    return len <= 0 ? 0 : static_cast<int>((min(len, cap) + kBlk - 1) / kBlk);
+    const int len = p.seq_len[b], cap = p.max_blocks * kBlk;
+    *bad |= len < 0 || len > cap;
+    return max(0, min(len, cap));
 }
 
 // Items of a pair.
-__device__ __forceinline__ int pair_items(const PagedAttnParams &p, int pair, bool *bad)
+__device__ __noinline__ int pair_items(const PagedAttnParams &p, int pair, bool *bad)
 {
     if (p.blk_idx == nullptr)
-        return request_blocks(p, pair / p.H_kv, bad);
+        return (request_len(p, pair / p.H_kv, bad) + kBlk - 1) / kBlk;
     const int n = p.count[pair];
-    if (n < 0 || n > p.k_tot)
-        *bad = true;
-    return n < 0 ? 0 : min(n, p.k_tot);
+    *bad |= n < 0 || n > p.k_tot;
+    return max(0, min(n, p.k_tot));
 }
 
-// Its length in the flattened list.
-__device__ __forceinline__ long long pair_length(int n)
+// Its length in the flattened list (all of it has at most 2^31 - 1 places).
+__device__ __forceinline__ int pair_length(int n)
 {
-    return n > 0 ? static_cast<long long>(n) + kPairCost : 0;
-}
-
-// The CTA whose range [c per, (c + 1) per) holds a place of the list.
-__device__ __forceinline__ int cta_of(long long at, long long per)
-{
-    return ((at | per) >> 32) == 0 ? static_cast<int>(static_cast<uint32_t>(at) / static_cast<uint32_t>(per))
-                                   : static_cast<int>(at / per);
+    return n > 0 ? n + kPairCost : 0;
 }
 
 // Workspace slot of CTA c's state of a pair whose items begin in CTA c0: a CTA has at most
@@ -369,137 +361,63 @@ __device__ __forceinline__ void attend(State<NT> &st, const Query<NT> &q, uint32
 __device__ __forceinline__ void write_out(const PagedAttnParams &p, int pair, int row, int d, float4 o, float m, float l,
                                           float mo)
 {
-    const size_t at = (static_cast<size_t>(pair / p.H_kv) * p.H_q + static_cast<size_t>(pair % p.H_kv) * p.G + row);
-    const float f = l > 0.f ? exp2f(mo - m) / l : l == 0.f ? 0.f : l;   // l NaN: the row is NaN
+    const size_t at = static_cast<size_t>(pair) * p.G + row;   // = b * H_q + g * G + row
+    // 2^(mo - m) in two factors: a page of tiny values takes it below the smallest fp32 number
+    const float h = l == 0.f ? 0.f : ex2_approx(0.5f * (mo - m)), inv = l == 0.f ? 0.f : __fdividef(1.f, l);
     if (l == 0.f)
         o = make_float4(0.f, 0.f, 0.f, 0.f);
-    *reinterpret_cast<uint2 *>(p.O + at * kD + d) = make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
+    *reinterpret_cast<uint2 *>(p.O + at * kD + d) =
+        make_uint2(pack_bf16x2(o.x * h * inv * h, o.y * h * inv * h), pack_bf16x2(o.z * h * inv * h, o.w * h * inv * h));
     if (d == 0 && p.lse != nullptr)
-        p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+        p.lse[at] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994530942f;
 }
 
-// The states of CTAs first, first + step, ... (n of them, at most kDirect; all but the first
-// at multiples of `step`) of a pair, merged in that order: into O, or (to >= 0) into the
-// workspace's slot `to`.  The consumer threads all call it; w holds 4 * kDirect * ROWS floats.
-template <int NT, typename Sync>
-__device__ __forceinline__ bool merge_parts(const PagedAttnParams &p, int pair, int c0, int first, int n, int step, int to,
-                                            float *w, int tid, Sync sync)
+// The consumer warps meet at `bar` (their meetings take turns of its parity); false where one
+// of them gave up: it leaves, and so do the others.
+__device__ __noinline__ bool meet(uint32_t bar, int parity)
 {
-    constexpr int ROWS = 8 * NT;
-    constexpr int PART = part_floats<NT>();
-    float *wm = w, *wl = wm + kDirect * ROWS, *wmo = wl + kDirect * ROWS, *row_stat = wmo + kDirect * ROWS;
-    auto slot = [&](int j) { return part_slot(j == 0 ? first : (first / step + j) * step, c0); };
-    for (int e = tid; e < n * ROWS; e += kWarps * 32) {
-        const float *src = p.parts + static_cast<size_t>(slot(e / ROWS)) * PART + ROWS * kD + e % ROWS;
-        if (e % ROWS < p.G) {
-            wm[e] = __ldcg(src);
-            wl[e] = __ldcg(src + ROWS);
-            wmo[e] = __ldcg(src + 2 * ROWS);
-        }
-    }
-    if (!sync())
-        return false;
-    // a warp takes a row, a lane a state
-    for (int row = tid >> 5; row < p.G; row += kWarps) {
-        const int lane = tid & 31, e = lane * ROWS + row;
-        const bool in = lane < n;
-        const float mj = in ? wm[e] : -INFINITY, lj = in ? wl[e] : 0.f, moj = in ? wmo[e] : -INFINITY;
-        float m = mj, mo = moj;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            mo = fmaxf(mo, __shfl_xor_sync(0xffffffffu, mo, o));
-        }
-        float l = lj == 0.f ? 0.f : lj * exp2f(mj - m);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            l += __shfl_xor_sync(0xffffffffu, l, o);
-        if (in)
-            wmo[e] = moj == -INFINITY ? 0.f : exp2f(moj - mo);   // O's weight
-        if (lane == 0) {
-            row_stat[row] = m;
-            row_stat[ROWS + row] = l;
-            row_stat[2 * ROWS + row] = mo;
-        }
-    }
-    if (!sync())
-        return false;
-    float *dst = p.parts + static_cast<size_t>(to < 0 ? 0 : to) * PART;
-    const int items = p.G * (kD / 4);
-    // kPer items (a row's four dims) of kStep states a thread in flight
-    constexpr int kPer = 3, kStep = 8;
-    for (int e0 = tid; e0 < items; e0 += kPer * kWarps * 32) {
-        float4 o[kPer];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int j0 = 0; j0 < n; j0 += kStep) {
-            float4 x[kStep][kPer];
-#pragma unroll
-            for (int u = 0; u < kStep; ++u) {
-                // an item's place in a state is its number
-                const float4 *src = reinterpret_cast<const float4 *>(p.parts + static_cast<size_t>(slot(j0 + u)) * PART);
-#pragma unroll
-                for (int i = 0; i < kPer; ++i)
-                    x[u][i] = j0 + u < n && e0 + i * kWarps * 32 < items ? __ldcg(src + e0 + i * kWarps * 32) : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-#pragma unroll
-            for (int u = 0; u < kStep; ++u)
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    const int row = min(e0 + i * kWarps * 32, items - 1) / (kD / 4);
-                    const float f = j0 + u < n ? wmo[(j0 + u) * ROWS + row] : 0.f;
-                    o[i].x = fmaf(f, x[u][i].x, o[i].x);
-                    o[i].y = fmaf(f, x[u][i].y, o[i].y);
-                    o[i].z = fmaf(f, x[u][i].z, o[i].z);
-                    o[i].w = fmaf(f, x[u][i].w, o[i].w);
-                }
-        }
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int e = e0 + i * kWarps * 32;
-            if (e >= items)
-                break;
-            const int row = e / (kD / 4), d = 4 * (e % (kD / 4));
-            const float m = row_stat[row], l = row_stat[ROWS + row], mo = row_stat[2 * ROWS + row];
-            if (to < 0) {
-                write_out(p, pair, row, d, o[i], m, l, mo);
-            } else {
-                // slot `to` is one of those read, each element by the thread that writes it;
-                // its statistics were read before the barriers
-                *reinterpret_cast<float4 *>(dst + row * kD + d) = o[i];
-                if (d == 0) {
-                    dst[ROWS * kD + row] = m;
-                    dst[ROWS * kD + ROWS + row] = l;
-                    dst[ROWS * kD + 2 * ROWS + row] = mo;
-                }
-            }
-        }
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        mbar_arrive(bar);
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, 2 * kWaitNs)) != 0;
+}
+
+// One of the `expect` arrivals at a counter, for the whole CTA: true for the last, which
+// resets the counter and then sees what all wrote before theirs.
+__device__ __forceinline__ bool arrive_last(int *counter, int expect, int *flag, int tid)
+{
+    if (tid == 0) {
+        __threadfence();
+        const int prev = atomicAdd(counter, 1);
+        *flag = prev == expect - 1;
+        if (prev == expect - 1)
+            *counter = 0;   // for the next call
+        __threadfence();
     }
     return true;
 }
 
-// The CTA's part of a pair: its 4 warps' states merged, and written out, or left in the
+// The CTA's part of a pair: its warps' states merged, and written out, or left in the
 // workspace for the last of the pair's CTAs to merge.  All consumer threads call it.
-template <int NT, typename Sync>
-__device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const State<NT> &st, const Part &of, int c, long long lo,
-                                            long long hi, long long len, uint8_t *base, int *s_last, int warp,
-                                            int lane, Sync sync)
+template <int NT>
+__device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const State<NT> &st, const Part &of, int c, int lo,
+                                            int hi, int len, uint8_t *base, uint32_t bar, int &meetings, int *flag, int warp,
+                                            int lane)
 {
     constexpr int ROWS = 8 * NT;
     constexpr int PART = part_floats<NT>();
     using S = Smem<NT>;
-    const int tid = warp * 32 + lane, pairs = p.B * p.H_kv;
+    const int tid = warp * 32 + lane;
     float *wo = reinterpret_cast<float *>(base + S::kWo);
-    float *wm = reinterpret_cast<float *>(base + S::kStat);   // [4][ROWS] each: m, l, mo
+    float *wm = reinterpret_cast<float *>(base + S::kStat);   // [kWarps][ROWS] each: m, l, mo
     float *wl = wm + kWarps * ROWS, *wmo = wl + kWarps * ROWS;
     const int g8 = lane >> 2, t4 = lane & 3;
     const bool whole = of.start >= lo && of.start + of.n <= hi;
-    const int c0 = whole ? c : cta_of(of.start, len), c1 = whole ? c : cta_of(of.start + of.n - 1, len);
+    const int c0 = of.start / len, c1 = (of.start + of.n - 1) / len;
     float *part = p.parts + static_cast<size_t>(part_slot(c, c0)) * PART;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        if (nt > 0 && !sync())   // wo is free again
+        if (nt > 0 && !meet(bar, meetings++ & 1))   // wo is free again
             return false;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -520,8 +438,9 @@ __device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const Stat
                     make_float4(st.acc[2 * i][nt][h], st.acc[2 * i][nt][h + 2], st.acc[2 * i + 1][nt][h],
                                 st.acc[2 * i + 1][nt][h + 2]);
         }
-        if (!sync())
+        if (!meet(bar, meetings++ & 1))
             return false;
+#pragma unroll 1
         for (int e = tid; e < min(8, p.G - nt * 8) * (kD / 4); e += kWarps * 32) {
             const int r8 = e / (kD / 4), row = nt * 8 + r8, d = 4 * (e % (kD / 4));
             float m = -INFINITY, mo = -INFINITY, l = 0.f;
@@ -534,8 +453,8 @@ __device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const Stat
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float lw = wl[w * ROWS + row];
-                l += lw == 0.f ? 0.f : lw * exp2f(wm[w * ROWS + row] - m);
-                const float f = wmo[w * ROWS + row] == -INFINITY ? 0.f : exp2f(wmo[w * ROWS + row] - mo);
+                l += lw == 0.f ? 0.f : lw * ex2_approx(wm[w * ROWS + row] - m);
+                const float f = wmo[w * ROWS + row] == -INFINITY ? 0.f : ex2_approx(wmo[w * ROWS + row] - mo);
                 const float4 x = *reinterpret_cast<const float4 *>(wo + (w * 8 + r8) * kStride + d);
                 o.x = fmaf(f, x.x, o.x);
                 o.y = fmaf(f, x.y, o.y);
@@ -554,50 +473,134 @@ __device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const Stat
             }
         }
     }
-    // ---- the states of a pair's CTAs, merged by the last of them; where they are many,
-    // by the last of each kGroup neighbours first
-    int *count_of = p.arrivals + of.pair;
-    int expect = c1 - c0 + 1, first = c0, step = 1;
-    if (c1 > c0 && expect > kDirect) {
-        const int g = c / kGroup, g_first = max(c0, g * kGroup), g_n = min(c1, g * kGroup + kGroup - 1) - g_first + 1;
-        // at most two such pairs meet a group: one from before it, one that starts in it
-        int *group_count = p.arrivals + pairs + 2 * g + (c0 < g * kGroup ? 0 : 1);
-        __threadfence();
-        if (!sync())
-            return false;
-        if (tid == 0) {
-            const int prev = atomicAdd(group_count, 1);
-            if (prev == g_n - 1)
-                *group_count = 0;   // for the next call
-            *s_last = prev == g_n - 1;
-            __threadfence();
-        }
-        if (!sync())
-            return false;
-        if (*s_last) {
-            if (!merge_parts<NT>(p, of.pair, c0, g_first, g_n, 1, part_slot(g_first, c0), wo, tid, sync))
-                return false;
-            expect = c1 / kGroup - c0 / kGroup + 1;
-            step = kGroup;
+    if (whole)
+        return true;
+
+    // The states of the pair's CTAs, merged by the last of them, in their order.  Where they
+    // are many, the last of each kGroup neighbours merges theirs first (into the slot of the
+    // first of them), and the last of those the groups'.
+    float *sm = wo, *sl = sm + kDirect * ROWS, *smo = sl + kDirect * ROWS, *row_stat = smo + kDirect * ROWS;
+    const bool grouped = c1 - c0 + 1 > kDirect;
+    const int g = c / kGroup, g0 = c0 / kGroup;
+#pragma unroll 1
+    for (int level = grouped ? 0 : 1; level < 2; ++level) {
+        // the states of CTAs first, then of those `step` apart
+        int *counter;
+        int first = c0, n = c1 - c0 + 1, step = 1;
+        if (level == 0) {
+            // at most two such pairs meet a group: one from before it, one that starts in it
+            counter = p.arrivals + p.B * p.H_kv + 2 * g + (c0 < g * kGroup ? 0 : 1);
+            first = max(c0, g * kGroup);
+            n = min(c1, g * kGroup + kGroup - 1) - first + 1;
         } else {
-            expect = 0;   // this CTA's part is done
+            counter = p.arrivals + of.pair;
+            if (grouped) {
+                n = c1 / kGroup - g0 + 1;
+                step = kGroup;
+            }
         }
-    }
-    if (c1 > c0 && expect > 0) {
-        __threadfence();
-        if (!sync())
+        if (!meet(bar, meetings++ & 1))   // the CTA's state is written
             return false;
-        if (tid == 0) {
-            const int prev = atomicAdd(count_of, 1);
-            if (prev == expect - 1)
-                *count_of = 0;
-            *s_last = prev == expect - 1;
-            __threadfence();
+        arrive_last(counter, n, flag, tid);
+        if (!meet(bar, meetings++ & 1))
+            return false;
+        if (*flag == 0)
+            return true;
+        auto slot = [&](int j) {
+            return p.parts + static_cast<size_t>(part_slot(j == 0 ? first : step == 1 ? first + j : (g0 + j) * kGroup, c0)) * PART;
+        };
+#pragma unroll 1
+        for (int e = tid; e < n * ROWS; e += kWarps * 32) {
+            const float *src = slot(e / ROWS) + ROWS * kD + e % ROWS;
+            if (e % ROWS < p.G) {
+                sm[e] = __ldcg(src);
+                sl[e] = __ldcg(src + ROWS);
+                smo[e] = __ldcg(src + 2 * ROWS);
+            }
         }
-        if (!sync())
+        if (!meet(bar, meetings++ & 1))
             return false;
-        if (*s_last && !merge_parts<NT>(p, of.pair, c0, first, expect, step, -1, wo, tid, sync))
+        // a warp takes a row, a lane a state
+#pragma unroll 1
+        for (int row = warp; row < p.G; row += kWarps) {
+            const int e = lane * ROWS + row;
+            const bool in = lane < n;
+            const float mj = in ? sm[e] : -INFINITY, lj = in ? sl[e] : 0.f, moj = in ? smo[e] : -INFINITY;
+            float m = mj, mo = moj;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                mo = fmaxf(mo, __shfl_xor_sync(0xffffffffu, mo, o));
+            }
+            float l = lj == 0.f ? 0.f : lj * ex2_approx(mj - m);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                l += __shfl_xor_sync(0xffffffffu, l, o);
+            if (in)
+                smo[e] = moj == -INFINITY ? 0.f : ex2_approx(moj - mo);   // O's weight
+            if (lane == 0) {
+                row_stat[row] = m;
+                row_stat[ROWS + row] = l;
+                row_stat[2 * ROWS + row] = mo;
+            }
+        }
+        if (!meet(bar, meetings++ & 1))
             return false;
+        float *dst = slot(0);
+        const int quads = p.G * (kD / 4);   // four dims of a row each
+        // kPer quads of kStep states a thread in flight
+        constexpr int kPer = 3, kStep = 8;
+#pragma unroll 1
+        for (int e0 = tid; e0 < quads; e0 += kPer * kWarps * 32) {
+            float4 o[kPer];
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+            for (int j0 = 0; j0 < n; j0 += kStep) {
+                float4 x[kStep][kPer];
+#pragma unroll
+                for (int u = 0; u < kStep; ++u) {
+                    // a quad's place in a state is its number
+                    const float4 *src = reinterpret_cast<const float4 *>(slot(j0 + u));
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i)
+                        x[u][i] = j0 + u < n && e0 + i * kWarps * 32 < quads ? __ldcg(src + e0 + i * kWarps * 32)
+                                                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+#pragma unroll
+                for (int u = 0; u < kStep; ++u)
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) {
+                        const int row = min(e0 + i * kWarps * 32, quads - 1) / (kD / 4);
+                        const float f = j0 + u < n ? smo[(j0 + u) * ROWS + row] : 0.f;
+                        o[i].x = fmaf(f, x[u][i].x, o[i].x);
+                        o[i].y = fmaf(f, x[u][i].y, o[i].y);
+                        o[i].z = fmaf(f, x[u][i].z, o[i].z);
+                        o[i].w = fmaf(f, x[u][i].w, o[i].w);
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int e = e0 + i * kWarps * 32;
+                if (e >= quads)
+                    break;
+                const int row = e / (kD / 4), d = 4 * (e % (kD / 4));
+                const float m = row_stat[row], l = row_stat[ROWS + row], mo = row_stat[2 * ROWS + row];
+                if (level == 1) {
+                    write_out(p, of.pair, row, d, o[i], m, l, mo);
+                } else {
+                    // each element of the slot was read by the thread that writes it, and its
+                    // statistics before the meetings
+                    *reinterpret_cast<float4 *>(dst + row * kD + d) = o[i];
+                    if (d == 0) {
+                        dst[ROWS * kD + row] = m;
+                        dst[ROWS * kD + ROWS + row] = l;
+                        dst[ROWS * kD + 2 * ROWS + row] = mo;
+                    }
+                }
+            }
+        }
     }
     return true;
 }
@@ -614,20 +617,18 @@ __device__ __forceinline__ void give_up(const PagedAttnParams &p, int lane)
 
 template <int NT>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
-    paged_attn_kernel(const __grid_constant__ CUtensorMap map, const PagedAttnParams p)
+    paged_attn_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ PagedAttnParams p)
 {
     constexpr int ROWS = 8 * NT;
     using S = Smem<NT>;
     static_assert((3 * kDirect + 3) * ROWS <= kWarps * 8 * kStride, "the merge's weights fit the warps' states");
     extern __shared__ uint8_t smem_raw[];
-    __shared__ long long s_sum[kWarps + 1];
-    __shared__ long long s_start;
-    __shared__ int s_pair, s_n, s_last;
+    __shared__ int s_sum[kWarps + 1], s_pair, s_n, s_start, s_last;
     const uint32_t base_s = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *base = smem_raw + (base_s - smem_u32(smem_raw));
     Item *items = reinterpret_cast<Item *>(base + S::kItems);
     Part *parts = reinterpret_cast<Part *>(base + S::kParts);
-    const uint32_t full = base_s + S::kBars, empty = full + 8 * kStages, meet = empty + 8 * kStages;
+    const uint32_t full = base_s + S::kBars, empty = full + 8 * kStages, bar = empty + 8 * kStages;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
@@ -635,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             mbar_init(full + 8 * i, 2);          // the load's expect_tx, and the item record
             mbar_init(empty + 8 * i, 1);         // the warp that took the tile
         }
-        mbar_init(meet, kWarps);
+        mbar_init(bar, kWarps);
         fence_barrier_init();
     }
     if (tid == kWarps * 32)
@@ -651,44 +652,41 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     const int per = (units + kThreads - 1) / kThreads;
     const int u0 = min(units, tid * per), u1 = min(units, u0 + per);
     bool bad = false;
-    long long mine = 0;
+    int mine = 0;
     for (int u = u0; u < u1; ++u)
         mine += pair_length(pair_items(p, u * heads, &bad)) * heads;
     if (bad && blockIdx.x == 0)
         report(p.status, SPARSE_ERR_BAD_INDEX);
-    long long incl = mine;
+    int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o)
             incl += v;
     }
     if (lane == 31)
         s_sum[warp] = incl;
     __syncthreads();
-    long long N = 0;
+    int N = 0;
 #pragma unroll
     for (int w = 0; w <= kWarps; ++w) {
         if (w < warp)
             incl += s_sum[w];
         N += s_sum[w];
     }
-    const long long even = (N >> 31) == 0 ? (static_cast<uint32_t>(N) + gridDim.x - 1) / gridDim.x
-                                          : (N + gridDim.x - 1) / gridDim.x;
-    const long long len = max(static_cast<long long>(kMinItems), even);   // a CTA's range
+    const int len = max(kMinItems, static_cast<int>((static_cast<uint32_t>(N) + gridDim.x - 1) / gridDim.x));   // a CTA's range
     const int c = static_cast<int>(blockIdx.x);
-    const long long lo = min(N, c * len), hi = min(N, lo + len);
+    const int lo = static_cast<int>(min(static_cast<uint32_t>(N), static_cast<uint32_t>(c) * len)), hi = min(N - lo, len) + lo;
     if (lo < hi && incl - mine <= lo && lo < incl) {
         // the pair that holds `lo`
-        long long at = incl - mine;
-        int u = u0, n = 0;
+        int at = incl - mine, u = u0, n = 0;
         for (; u < u1; ++u) {
             n = pair_items(p, u * heads, &bad);
             if (at + pair_length(n) * heads > lo)
                 break;
             at += pair_length(n) * heads;
         }
-        const int h = all ? cta_of(lo - at, pair_length(n)) : 0;
+        const int h = all ? (lo - at) / pair_length(n) : 0;
         s_pair = u * heads + h;
         s_start = at + h * pair_length(n);
         s_n = n;
@@ -707,15 +705,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         // first the pair that holds `lo`, then 32 pairs at a time, one a lane: their counts
         // are loaded a step ahead
         int pair = s_pair, n = lane == 0 ? s_n : 0;
-        long long start = s_start;     // where this group of pairs starts in the list
+        int start = s_start;           // where this group of pairs starts in the list
         int group = 1;
         while (start < hi && pair < pairs && !stop) {
             const int n_next = pair + group + lane < pairs ? pair_items(p, pair + group + lane, &bad) : 0;
-            long long end = pair_length(n);
+            int end = pair_length(n);
             if (group > 1) {
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const long long v = __shfl_up_sync(0xffffffffu, end, o);
+                    const int v = __shfl_up_sync(0xffffffffu, end, o);
                     if (lane >= o)
                         end += v;
                 }
@@ -724,9 +722,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             }
             end += start;
             // items [a, a + cnt) of the lane's pair are the CTA's
-            const long long first = end - n;   // the pair's items start here
-            const int a = static_cast<int>(max(0LL, min(static_cast<long long>(n), lo - first)));
-            const int cnt = max(0, static_cast<int>(min(static_cast<long long>(n), hi - first)) - a);
+            const int first = end - n;   // the pair's items start here
+            const int a = max(0, min(n, lo - first)), cnt = max(0, min(n, hi - first) - a);
             int upto = cnt;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -738,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             const unsigned has = __ballot_sync(0xffffffffu, cnt > 0);
             const int my_part = part + __popc(has & ((1u << lane) - 1));
             if (cnt > 0)
-                parts[my_part % kMeta] = Part{first, n, pair + lane};
+                parts[my_part % kMeta] = Part{first, n, pair + lane, 0};
             for (int done = 0; done < total && !stop; done += 32) {
                 // lane j resolves item done + j: of the first pair whose count reaches past it
                 const int take = min(32, total - done);
@@ -758,16 +755,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 if (lane < take) {
                     const int b = of / p.H_kv;
                     const int blk = all ? i : p.blk_idx[static_cast<size_t>(of) * p.k_tot + i];
-                    const long long rows = min(static_cast<long long>(p.seq_len[b]), static_cast<long long>(p.max_blocks) * kBlk) -
-                                           static_cast<long long>(blk) * kBlk;
+                    const int tokens = request_len(p, b, &bad);
                     if (blk < 0 || blk >= p.max_blocks) {
                         wrong = true;
-                    } else if (rows > 0) {
+                    } else if (blk * kBlk < tokens) {
                         const int page = p.block_table[static_cast<size_t>(b) * p.max_blocks + blk];
                         if (page < 0 || page >= p.n_pages) {
                             wrong = true;
                         } else {
-                            item.rows = static_cast<int>(min(rows, static_cast<long long>(kBlk)));
+                            item.rows = min(tokens - blk * kBlk, kBlk);
                             unit = page * p.H_kv + of % p.H_kv;
                             sc = *reinterpret_cast<const float2 *>(p.kv_scale + 2 * static_cast<size_t>(unit));
                         }
@@ -837,14 +833,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
 
     // ---------------------------------------------------------------- consumers
-    // the consumer warps meet; false where one of them gave up (it leaves, and so do the others)
-    int meetings = 0;
-    auto sync = [&] {
-        __syncwarp();
-        if (lane == 0)
-            mbar_arrive(meet);
-        return __all_sync(0xffffffffu, mbar_wait(meet, meetings++ & 1, 2 * kWaitNs)) != 0;
-    };
     // rows of pairs without items, shared out over the CTAs
     for (int pair = c + static_cast<int>(gridDim.x) * warp; pair < pairs; pair += static_cast<int>(gridDim.x) * kWarps)
         if (pair_items(p, pair, &bad) == 0)
@@ -859,8 +847,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // While the first tiles travel: the first pair's queries, and a pass (`warm`) over whatever
     // the stage holds, which brings the loop's code into the instruction cache; its result is
     // dropped.
-    int part = 0, q_part = 0;
-    q.load(p, s_pair, lane);
+    int part = 0, q_part = -1, meetings = 0;
     bool warm = true;
 #pragma unroll 1
     for (int it = warp;;) {
@@ -876,9 +863,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             // the parts before the item's are complete once every warp has come this far
             for (; part < next; ++part) {
                 const Part of = parts[part % kMeta];
-                bool ok = finish_part<NT>(p, st, of, c, lo, hi, len, base, &s_last, warp, lane, sync);
+                bool ok = finish_part<NT>(p, st, of, c, lo, hi, len, base, bar, meetings, &s_last, warp, lane);
                 st.reset();
-                ok = ok && sync();   // shared memory is free again
+                ok = ok && meet(bar, meetings++ & 1);   // shared memory is free again
                 if (!ok) {
                     give_up(p, lane);
                     return;
@@ -886,10 +873,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             }
             if (item.part & kEnd)
                 return;
-            if (part != q_part && item.rows > 0) {
-                q_part = part;
-                q.load(p, parts[part % kMeta].pair, lane);
-            }
+        }
+        if (part != q_part && item.rows > 0) {
+            q_part = part;
+            q.load(p, warm ? s_pair : parts[part % kMeta].pair, lane);
         }
         if (item.rows > 0)
             attend<NT>(st, q, base_s + stage * kStageBytes, item.ks, item.log2_vs, item.rows, lane);
@@ -975,6 +962,11 @@ extern "C" SPARSE_API int sparse_paged_decode_attn_f8(const uint16_t *Q, const u
     const size_t need = sparse_paged_decode_attn_f8_workspace_size(B, H_q, H_kv);
     if (workspace_bytes < need)
         return fail(SPARSE_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", name, workspace_bytes, need);
+    const long long places = static_cast<long long>(B) * H_kv * ((blk_idx != nullptr ? k_tot : max_blocks) + kPairCost);
+    if (places > INT_MAX)
+        return fail(SPARSE_ERR_UNSUPPORTED, "%s: %lld (pair, block) items", name, places);
+    if (max_blocks > INT_MAX / kBlk)
+        return fail(SPARSE_ERR_UNSUPPORTED, "%s: max_blocks=%d: token positions past 2^31", name, max_blocks);
     if (2LL * n_pages * H_kv > INT_MAX)
         return fail(SPARSE_ERR_UNSUPPORTED, "%s: n_pages * H_kv = %lld > 2^30", name, static_cast<long long>(n_pages) * H_kv);
     sp_host::DeviceInfo dev;
