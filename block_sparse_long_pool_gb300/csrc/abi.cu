@@ -167,7 +167,7 @@ int make_page_tensor_map(CUtensorMap *map, const void *base, long long tiles)
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(sp::kD), static_cast<cuuint64_t>(sp::kBlk),
                                 static_cast<cuuint64_t>(tiles)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(sp::kD), static_cast<cuuint64_t>(sp::kD) * sp::kBlk};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(sp::kD), static_cast<cuuint32_t>(sp::kBlk), 2};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(sp::kD), static_cast<cuuint32_t>(sp::kBlk), 1};
     const cuuint32_t elem_strides[3] = {1, 1, 1};
     CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box,
                           elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,

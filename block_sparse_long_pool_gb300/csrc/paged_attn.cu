@@ -7,8 +7,9 @@
 // and its state is merged.  So requests of very different lengths load the SMs evenly.  A
 // pair whose items lie in several CTAs is merged by the one that finishes last, in CTA order.
 //
-// Per CTA: warp 3 resolves items to pages, 32 at a time (list -> block table -> scales), and
-// streams tiles with one TMA load each into a ring of 6; warps 0..2 take whole tiles in turn.
+// Per CTA: warp 4 resolves items to pages, 32 at a time (list -> block table -> scales), and
+// streams their keys and values, a TMA load each; warps 0..3 take whole tiles in turn, each
+// from three 8 KB slots of its own: while it works on one, the next two travel.
 //   S^T = K Q^T and O^T += V^T P^T run on mma.m16n8k16 in f16: every e4m3 value is an f16
 // value, so the tiles are converted without rounding, two elements an instruction.  Q rows
 // are scaled to f16's range by a power of two of their own.  Which 16 of the 128 dims make
@@ -28,10 +29,7 @@ namespace {
 
 using namespace sp;
 
-constexpr int kWarps = 3;                         // consumer warps
-constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kTile = kBlk * kD;                  // keys (or values) of a block: 8 KB
-constexpr int kStageBytes = 2 * kTile;
 constexpr int kCtasPerSm = 2;
 constexpr int kStride = kD + 4;                   // floats a row of the warps' states
 constexpr int kMeta = 64;                         // item and part records: 32 being written + the ring's
@@ -65,21 +63,32 @@ struct Part {
 };
 static_assert(sizeof(Part) == 16, "one 16-byte load");
 
-// Tiles in flight: a multiple of the consumer warps, so that a stage always belongs to the
-// same warp, which waits for each of its fills in turn (a wait by parity tells only
-// neighbouring fills apart).
-constexpr int kStages = 6;
-static_assert(kStages % kWarps == 0, "a stage belongs to one warp");
+// Consumer warps of a CTA: 4, or 3 for more than 8 rows, whose states need more registers than
+// five warps of two CTAs an SM can have.
+template <int NT>
+constexpr int warps()
+{
+    return NT == 1 ? 4 : 3;
+}
+
+// 8 KB slots a consumer warp has to itself.  Its i-th item's keys are their fill 2 i, its
+// values fill 2 i + 1; fill f goes to slot f % slots.  So a warp waits for every fill of its
+// slots in turn (a wait by parity tells only neighbouring fills apart).
+template <int NT>
+constexpr int slots()
+{
+    return NT == 1 ? 3 : 4;
+}
 
 template <int NT>
 struct Smem {
     static constexpr int kRows = 8 * NT;
-    static constexpr int kBars = kStages * kStageBytes;
-    static constexpr int kItems = kBars + 128;
+    static constexpr int kBars = warps<NT>() * slots<NT>() * kTile;
+    static constexpr int kItems = kBars + 256;
     static constexpr int kParts = kItems + kMeta * 16;
-    static constexpr int kWo = kParts + kMeta * 16;                          // [kWarps][8][kStride]
-    static constexpr int kStat = kWo + kWarps * 8 * kStride * 4;             // m, l, mo [kWarps][kRows]
-    static constexpr int kBytes = kStat + 3 * kWarps * kRows * 4 + 1024;     // + alignment
+    static constexpr int kWo = kParts + kMeta * 16;                               // [2][8][kStride]
+    static constexpr int kStat = kWo + 2 * 8 * kStride * 4;                       // m, l, mo [warps][kRows]
+    static constexpr int kBytes = kStat + 3 * warps<NT>() * kRows * 4 + 1024;     // + alignment
 };
 
 // One partial state in the workspace: O [kRows][128], then m, l, mo [kRows].
@@ -120,7 +129,7 @@ __device__ __forceinline__ int request_len(const PagedAttnParams &p, int b, bool
 }
 
 // Items of a pair.
-__device__ __noinline__ int pair_items(const PagedAttnParams &p, int pair, bool *bad)
+__device__ __forceinline__ int pair_items(const PagedAttnParams &p, int pair, bool *bad)
 {
     if (p.blk_idx == nullptr)
         return (request_len(p, pair / p.H_kv, bad) + kBlk - 1) / kBlk;
@@ -237,38 +246,54 @@ struct State {
     }
 };
 
-// One warp over a tile, `rows` (1..64) of its tokens valid.
-template <int NT>
-__device__ __forceinline__ void attend(State<NT> &st, const Query<NT> &q, uint32_t tile, float ks_scale, float log2_vs,
-                                       int rows, int lane)
+// One warp over a tile, `rows` (1..64) of its tokens valid.  The keys are at `tile`; values()
+// releases them and gives the place of the values, once those are there (0: they never came).
+template <int NT, typename Values>
+__device__ __forceinline__ bool attend(State<NT> &st, const Query<NT> &q, uint32_t tile, Values values, float ks_scale,
+                                       float log2_vs, int rows, int lane)
 {
     const int g8 = lane >> 2, t4 = lane & 3;
-    // scores: m-tile mt holds tokens 16 mt + g8 and + 8 (elements 0/1 and 2/3)
-    float s[4][NT][4];
-    const uint32_t k0 = tile + g8 * kD;
+    // scores: m-tile mt holds tokens 16 mt + g8 and + 8 (elements 0/1 and 2/3).  One m-tile a
+    // pass, in a loop that stays a loop: its code and the values' take half the instruction
+    // cache's first level, unrolled they would be three times as long.
+    float s[4][NT][4] = {};
     const uint32_t c0 = static_cast<uint32_t>((2 * t4) ^ g8) << 4, c1 = static_cast<uint32_t>((2 * t4 + 1) ^ g8) << 4;
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
+    uint32_t k0 = tile + g8 * kD;
+#pragma unroll 1
+    for (int pass = 0; pass < 4; ++pass, k0 += 16 * kD) {
         // 16-byte chunks 2 t4 and 2 t4 + 1: dims 32 t4 .. 32 t4 + 31
         uint32_t ka[8], kb[8];
-        *reinterpret_cast<uint4 *>(ka) = lds_v4(k0 + mt * 16 * kD + c0);
-        *reinterpret_cast<uint4 *>(ka + 4) = lds_v4(k0 + mt * 16 * kD + c1);
-        *reinterpret_cast<uint4 *>(kb) = lds_v4(k0 + mt * 16 * kD + 8 * kD + c0);
-        *reinterpret_cast<uint4 *>(kb + 4) = lds_v4(k0 + mt * 16 * kD + 8 * kD + c1);
+        float half[NT][4];   // the odd k-steps' sums: two chains of products, each half as long
+        *reinterpret_cast<uint4 *>(ka) = lds_v4(k0 + c0);
+        *reinterpret_cast<uint4 *>(ka + 4) = lds_v4(k0 + c1);
+        *reinterpret_cast<uint4 *>(kb) = lds_v4(k0 + 8 * kD + c0);
+        *reinterpret_cast<uint4 *>(kb + 4) = lds_v4(k0 + 8 * kD + c1);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                s[mt][nt][i] = 0.f;
+            for (int i = 0; i < 4; ++i) {
+                s[0][nt][i] = s[1][nt][i];
+                s[1][nt][i] = s[2][nt][i];
+                s[2][nt][i] = s[3][nt][i];
+                s[3][nt][i] = half[nt][i] = 0.f;
+            }
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
             const uint32_t a[4] = {f8x2_to_f16x2(ka[ks]), f8x2_to_f16x2(kb[ks]), f8x2_to_f16x2(ka[ks] >> 16),
                                    f8x2_to_f16x2(kb[ks] >> 16)};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-                mma_f16(s[mt][nt], a, q.b[nt][ks][0], q.b[nt][ks][1]);
+                mma_f16(ks & 1 ? half[nt] : s[3][nt], a, q.b[nt][ks][0], q.b[nt][ks][1]);
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                s[3][nt][i] += half[nt][i];
     }
+    const uint32_t vtile = values();
+    if (vtile == 0u)
+        return false;
     uint32_t pb[4][NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -324,20 +349,21 @@ __device__ __forceinline__ void attend(State<NT> &st, const Query<NT> &q, uint32
             pb[mt][nt][1] = movmatrix_trans(pack_f16x2(s[mt][nt][2], s[mt][nt][3]));
         }
     }
-    // values, 16 tokens a step: tokens 2 t4, 2 t4 + 1, + 8, + 9, chunk g8 (dims 16 g8 ..+15)
-    const uint32_t v0 = tile + kTile + 2 * t4 * kD;
+    // values, 16 tokens a pass: tokens 2 t4, 2 t4 + 1, + 8, + 9, chunk g8 (dims 16 g8 ..+15)
+    uint32_t v0 = vtile + 2 * t4 * kD;
     const uint32_t d0 = static_cast<uint32_t>(g8 ^ (2 * t4)) << 4, d1 = static_cast<uint32_t>(g8 ^ (2 * t4 + 1)) << 4;
-#pragma unroll
-    for (int kt = 0; kt < 4; ++kt) {
+    int tok = 2 * t4;
+#pragma unroll 1
+    for (int pass = 0; pass < 4; ++pass, v0 += 16 * kD, tok += 16) {
         uint32_t v[4][4];
-        *reinterpret_cast<uint4 *>(v[0]) = lds_v4(v0 + kt * 16 * kD + d0);
-        *reinterpret_cast<uint4 *>(v[1]) = lds_v4(v0 + kt * 16 * kD + kD + d1);
-        *reinterpret_cast<uint4 *>(v[2]) = lds_v4(v0 + kt * 16 * kD + 8 * kD + d0);
-        *reinterpret_cast<uint4 *>(v[3]) = lds_v4(v0 + kt * 16 * kD + 9 * kD + d1);
+        *reinterpret_cast<uint4 *>(v[0]) = lds_v4(v0 + d0);
+        *reinterpret_cast<uint4 *>(v[1]) = lds_v4(v0 + kD + d1);
+        *reinterpret_cast<uint4 *>(v[2]) = lds_v4(v0 + 8 * kD + d0);
+        *reinterpret_cast<uint4 *>(v[3]) = lds_v4(v0 + 9 * kD + d1);
         if (rows < kBlk) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (16 * kt + 2 * t4 + (i & 1) + (i >> 1) * 8 >= rows)
+                if (tok + (i & 1) + (i >> 1) * 8 >= rows)
                     v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0u;
         }
 #pragma unroll
@@ -351,10 +377,19 @@ __device__ __forceinline__ void attend(State<NT> &st, const Query<NT> &q, uint32
                                        f8x2_to_f16x2(cd >> 16)};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
-                    mma_f16(st.acc[2 * wi + x][nt], a, pb[kt][nt][0], pb[kt][nt][1]);
+                    mma_f16(st.acc[2 * wi + x][nt], a, pb[0][nt][0], pb[0][nt][1]);
             }
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                pb[0][nt][i] = pb[1][nt][i];
+                pb[1][nt][i] = pb[2][nt][i];
+                pb[2][nt][i] = pb[3][nt][i];
+            }
     }
+    return true;
 }
 
 // Four adjacent output dims of one row, from its unnormalised O (units of 2^mo), m, l.
@@ -406,6 +441,8 @@ __device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const Stat
 {
     constexpr int ROWS = 8 * NT;
     constexpr int PART = part_floats<NT>();
+    constexpr int kWarps = warps<NT>();
+    constexpr int kQuads = (8 + kWarps - 1) / kWarps;   // quads (four dims of a row) a thread sums
     using S = Smem<NT>;
     const int tid = warp * 32 + lane;
     float *wo = reinterpret_cast<float *>(base + S::kWo);
@@ -417,58 +454,88 @@ __device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const Stat
     float *part = p.parts + static_cast<size_t>(part_slot(c, c0)) * PART;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+        // every warp's statistics, and the O of the warps from 2, then of warps 0 and 1; warp w
+        // sums rows w, w + kWarps, ...
         if (nt > 0 && !meet(bar, meetings++ & 1))   // wo is free again
             return false;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int row = 2 * t4 + h;
             float l = st.l[nt][h];
             l += __shfl_xor_sync(0xffffffffu, l, 4);
             l += __shfl_xor_sync(0xffffffffu, l, 8);
             l += __shfl_xor_sync(0xffffffffu, l, 16);
             if (g8 == 0) {
-                wm[warp * ROWS + nt * 8 + row] = st.m[nt][h];
-                wl[warp * ROWS + nt * 8 + row] = l;
-                wmo[warp * ROWS + nt * 8 + row] = st.mo[nt][h];
+                const int at = warp * ROWS + nt * 8 + 2 * t4 + h;
+                wm[at] = st.m[nt][h];
+                wl[at] = l;
+                wmo[at] = st.mo[nt][h];
             }
-            float *dst = wo + (warp * 8 + row) * kStride + 16 * g8;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<float4 *>(dst + 4 * i) =
-                    make_float4(st.acc[2 * i][nt][h], st.acc[2 * i][nt][h + 2], st.acc[2 * i + 1][nt][h],
-                                st.acc[2 * i + 1][nt][h + 2]);
         }
-        if (!meet(bar, meetings++ & 1))
-            return false;
-#pragma unroll 1
-        for (int e = tid; e < min(8, p.G - nt * 8) * (kD / 4); e += kWarps * 32) {
-            const int r8 = e / (kD / 4), row = nt * 8 + r8, d = 4 * (e % (kD / 4));
-            float m = -INFINITY, mo = -INFINITY, l = 0.f;
+        float4 o[kQuads];
+        float m[kQuads], mo[kQuads];
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                m = fmaxf(m, wm[w * ROWS + row]);
-                mo = fmaxf(mo, wmo[w * ROWS + row]);
+        for (int half = 1; half >= 0; --half) {
+            if (half == 0 && !meet(bar, meetings++ & 1))   // wo is free again
+                return false;
+            if (warp >> 1 == half) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float *dst = wo + ((warp & 1) * 8 + 2 * t4 + h) * kStride + 16 * g8;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<float4 *>(dst + 4 * i) =
+                            make_float4(st.acc[2 * i][nt][h], st.acc[2 * i][nt][h + 2], st.acc[2 * i + 1][nt][h],
+                                        st.acc[2 * i + 1][nt][h + 2]);
+                }
             }
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (!meet(bar, meetings++ & 1))
+                return false;
+#pragma unroll
+            for (int x = 0; x < kQuads; ++x) {
+                const int r8 = min(warp + kWarps * x, 7), row = nt * 8 + r8;
+                if (half == 1) {
+                    o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    m[x] = wm[row];
+                    mo[x] = wmo[row];
+#pragma unroll
+                    for (int w = 1; w < kWarps; ++w) {
+                        m[x] = fmaxf(m[x], wm[w * ROWS + row]);
+                        mo[x] = fmaxf(mo[x], wmo[w * ROWS + row]);
+                    }
+                }
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    if (2 * half + w >= kWarps)
+                        break;
+                    const float mw = wmo[(2 * half + w) * ROWS + row];
+                    const float f = mw == -INFINITY ? 0.f : ex2_approx(mw - mo[x]);
+                    const float4 v = *reinterpret_cast<const float4 *>(wo + (w * 8 + r8) * kStride + 4 * lane);
+                    o[x].x = fmaf(f, v.x, o[x].x);
+                    o[x].y = fmaf(f, v.y, o[x].y);
+                    o[x].z = fmaf(f, v.z, o[x].z);
+                    o[x].w = fmaf(f, v.w, o[x].w);
+                }
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < kQuads; ++x) {
+            const int row = nt * 8 + warp + kWarps * x;
+            if (warp + kWarps * x >= 8 || row >= p.G)
+                continue;
+            float l = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float lw = wl[w * ROWS + row];
-                l += lw == 0.f ? 0.f : lw * ex2_approx(wm[w * ROWS + row] - m);
-                const float f = wmo[w * ROWS + row] == -INFINITY ? 0.f : ex2_approx(wmo[w * ROWS + row] - mo);
-                const float4 x = *reinterpret_cast<const float4 *>(wo + (w * 8 + r8) * kStride + d);
-                o.x = fmaf(f, x.x, o.x);
-                o.y = fmaf(f, x.y, o.y);
-                o.z = fmaf(f, x.z, o.z);
-                o.w = fmaf(f, x.w, o.w);
+                l += lw == 0.f ? 0.f : lw * ex2_approx(wm[w * ROWS + row] - m[x]);
             }
             if (whole) {
-                write_out(p, of.pair, row, d, o, m, l, mo);
+                write_out(p, of.pair, row, 4 * lane, o[x], m[x], l, mo[x]);
             } else {
-                *reinterpret_cast<float4 *>(part + row * kD + d) = o;
-                if (d == 0) {
-                    part[ROWS * kD + row] = m;
+                *reinterpret_cast<float4 *>(part + row * kD + 4 * lane) = o[x];
+                if (lane == 0) {
+                    part[ROWS * kD + row] = m[x];
                     part[ROWS * kD + ROWS + row] = l;
-                    part[ROWS * kD + 2 * ROWS + row] = mo;
+                    part[ROWS * kD + 2 * ROWS + row] = mo[x];
                 }
             }
         }
@@ -509,6 +576,22 @@ __device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const Stat
         auto slot = [&](int j) {
             return p.parts + static_cast<size_t>(part_slot(j == 0 ? first : step == 1 ? first + j : (g0 + j) * kGroup, c0)) * PART;
         };
+        // a thread sums kPer quads (a quad's place in a state is its number);
+        // kStep states' quads are on their way at a time, the first ones already now
+        constexpr int kPer = 2, kStep = 8;
+        const int quads = p.G * (kD / 4);
+        float4 x[kStep][kPer];
+        auto fetch = [&](int e0, int j0) {
+#pragma unroll
+            for (int u = 0; u < kStep; ++u) {
+                const float4 *src = reinterpret_cast<const float4 *>(slot(j0 + u));
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    x[u][i] = j0 + u < n && e0 + i * kWarps * 32 < quads ? __ldcg(src + e0 + i * kWarps * 32)
+                                                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        };
+        fetch(tid, 0);
 #pragma unroll 1
         for (int e = tid; e < n * ROWS; e += kWarps * 32) {
             const float *src = slot(e / ROWS) + ROWS * kD + e % ROWS;
@@ -547,9 +630,6 @@ __device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const Stat
         if (!meet(bar, meetings++ & 1))
             return false;
         float *dst = slot(0);
-        const int quads = p.G * (kD / 4);   // four dims of a row each
-        // kPer quads of kStep states a thread in flight
-        constexpr int kPer = 3, kStep = 8;
 #pragma unroll 1
         for (int e0 = tid; e0 < quads; e0 += kPer * kWarps * 32) {
             float4 o[kPer];
@@ -558,16 +638,8 @@ __device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const Stat
                 o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
             for (int j0 = 0; j0 < n; j0 += kStep) {
-                float4 x[kStep][kPer];
-#pragma unroll
-                for (int u = 0; u < kStep; ++u) {
-                    // a quad's place in a state is its number
-                    const float4 *src = reinterpret_cast<const float4 *>(slot(j0 + u));
-#pragma unroll
-                    for (int i = 0; i < kPer; ++i)
-                        x[u][i] = j0 + u < n && e0 + i * kWarps * 32 < quads ? __ldcg(src + e0 + i * kWarps * 32)
-                                                                             : make_float4(0.f, 0.f, 0.f, 0.f);
-                }
+                if (e0 != tid || j0 != 0)
+                    fetch(e0, j0);
 #pragma unroll
                 for (int u = 0; u < kStep; ++u)
 #pragma unroll
@@ -616,30 +688,36 @@ __device__ __forceinline__ void give_up(const PagedAttnParams &p, int lane)
 }
 
 template <int NT>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+__global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
     paged_attn_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ PagedAttnParams p)
 {
     constexpr int ROWS = 8 * NT;
+    constexpr int kWarps = warps<NT>(), kSlots = slots<NT>(), kThreads = (kWarps + 1) * 32;
     using S = Smem<NT>;
-    static_assert((3 * kDirect + 3) * ROWS <= kWarps * 8 * kStride, "the merge's weights fit the warps' states");
+    static_assert((3 * kDirect + 3) * ROWS <= 2 * 8 * kStride, "the merge's weights fit the warps' states");
     extern __shared__ uint8_t smem_raw[];
     __shared__ int s_sum[kWarps + 1], s_pair, s_n, s_start, s_last;
     const uint32_t base_s = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *base = smem_raw + (base_s - smem_u32(smem_raw));
     Item *items = reinterpret_cast<Item *>(base + S::kItems);
     Part *parts = reinterpret_cast<Part *>(base + S::kParts);
-    const uint32_t full = base_s + S::kBars, empty = full + 8 * kStages, bar = empty + 8 * kStages;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // fill barriers [warp][slot], release barriers [warp][slot], and the consumers' meetings
+    const uint32_t full = base_s + S::kBars, empty = full + 8 * kWarps * kSlots, bar = empty + 8 * kWarps * kSlots;
+    const int tid = threadIdx.x, lane = tid & 31;
+    // roles: 0 .. kWarps - 1 consumers, kWarps the producer.  Four warps lie one on each of the
+    // SM's partitions: the second half of the grid turns them, so that an SM's two producers
+    // share a partition with a consumer each.
+    const int warp = kWarps == 3 && 2 * blockIdx.x >= gridDim.x ? (tid / 32 + 2) % 4 : tid / 32;
 
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < kWarps * kSlots; ++i) {
             mbar_init(full + 8 * i, 2);          // the load's expect_tx, and the item record
-            mbar_init(empty + 8 * i, 1);         // the warp that took the tile
+            mbar_init(empty + 8 * i, 1);         // the warp is done with it
         }
         mbar_init(bar, kWarps);
         fence_barrier_init();
     }
-    if (tid == kWarps * 32)
+    if (warp == kWarps && lane == 0)
         prefetch_tensormap(&map);
     griddep_wait();
     griddep_launch_dependents();
@@ -653,6 +731,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     const int u0 = min(units, tid * per), u1 = min(units, u0 + per);
     bool bad = false;
     int mine = 0;
+#pragma unroll 1
     for (int u = u0; u < u1; ++u)
         mine += pair_length(pair_items(p, u * heads, &bad)) * heads;
     if (bad && blockIdx.x == 0)
@@ -665,12 +744,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             incl += v;
     }
     if (lane == 31)
-        s_sum[warp] = incl;
+        s_sum[tid / 32] = incl;
     __syncthreads();
     int N = 0;
 #pragma unroll
     for (int w = 0; w <= kWarps; ++w) {
-        if (w < warp)
+        if (w < tid / 32)
             incl += s_sum[w];
         N += s_sum[w];
     }
@@ -680,6 +759,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if (lo < hi && incl - mine <= lo && lo < incl) {
         // the pair that holds `lo`
         int at = incl - mine, u = u0, n = 0;
+#pragma unroll 1
         for (; u < u1; ++u) {
             n = pair_items(p, u * heads, &bad);
             if (at + pair_length(n) * heads > lo)
@@ -702,6 +782,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         const uint64_t pol = policy_evict_first();
         int it = 0, part = 0;          // the CTA's next item and part
         bool stop = false, wrong = false;
+        auto free_slot = [&](int slot, int fill) {
+            return fill < kSlots || mbar_wait(empty + 8 * slot, (fill / kSlots - 1) & 1, kWaitNs);
+        };
+        auto load = [&](int slot, int tile, int rows) {
+            if (rows > 0) {
+                mbar_arrive_expect_tx(full + 8 * slot, kTile);
+                tma_load_3d(base_s + slot * kTile, &map, full + 8 * slot, 0, 0, tile, pol);
+            } else {
+                mbar_arrive(full + 8 * slot);
+            }
+        };
         // first the pair that holds `lo`, then 32 pairs at a time, one a lane: their counts
         // are loaded a step ahead
         int pair = s_pair, n = lane == 0 ? s_n : 0;
@@ -736,6 +827,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             const int my_part = part + __popc(has & ((1u << lane) - 1));
             if (cnt > 0)
                 parts[my_part % kMeta] = Part{first, n, pair + lane, 0};
+#pragma unroll 1
             for (int done = 0; done < total && !stop; done += 32) {
                 // lane j resolves item done + j: of the first pair whose count reaches past it
                 const int take = min(32, total - done);
@@ -769,40 +861,38 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                         }
                     }
                 }
-                // the ring is empty at first: those loads go out before the scales are here
-                const int ahead = it == 0 ? min(take, kStages) : 0;
+                // the slots are empty at first: the first items' keys go out before the scales are here
+                const int ahead = it == 0 ? min(take, kWarps) : 0;
+#pragma unroll 1
                 for (int j = 0; j < ahead; ++j) {
                     const int u = __shfl_sync(0xffffffffu, unit, j), rows = __shfl_sync(0xffffffffu, item.rows, j);
-                    if (lane == 0) {
-                        if (rows > 0) {
-                            mbar_arrive_expect_tx(full + 8 * j, kStageBytes);
-                            tma_load_3d(base_s + j * kStageBytes, &map, full + 8 * j, 0, 0, 2 * u, pol);
-                        } else {
-                            mbar_arrive(full + 8 * j);
-                        }
-                    }
+                    if (lane == 0)
+                        load(j * kSlots, 2 * u, rows);
                 }
                 item.ks = sc.x;
-                item.log2_vs = log2f(sc.y);
+                item.log2_vs = __log2f(sc.y);
                 if (lane < take)
                     items[(it + lane) % kMeta] = item;
                 __syncwarp();
+#pragma unroll 1
                 for (int j = 0; j < take && !stop; ++j) {
                     const int u = __shfl_sync(0xffffffffu, unit, j), rows = __shfl_sync(0xffffffffu, item.rows, j);
-                    const int stage = (it + j) % kStages, use = (it + j) / kStages;
                     if (lane == 0) {
+                        const int ring = (it + j) % kWarps * kSlots, fill = (it + j) / kWarps * 2;
+                        const int k_slot = ring + fill % kSlots, v_slot = ring + (fill + 1) % kSlots;
                         if (j >= ahead) {
-                            if (use > 0 && !mbar_wait(empty + 8 * stage, (use - 1) & 1, kWaitNs)) {
-                                stop = true;
-                            } else if (rows > 0) {
-                                mbar_arrive_expect_tx(full + 8 * stage, kStageBytes);
-                                tma_load_3d(base_s + stage * kStageBytes, &map, full + 8 * stage, 0, 0, 2 * u, pol);
-                            } else {
-                                mbar_arrive(full + 8 * stage);
-                            }
+                            stop = !free_slot(k_slot, fill);
+                            if (!stop)
+                                load(k_slot, 2 * u, rows);
                         }
-                        if (!stop)
-                            mbar_arrive(full + 8 * stage);   // the item record
+                        if (!stop) {
+                            mbar_arrive(full + 8 * k_slot);   // the item record
+                            stop = !free_slot(v_slot, fill + 1);
+                        }
+                        if (!stop) {
+                            load(v_slot, 2 * u + 1, rows);
+                            mbar_arrive(full + 8 * v_slot);
+                        }
                     }
                     stop = __shfl_sync(0xffffffffu, stop ? 1 : 0, 0) != 0;
                 }
@@ -815,15 +905,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             n = n_next;
         }
         // each consumer warp gets an item that ends it
+#pragma unroll 1
         for (int j = 0; j < kWarps && lane == 0 && !stop; ++j, ++it) {
-            const int stage = it % kStages, use = it / kStages;
-            if (use > 0 && !mbar_wait(empty + 8 * stage, (use - 1) & 1, kWaitNs)) {
+            const int fill = it / kWarps * 2, slot = it % kWarps * kSlots + fill % kSlots;
+            if (!free_slot(slot, fill)) {
                 stop = true;
                 break;
             }
             items[it % kMeta] = Item{1.f, 0.f, 0, part + kEnd};
-            mbar_arrive(full + 8 * stage);
-            mbar_arrive(full + 8 * stage);
+            mbar_arrive(full + 8 * slot);
+            mbar_arrive(full + 8 * slot);
         }
         if (__any_sync(0xffffffffu, wrong) && lane == 0)
             report(p.status, SPARSE_ERR_BAD_INDEX);
@@ -834,8 +925,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
     // ---------------------------------------------------------------- consumers
     // rows of pairs without items, shared out over the CTAs
+#pragma unroll 1
     for (int pair = c + static_cast<int>(gridDim.x) * warp; pair < pairs; pair += static_cast<int>(gridDim.x) * kWarps)
         if (pair_items(p, pair, &bad) == 0)
+#pragma unroll 1
             for (int row = 0; row < p.G; ++row)
                 write_out(p, pair, row, 4 * lane, make_float4(0.f, 0.f, 0.f, 0.f), 0.f, 0.f, 0.f);
     if (idle)
@@ -850,17 +943,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     int part = 0, q_part = -1, meetings = 0;
     bool warm = true;
 #pragma unroll 1
-    for (int it = warp;;) {
-        const int stage = it % kStages;
+    for (int it = warp, fill = 0;;) {
+        const int k_slot = warp * kSlots + fill % kSlots, v_slot = warp * kSlots + (fill + 1) % kSlots;
         Item item{1.f, 0.f, kBlk, 0};
         if (!warm) {
-            if (!__all_sync(0xffffffffu, mbar_wait(full + 8 * stage, (it / kStages) & 1, kWaitNs))) {
+            if (!__all_sync(0xffffffffu, mbar_wait(full + 8 * k_slot, (fill / kSlots) & 1, kWaitNs))) {
                 give_up(p, lane);
                 return;
             }
             item = items[it % kMeta];
             const int next = item.part & ~kEnd;
             // the parts before the item's are complete once every warp has come this far
+#pragma unroll 1
             for (; part < next; ++part) {
                 const Part of = parts[part % kMeta];
                 bool ok = finish_part<NT>(p, st, of, c, lo, hi, len, base, bar, meetings, &s_last, warp, lane);
@@ -878,17 +972,31 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             q_part = part;
             q.load(p, warm ? s_pair : parts[part % kMeta].pair, lane);
         }
-        if (item.rows > 0)
-            attend<NT>(st, q, base_s + stage * kStageBytes, item.ks, item.log2_vs, item.rows, lane);
+        auto values = [&]() -> uint32_t {
+            if (warm)
+                return base_s + v_slot * kTile;
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(empty + 8 * k_slot);
+            const bool there = __all_sync(0xffffffffu, mbar_wait(full + 8 * v_slot, ((fill + 1) / kSlots) & 1, kWaitNs));
+            return there ? base_s + v_slot * kTile : 0u;
+        };
+        const bool ok = item.rows > 0 ? attend<NT>(st, q, base_s + k_slot * kTile, values, item.ks, item.log2_vs, item.rows, lane)
+                                      : values() != 0u;
+        if (!ok) {
+            give_up(p, lane);
+            return;
+        }
         if (warm) {
             warm = false;
             st.reset();
             continue;
         }
-        it += kWarps;
         __syncwarp();
         if (lane == 0)
-            mbar_arrive(empty + 8 * stage);
+            mbar_arrive(empty + 8 * v_slot);
+        it += kWarps;
+        fill += 2;
     }
 }
 
@@ -920,7 +1028,8 @@ int launch(const PagedAttnParams &p, const CUtensorMap &map, const sp_host::Devi
     if (rc != SPARSE_OK)
         return rc;
     return sp_host::cuda_status(
-        launch_pdl(kern, dim3(static_cast<unsigned>(kCtasPerSm * dev.sm_count)), kThreads, Smem<NT>::kBytes, stream, map, p),
+        launch_pdl(kern, dim3(static_cast<unsigned>(kCtasPerSm * dev.sm_count)), (warps<NT>() + 1) * 32, Smem<NT>::kBytes, stream,
+                   map, p),
         name);
 }
 
