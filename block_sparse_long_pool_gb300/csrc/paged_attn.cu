@@ -35,12 +35,9 @@ constexpr int kStride = kD + 4;                   // floats a row of the warps' 
 constexpr int kMeta = 64;                         // item and part records: 32 being written + the ring's
 constexpr float kWeightBits = 12.f;               // weights reach 2^12: f16 holds them down to 2^-24
 constexpr uint64_t kWaitNs = 2000000000ull;
-#ifndef MINI
-#define MINI 6
-#define PCOST 4
-#endif
-constexpr int kMinItems = MINI;                   // a CTA's range at least
-constexpr int kPairCost = PCOST;                  // what a pair costs beside its items, in items
+constexpr int kMinItems = 6;                      // a CTA's range at least
+constexpr int kPairCost = 7;                      // what a pair costs beside its items, in items
+constexpr int kWhole = 12;                        // pairs of up to so many items stay with one CTA
 constexpr int kDirect = 32;                       // partial states that are merged in one go
 constexpr int kGroup = 16;                        // CTAs whose states are merged first where there are more
 
@@ -63,8 +60,9 @@ struct Part {
 };
 static_assert(sizeof(Part) == 16, "one 16-byte load");
 
-// Consumer warps of a CTA: 4, or 3 for more than 8 rows, whose states need more registers than
-// five warps of two CTAs an SM can have.
+// Consumer warps of a CTA: 4, or 3 for more than 8 rows.  Five warps of two CTAs an SM have 168
+// registers a thread, and what does not fit goes to an L1 of few KB beside this much shared
+// memory: 16 rows' state and queries spill there, and their tiles take 1.5 times as long.
 template <int NT>
 constexpr int warps()
 {
@@ -144,6 +142,17 @@ __device__ __forceinline__ int pair_length(int n)
     return n > 0 ? n + kPairCost : 0;
 }
 
+// The items [x, x + y) of a pair of n items, which start at place `first`, that belong to the
+// CTA with the range [lo, hi): those that lie in it, or all of a short pair that starts in it
+// (to merge the states of two CTAs takes longer than to attend over a few tiles more).
+__device__ __forceinline__ int2 pair_share(int first, int n, int lo, int hi)
+{
+    if (n <= kWhole)
+        return make_int2(0, lo <= first && first < hi ? n : 0);
+    const int a = max(0, min(n, lo - first));
+    return make_int2(a, max(0, min(n, hi - first) - a));
+}
+
 // Workspace slot of CTA c's state of a pair whose items begin in CTA c0: a CTA has at most
 // one pair that began before it, and one that goes on after it.
 __device__ __forceinline__ int part_slot(int c, int c0)
@@ -166,85 +175,183 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// The pair's queries as mma B fragments (row g8 of each n-tile, dims 32 t4 + 4 ks ..+3 for
-// k-step ks), scaled by a power of two to just below f16's largest value (negated where the
-// softmax scale is negative), and what undoes it, times the softmax scale, for the rows
-// 2 t4 + {0, 1} whose scores this lane holds.
+// A lane's part of a query row: dims 32 t4 + 4 ks .. + 3 for k-step ks, scaled by a power of two
+// to just below f16's largest value (negated where the softmax scale is negative); returns
+// what undoes that, times the softmax scale.
+__device__ __forceinline__ float load_row(uint32_t (&b)[8][2], const PagedAttnParams &p, int pair, int row, int lane)
+{
+    uint4 x[4] = {};
+    if (row < p.G) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.Q + (static_cast<size_t>(pair) * p.G + row) * kD + 32 * (lane & 3));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            x[i] = src[i];
+    }
+    float f[32], amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+            f[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        amax = fmaxf(amax, fabsf(f[i]));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    // the exponent of the row's largest value becomes 14
+    const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
+    const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23), p.scale_log2);
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) {
+        b[ks][0] = pack_f16x2(f[4 * ks] * up, f[4 * ks + 1] * up);
+        b[ks][1] = pack_f16x2(f[4 * ks + 2] * up, f[4 * ks + 3] * up);
+    }
+    return __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23) * fabsf(p.scale_log2);
+}
+
+// Up to 8 rows: S^T = K Q^T (tokens on M, the rows on N), then O^T += V^T P^T.  A lane holds the
+// scores of rows 2 t4 + {0, 1}.
+// 9 to 16 rows: S = Q K^T (the rows on M, tokens on N), then O += P V.  A lane holds the scores of
+// rows g8 and g8 + 8; a row's tokens are spread over 4 lanes instead of 8, and the weights
+// are O's A operand as they are, without a transposition.
 template <int NT>
-struct Query {
-    uint32_t b[NT][8][2];
-    float mul[NT][2];
+struct Query;
+
+template <>
+struct Query<1> {
+    uint32_t b[8][2];   // the B operand: row g8
+    float mul[2];       // of the rows whose scores this lane holds
 
     __device__ __forceinline__ void load(const PagedAttnParams &p, int pair, int lane)
     {
-        const int g8 = lane >> 2, t4 = lane & 3;
-        const int bb = pair / p.H_kv, g = pair % p.H_kv;
+        const float down = load_row(b, p, pair, lane >> 2, lane);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int row = nt * 8 + g8;
-            uint4 x[4] = {};
-            if (row < p.G) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(
-                    p.Q + (static_cast<size_t>(bb) * p.H_q + static_cast<size_t>(g) * p.G + row) * kD + 32 * t4);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    x[i] = src[i];
-            }
-            float f[32], amax = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    f[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-                    f[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                amax = fmaxf(amax, fabsf(f[i]));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            // the exponent of the row's largest value becomes 14
-            const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
-            const float up = copysignf(__uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23), p.scale_log2);
-            const float down = __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23) * fabsf(p.scale_log2);
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-                b[nt][ks][0] = pack_f16x2(f[4 * ks] * up, f[4 * ks + 1] * up);
-                b[nt][ks][1] = pack_f16x2(f[4 * ks + 2] * up, f[4 * ks + 3] * up);
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                mul[nt][h] = __shfl_sync(0xffffffffu, down, (2 * t4 + h) * 4);
-        }
+        for (int h = 0; h < 2; ++h)
+            mul[h] = __shfl_sync(0xffffffffu, down, (2 * (lane & 3) + h) * 4);
     }
 };
 
-// A warp's online-softmax state: rows 2 t4 + {0, 1} of every n-tile.  acc[mt][nt] holds dims
-// 16 g8 + 2 mt + {0, 1} (elements 0/1 and 2/3) of those rows, in units of 2^mo.
+template <>
+struct Query<2> {
+    uint32_t a[2][8][2];   // the A operand: rows g8 and g8 + 8
+    float mul[2];
+
+    __device__ __forceinline__ void load(const PagedAttnParams &p, int pair, int lane)
+    {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            mul[h] = load_row(a[h], p, pair, 8 * h + (lane >> 2), lane);
+    }
+};
+
+// A warp's online-softmax state of the two rows h whose scores the lane holds, and its part of
+// O in units of 2^mo.  NT = 1: acc[mt] has dims 16 g8 + 2 mt + {0, 1} (elements 0/1 and 2/3) of
+// the rows.  NT = 2: acc[j] has dims 32 t4 + j and 32 t4 + 16 + j of row 0 (elements 0, 1) and
+// of row 1 (2, 3).
 template <int NT>
 struct State {
-    float m[NT][2], mo[NT][2], l[NT][2], acc[8][NT][4];
+    float m[2], mo[2], l[2], acc[8 * NT][4];
 
     __device__ __forceinline__ void reset()
     {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int h = 0; h < 2; ++h) {
+            m[h] = mo[h] = -INFINITY;
+            l[h] = 0.f;
+        }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                m[nt][h] = mo[nt][h] = -INFINITY;
-                l[nt][h] = 0.f;
+        for (int j = 0; j < 8 * NT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[j][i] = 0.f;
+    }
+
+    // rows 8 group .. + 7: the maxima and sums, to [8] floats each
+    __device__ __forceinline__ void put_stats(float *to_m, float *to_l, float *to_mo, int group, int lane) const
+    {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (NT == 2 && h != group)
+                continue;
+            float sum = l[h];
+            if (NT == 1) {
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1)
+                    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            } else {
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
             }
+            if (NT == 1 ? lane < 4 : (lane & 3) == 0) {
+                const int row = NT == 1 ? 2 * lane + h : lane >> 2;
+                to_m[row] = m[h];
+                to_l[row] = sum;
+                to_mo[row] = mo[h];
+            }
+        }
+    }
+
+    // and their O, to [8][kStride]
+    __device__ __forceinline__ void put_o(float *to, int group, int lane) const
+    {
+        const int g8 = lane >> 2, t4 = lane & 3;
 #pragma unroll
-        for (int mt = 0; mt < 8; ++mt)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+        for (int h = 0; h < 2; ++h) {
+            if (NT == 1) {
+                float *dst = to + (2 * t4 + h) * kStride + 16 * g8;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    acc[mt][nt][i] = 0.f;
+                    *reinterpret_cast<float4 *>(dst + 4 * i) =
+                        make_float4(acc[2 * i][h], acc[2 * i][h + 2], acc[2 * i + 1][h], acc[2 * i + 1][h + 2]);
+            } else {
+                // h: the lane's first or second 16 dims
+                float *dst = to + g8 * kStride + 32 * t4 + 16 * h;
+#pragma unroll
+                for (int i = 0; i < 4 * NT; i += NT)
+                    *reinterpret_cast<float4 *>(dst + 4 * i / NT) =
+                        make_float4(acc[2 * i][2 * group + h], acc[2 * i + 1][2 * group + h], acc[2 * i + NT][2 * group + h],
+                                    acc[2 * i + NT + 1][2 * group + h]);
+            }
+        }
     }
 };
+
+// The scores of one of the lane's rows (n of them) become weights: the row's maximum and sum go
+// on, the weights for O are left in `s` in units of 2^mo, and what O has to be scaled by is
+// returned.  `lanes`: the xor distances of the lanes that share the row.
+template <int N>
+__device__ __forceinline__ float weigh(float (&s)[N], float mul, float log2_vs, float &row_m, float &row_l, float &row_mo,
+                                       int first_lane, int last_lane)
+{
+    float mx = s[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i)
+        mx = fmaxf(mx, s[i]);
+#pragma unroll
+    for (int o = first_lane; o <= last_lane; o <<= 1)
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    mx *= mul;
+    const float m_new = fmaxf(row_m, mx), mo_new = fmaxf(row_mo, mx + log2_vs - kWeightBits);
+    const float m_use = m_new == -INFINITY ? 0.f : m_new, mo_use = mo_new == -INFINITY ? 0.f : mo_new;
+    float l = row_l * ex2_approx(row_m - m_use);
+    const float alpha = ex2_approx(row_mo - mo_use);
+    // from units of 2^m to 2^mo; the bound is only reached by weights below 2^-100
+    const float to_o = ex2_approx(fminf(log2_vs + (m_use - mo_use), 112.f));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float w = ex2_approx(fmaf(s[i], mul, -m_use));
+        l += w;
+        s[i] = w * to_o;
+    }
+    row_l = l;
+    row_m = m_new;
+    row_mo = mo_new;
+    return alpha;
+}
 
 // One warp over a tile, `rows` (1..64) of its tokens valid.  The keys are at `tile`; values()
 // releases them and gives the place of the values, once those are there (0: they never came).
@@ -253,14 +360,14 @@ __device__ __forceinline__ bool attend(State<NT> &st, const Query<NT> &q, uint32
                                        float log2_vs, int rows, int lane)
 {
     const int g8 = lane >> 2, t4 = lane & 3;
-    // scores: m-tile mt holds tokens 16 mt + g8 and + 8 (elements 0/1 and 2/3).  One m-tile a
-    // pass, in a loop that stays a loop: its code and the values' take half the instruction
-    // cache's first level, unrolled they would be three times as long.
-    float s[4][NT][4] = {};
+    // Scores, 16 tokens a pass.  s[x][i]: NT = 1, m-tile x: token 16 x + g8 + 8 (i >> 1), row i & 1;
+    // NT = 2, n-tile x (two a pass): token 8 x + 2 t4 + (i & 1), row i >> 1.
+    constexpr int kScores = 4 * NT;
+    float s[kScores][4];
     const uint32_t c0 = static_cast<uint32_t>((2 * t4) ^ g8) << 4, c1 = static_cast<uint32_t>((2 * t4 + 1) ^ g8) << 4;
-    uint32_t k0 = tile + g8 * kD;
-#pragma unroll 1
-    for (int pass = 0; pass < 4; ++pass, k0 += 16 * kD) {
+#pragma unroll
+    for (int pass = 0; pass < 4; ++pass) {
+        const uint32_t k0 = tile + (16 * pass + g8) * kD;
         // 16-byte chunks 2 t4 and 2 t4 + 1: dims 32 t4 .. 32 t4 + 31
         uint32_t ka[8], kb[8];
         float half[NT][4];   // the odd k-steps' sums: two chains of products, each half as long
@@ -268,93 +375,87 @@ __device__ __forceinline__ bool attend(State<NT> &st, const Query<NT> &q, uint32
         *reinterpret_cast<uint4 *>(ka + 4) = lds_v4(k0 + c1);
         *reinterpret_cast<uint4 *>(kb) = lds_v4(k0 + 8 * kD + c0);
         *reinterpret_cast<uint4 *>(kb + 4) = lds_v4(k0 + 8 * kD + c1);
+        float(&sp)[NT][4] = *reinterpret_cast<float(*)[NT][4]>(&s[pass * NT]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                s[0][nt][i] = s[1][nt][i];
-                s[1][nt][i] = s[2][nt][i];
-                s[2][nt][i] = s[3][nt][i];
-                s[3][nt][i] = half[nt][i] = 0.f;
-            }
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-            const uint32_t a[4] = {f8x2_to_f16x2(ka[ks]), f8x2_to_f16x2(kb[ks]), f8x2_to_f16x2(ka[ks] >> 16),
-                                   f8x2_to_f16x2(kb[ks] >> 16)};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                mma_f16(ks & 1 ? half[nt] : s[3][nt], a, q.b[nt][ks][0], q.b[nt][ks][1]);
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int x = 0; x < NT; ++x)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                s[3][nt][i] += half[nt][i];
+                sp[x][i] = half[x][i] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+            const uint32_t a_lo = f8x2_to_f16x2(ka[ks]), a_hi = f8x2_to_f16x2(ka[ks] >> 16), b_lo = f8x2_to_f16x2(kb[ks]),
+                           b_hi = f8x2_to_f16x2(kb[ks] >> 16);
+            if constexpr (NT == 1) {
+                const uint32_t a[4] = {a_lo, b_lo, a_hi, b_hi};
+                mma_f16(ks & 1 ? half[0] : sp[0], a, q.b[ks][0], q.b[ks][1]);
+            } else {
+                const uint32_t a[4] = {q.a[0][ks][0], q.a[1][ks][0], q.a[0][ks][1], q.a[1][ks][1]};
+                mma_f16(ks & 1 ? half[0] : sp[0], a, a_lo, a_hi);
+                mma_f16(ks & 1 ? half[NT - 1] : sp[NT - 1], a, b_lo, b_hi);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                sp[x][i] += half[x][i];
     }
     const uint32_t vtile = values();
     if (vtile == 0u)
         return false;
-    uint32_t pb[4][NT][2];
+    float mul[2] = {ks_scale * q.mul[0], ks_scale * q.mul[1]};
+    if (rows < kBlk) {
+        // the request ends in this tile: what lies behind it may be any bytes
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        float mul[2], alpha[2];
-        mul[0] = ks_scale * q.mul[nt][0];
-        mul[1] = ks_scale * q.mul[nt][1];
-        if (rows < kBlk) {
-            // the request ends in this tile: what lies behind it may be any bytes
+        for (int x = 0; x < kScores; ++x)
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    s[mt][nt][i] = 16 * mt + g8 + (i >> 1) * 8 < rows ? s[mt][nt][i] * mul[i & 1] : -INFINITY;
-            mul[0] = mul[1] = 1.f;
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float mx = fmaxf(s[0][nt][h], s[0][nt][h + 2]);
-#pragma unroll
-            for (int mt = 1; mt < 4; ++mt)
-                mx = fmaxf(mx, fmaxf(s[mt][nt][h], s[mt][nt][h + 2]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) * mul[h];
-            const float m_new = fmaxf(st.m[nt][h], mx), mo_new = fmaxf(st.mo[nt][h], mx + log2_vs - kWeightBits);
-            const float m_use = m_new == -INFINITY ? 0.f : m_new, mo_use = mo_new == -INFINITY ? 0.f : mo_new;
-            float l = st.l[nt][h] * ex2_approx(st.m[nt][h] - m_use);
-            alpha[h] = ex2_approx(st.mo[nt][h] - mo_use);
-            // from units of 2^m to 2^mo; the bound is only reached by weights below 2^-100
-            const float to_o = ex2_approx(fminf(log2_vs + (m_use - mo_use), 112.f));
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-                for (int i = h; i < 4; i += 2) {
-                    const float w = ex2_approx(fmaf(s[mt][nt][i], mul[h], -m_use));
-                    l += w;
-                    s[mt][nt][i] = w * to_o;
-                }
-            st.l[nt][h] = l;
-            st.m[nt][h] = m_new;
-            st.mo[nt][h] = mo_new;
-        }
-        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-#pragma unroll
-            for (int mt = 0; mt < 8; ++mt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    st.acc[mt][nt][i] *= alpha[i & 1];
-        }
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
-            pb[mt][nt][0] = movmatrix_trans(pack_f16x2(s[mt][nt][0], s[mt][nt][1]));
-            pb[mt][nt][1] = movmatrix_trans(pack_f16x2(s[mt][nt][2], s[mt][nt][3]));
-        }
+            for (int i = 0; i < 4; ++i) {
+                const int tok = NT == 1 ? 16 * x + g8 + 8 * (i >> 1) : 8 * x + 2 * t4 + (i & 1);
+                s[x][i] = tok < rows ? s[x][i] * mul[NT == 1 ? i & 1 : i >> 1] : -INFINITY;
+            }
+        mul[0] = mul[1] = 1.f;
     }
+    float alpha[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float w[2 * kScores];
+#pragma unroll
+        for (int x = 0; x < kScores; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+                w[2 * x + y] = s[x][NT == 1 ? h + 2 * y : 2 * h + y];
+        alpha[h] = weigh(w, mul[h], log2_vs, st.m[h], st.l[h], st.mo[h], NT == 1 ? 4 : 1, NT == 1 ? 16 : 2);
+#pragma unroll
+        for (int x = 0; x < kScores; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+                s[x][NT == 1 ? h + 2 * y : 2 * h + y] = w[2 * x + y];
+    }
+    if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+        for (int j = 0; j < 8 * NT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                st.acc[j][i] *= alpha[NT == 1 ? i & 1 : i >> 1];
+    }
+    // the weights as operand of O: 16 tokens each, tokens 2 t4, + 1, + 8, + 9 of a row
+    uint32_t pw[4][2 * NT];
+#pragma unroll
+    for (int x = 0; x < kScores; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const uint32_t h2 = pack_f16x2(s[x][2 * y], s[x][2 * y + 1]);
+            if (NT == 1)
+                pw[x][y] = movmatrix_trans(h2);
+            else
+                pw[x / NT][(x % NT) * 2 + y] = h2;
+        }
     // values, 16 tokens a pass: tokens 2 t4, 2 t4 + 1, + 8, + 9, chunk g8 (dims 16 g8 ..+15)
-    uint32_t v0 = vtile + 2 * t4 * kD;
     const uint32_t d0 = static_cast<uint32_t>(g8 ^ (2 * t4)) << 4, d1 = static_cast<uint32_t>(g8 ^ (2 * t4 + 1)) << 4;
-    int tok = 2 * t4;
-#pragma unroll 1
-    for (int pass = 0; pass < 4; ++pass, v0 += 16 * kD, tok += 16) {
+#pragma unroll
+    for (int pass = 0; pass < 4; ++pass) {
+        const uint32_t v0 = vtile + (16 * pass + 2 * t4) * kD;
+        const uint32_t *w = pw[pass];
         uint32_t v[4][4];
         *reinterpret_cast<uint4 *>(v[0]) = lds_v4(v0 + d0);
         *reinterpret_cast<uint4 *>(v[1]) = lds_v4(v0 + kD + d1);
@@ -363,7 +464,7 @@ __device__ __forceinline__ bool attend(State<NT> &st, const Query<NT> &q, uint32
         if (rows < kBlk) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (tok + (i & 1) + (i >> 1) * 8 >= rows)
+                if (16 * pass + 2 * t4 + (i & 1) + (i >> 1) * 8 >= rows)
                     v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0u;
         }
 #pragma unroll
@@ -373,21 +474,18 @@ __device__ __forceinline__ bool attend(State<NT> &st, const Query<NT> &q, uint32
                 // bytes 2x, 2x + 1 of the word: dims 4 wi + 2 x and + 1 of two tokens side by side
                 const uint32_t sel = x == 0 ? 0x5140u : 0x7362u;
                 const uint32_t ab = __byte_perm(v[0][wi], v[1][wi], sel), cd = __byte_perm(v[2][wi], v[3][wi], sel);
-                const uint32_t a[4] = {f8x2_to_f16x2(ab), f8x2_to_f16x2(ab >> 16), f8x2_to_f16x2(cd),
-                                       f8x2_to_f16x2(cd >> 16)};
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    mma_f16(st.acc[2 * wi + x][nt], a, pb[0][nt][0], pb[0][nt][1]);
+                const uint32_t ab0 = f8x2_to_f16x2(ab), ab1 = f8x2_to_f16x2(ab >> 16), cd0 = f8x2_to_f16x2(cd),
+                               cd1 = f8x2_to_f16x2(cd >> 16);
+                if constexpr (NT == 1) {
+                    const uint32_t a[4] = {ab0, ab1, cd0, cd1};
+                    mma_f16(st.acc[2 * wi + x], a, w[0], w[1]);
+                } else {
+                    const uint32_t a[4] = {w[0], w[1], w[2], w[3]};
+                    mma_f16(st.acc[(4 * wi + 2 * x) % (8 * NT)], a, ab0, cd0);
+                    mma_f16(st.acc[(4 * wi + 2 * x + 1) % (8 * NT)], a, ab1, cd1);
+                }
             }
         }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                pb[0][nt][i] = pb[1][nt][i];
-                pb[1][nt][i] = pb[2][nt][i];
-                pb[2][nt][i] = pb[3][nt][i];
-            }
     }
     return true;
 }
@@ -407,6 +505,16 @@ __device__ __forceinline__ void write_out(const PagedAttnParams &p, int pair, in
         p.lse[at] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994530942f;
 }
 
+// mbar_wait that looks at the clock only after some tries (each of which sleeps a while).
+__device__ __forceinline__ bool wait_for(uint32_t bar, int parity, uint64_t limit_ns)
+{
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+        if (mbar_try_wait(bar, parity))
+            return true;
+    return mbar_wait(bar, parity, limit_ns);
+}
+
 // The consumer warps meet at `bar` (their meetings take turns of its parity); false where one
 // of them gave up: it leaves, and so do the others.
 __device__ __noinline__ bool meet(uint32_t bar, int parity)
@@ -414,22 +522,19 @@ __device__ __noinline__ bool meet(uint32_t bar, int parity)
     __syncwarp();
     if ((threadIdx.x & 31) == 0)
         mbar_arrive(bar);
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, 2 * kWaitNs)) != 0;
+    return __all_sync(0xffffffffu, wait_for(bar, parity, 2 * kWaitNs)) != 0;
 }
 
-// One of the `expect` arrivals at a counter, for the whole CTA: true for the last, which
-// resets the counter and then sees what all wrote before theirs.
-__device__ __forceinline__ bool arrive_last(int *counter, int expect, int *flag, int tid)
+// One of `expect` arrivals at a counter, by one thread for its CTA, which has met: true for the
+// last one, which resets the counter.  The release makes visible what the CTA wrote before
+// the meeting, the acquire what the other CTAs did.
+__device__ __forceinline__ bool arrive_last(int *counter, int expect)
 {
-    if (tid == 0) {
-        __threadfence();
-        const int prev = atomicAdd(counter, 1);
-        *flag = prev == expect - 1;
-        if (prev == expect - 1)
-            *counter = 0;   // for the next call
-        __threadfence();
-    }
-    return true;
+    int prev;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(prev) : "l"(counter) : "memory");
+    if (prev == expect - 1)
+        *counter = 0;   // for the next call
+    return prev == expect - 1;
 }
 
 // The CTA's part of a pair: its warps' states merged, and written out, or left in the
@@ -448,8 +553,7 @@ __device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const Stat
     float *wo = reinterpret_cast<float *>(base + S::kWo);
     float *wm = reinterpret_cast<float *>(base + S::kStat);   // [kWarps][ROWS] each: m, l, mo
     float *wl = wm + kWarps * ROWS, *wmo = wl + kWarps * ROWS;
-    const int g8 = lane >> 2, t4 = lane & 3;
-    const bool whole = of.start >= lo && of.start + of.n <= hi;
+    const bool whole = of.n <= kWhole || (of.start >= lo && of.start + of.n <= hi);
     const int c0 = of.start / len, c1 = (of.start + of.n - 1) / len;
     float *part = p.parts + static_cast<size_t>(part_slot(c, c0)) * PART;
 #pragma unroll
@@ -458,36 +562,15 @@ __device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const Stat
         // sums rows w, w + kWarps, ...
         if (nt > 0 && !meet(bar, meetings++ & 1))   // wo is free again
             return false;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float l = st.l[nt][h];
-            l += __shfl_xor_sync(0xffffffffu, l, 4);
-            l += __shfl_xor_sync(0xffffffffu, l, 8);
-            l += __shfl_xor_sync(0xffffffffu, l, 16);
-            if (g8 == 0) {
-                const int at = warp * ROWS + nt * 8 + 2 * t4 + h;
-                wm[at] = st.m[nt][h];
-                wl[at] = l;
-                wmo[at] = st.mo[nt][h];
-            }
-        }
+        st.put_stats(wm + warp * ROWS + nt * 8, wl + warp * ROWS + nt * 8, wmo + warp * ROWS + nt * 8, nt, lane);
         float4 o[kQuads];
         float m[kQuads], mo[kQuads];
 #pragma unroll
         for (int half = 1; half >= 0; --half) {
             if (half == 0 && !meet(bar, meetings++ & 1))   // wo is free again
                 return false;
-            if (warp >> 1 == half) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float *dst = wo + ((warp & 1) * 8 + 2 * t4 + h) * kStride + 16 * g8;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        *reinterpret_cast<float4 *>(dst + 4 * i) =
-                            make_float4(st.acc[2 * i][nt][h], st.acc[2 * i][nt][h + 2], st.acc[2 * i + 1][nt][h],
-                                        st.acc[2 * i + 1][nt][h + 2]);
-                }
-            }
+            if (warp >> 1 == half)
+                st.put_o(wo + (warp & 1) * 8 * kStride, nt, lane);
             if (!meet(bar, meetings++ & 1))
                 return false;
 #pragma unroll
@@ -546,7 +629,6 @@ __device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const Stat
     // The states of the pair's CTAs, merged by the last of them, in their order.  Where they
     // are many, the last of each kGroup neighbours merges theirs first (into the slot of the
     // first of them), and the last of those the groups'.
-    float *sm = wo, *sl = sm + kDirect * ROWS, *smo = sl + kDirect * ROWS, *row_stat = smo + kDirect * ROWS;
     const bool grouped = c1 - c0 + 1 > kDirect;
     const int g = c / kGroup, g0 = c0 / kGroup;
 #pragma unroll 1
@@ -568,7 +650,8 @@ __device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const Stat
         }
         if (!meet(bar, meetings++ & 1))   // the CTA's state is written
             return false;
-        arrive_last(counter, n, flag, tid);
+        if (tid == 0)
+            *flag = arrive_last(counter, n);
         if (!meet(bar, meetings++ & 1))
             return false;
         if (*flag == 0)
@@ -576,99 +659,77 @@ __device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const Stat
         auto slot = [&](int j) {
             return p.parts + static_cast<size_t>(part_slot(j == 0 ? first : step == 1 ? first + j : (g0 + j) * kGroup, c0)) * PART;
         };
-        // a thread sums kPer quads (a quad's place in a state is its number);
-        // kStep states' quads are on their way at a time, the first ones already now
-        constexpr int kPer = 2, kStep = 8;
-        const int quads = p.G * (kD / 4);
-        float4 x[kStep][kPer];
-        auto fetch = [&](int e0, int j0) {
-#pragma unroll
-            for (int u = 0; u < kStep; ++u) {
-                const float4 *src = reinterpret_cast<const float4 *>(slot(j0 + u));
-#pragma unroll
-                for (int i = 0; i < kPer; ++i)
-                    x[u][i] = j0 + u < n && e0 + i * kWarps * 32 < quads ? __ldcg(src + e0 + i * kWarps * 32)
-                                                                         : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-        };
-        fetch(tid, 0);
-#pragma unroll 1
-        for (int e = tid; e < n * ROWS; e += kWarps * 32) {
-            const float *src = slot(e / ROWS) + ROWS * kD + e % ROWS;
-            if (e % ROWS < p.G) {
-                sm[e] = __ldcg(src);
-                sl[e] = __ldcg(src + ROWS);
-                smo[e] = __ldcg(src + 2 * ROWS);
-            }
-        }
-        if (!meet(bar, meetings++ & 1))
-            return false;
-        // a warp takes a row, a lane a state
-#pragma unroll 1
-        for (int row = warp; row < p.G; row += kWarps) {
-            const int e = lane * ROWS + row;
-            const bool in = lane < n;
-            const float mj = in ? sm[e] : -INFINITY, lj = in ? sl[e] : 0.f, moj = in ? smo[e] : -INFINITY;
-            float m = mj, mo = moj;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                mo = fmaxf(mo, __shfl_xor_sync(0xffffffffu, mo, o));
-            }
-            float l = lj == 0.f ? 0.f : lj * ex2_approx(mj - m);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                l += __shfl_xor_sync(0xffffffffu, l, o);
-            if (in)
-                smo[e] = moj == -INFINITY ? 0.f : ex2_approx(moj - mo);   // O's weight
-            if (lane == 0) {
-                row_stat[row] = m;
-                row_stat[ROWS + row] = l;
-                row_stat[2 * ROWS + row] = mo;
-            }
-        }
-        if (!meet(bar, meetings++ & 1))
-            return false;
+        // A warp takes two rows at a time, its lanes four dims each of O, and before that a state's
+        // statistics each, from which the rows' come by shuffles.  All loads of up to kStep
+        // states go out together.
+        constexpr int kStep = 8;
         float *dst = slot(0);
 #pragma unroll 1
-        for (int e0 = tid; e0 < quads; e0 += kPer * kWarps * 32) {
-            float4 o[kPer];
+        for (int row0 = warp; row0 < p.G; row0 += 2 * kWarps) {
+            const int rows[2] = {row0, row0 + kWarps};
+            float4 x[2][kStep];
+            auto fetch = [&](int j0) {
 #pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int u = 0; u < kStep; ++u) {
+                    const float4 *src = reinterpret_cast<const float4 *>(slot(j0 + u)) + lane;
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        x[r][u] = j0 + u < n && rows[r] < p.G ? __ldcg(src + rows[r] * (kD / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+            };
+            const float *stat = slot(min(lane, n - 1)) + ROWS * kD + row0;
+            float m[2], l[2], mo[2], w[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const bool in = lane < n && rows[r] < p.G;
+                m[r] = in ? __ldcg(stat + r * kWarps) : -INFINITY;
+                l[r] = in ? __ldcg(stat + ROWS + r * kWarps) : 0.f;
+                mo[r] = in ? __ldcg(stat + 2 * ROWS + r * kWarps) : -INFINITY;
+            }
+            fetch(0);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float mj = m[r], moj = mo[r];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    m[r] = fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], o));
+                    mo[r] = fmaxf(mo[r], __shfl_xor_sync(0xffffffffu, mo[r], o));
+                }
+                l[r] = l[r] == 0.f ? 0.f : l[r] * ex2_approx(mj - m[r]);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
+                w[r] = moj == -INFINITY ? 0.f : ex2_approx(moj - mo[r]);   // O's weight
+            }
+            float4 o[2] = {};
 #pragma unroll 1
             for (int j0 = 0; j0 < n; j0 += kStep) {
-                if (e0 != tid || j0 != 0)
-                    fetch(e0, j0);
+                if (j0 > 0)
+                    fetch(j0);
 #pragma unroll
                 for (int u = 0; u < kStep; ++u)
 #pragma unroll
-                    for (int i = 0; i < kPer; ++i) {
-                        const int row = min(e0 + i * kWarps * 32, quads - 1) / (kD / 4);
-                        const float f = j0 + u < n ? smo[(j0 + u) * ROWS + row] : 0.f;
-                        o[i].x = fmaf(f, x[u][i].x, o[i].x);
-                        o[i].y = fmaf(f, x[u][i].y, o[i].y);
-                        o[i].z = fmaf(f, x[u][i].z, o[i].z);
-                        o[i].w = fmaf(f, x[u][i].w, o[i].w);
+                    for (int r = 0; r < 2; ++r) {
+                        const float f = __shfl_sync(0xffffffffu, w[r], j0 + u);
+                        o[r].x = fmaf(f, x[r][u].x, o[r].x);
+                        o[r].y = fmaf(f, x[r][u].y, o[r].y);
+                        o[r].z = fmaf(f, x[r][u].z, o[r].z);
+                        o[r].w = fmaf(f, x[r][u].w, o[r].w);
                     }
             }
+            __syncwarp();   // what goes into the first of the slots has been read
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int e = e0 + i * kWarps * 32;
-                if (e >= quads)
+            for (int r = 0; r < 2; ++r) {
+                if (rows[r] >= p.G)
                     break;
-                const int row = e / (kD / 4), d = 4 * (e % (kD / 4));
-                const float m = row_stat[row], l = row_stat[ROWS + row], mo = row_stat[2 * ROWS + row];
                 if (level == 1) {
-                    write_out(p, of.pair, row, d, o[i], m, l, mo);
+                    write_out(p, of.pair, rows[r], 4 * lane, o[r], m[r], l[r], mo[r]);
                 } else {
-                    // each element of the slot was read by the thread that writes it, and its
-                    // statistics before the meetings
-                    *reinterpret_cast<float4 *>(dst + row * kD + d) = o[i];
-                    if (d == 0) {
-                        dst[ROWS * kD + row] = m;
-                        dst[ROWS * kD + ROWS + row] = l;
-                        dst[ROWS * kD + 2 * ROWS + row] = mo;
+                    *(reinterpret_cast<float4 *>(dst + rows[r] * kD) + lane) = o[r];
+                    if (lane == 0) {
+                        dst[ROWS * kD + rows[r]] = m[r];
+                        dst[ROWS * kD + ROWS + rows[r]] = l[r];
+                        dst[ROWS * kD + 2 * ROWS + rows[r]] = mo[r];
                     }
                 }
             }
@@ -691,10 +752,9 @@ template <int NT>
 __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
     paged_attn_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ PagedAttnParams p)
 {
-    constexpr int ROWS = 8 * NT;
     constexpr int kWarps = warps<NT>(), kSlots = slots<NT>(), kThreads = (kWarps + 1) * 32;
     using S = Smem<NT>;
-    static_assert((3 * kDirect + 3) * ROWS <= 2 * 8 * kStride, "the merge's weights fit the warps' states");
+    static_assert(kDirect <= 32, "a lane holds a state's statistics");
     extern __shared__ uint8_t smem_raw[];
     __shared__ int s_sum[kWarps + 1], s_pair, s_n, s_start, s_last;
     const uint32_t base_s = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -708,7 +768,6 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
     // SM's partitions: the second half of the grid turns them, so that an SM's two producers
     // share a partition with a consumer each.
     const int warp = kWarps == 3 && 2 * blockIdx.x >= gridDim.x ? (tid / 32 + 2) % 4 : tid / 32;
-
     if (tid == 0) {
         for (int i = 0; i < kWarps * kSlots; ++i) {
             mbar_init(full + 8 * i, 2);          // the load's expect_tx, and the item record
@@ -721,6 +780,16 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
         prefetch_tensormap(&map);
     griddep_wait();
     griddep_launch_dependents();
+
+    // the tables into L2, while the lengths are summed
+    {
+        const size_t line = static_cast<size_t>(blockIdx.x) * kThreads + tid;
+        const size_t rows = static_cast<size_t>(p.B) * p.max_blocks, ids = p.blk_idx != nullptr ? static_cast<size_t>(p.B) * p.H_kv * p.k_tot : 0;
+        if (line * 32 < rows)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.block_table + line * 32));
+        if (line * 32 < ids)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.blk_idx + line * 32));
+    }
 
     // ---- length before each unit (a request where every block is attended over, else a pair)
     const bool all = p.blk_idx == nullptr;
@@ -772,8 +841,7 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
         s_n = n;
     }
     __syncthreads();
-    // no items: an empty range, or one within what a pair costs beside its items
-    const bool idle = lo >= hi || s_start + kPairCost >= hi;
+    const bool idle = lo >= hi;
 
     if (warp == kWarps) {
         // ------------------------------------------------------------ producer
@@ -783,7 +851,7 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
         int it = 0, part = 0;          // the CTA's next item and part
         bool stop = false, wrong = false;
         auto free_slot = [&](int slot, int fill) {
-            return fill < kSlots || mbar_wait(empty + 8 * slot, (fill / kSlots - 1) & 1, kWaitNs);
+            return fill < kSlots || wait_for(empty + 8 * slot, (fill / kSlots - 1) & 1, kWaitNs);
         };
         auto load = [&](int slot, int tile, int rows) {
             if (rows > 0) {
@@ -814,7 +882,8 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
             end += start;
             // items [a, a + cnt) of the lane's pair are the CTA's
             const int first = end - n;   // the pair's items start here
-            const int a = max(0, min(n, lo - first)), cnt = max(0, min(n, hi - first) - a);
+            const int2 share = pair_share(first, n, lo, hi);
+            const int a = share.x, cnt = share.y;
             int upto = cnt;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -940,14 +1009,16 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
     // While the first tiles travel: the first pair's queries, and a pass (`warm`) over whatever
     // the stage holds, which brings the loop's code into the instruction cache; its result is
     // dropped.
-    int part = 0, q_part = -1, meetings = 0;
+    int part = 0, meetings = 0;
+    q.load(p, s_pair, lane);
+    bool loaded = pair_share(s_start + kPairCost, s_n, lo, hi).y > 0;   // else it is not the CTA's first
     bool warm = true;
 #pragma unroll 1
     for (int it = warp, fill = 0;;) {
         const int k_slot = warp * kSlots + fill % kSlots, v_slot = warp * kSlots + (fill + 1) % kSlots;
         Item item{1.f, 0.f, kBlk, 0};
         if (!warm) {
-            if (!__all_sync(0xffffffffu, mbar_wait(full + 8 * k_slot, (fill / kSlots) & 1, kWaitNs))) {
+            if (!__all_sync(0xffffffffu, wait_for(full + 8 * k_slot, (fill / kSlots) & 1, kWaitNs))) {
                 give_up(p, lane);
                 return;
             }
@@ -958,6 +1029,8 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
             for (; part < next; ++part) {
                 const Part of = parts[part % kMeta];
                 bool ok = finish_part<NT>(p, st, of, c, lo, hi, len, base, bar, meetings, &s_last, warp, lane);
+                if (part + 1 < next || (item.part & kEnd) == 0)
+                    q.load(p, parts[(part + 1) % kMeta].pair, lane);
                 st.reset();
                 ok = ok && meet(bar, meetings++ & 1);   // shared memory is free again
                 if (!ok) {
@@ -967,10 +1040,10 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
             }
             if (item.part & kEnd)
                 return;
-        }
-        if (part != q_part && item.rows > 0) {
-            q_part = part;
-            q.load(p, warm ? s_pair : parts[part % kMeta].pair, lane);
+            if (part == 0 && !loaded) {
+                loaded = true;
+                q.load(p, parts[0].pair, lane);
+            }
         }
         auto values = [&]() -> uint32_t {
             if (warm)
@@ -978,7 +1051,7 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(empty + 8 * k_slot);
-            const bool there = __all_sync(0xffffffffu, mbar_wait(full + 8 * v_slot, ((fill + 1) / kSlots) & 1, kWaitNs));
+            const bool there = __all_sync(0xffffffffu, wait_for(full + 8 * v_slot, ((fill + 1) / kSlots) & 1, kWaitNs));
             return there ? base_s + v_slot * kTile : 0u;
         };
         const bool ok = item.rows > 0 ? attend<NT>(st, q, base_s + k_slot * kTile, values, item.ks, item.log2_vs, item.rows, lane)
