@@ -484,10 +484,10 @@ _F8 = torch.float8_e4m3fn
 # is wrong is looked for (_explain) only when something is.
 
 
-def _sound(idx, specs) -> bool:
-    """Whether every (tensor, dtype, shape) is contiguous on device ``idx``."""
+def _sound(idx, dtype, shape, *tensors) -> bool:
+    """Whether every tensor has this type and shape and is contiguous on device ``idx``."""
     try:
-        for t, dtype, shape in specs:
+        for t in tensors:
             if t.dtype is not dtype or t.shape != shape or t.get_device() != idx or not t.is_contiguous():
                 return False
     except AttributeError:   # not a tensor
@@ -495,8 +495,9 @@ def _sound(idx, specs) -> bool:
     return True
 
 
-def _explain(idx, names, specs):
-    for name, (t, dtype, shape) in zip(names, specs):
+def _explain(idx, dtype, shape, **tensors):
+    """Raises for the first tensor that is not as _sound wants it."""
+    for name, t in tensors.items():
         _need(t, name, dtype, shape=shape)
         if t.get_device() != idx:
             raise ValueError(f"{name} is on {t.device}, expected device {idx}")
@@ -540,15 +541,17 @@ def sparse_page_plan(seq_len, n_new, block_table, free_pages, n_free, cu_new, st
     B, max_blocks = block_table.shape
     n_pages, n_tok = free_pages.numel(), slot_map.numel()
     per_request, one, rows = (B,), (1,), (n_tok,)
-    specs = [(block_table, i32, (B, max_blocks)), (seq_len, i32, per_request), (n_new, i32, per_request),
-             (free_pages, i32, (n_pages,)), (n_free, i32, one), (cu_new, i32, (B + 1,)), (start, i32, per_request),
-             (seq_len_out, i32, per_request), (n_free_out, i32, one), (slot_map, i32, rows), (tok_req, i32, rows),
-             (tok_pos, i32, rows)]
-    if status is not None:
-        specs.append((status, i32, one))
-    if not _sound(idx, specs):
-        _explain(idx, ("block_table", "seq_len", "n_new", "free_pages", "n_free", "cu_new", "start", "seq_len_out",
-                       "n_free_out", "slot_map", "tok_req", "tok_pos", "status"), specs)
+    if not (_sound(idx, i32, per_request, seq_len, n_new, start, seq_len_out)
+            and _sound(idx, i32, rows, slot_map, tok_req, tok_pos) and _sound(idx, i32, one, n_free, n_free_out)
+            and _sound(idx, i32, (B, max_blocks), block_table) and _sound(idx, i32, (n_pages,), free_pages)
+            and _sound(idx, i32, (B + 1,), cu_new) and (status is None or _sound(idx, i32, one, status))):
+        _explain(idx, i32, per_request, seq_len=seq_len, n_new=n_new, start=start, seq_len_out=seq_len_out)
+        _explain(idx, i32, rows, slot_map=slot_map, tok_req=tok_req, tok_pos=tok_pos)
+        _explain(idx, i32, one, n_free=n_free, n_free_out=n_free_out)
+        _explain(idx, i32, (B, max_blocks), block_table=block_table)
+        _explain(idx, i32, (n_pages,), free_pages=free_pages)
+        _explain(idx, i32, (B + 1,), cu_new=cu_new)
+        _explain(idx, i32, one, status=status)
     _call((_lib or load()).sparse_page_plan, "sparse_page_plan", idx, stream, seq_len.data_ptr(), n_new.data_ptr(), B,
           block_table.data_ptr(), max_blocks, free_pages.data_ptr(), n_pages, n_free.data_ptr(), cu_new.data_ptr(),
           start.data_ptr(), seq_len_out.data_ptr(), n_free_out.data_ptr(), slot_map.data_ptr(), tok_req.data_ptr(),
@@ -583,26 +586,27 @@ def sparse_paged_append_f8(kv_pages, kv_scale, k_new, v_new, slot_map, ktil=None
     n_tok = slot_map.numel()
     i32, f32, rows = torch.int32, torch.float32, (n_tok,)
     ks, vs = _token_stride(k_new, "k_new", idx, n_tok, H_kv), _token_stride(v_new, "v_new", idx, n_tok, H_kv)
-    specs = [(kv_pages, _F8, (n_pages, H_kv, 2, BLK, D)), (kv_scale, f32, (n_pages, H_kv, 2)), (slot_map, i32, rows)]
-    names = ["kv_pages", "kv_scale", "slot_map"]
+    pages, scales, one = (n_pages, H_kv, 2, BLK, D), (n_pages, H_kv, 2), (1,)
     B = N_cap = 0
     kt = req = pos = st = None
+    if not (_sound(idx, _F8, pages, kv_pages) and _sound(idx, f32, scales, kv_scale) and _sound(idx, i32, rows, slot_map)
+            and (status is None or _sound(idx, i32, one, status))):
+        _explain(idx, _F8, pages, kv_pages=kv_pages)
+        _explain(idx, f32, scales, kv_scale=kv_scale)
+        _explain(idx, i32, rows, slot_map=slot_map)
+        _explain(idx, i32, one, status=status)
     if ktil is not None:
         if tok_req is None or tok_pos is None:
             raise ValueError("ktil needs tok_req and tok_pos")
         _tensors(("ktil", ktil))
         B, _, N_cap, _ = ktil.shape
-        specs += [(ktil, f32, (B, H_kv, N_cap, D)), (tok_req, i32, rows), (tok_pos, i32, rows)]
-        names += ["ktil", "tok_req", "tok_pos"]
-    if status is not None:
-        specs.append((status, i32, (1,)))
-        names.append("status")
-    if not _sound(idx, specs):
-        _explain(idx, names, specs)
+        keys = (B, H_kv, N_cap, D)
+        if not (_sound(idx, f32, keys, ktil) and _sound(idx, i32, rows, tok_req, tok_pos)):
+            _explain(idx, f32, keys, ktil=ktil)
+            _explain(idx, i32, rows, tok_req=tok_req, tok_pos=tok_pos)
+        kt, req, pos = ktil.data_ptr(), tok_req.data_ptr(), tok_pos.data_ptr()
     if status is not None:
         st = status.data_ptr()
-    if ktil is not None:
-        kt, req, pos = ktil.data_ptr(), tok_req.data_ptr(), tok_pos.data_ptr()
     _call((_lib or load()).sparse_paged_append_f8, "sparse_paged_append_f8", idx, stream, kv_pages.data_ptr(),
           kv_scale.data_ptr(), n_pages, H_kv, k_new.data_ptr(), v_new.data_ptr(), ks, vs, slot_map.data_ptr(), n_tok, kt, B,
           N_cap, req, pos, st)
@@ -632,33 +636,33 @@ def sparse_paged_decode_attn_f8(Q, kv_pages, kv_scale, block_table, seq_len, O, 
     H_q = Q.shape[1]
     i32, f32, b16 = torch.int32, torch.float32, torch.bfloat16
     ws_bytes = workspace.numel()
-    specs = [(kv_pages, _F8, (n_pages, H_kv, 2, BLK, D)), (kv_scale, f32, (n_pages, H_kv, 2)), (Q, b16, (B, H_q, D)),
-             (O, b16, (B, H_q, D)), (block_table, i32, (B, max_blocks)), (seq_len, i32, (B,)),
-             (workspace, torch.uint8, (ws_bytes,))]
-    names = ["kv_pages", "kv_scale", "Q", "O", "block_table", "seq_len", "workspace"]
+    pages, scales, heads, table = (n_pages, H_kv, 2, BLK, D), (n_pages, H_kv, 2), (B, H_q, D), (B, max_blocks)
+    if not (_sound(idx, _F8, pages, kv_pages) and _sound(idx, f32, scales, kv_scale) and _sound(idx, b16, heads, Q, O)
+            and _sound(idx, i32, table, block_table) and _sound(idx, i32, (B,), seq_len)
+            and _sound(idx, torch.uint8, (ws_bytes,), workspace) and (lse is None or _sound(idx, f32, (B, H_q), lse))
+            and (status is None or _sound(idx, i32, (1,), status))):
+        _explain(idx, _F8, pages, kv_pages=kv_pages)
+        _explain(idx, f32, scales, kv_scale=kv_scale)
+        _explain(idx, b16, heads, Q=Q, O=O)
+        _explain(idx, i32, table, block_table=block_table)
+        _explain(idx, i32, (B,), seq_len=seq_len)
+        _explain(idx, torch.uint8, (ws_bytes,), workspace=workspace)
+        if lse is not None:
+            _explain(idx, f32, (B, H_q), lse=lse)
+        _explain(idx, i32, (1,), status=status)
     k_tot = 0
-    blocks = counts = lse_at = st = None
+    blocks = counts = None
     if blk_idx is not None:
         if count is None:
             raise ValueError("blk_idx needs count")
-        _tensors(("blk_idx", blk_idx), ("count", count))
+        _tensors(("blk_idx", blk_idx))
         k_tot = blk_idx.shape[2]
-        specs += [(blk_idx, i32, (B, H_kv, k_tot)), (count, i32, (B, H_kv))]
-        names += ["blk_idx", "count"]
-    if lse is not None:
-        specs.append((lse, f32, (B, H_q)))
-        names.append("lse")
-    if status is not None:
-        specs.append((status, i32, (1,)))
-        names.append("status")
-    if not _sound(idx, specs):
-        _explain(idx, names, specs)
-    if blk_idx is not None:
+        if not (_sound(idx, i32, (B, H_kv, k_tot), blk_idx) and _sound(idx, i32, (B, H_kv), count)):
+            _explain(idx, i32, (B, H_kv, k_tot), blk_idx=blk_idx)
+            _explain(idx, i32, (B, H_kv), count=count)
         blocks, counts = blk_idx.data_ptr(), count.data_ptr()
-    if lse is not None:
-        lse_at = lse.data_ptr()
-    if status is not None:
-        st = status.data_ptr()
+    lse_at = None if lse is None else lse.data_ptr()
+    st = None if status is None else status.data_ptr()
     _call((_lib or load()).sparse_paged_decode_attn_f8, "sparse_paged_decode_attn_f8", idx, stream, Q.data_ptr(),
           kv_pages.data_ptr(), kv_scale.data_ptr(), n_pages, block_table.data_ptr(), max_blocks, blocks, counts, k_tot,
           seq_len.data_ptr(), B, H_q, H_kv, scale, O.data_ptr(), lse_at, workspace.data_ptr(), ws_bytes, st)

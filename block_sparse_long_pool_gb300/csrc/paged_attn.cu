@@ -799,10 +799,13 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
     const int per = (units + kThreads - 1) / kThreads;
     const int u0 = min(units, tid * per), u1 = min(units, u0 + per);
     bool bad = false;
-    int mine = 0;
+    int mine = 0, n_first = 0;   // the thread's units' length, and its first one's items
 #pragma unroll 1
-    for (int u = u0; u < u1; ++u)
-        mine += pair_length(pair_items(p, u * heads, &bad)) * heads;
+    for (int u = u0; u < u1; ++u) {
+        const int n = pair_items(p, u * heads, &bad);
+        n_first = u == u0 ? n : n_first;
+        mine += pair_length(n) * heads;
+    }
     if (bad && blockIdx.x == 0)
         report(p.status, SPARSE_ERR_BAD_INDEX);
     int incl = mine;
@@ -827,13 +830,11 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
     const int lo = static_cast<int>(min(static_cast<uint32_t>(N), static_cast<uint32_t>(c) * len)), hi = min(N - lo, len) + lo;
     if (lo < hi && incl - mine <= lo && lo < incl) {
         // the pair that holds `lo`
-        int at = incl - mine, u = u0, n = 0;
+        int at = incl - mine, u = u0, n = n_first;
 #pragma unroll 1
-        for (; u < u1; ++u) {
-            n = pair_items(p, u * heads, &bad);
-            if (at + pair_length(n) * heads > lo)
-                break;
+        while (at + pair_length(n) * heads <= lo) {
             at += pair_length(n) * heads;
+            n = pair_items(p, ++u * heads, &bad);
         }
         const int h = all ? (lo - at) / pair_length(n) : 0;
         s_pair = u * heads + h;
@@ -885,13 +886,15 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
             const int2 share = pair_share(first, n, lo, hi);
             const int a = share.x, cnt = share.y;
             int upto = cnt;
+            if (group > 1) {
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o)
-                    upto += v;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o)
+                        upto += v;
+                }
             }
-            const int total = __shfl_sync(0xffffffffu, upto, 31);
+            const int total = __shfl_sync(0xffffffffu, upto, group - 1);
             const unsigned has = __ballot_sync(0xffffffffu, cnt > 0);
             const int my_part = part + __popc(has & ((1u << lane) - 1));
             if (cnt > 0)
@@ -901,10 +904,12 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
                 // lane j resolves item done + j: of the first pair whose count reaches past it
                 const int take = min(32, total - done);
                 int k = 0;
+                if (group > 1) {
 #pragma unroll
-                for (int half = 16; half > 0; half >>= 1)
-                    if (__shfl_sync(0xffffffffu, upto, k + half - 1) <= done + lane)
-                        k += half;
+                    for (int half = 16; half > 0; half >>= 1)
+                        if (__shfl_sync(0xffffffffu, upto, k + half - 1) <= done + lane)
+                            k += half;
+                }
                 const int in_pair = done + lane - (__shfl_sync(0xffffffffu, upto, k) - __shfl_sync(0xffffffffu, cnt, k));
                 const int i = __shfl_sync(0xffffffffu, a, k) + in_pair;
                 Item item;
@@ -930,13 +935,16 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
                         }
                     }
                 }
-                // the slots are empty at first: the first items' keys go out before the scales are here
+                // The slots are empty at first: the first items' keys and values go out before the
+                // scales are here, each from a lane of its own (one after another they would take
+                // 0.15 us each).
                 const int ahead = it == 0 ? min(take, kWarps) : 0;
-#pragma unroll 1
-                for (int j = 0; j < ahead; ++j) {
+                if (ahead > 0) {
+                    const int j = lane % kWarps;
                     const int u = __shfl_sync(0xffffffffu, unit, j), rows = __shfl_sync(0xffffffffu, item.rows, j);
-                    if (lane == 0)
-                        load(j * kSlots, 2 * u, rows);
+                    if (lane < 2 * kWarps && j < ahead)
+                        load(j * kSlots + lane / kWarps, 2 * u + lane / kWarps, rows);
+                    __syncwarp();
                 }
                 item.ks = sc.x;
                 item.log2_vs = __log2f(sc.y);
@@ -949,18 +957,21 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
                     if (lane == 0) {
                         const int ring = (it + j) % kWarps * kSlots, fill = (it + j) / kWarps * 2;
                         const int k_slot = ring + fill % kSlots, v_slot = ring + (fill + 1) % kSlots;
-                        if (j >= ahead) {
-                            stop = !free_slot(k_slot, fill);
-                            if (!stop)
-                                load(k_slot, 2 * u, rows);
-                        }
-                        if (!stop) {
+                        // (values have no record: both of their arrivals come with the load)
+                        if (j < ahead) {
                             mbar_arrive(full + 8 * k_slot);   // the item record
-                            stop = !free_slot(v_slot, fill + 1);
-                        }
-                        if (!stop) {
-                            load(v_slot, 2 * u + 1, rows);
                             mbar_arrive(full + 8 * v_slot);
+                        } else {
+                            stop = !free_slot(k_slot, fill);
+                            if (!stop) {
+                                load(k_slot, 2 * u, rows);
+                                mbar_arrive(full + 8 * k_slot);
+                                stop = !free_slot(v_slot, fill + 1);
+                            }
+                            if (!stop) {
+                                load(v_slot, 2 * u + 1, rows);
+                                mbar_arrive(full + 8 * v_slot);
+                            }
                         }
                     }
                     stop = __shfl_sync(0xffffffffu, stop ? 1 : 0, 0) != 0;
@@ -985,7 +996,7 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
             mbar_arrive(full + 8 * slot);
             mbar_arrive(full + 8 * slot);
         }
-        if (__any_sync(0xffffffffu, wrong) && lane == 0)
+        if (__any_sync(0xffffffffu, wrong || bad) && lane == 0)
             report(p.status, SPARSE_ERR_BAD_INDEX);
         if (__any_sync(0xffffffffu, stop))
             give_up(p, lane);

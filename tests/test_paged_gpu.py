@@ -390,6 +390,38 @@ def test_attn_lists_and_tables_outside_are_skipped_and_reported():
     assert a.status.item() == want_status and (a.O[:2] == 0).all() and torch.isinf(a.lse[:2]).all()
 
 
+@pytest.mark.parametrize("selected", [False, True])
+@pytest.mark.parametrize("length", [-1, 4 * BLK + 1])
+def test_attn_a_length_outside_its_table_is_reported(selected, length):
+    rng = np.random.default_rng(10)
+    c, table, Q = attn_case(rng, [200, 250], 2, 2, extra_blocks=0)
+    a = Attn(2, 4, 2)
+    idx, count = i32(np.tile(np.arange(4), (2, 2, 1))), i32(np.full((2, 2), 4))
+    a.call(Q, c, i32(table), i32([200, length]), *((idx, count) if selected else ()))
+    torch.cuda.synchronize()
+    assert a.status.item() == binding.SPARSE_ERR_BAD_INDEX
+    want = ref.attn(ref.f64(Q), ref.f8_values(c.pages), ref.f64(c.scale), table, [200, 0])
+    ref.assert_attn(a.O[:1], a.lse[:1], [x[:1] for x in want], 256)
+    if length < 0:
+        assert (a.O[1] == 0).all() and torch.isinf(a.lse[1]).all()
+
+
+def test_attn_values_of_tiny_and_huge_pages():
+    """Value scales at the ends of what the append writes: outputs near fp32's limits."""
+    rng = np.random.default_rng(14)
+    lens = [500, 500]
+    c, table, Q = attn_case(rng, lens, 1, 8)
+    used = torch.as_tensor(table[0][table[0] >= 0].astype(np.int64), device=DEV)
+    c.scale[:, :, 1] = 2.0 ** 110
+    c.scale[used, :, 1] = 2.0 ** -118
+    a = Attn(2, 8, 1)
+    a.call(Q, c, i32(table), i32(lens))
+    torch.cuda.synchronize()
+    want = ref.attn(ref.f64(Q), ref.f8_values(c.pages), ref.f64(c.scale), table, lens)
+    for b in range(2):
+        ref.assert_attn(a.O[b:b + 1], a.lse[b:b + 1], [x[b:b + 1] for x in want], 500)
+
+
 def test_attn_scale_and_large_scores():
     """Scores of several hundred, a scale of the caller's, scales of very different pages."""
     rng = np.random.default_rng(21)
