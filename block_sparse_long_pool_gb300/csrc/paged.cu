@@ -20,7 +20,7 @@ constexpr int kPlanMaxB = 4096;
 constexpr int kPlanPer = kPlanMaxB / kPlanThreads;   // requests a thread scans, at most
 constexpr int kRowThreads = 256;
 constexpr int kRowsPerCta = 1024;
-constexpr int kRowsOneCta = 1024;   // rows that the planning CTA writes itself
+constexpr int kRowsOneCta = 1024;   // rows that the planning CTA writes itself, one a thread
 
 struct PlanParams {
     const int *seq_len;
@@ -87,13 +87,29 @@ __device__ __forceinline__ int pages_taken(const int *cu, const int *first, int 
     return st < 0 ? 0 : (st + (cu[b + 1] - cu[b]) + kBlk - 1) / kBlk - (st + kBlk - 1) / kBlk;
 }
 
+// Where the i-th returned page is: in the table of the request that returns it.
+__device__ __forceinline__ const int *returned_page(const PlanParams &p, const int *relpre, int i)
+{
+    int b = 0, hi = p.B - 1;
+    while (b < hi) {
+        const int mid = (b + hi + 1) >> 1;
+        if (relpre[mid] <= i)   // of requests with equal ones the last returns pages
+            b = mid;
+        else
+            hi = mid - 1;
+    }
+    return p.block_table + static_cast<size_t>(b) * p.max_blocks + (i - relpre[b]);
+}
+
 // Rows [t0, t0 + n), R of them (1 or 4, t0 a multiple of R) a thread and pass: the first
 // row's request by binary search, the next rows' by steps from it; then the pages, whose
 // loads are in flight together; then the three entries, as words of R.  A new block's page
 // comes from the free list and is entered into the table by the row that starts the block.
+//   With `relpre` the pages returned in this step (places F0 .. F - 1 of the list) are taken from
+// the tables of the requests that return them: the list may not hold them yet.
 template <int R>
 __device__ __forceinline__ void plan_rows(const PlanParams &p, const int *cu, const int *first, const int *npre, int F,
-                                          int t0, int n)
+                                          int t0, int n, const int *relpre = nullptr, int F0 = 0)
 {
     const int total = cu[p.B];
     for (int i = R * static_cast<int>(threadIdx.x); i < n; i += R * static_cast<int>(blockDim.x)) {
@@ -125,7 +141,9 @@ __device__ __forceinline__ void plan_rows(const PlanParams &p, const int *cu, co
                     pos[j] = st + t + j - cu[b];
                     const int blk = pos[j] / kBlk, used = (st + kBlk - 1) / kBlk;
                     int *at = p.block_table + static_cast<size_t>(b) * p.max_blocks + blk;
-                    from[j] = blk < used ? at : p.free_pages + (F - 1 - (npre[b] + blk - used));
+                    const int place = F - 1 - (npre[b] + blk - used);
+                    from[j] = blk < used ? at : relpre != nullptr && place >= F0 ? returned_page(p, relpre, place - F0)
+                                                                                 : p.free_pages + place;
                     to[j] = blk >= used && pos[j] % kBlk == 0 ? at : nullptr;
                 }
             }
@@ -158,7 +176,11 @@ __device__ __forceinline__ void plan_rows(const PlanParams &p, const int *cu, co
     }
 }
 
-__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParams p, int with_rows)
+// Every CTA works out the requests' places for itself (B is small, and this costs less than a
+// second launch); CTA 0 writes them, and each writes `rows` rows (0: page_rows_kernel does).
+// More than one CTA only where no output is an input's buffer: one CTA's writes would change
+// what another still has to read.
+__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParams p, int rows)
 {
     extern __shared__ int plan_smem[];
     __shared__ long long red[33];
@@ -246,43 +268,36 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
             if (ok)
                 s_taken += need[i];
             refused |= !ok && !ends[i];
-            p.start[b] = first[b];
-            p.cu_new[b + 1] = cu[b + 1];
-            p.seq_len_out[b] = static_cast<int>(ends[i] ? 0 : ok ? len[i] + add[i] : len[i]);
-        }
-    }
-    if (tid == 0)
-        p.cu_new[0] = 0;
-    if (bad)
-        report(p.status, SPARSE_ERR_BAD_INDEX);
-    if (refused)
-        report(p.status, SPARSE_ERR_NO_PAGES);
-    long long all_taken;
-    block_scan(s_taken, red, &all_taken);   // its barriers also publish cu, first, npre, rel
-    if (tid == 0)
-        p.n_free_out[0] = F - static_cast<int>(all_taken);
-    if (all_rel > 0) {
-        // returned pages, one a thread: its request by binary search
-        const int end = static_cast<int>(min(all_rel, static_cast<long long>(p.n_pages - F0)));
-        for (int i = tid; i < end; i += kPlanThreads) {
-            int b = 0, hi = p.B - 1;
-            while (b < hi) {
-                const int mid = (b + hi + 1) >> 1;
-                if (relpre[mid] <= i)
-                    b = mid;
-                else
-                    hi = mid - 1;
+            if (blockIdx.x == 0) {
+                p.start[b] = first[b];
+                p.cu_new[b + 1] = cu[b + 1];
+                p.seq_len_out[b] = static_cast<int>(ends[i] ? 0 : ok ? len[i] + add[i] : len[i]);
             }
-            p.free_pages[F0 + i] = p.block_table[static_cast<size_t>(b) * p.max_blocks + i - relpre[b]];
         }
-        __syncthreads();
     }
-    if (with_rows)
-        plan_rows<1>(p, cu, first, npre, F, 0, p.n_tok);
+    long long all_taken;
+    block_scan(s_taken, red, &all_taken);   // its barriers also publish cu, first, npre, relpre
+    if (blockIdx.x == 0) {
+        if (bad)
+            report(p.status, SPARSE_ERR_BAD_INDEX);
+        if (refused)
+            report(p.status, SPARSE_ERR_NO_PAGES);
+        if (tid == 0) {
+            p.cu_new[0] = 0;
+            p.n_free_out[0] = F - static_cast<int>(all_taken);
+        }
+        for (int i = tid; i < F - F0; i += kPlanThreads)
+            p.free_pages[F0 + i] = *returned_page(p, relpre, i);
+    }
+    const int t0 = static_cast<int>(blockIdx.x) * rows, n = min(p.n_tok - t0, rows);
+    if (rows > kPlanThreads)
+        plan_rows<4>(p, cu, first, npre, F, t0, n, relpre, F0);
+    else if (rows > 0)
+        plan_rows<1>(p, cu, first, npre, F, t0, n, relpre, F0);
 }
 
-// Steps with many rows: the grid writes them after page_plan_kernel, whose outputs give it
-// all it needs (F = what is left on the list and what was taken).
+// Steps with many rows whose outputs replace their inputs: the rows, after page_plan_kernel,
+// whose outputs give all that is needed (F = what is left on the list and what was taken).
 __global__ void __launch_bounds__(kRowThreads) page_rows_kernel(const PlanParams p)
 {
     extern __shared__ int plan_smem[];
@@ -698,10 +713,16 @@ extern "C" SPARSE_API int sparse_page_plan(const int *seq_len, const int *n_new,
                                        (3 * kPlanMaxB + 1) * static_cast<int>(sizeof(int)), dev.device, configured[1]);
     if (rc != SPARSE_OK)
         return rc;
-    const int with_rows = n_tok <= kRowsOneCta;
-    rc = sp_host::cuda_status(launch_pdl(reinterpret_cast<const void *>(page_plan_kernel), dim3(1), kPlanThreads,
-                                         (4 * B + 1) * static_cast<int>(sizeof(int)), stream, p, with_rows), name);
-    if (rc != SPARSE_OK || with_rows)
+    // One row a thread up to a CTA an SM (the kernel's registers allow one), then four a pass.
+    const bool in_place = seq_len_out == seq_len || n_free_out == n_free;
+    const bool one_launch = n_tok <= kRowsOneCta || !in_place;
+    const int per_sm = (n_tok + dev.sm_count - 1) / dev.sm_count, pass = 4 * kRowsOneCta;
+    const int rows = !one_launch ? 0 : per_sm <= kRowsOneCta ? kRowsOneCta : (per_sm + pass - 1) / pass * pass;
+    const int smem = (4 * B + 1) * static_cast<int>(sizeof(int));
+    const unsigned grid = one_launch ? (static_cast<unsigned>(n_tok) + rows - 1) / rows : 1u;
+    rc = sp_host::cuda_status(
+        launch_pdl(reinterpret_cast<const void *>(page_plan_kernel), dim3(grid), kPlanThreads, smem, stream, p, rows), name);
+    if (rc != SPARSE_OK || one_launch)
         return rc;
     const unsigned ctas = (static_cast<unsigned>(n_tok) + kRowsPerCta - 1) / kRowsPerCta;
     return sp_host::cuda_status(launch_pdl(reinterpret_cast<const void *>(page_rows_kernel), dim3(ctas), kRowThreads,
