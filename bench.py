@@ -1066,6 +1066,94 @@ def run_single_layer_case(args, dev, sh, name):
     print(json.dumps(line), flush=True)
 
 
+class _PagedLayer:
+    """The decode layer of a single-layer workload over the paged 8-bit cache: its prompts
+    planned and appended in one call each, then steps of one token a request."""
+
+    def __init__(self, sh, dev):
+        import torch
+        from block_sparse_long_pool_gb300 import binding
+        from block_sparse_long_pool_gb300 import workloads as wl
+        self.sh, self.binding = sh, binding
+        x = self.x = wl.single_layer(sh, dev)
+        B, H_kv, H_q = sh.B, sh.H_kv, sh.H_q
+        i32 = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=dev)
+        n_pages, max_blocks = B * sh.N_b + 8, sh.N_b
+        self.kv_pages = torch.zeros((n_pages, H_kv, 2, BLK, D), dtype=torch.float8_e4m3fn, device=dev)
+        self.kv_scale = torch.zeros((n_pages, H_kv, 2), device=dev)
+        self.ktil = torch.zeros((B, H_kv, sh.N_b, D), dtype=torch.float32, device=dev)
+        self.status = i32(1)
+        self.table, self.seq, self.seq_out = i32(B, max_blocks), i32(B), i32(B)
+        self.free, self.n_free, self.n_free_out = torch.randperm(n_pages, device=dev).to(torch.int32), i32(1), i32(1)
+        self.n_free.fill_(n_pages)
+        self.n_new, self.cu, self.start = i32(B), i32(B + 1), i32(B)
+        rows = lambda t: t.transpose(1, 2).reshape(-1, H_kv, D)   # [B][H_kv][n][128] -> packed rows
+        self.n_new.fill_(sh.T)
+        prompt = [i32(B * sh.T) for _ in range(3)]
+        self._plan(prompt, self.seq, self.n_free)
+        binding.sparse_paged_append_f8(self.kv_pages, self.kv_scale, rows(x["K"][:, :, :sh.T]), rows(x["V"][:, :, :sh.T]),
+                                       prompt[0], self.ktil, prompt[1], prompt[2], status=self.status)
+        self.n_new.fill_(sh.n_new)
+        self.maps = [i32(B * sh.n_new) for _ in range(3)]
+        self.k_new, self.v_new = rows(x["k_new"]), rows(x["v_new"])
+        self.F, self.Q = x["F"], x["Q"]
+        self.idx, self.cnt = i32(B, H_kv, sh.k_tot), i32(B, H_kv)
+        self.O = torch.empty((B, H_q, D), dtype=torch.bfloat16, device=dev)
+        self.ws = binding.paged_workspace(B, H_q, H_kv, device=dev)
+
+    def _plan(self, maps, seq_out, n_free_out):
+        self.binding.sparse_page_plan(self.seq, self.n_new, self.table, self.free, self.n_free, self.cu, self.start, seq_out,
+                                      n_free_out, *maps, status=self.status)
+
+    def attend(self, selected=True):
+        self.binding.sparse_paged_decode_attn_f8(self.Q, self.kv_pages, self.kv_scale, self.table, self.seq_out, self.O, self.ws,
+                                                 blk_idx=self.idx if selected else None,
+                                                 count=self.cnt if selected else None, status=self.status)
+
+    def step(self):
+        sh, bd = self.sh, self.binding
+        # the lengths before the step are kept: the same token at the same place every step
+        self._plan(self.maps, self.seq_out, self.n_free_out)
+        bd.sparse_paged_append_f8(self.kv_pages, self.kv_scale, self.k_new, self.v_new, self.maps[0], self.ktil, self.maps[1],
+                                  self.maps[2], status=self.status)
+        bd.sparse_select_topk(self.F, self.ktil, self.seq_out, sh.n_init, sh.n_local, sh.k, self.idx, self.cnt,
+                              status=self.status)
+        self.attend()
+
+
+def run_paged_case(args, dev):
+    import torch
+    from block_sparse_long_pool_gb300 import workloads as wl
+    peak, src = measured_peaks()
+    sh = wl.LLAMA8B_32K
+    lay = _PagedLayer(sh, dev)
+    evict = torch.ones(512 << 20 >> 2, dtype=torch.int32, device=dev)
+    with ClockSampler(dev.index or 0) as clk:
+        t = _event_times(lay.step, args.steps, args.warmup, evict)
+        dense = _event_times(lambda: lay.attend(selected=False), args.steps, args.warmup, evict)
+    torch.cuda.synchronize()
+    assert lay.status.item() == 0, f"device status {lay.status.item()}"
+    tile = 2 * BLK * D + 8                     # a block's e4m3 rows and its two scales
+    kv = sh.pairs * sh.k_tot * tile
+    sel = sh.pairs * n_candidates(sh) * KTIL_ROW_BYTES
+    app = sh.pairs * (sh.n_new * (2 * 2 * D + 2 * D) + 2 * KTIL_ROW_BYTES)
+    gbs, frac = _rate(kv + sel + app, t["median_us"], peak)
+    all_kv = sh.pairs * sh.N_b * tile
+    line = {"case": "paged32k", "workload": sh.name + ", paged e4m3 cache",
+            "unit_of_work": "one decode step (page plan + append + select + attention)",
+            "steps_per_s": round(1e6 / t["median_us"], 1), **t, "launches_per_step": 4,
+            "algorithmic_bytes": {"selected_kv": kv, "compressed_keys": sel, "append": app},
+            "achieved_gbs": gbs, "frac_of_measured_hbm": frac, "peak_gbs": peak, "peak_source": src,
+            "attention_over_all_blocks": {**dense, "algorithmic_bytes": all_kv,
+                                          "frac_of_measured_hbm": _rate(all_kv, dense["median_us"], peak)[1]},
+            "roofline": case_roofline("the step's 4 launches (page_plan_kernel, paged_append_kernel, "
+                                      "decode_forecast_kernel<1, false>, paged_attn_kernel)", kv + sel + app,
+                                      t["median_us"], peak, src),
+            "l2": "512 MB read evicts L2 before each step", "clocks": clk.summary(),
+            "cpu_baseline": None if args.no_cpu_baseline else single_layer_oracle(lay, args.case_cpu_seconds)}
+    print(json.dumps(line), flush=True)
+
+
 def contraction_name(args):
     return "tcgen05.mma, tensor-memory accumulators" if getattr(args, "tensor_memory", False) else "mma.sync"
 
@@ -1721,7 +1809,7 @@ def run_refresh_case(args, dev):
 
 
 OTHER_CASES = ("decode128k_b1", "single4k", "append32k", "verify64k", "offload128k", "nsa128k", "prefill32k",
-               "refresh64k")
+               "refresh64k", "paged32k")
 
 
 def run_other_case(args, local_rank):
@@ -1735,6 +1823,8 @@ def run_other_case(args, local_rank):
         run_single_layer_case(args, dev, wl.SINGLE_4K, "single4k")
     elif args.case == "append32k":
         run_single_layer_case(args, dev, wl.LLAMA8B_32K, "append32k")
+    elif args.case == "paged32k":
+        run_paged_case(args, dev)
     elif args.case == "verify64k":
         run_verify_case(args, dev)
     elif args.case == "nsa128k":
@@ -1759,8 +1849,8 @@ def main():
                     help="step: the 80-layer decode step (the bench line); layer: one physical layer, "
                          "kernels serialised and timed alone (for profiling); select: selection only; "
                          "decode128k_b1: the 128K step at B = 1 with all 80 layers resident; "
-                         "single4k / append32k / verify64k / offload128k / nsa128k / prefill32k / refresh64k: "
-                         "the other workloads, one line each")
+                         "single4k / append32k / verify64k / offload128k / nsa128k / prefill32k / refresh64k / "
+                         "paged32k: the other workloads, one line each")
     ap.add_argument("--case-cpu-seconds", type=float, default=3.0,
                     help="other cases: host seconds of oracle work for their cpu_baseline")
     ap.add_argument("--layers", type=int, default=0,
