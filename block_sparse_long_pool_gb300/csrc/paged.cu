@@ -14,6 +14,12 @@ namespace {
 using namespace sp;
 
 // ---------------------------------------------------------------- page plan
+//
+// Three prefix sums over the requests (pages returned, new tokens, pages needed) by one CTA of
+// 1024 threads, then a row's place by arithmetic: no row waits for a table entry that this
+// step writes, since a new page's id follows from the request's prefix and the free list.
+// All latency: a step of 8 requests takes 4.3 us on GB300, back to back in a graph, 512 requests
+// with 16 384 rows 7.2 us, 2^20 rows 9.5 us (12.6 MB stored: 1.9 us at the copy rate).
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanMaxB = 4096;
@@ -332,8 +338,19 @@ __global__ void __launch_bounds__(kRowThreads) page_rows_kernel(const PlanParams
 
 // ---------------------------------------------------------------- append
 
+// One pass over the new rows: they stay in registers between the maximum that gives the scale
+// and the rounding, so 512 B are read and 256 B written a (token, head), the floor.  A CTA
+// takes the keys or the values of one (run, head); the scale is a power of two, so old rows
+// move to a larger one by an exponent shift, which rounds nothing but subnormals, and e4m3
+// loses no precision to it (its precision is relative).  What bounds it is DRAM: 131 072 tokens
+// of 8 heads in 126 us, 6.4 TB/s, 0.95 of the copy rate.  A CTA's life is a chain of three
+// loads (slots, rows, stores); 9 CTAs an SM cover it only with the rows of the CTAs 3 an SM
+// ahead already asked for (162 us without; 2, 4 and 5 ahead: 127 to 128; 8 ahead, whose rows
+// leave L2's sets before they are used: 140 and more).  Keys and values in one CTA of 256
+// threads: 150 us.  Small calls are latency: 8 rows 4.3 us, 256 rows 5.6 us, and the rows of a
+// decode step, runs of one, go to a warp each (18.3 us with a CTA each).
 constexpr int kAppendThreads = 128;
-constexpr int kAhead = 4;       // CTAs an SM ahead whose rows a CTA brings into L2
+constexpr int kAhead = 3;       // CTAs an SM ahead whose rows a CTA brings into L2
 constexpr int kShort = 2;       // rows of a run that one warp appends
 constexpr int kMinExp = -120;   // least exponent of a scale: its reciprocal is a normal fp32 value
 
@@ -606,7 +623,7 @@ __device__ __forceinline__ void append_long(const PagedAppendParams &p, int t, i
 
 // CTA (window, head, K or V): the runs that start in the window.  Of the window's short
 // runs, which a warp appends whole, the K and the V CTA take four in turn.
-__global__ void __launch_bounds__(kAppendThreads, 8) paged_append_kernel(const PagedAppendParams p)
+__global__ void __launch_bounds__(kAppendThreads, 9) paged_append_kernel(const PagedAppendParams p)
 {
     __shared__ float s_amax[4];
     __shared__ __align__(16) float red[8][kD + 4];

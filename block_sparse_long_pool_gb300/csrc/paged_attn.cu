@@ -7,18 +7,31 @@
 // and its state is merged.  So requests of very different lengths load the SMs evenly.  A
 // pair whose items lie in several CTAs is merged by the one that finishes last, in CTA order.
 //
-// Per CTA: warp 4 resolves items to pages, 32 at a time (list -> block table -> scales), and
-// streams their keys and values, a TMA load each; warps 0..3 take whole tiles in turn, each
-// from three 8 KB slots of its own: while it works on one, the next two travel.
-//   S^T = K Q^T and O^T += V^T P^T run on mma.m16n8k16 in f16: every e4m3 value is an f16
-// value, so the tiles are converted without rounding, two elements an instruction.  Q rows
-// are scaled to f16's range by a power of two of their own.  Which 16 of the 128 dims make
-// a k-step, and which rows an m-tile, is free as long as both operands agree: lanes take
-// whole 16-byte chunks of the swizzled tile, without bank conflicts.
+// Per CTA: the last warp resolves items to pages, 32 at a time (list -> block table -> scales),
+// and streams their keys and values, a TMA load of 8 KB each; the others take whole tiles in
+// turn, each from slots of its own: while it works on one half tile, the next travel.  A warp
+// over a whole tile needs 6 shuffles for the row maxima and one rescaling where four warps
+// with 16 tokens each need 24 and four.
+//   S = Q K^T and O += P V run on mma.m16n8k16 in f16: every e4m3 value is an f16 value, so the
+// tiles are converted without rounding, two elements an instruction.  Q rows are scaled to
+// f16's range by a power of two of their own.  Which 16 of the 128 dims make a k-step, and
+// which column of an operand a dim is, is free as long as both operands agree: lanes take
+// whole 16-byte chunks of the swizzled tile, without bank conflicts.  (e4m3 tensor-core
+// products need Q and P in e4m3, in two or three terms; a weight's range does not fit two.)
 //   The scales of a page: ks multiplies its scores.  vs is folded into the weights' exponent,
 // p_o = 2^(s + log2 vs - mo) with a running maximum mo of its own (scores are in log2
 // units), so that a weight rounded to f16 (11 bits) keeps its precision whatever the pages'
 // scales are; the row sum l uses the fp32 weights 2^(s - m).
+//
+// What bounds it.  The tiles' stream in the middle, latency at both ends.  On GB300, back to back
+// in a graph: 537 MB (32K tokens x 8 requests x 8 KV heads, G = 4) in 91.5 us, 5.9 TB/s, 0.86 of
+// the copy rate; of these about 3.5 us pass before the first tile is there (lengths, table,
+// load: three round trips), and 4 us after the last one in the merge of the pairs that the
+// CTAs share.  70.6 MB of selected blocks (64 pairs x 67) in 22.4 us, 2.1 MB (one request of 4K
+// tokens, 2 KV heads) in 12.6 us: those ends.  64 requests of 1 to 16K tokens in 41 us (0.59):
+// each part of a pair ends with its warps waiting for one another.  A tile takes a warp about
+// 2900 cycles at G <= 8 and 3900 at G = 16 (537 MB in 105 us, 0.75): the conversions' half-rate
+// instructions (cvt, prmt, shift) and the products' latency.
 #include <limits.h>
 #include <math.h>
 
@@ -35,11 +48,19 @@ constexpr int kStride = kD + 4;                   // floats a row of the warps' 
 constexpr int kMeta = 64;                         // item and part records: 32 being written + the ring's
 constexpr float kWeightBits = 12.f;               // weights reach 2^12: f16 holds them down to 2^-24
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr int kMinItems = 6;                      // a CTA's range at least
-constexpr int kPairCost = 7;                      // what a pair costs beside its items, in items
-constexpr int kWhole = 12;                        // pairs of up to so many items stay with one CTA
-constexpr int kDirect = 32;                       // partial states that are merged in one go
-constexpr int kGroup = 16;                        // CTAs whose states are merged first where there are more
+// How the list is cut, in items (tiles).  Measured back to back in a graph:
+//   a range at least: 1 x 2 pairs of 64 tiles 11.7 us (3: 11.9, 6: 12.9, 12: 14.9), 8 pairs of 16
+//   tiles 10.7 us (6: 12.1): a merge over more CTAs against more tiles a warp;
+constexpr int kMinItems = 4;
+//   what a pair costs beside its items: 64 requests of 1 to 16K tokens 41 us (2: 60, 4: 45, 10: 41.4);
+constexpr int kPairCost = 7;
+//   pairs of up to so many items stay with one CTA: 48 pairs of up to 4 tiles 8.8 us (0: 10.5), 512
+//   of up to 8 tiles 16.8 us (0: 18.4), 8 of 16 tiles 12.1 us where 16 makes it 14.4;
+constexpr int kWhole = 12;
+//   partial states that one CTA merges in one go, and the neighbours whose states are merged first
+//   where there are more (38 states: 55 us with groups of 12, 58.8 with 16, 60.2 with 32).
+constexpr int kDirect = 32;
+constexpr int kGroup = 12;
 
 // What the warp that takes an item needs to know of it.
 struct Item {
@@ -754,7 +775,7 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
 {
     constexpr int kWarps = warps<NT>(), kSlots = slots<NT>(), kThreads = (kWarps + 1) * 32;
     using S = Smem<NT>;
-    static_assert(kDirect <= 32, "a lane holds a state's statistics");
+    static_assert(kDirect <= 32 && kGroup <= kDirect, "a lane holds a state's statistics");
     extern __shared__ uint8_t smem_raw[];
     __shared__ int s_sum[kWarps + 1], s_pair, s_n, s_start, s_last;
     const uint32_t base_s = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -1090,17 +1111,23 @@ bool sizes_ok(int B, int H_q, int H_kv)
            static_cast<long long>(B) * H_kv <= 65535;
 }
 
-// Workspace: an arrival count a pair, two a group of CTAs, then two partial states a CTA.
-size_t counter_bytes(long long pairs, int sm_count)
+// CTAs of a launch: two an SM, and no more groups than one CTA merges in one go.
+int grid_ctas(int sm_count)
 {
-    const long long groups = (kCtasPerSm * sm_count + kGroup - 1) / kGroup;
-    return (static_cast<size_t>(pairs + 2 * groups) * sizeof(int) + 255) & ~static_cast<size_t>(255);
+    const int most = kGroup * (kDirect - 1);
+    return kCtasPerSm * sm_count < most ? kCtasPerSm * sm_count : most;
 }
 
-size_t workspace_bytes_of(int B, int H_q, int H_kv, int sm_count)
+// Workspace: an arrival count a pair, two a group of CTAs, then two partial states a CTA.
+size_t counter_bytes(long long pairs, int ctas)
+{
+    return (static_cast<size_t>(pairs + 2 * ((ctas + kGroup - 1) / kGroup)) * sizeof(int) + 255) & ~static_cast<size_t>(255);
+}
+
+size_t workspace_bytes_of(int B, int H_q, int H_kv, int ctas)
 {
     const size_t part = H_q / H_kv <= 8 ? part_floats<1>() : part_floats<2>();
-    return counter_bytes(static_cast<long long>(B) * H_kv, sm_count) + 2ull * kCtasPerSm * sm_count * part * sizeof(float);
+    return counter_bytes(static_cast<long long>(B) * H_kv, ctas) + 2ull * ctas * part * sizeof(float);
 }
 
 template <int NT>
@@ -1112,7 +1139,7 @@ int launch(const PagedAttnParams &p, const CUtensorMap &map, const sp_host::Devi
     if (rc != SPARSE_OK)
         return rc;
     return sp_host::cuda_status(
-        launch_pdl(kern, dim3(static_cast<unsigned>(kCtasPerSm * dev.sm_count)), (warps<NT>() + 1) * 32, Smem<NT>::kBytes, stream,
+        launch_pdl(kern, dim3(static_cast<unsigned>(grid_ctas(dev.sm_count))), (warps<NT>() + 1) * 32, Smem<NT>::kBytes, stream,
                    map, p),
         name);
 }
@@ -1124,7 +1151,7 @@ extern "C" SPARSE_API size_t sparse_paged_decode_attn_f8_workspace_size(int B, i
     sp_host::DeviceInfo dev;
     if (!sizes_ok(B, H_q, H_kv) || sp_host::device_info(&dev) != SPARSE_OK)
         return 0;
-    return workspace_bytes_of(B, H_q, H_kv, dev.sm_count);
+    return workspace_bytes_of(B, H_q, H_kv, grid_ctas(dev.sm_count));
 }
 
 extern "C" SPARSE_API int sparse_paged_decode_attn_f8(const uint16_t *Q, const uint8_t *kv_pages, const float *kv_scale,
@@ -1180,7 +1207,7 @@ extern "C" SPARSE_API int sparse_paged_decode_attn_f8(const uint16_t *Q, const u
                             lse,
                             status,
                             static_cast<int *>(workspace),
-                            reinterpret_cast<float *>(static_cast<char *>(workspace) + counter_bytes(static_cast<long long>(B) * H_kv, dev.sm_count)),
+                            reinterpret_cast<float *>(static_cast<char *>(workspace) + counter_bytes(static_cast<long long>(B) * H_kv, grid_ctas(dev.sm_count))),
                             s * 1.44269504088896340736f,   // log2(e): scores are exponentiated base 2
                             n_pages,
                             max_blocks,

@@ -553,7 +553,8 @@ SPARSE_API int sparse_gather_offloaded(const uint16_t *k_host, const uint16_t *v
  * selectors run on it unchanged.
  *   page         64 tokens of every KV head: kv_pages [n_pages][H_kv][2][64][128] e4m3
  *                (0: keys, 1: values), one byte an element.
- *   kv_scale     [n_pages][H_kv][2] fp32: the element's value is e4m3 * scale.
+ *   kv_scale     [n_pages][H_kv][2] fp32, finite and not negative: the element's value is
+ *                e4m3 * scale.
  *   block table  [B][max_blocks] int32: the page that holds block j (tokens 64 j ..
  *                64 j + 63) of request b.
  *   slot         64 * page + row: the place of one token's rows.
@@ -649,7 +650,9 @@ SPARSE_API int sparse_paged_append_f8(uint8_t *kv_pages, float *kv_scale, int n_
  * nothing.  A negative block or one past max_blocks, a page outside [0, n_pages), a count
  * outside [0, k_tot] (clamped) and a length past 64 max_blocks (clamped) are reported as
  * SPARSE_ERR_BAD_INDEX; such a block is left out.  The result does not depend on timing.
- * G = H_q / H_kv <= 16, B * H_kv <= 65535, k_tot <= 2^25.
+ * G = H_q / H_kv <= 16, B * H_kv <= 65535, n_pages and k_tot <= 2^25, max_blocks < 2^25,
+ * n_pages * H_kv < 2^30, and B * H_kv * (k_tot + 7), or (max_blocks + 7) where every block
+ * is attended over, below 2^31.
  */
 SPARSE_API int sparse_paged_decode_attn_f8(const uint16_t *Q, const uint8_t *kv_pages, const float *kv_scale,
                                            int n_pages, const int *block_table, int max_blocks,
