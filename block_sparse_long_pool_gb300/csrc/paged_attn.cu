@@ -127,7 +127,7 @@ struct PagedAttnParams {
     uint16_t *O;
     float *lse;
     int *status;
-    int *arrivals;     // [pairs], then [2 * groups of CTAs]; zero between calls
+    int *arrivals;     // [2 * kDirect] of groups of CTAs, then [pairs]; zero between calls
     float *parts;      // [2 * CTAs][part_floats]
     float scale_log2;
     int n_pages;
@@ -659,11 +659,11 @@ __device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const Stat
         int first = c0, n = c1 - c0 + 1, step = 1;
         if (level == 0) {
             // at most two such pairs meet a group: one from before it, one that starts in it
-            counter = p.arrivals + p.B * p.H_kv + 2 * g + (c0 < g * kGroup ? 0 : 1);
+            counter = p.arrivals + 2 * g + (c0 < g * kGroup ? 0 : 1);
             first = max(c0, g * kGroup);
             n = min(c1, g * kGroup + kGroup - 1) - first + 1;
         } else {
-            counter = p.arrivals + of.pair;
+            counter = p.arrivals + 2 * kDirect + of.pair;
             if (grouped) {
                 n = c1 / kGroup - g0 + 1;
                 step = kGroup;
@@ -1105,10 +1105,12 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
     }
 }
 
+constexpr int kMaxPairs = 65535;
+
 bool sizes_ok(int B, int H_q, int H_kv)
 {
     return B >= 1 && H_kv >= 1 && H_q >= H_kv && H_q % H_kv == 0 && H_q / H_kv <= 16 &&
-           static_cast<long long>(B) * H_kv <= 65535;
+           static_cast<long long>(B) * H_kv <= kMaxPairs;
 }
 
 // CTAs of a launch: two an SM, and no more groups than one CTA merges in one go.
@@ -1118,16 +1120,14 @@ int grid_ctas(int sm_count)
     return kCtasPerSm * sm_count < most ? kCtasPerSm * sm_count : most;
 }
 
-// Workspace: an arrival count a pair, two a group of CTAs, then two partial states a CTA.
-size_t counter_bytes(long long pairs, int ctas)
-{
-    return (static_cast<size_t>(pairs + 2 * ((ctas + kGroup - 1) / kGroup)) * sizeof(int) + 255) & ~static_cast<size_t>(255);
-}
+// Workspace: the arrival counts, at the same places whatever the sizes of a call, so that calls
+// of different sizes may take turns with it; then two partial states a CTA.
+constexpr size_t kCounterBytes = (kMaxPairs + 1 + 2 * kDirect) * sizeof(int);
+static_assert(kCounterBytes % 16 == 0, "the states are read 16 bytes at a time");
 
-size_t workspace_bytes_of(int B, int H_q, int H_kv, int ctas)
+size_t workspace_bytes_of(int G, int ctas)
 {
-    const size_t part = H_q / H_kv <= 8 ? part_floats<1>() : part_floats<2>();
-    return counter_bytes(static_cast<long long>(B) * H_kv, ctas) + 2ull * ctas * part * sizeof(float);
+    return kCounterBytes + 2ull * ctas * (G <= 8 ? part_floats<1>() : part_floats<2>()) * sizeof(float);
 }
 
 template <int NT>
@@ -1151,7 +1151,7 @@ extern "C" SPARSE_API size_t sparse_paged_decode_attn_f8_workspace_size(int B, i
     sp_host::DeviceInfo dev;
     if (!sizes_ok(B, H_q, H_kv) || sp_host::device_info(&dev) != SPARSE_OK)
         return 0;
-    return workspace_bytes_of(B, H_q, H_kv, grid_ctas(dev.sm_count));
+    return workspace_bytes_of(H_q / H_kv, grid_ctas(dev.sm_count));
 }
 
 extern "C" SPARSE_API int sparse_paged_decode_attn_f8(const uint16_t *Q, const uint8_t *kv_pages, const float *kv_scale,
@@ -1207,7 +1207,7 @@ extern "C" SPARSE_API int sparse_paged_decode_attn_f8(const uint16_t *Q, const u
                             lse,
                             status,
                             static_cast<int *>(workspace),
-                            reinterpret_cast<float *>(static_cast<char *>(workspace) + counter_bytes(static_cast<long long>(B) * H_kv, grid_ctas(dev.sm_count))),
+                            reinterpret_cast<float *>(static_cast<char *>(workspace) + kCounterBytes),
                             s * 1.44269504088896340736f,   // log2(e): scores are exponentiated base 2
                             n_pages,
                             max_blocks,

@@ -644,7 +644,8 @@ SPARSE_API int sparse_paged_append_f8(uint8_t *kv_pages, float *kv_scale, int n_
  *                lse = -inf.
  *   workspace    sparse_paged_decode_attn_f8_workspace_size() bytes, 16-byte aligned, all
  *                zero before the first call that uses it; every call leaves its counters
- *                zero again.  Calls that share a workspace must not run at the same time.
+ *                zero again.  Calls of any sizes may share a workspace that is large enough
+ *                for each, but not at the same time.
  * Rows past seq_len in a request's last page are never used, whatever bytes they hold.
  * Listed blocks are expected to be distinct.  A block past the request's length adds
  * nothing.  A negative block or one past max_blocks, a page outside [0, n_pages), a count

@@ -488,6 +488,70 @@ def test_attn_is_repeatable_and_runs_on_another_stream():
         assert torch.equal(x.O, first[0]) and torch.equal(x.lse, first[1])
 
 
+def test_attn_calls_of_different_sizes_share_a_workspace():
+    rng = np.random.default_rng(41)
+    shared = Attn(3, 48, 3)   # the largest workspace: more than 8 rows a pair
+    for lens, H, G in (([9000, 1, 700], 3, 16), ([20000], 1, 4), ([300] * 3, 2, 8), ([5000, 4000], 2, 16), ([40000], 2, 1),
+                       ([9000, 1, 700], 3, 16)):
+        c, table, Q = attn_case(rng, lens, H, G)
+        a = Attn(len(lens), H * G, H)
+        a.ws = shared.ws
+        a.call(Q, c, i32(table), i32(lens))
+        torch.cuda.synchronize()
+        ref.assert_attn(a.O, a.lse, ref.attn(ref.f64(Q), ref.f8_values(c.pages), ref.f64(c.scale), table, lens), max(lens))
+        assert a.status.item() == 0
+
+
+def test_attn_lists_of_nothing():
+    """Every listed block outside, or past the length: no tokens, but a row that is written."""
+    rng = np.random.default_rng(43)
+    c, table, Q = attn_case(rng, [100, 100, 5000], 2, 5, extra_blocks=0)
+    idx = np.tile(np.arange(70, dtype=np.int32), (3, 2, 1))
+    idx[0], idx[1] = -1, np.arange(2, 72)   # request 1: past its length, or (past 78 blocks) outside
+    a = Attn(3, 10, 2)
+    a.call(Q, c, i32(table), i32([100, 100, 0]), i32(idx), i32(np.full((3, 2), 70)))
+    torch.cuda.synchronize()
+    assert (a.O == 0).all() and torch.isinf(a.lse).all() and (a.lse < 0).all()
+    assert a.status.item() == binding.SPARSE_ERR_BAD_INDEX
+
+
+def test_attn_a_query_of_nan_stays_in_its_row():
+    rng = np.random.default_rng(44)
+    for G in (4, 16):
+        c, table, Q = attn_case(rng, [700], 2, G)
+        a = Attn(1, 2 * G, 2)
+        Q[0, 2, 17] = float("nan")
+        a.call(Q, c, i32(table), i32([700]))
+        torch.cuda.synchronize()
+        assert torch.isnan(a.O[0, 2]).all()
+        keep = [r for r in range(2 * G) if r != 2]
+        want = ref.attn(ref.f64(Q[:, keep]).reshape(1, -1, D), ref.f8_values(c.pages)[:, :1], ref.f64(c.scale)[:, :1], table, [700])
+        ref.assert_attn(a.O[:, keep[:G - 1]], a.lse[:, keep[:G - 1]], [x[:, :G - 1] for x in want], 700)
+
+
+def test_attn_captured_with_lengths_that_grow():
+    """One captured call, replayed as the lengths grow over page ends and a request appears,
+    with eager calls on another workspace between."""
+    rng = np.random.default_rng(45)
+    c, table, Q = attn_case(rng, [2600, 130, 64], 2, 6)
+    a, eager = Attn(3, 12, 2), Attn(3, 12, 2)
+    t, lens = i32(table), i32([2500, 60, 0])
+    a.call(Q, c, t, lens)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        a.call(Q, c, t, lens)
+    pages = ref.f8_values(c.pages)
+    for now in ([2500, 60, 0], [2560, 64, 1], [2561, 65, 63], [2600, 130, 64], [0, 0, 0], [1, 129, 2]):
+        lens.copy_(i32(now))
+        g.replay()
+        eager.call(Q, c, t, lens)
+        torch.cuda.synchronize()
+        want = ref.attn(ref.f64(Q), pages, ref.f64(c.scale), table, now)
+        for x in (a, eager):
+            ref.assert_attn(x.O, x.lse, want, 2600, str(now))
+
+
 def test_attn_many_calls_of_a_full_grid():
     """Every SM busy, ranges that begin and end inside a pair's list: the same bits each time,
     equal to the plain implementation for a few pairs."""
@@ -514,6 +578,50 @@ def test_attn_many_calls_of_a_full_grid():
         want = ref.attn(ref.f64(Q[rows]), ref.f8_values(pages), ref.f64(scale), table[rows].cpu().numpy(),
                         lens[rows].cpu().numpy(), idx[rows].cpu().numpy(), count[rows].cpu().numpy())
         ref.assert_attn(a.O[rows], a.lse[rows], want, k * BLK)
+
+
+# ---------------------------------------------------------------- refusals of the binding
+
+
+def test_binding_refusals():
+    s = Plan([1, 2], np.full((2, 3), 0, np.int32), np.arange(6), 6, 4)
+    for name, bad, error in (("seq_len", s.seq_len.long(), TypeError), ("n_new", filled(3, 0), ValueError),
+                             ("table", s.table.t(), ValueError), ("slot", s.slot.cpu(), ValueError),
+                             ("status", torch.zeros(2, dtype=torch.int32, device=DEV), ValueError), ("cu", filled(2), ValueError),
+                             ("free", None, TypeError)):
+        keep = getattr(s, name)
+        setattr(s, name, bad)
+        with pytest.raises(error):
+            s.call()
+        setattr(s, name, keep)
+    c = Cache(np.random.default_rng(1), 2, 2, 1, 1)
+    k, v = rows(np.random.default_rng(1), 3, 2, True)
+    wide = torch.zeros((3, 2, 2 * D), dtype=torch.bfloat16, device=DEV)
+    for bad, error in ((k.float(), TypeError), (k[:2], ValueError), (k.transpose(0, 1).contiguous().transpose(0, 1), ValueError),
+                       (wide[:, :, ::2], ValueError), (wide[:, :, :D], ValueError), (None, TypeError), (k.cpu(), ValueError)):
+        with pytest.raises(error):
+            c.append(bad, v, [0, 1, 2])
+        with pytest.raises(error):
+            c.append(k, bad, [0, 1, 2])
+    with pytest.raises(ValueError, match="tok_req"):
+        binding.sparse_paged_append_f8(c.pages, c.scale, k, v, i32([0, 1, 2]), c.ktil)
+    with pytest.raises(TypeError):
+        binding.sparse_paged_append_f8(c.pages.view(torch.uint8), c.scale, k, v, i32([0, 1, 2]))
+    with pytest.raises(binding.SparsePoolError, match="strides"):   # rows that overlap
+        flat = torch.zeros(3 * 256, dtype=torch.bfloat16, device=DEV)
+        c.append(flat.as_strided((3, 2, D), (128, 128, 1)), v, [0, 1, 2])
+    a = Attn(1, 8, 2)
+    Q, t, n = torch.zeros((1, 8, D), dtype=torch.bfloat16, device=DEV), i32([[0]]), i32([5])
+    with pytest.raises(binding.SparsePoolError, match="workspace"):
+        binding.sparse_paged_decode_attn_f8(Q, c.pages, c.scale, t, n, a.O, a.ws[:4096])
+    with pytest.raises(ValueError, match="count"):
+        binding.sparse_paged_decode_attn_f8(Q, c.pages, c.scale, t, n, a.O, a.ws, blk_idx=i32([[[0], [0]]]))
+    for bad in ({"Q": Q.float()}, {"Q": Q[:, :7]}, {"seq_len": n[:0]}, {"O": a.O.transpose(1, 2)}, {"lse": a.lse[:, :4]},
+                {"block_table": t.long()}, {"workspace": a.ws.cpu()}, {"kv_scale": c.scale.half()}):
+        args = {**dict(Q=Q, kv_pages=c.pages, kv_scale=c.scale, block_table=t, seq_len=n, O=a.O, workspace=a.ws), **bad}
+        with pytest.raises((TypeError, ValueError)):
+            binding.sparse_paged_decode_attn_f8(**args)
+    torch.cuda.synchronize()
 
 
 # ---------------------------------------------------------------- together
