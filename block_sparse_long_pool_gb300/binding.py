@@ -4,11 +4,14 @@ Argument marshalling only: every function checks dtype/device/shape/contiguity o
 the tensors it is given, passes their data pointers and the current CUDA stream to
 the C entry point of the same name, and raises ``SparsePoolError`` on a non-zero
 status.  Every step of the computation runs in the CUDA kernels; there is no CPU
-fallback, and a missing library raises at the first call.
+fallback, and a missing library raises at the first call.  The paged cache's three calls
+are marshalled by csrc/marshal.c, the same way: they are short enough that checking their
+tensors in Python takes longer than they do.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -16,8 +19,10 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libsparsepool.so")
+MARSHAL_PATH = os.path.join(_PKG, "_marshal.so")
 _lock = threading.Lock()
 _lib = None
+_marshal = None   # csrc/marshal.c, which passes the paged cache's tensors on
 
 D = 128
 BLK = 64
@@ -84,18 +89,26 @@ class SparsePoolError(RuntimeError):
 
 def load(path: str = LIB_PATH):
     """Load libsparsepool.so (built in-tree by ``block_sparse_long_pool_gb300.build``)."""
-    global _lib
+    global _lib, _marshal
     with _lock:
         if _lib is not None:
             return _lib
-        if not os.path.exists(path):
-            raise RuntimeError(f"{path} is not built; run `python -m block_sparse_long_pool_gb300.build` "
-                               "(there is no CPU fallback)")
+        for need in (path, MARSHAL_PATH):
+            if not os.path.exists(need):
+                raise RuntimeError(f"{need} is not built; run `python -m block_sparse_long_pool_gb300.build` "
+                                   "(there is no CPU fallback)")
         lib = ctypes.CDLL(path)
         for name, (res, args) in SIGNATURES.items():
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args
+        spec = importlib.util.spec_from_file_location("_marshal", MARSHAL_PATH)
+        marshal = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(marshal)
+        marshal.setup(torch.int32, torch.float32, torch.bfloat16, torch.float8_e4m3fn, torch.uint8,
+                      *(ctypes.cast(getattr(lib, f"sparse_{name}"), ctypes.c_void_p).value
+                        for name in ("page_plan", "paged_append_f8", "paged_decode_attn_f8")))
+        _marshal = marshal
         _lib = lib
         return lib
 
@@ -479,39 +492,35 @@ def sparse_prefill_select(F, ktil, seq_len, n_init: int, n_local: int, k: int, i
 _F8 = torch.float8_e4m3fn
 
 
-# The calls of this cache are short: a decode step's plan or append takes a few microseconds
-# on the device.  So their arguments are checked in one pass of plain comparisons, and what
-# is wrong is looked for (_explain) only when something is.
-
-
-def _sound(idx, dtype, shape, *tensors) -> bool:
-    """Whether every tensor has this type and shape and is contiguous on device ``idx``."""
-    try:
-        for t in tensors:
-            if t.dtype is not dtype or t.shape != shape or t.get_device() != idx or not t.is_contiguous():
-                return False
-    except AttributeError:   # not a tensor
-        return False
-    return True
+# The calls of this cache are short: a decode step's plan or append takes 4 to 6 us on the
+# device.  So their tensors are checked and passed on by csrc/marshal.c; what is wrong is
+# looked for here, only when something is.
 
 
 def _explain(idx, dtype, shape, **tensors):
-    """Raises for the first tensor that is not as _sound wants it."""
+    """Raises for the first tensor that is not of this type and shape, contiguous, on device ``idx``."""
     for name, t in tensors.items():
         _need(t, name, dtype, shape=shape)
         if t.get_device() != idx:
             raise ValueError(f"{name} is on {t.device}, expected device {idx}")
 
 
-def _call(fn, name, idx, stream, *args):
-    """The C entry point on device ``idx``, which need not be the current one."""
+def _passed(name, idx, stream, *args) -> bool:
+    """Calls ``name`` on device ``idx``, which need not be the current one; false where marshal.c
+    refused a tensor, and nothing was called."""
+    if _lib is None:
+        load()
+    call = getattr(_marshal, name)
     if idx == torch._C._cuda_getDevice():
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(idx) if stream is None else stream.cuda_stream)
+        rc = call(idx, torch._C._cuda_getCurrentRawStream(idx) if stream is None else stream.cuda_stream, *args)
     else:
         with torch.cuda.device(idx):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(idx) if stream is None else stream.cuda_stream)
+            rc = call(idx, torch._C._cuda_getCurrentRawStream(idx) if stream is None else stream.cuda_stream, *args)
+    if rc is None:
+        return False
     if rc != SPARSE_OK:
-        _check(rc, name)
+        _check(rc, "sparse_" + name)
+    return True
 
 
 def _device_index(t, name) -> int:
@@ -522,10 +531,16 @@ def _device_index(t, name) -> int:
     return t.get_device()
 
 
-def _tensors(*named):
-    for name, t in named:
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
+def _shape(t, name, dims):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {dims} extents")
+    return t.shape
+
+
+def _refused(name):
+    return ValueError(f"{name}: an extent does not fit 32 bits")
 
 
 def sparse_page_plan(seq_len, n_new, block_table, free_pages, n_free, cu_new, start, seq_len_out, n_free_out, slot_map,
@@ -536,30 +551,22 @@ def sparse_page_plan(seq_len, n_new, block_table, free_pages, n_free, cu_new, st
     Writes cu_new [B + 1], start [B] (-1: not granted), seq_len_out [B], n_free_out [1] (the
     last two may be seq_len and n_free themselves) and slot_map, tok_req, tok_pos [n_tok]."""
     idx = _device_index(block_table, "block_table")
-    _tensors(("free_pages", free_pages), ("slot_map", slot_map))
+    if _passed("page_plan", idx, stream, seq_len, n_new, block_table, free_pages, n_free, cu_new, start, seq_len_out,
+               n_free_out, slot_map, tok_req, tok_pos, status):
+        return
     i32 = torch.int32
-    B, max_blocks = block_table.shape
-    n_pages, n_tok = free_pages.numel(), slot_map.numel()
-    per_request, one, rows = (B,), (1,), (n_tok,)
-    if not (_sound(idx, i32, per_request, seq_len, n_new, start, seq_len_out)
-            and _sound(idx, i32, rows, slot_map, tok_req, tok_pos) and _sound(idx, i32, one, n_free, n_free_out)
-            and _sound(idx, i32, (B, max_blocks), block_table) and _sound(idx, i32, (n_pages,), free_pages)
-            and _sound(idx, i32, (B + 1,), cu_new) and (status is None or _sound(idx, i32, one, status))):
-        _explain(idx, i32, per_request, seq_len=seq_len, n_new=n_new, start=start, seq_len_out=seq_len_out)
-        _explain(idx, i32, rows, slot_map=slot_map, tok_req=tok_req, tok_pos=tok_pos)
-        _explain(idx, i32, one, n_free=n_free, n_free_out=n_free_out)
-        _explain(idx, i32, (B, max_blocks), block_table=block_table)
-        _explain(idx, i32, (n_pages,), free_pages=free_pages)
-        _explain(idx, i32, (B + 1,), cu_new=cu_new)
-        _explain(idx, i32, one, status=status)
-    _call((_lib or load()).sparse_page_plan, "sparse_page_plan", idx, stream, seq_len.data_ptr(), n_new.data_ptr(), B,
-          block_table.data_ptr(), max_blocks, free_pages.data_ptr(), n_pages, n_free.data_ptr(), cu_new.data_ptr(),
-          start.data_ptr(), seq_len_out.data_ptr(), n_free_out.data_ptr(), slot_map.data_ptr(), tok_req.data_ptr(),
-          tok_pos.data_ptr(), n_tok, None if status is None else status.data_ptr())
+    B, max_blocks = _shape(block_table, "block_table", 2)
+    _explain(idx, i32, (B, max_blocks), block_table=block_table)
+    _explain(idx, i32, (B,), seq_len=seq_len, n_new=n_new, start=start, seq_len_out=seq_len_out)
+    _explain(idx, i32, (1,), n_free=n_free, n_free_out=n_free_out, **({} if status is None else {"status": status}))
+    _explain(idx, i32, (B + 1,), cu_new=cu_new)
+    _explain(idx, i32, tuple(_shape(free_pages, "free_pages", 1)), free_pages=free_pages)
+    _explain(idx, i32, tuple(_shape(slot_map, "slot_map", 1)), slot_map=slot_map, tok_req=tok_req, tok_pos=tok_pos)
+    raise _refused("sparse_page_plan")
 
 
-def _token_stride(t, name, idx, n_tok, H_kv):
-    """Token stride of k_new / v_new [n_tok][H_kv][128], whose tokens may be apart."""
+def _explain_rows(t, name, idx, n_tok, H_kv):
+    """k_new / v_new [n_tok][H_kv][128], whose tokens may be apart."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not torch.bfloat16:
@@ -568,10 +575,9 @@ def _token_stride(t, name, idx, n_tok, H_kv):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n_tok, H_kv, D)}")
     if t.get_device() != idx:
         raise ValueError(f"{name} is on {t.device}, expected device {idx}")
-    step, head, dim = t.stride()
+    _, head, dim = t.stride()
     if dim != 1 or (head != D and H_kv > 1):
         raise ValueError(f"{name}: the values of a token must be contiguous")
-    return step if n_tok > 1 else H_kv * D   # one token: its stride is not used
 
 
 def sparse_paged_append_f8(kv_pages, kv_scale, k_new, v_new, slot_map, ktil=None, tok_req=None, tok_pos=None,
@@ -581,35 +587,25 @@ def sparse_paged_append_f8(kv_pages, kv_scale, k_new, v_new, slot_map, ktil=None
     (torch.float8_e4m3fn), with kv_scale [n_pages][H_kv][2] fp32; with ktil
     [B][H_kv][N_cap][128], tok_req and tok_pos [n_tok], update the compressed keys."""
     idx = _device_index(kv_pages, "kv_pages")
-    _tensors(("slot_map", slot_map))
-    n_pages, H_kv = kv_pages.shape[:2]
-    n_tok = slot_map.numel()
-    i32, f32, rows = torch.int32, torch.float32, (n_tok,)
-    ks, vs = _token_stride(k_new, "k_new", idx, n_tok, H_kv), _token_stride(v_new, "v_new", idx, n_tok, H_kv)
-    pages, scales, one = (n_pages, H_kv, 2, BLK, D), (n_pages, H_kv, 2), (1,)
-    B = N_cap = 0
-    kt = req = pos = st = None
-    if not (_sound(idx, _F8, pages, kv_pages) and _sound(idx, f32, scales, kv_scale) and _sound(idx, i32, rows, slot_map)
-            and (status is None or _sound(idx, i32, one, status))):
-        _explain(idx, _F8, pages, kv_pages=kv_pages)
-        _explain(idx, f32, scales, kv_scale=kv_scale)
-        _explain(idx, i32, rows, slot_map=slot_map)
-        _explain(idx, i32, one, status=status)
+    if ktil is not None and (tok_req is None or tok_pos is None):
+        raise ValueError("ktil needs tok_req and tok_pos")
+    if _passed("paged_append_f8", idx, stream, kv_pages, kv_scale, k_new, v_new, slot_map, ktil, tok_req, tok_pos, status):
+        return
+    i32, f32 = torch.int32, torch.float32
+    n_pages, H_kv = _shape(kv_pages, "kv_pages", 5)[:2]
+    (n_tok,) = _shape(slot_map, "slot_map", 1)
+    _explain(idx, _F8, (n_pages, H_kv, 2, BLK, D), kv_pages=kv_pages)
+    _explain(idx, f32, (n_pages, H_kv, 2), kv_scale=kv_scale)
+    _explain_rows(k_new, "k_new", idx, n_tok, H_kv)
+    _explain_rows(v_new, "v_new", idx, n_tok, H_kv)
+    _explain(idx, i32, (n_tok,), slot_map=slot_map)
     if ktil is not None:
-        if tok_req is None or tok_pos is None:
-            raise ValueError("ktil needs tok_req and tok_pos")
-        _tensors(("ktil", ktil))
-        B, _, N_cap, _ = ktil.shape
-        keys = (B, H_kv, N_cap, D)
-        if not (_sound(idx, f32, keys, ktil) and _sound(idx, i32, rows, tok_req, tok_pos)):
-            _explain(idx, f32, keys, ktil=ktil)
-            _explain(idx, i32, rows, tok_req=tok_req, tok_pos=tok_pos)
-        kt, req, pos = ktil.data_ptr(), tok_req.data_ptr(), tok_pos.data_ptr()
+        B, _, N_cap, _ = _shape(ktil, "ktil", 4)
+        _explain(idx, f32, (B, H_kv, N_cap, D), ktil=ktil)
+        _explain(idx, i32, (n_tok,), tok_req=tok_req, tok_pos=tok_pos)
     if status is not None:
-        st = status.data_ptr()
-    _call((_lib or load()).sparse_paged_append_f8, "sparse_paged_append_f8", idx, stream, kv_pages.data_ptr(),
-          kv_scale.data_ptr(), n_pages, H_kv, k_new.data_ptr(), v_new.data_ptr(), ks, vs, slot_map.data_ptr(), n_tok, kt, B,
-          N_cap, req, pos, st)
+        _explain(idx, i32, (1,), status=status)
+    raise _refused("sparse_paged_append_f8")
 
 
 def sparse_paged_decode_attn_f8_workspace_size(B: int, H_q: int, H_kv: int) -> int:
@@ -630,39 +626,27 @@ def sparse_paged_decode_attn_f8(Q, kv_pages, kv_scale, block_table, seq_len, O, 
     every block of each request's seq_len [B] tokens, or the logical blocks blk_idx
     [B][H_kv][k_tot] with count [B][H_kv]."""
     idx = _device_index(kv_pages, "kv_pages")
-    _tensors(("Q", Q), ("block_table", block_table), ("workspace", workspace))
-    n_pages, H_kv = kv_pages.shape[:2]
-    B, max_blocks = block_table.shape
-    H_q = Q.shape[1]
+    if blk_idx is not None and count is None:
+        raise ValueError("blk_idx needs count")
+    if _passed("paged_decode_attn_f8", idx, stream, Q, kv_pages, kv_scale, block_table, seq_len, O, workspace, blk_idx,
+               count, lse, scale, status):
+        return
     i32, f32, b16 = torch.int32, torch.float32, torch.bfloat16
-    ws_bytes = workspace.numel()
-    pages, scales, heads, table = (n_pages, H_kv, 2, BLK, D), (n_pages, H_kv, 2), (B, H_q, D), (B, max_blocks)
-    if not (_sound(idx, _F8, pages, kv_pages) and _sound(idx, f32, scales, kv_scale) and _sound(idx, b16, heads, Q, O)
-            and _sound(idx, i32, table, block_table) and _sound(idx, i32, (B,), seq_len)
-            and _sound(idx, torch.uint8, (ws_bytes,), workspace) and (lse is None or _sound(idx, f32, (B, H_q), lse))
-            and (status is None or _sound(idx, i32, (1,), status))):
-        _explain(idx, _F8, pages, kv_pages=kv_pages)
-        _explain(idx, f32, scales, kv_scale=kv_scale)
-        _explain(idx, b16, heads, Q=Q, O=O)
-        _explain(idx, i32, table, block_table=block_table)
-        _explain(idx, i32, (B,), seq_len=seq_len)
-        _explain(idx, torch.uint8, (ws_bytes,), workspace=workspace)
-        if lse is not None:
-            _explain(idx, f32, (B, H_q), lse=lse)
-        _explain(idx, i32, (1,), status=status)
-    k_tot = 0
-    blocks = counts = None
+    n_pages, H_kv = _shape(kv_pages, "kv_pages", 5)[:2]
+    B, max_blocks = _shape(block_table, "block_table", 2)
+    H_q = _shape(Q, "Q", 3)[1]
+    _explain(idx, _F8, (n_pages, H_kv, 2, BLK, D), kv_pages=kv_pages)
+    _explain(idx, f32, (n_pages, H_kv, 2), kv_scale=kv_scale)
+    _explain(idx, b16, (B, H_q, D), Q=Q, O=O)
+    _explain(idx, i32, (B, max_blocks), block_table=block_table)
+    _explain(idx, i32, (B,), seq_len=seq_len)
+    _explain(idx, torch.uint8, tuple(_shape(workspace, "workspace", 1)), workspace=workspace)
     if blk_idx is not None:
-        if count is None:
-            raise ValueError("blk_idx needs count")
-        _tensors(("blk_idx", blk_idx))
-        k_tot = blk_idx.shape[2]
-        if not (_sound(idx, i32, (B, H_kv, k_tot), blk_idx) and _sound(idx, i32, (B, H_kv), count)):
-            _explain(idx, i32, (B, H_kv, k_tot), blk_idx=blk_idx)
-            _explain(idx, i32, (B, H_kv), count=count)
-        blocks, counts = blk_idx.data_ptr(), count.data_ptr()
-    lse_at = None if lse is None else lse.data_ptr()
-    st = None if status is None else status.data_ptr()
-    _call((_lib or load()).sparse_paged_decode_attn_f8, "sparse_paged_decode_attn_f8", idx, stream, Q.data_ptr(),
-          kv_pages.data_ptr(), kv_scale.data_ptr(), n_pages, block_table.data_ptr(), max_blocks, blocks, counts, k_tot,
-          seq_len.data_ptr(), B, H_q, H_kv, scale, O.data_ptr(), lse_at, workspace.data_ptr(), ws_bytes, st)
+        k_tot = _shape(blk_idx, "blk_idx", 3)[2]
+        _explain(idx, i32, (B, H_kv, k_tot), blk_idx=blk_idx)
+        _explain(idx, i32, (B, H_kv), count=count)
+    if lse is not None:
+        _explain(idx, f32, (B, H_q), lse=lse)
+    if status is not None:
+        _explain(idx, i32, (1,), status=status)
+    raise _refused("sparse_paged_decode_attn_f8")

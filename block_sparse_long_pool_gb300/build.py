@@ -2,7 +2,8 @@
 
 Each translation unit is compiled by nvcc in parallel, then linked into
 ``block_sparse_long_pool_gb300/libsparsepool.so``.  No cmake, no torch extension
-machinery: the product is a plain C-ABI shared library.
+machinery: the product is a plain C-ABI shared library.  ``_marshal.so`` beside it, from
+csrc/marshal.c by gcc, passes tensors from Python to three of its calls.
 """
 from __future__ import annotations
 
@@ -12,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsparsepool.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -39,6 +42,21 @@ def _stale(obj: str, src: str, deps: list[str]) -> bool:
         return True
     t = os.path.getmtime(obj)
     return any(os.path.getmtime(x) > t for x in [src] + deps)
+
+
+def build_marshal(verbose: bool = False, force: bool = False) -> str:
+    src = os.path.join(CSRC, "marshal.c")
+    if force or _stale(MARSHAL, src, [os.path.join(INCLUDE, "sparse_pool.h"), os.path.abspath(__file__)]):
+        tmp = MARSHAL + f".{os.getpid()}.tmp"
+        cmd = [os.environ.get("CC") or shutil.which("gcc") or "cc", "-O2", "-Wall", "-shared", "-fPIC", "-fvisibility=hidden",
+               f"-I{INCLUDE}", f"-I{sysconfig.get_paths()['include']}", src, "-o", tmp]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if verbose or r.returncode != 0:
+            sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+        if r.returncode != 0:
+            raise RuntimeError("gcc failed on marshal.c")
+        os.replace(tmp, MARSHAL)
+    return MARSHAL
 
 
 def build(verbose: bool = False, extra=(), force: bool = False) -> str:
@@ -69,6 +87,7 @@ def build(verbose: bool = False, extra=(), force: bool = False) -> str:
             sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             raise RuntimeError("link failed")
         os.replace(tmp, LIB)
+    build_marshal(verbose, force)
     return LIB
 
 
