@@ -532,10 +532,6 @@ int current_context_id(unsigned long long *id);
 // swizzle (the layout the attention kernel reads).  Returns SPARSE_OK or an error.
 int make_kv_tensor_map(CUtensorMap *map, const void *base, long long rows_per_pair, long long pairs);
 
-// 3-D tiled tensor map over [tiles][64][128] bytes with a 128 x 64 box and 128-byte
-// swizzle: the paged cache, a tile the keys or the values of a (page, head).
-int make_page_tensor_map(CUtensorMap *map, const void *base, long long tiles);
-
 // Configure a kernel once per device: its dynamic shared memory limit, and the
 // largest shared-memory carveout.  All kernels of the library prefer the same
 // carveout, so their CTAs can share an SM without the SM being reconfigured (a small

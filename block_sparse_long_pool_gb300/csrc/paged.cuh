@@ -5,6 +5,14 @@
 
 #include "common.cuh"
 
+namespace sp_host {
+
+// 3-D tiled tensor map over [tiles][64][128] bytes with a 128 x 64 box and 128-byte
+// swizzle: the paged cache, a tile the keys or the values of a (page, head).
+int make_page_tensor_map(CUtensorMap *map, const void *base, long long tiles);
+
+}  // namespace sp_host
+
 namespace {
 
 constexpr int kMaxPages = 1 << 25;   // 64 * page fits an int32 slot
