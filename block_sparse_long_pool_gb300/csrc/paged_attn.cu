@@ -5,7 +5,8 @@
 // of the flattened item list (its length is known on the device only: every CTA sums the
 // counts itself), in which a pair also counts as kPairCost items: its queries are loaded
 // and its state is merged.  So requests of very different lengths load the SMs evenly.  A
-// pair whose items lie in several CTAs is merged by the one that finishes last, in CTA order.
+// pair whose items lie in several CTAs is merged, each row by the warp that finishes it last, in
+// CTA order.
 //
 // Per CTA: the last warp resolves items to pages, 32 at a time (list -> block table -> scales),
 // and streams their keys and values, a TMA load of 8 KB each; the others take whole tiles in
@@ -24,13 +25,13 @@
 // scales are; the row sum l uses the fp32 weights 2^(s - m).
 //
 // What bounds it.  The tiles' stream in the middle, latency at both ends.  On GB300, back to back
-// in a graph: 537 MB (32K tokens x 8 requests x 8 KV heads, G = 4) in 91.5 us, 5.9 TB/s, 0.86 of
+// in a graph: 537 MB (32K tokens x 8 requests x 8 KV heads, G = 4) in 88.2 us, 6.1 TB/s, 0.90 of
 // the copy rate; of these about 3.5 us pass before the first tile is there (lengths, table,
-// load: three round trips), and 4 us after the last one in the merge of the pairs that the
-// CTAs share.  70.6 MB of selected blocks (64 pairs x 67) in 22.4 us, 2.1 MB (one request of 4K
-// tokens, 2 KV heads) in 12.6 us: those ends.  64 requests of 1 to 16K tokens in 41 us (0.59):
+// load: three round trips), and 3 us after the last one in the merge of the pairs that the
+// CTAs share.  70.6 MB of selected blocks (64 pairs x 67) in 20.5 us, 2.1 MB (one request of 4K
+// tokens, 2 KV heads) in 10.3 us: those ends.  64 requests of 1 to 16K tokens in 40.4 us (0.60):
 // each part of a pair ends with its warps waiting for one another.  A tile takes a warp about
-// 2900 cycles at G <= 8 and 3900 at G = 16 (537 MB in 105 us, 0.75): the conversions' half-rate
+// 2900 cycles at G <= 8 and 3900 at G = 16 (537 MB in 107 us, 0.74): the conversions' half-rate
 // instructions (cvt, prmt, shift) and the products' latency.
 #include <limits.h>
 #include <math.h>
@@ -49,18 +50,22 @@ constexpr int kMeta = 64;                         // item and part records: 32 b
 constexpr float kWeightBits = 12.f;               // weights reach 2^12: f16 holds them down to 2^-24
 constexpr uint64_t kWaitNs = 2000000000ull;
 // How the list is cut, in items (tiles).  Measured back to back in a graph:
-//   a range at least: 1 x 2 pairs of 64 tiles 11.7 us (3: 11.9, 6: 12.9, 12: 14.9), 8 pairs of 16
-//   tiles 10.7 us (6: 12.1): a merge over more CTAs against more tiles a warp;
+//   a range at least: 1 x 2 pairs of 64 tiles 10.6 us (2: 11.9, 3: 10.8, 6: 11.7), 8 pairs of 16
+//   tiles 9.8 us (2: 10.3, 6: 11.3): a merge over more CTAs against more tiles a warp;
 constexpr int kMinItems = 4;
-//   what a pair costs beside its items: 64 requests of 1 to 16K tokens 41 us (2: 60, 4: 45, 10: 41.4);
-constexpr int kPairCost = 7;
-//   pairs of up to so many items stay with one CTA: 48 pairs of up to 4 tiles 8.8 us (0: 10.5), 512
-//   of up to 8 tiles 16.8 us (0: 18.4), 8 of 16 tiles 12.1 us where 16 makes it 14.4;
-constexpr int kWhole = 12;
+//   what a pair costs beside its items: 64 requests of 1 to 16K tokens 40.4 us (4: 42.7, 7: 39.9,
+//   9: 41.0), 32K tokens x 64 pairs 88.1 us (4: 91.7, 7: 89.6, 9: 88.4);
+constexpr int kPairCost = 8;
+//   pairs of up to so many items stay with one CTA: 512 pairs of up to 8 tiles 16.3 us (0: 17.2), 32
+//   of 10 tiles 10.1 us and 64 of 12 tiles 10.6 us where 12 makes them 11.4 and 13.1 (kPairCost 7);
+constexpr int kWhole = 8;
 //   partial states that one CTA merges in one go, and the neighbours whose states are merged first
-//   where there are more (38 states: 55 us with groups of 12, 58.8 with 16, 60.2 with 32).
+//   where there are more (8 pairs in 38 states each: 53.4 us with groups of 12, 57.2 with 16).
 constexpr int kDirect = 32;
 constexpr int kGroup = 12;
+
+constexpr int kMaxPairs = 65535;
+constexpr int kCounters = 2 * kDirect + kMaxPairs + 1;   // arrival counts of a warp's rows
 
 // What the warp that takes an item needs to know of it.
 struct Item {
@@ -127,7 +132,7 @@ struct PagedAttnParams {
     uint16_t *O;
     float *lse;
     int *status;
-    int *arrivals;     // [2 * kDirect] of groups of CTAs, then [pairs]; zero between calls
+    int *arrivals;     // a warp: [2 * kDirect] of groups of CTAs, then [pairs]; zero between calls
     float *parts;      // [2 * CTAs][part_floats]
     float scale_log2;
     int n_pages;
@@ -546,31 +551,34 @@ __device__ __noinline__ bool meet(uint32_t bar, int parity)
     return __all_sync(0xffffffffu, wait_for(bar, parity, 2 * kWaitNs)) != 0;
 }
 
-// One of `expect` arrivals at a counter, by one thread for its CTA, which has met: true for the
-// last one, which resets the counter.  The release makes visible what the CTA wrote before
-// the meeting, the acquire what the other CTAs did.
-__device__ __forceinline__ bool arrive_last(int *counter, int expect)
+// One of `expect` arrivals of warps at a counter: true for the last one's lanes; it resets the
+// counter.  The release makes visible what the warp wrote before, the acquire what the others
+// did.
+__device__ __forceinline__ bool arrive_last(int *counter, int expect, int lane)
 {
-    int prev;
-    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(prev) : "l"(counter) : "memory");
-    if (prev == expect - 1)
-        *counter = 0;   // for the next call
-    return prev == expect - 1;
+    int prev = 0;
+    __syncwarp();
+    if (lane == 0) {
+        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(prev) : "l"(counter) : "memory");
+        if (prev == expect - 1)
+            *counter = 0;   // for the next call
+    }
+    return __shfl_sync(0xffffffffu, prev, 0) == expect - 1;
 }
 
 // The CTA's part of a pair: its warps' states merged, and written out, or left in the
-// workspace for the last of the pair's CTAs to merge.  All consumer threads call it.
+// workspace for the last of the pair's CTAs to merge.  All consumer threads call it.  Row r
+// belongs to warp r % 8 % kWarps in every CTA: a warp writes and merges its rows without waiting
+// for the CTA's other warps.
 template <int NT>
 __device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const State<NT> &st, const Part &of, int c, int lo,
-                                            int hi, int len, uint8_t *base, uint32_t bar, int &meetings, int *flag, int warp,
-                                            int lane)
+                                            int hi, int len, uint8_t *base, uint32_t bar, int &meetings, int warp, int lane)
 {
     constexpr int ROWS = 8 * NT;
     constexpr int PART = part_floats<NT>();
     constexpr int kWarps = warps<NT>();
     constexpr int kQuads = (8 + kWarps - 1) / kWarps;   // quads (four dims of a row) a thread sums
     using S = Smem<NT>;
-    const int tid = warp * 32 + lane;
     float *wo = reinterpret_cast<float *>(base + S::kWo);
     float *wm = reinterpret_cast<float *>(base + S::kStat);   // [kWarps][ROWS] each: m, l, mo
     float *wl = wm + kWarps * ROWS, *wmo = wl + kWarps * ROWS;
@@ -579,8 +587,8 @@ __device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const Stat
     float *part = p.parts + static_cast<size_t>(part_slot(c, c0)) * PART;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        // every warp's statistics, and the O of the warps from 2, then of warps 0 and 1; warp w
-        // sums rows w, w + kWarps, ...
+        // every warp's statistics, and the O of the warps from 2, then of warps 0 and 1; a warp
+        // sums its rows, a lane four dims
         if (nt > 0 && !meet(bar, meetings++ & 1))   // wo is free again
             return false;
         st.put_stats(wm + warp * ROWS + nt * 8, wl + warp * ROWS + nt * 8, wmo + warp * ROWS + nt * 8, nt, lane);
@@ -647,9 +655,9 @@ __device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const Stat
     if (whole)
         return true;
 
-    // The states of the pair's CTAs, merged by the last of them, in their order.  Where they
-    // are many, the last of each kGroup neighbours merges theirs first (into the slot of the
-    // first of them), and the last of those the groups'.
+    // The states of the pair's CTAs, a warp's rows merged by the last of them to write them, in
+    // the CTAs' order.  Where they are many, the last of each kGroup neighbours merges theirs
+    // first (into the slot of the first of them), and the last of those the groups'.
     const bool grouped = c1 - c0 + 1 > kDirect;
     const int g = c / kGroup, g0 = c0 / kGroup;
 #pragma unroll 1
@@ -669,43 +677,39 @@ __device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const Stat
                 step = kGroup;
             }
         }
-        if (!meet(bar, meetings++ & 1))   // the CTA's state is written
-            return false;
-        if (tid == 0)
-            *flag = arrive_last(counter, n);
-        if (!meet(bar, meetings++ & 1))
-            return false;
-        if (*flag == 0)
+        if (!arrive_last(counter + warp * kCounters, n, lane))
             return true;
-        auto slot = [&](int j) {
-            return p.parts + static_cast<size_t>(part_slot(j == 0 ? first : step == 1 ? first + j : (g0 + j) * kGroup, c0)) * PART;
+        auto slot = [&](int j) {   // in 4 bytes: at most 2 * kGroup * (kDirect - 1) states
+            return part_slot(j == 0 ? first : step == 1 ? first + j : (g0 + j) * kGroup, c0) * PART;
         };
-        // A warp takes two rows at a time, its lanes four dims each of O, and before that a state's
-        // statistics each, from which the rows' come by shuffles.  All loads of up to kStep
+        // Two rows at a time: lanes take four dims each of O, and before that a state's statistics
+        // each, from which the rows' come by shuffles.  The loads of all statistics and of kStep
         // states go out together.
         constexpr int kStep = 8;
-        float *dst = slot(0);
+        float *dst = p.parts + slot(0);
 #pragma unroll 1
-        for (int row0 = warp; row0 < p.G; row0 += 2 * kWarps) {
-            const int rows[2] = {row0, row0 + kWarps};
+        for (int row0 = warp; row0 < min(p.G, 8); row0 += NT == 1 ? 2 * kWarps : kWarps) {
+            const int rows[2] = {row0, row0 + (NT == 1 ? kWarps : 8)};
             float4 x[2][kStep];
             auto fetch = [&](int j0) {
 #pragma unroll
-                for (int u = 0; u < kStep; ++u) {
-                    const float4 *src = reinterpret_cast<const float4 *>(slot(j0 + u)) + lane;
+                for (int u = 0; u < kStep; ++u)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r)
-                        x[r][u] = j0 + u < n && rows[r] < p.G ? __ldcg(src + rows[r] * (kD / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
-                }
+                    for (int r = 0; r < 2; ++r) {
+                        const int j = j0 + u;
+                        x[r][u] = j < n && rows[r] < p.G
+                                      ? __ldcg(reinterpret_cast<const float4 *>(p.parts + (slot(j) + rows[r] * kD + 4 * lane)))
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
             };
-            const float *stat = slot(min(lane, n - 1)) + ROWS * kD + row0;
+            const float *stat = p.parts + (slot(min(lane, n - 1)) + ROWS * kD);
             float m[2], l[2], mo[2], w[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const bool in = lane < n && rows[r] < p.G;
-                m[r] = in ? __ldcg(stat + r * kWarps) : -INFINITY;
-                l[r] = in ? __ldcg(stat + ROWS + r * kWarps) : 0.f;
-                mo[r] = in ? __ldcg(stat + 2 * ROWS + r * kWarps) : -INFINITY;
+                m[r] = in ? __ldcg(stat + rows[r]) : -INFINITY;
+                l[r] = in ? __ldcg(stat + ROWS + rows[r]) : 0.f;
+                mo[r] = in ? __ldcg(stat + 2 * ROWS + rows[r]) : -INFINITY;
             }
             fetch(0);
 #pragma unroll
@@ -777,7 +781,7 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
     using S = Smem<NT>;
     static_assert(kDirect <= 32 && kGroup <= kDirect, "a lane holds a state's statistics");
     extern __shared__ uint8_t smem_raw[];
-    __shared__ int s_sum[kWarps + 1], s_pair, s_n, s_start, s_last;
+    __shared__ int s_sum[kWarps + 1], s_pair, s_n, s_start;
     const uint32_t base_s = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *base = smem_raw + (base_s - smem_u32(smem_raw));
     Item *items = reinterpret_cast<Item *>(base + S::kItems);
@@ -1060,7 +1064,7 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
 #pragma unroll 1
             for (; part < next; ++part) {
                 const Part of = parts[part % kMeta];
-                bool ok = finish_part<NT>(p, st, of, c, lo, hi, len, base, bar, meetings, &s_last, warp, lane);
+                bool ok = finish_part<NT>(p, st, of, c, lo, hi, len, base, bar, meetings, warp, lane);
                 if (part + 1 < next || (item.part & kEnd) == 0)
                     q.load(p, parts[(part + 1) % kMeta].pair, lane);
                 st.reset();
@@ -1105,8 +1109,6 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
     }
 }
 
-constexpr int kMaxPairs = 65535;
-
 bool sizes_ok(int B, int H_q, int H_kv)
 {
     return B >= 1 && H_kv >= 1 && H_q >= H_kv && H_q % H_kv == 0 && H_q / H_kv <= 16 &&
@@ -1122,7 +1124,7 @@ int grid_ctas(int sm_count)
 
 // Workspace: the arrival counts, at the same places whatever the sizes of a call, so that calls
 // of different sizes may take turns with it; then two partial states a CTA.
-constexpr size_t kCounterBytes = (kMaxPairs + 1 + 2 * kDirect) * sizeof(int);
+constexpr size_t kCounterBytes = static_cast<size_t>(kCounters) * warps<1>() * sizeof(int);
 static_assert(kCounterBytes % 16 == 0, "the states are read 16 bytes at a time");
 
 size_t workspace_bytes_of(int G, int ctas)

@@ -644,15 +644,16 @@ SPARSE_API int sparse_paged_append_f8(uint8_t *kv_pages, float *kv_scale, int n_
  *                lse = -inf.
  *   workspace    sparse_paged_decode_attn_f8_workspace_size() bytes, 16-byte aligned, all
  *                zero before the first call that uses it; every call leaves its counters
- *                zero again.  Calls of any sizes may share a workspace that is large enough
- *                for each, but not at the same time.
+ *                zero again, but one that reports SPARSE_ERR_TIMEOUT: zero it again then.
+ *                Calls of any sizes may share a workspace that is large enough for each, but
+ *                not at the same time.
  * Rows past seq_len in a request's last page are never used, whatever bytes they hold.
  * Listed blocks are expected to be distinct.  A block past the request's length adds
  * nothing.  A negative block or one past max_blocks, a page outside [0, n_pages), a count
  * outside [0, k_tot] (clamped) and a length past 64 max_blocks (clamped) are reported as
  * SPARSE_ERR_BAD_INDEX; such a block is left out.  The result does not depend on timing.
  * G = H_q / H_kv <= 16, B * H_kv <= 65535, n_pages and k_tot <= 2^25, max_blocks < 2^25,
- * n_pages * H_kv < 2^30, and B * H_kv * (k_tot + 7), or (max_blocks + 7) where every block
+ * n_pages * H_kv < 2^30, and B * H_kv * (k_tot + 8), or (max_blocks + 8) where every block
  * is attended over, below 2^31.
  */
 SPARSE_API int sparse_paged_decode_attn_f8(const uint16_t *Q, const uint8_t *kv_pages, const float *kv_scale,
