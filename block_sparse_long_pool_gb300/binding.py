@@ -19,10 +19,10 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libsparsepool.so")
-MARSHAL_PATH = os.path.join(_PKG, "_marshal.so")
+MARSHAL_PATH = os.path.join(_PKG, f"_marshal_{torch.__version__}.so")
 _lock = threading.Lock()
 _lib = None
-_marshal = None   # csrc/marshal.c, which passes the paged cache's tensors on
+_marshal = None   # csrc/marshal.cpp, which passes the paged cache's tensors on
 
 D = 128
 BLK = 64
@@ -105,8 +105,7 @@ def load(path: str = LIB_PATH):
         spec = importlib.util.spec_from_file_location("_marshal", MARSHAL_PATH)
         marshal = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(marshal)
-        marshal.setup(torch.int32, torch.float32, torch.bfloat16, torch.float8_e4m3fn, torch.uint8,
-                      *(ctypes.cast(getattr(lib, f"sparse_{name}"), ctypes.c_void_p).value
+        marshal.setup(*(ctypes.cast(getattr(lib, f"sparse_{name}"), ctypes.c_void_p).value
                         for name in ("page_plan", "paged_append_f8", "paged_decode_attn_f8")))
         _marshal = marshal
         _lib = lib
@@ -493,7 +492,7 @@ _F8 = torch.float8_e4m3fn
 
 
 # The calls of this cache are short: a decode step's plan or append takes 4 to 6 us on the
-# device.  So their tensors are checked and passed on by csrc/marshal.c; what is wrong is
+# device.  So their tensors are checked and passed on by csrc/marshal.cpp; what is wrong is
 # looked for here, only when something is.
 
 
@@ -506,7 +505,7 @@ def _explain(idx, dtype, shape, **tensors):
 
 
 def _passed(name, idx, stream, *args) -> bool:
-    """Calls ``name`` on device ``idx``, which need not be the current one; false where marshal.c
+    """Calls ``name`` on device ``idx``, which need not be the current one; false where marshal.cpp
     refused a tensor, and nothing was called."""
     if _lib is None:
         load()

@@ -2,8 +2,8 @@
 
 Each translation unit is compiled by nvcc in parallel, then linked into
 ``block_sparse_long_pool_gb300/libsparsepool.so``.  No cmake, no torch extension
-machinery: the product is a plain C-ABI shared library.  ``_marshal.so`` beside it, from
-csrc/marshal.c by gcc, passes tensors from Python to three of its calls.
+machinery: the product is a plain C-ABI shared library.  ``_marshal_<torch version>.so`` beside
+it, from csrc/marshal.cpp by g++, passes tensors from Python to three of its calls.
 """
 from __future__ import annotations
 
@@ -15,13 +15,15 @@ import subprocess
 import sys
 import sysconfig
 
+import torch
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsparsepool.so")
-MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL = os.path.join(PKG, f"_marshal_{torch.__version__}.so")   # reads that version's tensor objects
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -45,16 +47,20 @@ def _stale(obj: str, src: str, deps: list[str]) -> bool:
 
 
 def build_marshal(verbose: bool = False, force: bool = False) -> str:
-    src = os.path.join(CSRC, "marshal.c")
+    src = os.path.join(CSRC, "marshal.cpp")
     if force or _stale(MARSHAL, src, [os.path.join(INCLUDE, "sparse_pool.h"), os.path.abspath(__file__)]):
         tmp = MARSHAL + f".{os.getpid()}.tmp"
-        cmd = [os.environ.get("CC") or shutil.which("gcc") or "cc", "-O2", "-Wall", "-shared", "-fPIC", "-fvisibility=hidden",
-               f"-I{INCLUDE}", f"-I{sysconfig.get_paths()['include']}", src, "-o", tmp]
+        root = os.path.dirname(torch.__file__)
+        cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-Wall", "-std=c++17", "-shared", "-fPIC",
+               "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}",
+               *(f"-isystem{x}" for x in (f"{root}/include", f"{root}/include/torch/csrc/api/include",
+                                          sysconfig.get_paths()["include"])),
+               src, f"-L{root}/lib", "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", tmp]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if verbose or r.returncode != 0:
             sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
         if r.returncode != 0:
-            raise RuntimeError("gcc failed on marshal.c")
+            raise RuntimeError("g++ failed on marshal.cpp")
         os.replace(tmp, MARSHAL)
     return MARSHAL
 
@@ -72,7 +78,8 @@ def build(verbose: bool = False, extra=(), force: bool = False) -> str:
         objs.append(obj)
         if force or _stale(obj, src, deps):
             jobs.append([cc] + flags(extra) + ["-c", src, "-o", obj])
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 4))) as ex:
+        marshal = ex.submit(build_marshal, verbose, force)
         results = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
     for cmd, r in zip(jobs, results):
         if verbose or r.returncode != 0:
@@ -87,7 +94,7 @@ def build(verbose: bool = False, extra=(), force: bool = False) -> str:
             sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             raise RuntimeError("link failed")
         os.replace(tmp, LIB)
-    build_marshal(verbose, force)
+    marshal.result()
     return LIB
 
 
