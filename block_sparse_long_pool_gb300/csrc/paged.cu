@@ -15,18 +15,22 @@ using namespace sp;
 
 // ---------------------------------------------------------------- page plan
 //
-// Three prefix sums over the requests (pages returned, new tokens, pages needed) by one CTA of
-// 1024 threads, then a row's place by arithmetic: no row waits for a table entry that this
-// step writes, since a new page's id follows from the request's prefix and the free list.
-// All latency: a step of 8 requests takes 4.3 us on GB300, back to back in a graph, 512 requests
-// with 16 384 rows 7.2 us, 2^20 rows 9.5 us (12.6 MB stored: 1.9 us at the copy rate).
+// Three prefix sums over the requests (pages returned, new tokens, pages needed) by every CTA,
+// then a row's place by arithmetic: no row waits for a table entry that this step writes,
+// since a new page's id follows from the request's prefix and the free list.
+// All latency: a step of 8 requests takes 3.0 us on GB300, back to back in a graph, 512 requests
+// with 16 384 rows 4.8 us, 2^20 rows 8.8 us (12.6 MB stored: 1.9 us at the copy rate).
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanMaxB = 4096;
 constexpr int kPlanPer = kPlanMaxB / kPlanThreads;   // requests a thread scans, at most
+// Threads a CTA where they are enough (kPlanPer requests each).  1024 for all: a step of 8 requests
+// 4.4 us (3.0), 512 requests with 16 384 rows 7.1 (4.8): warps to start and to join.  512: 3.3 and
+// 4.9; 128: 3.0 and 5.2.
+constexpr int kPlanLeast = 256;
 constexpr int kRowThreads = 256;
 constexpr int kRowsPerCta = 1024;
-constexpr int kRowsOneCta = 1024;   // rows that the planning CTA writes itself, one a thread
+constexpr int kRowsOneCta = 1024;   // rows that one planning CTA writes itself, where outputs are inputs
 
 struct PlanParams {
     const int *seq_len;
@@ -48,37 +52,35 @@ struct PlanParams {
     int n_tok;
 };
 
-// Inclusive block-wide prefix sum of one value a thread; `tot` gets the block's sum.
-// `red` holds 33 entries; the caller's threads all take part.
-__device__ __forceinline__ long long block_scan(long long v, long long *red, long long *tot)
+// Inclusive block-wide prefix sums of K values a thread; `tot` gets the block's sums.  One barrier:
+// each warp sums the warps before it for itself.  `red` is the call's own, [K][32].
+template <int K>
+__device__ __forceinline__ void block_scan(long long (&v)[K], long long (*red)[32], long long (&tot)[K])
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o)
-            v += u;
-    }
-    __syncthreads();
-    if (lane == 31)
-        red[warp] = v;
-    __syncthreads();
-    if (warp == 0) {
-        const int nw = blockDim.x >> 5;
-        long long w = lane < nw ? red[lane] : 0;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    auto scan = [&](long long x) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long u = __shfl_up_sync(0xffffffffu, w, o);
+            const long long u = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o)
-                w += u;
+                x += u;
         }
-        red[lane] = w;
+        return x;
+    };
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        v[k] = scan(v[k]);
+        if (lane == 31)
+            red[k][warp] = v[k];
     }
     __syncthreads();
-    if (warp > 0)
-        v += red[warp - 1];
-    *tot = red[(blockDim.x >> 5) - 1];
-    return v;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const long long w = scan(lane < warps ? red[k][lane] : 0);
+        const long long before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+        v[k] += warp > 0 ? before : 0;
+        tot[k] = __shfl_sync(0xffffffffu, w, 31);
+    }
 }
 
 __device__ __forceinline__ int saturate(long long v)
@@ -109,7 +111,8 @@ __device__ __forceinline__ const int *returned_page(const PlanParams &p, const i
 
 // Rows [t0, t0 + n), R of them (1 or 4, t0 a multiple of R) a thread and pass: the first
 // row's request by binary search, the next rows' by steps from it; then the pages, whose
-// loads are in flight together; then the three entries, as words of R.  A new block's page
+// loads are in flight together; then the three entries, as words of R (8 rows a thread spill:
+// 2^20 rows 11.9 us against 8.8).  A new block's page
 // comes from the free list and is entered into the table by the row that starts the block.
 //   With `relpre` the pages returned in this step (places F0 .. F - 1 of the list) are taken from
 // the tables of the requests that return them: the list may not hold them yet.
@@ -183,13 +186,15 @@ __device__ __forceinline__ void plan_rows(const PlanParams &p, const int *cu, co
 }
 
 // Every CTA works out the requests' places for itself (B is small, and this costs less than a
-// second launch); CTA 0 writes them, and each writes `rows` rows (0: page_rows_kernel does).
+// second launch); CTA 0 writes them, and each writes `rows` rows (0: page_rows_kernel does) and
+// its part of the returned pages.
 // More than one CTA only where no output is an input's buffer: one CTA's writes would change
 // what another still has to read.
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParams p, int rows)
 {
     extern __shared__ int plan_smem[];
-    __shared__ long long red[33];
+    __shared__ long long red[3][32];
+    __shared__ int taken;
     int *cu = plan_smem;                 // [B + 1]
     int *first = cu + p.B + 1;           // [B] start, -1: not granted
     int *npre = first + p.B;             // [B] pages granted before the request's own
@@ -197,8 +202,11 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
     griddep_wait();
     griddep_launch_dependents();
 
-    const int tid = threadIdx.x;
-    const int per = (p.B + kPlanThreads - 1) / kPlanThreads;
+    const int tid = threadIdx.x, threads = static_cast<int>(blockDim.x);
+    const int per = (p.B + threads - 1) / threads;
+    int F0 = p.n_free[0];
+    if (tid == 0)
+        taken = 0;
     long long len[kPlanPer], add[kPlanPer];
     bool ends[kPlanPer], sound[kPlanPer];
     long long s_rel = 0, s_add = 0;
@@ -222,10 +230,10 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
                 s_rel += (len[i] + kBlk - 1) / kBlk;
         }
     }
-    long long all_rel, all_add;
-    long long o_rel = block_scan(s_rel, red, &all_rel) - s_rel;
-    long long o_add = block_scan(s_add, red, &all_add) - s_add;
-    int F0 = p.n_free[0];
+    long long sums[2] = {s_rel, s_add}, all[2];
+    block_scan(sums, red, all);
+    const long long all_rel = all[0];
+    long long o_rel = sums[0] - s_rel, o_add = sums[1] - s_add;
     if (F0 < 0 || F0 > p.n_pages) {
         bad = 1;
         F0 = F0 < 0 ? 0 : p.n_pages;
@@ -259,8 +267,9 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
             }
         }
     }
-    long long all_need;
-    long long o_need = block_scan(s_need, red, &all_need) - s_need;
+    long long needs[1] = {s_need}, all_need[1];
+    block_scan(needs, red + 2, all_need);
+    long long o_need = needs[0] - s_need;
     long long s_taken = 0;
     int refused = 0;
 #pragma unroll
@@ -281,8 +290,10 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
             }
         }
     }
-    long long all_taken;
-    block_scan(s_taken, red, &all_taken);   // its barriers also publish cu, first, npre, relpre
+    const int warp_taken = __reduce_add_sync(0xffffffffu, static_cast<int>(s_taken));   // of at most n_pages
+    if (blockIdx.x == 0 && (tid & 31) == 0)
+        atomicAdd(&taken, warp_taken);
+    __syncthreads();   // of cu, first, npre, relpre and taken
     if (blockIdx.x == 0) {
         if (bad)
             report(p.status, SPARSE_ERR_BAD_INDEX);
@@ -290,13 +301,24 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
             report(p.status, SPARSE_ERR_NO_PAGES);
         if (tid == 0) {
             p.cu_new[0] = 0;
-            p.n_free_out[0] = F - static_cast<int>(all_taken);
+            p.n_free_out[0] = F - taken;
         }
-        for (int i = tid; i < F - F0; i += kPlanThreads)
-            p.free_pages[F0 + i] = *returned_page(p, relpre, i);
+    }
+    // the returned pages' ids, four loads of a thread in flight
+    const int ways = threads * static_cast<int>(gridDim.x);
+#pragma unroll 1
+    for (int i = static_cast<int>(blockIdx.x) * threads + tid; i < F - F0; i += 4 * ways) {
+        int page[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            page[j] = i + j * ways < F - F0 ? *returned_page(p, relpre, i + j * ways) : 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i + j * ways < F - F0)
+                p.free_pages[F0 + i + j * ways] = page[j];
     }
     const int t0 = static_cast<int>(blockIdx.x) * rows, n = min(p.n_tok - t0, rows);
-    if (rows > kPlanThreads)
+    if (rows > threads)
         plan_rows<4>(p, cu, first, npre, F, t0, n, relpre, F0);
     else if (rows > 0)
         plan_rows<1>(p, cu, first, npre, F, t0, n, relpre, F0);
@@ -307,7 +329,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
 __global__ void __launch_bounds__(kRowThreads) page_rows_kernel(const PlanParams p)
 {
     extern __shared__ int plan_smem[];
-    __shared__ long long red[33];
+    __shared__ long long red[1][32];
     int *cu = plan_smem;          // [B + 1]
     int *first = cu + p.B + 1;    // [B]
     int *npre = first + p.B;      // [B]
@@ -325,15 +347,16 @@ __global__ void __launch_bounds__(kRowThreads) page_rows_kernel(const PlanParams
     int mine = 0;
     for (int b = b0; b < b1; ++b)
         mine += pages_taken(cu, first, b);
-    long long all;
-    int o = static_cast<int>(block_scan(mine, red, &all)) - mine;
+    long long sum[1] = {mine}, all[1];
+    block_scan(sum, red, all);
+    int o = static_cast<int>(sum[0]) - mine;
     for (int b = b0; b < b1; ++b) {
         npre[b] = o;
         o += pages_taken(cu, first, b);
     }
     __syncthreads();
     const int t0 = static_cast<int>(blockIdx.x) * kRowsPerCta;
-    plan_rows<4>(p, cu, first, npre, p.n_free_out[0] + static_cast<int>(all), t0, min(p.n_tok - t0, kRowsPerCta));
+    plan_rows<4>(p, cu, first, npre, p.n_free_out[0] + static_cast<int>(all[0]), t0, min(p.n_tok - t0, kRowsPerCta));
 }
 
 // ---------------------------------------------------------------- append
@@ -730,19 +753,21 @@ extern "C" SPARSE_API int sparse_page_plan(const int *seq_len, const int *n_new,
                                        (3 * kPlanMaxB + 1) * static_cast<int>(sizeof(int)), dev.device, configured[1]);
     if (rc != SPARSE_OK)
         return rc;
-    // One row a thread up to a CTA an SM (the kernel's registers allow one), then four a pass.
     const bool in_place = seq_len_out == seq_len || n_free_out == n_free;
     const bool one_launch = n_tok <= kRowsOneCta || !in_place;
-    const int per_sm = (n_tok + dev.sm_count - 1) / dev.sm_count, pass = 4 * kRowsOneCta;
-    const int rows = !one_launch ? 0 : per_sm <= kRowsOneCta ? kRowsOneCta : (per_sm + pass - 1) / pass * pass;
+    const int threads = B <= kPlanPer * kPlanLeast ? kPlanLeast : kPlanThreads;
+    // One row a thread while that does not fill the SMs, then equal shares in whole 128-byte lines
+    // (shares of whole passes: 2^20 rows 9.4 us; half as many CTAs: 9.3).
+    const int ctas = dev.sm_count * (kPlanThreads / threads), share = ((n_tok - 1) / ctas + 32) / 32 * 32;
+    const int rows = !one_launch ? 0 : in_place ? kRowsOneCta : std::max(threads, share);
     const int smem = (4 * B + 1) * static_cast<int>(sizeof(int));
     const unsigned grid = one_launch ? (static_cast<unsigned>(n_tok) + rows - 1) / rows : 1u;
     rc = sp_host::cuda_status(
-        launch_pdl(reinterpret_cast<const void *>(page_plan_kernel), dim3(grid), kPlanThreads, smem, stream, p, rows), name);
+        launch_pdl(reinterpret_cast<const void *>(page_plan_kernel), dim3(grid), threads, smem, stream, p, rows), name);
     if (rc != SPARSE_OK || one_launch)
         return rc;
-    const unsigned ctas = (static_cast<unsigned>(n_tok) + kRowsPerCta - 1) / kRowsPerCta;
-    return sp_host::cuda_status(launch_pdl(reinterpret_cast<const void *>(page_rows_kernel), dim3(ctas), kRowThreads,
+    const unsigned row_ctas = (static_cast<unsigned>(n_tok) + kRowsPerCta - 1) / kRowsPerCta;
+    return sp_host::cuda_status(launch_pdl(reinterpret_cast<const void *>(page_rows_kernel), dim3(row_ctas), kRowThreads,
                                            (3 * B + 1) * static_cast<int>(sizeof(int)), stream, p), name);
 }
 
