@@ -367,13 +367,16 @@ __global__ void __launch_bounds__(kRowThreads) page_rows_kernel(const PlanParams
 // move to a larger one by an exponent shift, which rounds nothing but subnormals, and e4m3
 // loses no precision to it (its precision is relative).  What bounds it is DRAM: 131 072 tokens
 // of 8 heads in 126 us, 6.4 TB/s, 0.95 of the copy rate.  A CTA's life is a chain of three
-// loads (slots, rows, stores); 9 CTAs an SM cover it only with the rows of the CTAs 3 an SM
-// ahead already asked for (162 us without; 2, 4 and 5 ahead: 127 to 128; 8 ahead, whose rows
+// loads (slots, rows, stores); 9 CTAs an SM cover it only with the rows of the CTAs 2 an SM
+// ahead already asked for (162 us without; 3 and 4 ahead: 127 and 128; 8 ahead, whose rows
 // leave L2's sets before they are used: 140 and more).  Keys and values in one CTA of 256
-// threads: 150 us.  Small calls are latency: 8 rows 4.3 us, 256 rows 5.6 us, and the rows of a
-// decode step, runs of one, go to a warp each (18.3 us with a CTA each).
+// threads: 150 us.  Small calls are latency: 8 rows 2.5 us, 256 rows 3.3 us.  The rows of a decode
+// step, runs of one, go to a warp each (18.3 us with a CTA each), which finds them from what
+// its lanes tell of a row each (4.3 and 5.6 us where it walks over the window's runs).  A step
+// whose rows make scales grow takes up to 4.5 us more (63 old rows; batches of 8 and 16 of
+// their loads spill: 131 072 tokens 151 and 351 us).
 constexpr int kAppendThreads = 128;
-constexpr int kAhead = 3;       // CTAs an SM ahead whose rows a CTA brings into L2
+constexpr int kAhead = 2;       // CTAs an SM ahead whose rows a CTA brings into L2
 constexpr int kShort = 2;       // rows of a run that one warp appends
 constexpr int kMinExp = -120;   // least exponent of a scale: its reciprocal is a normal fp32 value
 
@@ -693,23 +696,53 @@ __global__ void __launch_bounds__(kAppendThreads, 9) paged_append_kernel(const P
     uint64_t leads = held & ~on_lo;
     if (p.window < 64)
         leads &= (1ull << p.window) - 1;
-    int short_no = 0;
-    while (leads != 0) {
-        const int i = __ffsll(static_cast<long long>(leads)) - 1;
-        leads &= leads - 1;
+    // rows of the run that starts at row i: those behind it that go on, the bits from i + 1 of the
+    // 128
+    auto rows_of = [&](int i) {
+        const uint64_t rest = i == 63 ? on_hi : (on_lo >> (i + 1)) | (on_hi << (63 - i));
+        return 1 + (~rest == 0 ? 63 : __ffsll(static_cast<long long>(~rest)) - 1);
+    };
+    // of the short runs every eighth is the warp's: lanes tell rows lane and 32 + lane
+    uint64_t shorts = 0;
+    if ((leads & (leads - 1)) != 0) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const bool is_short = (leads >> (32 * k + lane) & 1) != 0 && rows_of(32 * k + lane) <= kShort;
+            shorts |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, is_short)) << 32 * k;
+        }
+    } else if (leads != 0 && rows_of(__ffsll(static_cast<long long>(leads)) - 1) <= kShort) {
+        shorts = leads;
+    }
+    if (shorts != 0) {
+        uint64_t mine = 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int i = 32 * k + lane, no = __popcll(shorts & ((1ull << i) - 1));
+            mine |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, (shorts >> i & 1) != 0 && no % 8 == 4 * kv + warp)) << 32 * k;
+        }
+        while (mine != 0) {
+            const int i = __ffsll(static_cast<long long>(mine)) - 1;
+            mine &= mine - 1;
+            const int at = __shfl_sync(0xffffffffu, i < 32 ? slot[0] : slot[1], i & 31);
+            if (at / kBlk < p.n_pages)
+                append_short(p, t0 + i, at, rows_of(i), head, lane);
+            else if (lane == 0)
+                report(p.status, SPARSE_ERR_BAD_INDEX);
+        }
+    }
+    uint64_t longs = leads & ~shorts;
+    while (longs != 0) {
+        const int i = __ffsll(static_cast<long long>(longs)) - 1;
+        longs &= longs - 1;
         const int at = __shfl_sync(0xffffffffu, i < 32 ? slot[0] : slot[1], i & 31);
-        // rows behind i that go on: the bits from i + 1 of the 128
+        // rows_of(i), written out: called here too it costs append_long registers (137 us)
         const uint64_t rest = i == 63 ? on_hi : (on_lo >> (i + 1)) | (on_hi << (63 - i));
         const int n = 1 + (~rest == 0 ? 63 : __ffsll(static_cast<long long>(~rest)) - 1);
         if (at / kBlk >= p.n_pages) {
             if (threadIdx.x == 0)
                 report(p.status, SPARSE_ERR_BAD_INDEX);
-        } else if (n > kShort) {
-            append_long(p, t0 + i, at, n, head, kv, s_amax, red);
         } else {
-            if (short_no % 8 == 4 * kv + warp)
-                append_short(p, t0 + i, at, n, head, lane);
-            ++short_no;
+            append_long(p, t0 + i, at, n, head, kv, s_amax, red);
         }
     }
 }
@@ -804,8 +837,9 @@ extern "C" SPARSE_API int sparse_paged_append_f8(uint8_t *kv_pages, float *kv_sc
     if (rc != SPARSE_OK)
         return rc;
     // rows a CTA looks over: with 8, every warp has a row of a decode step; more, up to a
-    // block's 64, once that alone makes over 8 CTAs an SM (prompts have a run in 64 rows)
-    while (window < kBlk && static_cast<long long>(n_tok) * H_kv > 8LL * dev.sm_count * window)
+    // block's 64, while that alone makes over 32 CTAs an SM (prompts have a run in 64 rows):
+    // 8191 rows of 8 heads 14.1 us with 32 (16: 15.4, 64: 14.9, 128: 20.5)
+    while (window < kBlk && static_cast<long long>(n_tok) * H_kv > 16LL * dev.sm_count * window)
         window *= 2;
     const PagedAppendParams p{kv_pages, kv_scale, k_new, v_new, slot_map, ktil, tok_req, tok_pos, status, k_stride, v_stride,
                               n_pages, H_kv, n_tok, window, B, N_cap, kAhead * dev.sm_count};
