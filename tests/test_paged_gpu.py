@@ -224,6 +224,31 @@ def test_append(H, lens, new, strided):
     assert c.status.item() == 0
 
 
+@pytest.mark.parametrize("n_tok", [200, 420, 800, 1500])
+def test_append_short_and_long_runs_side_by_side(n_tok):
+    """64 heads, so that a CTA looks over 8, 16, 32 or 64 rows: runs of one row to whole pages
+    in one window, rows without a slot between them, pages that held rows before."""
+    rng = np.random.default_rng(n_tok)
+    H, slots, req, pos, lens = 64, [], [], [], []
+    while len(slots) < n_tok:
+        new = int(rng.choice([1, 1, 1, 1, 2, 2, 3, 7, 40, 64, 90]))
+        b, a = len(lens), int(rng.integers(0, 2 * BLK))
+        for x in range(a, a + new):
+            slots.append((3 * b + x // BLK - a // BLK) * BLK + x % BLK)
+            req.append(b)
+            pos.append(x)
+        lens.append(a + new)
+        if rng.random() < 0.2:
+            slots, req, pos = slots + [-1], req + [-1], pos + [-1]
+    B, N = len(lens), max(ref.nblk(n) for n in lens)
+    c = Cache(rng, 3 * B, H, B, N)
+    k, v = rows(rng, len(slots), H, True)
+    want = ref.append(*c.state()[:2], ref.f64(k), ref.f64(v), slots, c.state()[2], req, pos)
+    c.append(k, v, slots, req, pos)
+    c.check(want)
+    assert c.status.item() == 0
+
+
 def test_append_row_by_row_gives_one_scale_and_the_pooled_keys():
     """64 calls of one row each: the scale grows, and rows rounded before are moved exactly."""
     rng = np.random.default_rng(3)
