@@ -25,13 +25,13 @@
 // scales are; the row sum l uses the fp32 weights 2^(s - m).
 //
 // What bounds it.  The tiles' stream in the middle, latency at both ends.  On GB300, back to back
-// in a graph: 537 MB (32K tokens x 8 requests x 8 KV heads, G = 4) in 88.2 us, 6.1 TB/s, 0.90 of
+// in a graph: 537 MB (32K tokens x 8 requests x 8 KV heads, G = 4) in 87.5 us, 6.1 TB/s, 0.90 of
 // the copy rate; of these about 3.5 us pass before the first tile is there (lengths, table,
 // load: three round trips), and 3 us after the last one in the merge of the pairs that the
-// CTAs share.  70.6 MB of selected blocks (64 pairs x 67) in 20.5 us, 2.1 MB (one request of 4K
-// tokens, 2 KV heads) in 10.3 us: those ends.  64 requests of 1 to 16K tokens in 40.4 us (0.60):
+// CTAs share.  70.6 MB of selected blocks (64 pairs x 67) in 20.4 us, 2.1 MB (one request of 4K
+// tokens, 2 KV heads) in 9.7 us: those ends.  64 requests of 1 to 16K tokens in 39 us (0.62):
 // each part of a pair ends with its warps waiting for one another.  A tile takes a warp about
-// 2900 cycles at G <= 8 and 3900 at G = 16 (537 MB in 107 us, 0.74): the conversions' half-rate
+// 2900 cycles at G <= 8 and 3900 at G = 16 (537 MB in 104.6 us, 0.76): the conversions' half-rate
 // instructions (cvt, prmt, shift) and the products' latency.
 #include <limits.h>
 #include <math.h>
@@ -50,11 +50,11 @@ constexpr int kMeta = 64;                         // item and part records: 32 b
 constexpr float kWeightBits = 12.f;               // weights reach 2^12: f16 holds them down to 2^-24
 constexpr uint64_t kWaitNs = 2000000000ull;
 // How the list is cut, in items (tiles).  Measured back to back in a graph:
-//   a range at least: 1 x 2 pairs of 64 tiles 10.6 us (2: 11.9, 3: 10.8, 6: 11.7), 8 pairs of 16
+//   a range at least: 1 x 2 pairs of 64 tiles 9.7 us (3: 10.2; 2 and 6 before: 1.3 and 1.1 more), 8 pairs of 16
 //   tiles 9.8 us (2: 10.3, 6: 11.3): a merge over more CTAs against more tiles a warp;
 constexpr int kMinItems = 4;
-//   what a pair costs beside its items: 64 requests of 1 to 16K tokens 40.4 us (4: 42.7, 7: 39.9,
-//   9: 41.0), 32K tokens x 64 pairs 88.1 us (4: 91.7, 7: 89.6, 9: 88.4);
+//   what a pair costs beside its items: 64 requests of 1 to 16K tokens 39.1 us (5: 38.5, 7: 38.6,
+//   9: 39.8), 32K tokens x 64 pairs 88.2 us (5: 90.1, 7: 89.7, 9: 88.7);
 constexpr int kPairCost = 8;
 //   pairs of up to so many items stay with one CTA: 512 pairs of up to 8 tiles 16.3 us (0: 17.2), 32
 //   of 10 tiles 10.1 us and 64 of 12 tiles 10.6 us where 12 makes them 11.4 and 13.1 (kPairCost 7);
@@ -321,13 +321,15 @@ struct State {
         }
     }
 
-    // and their O, to [8][kStride]
-    __device__ __forceinline__ void put_o(float *to, int group, int lane) const
+    // and their O, of the first `rows` (NT = 1; else of all), to [8][kStride]
+    __device__ __forceinline__ void put_o(float *to, int group, int rows, int lane) const
     {
         const int g8 = lane >> 2, t4 = lane & 3;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             if (NT == 1) {
+                if (2 * t4 + h >= rows)
+                    continue;
                 float *dst = to + (2 * t4 + h) * kStride + 16 * g8;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -551,6 +553,15 @@ __device__ __noinline__ bool meet(uint32_t bar, int parity)
     return __all_sync(0xffffffffu, wait_for(bar, parity, 2 * kWaitNs)) != 0;
 }
 
+// The first half of a meeting: the warp waits for it later, before the next.
+__device__ __forceinline__ void arrive_at(uint32_t bar, int &meetings)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        mbar_arrive(bar);
+    ++meetings;
+}
+
 // One of `expect` arrivals of warps at a counter: true for the last one's lanes; it resets the
 // counter.  The release makes visible what the warp wrote before, the acquire what the others
 // did.
@@ -582,13 +593,16 @@ __device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const Stat
     float *wo = reinterpret_cast<float *>(base + S::kWo);
     float *wm = reinterpret_cast<float *>(base + S::kStat);   // [kWarps][ROWS] each: m, l, mo
     float *wl = wm + kWarps * ROWS, *wmo = wl + kWarps * ROWS;
+    const bool few = NT == 1 && p.G <= 4;
     const bool whole = of.n <= kWhole || (of.start >= lo && of.start + of.n <= hi);
     const int c0 = of.start / len, c1 = (of.start + of.n - 1) / len;
     float *part = p.parts + static_cast<size_t>(part_slot(c, c0)) * PART;
+    if (meetings > 0 && !__all_sync(0xffffffffu, wait_for(bar, (meetings - 1) & 1, 2 * kWaitNs)))
+        return false;   // the part before has been read from shared memory
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        // every warp's statistics, and the O of the warps from 2, then of warps 0 and 1; a warp
-        // sums its rows, a lane four dims
+        // every warp's statistics, and their O: of up to 4 rows all at once, else of the warps from
+        // 2, then of warps 0 and 1; a warp sums its rows, a lane four dims
         if (nt > 0 && !meet(bar, meetings++ & 1))   // wo is free again
             return false;
         st.put_stats(wm + warp * ROWS + nt * 8, wl + warp * ROWS + nt * 8, wmo + warp * ROWS + nt * 8, nt, lane);
@@ -596,15 +610,21 @@ __device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const Stat
         float m[kQuads], mo[kQuads];
 #pragma unroll
         for (int half = 1; half >= 0; --half) {
+            if (half == 0 && few)
+                break;
             if (half == 0 && !meet(bar, meetings++ & 1))   // wo is free again
                 return false;
-            if (warp >> 1 == half)
-                st.put_o(wo + (warp & 1) * 8 * kStride, nt, lane);
+            if (few)
+                st.put_o(wo + warp * 4 * kStride, nt, 4, lane);
+            else if (warp >> 1 == half)
+                st.put_o(wo + (warp & 1) * 8 * kStride, nt, 8, lane);
             if (!meet(bar, meetings++ & 1))
                 return false;
 #pragma unroll
             for (int x = 0; x < kQuads; ++x) {
                 const int r8 = min(warp + kWarps * x, 7), row = nt * 8 + r8;
+                if (few && x > 0)
+                    continue;
                 if (half == 1) {
                     o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
                     m[x] = wm[row];
@@ -616,12 +636,13 @@ __device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const Stat
                     }
                 }
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    if (2 * half + w >= kWarps)
-                        break;
-                    const float mw = wmo[(2 * half + w) * ROWS + row];
+                for (int w = 0; w < kWarps; ++w) {
+                    if (!few && w >> 1 != half)
+                        continue;
+                    const float mw = wmo[w * ROWS + row];
                     const float f = mw == -INFINITY ? 0.f : ex2_approx(mw - mo[x]);
-                    const float4 v = *reinterpret_cast<const float4 *>(wo + (w * 8 + r8) * kStride + 4 * lane);
+                    const int at = few ? w * 4 + r8 : (w & 1) * 8 + r8;
+                    const float4 v = *reinterpret_cast<const float4 *>(wo + at * kStride + 4 * lane);
                     o[x].x = fmaf(f, v.x, o[x].x);
                     o[x].y = fmaf(f, v.y, o[x].y);
                     o[x].z = fmaf(f, v.z, o[x].z);
@@ -1064,15 +1085,15 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
 #pragma unroll 1
             for (; part < next; ++part) {
                 const Part of = parts[part % kMeta];
-                bool ok = finish_part<NT>(p, st, of, c, lo, hi, len, base, bar, meetings, warp, lane);
+                const bool ok = finish_part<NT>(p, st, of, c, lo, hi, len, base, bar, meetings, warp, lane);
                 if (part + 1 < next || (item.part & kEnd) == 0)
                     q.load(p, parts[(part + 1) % kMeta].pair, lane);
                 st.reset();
-                ok = ok && meet(bar, meetings++ & 1);   // shared memory is free again
                 if (!ok) {
                     give_up(p, lane);
                     return;
                 }
+                arrive_at(bar, meetings);   // the warp needs the part's shared memory no more
             }
             if (item.part & kEnd)
                 return;
