@@ -846,7 +846,8 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
     const int u0 = min(units, tid * per), u1 = min(units, u0 + per);
     bool bad = false;
     int mine = 0, n_first = 0;   // the thread's units' length, and its first one's items
-#pragma unroll 1
+    // loads of four in flight: 8000 pairs of 8 tiles 210 us (216 one by one)
+#pragma unroll 4
     for (int u = u0; u < u1; ++u) {
         const int n = pair_items(p, u * heads, &bad);
         n_first = u == u0 ? n : n_first;
