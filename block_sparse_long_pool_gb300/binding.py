@@ -5,7 +5,7 @@ the tensors it is given, passes their data pointers and the current CUDA stream 
 the C entry point of the same name, and raises ``SparsePoolError`` on a non-zero
 status.  Every step of the computation runs in the CUDA kernels; there is no CPU
 fallback, and a missing library raises at the first call.  The paged cache's three calls
-are marshalled by csrc/marshal.c, the same way: they are short enough that checking their
+are marshalled by csrc/marshal.cpp, the same way: they are short enough that checking their
 tensors in Python takes longer than they do.
 """
 from __future__ import annotations

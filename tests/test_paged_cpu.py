@@ -53,7 +53,13 @@ ATTN = dict(Q=FAKE, pages=FAKE, scale=FAKE, n_pages=32, table=FAKE, max_blocks=8
     ("sparse_paged_decode_attn_f8", ATTN, {"B": 32768}, UNSUPPORTED),
     ("sparse_paged_decode_attn_f8", ATTN, {"sm": float("nan")}, INVALID),
     ("sparse_paged_decode_attn_f8", ATTN, {"sm": float("inf")}, INVALID),
-    ("sparse_paged_decode_attn_f8", ATTN, {"n_pages": (1 << 25) + 1}, UNSUPPORTED)])
+    ("sparse_paged_decode_attn_f8", ATTN, {"n_pages": (1 << 25) + 1}, UNSUPPORTED),
+    # 128 pairs of 2^24 places each, 8 of them a pair's own: 2^31 in all
+    ("sparse_paged_decode_attn_f8", ATTN, {"B": 64, "k_tot": (1 << 24) - 8}, UNSUPPORTED),
+    ("sparse_paged_decode_attn_f8", ATTN, {"B": 64, "idx": None, "count": None, "max_blocks": (1 << 24) - 8}, UNSUPPORTED),
+    ("sparse_paged_decode_attn_f8", ATTN, {"max_blocks": 1 << 25}, UNSUPPORTED),
+    ("sparse_paged_decode_attn_f8", ATTN, {"k_tot": (1 << 25) + 1}, UNSUPPORTED),
+    ("sparse_paged_decode_attn_f8", ATTN, {"n_pages": 1 << 25, "B": 1, "H_q": 32, "H_kv": 32}, UNSUPPORTED)])
 def test_refusals(lib, name, good, change, code):
     args = {**good, **change}
     assert getattr(lib, name)(*args.values()) == code
