@@ -605,6 +605,35 @@ def test_attn_many_calls_of_a_full_grid():
         ref.assert_attn(a.O[rows], a.lse[rows], want, k * BLK)
 
 
+@pytest.mark.parametrize("G", [1, 4, 5, 8, 9, 16])
+def test_attn_many_short_parts_of_a_full_grid(G):
+    """1200 pairs of 0 to 20 blocks, so that a CTA ends several parts of its own and shares
+    the first and the last: the same bits each time, equal to the plain implementation."""
+    rng = np.random.default_rng(G)
+    B, H, max_blocks, n_pages = 150, 8, 20, 500
+    g = torch.Generator(device=DEV)
+    g.manual_seed(G)
+    pages = (torch.randn((n_pages, H, 2, BLK, D), generator=g, device=DEV) * 64).clamp(-448, 448).to(F8)
+    scale = torch.exp2(torch.randint(-8, -4, (n_pages, H, 2), generator=g, device=DEV).float())
+    table = torch.randint(0, n_pages, (B, max_blocks), generator=g, device=DEV, dtype=torch.int32)
+    lens = rng.integers(0, max_blocks * BLK + 1, B)
+    lens[rng.permutation(B)[:60]] = rng.integers(0, 3 * BLK, 60)
+    t_lens = i32(lens.tolist())
+    Q = torch.randn((B, H * G, D), generator=g, device=DEV).to(torch.bfloat16)
+    a = Attn(B, H * G, H)
+    for i in range(60):
+        binding.sparse_paged_decode_attn_f8(Q, pages, scale, table, t_lens, a.O, a.ws, lse=a.lse, status=a.status)
+        if i == 0:
+            first = a.O.clone(), a.lse.clone()
+    torch.cuda.synchronize()
+    assert a.status.item() == 0 and torch.equal(a.O, first[0]) and torch.equal(a.lse, first[1])
+    values, scales = ref.f8_values(pages), ref.f64(scale)
+    for b in (0, 1, 74, 75, 148, 149, int(lens.argmax()), int(lens.argmin())):
+        rows = slice(b, b + 1)
+        want = ref.attn(ref.f64(Q[rows]), values, scales, table[rows].cpu().numpy(), lens[rows])
+        ref.assert_attn(a.O[rows], a.lse[rows], want, max_blocks * BLK)
+
+
 # ---------------------------------------------------------------- refusals of the binding
 
 
