@@ -25,13 +25,13 @@
 // scales are; the row sum l uses the fp32 weights 2^(s - m).
 //
 // What bounds it.  The tiles' stream in the middle, latency at both ends.  On GB300, back to back
-// in a graph: 537 MB (32K tokens x 8 requests x 8 KV heads, G = 4) in 87.5 us, 6.1 TB/s, 0.90 of
+// in a graph: 537 MB (32K tokens x 8 requests x 8 KV heads, G = 4) in 87.9 us, 6.1 TB/s, 0.90 of
 // the copy rate; of these about 3.5 us pass before the first tile is there (lengths, table,
 // load: three round trips), and 3 us after the last one in the merge of the pairs that the
-// CTAs share.  70.6 MB of selected blocks (64 pairs x 67) in 20.4 us, 2.1 MB (one request of 4K
-// tokens, 2 KV heads) in 9.7 us: those ends.  64 requests of 1 to 16K tokens in 39 us (0.62):
+// CTAs share.  70.6 MB of selected blocks (64 pairs x 67) in 20.5 us, 2.1 MB (one request of 4K
+// tokens, 2 KV heads) in 9.8 us: those ends.  64 requests of 1 to 16K tokens in 37 us (0.66):
 // each part of a pair ends with its warps waiting for one another.  A tile takes a warp about
-// 2900 cycles at G <= 8 and 3900 at G = 16 (537 MB in 104.6 us, 0.76): the conversions' half-rate
+// 2900 cycles at G <= 8 and 3900 at G = 16 (537 MB in 106 us, 0.74): the conversions' half-rate
 // instructions (cvt, prmt, shift) and the products' latency.
 #include <limits.h>
 #include <math.h>
@@ -846,7 +846,7 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
     const int u0 = min(units, tid * per), u1 = min(units, u0 + per);
     bool bad = false;
     int mine = 0, n_first = 0;   // the thread's units' length, and its first one's items
-    // loads of four in flight: 8000 pairs of 8 tiles 210 us (216 one by one)
+    // loads of four in flight: 8000 pairs of 8 tiles 2 % less than one by one
 #pragma unroll 4
     for (int u = u0; u < u1; ++u) {
         const int n = pair_items(p, u * heads, &bad);
@@ -897,6 +897,13 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
             return;
         const uint64_t pol = policy_evict_first();
         int it = 0, part = 0;          // the CTA's next item and part
+        // Where more pairs than CTAs end inside the ranges, each warp's ring is fed by itself, so
+        // that the warps which wait for one another at a part's end find their next tiles
+        // there: 64 requests of 1 to 16K tokens x 8 heads 37.0 us (39.0 in the list's order), 256 x
+        // 8 lists of 16 blocks 79 (96), 8000 of 8 blocks 167 (211).  Else in the list's order, in
+        // which an item's keys and values, 16 KB in one piece, leave one after the other: 8 pairs
+        // of 2048 tiles 51.5 us (53.5), 64 of 512 87 (88.2).
+        const bool apart = pairs > static_cast<int>(gridDim.x);
         bool stop = false, wrong = false;
         auto free_slot = [&](int slot, int fill) {
             return fill < kSlots || wait_for(empty + 8 * slot, (fill / kSlots - 1) & 1, kWaitNs);
@@ -998,30 +1005,70 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
                 if (lane < take)
                     items[(it + lane) % kMeta] = item;
                 __syncwarp();
+                if (!apart) {
 #pragma unroll 1
-                for (int j = 0; j < take && !stop; ++j) {
-                    const int u = __shfl_sync(0xffffffffu, unit, j), rows = __shfl_sync(0xffffffffu, item.rows, j);
-                    if (lane == 0) {
-                        const int ring = (it + j) % kWarps * kSlots, fill = (it + j) / kWarps * 2;
-                        const int k_slot = ring + fill % kSlots, v_slot = ring + (fill + 1) % kSlots;
-                        // (values have no record: both of their arrivals come with the load)
-                        if (j < ahead) {
-                            mbar_arrive(full + 8 * k_slot);   // the item record
-                            mbar_arrive(full + 8 * v_slot);
-                        } else {
-                            stop = !free_slot(k_slot, fill);
-                            if (!stop) {
-                                load(k_slot, 2 * u, rows);
-                                mbar_arrive(full + 8 * k_slot);
-                                stop = !free_slot(v_slot, fill + 1);
-                            }
-                            if (!stop) {
-                                load(v_slot, 2 * u + 1, rows);
+                    for (int j = 0; j < take && !stop; ++j) {
+                        const int u = __shfl_sync(0xffffffffu, unit, j), rows = __shfl_sync(0xffffffffu, item.rows, j);
+                        if (lane == 0) {
+                            const int ring = (it + j) % kWarps * kSlots, fill = (it + j) / kWarps * 2;
+                            const int k_slot = ring + fill % kSlots, v_slot = ring + (fill + 1) % kSlots;
+                            // (values have no record: both of their arrivals come with the load)
+                            if (j < ahead) {
+                                mbar_arrive(full + 8 * k_slot);   // the item record
                                 mbar_arrive(full + 8 * v_slot);
+                            } else {
+                                stop = !free_slot(k_slot, fill);
+                                if (!stop) {
+                                    load(k_slot, 2 * u, rows);
+                                    mbar_arrive(full + 8 * k_slot);
+                                    stop = !free_slot(v_slot, fill + 1);
+                                }
+                                if (!stop) {
+                                    load(v_slot, 2 * u + 1, rows);
+                                    mbar_arrive(full + 8 * v_slot);
+                                }
                             }
                         }
+                        stop = __shfl_sync(0xffffffffu, stop ? 1 : 0, 0) != 0;
                     }
-                    stop = __shfl_sync(0xffffffffu, stop ? 1 : 0, 0) != 0;
+                    it += take;
+                    continue;
+                }
+                // Lane w feeds warp w's ring: of the batch's items its own, keys then values, as the
+                // slots come free.
+                int j = lane < kWarps ? (lane + kWarps - it % kWarps) % kWarps : take, half = 0;
+                if (j < ahead) {
+                    const int ring = lane * kSlots;
+                    mbar_arrive(full + 8 * ring);         // the item record
+                    mbar_arrive(full + 8 * (ring + 1));   // (values have none)
+                    j += kWarps;
+                }
+                uint64_t since = 0;
+#pragma unroll 1
+                for (int idle_turns = 0; __any_sync(0xffffffffu, j < take);) {
+                    const int u = __shfl_sync(0xffffffffu, unit, j & 31), rows = __shfl_sync(0xffffffffu, item.rows, j & 31);
+                    bool fed = false;
+                    if (j < take) {
+                        const int fill = (it + j) / kWarps * 2 + half, slot = lane * kSlots + fill % kSlots;
+                        fed = fill < kSlots || mbar_test(empty + 8 * slot, (fill / kSlots - 1) & 1);
+                        if (fed) {
+                            load(slot, 2 * u + half, rows);
+                            mbar_arrive(full + 8 * slot);
+                            j += half * kWarps;
+                            half ^= 1;
+                        }
+                    }
+                    if (__any_sync(0xffffffffu, fed)) {
+                        idle_turns = 0;
+                    } else if (++idle_turns == 1024) {
+                        since = globaltimer();
+                    } else if (idle_turns > 1024) {
+                        stop = __any_sync(0xffffffffu, globaltimer() - since > kWaitNs);
+                        if (stop)
+                            break;
+                        idle_turns = 1025;
+                        __nanosleep(100);
+                    }
                 }
                 it += take;
             }

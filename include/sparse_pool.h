@@ -581,7 +581,7 @@ SPARSE_API int sparse_gather_offloaded(const uint16_t *k_host, const uint16_t *v
  *   4. row t of a granted request b gets tok_req = b, tok_pos = its position, slot_map = its
  *      slot; every other row (of requests not granted, and past cu_new[B]) gets -1 in all
  *      three, which sparse_paged_append_f8 skips.
- * The result does not depend on timing: no atomics, and pages go out in a fixed order.
+ * The result does not depend on timing: pages go out in a fixed order.
  *   seq_len, n_new   [B] int32.       block_table  [B][max_blocks] int32, entries added.
  *   free_pages       [n_pages] int32, the first *n_free are the list; entries added.
  *   n_free           one int32.       cu_new       [B + 1] int32, written.
