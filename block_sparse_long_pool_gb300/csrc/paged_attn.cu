@@ -53,8 +53,8 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 //   a range at least: 1 x 2 pairs of 64 tiles 9.7 us (3: 10.2; 2 and 6 before: 1.3 and 1.1 more), 8 pairs of 16
 //   tiles 9.8 us (2: 10.3, 6: 11.3): a merge over more CTAs against more tiles a warp;
 constexpr int kMinItems = 4;
-//   what a pair costs beside its items: 64 requests of 1 to 16K tokens 39.1 us (5: 38.5, 7: 38.6,
-//   9: 39.8), 32K tokens x 64 pairs 88.2 us (5: 90.1, 7: 89.7, 9: 88.7);
+//   what a pair costs beside its items: 64 requests of 1 to 16K tokens 37.3 us (3: 46.6, 5: 38.1,
+//   6: 37.5), 32K tokens x 64 pairs 88.4 us (3: 91.2, 5: 90.2, 6: 89.8);
 constexpr int kPairCost = 8;
 //   pairs of up to so many items stay with one CTA: 512 pairs of up to 8 tiles 16.3 us (0: 17.2), 32
 //   of 10 tiles 10.1 us and 64 of 12 tiles 10.6 us where 12 makes them 11.4 and 13.1 (kPairCost 7);
