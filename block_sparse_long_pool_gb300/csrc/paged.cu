@@ -147,7 +147,7 @@ __device__ __forceinline__ void plan_rows(const PlanParams &p, const int *cu, co
                 const int st = first[b];
                 if (st >= 0) {
                     req[j] = b;
-                    pos[j] = st + t + j - cu[b];
+                    pos[j] = st + (t + j - cu[b]);
                     const int blk = pos[j] / kBlk, used = (st + kBlk - 1) / kBlk;
                     int *at = p.block_table + static_cast<size_t>(b) * p.max_blocks + blk;
                     const int place = F - 1 - (npre[b] + blk - used);
@@ -770,9 +770,11 @@ extern "C" SPARSE_API int sparse_page_plan(const int *seq_len, const int *n_new,
                     n_pages, n_tok);
     if (B > kPlanMaxB)
         return fail(SPARSE_ERR_UNSUPPORTED, "%s: B=%d > %d", name, B, kPlanMaxB);
-    if (n_pages > kMaxPages || max_blocks > kMaxPages || n_tok > kMaxRows)
-        return fail(SPARSE_ERR_UNSUPPORTED, "%s: n_pages=%d or max_blocks=%d > %d, or n_tok=%d > %d", name, n_pages,
-                    max_blocks, kMaxPages, n_tok, kMaxRows);
+    if (n_pages > kMaxPages || n_tok > kMaxRows)
+        return fail(SPARSE_ERR_UNSUPPORTED, "%s: n_pages=%d > %d or n_tok=%d > %d", name, n_pages, kMaxPages, n_tok, kMaxRows);
+    // a position is at most 2^31 - 65, so that a block's count of it, (position + 63) / 64, fits 32 bits
+    if (max_blocks > INT_MAX / kBlk)
+        return fail(SPARSE_ERR_UNSUPPORTED, "%s: max_blocks=%d: token positions past 2^31", name, max_blocks);
     const PlanParams p{seq_len,    n_new,    block_table, free_pages, n_free, cu_new, start,      seq_len_out,
                        n_free_out, slot_map, tok_req,     tok_pos,    status, B,      max_blocks, n_pages, n_tok};
     sp_host::DeviceInfo dev;

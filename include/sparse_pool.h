@@ -594,7 +594,7 @@ SPARSE_API int sparse_gather_offloaded(const uint16_t *k_host, const uint16_t *v
  *                    ended one returns no pages), an *n_free outside [0, n_pages] (clamped),
  *                    more pages returned than the list holds (dropped) or a page id outside
  *                    [0, n_pages) (its rows get slot -1) is reported as SPARSE_ERR_BAD_INDEX.
- * B <= 4096; n_pages and max_blocks <= 2^25; n_tok <= 2^30; cu_new saturates at 2^31 - 1.
+ * B <= 4096; n_pages <= 2^25; max_blocks < 2^25; n_tok <= 2^30; cu_new saturates at 2^31 - 1.
  */
 SPARSE_API int sparse_page_plan(const int *seq_len, const int *n_new, int B, int *block_table, int max_blocks,
                                 int *free_pages, int n_pages, const int *n_free, int *cu_new, int *start,

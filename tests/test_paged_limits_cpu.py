@@ -1,0 +1,21 @@
+"""The paged 8-bit cache at the ends of what it accepts, without a GPU."""
+import pytest
+
+from block_sparse_long_pool_gb300 import binding, build
+from test_paged_cpu import FAKE, PLAN
+
+UNSUPPORTED = binding.SPARSE_ERR_UNSUPPORTED
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return binding.load()
+
+
+@pytest.mark.parametrize("max_blocks", [1 << 25, 2 ** 31 - 1])
+def test_plan_refuses_tables_past_31_bits_of_tokens(lib, max_blocks):
+    """2^25 blocks are 2^31 tokens: a length of 2^31 - 1 and one token more would not fit an int32
+    length, and a block count of it, (length + 63) / 64, would wrap."""
+    assert lib.sparse_page_plan(*{**PLAN, "max_blocks": max_blocks}.values()) == UNSUPPORTED
+    assert "max_blocks" in lib.sparse_last_error().decode()
