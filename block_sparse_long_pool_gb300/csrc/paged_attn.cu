@@ -564,7 +564,7 @@ __device__ __forceinline__ void arrive_at(uint32_t bar, int &meetings)
 
 // One of `expect` arrivals of warps at a counter: true for the last one's lanes; it resets the
 // counter.  The release makes visible what the warp wrote before, the acquire what the others
-// did.
+// did: lane 0's, handed on to the warp by the second __syncwarp (a shuffle orders no memory).
 __device__ __forceinline__ bool arrive_last(int *counter, int expect, int lane)
 {
     int prev = 0;
@@ -574,6 +574,7 @@ __device__ __forceinline__ bool arrive_last(int *counter, int expect, int lane)
         if (prev == expect - 1)
             *counter = 0;   // for the next call
     }
+    __syncwarp();
     return __shfl_sync(0xffffffffu, prev, 0) == expect - 1;
 }
 
@@ -949,6 +950,7 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
                 }
             }
             const int total = __shfl_sync(0xffffffffu, upto, group - 1);
+            __syncwarp();   // as for the items' records
             const unsigned has = __ballot_sync(0xffffffffu, cnt > 0);
             const int my_part = part + __popc(has & ((1u << lane) - 1));
             if (cnt > 0)
@@ -1002,6 +1004,7 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
                 }
                 item.ks = sc.x;
                 item.log2_vs = __log2f(sc.y);
+                __syncwarp();   // the records replaced have been read: the lanes that feed know by their slots
                 if (lane < take)
                     items[(it + lane) % kMeta] = item;
                 __syncwarp();
