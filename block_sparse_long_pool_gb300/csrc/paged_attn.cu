@@ -48,6 +48,7 @@ constexpr int kCtasPerSm = 2;
 constexpr int kStride = kD + 4;                   // floats a row of the warps' states
 constexpr int kMeta = 64;                         // item and part records: 32 being written + the ring's
 constexpr float kWeightBits = 12.f;               // weights reach 2^12: f16 holds them down to 2^-24
+constexpr float kFar = 100.f;                     // log2 of the largest factor from weights to O's
 constexpr uint64_t kWaitNs = 2000000000ull;
 // How the list is cut, in items (tiles).  Measured back to back in a graph:
 //   a range at least: 1 x 2 pairs of 64 tiles 9.7 us (3: 10.2; 2 and 6 before: 1.3 and 1.1 more), 8 pairs of 16
@@ -365,17 +366,20 @@ __device__ __forceinline__ float weigh(float (&s)[N], float mul, float log2_vs, 
     mx *= mul;
     const float m_new = fmaxf(row_m, mx), mo_new = fmaxf(row_mo, mx + log2_vs - kWeightBits);
     const float m_use = m_new == -INFINITY ? 0.f : m_new, mo_use = mo_new == -INFINITY ? 0.f : mo_new;
-    float l = row_l * ex2_approx(row_m - m_use);
     const float alpha = ex2_approx(row_mo - mo_use);
-    // from units of 2^m to 2^mo; the bound is only reached by weights below 2^-100
-    const float to_o = ex2_approx(fminf(log2_vs + (m_use - mo_use), 112.f));
+    // From units of 2^m to 2^mo by a factor of at most 2^kFar: weights that flush to zero (below 2^-126)
+    // are then below 2^-26, which f16 rounds to zero too.  Where this page's values are larger than
+    // the best scores' pages' by more than that, the weights are first lifted by the rest: those of
+    // O are at most 2^kWeightBits, so that the lifted ones stay below 2^(kWeightBits - kFar).
+    const float far = log2_vs + (m_use - mo_use), lift = fmaxf(far - kFar, 0.f), to_o = ex2_approx(fminf(far, kFar));
+    float l = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const float w = ex2_approx(fmaf(s[i], mul, -m_use));
+        const float w = ex2_approx(fmaf(s[i], mul, lift - m_use));
         l += w;
         s[i] = w * to_o;
     }
-    row_l = l;
+    row_l = fmaf(l, ex2_approx(-lift), row_l * ex2_approx(row_m - m_use));
     row_m = m_new;
     row_mo = mo_new;
     return alpha;

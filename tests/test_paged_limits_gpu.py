@@ -6,7 +6,7 @@ import torch
 
 import paged_utils as ref
 from block_sparse_long_pool_gb300 import binding
-from test_paged_gpu import BLK, DEV, Plan, i32
+from test_paged_gpu import BLK, D, DEV, F8, Attn, Cache, Plan, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +43,47 @@ def test_plan_of_the_largest_table(n_tok):
         assert np.array_equal(s.pos.cpu().numpy(), pos) and np.array_equal(s.slot.cpu().numpy(), page * BLK + pos % BLK)
         assert torch.equal(s.table[0, used:], i32(np.arange(max_blocks - used)))
         s.table.copy_(keep)
+
+
+# ---------------------------------------------------------------- attention
+
+
+def far_case(G, blocks, last, seed):
+    """One request whose pages' scores and value scales differ by up to 2^230: what one loses by its
+    softmax weight it gains by its values.  Scores in log2 units: block j's keys give about
+    -level[j]; its value scale is 2^vs[j]."""
+    rng = np.random.default_rng(seed)
+    n = len(blocks) * BLK - (BLK - last)
+    c = Cache(rng, len(blocks) + 1, 1)
+    table = rng.permutation(len(blocks) + 1)[:len(blocks)][None].astype(np.int32)
+    x = np.zeros((len(blocks) + 1, BLK, D), np.float32)
+    x[:, :, 1:] = rng.standard_normal((len(blocks) + 1, BLK, D - 1))
+    for j, (level, vs) in enumerate(blocks):
+        x[table[0, j], :, 0] = level             # the query's first element is -1
+        c.scale[int(table[0, j]), 0, 1] = 2.0 ** vs
+    c.pages[:, 0, 0] = torch.as_tensor(x, device=DEV).to(F8)
+    c.scale[:, 0, 0] = 1.0
+    Q = rng.standard_normal((1, G, D)) * 0.125   # scores spread by a few log2 units
+    Q[:, :, 0] = -1.0
+    return c, table, [n], ref.bf16(Q, DEV)
+
+
+@pytest.mark.parametrize("G", [1, 4, 8, 13, 16])
+@pytest.mark.parametrize("last", [BLK, 37])
+@pytest.mark.parametrize("blocks", [
+    [(0, -118), (120, 110)], [(120, 110), (0, -118)],                 # 2^228 apart: the far block is O
+    [(0, -118), (208, 110)], [(208, 110), (0, -118)],                 # its weights below 2^-126, its part 2^20 of O
+    [(0, -100), (112, 6)], [(0, -60), (96, 40), (120, 64)],           # comparable parts of O
+    [(0, -118), (224, 110), (104, -10)] * 2, [(52, 0), (0, -48), (104, 44)] * 20,
+    # 8 blocks or fewer stay with one CTA: the same warp meets both kinds
+    [(0, -118)] * 4 + [(120, 110)] * 4, [(120, 110)] * 3 + [(0, -118)] * 3, [(0, -118)] * 3 + [(208, 110)] * 3,
+    [(208, 110)] * 4 + [(0, -118)] * 4, [(0, -100)] * 3 + [(112, 6)] * 3, [(0, -60)] * 3 + [(96, 40)] * 3,
+    [(0, 110), (120, -118)]])
+def test_attn_pages_whose_scales_are_far_apart_in_one_request(blocks, last, G):
+    c, table, lens, Q = far_case(G, blocks, last, len(blocks) * 100 + G)
+    a = Attn(1, G, 1)
+    a.call(Q, c, i32(table), i32(lens), scale=float(np.log(2.0)))
+    torch.cuda.synchronize()
+    want = ref.attn(ref.f64(Q), ref.f8_values(c.pages), ref.f64(c.scale), table, lens, sm_scale=float(np.float32(np.log(2.0))))
+    ref.assert_attn(a.O, a.lse, want, lens[0])
+    assert a.status.item() == 0
