@@ -549,6 +549,7 @@ __device__ __forceinline__ void append_short(const PagedAppendParams &p, int t, 
     for (int r = 0; r < kShort; ++r)
         if (r < n)
             *reinterpret_cast<uint2 *>(dst + (off + r) * kD) = round8(x[r], inv, inf);
+    __syncwarp();   // every lane has read the old scale
     if (c == 0)
         p.kv_scale[unit] = scale;
     if (kt != nullptr && kv == 0) {

@@ -6,7 +6,7 @@ import torch
 
 import paged_utils as ref
 from block_sparse_long_pool_gb300 import binding
-from test_paged_gpu import BLK, D, DEV, F8, Attn, Cache, Plan, i32
+from test_paged_gpu import BLK, D, DEV, F8, Attn, Cache, Plan, i32, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -43,6 +43,34 @@ def test_plan_of_the_largest_table(n_tok):
         assert np.array_equal(s.pos.cpu().numpy(), pos) and np.array_equal(s.slot.cpu().numpy(), page * BLK + pos % BLK)
         assert torch.equal(s.table[0, used:], i32(np.arange(max_blocks - used)))
         s.table.copy_(keep)
+
+
+# ---------------------------------------------------------------- append
+
+
+def test_append_of_single_rows_is_the_same_in_every_call():
+    """512 runs of one row, of which half make their page's scale grow, on equal caches: the old
+    scale is read by all of a warp's lanes before one of them replaces it."""
+    rng = np.random.default_rng(31)
+    n, H = 512, 4
+    first = None
+    k, v = rows(rng, n, H, True)
+    k = k * torch.as_tensor(2.0 ** rng.integers(-6, 7, n), device=DEV).to(torch.bfloat16)[:, None, None]
+    slots = [p * BLK + int(r) for p, r in enumerate(rng.integers(1, BLK, n))]
+    c = Cache(rng, n, H)
+    was, old = c.pages.clone(), c.scale.clone()
+    want = ref.append(*c.state()[:2], ref.f64(k), ref.f64(v), slots)
+    grown = (want[1] > ref.f64(old)).mean()
+    assert 0.2 < grown < 0.8
+    t = i32(slots)
+    for _ in range(50):
+        c.pages.copy_(was)
+        c.scale.copy_(old)
+        binding.sparse_paged_append_f8(c.pages, c.scale, k, v, t, status=c.status)
+        now = c.pages.view(torch.uint8).clone(), c.scale.clone()
+        first = first or now
+        assert torch.equal(now[0], first[0]) and torch.equal(now[1], first[1])
+    c.check((want[0], want[1], None))
 
 
 # ---------------------------------------------------------------- attention
