@@ -464,6 +464,26 @@ __device__ __forceinline__ uint2 round8(const uint4 &x, float inv, bool inf)
     return make_uint2(f8x4_pack(f[0], f[1], f[2], f[3]), f8x4_pack(f[4], f[5], f[6], f[7]));
 }
 
+// As round8 for rows first, first + step, ... below n of `src` (read again: the caller's registers are
+// indexed by unrolled loops alone), divided by a scale that is no power of two, as pages that
+// this append did not write may have.  fp32 cannot hold such quotients, nor the reciprocal: a
+// multiplication by it puts 175 / 7 above the tie that it is.
+__device__ __noinline__ void divide_rows(const uint16_t *src, long long stride, uint8_t *dst, int first, int step, int n, float scale)
+{
+#pragma unroll 1
+    for (int r = first; r < n; r += step) {
+#pragma unroll 1
+        for (int j = 0; j < 8; j += 2) {
+            const uint32_t w = *reinterpret_cast<const uint32_t *>(src + r * stride + j);
+            float lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xffff0000u);
+            lo += lo - lo;   // NaN for infinities
+            hi += hi - hi;
+            *reinterpret_cast<uint16_t *>(dst + r * kD + j) =
+                static_cast<uint16_t>(f8x2_pack(quotient(lo, scale), quotient(hi, scale)));
+        }
+    }
+}
+
 __device__ __forceinline__ void add8(float (&sum)[8], const uint4 &x)
 {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -545,10 +565,14 @@ __device__ __forceinline__ void append_short(const PagedAppendParams &p, int t, 
     uint8_t *dst = p.kv_pages + unit * (kBlk * kD) + c * 8;
     if (off > 0 && old != scale)
         rescale_rows(dst, 0, 1, off, old * inv);
+    if (is_pow2(scale)) {
 #pragma unroll
-    for (int r = 0; r < kShort; ++r)
-        if (r < n)
-            *reinterpret_cast<uint2 *>(dst + (off + r) * kD) = round8(x[r], inv, inf);
+        for (int r = 0; r < kShort; ++r)
+            if (r < n)
+                *reinterpret_cast<uint2 *>(dst + (off + r) * kD) = round8(x[r], inv, inf);
+    } else {
+        divide_rows(src, stride, dst + off * kD, 0, 1, n, scale);
+    }
     __syncwarp();   // every lane has read the old scale
     if (c == 0)
         p.kv_scale[unit] = scale;
@@ -632,10 +656,14 @@ __device__ __forceinline__ void append_long(const PagedAppendParams &p, int t, i
     uint8_t *dst = p.kv_pages + unit * (kBlk * kD) + c * 8;
     if (off > 0 && old != scale)
         rescale_rows(dst, r0, 8, off, old * inv);
+    if (is_pow2(scale)) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (r0 + 8 * i < n)
-            *reinterpret_cast<uint2 *>(dst + (off + r0 + 8 * i) * kD) = round8(x[i], inv, inf);
+        for (int i = 0; i < 8; ++i)
+            if (r0 + 8 * i < n)
+                *reinterpret_cast<uint2 *>(dst + (off + r0 + 8 * i) * kD) = round8(x[i], inv, inf);
+    } else {
+        divide_rows(src, stride, dst + off * kD, r0, 8, n, scale);
+    }
     if (tid == 0)
         p.kv_scale[unit] = scale;
     if (kt != nullptr) {

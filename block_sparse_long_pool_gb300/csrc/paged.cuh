@@ -46,11 +46,42 @@ __device__ __forceinline__ float2 f8x2_to_float2(uint32_t x)
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
-// Four e4m3 values times `ratio`, rounded again.
+__device__ __forceinline__ bool is_pow2(float x)
+{
+    return (__float_as_uint(x) & 0x7fffffu) == 0;
+}
+
+// An fp32 value that stands for q + rest, |rest| within a step of q, only its sign known: its last bit
+// odd where there is a rest (rounding to odd), so that rounded again to the 4 bits of e4m3 it
+// gives what the exact value gives, ties told from values next to them.
+__device__ __forceinline__ float round_to_odd(float q, float rest)
+{
+    uint32_t u = __float_as_uint(q);
+    if (rest != 0.f)
+        u = (u - ((__float_as_uint(rest) ^ u) >> 31)) | 1u;
+    return __uint_as_float(u);
+}
+
+// x / s, and v * s, for s of any mantissa: to fp32, to odd.
+__device__ __forceinline__ float quotient(float x, float s)
+{
+    const float up = s < 1.f ? 0x1p64f : 1.f, q = x / s;   // the remainder stays a normal number
+    return round_to_odd(q, fmaf(-q, s * up, x * up));
+}
+
+__device__ __forceinline__ float product(float v, float s)
+{
+    const float q = v * s;
+    return round_to_odd(q, fmaf(v, s, -q));
+}
+
+// Four e4m3 values times `ratio`, rounded again; of a power of two the products are exact.
 __device__ __forceinline__ uint32_t f8x4_scaled(uint32_t w, float ratio)
 {
     const float2 a = f8x2_to_float2(w), b = f8x2_to_float2(w >> 16);
-    return f8x4_pack(a.x * ratio, a.y * ratio, b.x * ratio, b.y * ratio);
+    if (is_pow2(ratio))
+        return f8x4_pack(a.x * ratio, a.y * ratio, b.x * ratio, b.y * ratio);
+    return f8x4_pack(product(a.x, ratio), product(a.y, ratio), product(b.x, ratio), product(b.y, ratio));
 }
 
 // One launch with programmatic stream serialization: the kernel may be scheduled while the

@@ -73,6 +73,62 @@ def test_append_of_single_rows_is_the_same_in_every_call():
     c.check((want[0], want[1], None))
 
 
+@pytest.mark.parametrize("n", [1, 2, 3, 40])
+@pytest.mark.parametrize("old", [7.0, 0.3, 1.0 / 3, 3 * 2.0 ** -119, 1.9999998 * 2.0 ** 100, 5.0])
+def test_append_to_pages_with_other_scales(n, old):
+    """Pages whose scale is no power of two: rows are divided by it.  With a scale of 7, 175 is 25
+    units, a tie that goes to 24, where 175 times the rounded 1 / 7 is above it.  Row by row
+    every bf16 mantissa of e4m3's range, ties among them."""
+    rng = np.random.default_rng(n)
+    c = Cache(rng, 3, 2)
+    c.scale.fill_(old)
+    s = float(c.scale[0, 0, 0])
+    x = rng.integers(128, 256, (n, 2, D)) * 2.0 ** rng.integers(-16, 1, (n, 2, D))   # bf16, up to 255 units
+    x[:, :, ::3] = rng.integers(1, 29, x[:, :, ::3].shape)                          # whole numbers: ties at 17, 19, ...
+    k = ref.bf16(x * s if old in (7.0, 5.0) else x * 2.0 ** np.floor(np.log2(s)), DEV)
+    v = ref.bf16(-x * 2.0 ** np.floor(np.log2(s)), DEV)
+    if old == 7.0:
+        k[0, 0, 0] = 175.0
+    slots = [BLK + 9 + i for i in range(n)]
+    want = ref.append(*c.state()[:2], ref.f64(k), ref.f64(v), slots)
+    assert (want[1] == s).all()   # no scale grows
+    c.append(k, v, slots)
+    c.check((want[0], want[1], None))
+    if old == 7.0:
+        assert float(c.pages[1, 0, 0, 9, 0]) == 24.0
+    # a louder row: the scale grows to a power of two, and every row before is rounded again
+    k[0, 1, 5] = 500 * s
+    slots = [BLK + 9 + n]
+    want = ref.append(*c.state()[:2], ref.f64(k[:1]), ref.f64(v[:1]), slots)
+    assert want[1][1, 1, 0] > s
+    c.append(k[:1], v[:1], slots)
+    c.check((want[0], want[1], None))
+
+
+def test_append_rounds_quotients_and_products_once():
+    """Scales next to thirds and sevenths of powers of two, where x / scale lies within 2^-25 of a tie
+    that it is not: rounded to fp32 first it would become one."""
+    rng = np.random.default_rng(8)
+    base = np.array([1 / 3, 1 / 7, 3 / 5, 5 / 3, 7 / 9, 9 / 11, 15 / 17, 1 / 13]) * 4
+    near = np.float32(base)
+    scales = np.concatenate([near, np.nextafter(near, np.float32(8)), np.nextafter(near, np.float32(0))])
+    c = Cache(rng, len(scales), 1)
+    c.scale[:] = torch.as_tensor(scales, device=DEV)[:, None, None]
+    x = np.tile(np.arange(128, 256), (2 * len(scales), 1, 1)) * 0.25
+    x[1::2] *= 4
+    k, v = ref.bf16(x, DEV), ref.bf16(-x / 8, DEV)
+    slots = [p * BLK + 3 + i for p in range(len(scales)) for i in (0, 1)]
+    want = ref.append(*c.state()[:2], ref.f64(k), ref.f64(v), slots)
+    c.append(k, v, slots)
+    c.check((want[0], want[1], None))
+    # grown by a row each: all that the page holds, times old scale / new scale
+    k, v = ref.bf16(np.full((len(scales), 1, D), 3000.0), DEV), ref.bf16(np.full((len(scales), 1, D), 1500.0), DEV)
+    slots = [p * BLK + 5 for p in range(len(scales))]
+    want = ref.append(*c.state()[:2], ref.f64(k), ref.f64(v), slots)
+    c.append(k, v, slots)
+    c.check((want[0], want[1], None))
+
+
 # ---------------------------------------------------------------- attention
 
 
