@@ -88,6 +88,14 @@ __device__ __forceinline__ int saturate(long long v)
     return v > INT_MAX ? INT_MAX : static_cast<int>(v);
 }
 
+// An unsound input is reported in the place of a refusal too, so that a step with both reports the
+// same whichever thread is first.
+__device__ __forceinline__ void report_unsound(int *status)
+{
+    if (status != nullptr && atomicCAS(status, 0, SPARSE_ERR_BAD_INDEX) == SPARSE_ERR_NO_PAGES)
+        atomicCAS(status, SPARSE_ERR_NO_PAGES, SPARSE_ERR_BAD_INDEX);
+}
+
 // Pages that a granted request took.
 __device__ __forceinline__ int pages_taken(const int *cu, const int *first, int b)
 {
@@ -166,7 +174,7 @@ __device__ __forceinline__ void plan_rows(const PlanParams &p, const int *cu, co
                 *to[j] = page[j];
             const bool ok = page[j] >= 0 && page[j] < p.n_pages;
             if (from[j] != nullptr && !ok)
-                report(p.status, SPARSE_ERR_BAD_INDEX);
+                report_unsound(p.status);
             slot[j] = ok ? page[j] * kBlk + pos[j] % kBlk : -1;
         }
         if (R == 4 && t + 3 < p.n_tok) {
@@ -296,7 +304,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanParam
     __syncthreads();   // of cu, first, npre, relpre and taken
     if (blockIdx.x == 0) {
         if (bad)
-            report(p.status, SPARSE_ERR_BAD_INDEX);
+            report_unsound(p.status);
         if (refused)
             report(p.status, SPARSE_ERR_NO_PAGES);
         if (tid == 0) {

@@ -593,7 +593,8 @@ SPARSE_API int sparse_gather_offloaded(const uint16_t *k_host, const uint16_t *v
  *   status           a length outside [0, 64 max_blocks] (the request is not granted; an
  *                    ended one returns no pages), an *n_free outside [0, n_pages] (clamped),
  *                    more pages returned than the list holds (dropped) or a page id outside
- *                    [0, n_pages) (its rows get slot -1) is reported as SPARSE_ERR_BAD_INDEX.
+ *                    [0, n_pages) (its rows get slot -1) is reported as SPARSE_ERR_BAD_INDEX,
+ *                    also where the word holds SPARSE_ERR_NO_PAGES, of this step or before.
  * B <= 4096; n_pages <= 2^25; max_blocks < 2^25; n_tok <= 2^30; cu_new saturates at 2^31 - 1.
  */
 SPARSE_API int sparse_page_plan(const int *seq_len, const int *n_new, int B, int *block_table, int max_blocks,

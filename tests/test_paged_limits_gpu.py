@@ -171,3 +171,45 @@ def test_attn_pages_whose_scales_are_far_apart_in_one_request(blocks, last, G):
     want = ref.attn(ref.f64(Q), ref.f8_values(c.pages), ref.f64(c.scale), table, lens, sm_scale=float(np.float32(np.log(2.0))))
     ref.assert_attn(a.O, a.lse, want, lens[0])
     assert a.status.item() == 0
+
+
+# ---------------------------------------------------------------- what the status word says
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("n_tok", [1000, 4000])
+def test_plan_with_an_unsound_input_and_a_refusal_reports_the_unsound_one(n_tok, in_place):
+    """Each is found by another thread, CTA or launch; which one is reported does not depend on which
+    of them is first."""
+    B = 512
+    table = np.zeros((B, 2), np.int32)
+    table[:, 0] = np.arange(B)
+    bad = binding.SPARSE_ERR_BAD_INDEX
+    for at, refused in ((B - 1, 0), (0, B - 1), (300, 299)):
+        for kind in ("length", "page"):
+            lens = np.full(B, 60)
+            new = np.ones(B, np.int64)
+            new[refused] = 200                       # past its table
+            t = table.copy()
+            if kind == "length":
+                lens[at] = -1
+            else:
+                t[at, 0] = B + 7                     # found by the row that is written there
+            s = Plan(lens, t, np.full(B, -1), 0, n_tok)
+            s.n_new.copy_(i32(new))
+            for _ in range(20):
+                s.seq_len.copy_(i32(lens))
+                s.status.zero_()
+                s.call(in_place)
+                assert s.status.item() == bad, (kind, at)
+
+
+def test_an_unsound_input_of_a_later_step_replaces_a_refusal():
+    """A refusal is an ordinary end of a step; what follows it on the same word may not be."""
+    s = Plan([60, 60], np.array([[0], [1]], np.int32), np.full(2, -1), 0, 8)
+    for new, lens, want in (([9, 1], [60, 60], binding.SPARSE_ERR_NO_PAGES), ([1, 1], [60, 65], binding.SPARSE_ERR_BAD_INDEX),
+                            ([9, 1], [60, 60], binding.SPARSE_ERR_BAD_INDEX)):
+        s.n_new.copy_(i32(new))
+        s.seq_len.copy_(i32(lens))
+        s.call()
+        assert s.status.item() == want
