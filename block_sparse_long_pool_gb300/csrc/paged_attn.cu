@@ -66,7 +66,9 @@ constexpr int kDirect = 32;
 constexpr int kGroup = 12;
 
 constexpr int kMaxPairs = 65535;
-constexpr int kCounters = 2 * kDirect + kMaxPairs + 1;   // arrival counts of a warp's rows
+// Words a warp in the workspace: arrival counts of its rows, and one more.  The first of all says
+// that a call gave up and left counts behind; the counts are those after it.
+constexpr int kCounters = 2 * kDirect + kMaxPairs + 1;
 
 // What the warp that takes an item needs to know of it.
 struct Item {
@@ -133,6 +135,7 @@ struct PagedAttnParams {
     uint16_t *O;
     float *lse;
     int *status;
+    int *gave_up;      // not zero: a call gave up, and the workspace has to be zeroed
     int *arrivals;     // a warp: [2 * kDirect] of groups of CTAs, then [pairs]; zero between calls
     float *parts;      // [2 * CTAs][part_floats]
     float scale_log2;
@@ -789,12 +792,22 @@ __device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const Stat
     return true;
 }
 
-// A wait ran out: report it, and stay for longer than any load in flight takes to land in
+// A call that gave up leaves counts behind, with which later merges come too early: nothing milder
+// that the word holds may hide it.
+__device__ __forceinline__ void report_timeout(int *status)
+{
+    if (status != nullptr)
+        atomicExch(status, SPARSE_ERR_TIMEOUT);
+}
+
+// A wait ran out: report it, in the workspace too, for calls whose caller did not look; and stay for longer than any load in flight takes to land in
 // this CTA's shared memory.
 __device__ __forceinline__ void give_up(const PagedAttnParams &p, int lane)
 {
-    if (lane == 0)
-        report(p.status, SPARSE_ERR_TIMEOUT);
+    if (lane == 0) {
+        atomicExch(p.gave_up, 1);
+        report_timeout(p.status);
+    }
     for (int i = 0; i < 16; ++i)
         __nanosleep(1000000);
 }
@@ -850,6 +863,7 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
     const int per = (units + kThreads - 1) / kThreads;
     const int u0 = min(units, tid * per), u1 = min(units, u0 + per);
     bool bad = false;
+    const int spoilt = blockIdx.x == 0 && tid == 0 ? *p.gave_up : 0;   // by a call before
     int mine = 0, n_first = 0;   // the thread's units' length, and its first one's items
     // loads of four in flight: 8000 pairs of 8 tiles 2 % less than one by one
 #pragma unroll 4
@@ -860,6 +874,8 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
     }
     if (bad && blockIdx.x == 0)
         report(p.status, SPARSE_ERR_BAD_INDEX);
+    if (spoilt != 0)
+        report_timeout(p.status);
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -1285,6 +1301,7 @@ extern "C" SPARSE_API int sparse_paged_decode_attn_f8(const uint16_t *Q, const u
                             lse,
                             status,
                             static_cast<int *>(workspace),
+                            static_cast<int *>(workspace) + 1,
                             reinterpret_cast<float *>(static_cast<char *>(workspace) + kCounterBytes),
                             s * 1.44269504088896340736f,   // log2(e): scores are exponentiated base 2
                             n_pages,

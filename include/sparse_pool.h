@@ -18,8 +18,8 @@
  *     void*; NULL = the legacy default stream).  Arguments are validated on the host
  *     before any launch; a rejected call launches nothing and returns a negative
  *     status.  Errors found on the device (bad block ids, a wait that timed out) are
- *     written to the optional int32 `status` word in device memory (first error wins,
- *     0 = OK) and never trap.
+ *     written to the optional int32 `status` word in device memory (first error wins
+ *     unless a call says otherwise, 0 = OK) and never trap.
  *   - Calls return SPARSE_OK or a negative SPARSE_ERR_* code; sparse_last_error()
  *     gives a message for the last failing call on the calling host thread.
  */
@@ -645,7 +645,11 @@ SPARSE_API int sparse_paged_append_f8(uint8_t *kv_pages, float *kv_scale, int n_
  *                lse = -inf.
  *   workspace    sparse_paged_decode_attn_f8_workspace_size() bytes, 16-byte aligned, all
  *                zero before the first call that uses it; every call leaves its counters
- *                zero again, but one that reports SPARSE_ERR_TIMEOUT: zero it again then.
+ *                zero again, but one that gives up waiting.  Such a call reports
+ *                SPARSE_ERR_TIMEOUT, whatever the status word held before, and leaves the
+ *                workspace's first 32-bit word non-zero: every call that uses the workspace
+ *                reports SPARSE_ERR_TIMEOUT until it is zeroed again, and their O and lse are
+ *                not to be used.  Without a status word nothing tells.
  *                Calls of any sizes may share a workspace that is large enough for each, but
  *                not at the same time.
  * Rows past seq_len in a request's last page are never used, whatever bytes they hold.

@@ -6,7 +6,7 @@ import torch
 
 import paged_utils as ref
 from block_sparse_long_pool_gb300 import binding
-from test_paged_gpu import BLK, D, DEV, F8, Attn, Cache, Plan, i32, rows
+from test_paged_gpu import BLK, D, DEV, F8, Attn, Cache, Plan, attn_case, i32, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -213,3 +213,26 @@ def test_an_unsound_input_of_a_later_step_replaces_a_refusal():
         s.seq_len.copy_(i32(lens))
         s.call()
         assert s.status.item() == want
+
+
+@pytest.mark.parametrize("G", [4, 16])
+def test_attn_on_a_workspace_whose_call_gave_up(G):
+    """The first word of the workspace as a call that gave up leaves it: every call reports it, over
+    anything milder, until the workspace is zeroed."""
+    rng = np.random.default_rng(G)
+    lens = [3000, 100]
+    c, table, Q = attn_case(rng, lens, 2, G)
+    want = ref.attn(ref.f64(Q), ref.f8_values(c.pages), ref.f64(c.scale), table, lens)
+    a = Attn(2, 2 * G, 2)
+    a.ws[:4].view(torch.int32).fill_(1)
+    for before, n in ((0, lens), (binding.SPARSE_ERR_BAD_INDEX, lens), (0, [3000, -1]), (0, [0, 0])):
+        a.status.fill_(before)
+        a.call(Q, c, i32(table), i32(n))
+        assert a.status.item() == binding.SPARSE_ERR_TIMEOUT, n
+    binding.sparse_paged_decode_attn_f8(Q, c.pages, c.scale, i32(table), i32(lens), a.O, a.ws)   # no status word
+    a.ws.zero_()
+    a.status.zero_()
+    a.call(Q, c, i32(table), i32(lens))
+    assert a.status.item() == 0
+    ref.assert_attn(a.O, a.lse, want, 3000)
+    assert not a.ws[:1 << 20].any()   # the counters and the word: zero after the call
