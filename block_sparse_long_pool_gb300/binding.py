@@ -22,7 +22,7 @@ LIB_PATH = os.path.join(_PKG, "libsparsepool.so")
 MARSHAL_PATH = os.path.join(_PKG, f"_marshal_{torch.__version__}.so")
 _lock = threading.Lock()
 _lib = None
-_marshal = None   # csrc/marshal.cpp, which passes the paged cache's tensors on
+_marshal = None   # csrc/marshal.cpp, which passes the paged cache's tensors on; loaded by its first call
 
 D = 128
 BLK = 64
@@ -89,27 +89,38 @@ class SparsePoolError(RuntimeError):
 
 def load(path: str = LIB_PATH):
     """Load libsparsepool.so (built in-tree by ``block_sparse_long_pool_gb300.build``)."""
-    global _lib, _marshal
+    global _lib
     with _lock:
         if _lib is not None:
             return _lib
-        for need in (path, MARSHAL_PATH):
-            if not os.path.exists(need):
-                raise RuntimeError(f"{need} is not built; run `python -m block_sparse_long_pool_gb300.build` "
-                                   "(there is no CPU fallback)")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is not built; run `python -m block_sparse_long_pool_gb300.build` "
+                               "(there is no CPU fallback)")
         lib = ctypes.CDLL(path)
         for name, (res, args) in SIGNATURES.items():
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args
-        spec = importlib.util.spec_from_file_location("_marshal", MARSHAL_PATH)
-        marshal = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(marshal)
-        marshal.setup(*(ctypes.cast(getattr(lib, f"sparse_{name}"), ctypes.c_void_p).value
-                        for name in ("page_plan", "paged_append_f8", "paged_decode_attn_f8")))
-        _marshal = marshal
         _lib = lib
         return lib
+
+
+def _load_marshal():
+    """The module of the paged cache's calls, which reads this torch version's tensor objects; the
+    other calls do without it."""
+    global _marshal
+    lib = load()
+    with _lock:
+        if _marshal is None:
+            if not os.path.exists(MARSHAL_PATH):
+                raise RuntimeError(f"{MARSHAL_PATH} is not built for this torch; run "
+                                   "`python -m block_sparse_long_pool_gb300.build`")
+            spec = importlib.util.spec_from_file_location("_marshal", MARSHAL_PATH)
+            marshal = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(marshal)
+            marshal.setup(*(ctypes.cast(getattr(lib, f"sparse_{name}"), ctypes.c_void_p).value
+                            for name in ("page_plan", "paged_append_f8", "paged_decode_attn_f8")))
+            _marshal = marshal
 
 
 def status_string(status: int) -> str:
@@ -507,8 +518,8 @@ def _explain(idx, dtype, shape, **tensors):
 def _passed(name, idx, stream, *args) -> bool:
     """Calls ``name`` on device ``idx``, which need not be the current one; false where marshal.cpp
     refused a tensor, and nothing was called."""
-    if _lib is None:
-        load()
+    if _marshal is None:
+        _load_marshal()
     call = getattr(_marshal, name)
     if idx == torch._C._cuda_getDevice():
         rc = call(idx, torch._C._cuda_getCurrentRawStream(idx) if stream is None else stream.cuda_stream, *args)

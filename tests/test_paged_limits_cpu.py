@@ -19,3 +19,18 @@ def test_plan_refuses_tables_past_31_bits_of_tokens(lib, max_blocks):
     length, and a block count of it, (length + 63) / 64, would wrap."""
     assert lib.sparse_page_plan(*{**PLAN, "max_blocks": max_blocks}.values()) == UNSUPPORTED
     assert "max_blocks" in lib.sparse_last_error().decode()
+
+
+def test_only_the_paged_calls_need_the_module_that_marshals_them(monkeypatch, tmp_path):
+    """It is built for one version of torch: without it (another torch) every other call loads."""
+    build.build()
+    monkeypatch.setattr(binding, "MARSHAL_PATH", str(tmp_path / "absent.so"))
+    monkeypatch.setattr(binding, "_marshal", None)
+    monkeypatch.setattr(binding, "_lib", None)
+    assert binding.load().sparse_version() >= 100
+    assert binding.status_string(binding.SPARSE_ERR_NO_PAGES)
+    with pytest.raises(RuntimeError, match="absent.so is not built"):
+        binding._passed("page_plan", 0, None)
+    monkeypatch.undo()
+    binding._load_marshal()
+    assert binding._marshal is not None
