@@ -3,19 +3,19 @@
 Each translation unit is compiled by nvcc in parallel, then linked into
 ``block_sparse_long_pool_gb300/libsparsepool.so``.  No cmake, no torch extension
 machinery: the product is a plain C-ABI shared library.  ``_marshal_<torch version>.so`` beside
-it, from csrc/marshal.cpp by g++, passes tensors from Python to three of its calls.
+it, from csrc/marshal.cpp by g++, passes tensors from Python to three of its calls; it is left
+out where there is no torch, which the library does not need.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
 import sysconfig
-
-import torch
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -23,7 +23,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsparsepool.so")
-MARSHAL = os.path.join(PKG, f"_marshal_{torch.__version__}.so")   # reads that version's tensor objects
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -47,9 +46,11 @@ def _stale(obj: str, src: str, deps: list[str]) -> bool:
 
 
 def build_marshal(verbose: bool = False, force: bool = False) -> str:
+    import torch
+    out = os.path.join(PKG, f"_marshal_{torch.__version__}.so")   # reads that version's tensor objects
     src = os.path.join(CSRC, "marshal.cpp")
-    if force or _stale(MARSHAL, src, [os.path.join(INCLUDE, "sparse_pool.h"), os.path.abspath(__file__)]):
-        tmp = MARSHAL + f".{os.getpid()}.tmp"
+    if force or _stale(out, src, [os.path.join(INCLUDE, "sparse_pool.h"), os.path.abspath(__file__)]):
+        tmp = out + f".{os.getpid()}.tmp"
         root = os.path.dirname(torch.__file__)
         cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-Wall", "-std=c++17", "-shared", "-fPIC",
                "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}",
@@ -61,8 +62,8 @@ def build_marshal(verbose: bool = False, force: bool = False) -> str:
             sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
         if r.returncode != 0:
             raise RuntimeError("g++ failed on marshal.cpp")
-        os.replace(tmp, MARSHAL)
-    return MARSHAL
+        os.replace(tmp, out)
+    return out
 
 
 def build(verbose: bool = False, extra=(), force: bool = False) -> str:
@@ -79,7 +80,7 @@ def build(verbose: bool = False, extra=(), force: bool = False) -> str:
         if force or _stale(obj, src, deps):
             jobs.append([cc] + flags(extra) + ["-c", src, "-o", obj])
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 4))) as ex:
-        marshal = ex.submit(build_marshal, verbose, force)
+        marshal = ex.submit(build_marshal, verbose, force) if importlib.util.find_spec("torch") else None
         results = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
     for cmd, r in zip(jobs, results):
         if verbose or r.returncode != 0:
@@ -94,7 +95,8 @@ def build(verbose: bool = False, extra=(), force: bool = False) -> str:
             sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             raise RuntimeError("link failed")
         os.replace(tmp, LIB)
-    marshal.result()
+    if marshal is not None:
+        marshal.result()
     return LIB
 
 

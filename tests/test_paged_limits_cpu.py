@@ -1,4 +1,8 @@
 """The paged 8-bit cache at the ends of what it accepts, without a GPU."""
+import ctypes
+import subprocess
+import sys
+
 import pytest
 
 from block_sparse_long_pool_gb300 import binding, build
@@ -34,3 +38,16 @@ def test_only_the_paged_calls_need_the_module_that_marshals_them(monkeypatch, tm
     monkeypatch.undo()
     binding._load_marshal()
     assert binding._marshal is not None
+
+
+def test_the_library_builds_without_torch(tmp_path):
+    """A C program's user needs nvcc alone: linked here into a place of its own."""
+    build.build()
+    code = ("import sys; sys.modules['torch'] = None\n"
+            "from block_sparse_long_pool_gb300 import build\n"
+            f"build.LIB = {str(tmp_path / 'lib.so')!r}\n"
+            "print(build.build())")
+    r = subprocess.run([sys.executable, "-c", code], cwd=build.ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    assert r.stdout.strip() == str(tmp_path / "lib.so")
+    assert ctypes.CDLL(r.stdout.strip()).sparse_version() >= 100
