@@ -1268,8 +1268,10 @@ extern "C" SPARSE_API int sparse_paged_decode_attn_f8(const uint16_t *Q, const u
         (blk_idx != nullptr && k_tot < 1))
         return fail(SPARSE_ERR_INVALID_ARG, "%s: bad size (B=%d H_q=%d H_kv=%d n_pages=%d max_blocks=%d k_tot=%d)", name, B,
                     H_q, H_kv, n_pages, max_blocks, k_tot);
-    if (!isfinite(scale))
-        return fail(SPARSE_ERR_INVALID_ARG, "%s: scale is not finite", name);
+    // scores are exponentiated base 2
+    const float scale_log2 = (scale == 0.f ? 1.f / sqrtf(static_cast<float>(kD)) : scale) * 1.44269504088896340736f;
+    if (!isfinite(scale_log2))
+        return fail(SPARSE_ERR_INVALID_ARG, "%s: scale * log2(e) is not finite", name);
     if (!sizes_ok(B, H_q, H_kv) || n_pages > kMaxPages || max_blocks > kMaxPages || (blk_idx != nullptr && k_tot > kMaxPages))
         return fail(SPARSE_ERR_UNSUPPORTED, "%s: G=%d > 16, B*H_kv=%lld > 65535, or n_pages, max_blocks or k_tot > %d", name,
                     H_q / H_kv, static_cast<long long>(B) * H_kv, kMaxPages);
@@ -1290,7 +1292,6 @@ extern "C" SPARSE_API int sparse_paged_decode_attn_f8(const uint16_t *Q, const u
         rc = sp_host::make_page_tensor_map(&map, kv_pages, 2LL * n_pages * H_kv);
     if (rc != SPARSE_OK)
         return rc;
-    const float s = scale == 0.f ? 1.f / sqrtf(static_cast<float>(kD)) : scale;
     const PagedAttnParams p{Q,
                             kv_scale,
                             block_table,
@@ -1303,7 +1304,7 @@ extern "C" SPARSE_API int sparse_paged_decode_attn_f8(const uint16_t *Q, const u
                             static_cast<int *>(workspace),
                             static_cast<int *>(workspace) + 1,
                             reinterpret_cast<float *>(static_cast<char *>(workspace) + kCounterBytes),
-                            s * 1.44269504088896340736f,   // log2(e): scores are exponentiated base 2
+                            scale_log2,
                             n_pages,
                             max_blocks,
                             k_tot,

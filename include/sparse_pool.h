@@ -642,7 +642,7 @@ SPARSE_API int sparse_paged_append_f8(uint8_t *kv_pages, float *kv_scale, int n_
  *                sparse_select_topk writes them), or NULL: every block of every request
  *                (count and k_tot are then not used).
  *   Q, O, lse, scale, seq_len  as for sparse_decode_attn: a row with no token gets O = 0 and
- *                lse = -inf.
+ *                lse = -inf.  scale * log2(e) is finite in fp32 (|scale| <= 2.3e38).
  *   workspace    sparse_paged_decode_attn_f8_workspace_size() bytes, 16-byte aligned, all
  *                zero before the first call that uses it; every call leaves its counters
  *                zero again, but one that gives up waiting.  Such a call reports

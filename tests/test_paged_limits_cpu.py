@@ -6,9 +6,9 @@ import sys
 import pytest
 
 from block_sparse_long_pool_gb300 import binding, build
-from test_paged_cpu import FAKE, PLAN
+from test_paged_cpu import ATTN, PLAN
 
-UNSUPPORTED = binding.SPARSE_ERR_UNSUPPORTED
+INVALID, UNSUPPORTED = binding.SPARSE_ERR_INVALID_ARG, binding.SPARSE_ERR_UNSUPPORTED
 
 
 @pytest.fixture(scope="module")
@@ -23,6 +23,13 @@ def test_plan_refuses_tables_past_31_bits_of_tokens(lib, max_blocks):
     length, and a block count of it, (length + 63) / 64, would wrap."""
     assert lib.sparse_page_plan(*{**PLAN, "max_blocks": max_blocks}.values()) == UNSUPPORTED
     assert "max_blocks" in lib.sparse_last_error().decode()
+
+
+@pytest.mark.parametrize("scale", [2.4e38, -3.4e38, float("-inf")])
+def test_attn_refuses_scales_that_overflow_in_base_2(lib, scale):
+    """Times log2(e) they are infinite, which would make NaN of a score of zero."""
+    assert lib.sparse_paged_decode_attn_f8(*{**ATTN, "sm": scale}.values()) == INVALID
+    assert "scale" in lib.sparse_last_error().decode()
 
 
 def test_only_the_paged_calls_need_the_module_that_marshals_them(monkeypatch, tmp_path):
