@@ -3,8 +3,11 @@ import ctypes
 import subprocess
 import sys
 
+import numpy as np
 import pytest
+import torch
 
+import paged_long as long
 from block_sparse_long_pool_gb300 import binding, build
 from test_paged_cpu import ATTN, PLAN
 
@@ -58,3 +61,32 @@ def test_the_library_builds_without_torch(tmp_path):
     assert r.returncode == 0, r.stderr
     assert r.stdout.strip() == str(tmp_path / "lib.so")
     assert ctypes.CDLL(r.stdout.strip()).sparse_version() >= 100
+
+
+@pytest.mark.parametrize("n", [20032, 40000, 131072])
+def test_the_bound_of_long_lists_shows_a_lost_or_repeated_tile(n):
+    """What the attention's long lists are compared with: an answer with rounded weights passes, one
+    with a tile of 64 tokens left out or counted twice does not, wherever it is."""
+    rng = np.random.default_rng(n)
+    K, V = rng.standard_normal((2, n, 128)) * 64 / 2 ** 7
+    K, V = (torch.as_tensor(x * 32).to(torch.float8_e4m3fn).double().numpy() / 32 for x in (K, V))
+    Q = torch.as_tensor(rng.standard_normal((2, 128))).to(torch.bfloat16).double().numpy()
+    want = long.attend(Q, K, V)
+
+    def answer(times):
+        O, lse, _, _ = long.attend(Q, K, V, times=times)
+        return torch.as_tensor(O).to(torch.bfloat16).double().numpy(), lse.astype(np.float32)
+
+    long.assert_close(*answer(None), want)
+    s = Q @ K.T / np.sqrt(128)
+    p = np.exp(s - s.max(1, keepdims=True))
+    rounded = (p * 4096).astype(np.float16).astype(np.float64) / 4096   # the weights of O; the sum keeps its own
+    O = rounded @ V / p.sum(1, keepdims=True)
+    long.assert_close(torch.as_tensor(O).to(torch.bfloat16).double().numpy(), want[1].astype(np.float32), want)
+    blocks = -(-n // 64)
+    for j in [0, 1, blocks - 2, *rng.integers(0, blocks - 1, 5).tolist()]:
+        for count in (0.0, 2.0):
+            times = np.ones(n)
+            times[64 * j:64 * j + 64] = count
+            with pytest.raises(AssertionError, match="of its bound"):
+                long.assert_close(*answer(times), want)
