@@ -1005,11 +1005,12 @@ class _Layer:
                               workspace=self.ws, status=self.status, flags=self.attn_flags)
 
 
-def single_layer_oracle(lay, seconds):
+def single_layer_oracle(lay, seconds, cache=""):
     """The oracle on one decode step of a single-layer workload, all pairs: the
     compressed key of the block the appended token lands in (when the step appends),
     the Forecast selection and the attention, in fp64.  The compressed keys of the
-    other blocks are resident (pooled outside the timing)."""
+    other blocks are resident (pooled outside the timing).  It works on the contiguous bf16
+    cache; `cache` says so where the timed step's is another."""
     import numpy as np
     import oracle
     from block_sparse_long_pool_gb300 import workloads as wl
@@ -1033,7 +1034,7 @@ def single_layer_oracle(lay, seconds):
         idx, cnt, _ = oracle.select(F, ktil, lens, sh.n_init, sh.n_local, sh.k)
         oracle.attn(Q, K, V, idx, cnt, lens)
     what = ("append (the touched block's mean) + " if sh.n_new else "") + "select + attention"
-    return oracle_baseline(step, seconds, 1.0, "steps/s", f"the whole step ({what}) of all {P} pairs in fp64")
+    return oracle_baseline(step, seconds, 1.0, "steps/s", f"the whole step ({what}) of all {P} pairs in fp64{cache}")
 
 
 def run_single_layer_case(args, dev, sh, name):
@@ -1150,7 +1151,9 @@ def run_paged_case(args, dev):
                                       "decode_forecast_kernel<1, false>, paged_attn_kernel)", kv + sel + app,
                                       t["median_us"], peak, src),
             "l2": "512 MB read evicts L2 before each step", "clocks": clk.summary(),
-            "cpu_baseline": None if args.no_cpu_baseline else single_layer_oracle(lay, args.case_cpu_seconds)}
+            "cpu_baseline": None if args.no_cpu_baseline else
+            single_layer_oracle(lay, args.case_cpu_seconds,
+                                ", over the same tokens in a contiguous bf16 cache, without pages or a page plan")}
     print(json.dumps(line), flush=True)
 
 

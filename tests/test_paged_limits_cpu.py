@@ -1,7 +1,10 @@
 """The paged 8-bit cache at the ends of what it accepts, without a GPU."""
 import ctypes
+import json
+import os
 import subprocess
 import sys
+import types
 
 import numpy as np
 import pytest
@@ -9,7 +12,11 @@ import torch
 
 import paged_long as long
 from block_sparse_long_pool_gb300 import binding, build
+from block_sparse_long_pool_gb300 import workloads as wl
 from test_paged_cpu import ATTN, PLAN
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+import bench  # noqa: E402
 
 INVALID, UNSUPPORTED = binding.SPARSE_ERR_INVALID_ARG, binding.SPARSE_ERR_UNSUPPORTED
 
@@ -90,3 +97,22 @@ def test_the_bound_of_long_lists_shows_a_lost_or_repeated_tile(n):
             times[64 * j:64 * j + 64] = count
             with pytest.raises(AssertionError, match="of its bound"):
                 long.assert_close(*answer(times), want)
+
+
+def test_the_paged_case_says_what_its_cpu_baseline_is(monkeypatch):
+    """The oracle has no paged cache: the line says that the baseline's is the contiguous bf16 one."""
+    shape = wl.DecodeShape("tiny", B=1, H_q=2, H_kv=1, T=256, n_init=1, n_local=1, k=1, n_planted=1, n_new=1, seed=3)
+    lay = types.SimpleNamespace(sh=shape, x=wl.single_layer(shape))
+    plain = bench.single_layer_oracle(lay, 0.0)["sample"]
+    assert "in fp64;" in plain
+    lines = []
+    monkeypatch.setattr(bench, "measured_peaks", lambda: (1000.0, "test"))
+    monkeypatch.setattr(bench, "_PagedLayer", lambda sh, dev: types.SimpleNamespace(
+        sh=shape, x=lay.x, step=None, attend=None, status=torch.zeros(1)))
+    monkeypatch.setattr(bench, "_event_times", lambda *a: {"median_us": 1.0})
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda: None)
+    monkeypatch.setattr(torch, "ones", lambda *a, **k: None)
+    monkeypatch.setattr("builtins.print", lambda text, **k: lines.append(json.loads(text)))
+    args = types.SimpleNamespace(steps=1, warmup=0, no_cpu_baseline=False, case_cpu_seconds=0.0)
+    bench.run_paged_case(args, torch.device("cpu"))
+    assert "contiguous bf16 cache" in lines[0]["cpu_baseline"]["sample"]
