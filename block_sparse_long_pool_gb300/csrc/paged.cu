@@ -18,8 +18,9 @@ using namespace sp;
 // Three prefix sums over the requests (pages returned, new tokens, pages needed) by every CTA,
 // then a row's place by arithmetic: no row waits for a table entry that this step writes,
 // since a new page's id follows from the request's prefix and the free list.
-// All latency: a step of 8 requests takes 3.0 us on GB300, back to back in a graph, 512 requests
-// with 16 384 rows 4.8 us, 2^20 rows 8.8 us (12.6 MB stored: 1.9 us at the copy rate).
+// All latency: a step of 8 requests takes 3.1 us on GB300, back to back in a graph, 512 requests
+// with 16 384 rows 4.9 us, 2^20 rows 8.9 us (12.6 MB stored: 1.9 us at the copy rate).  With outputs in
+// the inputs' place: 512 requests 4.9 us in one launch, 7.6 with 2048 or 16 384 rows in two.
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanMaxB = 4096;
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(kRowThreads) page_rows_kernel(const PlanParams
 // loads (slots, rows, stores); 9 CTAs an SM cover it only with the rows of the CTAs 2 an SM
 // ahead already asked for (162 us without; 3 and 4 ahead: 127 and 128; 8 ahead, whose rows
 // leave L2's sets before they are used: 140 and more).  Keys and values in one CTA of 256
-// threads: 150 us.  Small calls are latency: 8 rows 2.5 us, 256 rows 3.3 us.  The rows of a decode
+// threads: 150 us.  Small calls are latency: 8 rows 2.6 us, 256 rows 3.3 us.  The rows of a decode
 // step, runs of one, go to a warp each (18.3 us with a CTA each), which finds them from what
 // its lanes tell of a row each (4.3 and 5.6 us where it walks over the window's runs).  A step
 // whose rows make scales grow takes up to 4.5 us more (63 old rows; batches of 8 and 16 of

@@ -25,13 +25,14 @@
 // scales are; the row sum l uses the fp32 weights 2^(s - m).
 //
 // What bounds it.  The tiles' stream in the middle, latency at both ends.  On GB300, back to back
-// in a graph: 537 MB (32K tokens x 8 requests x 8 KV heads, G = 4) in 87.9 us, 6.1 TB/s, 0.90 of
+// in a graph: 537 MB (32K tokens x 8 requests x 8 KV heads, G = 4) in 88.4 us, 6.1 TB/s, 0.90 of
 // the copy rate; of these about 3.5 us pass before the first tile is there (lengths, table,
 // load: three round trips), and 3 us after the last one in the merge of the pairs that the
-// CTAs share.  70.6 MB of selected blocks (64 pairs x 67) in 20.5 us, 2.1 MB (one request of 4K
-// tokens, 2 KV heads) in 9.8 us: those ends.  64 requests of 1 to 16K tokens in 37 us (0.66):
+// CTAs share.  70.6 MB of selected blocks (64 pairs x 67) in 22.2 us, 20.6 where a fifth of them share
+// pages (and come from L2), 2.1 MB (one request of 4K tokens, 2 KV heads) in 9.9 us: those ends.
+// 64 requests of 1 to 16K tokens in 37.5 us (0.65):
 // each part of a pair ends with its warps waiting for one another.  A tile takes a warp about
-// 2900 cycles at G <= 8 and 3900 at G = 16 (537 MB in 106 us, 0.74): the conversions' half-rate
+// 2900 cycles at G <= 8 and 3900 at G = 16 (537 MB in 106 us, 0.75): the conversions' half-rate
 // instructions (cvt, prmt, shift) and the products' latency.
 #include <limits.h>
 #include <math.h>
@@ -921,7 +922,8 @@ __global__ void __launch_bounds__((warps<NT>() + 1) * 32, kCtasPerSm)
         // Where more pairs than CTAs end inside the ranges, each warp's ring is fed by itself, so
         // that the warps which wait for one another at a part's end find their next tiles
         // there: 64 requests of 1 to 16K tokens x 8 heads 37.0 us (39.0 in the list's order), 256 x
-        // 8 lists of 16 blocks 79 (96), 8000 of 8 blocks 167 (211).  Else in the list's order, in
+        // 8 lists of 16 blocks 79 (96), 8000 of 8 blocks 167 (211), these on pages that requests
+        // share (on pages of their own 92 and 178).  Else in the list's order, in
         // which an item's keys and values, 16 KB in one piece, leave one after the other: 8 pairs
         // of 2048 tiles 51.5 us (53.5), 64 of 512 87 (88.2).
         const bool apart = pairs > static_cast<int>(gridDim.x);
