@@ -4,7 +4,7 @@ Argument marshalling only: every function checks dtype/device/shape/contiguity o
 the tensors it is given, passes their data pointers and the current CUDA stream to
 the C entry point of the same name, and raises ``SparsePoolError`` on a non-zero
 status.  Every step of the computation runs in the CUDA kernels; there is no CPU
-fallback, and a missing library raises at the first call.  The paged cache's three calls
+fallback, and a missing library raises at the first call.  The paged cache's calls
 are marshalled by csrc/marshal.cpp, the same way: they are short enough that checking their
 tensors in Python takes longer than they do.
 """
@@ -78,6 +78,12 @@ SIGNATURES = {
     "sparse_paged_decode_attn_f8": (_I, [_P, _P, _P, _I, _P, _I, _P, _P, _I, _P, _I, _I, _I, _F, _P, _P, _P, _SZ,
                                          _P, _P]),
     "sparse_paged_decode_attn_f8_workspace_size": (_SZ, [_I, _I, _I]),
+    "sparse_paged_chunk_attn_f8": (_I, [_P, _LL, _P, _P, _I, _P, _I, _P, _P, _I, _I, _I, _I, _F, _P, _P, _P, _SZ, _P, _P]),
+    "sparse_paged_chunk_attn_f8_workspace_size": (_SZ, [_I, _I, _I]),
+    "sparse_rope": (_I, [_P, _LL, _I, _P, _LL, _I, _P, _I, _P, _I, _I, _F, _P, _LL, _P, _LL, _P]),
+    "sparse_page_fork": (_I, [_P, _P, _I, _P, _P, _I, _P, _P, _I, _P, _P, _P, _P, _SZ, _P, _P]),
+    "sparse_page_fork_workspace_size": (_SZ, [_I, _I]),
+    "sparse_paged_copy_f8": (_I, [_P, _P, _I, _I, _P, _P, _I, _P, _I, _I, _P, _P, _P, _P]),
 }
 
 
@@ -119,7 +125,8 @@ def _load_marshal():
             marshal = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(marshal)
             marshal.setup(*(ctypes.cast(getattr(lib, f"sparse_{name}"), ctypes.c_void_p).value
-                            for name in ("page_plan", "paged_append_f8", "paged_decode_attn_f8")))
+                            for name in ("page_plan", "paged_append_f8", "paged_decode_attn_f8",
+                                         "paged_chunk_attn_f8", "rope", "page_fork", "paged_copy_f8")))
             _marshal = marshal
 
 
@@ -576,7 +583,7 @@ def sparse_page_plan(seq_len, n_new, block_table, free_pages, n_free, cu_new, st
 
 
 def _explain_rows(t, name, idx, n_tok, H_kv):
-    """k_new / v_new [n_tok][H_kv][128], whose tokens may be apart."""
+    """Rows [n_tok][H_kv][128], whose tokens may be apart."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not torch.bfloat16:
@@ -660,3 +667,121 @@ def sparse_paged_decode_attn_f8(Q, kv_pages, kv_scale, block_table, seq_len, O, 
     if status is not None:
         _explain(idx, i32, (1,), status=status)
     raise _refused("sparse_paged_decode_attn_f8")
+
+
+def sparse_paged_chunk_attn_f8_workspace_size(B: int, H_q: int, H_kv: int) -> int:
+    """Bytes of the workspace of sparse_paged_chunk_attn_f8 (0: invalid sizes)."""
+    return int(load().sparse_paged_chunk_attn_f8_workspace_size(B, H_q, H_kv))
+
+
+def paged_chunk_workspace(B: int, H_q: int, H_kv: int, device="cuda"):
+    """A workspace tensor for sparse_paged_chunk_attn_f8."""
+    with torch.cuda.device(device):
+        n = sparse_paged_chunk_attn_f8_workspace_size(B, H_q, H_kv)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def sparse_paged_chunk_attn_f8(Q, kv_pages, kv_scale, block_table, cu_new, start, O, workspace, lse=None,
+                               scale: float = 0.0, status=None, stream=None):
+    """O [n_tok][H_q][128] = attention of a step's new rows Q [n_tok][H_q][128] (a part of wider rows is
+    taken as it is) over the pages that block_table [B][max_blocks] names: request b's rows
+    cu_new[b] .. cu_new[b + 1] - 1 are at positions start[b], start[b] + 1, ... and see the tokens up to
+    their own.  lse [n_tok][H_q]."""
+    idx = _device_index(kv_pages, "kv_pages")
+    if _passed("paged_chunk_attn_f8", idx, stream, Q, kv_pages, kv_scale, block_table, cu_new, start, O, workspace, lse, scale,
+               status):
+        return
+    i32, f32 = torch.int32, torch.float32
+    n_pages, H_kv = _shape(kv_pages, "kv_pages", 5)[:2]
+    B, max_blocks = _shape(block_table, "block_table", 2)
+    n_tok, H_q, _ = _shape(Q, "Q", 3)
+    _explain(idx, _F8, (n_pages, H_kv, 2, BLK, D), kv_pages=kv_pages)
+    _explain(idx, f32, (n_pages, H_kv, 2), kv_scale=kv_scale)
+    _explain_rows(Q, "Q", idx, n_tok, H_q)
+    _explain(idx, torch.bfloat16, (n_tok, H_q, D), O=O)
+    _explain(idx, i32, (B, max_blocks), block_table=block_table)
+    _explain(idx, i32, (B + 1,), cu_new=cu_new)
+    _explain(idx, i32, (B,), start=start)
+    _explain(idx, torch.uint8, tuple(_shape(workspace, "workspace", 1)), workspace=workspace)
+    if lse is not None:
+        _explain(idx, f32, (n_tok, H_q), lse=lse)
+    if status is not None:
+        _explain(idx, i32, (1,), status=status)
+    raise _refused("sparse_paged_chunk_attn_f8")
+
+
+def sparse_rope(Q, K, pos, inv_freq, Q_out, K_out, interleaved: bool = False, factor: float = 1.0, stream=None):
+    """Turns the rows Q [n_tok][H_q][128] and K [n_tok][H_kv][128] bf16 (parts of wider rows are taken as
+    they are; K and K_out may be None) by their positions pos [n_tok] int32 into Q_out and K_out, which may be
+    the inputs themselves: pair i by pos * inv_freq[i], inv_freq [rot_dim / 2] fp64 (``rope.frequencies``),
+    pairs (i, i + rot_dim / 2) or interleaved (2 i, 2 i + 1).  Rows with a negative position are not written."""
+    idx = _device_index(Q, "Q")
+    if (K is None) != (K_out is None):
+        raise ValueError("K and K_out go together")
+    if _passed("rope", idx, stream, Q, K, pos, inv_freq, Q_out, K_out, bool(interleaved), factor):
+        return
+    n_tok, H_q, _ = _shape(Q, "Q", 3)
+    _explain_rows(Q, "Q", idx, n_tok, H_q)
+    _explain_rows(Q_out, "Q_out", idx, n_tok, H_q)
+    if K is not None:
+        H_kv = _shape(K, "K", 3)[1]
+        _explain_rows(K, "K", idx, n_tok, H_kv)
+        _explain_rows(K_out, "K_out", idx, n_tok, H_kv)
+    _explain(idx, torch.int32, (n_tok,), pos=pos)
+    _explain(idx, torch.float64, tuple(_shape(inv_freq, "inv_freq", 1)), inv_freq=inv_freq)
+    raise _refused("sparse_rope")
+
+
+def sparse_page_fork_workspace_size(B: int, max_blocks: int) -> int:
+    """Bytes of the workspace of sparse_page_fork (0: invalid sizes)."""
+    return int(load().sparse_page_fork_workspace_size(B, max_blocks))
+
+
+def page_fork_workspace(B: int, max_blocks: int, device="cuda"):
+    """A workspace tensor for sparse_page_fork."""
+    return torch.empty(sparse_page_fork_workspace_size(B, max_blocks), dtype=torch.uint8, device=device)
+
+
+def sparse_page_fork(src, seq_len, block_table, page_extra, free_pages, n_free, copy_src, copy_dst, workspace,
+                     fork_len=None, status=None, stream=None):
+    """Requests that become copies of others and requests that end, all int32: src [B] is a request's own
+    index (it stays), -1 (it ends) or the request that it becomes a copy of, whose full pages it then
+    shares (with fork_len [B] the first fork_len tokens, in whole blocks).  Updates seq_len [B],
+    block_table [B][max_blocks], page_extra [n_pages] (holders beyond the first), free_pages [n_pages] and
+    n_free [1]; writes the page pairs copy_src, copy_dst [B] for sparse_paged_copy_f8."""
+    idx = _device_index(block_table, "block_table")
+    if _passed("page_fork", idx, stream, src, seq_len, block_table, page_extra, free_pages, n_free, copy_src, copy_dst, workspace,
+               fork_len, status):
+        return
+    i32 = torch.int32
+    B, max_blocks = _shape(block_table, "block_table", 2)
+    _explain(idx, i32, (B, max_blocks), block_table=block_table)
+    _explain(idx, i32, (B,), src=src, seq_len=seq_len, copy_src=copy_src, copy_dst=copy_dst,
+             **({} if fork_len is None else {"fork_len": fork_len}))
+    _explain(idx, i32, tuple(_shape(free_pages, "free_pages", 1)), free_pages=free_pages, page_extra=page_extra)
+    _explain(idx, i32, (1,), n_free=n_free, **({} if status is None else {"status": status}))
+    _explain(idx, torch.uint8, tuple(_shape(workspace, "workspace", 1)), workspace=workspace)
+    raise _refused("sparse_page_fork")
+
+
+def sparse_paged_copy_f8(kv_pages, kv_scale, copy_src, copy_dst, ktil=None, src=None, seq_len=None, status=None, stream=None):
+    """Copies the pages copy_src [n] of kv_pages (and their scales) to copy_dst [n], both -1 where there is
+    nothing to copy; with ktil [B][H_kv][N_cap][128], src and seq_len [B] also the compressed keys of
+    request src[b] to request b."""
+    idx = _device_index(kv_pages, "kv_pages")
+    if ktil is not None and (src is None or seq_len is None):
+        raise ValueError("ktil needs src and seq_len")
+    if _passed("paged_copy_f8", idx, stream, kv_pages, kv_scale, copy_src, copy_dst, ktil, src, seq_len, status):
+        return
+    i32, f32 = torch.int32, torch.float32
+    n_pages, H_kv = _shape(kv_pages, "kv_pages", 5)[:2]
+    _explain(idx, _F8, (n_pages, H_kv, 2, BLK, D), kv_pages=kv_pages)
+    _explain(idx, f32, (n_pages, H_kv, 2), kv_scale=kv_scale)
+    _explain(idx, i32, tuple(_shape(copy_src, "copy_src", 1)), copy_src=copy_src, copy_dst=copy_dst)
+    if ktil is not None:
+        B, _, N_cap, _ = _shape(ktil, "ktil", 4)
+        _explain(idx, f32, (B, H_kv, N_cap, D), ktil=ktil)
+        _explain(idx, i32, (B,), src=src, seq_len=seq_len)
+    if status is not None:
+        _explain(idx, i32, (1,), status=status)
+    raise _refused("sparse_paged_copy_f8")

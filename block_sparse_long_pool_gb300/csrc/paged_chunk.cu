@@ -1,0 +1,1100 @@
+// paged_chunk.cu -- attention of a chunk of new tokens a request over the paged 8-bit cache.
+#include <limits.h>
+#include <math.h>
+
+#include "common.cuh"
+#include "paged.cuh"
+
+namespace {
+
+using namespace sp;
+
+constexpr int kTileRows = 128;                    // query rows of a tile: M of the products
+constexpr int kTiles = 2;                         // tiles of an item
+constexpr int kKv = 128;                          // tokens of a step: two pages
+constexpr int kMaxB = 4096;
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr float kLazy = 10.f;                     // log2 of the growth of a maximum that is let pass
+constexpr float kFarWeight = 60.f;                // log2 of the largest factor from a page's weights to O's
+constexpr int kItemCost = 320;                    // what an item costs beside its tokens, in tokens of one step
+constexpr int kMinWork = 1024;                    // the least share of a CTA, in the same units
+constexpr int kMinCut = 2;                        // steps on either side of a cut through an item
+
+constexpr int kSoftmaxWarps = 4 * kTiles;
+constexpr int kConvertWarp = kSoftmaxWarps;       // first of four
+constexpr int kMmaWarp = kConvertWarp + 4;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kSub = kKv * 128;                   // 64 of 128 dims of 128 f16 rows, 128 bytes a row: 16 KB
+constexpr int kOperand = 2 * kSub;                // 128 x 128 f16
+
+constexpr int kOffQ = 0;
+constexpr int kOffK = kOffQ + kTiles * kOperand;
+constexpr int kOffV = kOffK + 2 * kOperand;
+constexpr int kOffBars = kOffV + 2 * kOperand;
+enum {
+    kKFull = 0,      // [2] keys of a step converted
+    kKEmpty = 2,     // [2] its score products are done
+    kVFull = 4,      // [2] values converted
+    kVEmpty = 6,     // [2] its products with the weights are done
+    kQFull = 8,      // [tiles] queries of an item converted
+    kSFull = 10,     // [tiles] scores of a step
+    kPFull = 12,     // [tiles] its weights
+    kOFull = 14,     // [tiles] every product of an item
+    kRec = 16,       // [4] scales of a step
+    kDone = 20,      // [tiles][2] an item that the tile has steps of is finished; items in turn
+    kDrain = 24,
+    kNumBars = 25
+};
+constexpr int kOffRec = kOffBars + 256;           // float4 [4]: ks, ks, log2 vs, log2 vs (ks < 0: no page)
+constexpr int kOffCtrl = kOffRec + 64;            // int [16]
+constexpr int kOffStart = kOffCtrl + 64;          // Start
+constexpr int kOffQs = kOffStart + 64;            // float [tiles][128]
+constexpr int kOffNan = kOffQs + kTiles * kTileRows * 4;   // int [2][128], then int [2]
+constexpr int kOffScan = kOffNan + 2 * kD * 4 + 16;        // long long [16], int [16]
+constexpr int kOffLive = kOffScan + 16 * 12;               // uint16 [kMaxB]
+constexpr int kSmem = kOffLive + 2 * kMaxB + 1024;
+static_assert(kNumBars * 8 <= 256 && kOffRec % 16 == 0 && kOffStart % 8 == 0 && kOffScan % 8 == 0, "alignment");
+static_assert(kSmem <= 232448, "shared memory of a CTA");
+
+constexpr int kColS = 0, kColO = kTiles * 128;    // tensor memory: scores (weights in their place), outputs
+
+// A CTA's first item: where in the list of items it lies.
+struct Start {
+    long long at, lo, hi;
+    int live, head, chunk, n_live;
+};
+
+struct ChunkParams {
+    const uint16_t *Q;
+    const uint8_t *kv_pages;
+    const float *kv_scale;
+    const int *block_table;
+    const int *cu_new;
+    const int *start;
+    uint16_t *O;
+    float *lse;
+    float *parts;      // [2 * CTAs][part_floats]
+    int4 *tails;       // [CTAs]: first row, KV head, tokens of the item that a CTA begins and another ends; -1: none
+    int *heads;        // [CTAs]: the CTA's part of an item begun before it; 0 none, 1 goes on, 2 the last
+    int *status;
+    long long q_stride;
+    float scale_log2;  // not negative: the scale's sign is in the queries
+    uint32_t q_sign;
+    int n_pages;
+    int max_blocks;
+    int n_tok;
+    int B;
+    int H_q;
+    int H_kv;
+    int G;
+    int per_tile;      // tokens of a tile
+};
+
+// One partial state: O [256][128], then m, l, mo [256].
+constexpr int kPartFloats = kTiles * kTileRows * (kD + 3);
+
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn)
+{
+    return (1u << 4) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
+           (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// D (tensor memory) = A B (+ D), A in tensor memory.
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, bool accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+                 "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+                 : "memory");
+}
+
+#define R8(a, o) "=r"(a[o]), "=r"(a[o + 1]), "=r"(a[o + 2]), "=r"(a[o + 3]), "=r"(a[o + 4]), "=r"(a[o + 5]), "=r"(a[o + 6]), "=r"(a[o + 7])
+#define I8(a, o) "r"(a[o]), "r"(a[o + 1]), "r"(a[o + 2]), "r"(a[o + 3]), "r"(a[o + 4]), "r"(a[o + 5]), "r"(a[o + 6]), "r"(a[o + 7])
+
+// Warp-wide: 32 columns of this warp's lanes; complete after tc_wait_ld.
+__device__ __forceinline__ void tc_ld32(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+                 "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : R8(r, 0), R8(r, 8), R8(r, 16), R8(r, 24)
+                 : "r"(taddr));
+}
+
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        asm volatile("" : "+r"(r[i]));   // no use of a register moves before the wait
+}
+
+__device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+                 "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+                 I8(r, 0), I8(r, 8), I8(r, 16), I8(r, 24)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tc_st16u(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+                 "%15, %16};" ::"r"(taddr),
+                 I8(r, 0), I8(r, 8)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tc_wait_st()
+{
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// ---------------------------------------------------------------- the list of items
+
+// A request's new tokens, held to the packed rows.
+struct Request {
+    int row, n, start;   // first row, rows, position of the first (-1: no pages, no token is seen)
+};
+
+__device__ __forceinline__ Request request_of(const ChunkParams &p, int b, bool *bad)
+{
+    const int a = p.cu_new[b], z = p.cu_new[b + 1], s = p.start[b];
+    const int c0 = max(0, min(a, p.n_tok)), c1 = max(c0, min(z, p.n_tok));
+    const long long cap = static_cast<long long>(p.max_blocks) * kBlk;
+    if (s >= 0 && (a != c0 || z != c1 || static_cast<long long>(s) + (c1 - c0) > cap))
+        *bad = true;
+    return Request{c0, c1 - c0, s < 0 ? -1 : s};
+}
+
+// Work of the first `q` items of a head of a request: an item's is the position of its first
+// token and a constant, or the constant alone where no token is seen.
+__device__ __forceinline__ long long work_upto(const ChunkParams &p, const Request &r, long long q)
+{
+    if (r.start < 0)
+        return q * kItemCost;
+    return q * (static_cast<long long>(r.start) + kItemCost) + static_cast<long long>(kTiles * p.per_tile) * (q * (q - 1) / 2);
+}
+
+__device__ __forceinline__ int items_of(const ChunkParams &p, int n)
+{
+    const int t = kTiles * p.per_tile;
+    return n / t + (n % t != 0);
+}
+
+// An item: up to two tiles of one KV head's query rows, and the steps [j0, j1) of its tokens that
+// are this CTA's.
+struct Item {
+    int row, n;          // first row of the packed rows, tokens
+    int head, b;
+    int pos;             // position of the first token (-1: nothing is seen)
+    int steps[kTiles];   // steps that hold a token which a row of the tile sees
+    int all;             // steps of the item
+    int j0, j1;
+};
+
+struct Walk {
+    long long at, lo, hi;
+    int live, head, chunk, n_live, b;
+    Request r;
+    const uint16_t *list;
+
+    __device__ __forceinline__ void open(const ChunkParams &p, const Start *s, const uint16_t *live_list)
+    {
+        at = s->at;
+        lo = s->lo;
+        hi = s->hi;
+        live = s->live;
+        head = s->head;
+        chunk = s->chunk;
+        n_live = s->n_live;
+        list = live_list;
+        enter(p);
+    }
+    __device__ __forceinline__ void enter(const ChunkParams &p)
+    {
+        bool bad = false;
+        if (live < n_live) {
+            b = list[live];
+            r = request_of(p, b, &bad);
+        }
+    }
+    // The step of the item at `at` with work w that the border x between two CTAs falls on.
+    static __device__ __forceinline__ int cut(long long x, long long at, long long w, int all)
+    {
+        if (x <= at)
+            return 0;
+        if (x >= at + w)
+            return all;
+        const int j = static_cast<int>((x - at) * all / w);
+        return j < kMinCut ? 0 : all - j < kMinCut ? all : j;
+    }
+    // The next item that this CTA has steps of (or that it has to write, seeing nothing).
+    __device__ __forceinline__ bool next(const ChunkParams &p, Item &it)
+    {
+        while (live < n_live && at < hi) {
+            const int per = kTiles * p.per_tile;
+            const long long w = r.start < 0 ? kItemCost : static_cast<long long>(r.start) + kItemCost + static_cast<long long>(chunk) * per;
+            const int t0 = chunk * per;
+            it.row = r.row + t0;
+            it.n = min(per, r.n - t0);
+            it.head = head;
+            it.b = b;
+            it.pos = r.start < 0 ? -1 : r.start + t0;
+            it.all = 0;
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+                it.steps[t] = 0;
+                if (r.start >= 0 && it.n > t * p.per_tile) {
+                    const long long last = static_cast<long long>(it.pos) + min(it.n, (t + 1) * p.per_tile);
+                    it.steps[t] = static_cast<int>((min(last, static_cast<long long>(p.max_blocks) * kBlk) + kKv - 1) / kKv);
+                }
+                it.all = max(it.all, it.steps[t]);
+            }
+            it.j0 = cut(lo, at, w, it.all);
+            it.j1 = cut(hi, at, w, it.all);
+            const bool mine = it.all > 0 ? it.j0 < it.j1 : at >= lo;
+            at += w;
+            if (++chunk == items_of(p, r.n)) {
+                chunk = 0;
+                if (++head == p.H_kv) {
+                    head = 0;
+                    ++live;
+                    enter(p);
+                }
+            }
+            if (mine)
+                return true;
+        }
+        return false;
+    }
+};
+
+// Every thread: the requests with rows, the work up to each, and this CTA's share of it.
+__device__ __forceinline__ void find_start(const ChunkParams &p, uint8_t *base, int tid)
+{
+    long long *warp_work = reinterpret_cast<long long *>(base + kOffScan);
+    int *warp_live = reinterpret_cast<int *>(base + kOffScan + 16 * 8);
+    uint16_t *list = reinterpret_cast<uint16_t *>(base + kOffLive);
+    Start *s = reinterpret_cast<Start *>(base + kOffStart);
+    constexpr int kWarps = kThreads / 32;
+    const int warp = tid >> 5, lane = tid & 31;
+    const int per = (p.B + kThreads - 1) / kThreads, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+    long long sum = 0;
+    int count = 0;
+    bool bad = false;
+    for (int b = b0; b < b1; ++b) {
+        const Request r = request_of(p, b, &bad);
+        if (r.n > 0) {
+            sum += p.H_kv * work_upto(p, r, items_of(p, r.n));
+            ++count;
+        }
+    }
+    if (bad && blockIdx.x == 0)
+        report(p.status, SPARSE_ERR_BAD_INDEX);
+    long long up = sum;
+    int cup = count;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, up, o);
+        const int y = __shfl_up_sync(0xffffffffu, cup, o);
+        if (lane >= o) {
+            up += x;
+            cup += y;
+        }
+    }
+    if (lane == 31) {
+        warp_work[warp] = up;
+        warp_live[warp] = cup;
+    }
+    if (tid == 0)
+        s->n_live = 0;
+    __syncthreads();
+    long long before = up - sum, total = 0;
+    int cbefore = cup - count, ctotal = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) {
+            before += warp_work[w];
+            cbefore += warp_live[w];
+        }
+        total += warp_work[w];
+        ctotal += warp_live[w];
+    }
+    const long long n = max(1LL, min(static_cast<long long>(gridDim.x), total / kMinWork));
+    const long long c = blockIdx.x;
+    const long long lo = c >= n ? total : total / n * c + total % n * c / n;
+    const long long hi = c + 1 >= n ? total : total / n * (c + 1) + total % n * (c + 1) / n;
+    if (tid == 0 && lo >= hi) {
+        s->at = s->lo = s->hi = total;
+        s->live = s->n_live = 0;
+        s->head = s->chunk = 0;
+    }
+    for (int b = b0; b < b1; ++b) {
+        const Request r = request_of(p, b, &bad);
+        if (r.n <= 0)
+            continue;
+        const long long one = work_upto(p, r, items_of(p, r.n)), all = p.H_kv * one;
+        list[cbefore] = static_cast<uint16_t>(b);
+        if (lo < hi && before <= lo && lo < before + all) {
+            const int head = static_cast<int>((lo - before) / one);
+            const long long in = lo - before - head * one;
+            int a = 0, z = items_of(p, r.n);   // work_upto(a) <= in < work_upto(z)
+            while (z - a > 1) {
+                const int mid = (a + z) / 2;
+                if (work_upto(p, r, mid) <= in)
+                    a = mid;
+                else
+                    z = mid;
+            }
+            s->at = before + head * one + work_upto(p, r, a);
+            s->lo = lo;
+            s->hi = hi;
+            s->live = cbefore;
+            s->head = head;
+            s->chunk = a;
+            s->n_live = ctotal;
+        }
+        before += all;
+        ++cbefore;
+    }
+    __syncthreads();
+}
+
+// ---------------------------------------------------------------- keys and values
+
+// Sixteen e4m3 values to f16 in two 16-byte pieces of a swizzled row.  The lanes of a quarter
+// warp hold the eight pieces of a row; those of the second half store theirs the other way
+// round, so that no two store to the same banks.
+__device__ __forceinline__ void store_f16(uint32_t dst, int row, int c, uint4 x)
+{
+    uint4 a, b;
+    a.x = f8x2_to_f16x2(x.x);
+    a.y = f8x2_to_f16x2(x.x >> 16);
+    a.z = f8x2_to_f16x2(x.y);
+    a.w = f8x2_to_f16x2(x.y >> 16);
+    b.x = f8x2_to_f16x2(x.z);
+    b.y = f8x2_to_f16x2(x.z >> 16);
+    b.z = f8x2_to_f16x2(x.w);
+    b.w = f8x2_to_f16x2(x.w >> 16);
+    const uint32_t line = dst + (c >> 2) * kSub + row * 128;
+    const int pos = (c & 3) * 2;
+    const bool late = c >= 4;
+    const uint4 first = late ? b : a, second = late ? a : b;
+    const uint32_t o1 = ((pos + (late ? 1 : 0)) ^ (row & 7)) << 4, o2 = ((pos + (late ? 0 : 1)) ^ (row & 7)) << 4;
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(line + o1), "r"(first.x), "r"(first.y), "r"(first.z), "r"(first.w)
+                 : "memory");
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(line + o2), "r"(second.x), "r"(second.y), "r"(second.z), "r"(second.w)
+                 : "memory");
+}
+
+// NaN among the values: the products would spread it to rows that do not see its token.  It is
+// taken out, and the first token with NaN in each dim is kept: rows at or past it get NaN there.
+__device__ __noinline__ uint4 take_nan(uint4 x, int tok, int c, int *first)
+{
+    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    for (int i = 0; i < 16; ++i) {
+        const uint32_t byte = (w[i >> 2] >> (8 * (i & 3))) & 0x7fu;
+        if (byte == 0x7fu) {
+            atomicMin(&first[c * 16 + i], tok);
+            w[i >> 2] &= ~(0xffu << (8 * (i & 3)));
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ bool has_nan(uint4 x)
+{
+    auto f = [](uint32_t v) { return (v & 0x7f7f7f7fu) + 0x01010101u; };
+    return ((f(x.x) | f(x.y) | f(x.z) | f(x.w)) & 0x80808080u) != 0u;
+}
+
+// The four warps that convert: pieces i * 128 + tid of a tile of 128 tokens, eight a row.
+__device__ __forceinline__ void convert_loop(const ChunkParams &p, uint8_t *base, uint32_t base_s, int tid)
+{
+    const uint32_t bars = base_s + kOffBars;
+    Walk walk;
+    walk.open(p, reinterpret_cast<const Start *>(base + kOffStart), reinterpret_cast<const uint16_t *>(base + kOffLive));
+    const int row0 = tid >> 3, c = tid & 7, lane = tid & 31;
+    int fill = 0, items = 0;
+    uint32_t used[kTiles][2] = {};   // items of either parity that a tile had steps of
+    Item it;
+    bool ok = true;
+    while (walk.next(p, it)) {   // a thread that gave up still meets the others
+        if (it.all == 0)
+            continue;
+        int *first = reinterpret_cast<int *>(base + kOffNan) + (items & 1) * kD;
+        int *any = reinterpret_cast<int *>(base + kOffNan) + 2 * kD + (items & 1);
+        // the last of them is finished: a tile without steps does not wait for anyone, and does not count
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+            if (used[t][items & 1] > 0)
+                ok = ok && mbar_wait(bars + 8 * (kDone + 2 * t + (items & 1)), (used[t][items & 1] - 1) & 1, kWaitNs);
+            if (min(it.j1, it.steps[t]) > it.j0)
+                ++used[t][items & 1];
+        }
+        first[tid] = INT_MAX;
+        if (tid == 0)
+            *any = 0;
+        named_barrier_sync(2, 128);
+        ++items;
+        const int end = static_cast<int>(min(static_cast<long long>(it.pos) + it.n, static_cast<long long>(p.max_blocks) * kBlk));
+        const int *table = p.block_table + static_cast<size_t>(it.b) * p.max_blocks;
+        for (int j = it.j0; j < it.j1 && ok; ++j, ++fill) {
+            const int tok0 = j * kKv, stage = fill & 1;
+            // the two pages of the step
+            const uint8_t *src[2];
+            bool there[2];
+            float rec[4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int blk = 2 * j + i;
+                there[i] = blk * kBlk < end;
+                int page = there[i] ? table[blk] : 0;
+                if (there[i] && (page < 0 || page >= p.n_pages)) {
+                    there[i] = false;
+                    page = 0;
+                    if (tid == 0)
+                        report(p.status, SPARSE_ERR_BAD_INDEX);
+                }
+                const size_t at = static_cast<size_t>(page) * p.H_kv + it.head;
+                src[i] = p.kv_pages + at * (2 * kBlk * kD);
+                rec[i] = -1.f;
+                rec[2 + i] = 0.f;
+                if (tid == 0 && there[i]) {
+                    const float2 s = *reinterpret_cast<const float2 *>(p.kv_scale + at * 2);
+                    rec[i] = s.x;
+                    rec[2 + i] = log2f(s.y);
+                }
+            }
+            uint4 x[8], y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int row = i * 16 + row0;
+                const bool use = there[i >> 2] && tok0 + row < end;
+                const uint8_t *s = src[i >> 2] + (row & 63) * kD + c * 16;
+                x[i] = use ? *reinterpret_cast<const uint4 *>(s) : make_uint4(0u, 0u, 0u, 0u);
+                y[i] = use ? *reinterpret_cast<const uint4 *>(s + kBlk * kD) : make_uint4(0u, 0u, 0u, 0u);
+            }
+            if (tid == 0)
+                *reinterpret_cast<float4 *>(base + kOffRec + (fill & 3) * 16) = make_float4(rec[0], rec[1], rec[2], rec[3]);
+            if (fill >= 2)
+                ok = mbar_wait(bars + 8 * (kKEmpty + stage), ((fill >> 1) - 1) & 1, kWaitNs);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                store_f16(base_s + kOffK + stage * kOperand, i * 16 + row0, c, x[i]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bars + 8 * (kKFull + stage));
+                if (tid == 0)
+                    mbar_arrive(bars + 8 * (kRec + (fill & 3)));
+            }
+            if (fill >= 2)
+                ok = ok && mbar_wait(bars + 8 * (kVEmpty + stage), ((fill >> 1) - 1) & 1, kWaitNs);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (has_nan(y[i])) {
+                    y[i] = take_nan(y[i], tok0 + i * 16 + row0, c, first);
+                    *any = 1;
+                }
+                store_f16(base_s + kOffV + stage * kOperand, i * 16 + row0, c, y[i]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bars + 8 * (kVFull + stage));
+        }
+    }
+    if (!ok)
+        report(p.status, SPARSE_ERR_TIMEOUT);
+}
+
+// ---------------------------------------------------------------- products
+
+// One thread: S = Q K^T of a step, then O += P V of the step before, tile by tile in turn: while
+// one tile's softmax runs, the other's products do.
+__device__ __forceinline__ void mma_loop(const ChunkParams &p, uint8_t *base, uint32_t base_s, uint32_t tmem)
+{
+    const uint32_t bars = base_s + kOffBars;
+    constexpr uint32_t idS = idesc_f16(kTileRows, kKv, 0, 0);   // K-major queries and keys
+    constexpr uint32_t idO = idesc_f16(kTileRows, kD, 0, 1);    // weights; values as they are stored (dims contiguous)
+    Walk walk;
+    walk.open(p, reinterpret_cast<const Start *>(base + kOffStart), reinterpret_cast<const uint16_t *>(base + kOffLive));
+    uint32_t nq[kTiles] = {}, np[kTiles] = {};
+    int fill = 0;
+    Item it;
+    bool ok = true;
+    while (ok && walk.next(p, it)) {
+        if (it.all == 0)
+            continue;
+        int end[kTiles];
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+            end[t] = min(it.j1, it.steps[t]);
+            if (end[t] > it.j0)
+                ok = ok && mbar_wait(bars + 8 * (kQFull + t), nq[t]++ & 1, kWaitNs);
+        }
+        for (int j = it.j0; j <= it.j1 && ok; ++j) {
+            const int f = fill + j - it.j0, ks = f & 1, vs = (f - 1) & 1;
+            bool k_there = false, v_there = false;
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+                if (j > it.j0 && j - 1 < end[t]) {
+                    if (!v_there)
+                        ok = ok && mbar_wait(bars + 8 * (kVFull + vs), ((f - 1) >> 1) & 1, kWaitNs);
+                    v_there = true;
+                    ok = ok && mbar_wait(bars + 8 * (kPFull + t), np[t]++ & 1, kWaitNs);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    const uint32_t v_s = base_s + kOffV + vs * kOperand;
+#pragma unroll
+                    for (int i = 0; i < kKv / 16; ++i)   // 16 tokens a product: two groups of eight rows
+                        tc_mma_ts(tmem + kColO + t * 128, tmem + kColS + t * 128 + i * 8, tc_sdesc(v_s + i * 2048, kSub, 1024), idO,
+                                  j - 1 > it.j0 || i > 0);
+                    if (j == end[t])
+                        tc_commit(bars + 8 * (kOFull + t));
+                }
+                if (j < end[t]) {
+                    if (!k_there)
+                        ok = ok && mbar_wait(bars + 8 * (kKFull + ks), (f >> 1) & 1, kWaitNs);
+                    k_there = true;
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    const uint32_t q_s = base_s + kOffQ + t * kOperand, k_s = base_s + kOffK + ks * kOperand;
+#pragma unroll
+                    for (int i = 0; i < kD / 16; ++i)   // 16 dims a product; the last four in the second half
+                        tc_mma(tmem + kColS + t * 128, tc_sdesc(q_s + (i >> 2) * kSub + (i & 3) * 32, 16, 1024),
+                               tc_sdesc(k_s + (i >> 2) * kSub + (i & 3) * 32, 16, 1024), idS, i > 0);
+                    tc_commit(bars + 8 * (kSFull + t));
+                }
+            }
+            if (v_there)
+                tc_commit(bars + 8 * (kVEmpty + vs));
+            if (k_there)
+                tc_commit(bars + 8 * (kKEmpty + ks));
+        }
+        fill += it.j1 - it.j0;
+    }
+    if (!ok)
+        report(p.status, SPARSE_ERR_TIMEOUT);
+    // every product is done before the tensor memory is given back
+    tc_commit(bars + 8 * kDrain);
+    mbar_wait(bars + 8 * kDrain, 0, kWaitNs);
+}
+
+// ---------------------------------------------------------------- softmax
+
+// A tile's queries to f16, each row scaled by a power of two of its own (its largest element to
+// 2^14 .. 2^15), two rows a warp at a time; rows past the tile's are zero.
+__device__ __forceinline__ void load_queries(const ChunkParams &p, const Item &it, int t, uint8_t *base, uint32_t base_s, int warp,
+                                             int lane)
+{
+    float *qs = reinterpret_cast<float *>(base + kOffQs) + t * kTileRows;
+    const int c = lane & 15;
+    const int n = min(p.per_tile, it.n - t * p.per_tile) * p.G;
+#pragma unroll 1
+    for (int i0 = 0; i0 < 16; i0 += 8) {
+        uint4 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = warp * 32 + (i0 + i) * 2 + (lane >> 4);
+            x[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < n) {
+                const int tok = row / p.G, g = row - tok * p.G;
+                x[i] = *reinterpret_cast<const uint4 *>(p.Q + (it.row + t * p.per_tile + tok) * p.q_stride +
+                                                        static_cast<size_t>(it.head * p.G + g) * kD + c * 8);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = warp * 32 + (i0 + i) * 2 + (lane >> 4);
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            float v[8];
+            float top = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                v[2 * k] = __uint_as_float(w[k] << 16);
+                v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                top = fmaxf(top, fabsf(v[k]) <= 0x1.fep127f ? fabsf(v[k]) : 0.f);   // of the finite ones
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            // 2^up brings the row's largest element to 2^14 .. 2^15
+            const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+            const int up = top > 0.f ? max(-113, min(126, 14 - e)) : 0;
+            const float f = __uint_as_float(static_cast<uint32_t>(up + 127) << 23 | p.q_sign);
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                h[k] = pack_f16x2(v[2 * k] * f, v[2 * k + 1] * f);
+            const uint32_t at = base_s + kOffQ + t * kOperand + (c >> 3) * kSub + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+            if (c == 0)
+                qs[row] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+        }
+    }
+}
+
+// Writes a row of 128 values, 32 at a time, in bf16.
+__device__ __forceinline__ void store_bf16(uint16_t *dst, const float (&o)[32])
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<uint4 *>(dst + 8 * k) =
+            make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]), pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
+                       pack_bf16x2(o[8 * k + 4], o[8 * k + 5]), pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
+}
+
+// O in the units of the weights, 2^mo, to O: times 2^(mo - m) / l, in two factors of 2^(half), since
+// their product may be out of range where the result is not.
+struct Finish {
+    float half, rest;
+    __device__ __forceinline__ Finish(float m, float l, float mo)
+    {
+        half = l == 0.f || mo == -INFINITY ? 0.f : exp2f(0.5f * (mo - m));
+        rest = l == 0.f ? 0.f : half / l;
+        if (l != l)
+            half = rest = l;
+    }
+    __device__ __forceinline__ float operator()(float o) const { return o * half * rest; }
+};
+
+__device__ __forceinline__ float lse_of(float m, float l)
+{
+    return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309417f;
+}
+
+// One tile's softmax: a thread a row.
+__device__ __forceinline__ void softmax_loop(const ChunkParams &p, uint8_t *base, uint32_t base_s, uint32_t tmem, int t, int tid)
+{
+    const uint32_t bars = base_s + kOffBars;
+    const int warp = tid >> 5, lane = tid & 31;   // within the tile
+    const uint32_t s_t = tmem + kColS + t * 128 + (static_cast<uint32_t>(warp * 32) << 16);
+    const uint32_t o_t = tmem + kColO + t * 128 + (static_cast<uint32_t>(warp * 32) << 16);
+    const int tok_in = tid / p.G, g = tid - tok_in * p.G;
+    Walk walk;
+    walk.open(p, reinterpret_cast<const Start *>(base + kOffStart), reinterpret_cast<const uint16_t *>(base + kOffLive));
+    const float *qs = reinterpret_cast<const float *>(base + kOffQs) + t * kTileRows;
+    uint32_t ns = 0, no = 0;
+    int fill = 0, items = 0;
+    int4 tail = make_int4(-1, 0, 0, 0);
+    int head = 0;
+    Item it;
+    bool ok = true;
+    while (ok && walk.next(p, it)) {
+        const int tok = t * p.per_tile + tok_in;
+        const bool valid = tok_in < p.per_tile && tok < it.n;
+        const size_t out = static_cast<size_t>(it.row + tok) * p.H_q + it.head * p.G + g;
+        if (it.all == 0) {   // no token is seen
+            if (valid) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    *reinterpret_cast<uint4 *>(p.O + out * kD + 8 * k) = make_uint4(0u, 0u, 0u, 0u);
+                if (p.lse != nullptr)
+                    p.lse[out] = -INFINITY;
+            }
+            continue;
+        }
+        const int end = min(it.j1, it.steps[t]);
+        const int first_pos = it.pos + t * p.per_tile;
+        const int pos = valid ? it.pos + tok : -1;
+        float m = -INFINITY, mo = -INFINITY, l = 0.f;
+        if (end > it.j0) {
+            load_queries(p, it, t, base, base_s, warp, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bars + 8 * (kQFull + t));
+        }
+        const float q_scale = qs[tid];   // written by this warp
+        for (int j = it.j0; j < end && ok; ++j) {
+            const int f = fill + j - it.j0;
+            ok = mbar_wait(bars + 8 * (kRec + (f & 3)), (f >> 2) & 1, kWaitNs);
+            ok = __all_sync(0xffffffffu, ok && mbar_wait(bars + 8 * (kSFull + t), ns++ & 1, kWaitNs));
+            if (!ok)
+                break;
+            tc_fence_after();
+            const float4 rec = *reinterpret_cast<const float4 *>(base + kOffRec + (f & 3) * 16);
+            const int see = pos - j * kKv;   // columns up to this one
+            const bool masked = j * kKv + kKv - 1 > first_pos || rec.x < 0.f || rec.y < 0.f;
+            float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t s[32];
+                tc_ld32(s_t + 32 * k, s);
+                tc_wait_ld(s);
+                if (masked) {
+                    const int lim = (k < 2 ? rec.x : rec.y) < 0.f ? -1 : see - 32 * k;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        top[k >> 1] = fmaxf(top[k >> 1], i <= lim ? __uint_as_float(s[i]) : -INFINITY);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        top[k >> 1] = fmaxf(top[k >> 1], __uint_as_float(s[i]));
+                }
+            }
+            const float sc[2] = {q_scale * fmaxf(rec.x, 0.f), q_scale * fmaxf(rec.y, 0.f)};
+            const float lv[2] = {rec.z, rec.w};
+            float t_m = -INFINITY, t_o = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float x = top[i] == -INFINITY ? -INFINITY : top[i] * sc[i];
+                t_m = fmaxf(t_m, x);
+                t_o = fmaxf(t_o, x == -INFINITY ? -INFINITY : x + lv[i]);
+            }
+            if (t_m > m + kLazy) {
+                l *= ex2_approx(m - t_m);
+                m = t_m;
+            }
+            const bool grow = t_o > mo + kLazy;
+            const float alpha = grow ? ex2_approx(mo - t_o) : 1.f;
+            mo = grow ? t_o : mo;
+            if (j > it.j0 && __any_sync(0xffffffffu, grow)) {
+                // O holds every step up to the one before: its products were issued before these scores'
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t o[32];
+                    tc_ld32(o_t + 32 * k, o);
+                    tc_wait_ld(o);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                    tc_st32(o_t + 32 * k, o);
+                }
+            }
+            __syncwarp();
+            const float m_ref = m == -INFINITY ? 0.f : m;
+            float lf[2];
+            bool far = false;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                lf[i] = mo == -INFINITY ? -INFINITY : lv[i] + (m_ref - mo);
+                far = far || !(fabsf(lf[i]) <= kFarWeight);
+            }
+            far = __any_sync(0xffffffffu, far);
+            float sum[2] = {0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int h = k >> 1;
+                const float off = lf[h] - m_ref;
+                uint32_t s[32], w[16];
+                tc_ld32(s_t + 32 * k, s);
+                tc_wait_ld(s);
+                const int lim = !masked ? 31 : (k < 2 ? rec.x : rec.y) < 0.f ? -1 : see - 32 * k;
+                if (far) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float x = __uint_as_float(s[i]);
+                        const float e = i <= lim ? ex2_approx(fmaf(x, sc[h], off)) : 0.f;
+                        sum[h] += i <= lim ? ex2_approx(fmaf(x, sc[h], -m_ref)) : 0.f;
+                        s[i] = __float_as_uint(e);
+                    }
+                } else if (masked) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float e = i <= lim ? ex2_approx(fmaf(__uint_as_float(s[i]), sc[h], off)) : 0.f;
+                        sum[h] += e;
+                        s[i] = __float_as_uint(e);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float e = ex2_approx(fmaf(__uint_as_float(s[i]), sc[h], off));
+                        sum[h] += e;
+                        s[i] = __float_as_uint(e);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    w[i] = pack_f16x2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+                tc_st16u(s_t + 16 * k, w);
+            }
+            l += far ? sum[0] + sum[1] : sum[0] * ex2_approx(-lf[0]) + sum[1] * ex2_approx(-lf[1]);
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bars + 8 * (kPFull + t));
+        }
+        if (ok && end > it.j0) {
+            ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (kOFull + t), no++ & 1, kWaitNs));
+            tc_fence_after();
+        }
+        if (!ok)
+            break;
+        // the item's rows, or this CTA's part of them
+        const bool whole = it.j0 == 0 && it.j1 == it.all;
+        const int *first = reinterpret_cast<const int *>(base + kOffNan) + (items & 1) * kD;
+        const bool nan = end > it.j0 && *(reinterpret_cast<const int *>(base + kOffNan) + 2 * kD + (items & 1)) != 0;
+        const Finish fin(m, l, mo);
+        float *part = p.parts + static_cast<size_t>(2 * blockIdx.x + (it.j0 == 0 ? 1 : 0)) * kPartFloats;
+        const int prow = t * kTileRows + tid;
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+            uint32_t o[32];
+            float v[32];
+            __syncwarp();
+            if (end > it.j0) {
+                tc_ld32(o_t + 32 * k, o);
+                tc_wait_ld(o);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    o[i] = 0u;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                v[i] = __uint_as_float(o[i]);
+            if (nan) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    v[i] = first[32 * k + i] <= pos ? NAN : v[i];
+            }
+            if (valid && whole) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    v[i] = fin(v[i]);
+                store_bf16(p.O + out * kD + 32 * k, v);
+            } else if (valid) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<float4 *>(part + prow * kD + 32 * k + 4 * i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            }
+        }
+        if (valid) {
+            if (whole) {
+                if (p.lse != nullptr)
+                    p.lse[out] = lse_of(m, l);
+            } else {
+                float *stat = part + kTiles * kTileRows * kD;
+                stat[prow] = m;
+                stat[kTiles * kTileRows + prow] = l;
+                stat[2 * kTiles * kTileRows + prow] = mo;
+            }
+        }
+        if (it.j0 > 0)
+            head = it.j1 == it.all ? 2 : 1;
+        else if (!whole)
+            tail = make_int4(it.row, it.head, it.n, 0);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && end > it.j0)
+            mbar_arrive(bars + 8 * (kDone + 2 * t + (items & 1)));
+        ++items;
+        fill += it.j1 - it.j0;
+    }
+    if (!ok && lane == 0)
+        report(p.status, SPARSE_ERR_TIMEOUT);
+    if (t == 0 && tid == 0) {
+        p.tails[blockIdx.x] = ok ? tail : make_int4(-1, 0, 0, 0);
+        p.heads[blockIdx.x] = ok ? head : 0;
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_constant__ ChunkParams p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_s = smem_u32(smem_raw);
+    const uint32_t base_s = (raw_s + 1023u) & ~1023u;
+    uint8_t *base = smem_raw + (base_s - raw_s);
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const uint32_t bars = base_s + kOffBars;
+    int *ctrl = reinterpret_cast<int *>(base + kOffCtrl);
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bars + 8 * (kKFull + i), 4);
+            mbar_init(bars + 8 * (kKEmpty + i), 1);
+            mbar_init(bars + 8 * (kVFull + i), 4);
+            mbar_init(bars + 8 * (kVEmpty + i), 1);
+        }
+        for (int t = 0; t < kTiles; ++t) {
+            mbar_init(bars + 8 * (kQFull + t), 4);
+            mbar_init(bars + 8 * (kSFull + t), 1);
+            mbar_init(bars + 8 * (kPFull + t), 4);
+            mbar_init(bars + 8 * (kOFull + t), 1);
+            mbar_init(bars + 8 * (kDone + 2 * t), 4);
+            mbar_init(bars + 8 * (kDone + 2 * t + 1), 4);
+        }
+        for (int i = 0; i < 4; ++i)
+            mbar_init(bars + 8 * (kRec + i), 1);
+        mbar_init(bars + 8 * kDrain, 1);
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp)
+        tc_alloc(base_s + kOffCtrl, 512);
+    griddep_wait();
+    griddep_launch_dependents();
+    tc_fence_before();
+    find_start(p, base, tid);   // ends with a barrier
+    tc_fence_after();
+    const uint32_t tmem = static_cast<uint32_t>(ctrl[0]);
+    if (warp < kSoftmaxWarps)
+        softmax_loop(p, base, base_s, tmem, warp >> 2, tid & 127);
+    else if (warp < kMmaWarp)
+        convert_loop(p, base, base_s, tid & 127);
+    else if ((tid & 31) == 0)
+        mma_loop(p, base, base_s, tmem);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tc_dealloc(tmem, 512);
+    }
+}
+
+// Items that several CTAs share: CTA (c, y) takes rows y * 8 .. of the one that CTA c began, a warp a
+// row, and adds up its parts in CTA order.
+constexpr int kMergeRows = 8;
+
+__global__ void __launch_bounds__(32 * kMergeRows) paged_chunk_merge_kernel(const __grid_constant__ ChunkParams p, int n_ctas)
+{
+    griddep_wait();
+    const int c0 = blockIdx.x, lane = threadIdx.x & 31;
+    const int4 tail = p.tails[c0];
+    if (tail.x < 0)
+        return;
+    const int prow = blockIdx.y * kMergeRows + (threadIdx.x >> 5), t = prow / kTileRows, r = prow % kTileRows;
+    const int tok_in = r / p.G, g = r - tok_in * p.G, tok = t * p.per_tile + tok_in;
+    if (tok_in >= p.per_tile || tok >= tail.z)
+        return;
+    constexpr int kAll = kTiles * kTileRows;
+    float m = -INFINITY, mo = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = c0; c < n_ctas; ++c) {
+        const int kind = c == c0 ? 1 : p.heads[c];
+        if (kind == 0)
+            continue;
+        const float *part = p.parts + static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * kPartFloats;
+        const float *stat = part + kAll * kD;
+        const float pm = stat[prow], pl = stat[kAll + prow], pmo = stat[2 * kAll + prow];
+        const float4 x = *reinterpret_cast<const float4 *>(part + prow * kD + 4 * lane);
+        const float nm = fmaxf(m, pm), nmo = fmaxf(mo, pmo);
+        const float a = m == -INFINITY ? 0.f : exp2f(m - nm), b = pm == -INFINITY ? 0.f : exp2f(pm - nm);
+        l = l * a + pl * b;
+        m = nm;
+        const float ao = mo == -INFINITY ? 0.f : exp2f(mo - nmo), bo = pmo == -INFINITY ? 0.f : exp2f(pmo - nmo);
+        o = make_float4(o.x * ao + x.x * bo, o.y * ao + x.y * bo, o.z * ao + x.z * bo, o.w * ao + x.w * bo);
+        mo = nmo;
+        if (kind == 2)
+            break;
+    }
+    const Finish fin(m, l, mo);
+    const size_t out = static_cast<size_t>(tail.x + tok) * p.H_q + tail.y * p.G + g;
+    *reinterpret_cast<uint2 *>(p.O + out * kD + 4 * lane) =
+        make_uint2(pack_bf16x2(fin(o.x), fin(o.y)), pack_bf16x2(fin(o.z), fin(o.w)));
+    if (lane == 0 && p.lse != nullptr)
+        p.lse[out] = lse_of(m, l);
+}
+
+bool sizes_ok(int B, int H_q, int H_kv)
+{
+    return B >= 1 && B <= kMaxB && H_kv >= 1 && H_q >= H_kv && H_q % H_kv == 0 && H_q / H_kv <= 16 && H_kv <= 65535;
+}
+
+size_t workspace_bytes_of(int ctas)
+{
+    return static_cast<size_t>(ctas) * (sizeof(int4) + 16 + 2ull * kPartFloats * sizeof(float));
+}
+
+}  // namespace
+
+extern "C" SPARSE_API size_t sparse_paged_chunk_attn_f8_workspace_size(int B, int H_q, int H_kv)
+{
+    sp_host::DeviceInfo dev;
+    if (!sizes_ok(B, H_q, H_kv) || sp_host::device_info(&dev) != SPARSE_OK)
+        return 0;
+    return workspace_bytes_of(dev.sm_count);
+}
+
+extern "C" SPARSE_API int sparse_paged_chunk_attn_f8(const uint16_t *Q, long long q_stride, const uint8_t *kv_pages,
+                                                     const float *kv_scale, int n_pages, const int *block_table, int max_blocks,
+                                                     const int *cu_new, const int *start, int n_tok, int B, int H_q, int H_kv,
+                                                     float scale, uint16_t *O, float *lse, void *workspace,
+                                                     size_t workspace_bytes, int *status, void *stream)
+{
+    using sp_host::aligned16;
+    using sp_host::fail;
+    const char *name = "sparse_paged_chunk_attn_f8";
+    if (!Q || !kv_pages || !kv_scale || !block_table || !cu_new || !start || !O || !workspace)
+        return fail(SPARSE_ERR_INVALID_ARG, "%s: null pointer", name);
+    if (!aligned16(Q) || !aligned16(kv_pages) || !aligned16(kv_scale) || !aligned16(block_table) || !aligned16(cu_new) ||
+        !aligned16(start) || !aligned16(O) || !aligned16(workspace) || (lse != nullptr && !aligned16(lse)))
+        return fail(SPARSE_ERR_INVALID_ARG, "%s: buffers must be 16-byte aligned", name);
+    if (B < 1 || H_kv < 1 || H_q < H_kv || H_q % H_kv != 0 || n_pages < 1 || max_blocks < 1 || n_tok < 1)
+        return fail(SPARSE_ERR_INVALID_ARG, "%s: bad size (B=%d H_q=%d H_kv=%d n_pages=%d max_blocks=%d n_tok=%d)", name, B, H_q,
+                    H_kv, n_pages, max_blocks, n_tok);
+    if (q_stride < static_cast<long long>(H_q) * kD || q_stride % 8 != 0)
+        return fail(SPARSE_ERR_INVALID_ARG, "%s: q_stride=%lld, %lld or more and a multiple of 8 expected", name, q_stride,
+                    static_cast<long long>(H_q) * kD);
+    // scores are exponentiated base 2
+    const float scale_log2 = (scale == 0.f ? 1.f / sqrtf(static_cast<float>(kD)) : scale) * 1.44269504088896340736f;
+    if (!isfinite(scale_log2))
+        return fail(SPARSE_ERR_INVALID_ARG, "%s: scale * log2(e) is not finite", name);
+    if (!sizes_ok(B, H_q, H_kv) || n_pages > kMaxPages || max_blocks >= kMaxPages || n_tok > kMaxRows)
+        return fail(SPARSE_ERR_UNSUPPORTED, "%s: G=%d > 16, B=%d > %d, H_kv=%d > 65535, n_pages or max_blocks too large, or n_tok > %d",
+                    name, H_q / H_kv, B, kMaxB, H_kv, kMaxRows);
+    // the list's work fits 62 bits
+    const int per_tile = kTileRows / (H_q / H_kv);
+    const double work = (static_cast<double>(n_tok) / (kTiles * per_tile) + B) * H_kv * (static_cast<double>(max_blocks) * kBlk + n_tok + kItemCost);
+    if (work > 0x1p61)
+        return fail(SPARSE_ERR_UNSUPPORTED, "%s: n_tok, max_blocks and H_kv are too large together", name);
+    const size_t need = sparse_paged_chunk_attn_f8_workspace_size(B, H_q, H_kv);
+    if (workspace_bytes < need)
+        return fail(SPARSE_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", name, workspace_bytes, need);
+    sp_host::DeviceInfo dev;
+    int rc = sp_host::device_info(&dev);
+    if (rc != SPARSE_OK)
+        return rc;
+    static int configured[64];
+    const void *kern = reinterpret_cast<const void *>(paged_chunk_kernel);
+    rc = sp_host::configure_kernel(kern, kSmem, dev.device, configured);
+    if (rc != SPARSE_OK)
+        return rc;
+    const int ctas = dev.sm_count;
+    float *parts = static_cast<float *>(workspace);
+    int4 *tails = reinterpret_cast<int4 *>(parts + 2ull * ctas * kPartFloats);
+    ChunkParams p{};
+    p.Q = Q;
+    p.kv_pages = kv_pages;
+    p.kv_scale = kv_scale;
+    p.block_table = block_table;
+    p.cu_new = cu_new;
+    p.start = start;
+    p.O = O;
+    p.lse = lse;
+    p.parts = parts;
+    p.tails = tails;
+    p.heads = reinterpret_cast<int *>(tails + ctas);
+    p.status = status;
+    p.q_stride = q_stride;
+    p.scale_log2 = fabsf(scale_log2);
+    p.q_sign = scale_log2 < 0.f ? 0x80000000u : 0u;
+    p.n_pages = n_pages;
+    p.max_blocks = max_blocks;
+    p.n_tok = n_tok;
+    p.B = B;
+    p.H_q = H_q;
+    p.H_kv = H_kv;
+    p.G = H_q / H_kv;
+    p.per_tile = per_tile;
+    rc = sp_host::cuda_status(launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), kThreads, kSmem, stream, p), name);
+    if (rc != SPARSE_OK)
+        return rc;
+    const void *merge = reinterpret_cast<const void *>(paged_chunk_merge_kernel);
+    return sp_host::cuda_status(launch_pdl(merge, dim3(static_cast<unsigned>(ctas), kTiles * kTileRows / kMergeRows), 32 * kMergeRows, 0,
+                                           stream, p, ctas),
+                                name);
+}

@@ -670,6 +670,113 @@ SPARSE_API int sparse_paged_decode_attn_f8(const uint16_t *Q, const uint8_t *kv_
 /* Bytes of the sparse_paged_decode_attn_f8 workspace on the current device; 0 if the sizes are invalid. */
 SPARSE_API size_t sparse_paged_decode_attn_f8_workspace_size(int B, int H_q, int H_kv);
 
+/*
+ * sparse_paged_chunk_attn_f8 -- attention of the tokens that a step adds, over the paged
+ * cache: prompts, parts of prompts and single tokens, after sparse_paged_append_f8 has
+ * written their keys and values.  Request b's rows are t in [cu_new[b], cu_new[b + 1]), at
+ * positions start[b] + t - cu_new[b] (as sparse_page_plan writes both); row t sees the
+ * tokens up to its own position:
+ *     O[t][h] = sum_j softmax_j(scale * q_{t,h} . (ks k_j)) (vs v_j),  j <= position of t.
+ *   Q            [n_tok][H_q][128] bf16; a token's H_q * 128 values are contiguous and tokens
+ *                are q_stride elements apart (>= H_q * 128, a multiple of 8), so Q may be a part
+ *                of one projection's rows.
+ *   cu_new       [B + 1] int32, start [B] int32.  start[b] < 0 (a request that got no pages):
+ *                its rows see nothing, O = 0 and lse = -inf.  Rows before cu_new[0] and from
+ *                cu_new[B] on are left as they were.
+ *   O, lse       [n_tok][H_q][128] bf16 and [n_tok][H_q] fp32 (or NULL), contiguous.
+ *   scale        as for sparse_paged_decode_attn_f8.
+ *   workspace    sparse_paged_chunk_attn_f8_workspace_size() bytes, 16-byte aligned, of any
+ *                contents.  Calls of any sizes may share it, but not at the same time.
+ * A token's values that no row sees are never used, whatever bytes they hold; NaN among the
+ * values of a token reaches the rows that see it and no others.  A page outside [0, n_pages)
+ * (left out), rows outside [0, n_tok) (left out) and positions past 64 max_blocks (they see
+ * the table's tokens) are reported as SPARSE_ERR_BAD_INDEX; a call that gives up waiting as
+ * SPARSE_ERR_TIMEOUT (O and lse are then not to be used).  The result does not depend on
+ * timing.
+ * G = H_q / H_kv <= 16, B <= 4096, n_tok <= 2^30, n_pages <= 2^25, max_blocks < 2^25.
+ */
+SPARSE_API int sparse_paged_chunk_attn_f8(const uint16_t *Q, long long q_stride, const uint8_t *kv_pages,
+                                          const float *kv_scale, int n_pages, const int *block_table, int max_blocks,
+                                          const int *cu_new, const int *start, int n_tok, int B, int H_q, int H_kv,
+                                          float scale, uint16_t *O, float *lse, void *workspace,
+                                          size_t workspace_bytes, int *status, void *stream);
+
+/* Bytes of the sparse_paged_chunk_attn_f8 workspace on the current device; 0 if the sizes are invalid. */
+SPARSE_API size_t sparse_paged_chunk_attn_f8_workspace_size(int B, int H_q, int H_kv);
+
+/*
+ * sparse_rope -- rotary positions of projected rows, before they are appended and attended
+ * with.  Pair i (i < rot_dim / 2) of a row at position t = pos[row], elements a and b, becomes
+ *     factor * (a cos x - b sin x),  factor * (b cos x + a sin x),  x = t * inv_freq[i],
+ * in fp32, rounded once; the elements from rot_dim on are copied.
+ *   interleaved  0: pair i is elements i and i + rot_dim / 2; otherwise 2 i and 2 i + 1.
+ *   inv_freq     [rot_dim / 2] fp64, finite: the angle is that of the exact product at any position.
+ *   pos          [n_tok] int32; a row with a negative position is not written (padding, and
+ *                the rows of requests without pages, as in sparse_page_plan's tok_pos).
+ *   Q, K         [n_tok][H][128] bf16, tokens q_stride / k_stride elements apart (>= H * 128, a
+ *                multiple of 8); H_kv = 0: queries alone, K and K_out are not used.
+ *   Q_out, K_out the same with strides of their own; either may be its input (the same
+ *                address and stride), else they do not overlap the inputs.
+ * rot_dim is even, 2 .. 128; factor is finite.
+ */
+SPARSE_API int sparse_rope(const uint16_t *Q, long long q_stride, int H_q, const uint16_t *K, long long k_stride,
+                           int H_kv, const int *pos, int n_tok, const double *inv_freq, int rot_dim, int interleaved,
+                           float factor, uint16_t *Q_out, long long q_out_stride, uint16_t *K_out,
+                           long long k_out_stride, void *stream);
+
+/*
+ * sparse_page_fork -- requests that become copies of others (samples, beams, common prefixes)
+ * and requests that end, with full pages shared.  src[b] = b: request b stays as it is;
+ * src[b] < 0: it ends; else it becomes a copy of request s = src[b], which has to stay
+ * (src[s] = s).  page_extra [n_pages] int32 counts a page's holders beyond the first: all zero
+ * at the start, and kept by this call alone.  In this order:
+ *   1. the requests that end or become copies give up their pages (blocks [0, ceil(seq_len /
+ *      64))): a page held by others loses a holder, a page without any goes onto the end of the
+ *      free list, in the place of its last holder by request and block.  Then the list holds F pages.
+ *   2. a copy takes n = seq_len[s] tokens, or, where fork_len is given and 0 <= fork_len[b] < n, the
+ *      fork_len[b] tokens rounded down to whole blocks.  It shares the source's n / 64 full pages.  If
+ *      n is no multiple of 64 it also needs a page of its own for the rest; pages are taken from the end
+ *      of the list in request order.  A copy whose need, with those before it, is above F gets
+ *      nothing and ends (status: SPARSE_ERR_NO_PAGES).
+ *   3. seq_len[b] is n for a copy, 0 for a request that ended, as before for one that stays.
+ *      copy_src[b], copy_dst[b] are the pages that sparse_paged_copy_f8 has to copy for b in
+ *      every layer, -1 if none.
+ * A request whose pages are shared must end here, not by sparse_page_plan's negative n_new, which
+ * gives its pages to others at once.  The result does not depend on timing.
+ *   src, fork_len (or NULL), seq_len, copy_src, copy_dst  [B] int32.
+ *   block_table  [B][max_blocks] int32; free_pages [n_pages] int32 with n_free one int32, as
+ *                in sparse_page_plan; seq_len, block_table, page_extra, free_pages, n_free updated.
+ *   workspace    sparse_page_fork_workspace_size() bytes, 16-byte aligned, of any contents.
+ *   status       a source outside [0, B) or that does not stay (the request stays as it is), a length
+ *                outside [0, 64 max_blocks] (it gives up no pages, its copies end), a page outside
+ *                [0, n_pages), an *n_free outside [0, n_pages] (clamped), a count that is too small or more
+ *                pages returned than the list holds (dropped) is reported as SPARSE_ERR_BAD_INDEX, also
+ *                where the word holds SPARSE_ERR_NO_PAGES.
+ * B <= 4096; n_pages <= 2^25; max_blocks < 2^25; B * ceil(max_blocks / 32) < 2^30.
+ */
+SPARSE_API int sparse_page_fork(const int *src, const int *fork_len, int B, int *seq_len, int *block_table,
+                                int max_blocks, int *page_extra, int *free_pages, int n_pages, int *n_free,
+                                int *copy_src, int *copy_dst, void *workspace, size_t workspace_bytes, int *status,
+                                void *stream);
+
+/* Bytes of the sparse_page_fork workspace; 0 if the sizes are invalid. */
+SPARSE_API size_t sparse_page_fork_workspace_size(int B, int max_blocks);
+
+/*
+ * sparse_paged_copy_f8 -- what a fork has to copy in one layer: for i < n_copy the keys, values
+ * and scales of page copy_src[i] to page copy_dst[i] (both -1: nothing), and, with ktil
+ * [B][H_kv][N_cap][128] fp32, the compressed keys of the first ceil(seq_len[b] / 64) blocks of
+ * request src[b] to request b, for every b with 0 <= src[b] != b (src as for sparse_page_fork,
+ * seq_len as that call left it).  No page is copied to twice, or copied to and from.
+ *   ktil         NULL: pages alone; B, N_cap, src and seq_len are then not used.
+ *   status       a page outside [0, n_pages), a source that does not stay or a length outside
+ *                [0, 64 N_cap] is reported as SPARSE_ERR_BAD_INDEX and left out.
+ * n_pages <= 2^25, H_kv <= 65535, B <= 4096, B * N_cap / 32 < 2^30.
+ */
+SPARSE_API int sparse_paged_copy_f8(uint8_t *kv_pages, float *kv_scale, int n_pages, int H_kv, const int *copy_src,
+                                    const int *copy_dst, int n_copy, float *ktil, int B, int N_cap, const int *src,
+                                    const int *seq_len, int *status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
