@@ -21,9 +21,15 @@ constexpr int kMinWork = 1024;                    // the least share of a CTA, i
 constexpr int kMinCut = 2;                        // steps on either side of a cut through an item
 
 constexpr int kSoftmaxWarps = 4 * kTiles;
-constexpr int kConvertWarp = kSoftmaxWarps;       // first of four
-constexpr int kMmaWarp = kConvertWarp + 4;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kConvertWarp = kSoftmaxWarps;       // the first of them
+constexpr int kConvertWarps = 8;
+constexpr int kConvertThreads = 32 * kConvertWarps;
+constexpr int kPieces = kKv * kD / 16 / kConvertThreads;   // 16-byte pieces of a step's keys a thread
+constexpr int kMmaWarp = kConvertWarp + kConvertWarps;
+constexpr int kThreads = 32 * (kMmaWarp + 4);     // three warps are there for the registers' sake alone
+// Registers a thread of the five warpgroups; the block is launched with kRegs a thread.
+constexpr int kRegs = 96, kSoftmaxRegs = 144, kConvertRegs = 72, kMmaRegs = 48;
+static_assert(kTiles * kSoftmaxRegs + 2 * kConvertRegs + kMmaRegs <= 5 * kRegs, "the split is what the block has");
 constexpr int kSub = kKv * 128;                   // 64 of 128 dims of 128 f16 rows, 128 bytes a row: 16 KB
 constexpr int kOperand = 2 * kSub;                // 128 x 128 f16
 
@@ -50,8 +56,8 @@ constexpr int kOffCtrl = kOffRec + 64;            // int [16]
 constexpr int kOffStart = kOffCtrl + 64;          // Start
 constexpr int kOffQs = kOffStart + 64;            // float [tiles][128]
 constexpr int kOffNan = kOffQs + kTiles * kTileRows * 4;   // int [2][128], then int [2]
-constexpr int kOffScan = kOffNan + 2 * kD * 4 + 16;        // long long [16], int [16]
-constexpr int kOffLive = kOffScan + 16 * 12;               // uint16 [kMaxB]
+constexpr int kOffScan = kOffNan + 2 * kD * 4 + 16;        // long long [32], int [32]
+constexpr int kOffLive = kOffScan + 32 * 12;               // uint16 [kMaxB]
 constexpr int kSmem = kOffLive + 2 * kMaxB + 1024;
 static_assert(kNumBars * 8 <= 256 && kOffRec % 16 == 0 && kOffStart % 8 == 0 && kOffScan % 8 == 0, "alignment");
 static_assert(kSmem <= 232448, "shared memory of a CTA");
@@ -99,12 +105,28 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_m
            (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// D (tensor memory) = A B (+ D), A in tensor memory.
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, bool accumulate)
+// Upper and lower words of a matrix descriptor (tc_sdesc): a step along an operand adds to the lower one.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-                 "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+    return ((addr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
+}
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);   // 8-row groups 1024 bytes apart, version 1, 128-byte swizzle
+
+// D (tensor memory) = A B (+ D), both in shared memory.
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+                 "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+// The same with A in tensor memory.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+                 "r"(a_tmem), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate)
                  : "memory");
 }
 
@@ -133,14 +155,6 @@ __device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t (&r)[32])
     asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
                  "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
                  I8(r, 0), I8(r, 8), I8(r, 16), I8(r, 24)
-                 : "memory");
-}
-
-__device__ __forceinline__ void tc_st16u(uint32_t taddr, const uint32_t (&r)[16])
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-                 "%15, %16};" ::"r"(taddr),
-                 I8(r, 0), I8(r, 8)
                  : "memory");
 }
 
@@ -280,7 +294,7 @@ struct Walk {
 __device__ __forceinline__ void find_start(const ChunkParams &p, uint8_t *base, int tid)
 {
     long long *warp_work = reinterpret_cast<long long *>(base + kOffScan);
-    int *warp_live = reinterpret_cast<int *>(base + kOffScan + 16 * 8);
+    int *warp_live = reinterpret_cast<int *>(base + kOffScan + 32 * 8);
     uint16_t *list = reinterpret_cast<uint16_t *>(base + kOffLive);
     Start *s = reinterpret_cast<Start *>(base + kOffStart);
     constexpr int kWarps = kThreads / 32;
@@ -414,102 +428,141 @@ __device__ __forceinline__ bool has_nan(uint4 x)
     return ((f(x.x) | f(x.y) | f(x.z) | f(x.w)) & 0x80808080u) != 0u;
 }
 
-// The four warps that convert: pieces i * 128 + tid of a tile of 128 tokens, eight a row.
+// The converters' steps, one after another across items.
+struct Steps {
+    Walk walk;
+    Item it;
+    int j, items;
+    bool begins;             // the first step of an item
+    const uint8_t *src[2];   // the keys of its two pages, this thread's piece of the first row
+    int rows;                // tokens of the step that some row sees; those past it are zero
+    float rec[4];            // thread 0: scales
+
+    __device__ __forceinline__ void open(const ChunkParams &p, uint8_t *base)
+    {
+        walk.open(p, reinterpret_cast<const Start *>(base + kOffStart), reinterpret_cast<const uint16_t *>(base + kOffLive));
+        j = it.j1 = items = 0;
+    }
+    __device__ __forceinline__ bool next(const ChunkParams &p, int tid)
+    {
+        begins = ++j >= it.j1;
+        if (begins) {
+            do {
+                if (!walk.next(p, it))
+                    return false;
+            } while (it.all == 0);
+            j = it.j0;
+            ++items;
+        }
+        const int end = static_cast<int>(min(static_cast<long long>(it.pos) + it.n, static_cast<long long>(p.max_blocks) * kBlk));
+        rows = min(kKv, end - j * kKv);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            bool there = i * kBlk < rows;
+            int page = there ? p.block_table[static_cast<size_t>(it.b) * p.max_blocks + 2 * j + i] : 0;
+            if (there && (page < 0 || page >= p.n_pages)) {
+                there = false;
+                page = 0;
+                if (tid == 0)
+                    report(p.status, SPARSE_ERR_BAD_INDEX);
+            }
+            const size_t at = static_cast<size_t>(page) * p.H_kv + it.head;
+            src[i] = there ? p.kv_pages + at * (2 * kBlk * kD) + tid * 16 : nullptr;
+            rec[i] = -1.f;
+            rec[2 + i] = 0.f;
+            if (tid == 0 && there) {
+                const float2 s = *reinterpret_cast<const float2 *>(p.kv_scale + at * 2);
+                rec[i] = s.x;
+                rec[2 + i] = s.y;   // its logarithm is taken when it is handed on
+            }
+        }
+        return true;
+    }
+    // Pieces i * threads + tid of the step's keys (values: v = 1), eight a row.
+    __device__ __forceinline__ void load(uint4 (&x)[kPieces], int v, int tid) const
+    {
+        constexpr int kRowsOf = kKv / kPieces, kHalf = kPieces / 2;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const uint8_t *s = src[i / kHalf];
+            x[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (s != nullptr && i * kRowsOf + (tid >> 3) < rows)
+                x[i] = *reinterpret_cast<const uint4 *>(s + v * (kBlk * kD) + (i % kHalf) * (kRowsOf * kD));
+        }
+    }
+};
+
+// The warps that convert.  A step's values are on their way while its keys are converted, and the next
+// step's keys while its values are.
 __device__ __forceinline__ void convert_loop(const ChunkParams &p, uint8_t *base, uint32_t base_s, int tid)
 {
     const uint32_t bars = base_s + kOffBars;
-    Walk walk;
-    walk.open(p, reinterpret_cast<const Start *>(base + kOffStart), reinterpret_cast<const uint16_t *>(base + kOffLive));
     const int row0 = tid >> 3, c = tid & 7, lane = tid & 31;
-    int fill = 0, items = 0;
+    int fill = 0;
     uint32_t used[kTiles][2] = {};   // items of either parity that a tile had steps of
-    Item it;
     bool ok = true;
-    while (walk.next(p, it)) {   // a thread that gave up still meets the others
-        if (it.all == 0)
-            continue;
-        int *first = reinterpret_cast<int *>(base + kOffNan) + (items & 1) * kD;
-        int *any = reinterpret_cast<int *>(base + kOffNan) + 2 * kD + (items & 1);
-        // the last of them is finished: a tile without steps does not wait for anyone, and does not count
+    Steps st;
+    st.open(p, base);
+    uint4 x[kPieces], y[kPieces];
+    bool more = st.next(p, tid);
+    if (more)
+        st.load(x, 0, tid);
+    while (more) {   // a thread that gave up still meets the others
+        int *first = reinterpret_cast<int *>(base + kOffNan) + (st.items & 1) * kD;
+        int *any = reinterpret_cast<int *>(base + kOffNan) + 2 * kD + (st.items & 1);
+        const int tok0 = st.j * kKv, stage = fill & 1;
+        st.load(y, 1, tid);
+        if (st.begins) {
+            // the last item that used these words is finished: a tile without steps does not wait for anyone, and does
+            // not count
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-            if (used[t][items & 1] > 0)
-                ok = ok && mbar_wait(bars + 8 * (kDone + 2 * t + (items & 1)), (used[t][items & 1] - 1) & 1, kWaitNs);
-            if (min(it.j1, it.steps[t]) > it.j0)
-                ++used[t][items & 1];
-        }
-        first[tid] = INT_MAX;
-        if (tid == 0)
-            *any = 0;
-        named_barrier_sync(2, 128);
-        ++items;
-        const int end = static_cast<int>(min(static_cast<long long>(it.pos) + it.n, static_cast<long long>(p.max_blocks) * kBlk));
-        const int *table = p.block_table + static_cast<size_t>(it.b) * p.max_blocks;
-        for (int j = it.j0; j < it.j1 && ok; ++j, ++fill) {
-            const int tok0 = j * kKv, stage = fill & 1;
-            // the two pages of the step
-            const uint8_t *src[2];
-            bool there[2];
-            float rec[4];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int blk = 2 * j + i;
-                there[i] = blk * kBlk < end;
-                int page = there[i] ? table[blk] : 0;
-                if (there[i] && (page < 0 || page >= p.n_pages)) {
-                    there[i] = false;
-                    page = 0;
-                    if (tid == 0)
-                        report(p.status, SPARSE_ERR_BAD_INDEX);
-                }
-                const size_t at = static_cast<size_t>(page) * p.H_kv + it.head;
-                src[i] = p.kv_pages + at * (2 * kBlk * kD);
-                rec[i] = -1.f;
-                rec[2 + i] = 0.f;
-                if (tid == 0 && there[i]) {
-                    const float2 s = *reinterpret_cast<const float2 *>(p.kv_scale + at * 2);
-                    rec[i] = s.x;
-                    rec[2 + i] = log2f(s.y);
-                }
+            for (int t = 0; t < kTiles; ++t) {
+                uint32_t &n = used[t][st.items & 1];
+                if (n > 0)
+                    ok = ok && mbar_wait(bars + 8 * (kDone + 2 * t + (st.items & 1)), (n - 1) & 1, kWaitNs);
+                if (min(st.it.j1, st.it.steps[t]) > st.it.j0)
+                    ++n;
             }
-            uint4 x[8], y[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int row = i * 16 + row0;
-                const bool use = there[i >> 2] && tok0 + row < end;
-                const uint8_t *s = src[i >> 2] + (row & 63) * kD + c * 16;
-                x[i] = use ? *reinterpret_cast<const uint4 *>(s) : make_uint4(0u, 0u, 0u, 0u);
-                y[i] = use ? *reinterpret_cast<const uint4 *>(s + kBlk * kD) : make_uint4(0u, 0u, 0u, 0u);
-            }
+            if (tid < kD)
+                first[tid] = INT_MAX;
             if (tid == 0)
-                *reinterpret_cast<float4 *>(base + kOffRec + (fill & 3) * 16) = make_float4(rec[0], rec[1], rec[2], rec[3]);
-            if (fill >= 2)
-                ok = mbar_wait(bars + 8 * (kKEmpty + stage), ((fill >> 1) - 1) & 1, kWaitNs);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                store_f16(base_s + kOffK + stage * kOperand, i * 16 + row0, c, x[i]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bars + 8 * (kKFull + stage));
-                if (tid == 0)
-                    mbar_arrive(bars + 8 * (kRec + (fill & 3)));
-            }
-            if (fill >= 2)
-                ok = ok && mbar_wait(bars + 8 * (kVEmpty + stage), ((fill >> 1) - 1) & 1, kWaitNs);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (has_nan(y[i])) {
-                    y[i] = take_nan(y[i], tok0 + i * 16 + row0, c, first);
-                    *any = 1;
-                }
-                store_f16(base_s + kOffV + stage * kOperand, i * 16 + row0, c, y[i]);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(bars + 8 * (kVFull + stage));
+                *any = 0;
+            named_barrier_sync(2, kConvertThreads);
         }
+        if (tid == 0)
+            *reinterpret_cast<float4 *>(base + kOffRec + (fill & 3) * 16) =
+                make_float4(st.rec[0], st.rec[1], st.rec[0] < 0.f ? 0.f : log2f(st.rec[2]), st.rec[1] < 0.f ? 0.f : log2f(st.rec[3]));
+        if (fill >= 2)
+            ok = ok && mbar_wait(bars + 8 * (kKEmpty + stage), ((fill >> 1) - 1) & 1, kWaitNs);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+            store_f16(base_s + kOffK + stage * kOperand, i * (kKv / kPieces) + row0, c, x[i]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(bars + 8 * (kKFull + stage));
+            if (tid == 0)
+                mbar_arrive(bars + 8 * (kRec + (fill & 3)));
+        }
+        more = st.next(p, tid);
+        if (more)
+            st.load(x, 0, tid);
+        if (fill >= 2)
+            ok = ok && mbar_wait(bars + 8 * (kVEmpty + stage), ((fill >> 1) - 1) & 1, kWaitNs);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int row = i * (kKv / kPieces) + row0;
+            if (has_nan(y[i])) {
+                y[i] = take_nan(y[i], tok0 + row, c, first);
+                *any = 1;
+            }
+            store_f16(base_s + kOffV + stage * kOperand, row, c, y[i]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(bars + 8 * (kVFull + stage));
+        ++fill;
     }
     if (!ok)
         report(p.status, SPARSE_ERR_TIMEOUT);
@@ -553,11 +606,11 @@ __device__ __forceinline__ void mma_loop(const ChunkParams &p, uint8_t *base, ui
                     if (!ok)
                         break;
                     tc_fence_after();
-                    const uint32_t v_s = base_s + kOffV + vs * kOperand;
+                    const uint32_t v_lo = desc_lo(base_s + kOffV + vs * kOperand, kSub);
 #pragma unroll
                     for (int i = 0; i < kKv / 16; ++i)   // 16 tokens a product: two groups of eight rows
-                        tc_mma_ts(tmem + kColO + t * 128, tmem + kColS + t * 128 + i * 8, tc_sdesc(v_s + i * 2048, kSub, 1024), idO,
-                                  j - 1 > it.j0 || i > 0);
+                        mma_ts(tmem + kColO + t * 128, tmem + kColS + t * 128 + i * 8, v_lo + i * (2048 >> 4), idO,
+                               j - 1 > it.j0 || i > 0);
                     if (j == end[t])
                         tc_commit(bars + 8 * (kOFull + t));
                 }
@@ -568,11 +621,11 @@ __device__ __forceinline__ void mma_loop(const ChunkParams &p, uint8_t *base, ui
                     if (!ok)
                         break;
                     tc_fence_after();
-                    const uint32_t q_s = base_s + kOffQ + t * kOperand, k_s = base_s + kOffK + ks * kOperand;
+                    const uint32_t q_lo = desc_lo(base_s + kOffQ + t * kOperand, 16), k_lo = desc_lo(base_s + kOffK + ks * kOperand, 16);
 #pragma unroll
                     for (int i = 0; i < kD / 16; ++i)   // 16 dims a product; the last four in the second half
-                        tc_mma(tmem + kColS + t * 128, tc_sdesc(q_s + (i >> 2) * kSub + (i & 3) * 32, 16, 1024),
-                               tc_sdesc(k_s + (i >> 2) * kSub + (i & 3) * 32, 16, 1024), idS, i > 0);
+                        mma_ss(tmem + kColS + t * 128, q_lo + (((i >> 2) * kSub + (i & 3) * 32) >> 4),
+                               k_lo + (((i >> 2) * kSub + (i & 3) * 32) >> 4), idS, i > 0);
                     tc_commit(bars + 8 * (kSFull + t));
                 }
             }
@@ -675,6 +728,132 @@ __device__ __forceinline__ float lse_of(float m, float l)
     return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309417f;
 }
 
+// Two fp32 values an instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ float2 unpair(uint64_t x)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// The largest score of a row among 64 columns (one page), of those up to `lim`.  NaN is passed over.
+template <bool MASKED>
+__device__ __forceinline__ float row_max(uint32_t s_t, int lim)
+{
+    uint32_t a[32], b[32];
+    tc_ld32(s_t, a);
+    tc_ld32(s_t + 32, b);
+    tc_wait_ld(a);
+    tc_wait_ld(b);
+    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const float x = !MASKED || i <= lim ? __uint_as_float(a[i]) : -INFINITY;
+        const float y = !MASKED || i + 32 <= lim ? __uint_as_float(b[i]) : -INFINITY;
+        m[i & 3] = max3(m[i & 3], x, y);
+    }
+    return fmaxf(max3(m[0], m[1], m[2]), m[3]);
+}
+
+// The weights 2^(s sc + off) of 64 columns to tensor memory, in f16, and their sum (FAR: the sum of 2^(s sc -
+// m), where the two are too far apart for one to be had from the other).
+template <bool MASKED, bool FAR>
+__device__ __forceinline__ float row_weights(uint32_t s_t, uint32_t p_t, float sc, float off, float m, int lim)
+{
+    uint32_t a[32], b[32], w[32];
+    tc_ld32(s_t, a);
+    tc_ld32(s_t + 32, b);
+    tc_wait_ld(a);
+    tc_wait_ld(b);
+    const uint64_t sc2 = pair(sc, sc), off2 = pair(off, off);
+    uint64_t sum[2] = {0ull, 0ull};
+    float far = 0.f;
+    auto half = [&](uint32_t(&x)[32], int first) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float2 v = make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+            float2 e = unpair(fma2(pair(v.x, v.y), sc2, off2));
+            e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+            if (MASKED)
+                e = make_float2(first + 2 * i <= lim ? e.x : 0.f, first + 2 * i + 1 <= lim ? e.y : 0.f);
+            if (FAR) {
+                far += first + 2 * i <= lim ? ex2_approx(fmaf(v.x, sc, -m)) : 0.f;
+                far += first + 2 * i + 1 <= lim ? ex2_approx(fmaf(v.y, sc, -m)) : 0.f;
+            } else {
+                sum[i & 1] = add2(sum[i & 1], pair(e.x, e.y));
+            }
+            w[first / 2 + i] = pack_f16x2(e.x, e.y);
+        }
+    };
+    half(a, 0);
+    half(b, 32);
+    tc_st32(p_t, w);
+    if (FAR)
+        return far;
+    const float2 t = unpair(add2(sum[0], sum[1]));
+    return t.x + t.y;
+}
+
+// The steps of the two loops over pages that only some rows or steps need, out of the others' way (the
+// loop over the steps has to fit the instruction caches).
+__device__ __noinline__ float row_max_masked(uint32_t s_t, int lim)
+{
+    return row_max<true>(s_t, lim);
+}
+
+__device__ __noinline__ float row_weights_masked(uint32_t s_t, uint32_t p_t, float sc, float off, int lim)
+{
+    return row_weights<true, false>(s_t, p_t, sc, off, 0.f, lim);
+}
+
+__device__ __noinline__ float row_weights_far(uint32_t s_t, uint32_t p_t, float sc, float off, float m, int lim)
+{
+    return row_weights<true, true>(s_t, p_t, sc, off, m, lim);
+}
+
+// O of a row times alpha.
+__device__ __noinline__ void row_rescale(uint32_t o_t, float alpha)
+{
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+        uint32_t o[32];
+        tc_ld32(o_t + 32 * k, o);
+        tc_wait_ld(o);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+        tc_st32(o_t + 32 * k, o);
+    }
+}
+
 // One tile's softmax: a thread a row.
 __device__ __forceinline__ void softmax_loop(const ChunkParams &p, uint8_t *base, uint32_t base_s, uint32_t tmem, int t, int tid)
 {
@@ -687,7 +866,7 @@ __device__ __forceinline__ void softmax_loop(const ChunkParams &p, uint8_t *base
     walk.open(p, reinterpret_cast<const Start *>(base + kOffStart), reinterpret_cast<const uint16_t *>(base + kOffLive));
     const float *qs = reinterpret_cast<const float *>(base + kOffQs) + t * kTileRows;
     uint32_t ns = 0, no = 0;
-    int fill = 0, items = 0;
+    int fill = 0, items = 1;
     int4 tail = make_int4(-1, 0, 0, 0);
     int head = 0;
     Item it;
@@ -728,22 +907,13 @@ __device__ __forceinline__ void softmax_loop(const ChunkParams &p, uint8_t *base
             const float4 rec = *reinterpret_cast<const float4 *>(base + kOffRec + (f & 3) * 16);
             const int see = pos - j * kKv;   // columns up to this one
             const bool masked = j * kKv + kKv - 1 > first_pos || rec.x < 0.f || rec.y < 0.f;
-            float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint32_t s[32];
-                tc_ld32(s_t + 32 * k, s);
-                tc_wait_ld(s);
-                if (masked) {
-                    const int lim = (k < 2 ? rec.x : rec.y) < 0.f ? -1 : see - 32 * k;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        top[k >> 1] = fmaxf(top[k >> 1], i <= lim ? __uint_as_float(s[i]) : -INFINITY);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        top[k >> 1] = fmaxf(top[k >> 1], __uint_as_float(s[i]));
-                }
+            float top[2];
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                const float x = masked ? row_max_masked(s_t + 64 * h, (h ? rec.y : rec.x) < 0.f ? -1 : see - 64 * h)
+                                       : row_max<false>(s_t + 64 * h, 63);
+                top[0] = h ? top[0] : x;
+                top[1] = x;
             }
             const float sc[2] = {q_scale * fmaxf(rec.x, 0.f), q_scale * fmaxf(rec.y, 0.f)};
             const float lv[2] = {rec.z, rec.w};
@@ -763,16 +933,7 @@ __device__ __forceinline__ void softmax_loop(const ChunkParams &p, uint8_t *base
             mo = grow ? t_o : mo;
             if (j > it.j0 && __any_sync(0xffffffffu, grow)) {
                 // O holds every step up to the one before: its products were issued before these scores'
-#pragma unroll 1
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t o[32];
-                    tc_ld32(o_t + 32 * k, o);
-                    tc_wait_ld(o);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                    tc_st32(o_t + 32 * k, o);
-                }
+                row_rescale(o_t, alpha);
             }
             __syncwarp();
             const float m_ref = m == -INFINITY ? 0.f : m;
@@ -780,48 +941,23 @@ __device__ __forceinline__ void softmax_loop(const ChunkParams &p, uint8_t *base
             bool far = false;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                lf[i] = mo == -INFINITY ? -INFINITY : lv[i] + (m_ref - mo);
+                // as long as no page counts for O its weights are in any units: they are scaled away with mo
+                lf[i] = mo == -INFINITY ? 0.f : lv[i] + (m_ref - mo);
                 far = far || !(fabsf(lf[i]) <= kFarWeight);
             }
             far = __any_sync(0xffffffffu, far);
-            float sum[2] = {0.f, 0.f};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int h = k >> 1;
-                const float off = lf[h] - m_ref;
-                uint32_t s[32], w[16];
-                tc_ld32(s_t + 32 * k, s);
-                tc_wait_ld(s);
-                const int lim = !masked ? 31 : (k < 2 ? rec.x : rec.y) < 0.f ? -1 : see - 32 * k;
-                if (far) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float x = __uint_as_float(s[i]);
-                        const float e = i <= lim ? ex2_approx(fmaf(x, sc[h], off)) : 0.f;
-                        sum[h] += i <= lim ? ex2_approx(fmaf(x, sc[h], -m_ref)) : 0.f;
-                        s[i] = __float_as_uint(e);
-                    }
-                } else if (masked) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float e = i <= lim ? ex2_approx(fmaf(__uint_as_float(s[i]), sc[h], off)) : 0.f;
-                        sum[h] += e;
-                        s[i] = __float_as_uint(e);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float e = ex2_approx(fmaf(__uint_as_float(s[i]), sc[h], off));
-                        sum[h] += e;
-                        s[i] = __float_as_uint(e);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    w[i] = pack_f16x2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
-                tc_st16u(s_t + 16 * k, w);
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t s_h = s_t + 64 * h, p_h = s_t + 32 * h;
+                const float sc_h = h ? sc[1] : sc[0], lf_h = h ? lf[1] : lf[0], off = lf_h - m_ref;
+                const int lim = !masked ? 63 : (h ? rec.y : rec.x) < 0.f ? -1 : see - 64 * h;
+                if (far)
+                    l += row_weights_far(s_h, p_h, sc_h, off, m_ref, lim);
+                else if (masked)
+                    l += row_weights_masked(s_h, p_h, sc_h, off, lim) * ex2_approx(-lf_h);
+                else
+                    l += row_weights<false, false>(s_h, p_h, sc_h, off, 0.f, 63) * ex2_approx(-lf_h);
             }
-            l += far ? sum[0] + sum[1] : sum[0] * ex2_approx(-lf[0]) + sum[1] * ex2_approx(-lf[1]);
             tc_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -914,9 +1050,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     int *ctrl = reinterpret_cast<int *>(base + kOffCtrl);
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bars + 8 * (kKFull + i), 4);
+            mbar_init(bars + 8 * (kKFull + i), kConvertWarps);
             mbar_init(bars + 8 * (kKEmpty + i), 1);
-            mbar_init(bars + 8 * (kVFull + i), 4);
+            mbar_init(bars + 8 * (kVFull + i), kConvertWarps);
             mbar_init(bars + 8 * (kVEmpty + i), 1);
         }
         for (int t = 0; t < kTiles; ++t) {
@@ -940,12 +1076,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     find_start(p, base, tid);   // ends with a barrier
     tc_fence_after();
     const uint32_t tmem = static_cast<uint32_t>(ctrl[0]);
-    if (warp < kSoftmaxWarps)
+    if (warp < kSoftmaxWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         softmax_loop(p, base, base_s, tmem, warp >> 2, tid & 127);
-    else if (warp < kMmaWarp)
-        convert_loop(p, base, base_s, tid & 127);
-    else if ((tid & 31) == 0)
-        mma_loop(p, base, base_s, tmem);
+    } else if (warp < kMmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvertRegs));
+        convert_loop(p, base, base_s, tid - kConvertWarp * 32);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+        if (tid == kMmaWarp * 32)
+            mma_loop(p, base, base_s, tmem);
+    }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -1063,6 +1204,17 @@ extern "C" SPARSE_API int sparse_paged_chunk_attn_f8(const uint16_t *Q, long lon
     rc = sp_host::configure_kernel(kern, kSmem, dev.device, configured);
     if (rc != SPARSE_OK)
         return rc;
+    // a split of more registers than the block is launched with would wait for ever
+    static int regs[64];
+    if (regs[dev.device] == 0) {
+        cudaFuncAttributes attr;
+        rc = sp_host::cuda_status(cudaFuncGetAttributes(&attr, kern), name);
+        if (rc != SPARSE_OK)
+            return rc;
+        regs[dev.device] = attr.numRegs;
+    }
+    if (regs[dev.device] < kRegs)
+        return fail(SPARSE_ERR_UNSUPPORTED, "%s: built with %d registers a thread, %d expected", name, regs[dev.device], kRegs);
     const int ctas = dev.sm_count;
     float *parts = static_cast<float *>(workspace);
     int4 *tails = reinterpret_cast<int4 *>(parts + 2ull * ctas * kPartFloats);
