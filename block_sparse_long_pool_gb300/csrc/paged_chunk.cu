@@ -26,9 +26,9 @@ constexpr int kConvertWarps = 8;
 constexpr int kConvertThreads = 32 * kConvertWarps;
 constexpr int kPieces = kKv * kD / 16 / kConvertThreads;   // 16-byte pieces of a step's keys a thread
 constexpr int kMmaWarp = kConvertWarp + kConvertWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 4);     // three warps are there for the registers' sake alone
+constexpr int kThreads = 32 * (kMmaWarp + 4);     // the MMA warp, the one that looks up pages, and two for the registers' sake
 // Registers a thread of the five warpgroups; the block is launched with kRegs a thread.
-constexpr int kRegs = 96, kSoftmaxRegs = 144, kConvertRegs = 72, kMmaRegs = 48;
+constexpr int kRegs = 96, kSoftmaxRegs = 144, kConvertRegs = 64, kMmaRegs = 64;
 static_assert(kTiles * kSoftmaxRegs + 2 * kConvertRegs + kMmaRegs <= 5 * kRegs, "the split is what the block has");
 constexpr int kSub = kKv * 128;                   // 64 of 128 dims of 128 f16 rows, 128 bytes a row: 16 KB
 constexpr int kOperand = 2 * kSub;                // 128 x 128 f16
@@ -46,13 +46,16 @@ enum {
     kSFull = 10,     // [tiles] scores of a step
     kPFull = 12,     // [tiles] its weights
     kOFull = 14,     // [tiles] every product of an item
-    kRec = 16,       // [4] scales of a step
-    kDone = 20,      // [tiles][2] an item that the tile has steps of is finished; items in turn
-    kDrain = 24,
-    kNumBars = 25
+    kPages = 16,     // [2] a group of steps' pages are known
+    kScales = 18,    // [2] and their scales
+    kUsed = 20,      // [2] a group of steps is done
+    kDone = 22,      // [tiles][2] an item that the tile has steps of is finished; items in turn
+    kReset = 26,     // an item's words for NaN are reset
+    kDrain = 27,
+    kNumBars = 28
 };
-constexpr int kOffRec = kOffBars + 256;           // float4 [4]: ks, ks, log2 vs, log2 vs (ks < 0: no page)
-constexpr int kOffCtrl = kOffRec + 64;            // int [16]
+constexpr int kOffRec = kOffBars + 256;           // Step [2][kGroup]
+constexpr int kOffCtrl = kOffRec + 2 * 16 * 32;   // int [16]
 constexpr int kOffStart = kOffCtrl + 64;          // Start
 constexpr int kOffQs = kOffStart + 64;            // float [tiles][128]
 constexpr int kOffNan = kOffQs + kTiles * kTileRows * 4;   // int [2][128], then int [2]
@@ -63,6 +66,25 @@ static_assert(kNumBars * 8 <= 256 && kOffRec % 16 == 0 && kOffStart % 8 == 0 && 
 static_assert(kSmem <= 232448, "shared memory of a CTA");
 
 constexpr int kColS = 0, kColO = kTiles * 128;    // tensor memory: scores (weights in their place), outputs
+
+// What the warps need to know of a step, sixteen written at a time.
+constexpr int kGroup = 16;
+struct Step {
+    int page[2];       // page * H_kv + head, -1: none
+    int flags;
+    int tok;           // the first token
+    float ks[2];       // key scales, -1: no page
+    float log2_vs[2];
+};
+static_assert(sizeof(Step) == 32 && kOffCtrl == kOffRec + 2 * kGroup * 32, "two 16-byte loads");
+enum {
+    kActive = 1,       // << tile: the tile has rows that see a token of the step
+    kLast = 4,         // << tile: its last step of the item
+    kBegins = 16,      // the first step of an item
+    kOdd = 32,         // of an item with an odd number
+    kEnd = 64,         // no step: the end
+    kRowsShift = 8     // tokens of the step that a row sees; those past them are zero
+};
 
 // A CTA's first item: where in the list of items it lies.
 struct Start {
@@ -428,69 +450,116 @@ __device__ __forceinline__ bool has_nan(uint4 x)
     return ((f(x.x) | f(x.y) | f(x.z) | f(x.w)) & 0x80808080u) != 0u;
 }
 
-// The converters' steps, one after another across items.
-struct Steps {
+// One warp: the steps, one after another across items, with their pages and scales, two lanes a step.
+__device__ __forceinline__ void page_loop(const ChunkParams &p, uint8_t *base, uint32_t base_s, int lane)
+{
+    const uint32_t bars = base_s + kOffBars;
     Walk walk;
+    walk.open(p, reinterpret_cast<const Start *>(base + kOffStart), reinterpret_cast<const uint16_t *>(base + kOffLive));
     Item it;
-    int j, items;
-    bool begins;             // the first step of an item
-    const uint8_t *src[2];   // the keys of its two pages, this thread's piece of the first row
-    int rows;                // tokens of the step that some row sees; those past it are zero
-    float rec[4];            // thread 0: scales
+    int j = 0, items = 0;
+    it.j1 = 0;
+    bool more = true, ok = true, bad = false;
+    for (uint32_t group = 0; more; ++group) {
+        const int half = group & 1;
+        if (group >= 2)
+            ok = ok && mbar_wait(bars + 8 * (kUsed + half), ((group >> 1) - 1) & 1, kWaitNs);
+        if (!__all_sync(0xffffffffu, ok))
+            break;
+        int flags = kEnd, tok = 0, at = -1, head = 0;
+        const int *entry = nullptr;
+        for (int s = 0; s < kGroup && more; ++s) {
+            int f = 0;
+            if (j >= it.j1) {
+                do
+                    more = walk.next(p, it);
+                while (more && it.all == 0);
+                if (!more)
+                    break;
+                j = it.j0;
+                ++items;
+                f = kBegins;
+            }
+            if (lane >> 1 == s) {
+                const long long cap = static_cast<long long>(p.max_blocks) * kBlk;
+                const int end = static_cast<int>(min(static_cast<long long>(it.pos) + it.n, cap));
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) {
+                    const int last = min(it.j1, it.steps[t]) - 1;
+                    f |= j <= last ? kActive << t : 0;
+                    f |= j == last ? kLast << t : 0;
+                }
+                flags = f | (items & 1 ? kOdd : 0) | min(kKv, end - j * kKv) << kRowsShift;
+                tok = j * kKv;
+                head = it.head;
+                if (tok + (lane & 1) * kBlk < end)
+                    entry = p.block_table + static_cast<size_t>(it.b) * p.max_blocks + 2 * j + (lane & 1);
+            }
+            ++j;
+        }
+        if (entry != nullptr) {
+            const int page = *entry;
+            if (page >= 0 && page < p.n_pages)
+                at = page * p.H_kv + head;
+            else
+                bad = true;
+        }
+        Step *step = reinterpret_cast<Step *>(base + kOffRec) + half * kGroup + (lane >> 1);
+        step->page[lane & 1] = at;
+        if ((lane & 1) == 0) {
+            step->flags = flags;
+            step->tok = tok;
+        }
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(bars + 8 * (kPages + half));
+        float2 scale = make_float2(-1.f, 1.f);
+        if (at >= 0)
+            scale = reinterpret_cast<const float2 *>(p.kv_scale)[at];
+        step->ks[lane & 1] = scale.x;
+        step->log2_vs[lane & 1] = log2f(scale.y);
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(bars + 8 * (kScales + half));
+        // a full last group: the end is in the next one
+        if (!more && __shfl_sync(0xffffffffu, flags, 31) != kEnd)
+            more = true;
+    }
+    if (bad)
+        report(p.status, SPARSE_ERR_BAD_INDEX);
+    if (!ok)
+        report(p.status, SPARSE_ERR_TIMEOUT);
+}
 
-    __device__ __forceinline__ void open(const ChunkParams &p, uint8_t *base)
-    {
-        walk.open(p, reinterpret_cast<const Start *>(base + kOffStart), reinterpret_cast<const uint16_t *>(base + kOffLive));
-        j = it.j1 = items = 0;
-    }
-    __device__ __forceinline__ bool next(const ChunkParams &p, int tid)
-    {
-        begins = ++j >= it.j1;
-        if (begins) {
-            do {
-                if (!walk.next(p, it))
-                    return false;
-            } while (it.all == 0);
-            j = it.j0;
-            ++items;
-        }
-        const int end = static_cast<int>(min(static_cast<long long>(it.pos) + it.n, static_cast<long long>(p.max_blocks) * kBlk));
-        rows = min(kKv, end - j * kKv);
+__device__ __forceinline__ const Step *step_of(const uint8_t *base, int f)
+{
+    return reinterpret_cast<const Step *>(base + kOffRec) + (f & (2 * kGroup - 1));
+}
+
+// A thread that is to read step f, in turn: waits where a group begins.
+__device__ __forceinline__ bool wait_step(uint32_t bars, int which, int f)
+{
+    return (f & (kGroup - 1)) != 0 || mbar_wait(bars + 8 * (which + ((f / kGroup) & 1)), (f / (2 * kGroup)) & 1, kWaitNs);
+}
+
+// Pieces i * threads + tid of a step's keys (values: v = 1), eight a row.  They pass by L1, which is small
+// beside this much shared memory.
+__device__ __forceinline__ void load_pieces(const ChunkParams &p, const Step *step, int v, int tid, uint4 (&x)[kPieces])
+{
+    constexpr int kRowsOf = kKv / kPieces, kHalf = kPieces / 2;
+    const int rows = step->flags >> kRowsShift;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            bool there = i * kBlk < rows;
-            int page = there ? p.block_table[static_cast<size_t>(it.b) * p.max_blocks + 2 * j + i] : 0;
-            if (there && (page < 0 || page >= p.n_pages)) {
-                there = false;
-                page = 0;
-                if (tid == 0)
-                    report(p.status, SPARSE_ERR_BAD_INDEX);
-            }
-            const size_t at = static_cast<size_t>(page) * p.H_kv + it.head;
-            src[i] = there ? p.kv_pages + at * (2 * kBlk * kD) + tid * 16 : nullptr;
-            rec[i] = -1.f;
-            rec[2 + i] = 0.f;
-            if (tid == 0 && there) {
-                const float2 s = *reinterpret_cast<const float2 *>(p.kv_scale + at * 2);
-                rec[i] = s.x;
-                rec[2 + i] = s.y;   // its logarithm is taken when it is handed on
-            }
-        }
-        return true;
-    }
-    // Pieces i * threads + tid of the step's keys (values: v = 1), eight a row.
-    __device__ __forceinline__ void load(uint4 (&x)[kPieces], int v, int tid) const
-    {
-        constexpr int kRowsOf = kKv / kPieces, kHalf = kPieces / 2;
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            const uint8_t *s = src[i / kHalf];
-            x[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (s != nullptr && i * kRowsOf + (tid >> 3) < rows)
-                x[i] = *reinterpret_cast<const uint4 *>(s + v * (kBlk * kD) + (i % kHalf) * (kRowsOf * kD));
+    for (int i = 0; i < kPieces; ++i) {
+        const int at = step->page[i / kHalf];
+        x[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (at >= 0 && i * kRowsOf + (tid >> 3) < rows) {
+            const uint8_t *src = p.kv_pages + static_cast<size_t>(at) * (2 * kBlk * kD) + v * (kBlk * kD) + (i % kHalf) * (kRowsOf * kD) + tid * 16;
+            asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(x[i].x), "=r"(x[i].y), "=r"(x[i].z), "=r"(x[i].w)
+                         : "l"(src));
         }
     }
-};
+}
 
 // The warps that convert.  A step's values are on their way while its keys are converted, and the next
 // step's keys while its values are.
@@ -498,62 +567,60 @@ __device__ __forceinline__ void convert_loop(const ChunkParams &p, uint8_t *base
 {
     const uint32_t bars = base_s + kOffBars;
     const int row0 = tid >> 3, c = tid & 7, lane = tid & 31;
-    int fill = 0;
     uint32_t used[kTiles][2] = {};   // items of either parity that a tile had steps of
-    bool ok = true;
-    Steps st;
-    st.open(p, base);
+    uint32_t n_items = 0;
+    bool ok = wait_step(bars, kPages, 0);
     uint4 x[kPieces], y[kPieces];
-    bool more = st.next(p, tid);
-    if (more)
-        st.load(x, 0, tid);
-    while (more) {   // a thread that gave up still meets the others
-        int *first = reinterpret_cast<int *>(base + kOffNan) + (st.items & 1) * kD;
-        int *any = reinterpret_cast<int *>(base + kOffNan) + 2 * kD + (st.items & 1);
-        const int tok0 = st.j * kKv, stage = fill & 1;
-        st.load(y, 1, tid);
-        if (st.begins) {
+    const Step *step = step_of(base, 0);
+    int flags = ok ? step->flags : kEnd;
+    if (!(flags & kEnd))
+        load_pieces(p, step, 0, tid, x);
+    for (int f = 0; !(flags & kEnd); ++f) {
+        const int stage = f & 1, odd = (flags & kOdd) != 0, tok = step->tok;
+        int *first = reinterpret_cast<int *>(base + kOffNan) + odd * kD;
+        int *any = reinterpret_cast<int *>(base + kOffNan) + 2 * kD + odd;
+        load_pieces(p, step, 1, tid, y);
+        if (flags & kBegins) {
             // the last item that used these words is finished: a tile without steps does not wait for anyone, and does
             // not count
 #pragma unroll
             for (int t = 0; t < kTiles; ++t) {
-                uint32_t &n = used[t][st.items & 1];
+                const uint32_t n = odd ? used[t][1] : used[t][0], add = (flags >> t) & kActive;
                 if (n > 0)
-                    ok = ok && mbar_wait(bars + 8 * (kDone + 2 * t + (st.items & 1)), (n - 1) & 1, kWaitNs);
-                if (min(st.it.j1, st.it.steps[t]) > st.it.j0)
-                    ++n;
+                    ok = ok && mbar_wait(bars + 8 * (kDone + 2 * t + odd), (n - 1) & 1, kWaitNs);
+                used[t][0] += odd ? 0 : add;
+                used[t][1] += odd ? add : 0;
             }
             if (tid < kD)
                 first[tid] = INT_MAX;
             if (tid == 0)
                 *any = 0;
-            named_barrier_sync(2, kConvertThreads);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bars + 8 * kReset);
+            ok = ok && mbar_wait(bars + 8 * kReset, n_items++ & 1, kWaitNs);
         }
-        if (tid == 0)
-            *reinterpret_cast<float4 *>(base + kOffRec + (fill & 3) * 16) =
-                make_float4(st.rec[0], st.rec[1], st.rec[0] < 0.f ? 0.f : log2f(st.rec[2]), st.rec[1] < 0.f ? 0.f : log2f(st.rec[3]));
-        if (fill >= 2)
-            ok = ok && mbar_wait(bars + 8 * (kKEmpty + stage), ((fill >> 1) - 1) & 1, kWaitNs);
+        if (f >= 2)
+            ok = ok && mbar_wait(bars + 8 * (kKEmpty + stage), ((f >> 1) - 1) & 1, kWaitNs);
 #pragma unroll
         for (int i = 0; i < kPieces; ++i)
             store_f16(base_s + kOffK + stage * kOperand, i * (kKv / kPieces) + row0, c, x[i]);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
+        if (lane == 0)
             mbar_arrive(bars + 8 * (kKFull + stage));
-            if (tid == 0)
-                mbar_arrive(bars + 8 * (kRec + (fill & 3)));
-        }
-        more = st.next(p, tid);
-        if (more)
-            st.load(x, 0, tid);
-        if (fill >= 2)
-            ok = ok && mbar_wait(bars + 8 * (kVEmpty + stage), ((fill >> 1) - 1) & 1, kWaitNs);
+        ok = wait_step(bars, kPages, f + 1) && ok;
+        step = step_of(base, f + 1);
+        flags = __shfl_sync(0xffffffffu, step->flags, 0);
+        if (!(flags & kEnd))
+            load_pieces(p, step, 0, tid, x);
+        if (f >= 2)
+            ok = ok && mbar_wait(bars + 8 * (kVEmpty + stage), ((f >> 1) - 1) & 1, kWaitNs);
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
             const int row = i * (kKv / kPieces) + row0;
             if (has_nan(y[i])) {
-                y[i] = take_nan(y[i], tok0 + row, c, first);
+                y[i] = take_nan(y[i], tok + row, c, first);
                 *any = 1;
             }
             store_f16(base_s + kOffV + stage * kOperand, row, c, y[i]);
@@ -562,7 +629,8 @@ __device__ __forceinline__ void convert_loop(const ChunkParams &p, uint8_t *base
         __syncwarp();
         if (lane == 0)
             mbar_arrive(bars + 8 * (kVFull + stage));
-        ++fill;
+        if (!__all_sync(0xffffffffu, ok))
+            break;
     }
     if (!ok)
         report(p.status, SPARSE_ERR_TIMEOUT);
@@ -570,74 +638,84 @@ __device__ __forceinline__ void convert_loop(const ChunkParams &p, uint8_t *base
 
 // ---------------------------------------------------------------- products
 
-// One thread: S = Q K^T of a step, then O += P V of the step before, tile by tile in turn: while
-// one tile's softmax runs, the other's products do.
-__device__ __forceinline__ void mma_loop(const ChunkParams &p, uint8_t *base, uint32_t base_s, uint32_t tmem)
+// O += P V of a step and a tile.
+__device__ __forceinline__ void issue_pv(uint32_t base_s, uint32_t tmem, int t, int stage, bool first)
+{
+    constexpr uint32_t id = idesc_f16(kTileRows, kD, 0, 1);   // weights; values as they are stored (dims contiguous)
+    const uint32_t v_lo = desc_lo(base_s + kOffV + stage * kOperand, kSub);
+#pragma unroll
+    for (int i = 0; i < kKv / 16; ++i)   // 16 tokens a product: two groups of eight rows
+        mma_ts(tmem + kColO + t * 128, tmem + kColS + t * 128 + i * 8, v_lo + i * (2048 >> 4), id, !first || i > 0);
+}
+
+// S = Q K^T.
+__device__ __forceinline__ void issue_qk(uint32_t base_s, uint32_t tmem, int t, int stage)
+{
+    constexpr uint32_t id = idesc_f16(kTileRows, kKv, 0, 0);   // K-major queries and keys
+    const uint32_t q_lo = desc_lo(base_s + kOffQ + t * kOperand, 16), k_lo = desc_lo(base_s + kOffK + stage * kOperand, 16);
+#pragma unroll
+    for (int i = 0; i < kD / 16; ++i)   // 16 dims a product; the last four in the second half
+        mma_ss(tmem + kColS + t * 128, q_lo + (((i >> 2) * kSub + (i & 3) * 32) >> 4),
+               k_lo + (((i >> 2) * kSub + (i & 3) * 32) >> 4), id, i > 0);
+}
+
+// One thread: a step's scores and the products of the step before with its weights, tile by tile in
+// turn: while one tile's softmax runs, the other's products do.
+__device__ __forceinline__ void mma_loop(uint8_t *base, uint32_t base_s, uint32_t tmem, int *status)
 {
     const uint32_t bars = base_s + kOffBars;
-    constexpr uint32_t idS = idesc_f16(kTileRows, kKv, 0, 0);   // K-major queries and keys
-    constexpr uint32_t idO = idesc_f16(kTileRows, kD, 0, 1);    // weights; values as they are stored (dims contiguous)
-    Walk walk;
-    walk.open(p, reinterpret_cast<const Start *>(base + kOffStart), reinterpret_cast<const uint16_t *>(base + kOffLive));
-    uint32_t nq[kTiles] = {}, np[kTiles] = {};
-    int fill = 0;
-    Item it;
+    uint32_t np[kTiles] = {}, q_phase[kTiles] = {};
+    int before = 0;   // the flags of the step before
     bool ok = true;
-    while (ok && walk.next(p, it)) {
-        if (it.all == 0)
-            continue;
-        int end[kTiles];
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-            end[t] = min(it.j1, it.steps[t]);
-            if (end[t] > it.j0)
-                ok = ok && mbar_wait(bars + 8 * (kQFull + t), nq[t]++ & 1, kWaitNs);
-        }
-        for (int j = it.j0; j <= it.j1 && ok; ++j) {
-            const int f = fill + j - it.j0, ks = f & 1, vs = (f - 1) & 1;
-            bool k_there = false, v_there = false;
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-                if (j > it.j0 && j - 1 < end[t]) {
-                    if (!v_there)
-                        ok = ok && mbar_wait(bars + 8 * (kVFull + vs), ((f - 1) >> 1) & 1, kWaitNs);
-                    v_there = true;
-                    ok = ok && mbar_wait(bars + 8 * (kPFull + t), np[t]++ & 1, kWaitNs);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-                    const uint32_t v_lo = desc_lo(base_s + kOffV + vs * kOperand, kSub);
-#pragma unroll
-                    for (int i = 0; i < kKv / 16; ++i)   // 16 tokens a product: two groups of eight rows
-                        mma_ts(tmem + kColO + t * 128, tmem + kColS + t * 128 + i * 8, v_lo + i * (2048 >> 4), idO,
-                               j - 1 > it.j0 || i > 0);
-                    if (j == end[t])
-                        tc_commit(bars + 8 * (kOFull + t));
-                }
-                if (j < end[t]) {
-                    if (!k_there)
-                        ok = ok && mbar_wait(bars + 8 * (kKFull + ks), (f >> 1) & 1, kWaitNs);
-                    k_there = true;
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-                    const uint32_t q_lo = desc_lo(base_s + kOffQ + t * kOperand, 16), k_lo = desc_lo(base_s + kOffK + ks * kOperand, 16);
-#pragma unroll
-                    for (int i = 0; i < kD / 16; ++i)   // 16 dims a product; the last four in the second half
-                        mma_ss(tmem + kColS + t * 128, q_lo + (((i >> 2) * kSub + (i & 3) * 32) >> 4),
-                               k_lo + (((i >> 2) * kSub + (i & 3) * 32) >> 4), idS, i > 0);
-                    tc_commit(bars + 8 * (kSFull + t));
-                }
+    for (int f = 0; ok; ++f) {
+        ok = wait_step(bars, kPages, f);
+        if (!ok)
+            break;
+        const int flags = step_of(base, f)->flags, ks = f & 1, vs = ks ^ 1;
+        bool k_there = false, v_there = false;
+        // at the start of an item its queries are waited for after the products of the last one
+        const bool begins = (flags & kBegins) != 0;
+#pragma unroll 1
+        for (int u = 0; u < 2 * kTiles; ++u) {
+            const int t = begins ? u % kTiles : u / 2;
+            const bool pv = begins ? u < kTiles : u % 2 == 0;
+            if (pv && (before >> t & kActive)) {
+                if (!v_there)
+                    ok = ok && mbar_wait(bars + 8 * (kVFull + vs), ((f - 1) >> 1) & 1, kWaitNs);
+                v_there = true;
+                ok = ok && mbar_wait(bars + 8 * (kPFull + t), (t ? np[1]++ : np[0]++) & 1, kWaitNs);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                issue_pv(base_s, tmem, t, vs, (before & kBegins) != 0);
+                if (before & kLast << t)
+                    tc_commit(bars + 8 * (kOFull + t));
+            } else if (!pv && (flags >> t & kActive)) {
+                if (begins)
+                    ok = ok && mbar_wait(bars + 8 * (kQFull + t), (t ? q_phase[1]++ : q_phase[0]++) & 1, kWaitNs);
+                if (!k_there)
+                    ok = ok && mbar_wait(bars + 8 * (kKFull + ks), (f >> 1) & 1, kWaitNs);
+                k_there = true;
+                if (!ok)
+                    break;
+                tc_fence_after();
+                issue_qk(base_s, tmem, t, ks);
+                tc_commit(bars + 8 * (kSFull + t));
             }
-            if (v_there)
-                tc_commit(bars + 8 * (kVEmpty + vs));
-            if (k_there)
-                tc_commit(bars + 8 * (kKEmpty + ks));
         }
-        fill += it.j1 - it.j0;
+        if (v_there)
+            tc_commit(bars + 8 * (kVEmpty + vs));
+        if (k_there)
+            tc_commit(bars + 8 * (kKEmpty + ks));
+        // the weights of every step of the group before are there: its scales have been read
+        if (f > 0 && f % kGroup == 0)
+            mbar_arrive(bars + 8 * (kUsed + ((f / kGroup - 1) & 1)));
+        before = flags;
+        if (flags & kEnd)
+            break;
     }
     if (!ok)
-        report(p.status, SPARSE_ERR_TIMEOUT);
+        report(status, SPARSE_ERR_TIMEOUT);
     // every product is done before the tensor memory is given back
     tc_commit(bars + 8 * kDrain);
     mbar_wait(bars + 8 * kDrain, 0, kWaitNs);
@@ -899,12 +977,14 @@ __device__ __forceinline__ void softmax_loop(const ChunkParams &p, uint8_t *base
         const float q_scale = qs[tid];   // written by this warp
         for (int j = it.j0; j < end && ok; ++j) {
             const int f = fill + j - it.j0;
-            ok = mbar_wait(bars + 8 * (kRec + (f & 3)), (f >> 2) & 1, kWaitNs);
-            ok = __all_sync(0xffffffffu, ok && mbar_wait(bars + 8 * (kSFull + t), ns++ & 1, kWaitNs));
+            // scales are known long before the scores; a group that the tile enters past its first step, too
+            ok = mbar_wait(bars + 8 * (kSFull + t), ns++ & 1, kWaitNs) &&
+                 mbar_wait(bars + 8 * (kScales + ((f / kGroup) & 1)), (f / (2 * kGroup)) & 1, kWaitNs);
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok)
                 break;
             tc_fence_after();
-            const float4 rec = *reinterpret_cast<const float4 *>(base + kOffRec + (f & 3) * 16);
+            const float4 rec = *reinterpret_cast<const float4 *>(step_of(base, f)->ks);
             const int see = pos - j * kKv;   // columns up to this one
             const bool masked = j * kKv + kKv - 1 > first_pos || rec.x < 0.f || rec.y < 0.f;
             float top[2];
@@ -1063,8 +1143,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             mbar_init(bars + 8 * (kDone + 2 * t), 4);
             mbar_init(bars + 8 * (kDone + 2 * t + 1), 4);
         }
-        for (int i = 0; i < 4; ++i)
-            mbar_init(bars + 8 * (kRec + i), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bars + 8 * (kPages + i), 1);
+            mbar_init(bars + 8 * (kScales + i), 1);
+            mbar_init(bars + 8 * (kUsed + i), 1);
+        }
+        mbar_init(bars + 8 * kReset, kConvertWarps);
         mbar_init(bars + 8 * kDrain, 1);
         fence_barrier_init();
     }
@@ -1085,7 +1169,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
         if (tid == kMmaWarp * 32)
-            mma_loop(p, base, base_s, tmem);
+            mma_loop(base, base_s, tmem, p.status);
+        else if (warp == kMmaWarp + 1)
+            page_loop(p, base, base_s, tid & 31);
     }
     __syncwarp();
     tc_fence_before();
@@ -1192,6 +1278,8 @@ extern "C" SPARSE_API int sparse_paged_chunk_attn_f8(const uint16_t *Q, long lon
     const double work = (static_cast<double>(n_tok) / (kTiles * per_tile) + B) * H_kv * (static_cast<double>(max_blocks) * kBlk + n_tok + kItemCost);
     if (work > 0x1p61)
         return fail(SPARSE_ERR_UNSUPPORTED, "%s: n_tok, max_blocks and H_kv are too large together", name);
+    if (static_cast<long long>(n_pages) * H_kv > INT_MAX)
+        return fail(SPARSE_ERR_UNSUPPORTED, "%s: n_pages * H_kv = %lld >= 2^31", name, static_cast<long long>(n_pages) * H_kv);
     const size_t need = sparse_paged_chunk_attn_f8_workspace_size(B, H_q, H_kv);
     if (workspace_bytes < need)
         return fail(SPARSE_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", name, workspace_bytes, need);
