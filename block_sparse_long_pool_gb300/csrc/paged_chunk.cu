@@ -22,14 +22,14 @@ constexpr int kMinCut = 2;                        // steps on either side of a c
 
 constexpr int kSoftmaxWarps = 4 * kTiles;
 constexpr int kConvertWarp = kSoftmaxWarps;       // the first of them
-constexpr int kConvertWarps = 8;
+constexpr int kConvertWarps = 4;
 constexpr int kConvertThreads = 32 * kConvertWarps;
 constexpr int kPieces = kKv * kD / 16 / kConvertThreads;   // 16-byte pieces of a step's keys a thread
 constexpr int kMmaWarp = kConvertWarp + kConvertWarps;
 constexpr int kThreads = 32 * (kMmaWarp + 4);     // the MMA warp, the one that looks up pages, and two for the registers' sake
-// Registers a thread of the five warpgroups; the block is launched with kRegs a thread.
-constexpr int kRegs = 96, kSoftmaxRegs = 144, kConvertRegs = 64, kMmaRegs = 64;
-static_assert(kTiles * kSoftmaxRegs + 2 * kConvertRegs + kMmaRegs <= 5 * kRegs, "the split is what the block has");
+// Registers a thread of the four warpgroups; the block is launched with kRegs a thread.
+constexpr int kRegs = 128, kSoftmaxRegs = 184, kConvertRegs = 96, kMmaRegs = 48;
+static_assert(kTiles * kSoftmaxRegs + kConvertRegs + kMmaRegs <= 4 * kRegs, "the split is what the block has");
 constexpr int kSub = kKv * 128;                   // 64 of 128 dims of 128 f16 rows, 128 bytes a row: 16 KB
 constexpr int kOperand = 2 * kSub;                // 128 x 128 f16
 
@@ -133,6 +133,15 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo)
     return ((addr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
 }
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);   // 8-row groups 1024 bytes apart, version 1, 128-byte swizzle
+
+// One lane of a converged warp: products are issued by one thread, and their operands are the warp's
+// uniform registers only where the whole warp comes by.
+__device__ __forceinline__ uint32_t elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
 
 // D (tensor memory) = A B (+ D), both in shared memory.
 __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate)
@@ -659,57 +668,70 @@ __device__ __forceinline__ void issue_qk(uint32_t base_s, uint32_t tmem, int t, 
                k_lo + (((i >> 2) * kSub + (i & 3) * 32) >> 4), id, i > 0);
 }
 
-// One thread: a step's scores and the products of the step before with its weights, tile by tile in
+// One warp: a step's scores and the products of the step before with its weights, tile by tile in
 // turn: while one tile's softmax runs, the other's products do.
 __device__ __forceinline__ void mma_loop(uint8_t *base, uint32_t base_s, uint32_t tmem, int *status)
 {
     const uint32_t bars = base_s + kOffBars;
-    uint32_t np[kTiles] = {}, q_phase[kTiles] = {};
+    uint32_t np[kTiles] = {}, nq[kTiles] = {};
     int before = 0;   // the flags of the step before
     bool ok = true;
     for (int f = 0; ok; ++f) {
-        ok = wait_step(bars, kPages, f);
-        if (!ok)
-            break;
-        const int flags = step_of(base, f)->flags, ks = f & 1, vs = ks ^ 1;
-        bool k_there = false, v_there = false;
+        ok = wait_step(bars, kPages, f) && wait_step(bars, kScales, f);   // the scales are read once the scores are there
+        const int flags = __shfl_sync(0xffffffffu, step_of(base, f)->flags, 0), ks = f & 1, vs = ks ^ 1;
         // at the start of an item its queries are waited for after the products of the last one
         const bool begins = (flags & kBegins) != 0;
-#pragma unroll 1
-        for (int u = 0; u < 2 * kTiles; ++u) {
-            const int t = begins ? u % kTiles : u / 2;
-            const bool pv = begins ? u < kTiles : u % 2 == 0;
-            if (pv && (before >> t & kActive)) {
-                if (!v_there)
-                    ok = ok && mbar_wait(bars + 8 * (kVFull + vs), ((f - 1) >> 1) & 1, kWaitNs);
-                v_there = true;
-                ok = ok && mbar_wait(bars + 8 * (kPFull + t), (t ? np[1]++ : np[0]++) & 1, kWaitNs);
-                if (!ok)
-                    break;
-                tc_fence_after();
+        if (before)
+            ok = ok && mbar_wait(bars + 8 * (kVFull + vs), ((f - 1) >> 1) & 1, kWaitNs);
+        auto pv = [&](int t) {
+            if (!(before >> t & kActive))
+                return;
+            ok = ok && mbar_wait(bars + 8 * (kPFull + t), np[t]++ & 1, kWaitNs);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok)
+                return;
+            tc_fence_after();
+            if (elect_one()) {
                 issue_pv(base_s, tmem, t, vs, (before & kBegins) != 0);
                 if (before & kLast << t)
                     tc_commit(bars + 8 * (kOFull + t));
-            } else if (!pv && (flags >> t & kActive)) {
-                if (begins)
-                    ok = ok && mbar_wait(bars + 8 * (kQFull + t), (t ? q_phase[1]++ : q_phase[0]++) & 1, kWaitNs);
-                if (!k_there)
-                    ok = ok && mbar_wait(bars + 8 * (kKFull + ks), (f >> 1) & 1, kWaitNs);
-                k_there = true;
-                if (!ok)
-                    break;
-                tc_fence_after();
+            }
+            __syncwarp();
+        };
+        auto qk = [&](int t) {
+            if (!(flags >> t & kActive))
+                return;
+            if (begins)
+                ok = ok && mbar_wait(bars + 8 * (kQFull + t), nq[t]++ & 1, kWaitNs);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok)
+                return;
+            tc_fence_after();
+            if (elect_one()) {
                 issue_qk(base_s, tmem, t, ks);
                 tc_commit(bars + 8 * (kSFull + t));
             }
+            __syncwarp();
+        };
+        pv(0);
+        if (begins)
+            pv(1);
+        if (!(flags & kEnd))
+            ok = ok && mbar_wait(bars + 8 * (kKFull + ks), (f >> 1) & 1, kWaitNs);
+        qk(0);
+        if (!begins)
+            pv(1);
+        qk(1);
+        if (elect_one()) {
+            if (before)
+                tc_commit(bars + 8 * (kVEmpty + vs));
+            if (!(flags & kEnd))
+                tc_commit(bars + 8 * (kKEmpty + ks));
+            // the weights of every step of the group before are there: its scales have been read
+            if (f > 0 && f % kGroup == 0)
+                mbar_arrive(bars + 8 * (kUsed + ((f / kGroup - 1) & 1)));
         }
-        if (v_there)
-            tc_commit(bars + 8 * (kVEmpty + vs));
-        if (k_there)
-            tc_commit(bars + 8 * (kKEmpty + ks));
-        // the weights of every step of the group before are there: its scales have been read
-        if (f > 0 && f % kGroup == 0)
-            mbar_arrive(bars + 8 * (kUsed + ((f / kGroup - 1) & 1)));
+        __syncwarp();
         before = flags;
         if (flags & kEnd)
             break;
@@ -717,7 +739,9 @@ __device__ __forceinline__ void mma_loop(uint8_t *base, uint32_t base_s, uint32_
     if (!ok)
         report(status, SPARSE_ERR_TIMEOUT);
     // every product is done before the tensor memory is given back
-    tc_commit(bars + 8 * kDrain);
+    __syncwarp();
+    if (elect_one())
+        tc_commit(bars + 8 * kDrain);
     mbar_wait(bars + 8 * kDrain, 0, kWaitNs);
 }
 
@@ -842,96 +866,21 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return r;
 }
 
-// The largest score of a row among 64 columns (one page), of those up to `lim`.  NaN is passed over.
-template <bool MASKED>
-__device__ __forceinline__ float row_max(uint32_t s_t, int lim)
-{
-    uint32_t a[32], b[32];
-    tc_ld32(s_t, a);
-    tc_ld32(s_t + 32, b);
-    tc_wait_ld(a);
-    tc_wait_ld(b);
-    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const float x = !MASKED || i <= lim ? __uint_as_float(a[i]) : -INFINITY;
-        const float y = !MASKED || i + 32 <= lim ? __uint_as_float(b[i]) : -INFINITY;
-        m[i & 3] = max3(m[i & 3], x, y);
-    }
-    return fmaxf(max3(m[0], m[1], m[2]), m[3]);
-}
-
-// The weights 2^(s sc + off) of 64 columns to tensor memory, in f16, and their sum (FAR: the sum of 2^(s sc -
-// m), where the two are too far apart for one to be had from the other).
-template <bool MASKED, bool FAR>
-__device__ __forceinline__ float row_weights(uint32_t s_t, uint32_t p_t, float sc, float off, float m, int lim)
-{
-    uint32_t a[32], b[32], w[32];
-    tc_ld32(s_t, a);
-    tc_ld32(s_t + 32, b);
-    tc_wait_ld(a);
-    tc_wait_ld(b);
-    const uint64_t sc2 = pair(sc, sc), off2 = pair(off, off);
-    uint64_t sum[2] = {0ull, 0ull};
-    float far = 0.f;
-    auto half = [&](uint32_t(&x)[32], int first) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float2 v = make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-            float2 e = unpair(fma2(pair(v.x, v.y), sc2, off2));
-            e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-            if (MASKED)
-                e = make_float2(first + 2 * i <= lim ? e.x : 0.f, first + 2 * i + 1 <= lim ? e.y : 0.f);
-            if (FAR) {
-                far += first + 2 * i <= lim ? ex2_approx(fmaf(v.x, sc, -m)) : 0.f;
-                far += first + 2 * i + 1 <= lim ? ex2_approx(fmaf(v.y, sc, -m)) : 0.f;
-            } else {
-                sum[i & 1] = add2(sum[i & 1], pair(e.x, e.y));
-            }
-            w[first / 2 + i] = pack_f16x2(e.x, e.y);
-        }
-    };
-    half(a, 0);
-    half(b, 32);
-    tc_st32(p_t, w);
-    if (FAR)
-        return far;
-    const float2 t = unpair(add2(sum[0], sum[1]));
-    return t.x + t.y;
-}
-
-// The steps of the two loops over pages that only some rows or steps need, out of the others' way (the
-// loop over the steps has to fit the instruction caches).
-__device__ __noinline__ float row_max_masked(uint32_t s_t, int lim)
-{
-    return row_max<true>(s_t, lim);
-}
-
-__device__ __noinline__ float row_weights_masked(uint32_t s_t, uint32_t p_t, float sc, float off, int lim)
-{
-    return row_weights<true, false>(s_t, p_t, sc, off, 0.f, lim);
-}
-
-__device__ __noinline__ float row_weights_far(uint32_t s_t, uint32_t p_t, float sc, float off, float m, int lim)
-{
-    return row_weights<true, true>(s_t, p_t, sc, off, m, lim);
-}
-
 // O of a row times alpha.
-__device__ __noinline__ void row_rescale(uint32_t o_t, float alpha)
+__device__ __forceinline__ void rescale(uint32_t o_t, float alpha)
 {
 #pragma unroll 1
-    for (int k = 0; k < 4; ++k) {
-        uint32_t o[32];
-        tc_ld32(o_t + 32 * k, o);
-        tc_wait_ld(o);
+    for (int k = 0; k < 8; ++k) {
+        float o[16];
+        tc_ld16(o_t + 16 * k, o);
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-        tc_st32(o_t + 32 * k, o);
+        for (int i = 0; i < 16; ++i)
+            o[i] *= alpha;
+        tc_st16(o_t + 16 * k, o);
     }
 }
 
+// One tile's softmax: a thread a row.
 // One tile's softmax: a thread a row.
 __device__ __forceinline__ void softmax_loop(const ChunkParams &p, uint8_t *base, uint32_t base_s, uint32_t tmem, int t, int tid)
 {
@@ -977,32 +926,42 @@ __device__ __forceinline__ void softmax_loop(const ChunkParams &p, uint8_t *base
         const float q_scale = qs[tid];   // written by this warp
         for (int j = it.j0; j < end && ok; ++j) {
             const int f = fill + j - it.j0;
-            // scales are known long before the scores; a group that the tile enters past its first step, too
-            ok = mbar_wait(bars + 8 * (kSFull + t), ns++ & 1, kWaitNs) &&
-                 mbar_wait(bars + 8 * (kScales + ((f / kGroup) & 1)), (f / (2 * kGroup)) & 1, kWaitNs);
-            ok = __all_sync(0xffffffffu, ok);
+            ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (kSFull + t), ns++ & 1, kWaitNs));
             if (!ok)
                 break;
             tc_fence_after();
-            const float4 rec = *reinterpret_cast<const float4 *>(step_of(base, f)->ks);
-            const int see = pos - j * kKv;   // columns up to this one
+            uint32_t s[4][32];   // the row's scores stay in registers
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                tc_ld32(s_t + 32 * k, s[k]);
+            const float4 rec = *reinterpret_cast<const float4 *>(step_of(base, f)->ks);   // there before the scores
             const bool masked = j * kKv + kKv - 1 > first_pos || rec.x < 0.f || rec.y < 0.f;
-            float top[2];
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-                const float x = masked ? row_max_masked(s_t + 64 * h, (h ? rec.y : rec.x) < 0.f ? -1 : see - 64 * h)
-                                       : row_max<false>(s_t + 64 * h, 63);
-                top[0] = h ? top[0] : x;
-                top[1] = x;
-            }
-            const float sc[2] = {q_scale * fmaxf(rec.x, 0.f), q_scale * fmaxf(rec.y, 0.f)};
+            // a factor of zero (keys of zero) would make NaN of masked scores
+            const float sc[2] = {fmaxf(q_scale * rec.x, 0x1p-126f), fmaxf(q_scale * rec.y, 0x1p-126f)};
             const float lv[2] = {rec.z, rec.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                tc_wait_ld(s[k]);
+            if (masked) {
+                const int see = pos - j * kKv;   // columns up to this one
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int lim = (k < 2 ? rec.x : rec.y) < 0.f ? -1 : see - 32 * k;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        s[k][i] = i <= lim ? s[k][i] : 0xff800000u;   // -inf
+                }
+            }
             float t_m = -INFINITY, t_o = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float x = top[i] == -INFINITY ? -INFINITY : top[i] * sc[i];
+            for (int h = 0; h < 2; ++h) {
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    top[i & 3] = max3(top[i & 3], __uint_as_float(s[2 * h][i]), __uint_as_float(s[2 * h + 1][i]));
+                const float x = fmaxf(max3(top[0], top[1], top[2]), top[3]) * sc[h];
                 t_m = fmaxf(t_m, x);
-                t_o = fmaxf(t_o, x == -INFINITY ? -INFINITY : x + lv[i]);
+                t_o = fmaxf(t_o, x == -INFINITY ? x : x + lv[h]);
             }
             if (t_m > m + kLazy) {
                 l *= ex2_approx(m - t_m);
@@ -1011,32 +970,42 @@ __device__ __forceinline__ void softmax_loop(const ChunkParams &p, uint8_t *base
             const bool grow = t_o > mo + kLazy;
             const float alpha = grow ? ex2_approx(mo - t_o) : 1.f;
             mo = grow ? t_o : mo;
-            if (j > it.j0 && __any_sync(0xffffffffu, grow)) {
-                // O holds every step up to the one before: its products were issued before these scores'
-                row_rescale(o_t, alpha);
-            }
-            __syncwarp();
+            if (__any_sync(0xffffffffu, grow) && j > it.j0)
+                rescale(o_t, alpha);   // O holds every step up to the one before: its products were issued before these scores'
             const float m_ref = m == -INFINITY ? 0.f : m;
             float lf[2];
             bool far = false;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int h = 0; h < 2; ++h) {
                 // as long as no page counts for O its weights are in any units: they are scaled away with mo
-                lf[i] = mo == -INFINITY ? 0.f : lv[i] + (m_ref - mo);
-                far = far || !(fabsf(lf[i]) <= kFarWeight);
+                lf[h] = mo == -INFINITY ? 0.f : lv[h] + (m_ref - mo);
+                far = far || !(fabsf(lf[h]) <= kFarWeight);
             }
             far = __any_sync(0xffffffffu, far);
-#pragma unroll 1
+            if (far) {   // l cannot be had from the weights of O
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        l += ex2_approx(fmaf(__uint_as_float(s[k][i]), sc[k >> 1], -m_ref));
+            }
+#pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint32_t s_h = s_t + 64 * h, p_h = s_t + 32 * h;
-                const float sc_h = h ? sc[1] : sc[0], lf_h = h ? lf[1] : lf[0], off = lf_h - m_ref;
-                const int lim = !masked ? 63 : (h ? rec.y : rec.x) < 0.f ? -1 : see - 64 * h;
-                if (far)
-                    l += row_weights_far(s_h, p_h, sc_h, off, m_ref, lim);
-                else if (masked)
-                    l += row_weights_masked(s_h, p_h, sc_h, off, lim) * ex2_approx(-lf_h);
-                else
-                    l += row_weights<false, false>(s_h, p_h, sc_h, off, 0.f, 63) * ex2_approx(-lf_h);
+                const float off = lf[h] - m_ref;
+                const uint64_t sc2 = pair(sc[h], sc[h]), off2 = pair(off, off);
+                uint64_t sum[2] = {0ull, 0ull};
+                uint32_t w[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const uint32_t *x = &s[2 * h + (i >> 4)][2 * (i & 15)];
+                    float2 e = unpair(fma2(pair(__uint_as_float(x[0]), __uint_as_float(x[1])), sc2, off2));
+                    e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+                    sum[i & 1] = add2(sum[i & 1], pair(e.x, e.y));
+                    w[i] = pack_f16x2(e.x, e.y);
+                }
+                tc_st32(s_t + 32 * h, w);
+                const float2 e = unpair(add2(sum[0], sum[1]));
+                l += far ? 0.f : (e.x + e.y) * ex2_approx(-lf[h]);
             }
             tc_wait_st();
             tc_fence_before();
@@ -1168,7 +1137,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         convert_loop(p, base, base_s, tid - kConvertWarp * 32);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
-        if (tid == kMmaWarp * 32)
+        if (warp == kMmaWarp)
             mma_loop(base, base_s, tmem, p.status);
         else if (warp == kMmaWarp + 1)
             page_loop(p, base, base_s, tid & 31);
