@@ -413,28 +413,31 @@ __device__ __forceinline__ void find_start(const ChunkParams &p, uint8_t *base, 
 
 // ---------------------------------------------------------------- keys and values
 
-// Sixteen e4m3 values to f16 in two 16-byte pieces of a swizzled row.  The lanes of a quarter
-// warp hold the eight pieces of a row; those of the second half store theirs the other way
-// round, so that no two store to the same banks.
-__device__ __forceinline__ void store_f16(uint32_t dst, int row, int c, uint4 x)
+// Which pieces of 16 e4m3 values a converting thread has: of every kRowStep-th row one.  The four
+// lanes that share a row write every other 16 bytes of its 128-byte line, and the next four lanes, a row on,
+// the ones between (the swizzle moves an odd row's by one), so that the eight lanes of a store use all banks.
+struct Piece {
+    int row, c;          // the first row, the piece of it
+    uint32_t lo, hi;     // where its two halves go
+    __device__ __forceinline__ explicit Piece(int tid)
+    {
+        c = (tid & 3) | (tid >> 1 & 4);
+        row = (tid >> 2 & 1) | (tid >> 4) << 1;
+        const uint32_t line = (c >> 2) * kSub + row * 128;
+        const int pos = (c & 3) * 2;
+        lo = line + ((pos ^ (row & 7)) << 4);
+        hi = line + (((pos + 1) ^ (row & 7)) << 4);
+    }
+};
+constexpr int kRowStep = kConvertThreads / 8;   // a multiple of 8: the swizzle is that of the first row
+
+__device__ __forceinline__ void store_f16(uint32_t lo, uint32_t hi, uint4 x)
 {
-    uint4 a, b;
-    a.x = f8x2_to_f16x2(x.x);
-    a.y = f8x2_to_f16x2(x.x >> 16);
-    a.z = f8x2_to_f16x2(x.y);
-    a.w = f8x2_to_f16x2(x.y >> 16);
-    b.x = f8x2_to_f16x2(x.z);
-    b.y = f8x2_to_f16x2(x.z >> 16);
-    b.z = f8x2_to_f16x2(x.w);
-    b.w = f8x2_to_f16x2(x.w >> 16);
-    const uint32_t line = dst + (c >> 2) * kSub + row * 128;
-    const int pos = (c & 3) * 2;
-    const bool late = c >= 4;
-    const uint4 first = late ? b : a, second = late ? a : b;
-    const uint32_t o1 = ((pos + (late ? 1 : 0)) ^ (row & 7)) << 4, o2 = ((pos + (late ? 0 : 1)) ^ (row & 7)) << 4;
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(line + o1), "r"(first.x), "r"(first.y), "r"(first.z), "r"(first.w)
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(lo), "r"(f8x2_to_f16x2(x.x)), "r"(f8x2_to_f16x2(x.x >> 16)),
+                 "r"(f8x2_to_f16x2(x.y)), "r"(f8x2_to_f16x2(x.y >> 16))
                  : "memory");
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(line + o2), "r"(second.x), "r"(second.y), "r"(second.z), "r"(second.w)
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(hi), "r"(f8x2_to_f16x2(x.z)), "r"(f8x2_to_f16x2(x.z >> 16)),
+                 "r"(f8x2_to_f16x2(x.w)), "r"(f8x2_to_f16x2(x.w >> 16))
                  : "memory");
 }
 
@@ -551,22 +554,33 @@ __device__ __forceinline__ bool wait_step(uint32_t bars, int which, int f)
     return (f & (kGroup - 1)) != 0 || mbar_wait(bars + 8 * (which + ((f / kGroup) & 1)), (f / (2 * kGroup)) & 1, kWaitNs);
 }
 
-// Pieces i * threads + tid of a step's keys (values: v = 1), eight a row.  They pass by L1, which is small
-// beside this much shared memory.
-__device__ __forceinline__ void load_pieces(const ChunkParams &p, const Step *step, int v, int tid, uint4 (&x)[kPieces])
+__device__ __forceinline__ uint4 load_piece(const uint8_t *src)
 {
-    constexpr int kRowsOf = kKv / kPieces, kHalf = kPieces / 2;
+    // past L1, which is small beside this much shared memory
+    uint4 x;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(src));
+    return x;
+}
+
+// A thread's pieces of a step's keys (values: v = 1).
+__device__ __forceinline__ void load_pieces(const ChunkParams &p, const Step *step, int v, const Piece &at, uint4 (&x)[kPieces])
+{
+    constexpr int kHalf = kPieces / 2;
+    const int2 page = *reinterpret_cast<const int2 *>(step->page);
     const int rows = step->flags >> kRowsShift;
+    const uint8_t *mine = p.kv_pages + v * (kBlk * kD) + at.row * kD + at.c * 16;
+    const uint8_t *src[2] = {mine + static_cast<size_t>(page.x) * (2 * kBlk * kD), mine + static_cast<size_t>(page.y) * (2 * kBlk * kD)};
+    if (page.x >= 0 && page.y >= 0 && rows == kKv) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+            x[i] = load_piece(src[i / kHalf] + (i % kHalf) * (kRowStep * kD));
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-        const int at = step->page[i / kHalf];
         x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (at >= 0 && i * kRowsOf + (tid >> 3) < rows) {
-            const uint8_t *src = p.kv_pages + static_cast<size_t>(at) * (2 * kBlk * kD) + v * (kBlk * kD) + (i % kHalf) * (kRowsOf * kD) + tid * 16;
-            asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(x[i].x), "=r"(x[i].y), "=r"(x[i].z), "=r"(x[i].w)
-                         : "l"(src));
-        }
+        if ((i < kHalf ? page.x : page.y) >= 0 && i * kRowStep + at.row < rows)
+            x[i] = load_piece(src[i / kHalf] + (i % kHalf) * (kRowStep * kD));
     }
 }
 
@@ -575,7 +589,8 @@ __device__ __forceinline__ void load_pieces(const ChunkParams &p, const Step *st
 __device__ __forceinline__ void convert_loop(const ChunkParams &p, uint8_t *base, uint32_t base_s, int tid)
 {
     const uint32_t bars = base_s + kOffBars;
-    const int row0 = tid >> 3, c = tid & 7, lane = tid & 31;
+    const int lane = tid & 31;
+    const Piece at(tid);
     uint32_t used[kTiles][2] = {};   // items of either parity that a tile had steps of
     uint32_t n_items = 0;
     bool ok = wait_step(bars, kPages, 0);
@@ -583,12 +598,13 @@ __device__ __forceinline__ void convert_loop(const ChunkParams &p, uint8_t *base
     const Step *step = step_of(base, 0);
     int flags = ok ? step->flags : kEnd;
     if (!(flags & kEnd))
-        load_pieces(p, step, 0, tid, x);
+        load_pieces(p, step, 0, at, x);
     for (int f = 0; !(flags & kEnd); ++f) {
         const int stage = f & 1, odd = (flags & kOdd) != 0, tok = step->tok;
+        const uint32_t k_s = base_s + kOffK + stage * kOperand, v_s = base_s + kOffV + stage * kOperand;
         int *first = reinterpret_cast<int *>(base + kOffNan) + odd * kD;
         int *any = reinterpret_cast<int *>(base + kOffNan) + 2 * kD + odd;
-        load_pieces(p, step, 1, tid, y);
+        load_pieces(p, step, 1, at, y);
         if (flags & kBegins) {
             // the last item that used these words is finished: a tile without steps does not wait for anyone, and does
             // not count
@@ -613,7 +629,7 @@ __device__ __forceinline__ void convert_loop(const ChunkParams &p, uint8_t *base
             ok = ok && mbar_wait(bars + 8 * (kKEmpty + stage), ((f >> 1) - 1) & 1, kWaitNs);
 #pragma unroll
         for (int i = 0; i < kPieces; ++i)
-            store_f16(base_s + kOffK + stage * kOperand, i * (kKv / kPieces) + row0, c, x[i]);
+            store_f16(k_s + at.lo + i * (kRowStep * 128), k_s + at.hi + i * (kRowStep * 128), x[i]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0)
@@ -622,17 +638,16 @@ __device__ __forceinline__ void convert_loop(const ChunkParams &p, uint8_t *base
         step = step_of(base, f + 1);
         flags = __shfl_sync(0xffffffffu, step->flags, 0);
         if (!(flags & kEnd))
-            load_pieces(p, step, 0, tid, x);
+            load_pieces(p, step, 0, at, x);
         if (f >= 2)
             ok = ok && mbar_wait(bars + 8 * (kVEmpty + stage), ((f >> 1) - 1) & 1, kWaitNs);
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-            const int row = i * (kKv / kPieces) + row0;
             if (has_nan(y[i])) {
-                y[i] = take_nan(y[i], tok + row, c, first);
+                y[i] = take_nan(y[i], tok + i * kRowStep + at.row, at.c, first);
                 *any = 1;
             }
-            store_f16(base_s + kOffV + stage * kOperand, row, c, y[i]);
+            store_f16(v_s + at.lo + i * (kRowStep * 128), v_s + at.hi + i * (kRowStep * 128), y[i]);
         }
         fence_proxy_async_smem();
         __syncwarp();
