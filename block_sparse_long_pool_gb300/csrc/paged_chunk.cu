@@ -45,14 +45,15 @@ enum {
     kQFull = 8,      // [tiles] queries of an item converted
     kSFull = 10,     // [tiles] scores of a step
     kPFull = 12,     // [tiles] its weights
-    kOFull = 14,     // [tiles] every product of an item
+    kOFull = 14,     // [tiles] the products of a step with its weights are done
     kPages = 16,     // [2] a group of steps' pages are known
     kScales = 18,    // [2] and their scales
     kUsed = 20,      // [2] a group of steps is done
     kDone = 22,      // [tiles][2] an item that the tile has steps of is finished; items in turn
     kReset = 26,     // an item's words for NaN are reset
-    kDrain = 27,
-    kNumBars = 28
+    kSFree = 27,     // [tiles] the scores of a step are read
+    kDrain = 29,
+    kNumBars = 30
 };
 constexpr int kOffRec = kOffBars + 256;           // Step [2][kGroup]
 constexpr int kOffCtrl = kOffRec + 2 * 16 * 32;   // int [16]
@@ -65,7 +66,8 @@ constexpr int kSmem = kOffLive + 2 * kMaxB + 1024;
 static_assert(kNumBars * 8 <= 256 && kOffRec % 16 == 0 && kOffStart % 8 == 0 && kOffScan % 8 == 0, "alignment");
 static_assert(kSmem <= 232448, "shared memory of a CTA");
 
-constexpr int kColS = 0, kColO = kTiles * 128;    // tensor memory: scores (weights in their place), outputs
+// Tensor memory: scores of one tile at a time, weights and outputs of each.
+constexpr int kColS = 0, kColP = 128, kColO = 256;
 
 // What the warps need to know of a step, sixteen written at a time.
 constexpr int kGroup = 16;
@@ -584,8 +586,9 @@ __device__ __forceinline__ void load_pieces(const ChunkParams &p, const Step *st
     }
 }
 
-// The warps that convert.  A step's values are on their way while its keys are converted, and the next
-// step's keys while its values are.
+// The warps that convert: the keys of a step, then its values, in one loop over both (the loops of the
+// three kinds of warps together have to stay in the instruction cache).  The next pieces are on
+// their way while these are converted.
 __device__ __forceinline__ void convert_loop(const ChunkParams &p, uint8_t *base, uint32_t base_s, int tid)
 {
     const uint32_t bars = base_s + kOffBars;
@@ -599,13 +602,12 @@ __device__ __forceinline__ void convert_loop(const ChunkParams &p, uint8_t *base
     int flags = ok ? step->flags : kEnd;
     if (!(flags & kEnd))
         load_pieces(p, step, 0, at, x);
-    for (int f = 0; !(flags & kEnd); ++f) {
-        const int stage = f & 1, odd = (flags & kOdd) != 0, tok = step->tok;
-        const uint32_t k_s = base_s + kOffK + stage * kOperand, v_s = base_s + kOffV + stage * kOperand;
+#pragma unroll 1
+    for (int g = 0; !(flags & kEnd); ++g) {
+        const int f = g >> 1, v = g & 1, stage = f & 1, odd = (flags & kOdd) != 0, tok = step->tok;
         int *first = reinterpret_cast<int *>(base + kOffNan) + odd * kD;
-        int *any = reinterpret_cast<int *>(base + kOffNan) + 2 * kD + odd;
-        load_pieces(p, step, 1, at, y);
-        if (flags & kBegins) {
+        const bool begins = v == 0 && (flags & kBegins) != 0;
+        if (begins) {
             // the last item that used these words is finished: a tile without steps does not wait for anyone, and does
             // not count
 #pragma unroll
@@ -619,40 +621,44 @@ __device__ __forceinline__ void convert_loop(const ChunkParams &p, uint8_t *base
             if (tid < kD)
                 first[tid] = INT_MAX;
             if (tid == 0)
-                *any = 0;
+                reinterpret_cast<int *>(base + kOffNan)[2 * kD + odd] = 0;
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(bars + 8 * kReset);
             ok = ok && mbar_wait(bars + 8 * kReset, n_items++ & 1, kWaitNs);
         }
+        if (v) {
+            ok = wait_step(bars, kPages, f + 1) && ok;
+            step = step_of(base, f + 1);
+            flags = __shfl_sync(0xffffffffu, step->flags, 0);
+        }
+        if (!(flags & kEnd))
+            load_pieces(p, step, v ^ 1, at, y);
         if (f >= 2)
-            ok = ok && mbar_wait(bars + 8 * (kKEmpty + stage), ((f >> 1) - 1) & 1, kWaitNs);
+            ok = ok && mbar_wait(bars + 8 * ((v ? kVEmpty : kKEmpty) + stage), ((f >> 1) - 1) & 1, kWaitNs);
+        if (v) {
+            bool nan = false;
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i)
+                nan = nan || has_nan(x[i]);
+            if (nan) {
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i)
+                    x[i] = take_nan(x[i], tok + i * kRowStep + at.row, at.c, first);
+                reinterpret_cast<int *>(base + kOffNan)[2 * kD + odd] = 1;
+            }
+        }
+        const uint32_t dst = base_s + (v ? kOffV : kOffK) + stage * kOperand;
 #pragma unroll
         for (int i = 0; i < kPieces; ++i)
-            store_f16(k_s + at.lo + i * (kRowStep * 128), k_s + at.hi + i * (kRowStep * 128), x[i]);
+            store_f16(dst + at.lo + i * (kRowStep * 128), dst + at.hi + i * (kRowStep * 128), x[i]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0)
-            mbar_arrive(bars + 8 * (kKFull + stage));
-        ok = wait_step(bars, kPages, f + 1) && ok;
-        step = step_of(base, f + 1);
-        flags = __shfl_sync(0xffffffffu, step->flags, 0);
-        if (!(flags & kEnd))
-            load_pieces(p, step, 0, at, x);
-        if (f >= 2)
-            ok = ok && mbar_wait(bars + 8 * (kVEmpty + stage), ((f >> 1) - 1) & 1, kWaitNs);
+            mbar_arrive(bars + 8 * ((v ? kVFull : kKFull) + stage));
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            if (has_nan(y[i])) {
-                y[i] = take_nan(y[i], tok + i * kRowStep + at.row, at.c, first);
-                *any = 1;
-            }
-            store_f16(v_s + at.lo + i * (kRowStep * 128), v_s + at.hi + i * (kRowStep * 128), y[i]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0)
-            mbar_arrive(bars + 8 * (kVFull + stage));
+        for (int i = 0; i < kPieces; ++i)
+            x[i] = y[i];
         if (!__all_sync(0xffffffffu, ok))
             break;
     }
@@ -667,9 +673,9 @@ __device__ __forceinline__ void issue_pv(uint32_t base_s, uint32_t tmem, int t, 
 {
     constexpr uint32_t id = idesc_f16(kTileRows, kD, 0, 1);   // weights; values as they are stored (dims contiguous)
     const uint32_t v_lo = desc_lo(base_s + kOffV + stage * kOperand, kSub);
-#pragma unroll
+#pragma unroll 2
     for (int i = 0; i < kKv / 16; ++i)   // 16 tokens a product: two groups of eight rows
-        mma_ts(tmem + kColO + t * 128, tmem + kColS + t * 128 + i * 8, v_lo + i * (2048 >> 4), id, !first || i > 0);
+        mma_ts(tmem + kColO + t * 128, tmem + kColP + t * 64 + i * 8, v_lo + i * (2048 >> 4), id, !first || i > 0);
 }
 
 // S = Q K^T.
@@ -677,66 +683,71 @@ __device__ __forceinline__ void issue_qk(uint32_t base_s, uint32_t tmem, int t, 
 {
     constexpr uint32_t id = idesc_f16(kTileRows, kKv, 0, 0);   // K-major queries and keys
     const uint32_t q_lo = desc_lo(base_s + kOffQ + t * kOperand, 16), k_lo = desc_lo(base_s + kOffK + stage * kOperand, 16);
-#pragma unroll
+#pragma unroll 2
     for (int i = 0; i < kD / 16; ++i)   // 16 dims a product; the last four in the second half
-        mma_ss(tmem + kColS + t * 128, q_lo + (((i >> 2) * kSub + (i & 3) * 32) >> 4),
+        mma_ss(tmem + kColS, q_lo + (((i >> 2) * kSub + (i & 3) * 32) >> 4),
                k_lo + (((i >> 2) * kSub + (i & 3) * 32) >> 4), id, i > 0);
 }
 
-// One warp: a step's scores and the products of the step before with its weights, tile by tile in
-// turn: while one tile's softmax runs, the other's products do.
+// One warp: a tile's scores of a step, then its products of the step before with the weights, which its
+// softmax worked on meanwhile; tile by tile in turn.  The softmax keeps scores in registers, so that
+// the next ones go to the same columns as soon as it has read them.
 __device__ __forceinline__ void mma_loop(uint8_t *base, uint32_t base_s, uint32_t tmem, int *status)
 {
     const uint32_t bars = base_s + kOffBars;
-    uint32_t np[kTiles] = {}, nq[kTiles] = {};
+    uint32_t phases = 0;   // of each tile's kPFull, kQFull and kSFree
     int before = 0;   // the flags of the step before
+    int reader = -1;  // the tile whose scores are in tensor memory
     bool ok = true;
     for (int f = 0; ok; ++f) {
         ok = wait_step(bars, kPages, f) && wait_step(bars, kScales, f);   // the scales are read once the scores are there
         const int flags = __shfl_sync(0xffffffffu, step_of(base, f)->flags, 0), ks = f & 1, vs = ks ^ 1;
         // at the start of an item its queries are waited for after the products of the last one
         const bool begins = (flags & kBegins) != 0;
-        if (before)
-            ok = ok && mbar_wait(bars + 8 * (kVFull + vs), ((f - 1) >> 1) & 1, kWaitNs);
-        auto pv = [&](int t) {
-            if (!(before >> t & kActive))
-                return;
-            ok = ok && mbar_wait(bars + 8 * (kPFull + t), np[t]++ & 1, kWaitNs);
+        bool v_there = false, k_there = false;
+#pragma unroll 1
+        for (int u = 0; u < 2 * kTiles; ++u) {
+            // scores and products of a tile in turn; where an item begins or all end, the products of the last one first
+            const bool first = begins || (flags & kEnd);
+            const int t = first ? u & 1 : u >> 1;
+            const bool pv = first ? u < kTiles : (u & 1) != 0;
+            if (!((pv ? before : flags) >> t & kActive))
+                continue;
+            if (pv) {
+                if (!v_there)
+                    ok = ok && mbar_wait(bars + 8 * (kVFull + vs), ((f - 1) >> 1) & 1, kWaitNs);
+                v_there = true;
+                ok = ok && mbar_wait(bars + 8 * (kPFull + t), (phases >> t) & 1, kWaitNs);
+                phases ^= 1 << t;
+            } else {
+                if (!k_there)
+                    ok = ok && mbar_wait(bars + 8 * (kKFull + ks), (f >> 1) & 1, kWaitNs);
+                k_there = true;
+                if (begins) {
+                    ok = ok && mbar_wait(bars + 8 * (kQFull + t), (phases >> (2 + t)) & 1, kWaitNs);
+                    phases ^= 4 << t;
+                }
+                if (reader >= 0) {
+                    ok = ok && mbar_wait(bars + 8 * (kSFree + reader), (phases >> (4 + reader)) & 1, kWaitNs);
+                    phases ^= 16 << reader;
+                }
+                reader = t;
+            }
             ok = __all_sync(0xffffffffu, ok);
             if (!ok)
-                return;
+                break;
             tc_fence_after();
             if (elect_one()) {
-                issue_pv(base_s, tmem, t, vs, (before & kBegins) != 0);
-                if (before & kLast << t)
+                if (pv) {
+                    issue_pv(base_s, tmem, t, vs, (before & kBegins) != 0);
                     tc_commit(bars + 8 * (kOFull + t));
+                } else {
+                    issue_qk(base_s, tmem, t, ks);
+                    tc_commit(bars + 8 * (kSFull + t));
+                }
             }
             __syncwarp();
-        };
-        auto qk = [&](int t) {
-            if (!(flags >> t & kActive))
-                return;
-            if (begins)
-                ok = ok && mbar_wait(bars + 8 * (kQFull + t), nq[t]++ & 1, kWaitNs);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok)
-                return;
-            tc_fence_after();
-            if (elect_one()) {
-                issue_qk(base_s, tmem, t, ks);
-                tc_commit(bars + 8 * (kSFull + t));
-            }
-            __syncwarp();
-        };
-        pv(0);
-        if (begins)
-            pv(1);
-        if (!(flags & kEnd))
-            ok = ok && mbar_wait(bars + 8 * (kKFull + ks), (f >> 1) & 1, kWaitNs);
-        qk(0);
-        if (!begins)
-            pv(1);
-        qk(1);
+        }
         if (elect_one()) {
             if (before)
                 tc_commit(bars + 8 * (kVEmpty + vs));
@@ -901,7 +912,8 @@ __device__ __forceinline__ void softmax_loop(const ChunkParams &p, uint8_t *base
 {
     const uint32_t bars = base_s + kOffBars;
     const int warp = tid >> 5, lane = tid & 31;   // within the tile
-    const uint32_t s_t = tmem + kColS + t * 128 + (static_cast<uint32_t>(warp * 32) << 16);
+    const uint32_t s_t = tmem + kColS + (static_cast<uint32_t>(warp * 32) << 16);
+    const uint32_t p_t = tmem + kColP + t * 64 + (static_cast<uint32_t>(warp * 32) << 16);
     const uint32_t o_t = tmem + kColO + t * 128 + (static_cast<uint32_t>(warp * 32) << 16);
     const int tok_in = tid / p.G, g = tid - tok_in * p.G;
     Walk walk;
@@ -957,6 +969,10 @@ __device__ __forceinline__ void softmax_loop(const ChunkParams &p, uint8_t *base
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 tc_wait_ld(s[k]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bars + 8 * (kSFree + t));
             if (masked) {
                 const int see = pos - j * kKv;   // columns up to this one
 #pragma unroll
@@ -985,8 +1001,15 @@ __device__ __forceinline__ void softmax_loop(const ChunkParams &p, uint8_t *base
             const bool grow = t_o > mo + kLazy;
             const float alpha = grow ? ex2_approx(mo - t_o) : 1.f;
             mo = grow ? t_o : mo;
-            if (__any_sync(0xffffffffu, grow) && j > it.j0)
-                rescale(o_t, alpha);   // O holds every step up to the one before: its products were issued before these scores'
+            if (j > it.j0) {
+                // the products with the weights of the step before are done: O may be scaled, the weights written over
+                ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (kOFull + t), no++ & 1, kWaitNs));
+                if (!ok)
+                    break;
+                tc_fence_after();
+                if (__any_sync(0xffffffffu, grow))
+                    rescale(o_t, alpha);
+            }
             const float m_ref = m == -INFINITY ? 0.f : m;
             float lf[2];
             bool far = false;
@@ -1018,7 +1041,7 @@ __device__ __forceinline__ void softmax_loop(const ChunkParams &p, uint8_t *base
                     sum[i & 1] = add2(sum[i & 1], pair(e.x, e.y));
                     w[i] = pack_f16x2(e.x, e.y);
                 }
-                tc_st32(s_t + 32 * h, w);
+                tc_st32(p_t + 32 * h, w);
                 const float2 e = unpair(add2(sum[0], sum[1]));
                 l += far ? 0.f : (e.x + e.y) * ex2_approx(-lf[h]);
             }
@@ -1124,6 +1147,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             mbar_init(bars + 8 * (kSFull + t), 1);
             mbar_init(bars + 8 * (kPFull + t), 4);
             mbar_init(bars + 8 * (kOFull + t), 1);
+            mbar_init(bars + 8 * (kSFree + t), 4);
             mbar_init(bars + 8 * (kDone + 2 * t), 4);
             mbar_init(bars + 8 * (kDone + 2 * t + 1), 4);
         }
