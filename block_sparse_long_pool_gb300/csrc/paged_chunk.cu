@@ -24,38 +24,39 @@ constexpr int kSoftmaxWarps = 4 * kTiles;
 constexpr int kConvertWarp = kSoftmaxWarps;       // the first of them
 constexpr int kConvertWarps = 4;
 constexpr int kConvertThreads = 32 * kConvertWarps;
-constexpr int kPieces = kKv * kD / 16 / kConvertThreads;   // 16-byte pieces of a step's keys a thread
+constexpr int kPieces = kKv * kD / 16 / kConvertThreads;   // 16-byte pieces of a step's values a thread
 constexpr int kMmaWarp = kConvertWarp + kConvertWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 4);     // the MMA warp, the one that looks up pages, and two for the registers' sake
+constexpr int kThreads = 32 * (kMmaWarp + 4);     // products, pages, keys, and a warp for the registers' sake
 // Registers a thread of the four warpgroups; the block is launched with kRegs a thread.
 constexpr int kRegs = 128, kSoftmaxRegs = 184, kConvertRegs = 96, kMmaRegs = 48;
 static_assert(kTiles * kSoftmaxRegs + kConvertRegs + kMmaRegs <= 4 * kRegs, "the split is what the block has");
-constexpr int kSub = kKv * 128;                   // 64 of 128 dims of 128 f16 rows, 128 bytes a row: 16 KB
-constexpr int kOperand = 2 * kSub;                // 128 x 128 f16
+constexpr int kSub = kKv * 128;                   // 128 rows of 128 bytes: 128 e4m3 dims, or 64 f16 ones
+constexpr int kOperand = 2 * kSub;                // 128 x 128 f16, or both e4m3 terms
+constexpr int kKStages = 4;
 
 constexpr int kOffQ = 0;
 constexpr int kOffK = kOffQ + kTiles * kOperand;
-constexpr int kOffV = kOffK + 2 * kOperand;
+constexpr int kOffV = kOffK + kKStages * kSub;
 constexpr int kOffBars = kOffV + 2 * kOperand;
 enum {
-    kKFull = 0,      // [2] keys of a step converted
-    kKEmpty = 2,     // [2] its score products are done
-    kVFull = 4,      // [2] values converted
-    kVEmpty = 6,     // [2] its products with the weights are done
-    kQFull = 8,      // [tiles] queries of an item converted
-    kSFull = 10,     // [tiles] scores of a step
-    kPFull = 12,     // [tiles] its weights
-    kOFull = 14,     // [tiles] the products of a step with its weights are done
-    kPages = 16,     // [2] a group of steps' pages are known
-    kScales = 18,    // [2] and their scales
-    kUsed = 20,      // [2] a group of steps is done
-    kDone = 22,      // [tiles][2] an item that the tile has steps of is finished; items in turn
-    kReset = 26,     // an item's words for NaN are reset
-    kSFree = 27,     // [tiles] the scores of a step are read
-    kDrain = 29,
-    kNumBars = 30
+    kKFull = 0,      // [stages] keys of a step have landed
+    kKEmpty = 4,     // [stages] its score products are done
+    kVFull = 8,      // [2] values converted
+    kVEmpty = 10,    // [2] its products with the weights are done
+    kQFull = 12,     // [tiles] queries of an item converted
+    kSFull = 14,     // [tiles] scores of a step
+    kSFree = 16,     // [tiles] they are read
+    kPFull = 18,     // [tiles] its weights
+    kOFull = 20,     // [tiles] the products of a step with its weights are done
+    kPages = 22,     // [2] a group of steps' pages are known
+    kScales = 24,    // [2] and their scales
+    kUsed = 26,      // [2] a group of steps is done
+    kDone = 28,      // [tiles][2] an item that the tile has steps of is finished; items in turn
+    kReset = 32,     // an item's words for NaN are reset
+    kDrain = 33,
+    kNumBars = 34
 };
-constexpr int kOffRec = kOffBars + 256;           // Step [2][kGroup]
+constexpr int kOffRec = kOffBars + 320;           // Step [2][kGroup]
 constexpr int kOffCtrl = kOffRec + 2 * 16 * 32;   // int [16]
 constexpr int kOffStart = kOffCtrl + 64;          // Start
 constexpr int kOffQs = kOffStart + 64;            // float [tiles][128]
@@ -63,7 +64,7 @@ constexpr int kOffNan = kOffQs + kTiles * kTileRows * 4;   // int [2][128], then
 constexpr int kOffScan = kOffNan + 2 * kD * 4 + 16;        // long long [32], int [32]
 constexpr int kOffLive = kOffScan + 32 * 12;               // uint16 [kMaxB]
 constexpr int kSmem = kOffLive + 2 * kMaxB + 1024;
-static_assert(kNumBars * 8 <= 256 && kOffRec % 16 == 0 && kOffStart % 8 == 0 && kOffScan % 8 == 0, "alignment");
+static_assert(kNumBars * 8 <= 320 && kOffRec % 16 == 0 && kOffStart % 8 == 0 && kOffScan % 8 == 0, "alignment");
 static_assert(kSmem <= 232448, "shared memory of a CTA");
 
 // Tensor memory: scores of one tile at a time, weights and outputs of each.
@@ -123,7 +124,9 @@ struct ChunkParams {
 // One partial state: O [256][128], then m, l, mo [256].
 constexpr int kPartFloats = kTiles * kTileRows * (kD + 3);
 
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn)
+// Instruction descriptor with f16 (kind::f16) or e4m3 (kind::f8f6f4) operands and an f32 accumulator: both
+// types are number 0 of their kind.
+__host__ __device__ constexpr uint32_t idesc(int M, int N, int a_mn, int b_mn)
 {
     return (1u << 4) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
            (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
@@ -145,16 +148,16 @@ __device__ __forceinline__ uint32_t elect_one()
     return r;
 }
 
-// D (tensor memory) = A B (+ D), both in shared memory.
+// D (tensor memory) = A B (+ D), both e4m3 in shared memory, 32 bytes of each row.
 __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate)
 {
     asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
                  "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate)
                  : "memory");
 }
 
-// The same with A in tensor memory.
+// The same in f16 with A in tensor memory.
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate)
 {
     asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
@@ -564,13 +567,13 @@ __device__ __forceinline__ uint4 load_piece(const uint8_t *src)
     return x;
 }
 
-// A thread's pieces of a step's keys (values: v = 1).
-__device__ __forceinline__ void load_pieces(const ChunkParams &p, const Step *step, int v, const Piece &at, uint4 (&x)[kPieces])
+// A thread's pieces of a step's values.
+__device__ __forceinline__ void load_pieces(const ChunkParams &p, const Step *step, const Piece &at, uint4 (&x)[kPieces])
 {
     constexpr int kHalf = kPieces / 2;
     const int2 page = *reinterpret_cast<const int2 *>(step->page);
     const int rows = step->flags >> kRowsShift;
-    const uint8_t *mine = p.kv_pages + v * (kBlk * kD) + at.row * kD + at.c * 16;
+    const uint8_t *mine = p.kv_pages + kBlk * kD + at.row * kD + at.c * 16;
     const uint8_t *src[2] = {mine + static_cast<size_t>(page.x) * (2 * kBlk * kD), mine + static_cast<size_t>(page.y) * (2 * kBlk * kD)};
     if (page.x >= 0 && page.y >= 0 && rows == kKv) {
 #pragma unroll
@@ -586,9 +589,7 @@ __device__ __forceinline__ void load_pieces(const ChunkParams &p, const Step *st
     }
 }
 
-// The warps that convert: the keys of a step, then its values, in one loop over both (the loops of the
-// three kinds of warps together have to stay in the instruction cache).  The next pieces are on
-// their way while these are converted.
+// The warps that convert a step's values; the next step's are on their way meanwhile.
 __device__ __forceinline__ void convert_loop(const ChunkParams &p, uint8_t *base, uint32_t base_s, int tid)
 {
     const uint32_t bars = base_s + kOffBars;
@@ -601,13 +602,12 @@ __device__ __forceinline__ void convert_loop(const ChunkParams &p, uint8_t *base
     const Step *step = step_of(base, 0);
     int flags = ok ? step->flags : kEnd;
     if (!(flags & kEnd))
-        load_pieces(p, step, 0, at, x);
+        load_pieces(p, step, at, x);
 #pragma unroll 1
-    for (int g = 0; !(flags & kEnd); ++g) {
-        const int f = g >> 1, v = g & 1, stage = f & 1, odd = (flags & kOdd) != 0, tok = step->tok;
+    for (int f = 0; !(flags & kEnd); ++f) {
+        const int stage = f & 1, odd = (flags & kOdd) != 0, tok = step->tok;
         int *first = reinterpret_cast<int *>(base + kOffNan) + odd * kD;
-        const bool begins = v == 0 && (flags & kBegins) != 0;
-        if (begins) {
+        if (flags & kBegins) {
             // the last item that used these words is finished: a tile without steps does not wait for anyone, and does
             // not count
 #pragma unroll
@@ -627,35 +627,31 @@ __device__ __forceinline__ void convert_loop(const ChunkParams &p, uint8_t *base
                 mbar_arrive(bars + 8 * kReset);
             ok = ok && mbar_wait(bars + 8 * kReset, n_items++ & 1, kWaitNs);
         }
-        if (v) {
-            ok = wait_step(bars, kPages, f + 1) && ok;
-            step = step_of(base, f + 1);
-            flags = __shfl_sync(0xffffffffu, step->flags, 0);
-        }
+        ok = wait_step(bars, kPages, f + 1) && ok;
+        step = step_of(base, f + 1);
+        flags = step->flags;
         if (!(flags & kEnd))
-            load_pieces(p, step, v ^ 1, at, y);
+            load_pieces(p, step, at, y);
         if (f >= 2)
-            ok = ok && mbar_wait(bars + 8 * ((v ? kVEmpty : kKEmpty) + stage), ((f >> 1) - 1) & 1, kWaitNs);
-        if (v) {
-            bool nan = false;
+            ok = ok && mbar_wait(bars + 8 * (kVEmpty + stage), ((f >> 1) - 1) & 1, kWaitNs);
+        bool nan = false;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+            nan = nan || has_nan(x[i]);
+        if (nan) {
 #pragma unroll
             for (int i = 0; i < kPieces; ++i)
-                nan = nan || has_nan(x[i]);
-            if (nan) {
-#pragma unroll
-                for (int i = 0; i < kPieces; ++i)
-                    x[i] = take_nan(x[i], tok + i * kRowStep + at.row, at.c, first);
-                reinterpret_cast<int *>(base + kOffNan)[2 * kD + odd] = 1;
-            }
+                x[i] = take_nan(x[i], tok + i * kRowStep + at.row, at.c, first);
+            reinterpret_cast<int *>(base + kOffNan)[2 * kD + odd] = 1;
         }
-        const uint32_t dst = base_s + (v ? kOffV : kOffK) + stage * kOperand;
+        const uint32_t dst = base_s + kOffV + stage * kOperand;
 #pragma unroll
         for (int i = 0; i < kPieces; ++i)
             store_f16(dst + at.lo + i * (kRowStep * 128), dst + at.hi + i * (kRowStep * 128), x[i]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0)
-            mbar_arrive(bars + 8 * ((v ? kVFull : kKFull) + stage));
+            mbar_arrive(bars + 8 * (kVFull + stage));
 #pragma unroll
         for (int i = 0; i < kPieces; ++i)
             x[i] = y[i];
@@ -666,27 +662,61 @@ __device__ __forceinline__ void convert_loop(const ChunkParams &p, uint8_t *base
         report(p.status, SPARSE_ERR_TIMEOUT);
 }
 
+// One thread: a step's keys, two pages, to shared memory as they are.
+__device__ __forceinline__ void key_loop(const CUtensorMap *map, uint8_t *base, uint32_t base_s, int *status)
+{
+    const uint32_t bars = base_s + kOffBars;
+    const uint64_t policy = policy_evict_last();   // other CTAs read them, too
+    bool ok = true;
+    int f = 0;
+    for (;; ++f) {
+        const int stage = f % kKStages;
+        ok = wait_step(bars, kPages, f);
+        if (!ok)
+            break;
+        const Step *step = step_of(base, f);
+        if (step->flags & kEnd)
+            break;
+        if (f >= kKStages)
+            ok = mbar_wait(bars + 8 * (kKEmpty + stage), (f / kKStages - 1) & 1, kWaitNs);
+        if (!ok)
+            break;
+        const uint32_t bar = bars + 8 * (kKFull + stage), dst = base_s + kOffK + stage * kSub;
+        const int a = step->page[0], z = step->page[1];
+        mbar_arrive_expect_tx(bar, (a >= 0 ? kBlk * kD : 0) + (z >= 0 ? kBlk * kD : 0));
+        // (scores of a page that is not there are masked, whatever the stage holds)
+        if (a >= 0)
+            tma_load_3d(dst, map, bar, 0, 0, 2 * a, policy);
+        if (z >= 0)
+            tma_load_3d(dst + kBlk * kD, map, bar, 0, 0, 2 * z, policy);
+    }
+    if (!ok)
+        report(status, SPARSE_ERR_TIMEOUT);
+    // no copy is in flight when the block ends
+    for (int i = f > kKStages ? f - kKStages : 0; i < f; ++i)
+        mbar_wait(bars + 8 * (kKFull + i % kKStages), (i / kKStages) & 1, kWaitNs);
+}
+
 // ---------------------------------------------------------------- products
 
 // O += P V of a step and a tile.
 __device__ __forceinline__ void issue_pv(uint32_t base_s, uint32_t tmem, int t, int stage, bool first)
 {
-    constexpr uint32_t id = idesc_f16(kTileRows, kD, 0, 1);   // weights; values as they are stored (dims contiguous)
+    constexpr uint32_t id = idesc(kTileRows, kD, 0, 1);   // weights; values as they are stored (dims contiguous)
     const uint32_t v_lo = desc_lo(base_s + kOffV + stage * kOperand, kSub);
 #pragma unroll 2
     for (int i = 0; i < kKv / 16; ++i)   // 16 tokens a product: two groups of eight rows
         mma_ts(tmem + kColO + t * 128, tmem + kColP + t * 64 + i * 8, v_lo + i * (2048 >> 4), id, !first || i > 0);
 }
 
-// S = Q K^T.
+// S = Q K^T, Q in two e4m3 terms: 32 dims a product, the four of the second term last.
 __device__ __forceinline__ void issue_qk(uint32_t base_s, uint32_t tmem, int t, int stage)
 {
-    constexpr uint32_t id = idesc_f16(kTileRows, kKv, 0, 0);   // K-major queries and keys
-    const uint32_t q_lo = desc_lo(base_s + kOffQ + t * kOperand, 16), k_lo = desc_lo(base_s + kOffK + stage * kOperand, 16);
+    constexpr uint32_t id = idesc(kTileRows, kKv, 0, 0);   // K-major queries and keys
+    const uint32_t q_lo = desc_lo(base_s + kOffQ + t * kOperand, 16), k_lo = desc_lo(base_s + kOffK + stage * kSub, 16);
 #pragma unroll 2
-    for (int i = 0; i < kD / 16; ++i)   // 16 dims a product; the last four in the second half
-        mma_ss(tmem + kColS, q_lo + (((i >> 2) * kSub + (i & 3) * 32) >> 4),
-               k_lo + (((i >> 2) * kSub + (i & 3) * 32) >> 4), id, i > 0);
+    for (int i = 0; i < 8; ++i)
+        mma_ss(tmem + kColS, q_lo + (((i >> 2) * kSub + (i & 3) * 32) >> 4), k_lo + (((i & 3) * 32) >> 4), id, i > 0);
 }
 
 // One warp: a tile's scores of a step, then its products of the step before with the weights, which its
@@ -701,7 +731,7 @@ __device__ __forceinline__ void mma_loop(uint8_t *base, uint32_t base_s, uint32_
     bool ok = true;
     for (int f = 0; ok; ++f) {
         ok = wait_step(bars, kPages, f) && wait_step(bars, kScales, f);   // the scales are read once the scores are there
-        const int flags = __shfl_sync(0xffffffffu, step_of(base, f)->flags, 0), ks = f & 1, vs = ks ^ 1;
+        const int flags = __shfl_sync(0xffffffffu, step_of(base, f)->flags, 0), ks = f % kKStages, vs = (f - 1) & 1;
         // at the start of an item its queries are waited for after the products of the last one
         const bool begins = (flags & kBegins) != 0;
         bool v_there = false, k_there = false;
@@ -721,7 +751,7 @@ __device__ __forceinline__ void mma_loop(uint8_t *base, uint32_t base_s, uint32_
                 phases ^= 1 << t;
             } else {
                 if (!k_there)
-                    ok = ok && mbar_wait(bars + 8 * (kKFull + ks), (f >> 1) & 1, kWaitNs);
+                    ok = ok && mbar_wait(bars + 8 * (kKFull + ks), (f / kKStages) & 1, kWaitNs);
                 k_there = true;
                 if (begins) {
                     ok = ok && mbar_wait(bars + 8 * (kQFull + t), (phases >> (2 + t)) & 1, kWaitNs);
@@ -773,8 +803,11 @@ __device__ __forceinline__ void mma_loop(uint8_t *base, uint32_t base_s, uint32_
 
 // ---------------------------------------------------------------- softmax
 
-// A tile's queries to f16, each row scaled by a power of two of its own (its largest element to
-// 2^14 .. 2^15), two rows a warp at a time; rows past the tile's are zero.
+// A tile's queries in two e4m3 terms, each row scaled by the largest power of two of its own that
+// leaves its largest element within 448.  bf16 has 8 bits and a term 4, so that the two hold elements
+// down to 2^-11 of the row's largest exactly and those below within 2^-19 of it (half of e4m3's
+// least step, 2^-10, of 2^8 and more; where the largest is past 1.75 times its power of two, of 2^7: 2^-10, 2^-18).
+// Two rows a warp at a time; rows past the tile's are zero, and those with an infinity are NaN.
 __device__ __forceinline__ void load_queries(const ChunkParams &p, const Item &it, int t, uint8_t *base, uint32_t base_s, int warp,
                                              int lane)
 {
@@ -806,21 +839,29 @@ __device__ __forceinline__ void load_queries(const ChunkParams &p, const Item &i
                 v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                top = fmaxf(top, fabsf(v[k]) <= 0x1.fep127f ? fabsf(v[k]) : 0.f);   // of the finite ones
+            for (int k = 0; k < 8; ++k) {
+                const bool finite = fabsf(v[k]) <= 0x1.fep127f;
+                top = fmaxf(top, finite ? fabsf(v[k]) : 0.f);
+                v[k] = finite ? v[k] : NAN;
+            }
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1)
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            // 2^up brings the row's largest element to 2^14 .. 2^15
-            const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-            const int up = top > 0.f ? max(-113, min(126, 14 - e)) : 0;
+            const uint32_t bits = __float_as_uint(top);
+            const int e = static_cast<int>(bits >> 23) - 127;   // top = 2^e times 1 to 2
+            const int up = top > 0.f ? max(-120, min(126, ((bits & 0x7fffffu) <= 0x600000u ? 8 : 7) - e)) : 0;
             const float f = __uint_as_float(static_cast<uint32_t>(up + 127) << 23 | p.q_sign);
-            uint32_t h[4];
+            uint32_t hi[2], lo[2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                h[k] = pack_f16x2(v[2 * k] * f, v[2 * k + 1] * f);
-            const uint32_t at = base_s + kOffQ + t * kOperand + (c >> 3) * kSub + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+            for (int k = 0; k < 2; ++k) {
+                const float a = v[4 * k] * f, b = v[4 * k + 1] * f, d = v[4 * k + 2] * f, g = v[4 * k + 3] * f;
+                hi[k] = f8x4_pack(a, b, d, g);
+                const float2 ab = f8x2_to_float2(hi[k]), dg = f8x2_to_float2(hi[k] >> 16);
+                lo[k] = f8x4_pack(a - ab.x, b - ab.y, d - dg.x, g - dg.y);
+            }
+            const uint32_t at = base_s + kOffQ + t * kOperand + row * 128 + (((c >> 1) ^ (row & 7)) << 4) + (c & 1) * 8;
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0]), "r"(hi[1]) : "memory");
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + kSub), "r"(lo[0]), "r"(lo[1]) : "memory");
             if (c == 0)
                 qs[row] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
         }
@@ -1126,7 +1167,7 @@ __device__ __forceinline__ void softmax_loop(const ChunkParams &p, uint8_t *base
     }
 }
 
-__global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_constant__ ChunkParams p)
+__global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ ChunkParams p)
 {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_s = smem_u32(smem_raw);
@@ -1137,8 +1178,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     int *ctrl = reinterpret_cast<int *>(base + kOffCtrl);
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bars + 8 * (kKFull + i), kConvertWarps);
-            mbar_init(bars + 8 * (kKEmpty + i), 1);
             mbar_init(bars + 8 * (kVFull + i), kConvertWarps);
             mbar_init(bars + 8 * (kVEmpty + i), 1);
         }
@@ -1155,6 +1194,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             mbar_init(bars + 8 * (kPages + i), 1);
             mbar_init(bars + 8 * (kScales + i), 1);
             mbar_init(bars + 8 * (kUsed + i), 1);
+        }
+        for (int i = 0; i < kKStages; ++i) {
+            mbar_init(bars + 8 * (kKFull + i), 1);
+            mbar_init(bars + 8 * (kKEmpty + i), 1);
         }
         mbar_init(bars + 8 * kReset, kConvertWarps);
         mbar_init(bars + 8 * kDrain, 1);
@@ -1180,6 +1223,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             mma_loop(base, base_s, tmem, p.status);
         else if (warp == kMmaWarp + 1)
             page_loop(p, base, base_s, tid & 31);
+        else if (tid == (kMmaWarp + 2) * 32)
+            key_loop(&map, base, base_s, p.status);
     }
     __syncwarp();
     tc_fence_before();
@@ -1286,8 +1331,8 @@ extern "C" SPARSE_API int sparse_paged_chunk_attn_f8(const uint16_t *Q, long lon
     const double work = (static_cast<double>(n_tok) / (kTiles * per_tile) + B) * H_kv * (static_cast<double>(max_blocks) * kBlk + n_tok + kItemCost);
     if (work > 0x1p61)
         return fail(SPARSE_ERR_UNSUPPORTED, "%s: n_tok, max_blocks and H_kv are too large together", name);
-    if (static_cast<long long>(n_pages) * H_kv > INT_MAX)
-        return fail(SPARSE_ERR_UNSUPPORTED, "%s: n_pages * H_kv = %lld >= 2^31", name, static_cast<long long>(n_pages) * H_kv);
+    if (2LL * n_pages * H_kv > INT_MAX)
+        return fail(SPARSE_ERR_UNSUPPORTED, "%s: n_pages * H_kv = %lld >= 2^30", name, static_cast<long long>(n_pages) * H_kv);
     const size_t need = sparse_paged_chunk_attn_f8_workspace_size(B, H_q, H_kv);
     if (workspace_bytes < need)
         return fail(SPARSE_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", name, workspace_bytes, need);
@@ -1311,6 +1356,10 @@ extern "C" SPARSE_API int sparse_paged_chunk_attn_f8(const uint16_t *Q, long lon
     }
     if (regs[dev.device] < kRegs)
         return fail(SPARSE_ERR_UNSUPPORTED, "%s: built with %d registers a thread, %d expected", name, regs[dev.device], kRegs);
+    CUtensorMap map;
+    rc = sp_host::make_page_tensor_map(&map, kv_pages, 2LL * n_pages * H_kv);
+    if (rc != SPARSE_OK)
+        return rc;
     const int ctas = dev.sm_count;
     float *parts = static_cast<float *>(workspace);
     int4 *tails = reinterpret_cast<int4 *>(parts + 2ull * ctas * kPartFloats);
@@ -1338,7 +1387,7 @@ extern "C" SPARSE_API int sparse_paged_chunk_attn_f8(const uint16_t *Q, long lon
     p.H_kv = H_kv;
     p.G = H_q / H_kv;
     p.per_tile = per_tile;
-    rc = sp_host::cuda_status(launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), kThreads, kSmem, stream, p), name);
+    rc = sp_host::cuda_status(launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), kThreads, kSmem, stream, map, p), name);
     if (rc != SPARSE_OK)
         return rc;
     const void *merge = reinterpret_cast<const void *>(paged_chunk_merge_kernel);

@@ -90,6 +90,11 @@ class Chunk:
             size = torch.einsum("hgnt,htd->hgnd", w.nan_to_num(), v.nan_to_num().abs())
             # scores: fp32 sums of 128 exact products, one more product, an exponent in fp32 and 2^x (2^-22)
             ds = torch.where(see, sabs, 0.0).amax(-1, keepdim=True) * 132 * 2.0 ** -24 + 2.0 ** -22
+            # queries in two e4m3 terms: the row's largest is scaled into (224, 448], each element is off by half of
+            # e4m3's least step at most (2^-10; its first term leaves a rest of 4 bits where that step allows), so
+            # by 2^-10 / 224 < 2^-17 of the largest, times the keys' sizes
+            ksum = torch.where(ok[None, :], kv[0].abs().nan_to_num().sum(-1), 0.0).amax(-1)[:, None, None, None]
+            ds = ds + q.abs().amax(-1, keepdim=True) * ksum * abs(scale) * 2.0 ** -17
             ds = ds + (sc.abs().where(see, torch.zeros_like(sc)).nan_to_num().amax(-1, keepdim=True) * 1.4427 + 16) * 2.0 ** -23
             # weights in f16 (2^-11, below 2^-14 of the best steps of 2^-24), fp32 sums over the steps; O in bf16
             t = o.nan_to_num().abs() * 2.0 ** -8 + size * (2.0 ** -11 + 2 * ds + 2.0 ** -18) * (1 + 2.0 ** -8)
