@@ -14,7 +14,7 @@ constexpr int kTiles = 2;                         // tiles of an item
 constexpr int kKv = 128;                          // tokens of a step: two pages
 constexpr int kMaxB = 4096;
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr float kLazy = 10.f;                     // log2 of the growth of a maximum that is let pass
+constexpr float kMost = 0x1p15f;                  // of the weights of a page, in f16: beyond it the row's maximum is taken anew
 constexpr float kFarWeight = 60.f;                // log2 of the largest factor from a page's weights to O's
 constexpr int kItemCost = 320;                    // what an item costs beside its tokens, in tokens of one step
 constexpr int kMinWork = 1024;                    // the least share of a CTA, in the same units
@@ -26,7 +26,7 @@ constexpr int kConvertWarps = 4;
 constexpr int kConvertThreads = 32 * kConvertWarps;
 constexpr int kPieces = kKv * kD / 16 / kConvertThreads;   // 16-byte pieces of a step's values a thread
 constexpr int kMmaWarp = kConvertWarp + kConvertWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 4);     // products, pages, keys, and a warp for the registers' sake
+constexpr int kThreads = 32 * (kMmaWarp + 4);     // scores, products with values, pages, keys
 // Registers a thread of the four warpgroups; the block is launched with kRegs a thread.
 constexpr int kRegs = 128, kSoftmaxRegs = 184, kConvertRegs = 96, kMmaRegs = 48;
 static_assert(kTiles * kSoftmaxRegs + kConvertRegs + kMmaRegs <= 4 * kRegs, "the split is what the block has");
@@ -53,8 +53,8 @@ enum {
     kUsed = 26,      // [2] a group of steps is done
     kDone = 28,      // [tiles][2] an item that the tile has steps of is finished; items in turn
     kReset = 32,     // an item's words for NaN are reset
-    kDrain = 33,
-    kNumBars = 34
+    kDrain = 33,     // [2] every product is done
+    kNumBars = 35
 };
 constexpr int kOffRec = kOffBars + 320;           // Step [2][kGroup]
 constexpr int kOffCtrl = kOffRec + 2 * 16 * 32;   // int [16]
@@ -436,14 +436,24 @@ struct Piece {
 };
 constexpr int kRowStep = kConvertThreads / 8;   // a multiple of 8: the swizzle is that of the first row
 
-__device__ __forceinline__ void store_f16(uint32_t lo, uint32_t hi, uint4 x)
+// Adds the values to `sum`, two f16 sums: NaN where one of them is (they are 448 at most, 128 a thread).
+__device__ __forceinline__ uint32_t store_f16(uint32_t lo, uint32_t hi, uint4 x, uint32_t sum)
 {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(lo), "r"(f8x2_to_f16x2(x.x)), "r"(f8x2_to_f16x2(x.x >> 16)),
-                 "r"(f8x2_to_f16x2(x.y)), "r"(f8x2_to_f16x2(x.y >> 16))
-                 : "memory");
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(hi), "r"(f8x2_to_f16x2(x.z)), "r"(f8x2_to_f16x2(x.z >> 16)),
-                 "r"(f8x2_to_f16x2(x.w)), "r"(f8x2_to_f16x2(x.w >> 16))
-                 : "memory");
+    const uint32_t w[8] = {f8x2_to_f16x2(x.x), f8x2_to_f16x2(x.x >> 16), f8x2_to_f16x2(x.y), f8x2_to_f16x2(x.y >> 16),
+                           f8x2_to_f16x2(x.z), f8x2_to_f16x2(x.z >> 16), f8x2_to_f16x2(x.w), f8x2_to_f16x2(x.w >> 16)};
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(lo), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(hi), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+    __half2 a = *reinterpret_cast<__half2 *>(&sum);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        a = __hadd2(a, *reinterpret_cast<const __half2 *>(&w[i]));
+    return *reinterpret_cast<uint32_t *>(&a);
+}
+
+__device__ __forceinline__ bool is_nan(uint32_t sum)
+{
+    const float2 f = __half22float2(*reinterpret_cast<__half2 *>(&sum));
+    return f.x != f.x || f.y != f.y;
 }
 
 // NaN among the values: the products would spread it to rows that do not see its token.  It is
@@ -459,12 +469,6 @@ __device__ __noinline__ uint4 take_nan(uint4 x, int tok, int c, int *first)
         }
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-__device__ __forceinline__ bool has_nan(uint4 x)
-{
-    auto f = [](uint32_t v) { return (v & 0x7f7f7f7fu) + 0x01010101u; };
-    return ((f(x.x) | f(x.y) | f(x.z) | f(x.w)) & 0x80808080u) != 0u;
 }
 
 // One warp: the steps, one after another across items, with their pages and scales, two lanes a step.
@@ -589,7 +593,7 @@ __device__ __forceinline__ void load_pieces(const ChunkParams &p, const Step *st
     }
 }
 
-// The warps that convert a step's values; the next step's are on their way meanwhile.
+// The warps that convert a step's values.  The next step's are asked for as soon as these are stored.
 __device__ __forceinline__ void convert_loop(const ChunkParams &p, uint8_t *base, uint32_t base_s, int tid)
 {
     const uint32_t bars = base_s + kOffBars;
@@ -598,7 +602,7 @@ __device__ __forceinline__ void convert_loop(const ChunkParams &p, uint8_t *base
     uint32_t used[kTiles][2] = {};   // items of either parity that a tile had steps of
     uint32_t n_items = 0;
     bool ok = wait_step(bars, kPages, 0);
-    uint4 x[kPieces], y[kPieces];
+    uint4 x[kPieces];
     const Step *step = step_of(base, 0);
     int flags = ok ? step->flags : kEnd;
     if (!(flags & kEnd))
@@ -627,34 +631,30 @@ __device__ __forceinline__ void convert_loop(const ChunkParams &p, uint8_t *base
                 mbar_arrive(bars + 8 * kReset);
             ok = ok && mbar_wait(bars + 8 * kReset, n_items++ & 1, kWaitNs);
         }
+        if (f >= 2)
+            ok = ok && mbar_wait(bars + 8 * (kVEmpty + stage), ((f >> 1) - 1) & 1, kWaitNs);
+        const uint32_t dst = base_s + kOffV + stage * kOperand;
+        uint32_t nan = 0u;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+            nan = store_f16(dst + at.lo + i * (kRowStep * 128), dst + at.hi + i * (kRowStep * 128), x[i], nan);
+        if (is_nan(nan)) {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                x[i] = take_nan(x[i], tok + i * kRowStep + at.row, at.c, first);
+                store_f16(dst + at.lo + i * (kRowStep * 128), dst + at.hi + i * (kRowStep * 128), x[i], 0u);
+            }
+            reinterpret_cast<int *>(base + kOffNan)[2 * kD + odd] = 1;
+        }
         ok = wait_step(bars, kPages, f + 1) && ok;
         step = step_of(base, f + 1);
         flags = step->flags;
         if (!(flags & kEnd))
-            load_pieces(p, step, at, y);
-        if (f >= 2)
-            ok = ok && mbar_wait(bars + 8 * (kVEmpty + stage), ((f >> 1) - 1) & 1, kWaitNs);
-        bool nan = false;
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i)
-            nan = nan || has_nan(x[i]);
-        if (nan) {
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i)
-                x[i] = take_nan(x[i], tok + i * kRowStep + at.row, at.c, first);
-            reinterpret_cast<int *>(base + kOffNan)[2 * kD + odd] = 1;
-        }
-        const uint32_t dst = base_s + kOffV + stage * kOperand;
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i)
-            store_f16(dst + at.lo + i * (kRowStep * 128), dst + at.hi + i * (kRowStep * 128), x[i]);
+            load_pieces(p, step, at, x);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0)
             mbar_arrive(bars + 8 * (kVFull + stage));
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i)
-            x[i] = y[i];
         if (!__all_sync(0xffffffffu, ok))
             break;
     }
@@ -704,7 +704,7 @@ __device__ __forceinline__ void issue_pv(uint32_t base_s, uint32_t tmem, int t, 
 {
     constexpr uint32_t id = idesc(kTileRows, kD, 0, 1);   // weights; values as they are stored (dims contiguous)
     const uint32_t v_lo = desc_lo(base_s + kOffV + stage * kOperand, kSub);
-#pragma unroll 2
+#pragma unroll
     for (int i = 0; i < kKv / 16; ++i)   // 16 tokens a product: two groups of eight rows
         mma_ts(tmem + kColO + t * 128, tmem + kColP + t * 64 + i * 8, v_lo + i * (2048 >> 4), id, !first || i > 0);
 }
@@ -714,83 +714,53 @@ __device__ __forceinline__ void issue_qk(uint32_t base_s, uint32_t tmem, int t, 
 {
     constexpr uint32_t id = idesc(kTileRows, kKv, 0, 0);   // K-major queries and keys
     const uint32_t q_lo = desc_lo(base_s + kOffQ + t * kOperand, 16), k_lo = desc_lo(base_s + kOffK + stage * kSub, 16);
-#pragma unroll 2
+#pragma unroll
     for (int i = 0; i < 8; ++i)
         mma_ss(tmem + kColS, q_lo + (((i >> 2) * kSub + (i & 3) * 32) >> 4), k_lo + (((i & 3) * 32) >> 4), id, i > 0);
 }
 
-// One warp: a tile's scores of a step, then its products of the step before with the weights, which its
-// softmax worked on meanwhile; tile by tile in turn.  The softmax keeps scores in registers, so that
-// the next ones go to the same columns as soon as it has read them.
-__device__ __forceinline__ void mma_loop(uint8_t *base, uint32_t base_s, uint32_t tmem, int *status)
+// The products are issued by two warps: issuing one takes until the one before has begun, so what a
+// warp waits for between them has to overlap with the other's.
+//
+// The first: scores of a step, tile by tile.  The softmax keeps scores in registers, so that the next ones go
+// to the same columns as soon as it has read them, before its weights are there.
+__device__ __forceinline__ void score_loop(uint8_t *base, uint32_t base_s, uint32_t tmem, int *status)
 {
     const uint32_t bars = base_s + kOffBars;
-    uint32_t phases = 0;   // of each tile's kPFull, kQFull and kSFree
-    int before = 0;   // the flags of the step before
-    int reader = -1;  // the tile whose scores are in tensor memory
+    uint32_t q_phase[kTiles] = {}, s_phase[kTiles] = {};
+    int reader = -1;   // the tile whose scores are in tensor memory
     bool ok = true;
+#pragma unroll 1
     for (int f = 0; ok; ++f) {
         ok = wait_step(bars, kPages, f) && wait_step(bars, kScales, f);   // the scales are read once the scores are there
-        const int flags = __shfl_sync(0xffffffffu, step_of(base, f)->flags, 0), ks = f % kKStages, vs = (f - 1) & 1;
-        // at the start of an item its queries are waited for after the products of the last one
-        const bool begins = (flags & kBegins) != 0;
-        bool v_there = false, k_there = false;
-#pragma unroll 1
-        for (int u = 0; u < 2 * kTiles; ++u) {
-            // scores and products of a tile in turn; where an item begins or all end, the products of the last one first
-            const bool first = begins || (flags & kEnd);
-            const int t = first ? u & 1 : u >> 1;
-            const bool pv = first ? u < kTiles : (u & 1) != 0;
-            if (!((pv ? before : flags) >> t & kActive))
+        const int flags = __shfl_sync(0xffffffffu, step_of(base, f)->flags, 0), stage = f % kKStages;
+        if (flags & kEnd)
+            break;
+        ok = ok && mbar_wait(bars + 8 * (kKFull + stage), (f / kKStages) & 1, kWaitNs);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+            if (!(flags >> t & kActive))
                 continue;
-            if (pv) {
-                if (!v_there)
-                    ok = ok && mbar_wait(bars + 8 * (kVFull + vs), ((f - 1) >> 1) & 1, kWaitNs);
-                v_there = true;
-                ok = ok && mbar_wait(bars + 8 * (kPFull + t), (phases >> t) & 1, kWaitNs);
-                phases ^= 1 << t;
-            } else {
-                if (!k_there)
-                    ok = ok && mbar_wait(bars + 8 * (kKFull + ks), (f / kKStages) & 1, kWaitNs);
-                k_there = true;
-                if (begins) {
-                    ok = ok && mbar_wait(bars + 8 * (kQFull + t), (phases >> (2 + t)) & 1, kWaitNs);
-                    phases ^= 4 << t;
-                }
-                if (reader >= 0) {
-                    ok = ok && mbar_wait(bars + 8 * (kSFree + reader), (phases >> (4 + reader)) & 1, kWaitNs);
-                    phases ^= 16 << reader;
-                }
-                reader = t;
-            }
+            if (flags & kBegins)
+                ok = ok && mbar_wait(bars + 8 * (kQFull + t), q_phase[t]++ & 1, kWaitNs);
+            if (reader == 0)
+                ok = ok && mbar_wait(bars + 8 * kSFree, s_phase[0]++ & 1, kWaitNs);
+            else if (reader == 1)
+                ok = ok && mbar_wait(bars + 8 * (kSFree + 1), s_phase[1]++ & 1, kWaitNs);
+            reader = t;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok)
                 break;
             tc_fence_after();
             if (elect_one()) {
-                if (pv) {
-                    issue_pv(base_s, tmem, t, vs, (before & kBegins) != 0);
-                    tc_commit(bars + 8 * (kOFull + t));
-                } else {
-                    issue_qk(base_s, tmem, t, ks);
-                    tc_commit(bars + 8 * (kSFull + t));
-                }
+                issue_qk(base_s, tmem, t, stage);
+                tc_commit(bars + 8 * (kSFull + t));
             }
             __syncwarp();
         }
-        if (elect_one()) {
-            if (before)
-                tc_commit(bars + 8 * (kVEmpty + vs));
-            if (!(flags & kEnd))
-                tc_commit(bars + 8 * (kKEmpty + ks));
-            // the weights of every step of the group before are there: its scales have been read
-            if (f > 0 && f % kGroup == 0)
-                mbar_arrive(bars + 8 * (kUsed + ((f / kGroup - 1) & 1)));
-        }
+        if (elect_one())
+            tc_commit(bars + 8 * (kKEmpty + stage));
         __syncwarp();
-        before = flags;
-        if (flags & kEnd)
-            break;
     }
     if (!ok)
         report(status, SPARSE_ERR_TIMEOUT);
@@ -799,6 +769,50 @@ __device__ __forceinline__ void mma_loop(uint8_t *base, uint32_t base_s, uint32_
     if (elect_one())
         tc_commit(bars + 8 * kDrain);
     mbar_wait(bars + 8 * kDrain, 0, kWaitNs);
+}
+
+// The second: O += P V of a step, tile by tile.
+__device__ __forceinline__ void value_loop(uint8_t *base, uint32_t base_s, uint32_t tmem, int *status)
+{
+    const uint32_t bars = base_s + kOffBars;
+    uint32_t phase[kTiles] = {};
+    bool ok = true;
+#pragma unroll 1
+    for (int f = 0; ok; ++f) {
+        ok = wait_step(bars, kPages, f);
+        const int flags = __shfl_sync(0xffffffffu, step_of(base, f)->flags, 0), stage = f & 1;
+        if (flags & kEnd)
+            break;
+        ok = ok && mbar_wait(bars + 8 * (kVFull + stage), (f >> 1) & 1, kWaitNs);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+            if (!(flags >> t & kActive))
+                continue;
+            ok = ok && mbar_wait(bars + 8 * (kPFull + t), phase[t]++ & 1, kWaitNs);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok)
+                break;
+            tc_fence_after();
+            if (elect_one()) {
+                issue_pv(base_s, tmem, t, stage, (flags & kBegins) != 0);
+                tc_commit(bars + 8 * (kOFull + t));
+            }
+            __syncwarp();
+        }
+        if (elect_one()) {
+            tc_commit(bars + 8 * (kVEmpty + stage));
+            // the weights of every step of the group are there: its scales have been read
+            if (f % kGroup == kGroup - 1)
+                mbar_arrive(bars + 8 * (kUsed + ((f / kGroup) & 1)));
+        }
+        __syncwarp();
+    }
+    if (!ok)
+        report(status, SPARSE_ERR_TIMEOUT);
+    __syncwarp();
+    if (elect_one())
+        tc_commit(bars + 8 * (kDrain + 1));
+    mbar_wait(bars + 8 * (kDrain + 1), 0, kWaitNs);
 }
 
 // ---------------------------------------------------------------- softmax
@@ -1024,68 +1038,84 @@ __device__ __forceinline__ void softmax_loop(const ChunkParams &p, uint8_t *base
                         s[k][i] = i <= lim ? s[k][i] : 0xff800000u;   // -inf
                 }
             }
-            float t_m = -INFINITY, t_o = -INFINITY;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    top[i & 3] = max3(top[i & 3], __uint_as_float(s[2 * h][i]), __uint_as_float(s[2 * h + 1][i]));
-                const float x = fmaxf(max3(top[0], top[1], top[2]), top[3]) * sc[h];
-                t_m = fmaxf(t_m, x);
-                t_o = fmaxf(t_o, x == -INFINITY ? x : x + lv[h]);
-            }
-            if (t_m > m + kLazy) {
-                l *= ex2_approx(m - t_m);
-                m = t_m;
-            }
-            const bool grow = t_o > mo + kLazy;
-            const float alpha = grow ? ex2_approx(mo - t_o) : 1.f;
-            mo = grow ? t_o : mo;
+            // The reference m is the maximum of the item's first step, and stays as long as no page's weights add up to
+            // more than kMost: only then (and in rows with NaN) is the maximum looked for and the step done again.
+            bool over = j == it.j0, again = over;
+            float add;
             if (j > it.j0) {
                 // the products with the weights of the step before are done: O may be scaled, the weights written over
                 ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (kOFull + t), no++ & 1, kWaitNs));
                 if (!ok)
                     break;
                 tc_fence_after();
-                if (__any_sync(0xffffffffu, grow))
-                    rescale(o_t, alpha);
             }
-            const float m_ref = m == -INFINITY ? 0.f : m;
-            float lf[2];
-            bool far = false;
+            for (int turn = 0;; ++turn) {
+                if (again) {
+                    float t_m = -INFINITY, t_o = -INFINITY;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                // as long as no page counts for O its weights are in any units: they are scaled away with mo
-                lf[h] = mo == -INFINITY ? 0.f : lv[h] + (m_ref - mo);
-                far = far || !(fabsf(lf[h]) <= kFarWeight);
-            }
-            far = __any_sync(0xffffffffu, far);
-            if (far) {   // l cannot be had from the weights of O
+                    for (int h = 0; h < 2; ++h) {
+                        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        l += ex2_approx(fmaf(__uint_as_float(s[k][i]), sc[k >> 1], -m_ref));
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float off = lf[h] - m_ref;
-                const uint64_t sc2 = pair(sc[h], sc[h]), off2 = pair(off, off);
-                uint64_t sum[2] = {0ull, 0ull};
-                uint32_t w[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const uint32_t *x = &s[2 * h + (i >> 4)][2 * (i & 15)];
-                    float2 e = unpair(fma2(pair(__uint_as_float(x[0]), __uint_as_float(x[1])), sc2, off2));
-                    e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-                    sum[i & 1] = add2(sum[i & 1], pair(e.x, e.y));
-                    w[i] = pack_f16x2(e.x, e.y);
+                        for (int i = 0; i < 32; ++i)
+                            top[i & 3] = max3(top[i & 3], __uint_as_float(s[2 * h][i]), __uint_as_float(s[2 * h + 1][i]));
+                        const float x = fmaxf(max3(top[0], top[1], top[2]), top[3]) * sc[h];
+                        t_m = fmaxf(t_m, x);
+                        t_o = fmaxf(t_o, x == -INFINITY ? x : x + lv[h]);
+                    }
+                    if (over && t_m > m) {
+                        l *= ex2_approx(m - t_m);
+                        m = t_m;
+                    }
+                    const bool grow = over && t_o > mo;
+                    const float alpha = grow ? ex2_approx(mo - t_o) : 1.f;
+                    mo = grow ? t_o : mo;
+                    if (__any_sync(0xffffffffu, grow) && j > it.j0)
+                        rescale(o_t, alpha);
                 }
-                tc_st32(p_t + 32 * h, w);
-                const float2 e = unpair(add2(sum[0], sum[1]));
-                l += far ? 0.f : (e.x + e.y) * ex2_approx(-lf[h]);
+                const float m_ref = m == -INFINITY ? 0.f : m;
+                float lf[2];
+                bool far = false;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    // as long as no page counts for O its weights are in any units: they are scaled away with mo
+                    lf[h] = mo == -INFINITY ? 0.f : lv[h] + (m_ref - mo);
+                    far = far || !(fabsf(lf[h]) <= kFarWeight);
+                }
+                far = __any_sync(0xffffffffu, far);
+                add = 0.f;
+                if (far) {   // l cannot be had from the weights of O
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            add += ex2_approx(fmaf(__uint_as_float(s[k][i]), sc[k >> 1], -m_ref));
+                }
+                over = far && !(add <= kMost);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float off = lf[h] - m_ref;
+                    const uint64_t sc2 = pair(sc[h], sc[h]), off2 = pair(off, off);
+                    uint64_t sum[2] = {0ull, 0ull};
+                    uint32_t w[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const uint32_t *x = &s[2 * h + (i >> 4)][2 * (i & 15)];
+                        float2 e = unpair(fma2(pair(__uint_as_float(x[0]), __uint_as_float(x[1])), sc2, off2));
+                        e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+                        sum[i & 1] = add2(sum[i & 1], pair(e.x, e.y));
+                        w[i] = pack_f16x2(e.x, e.y);
+                    }
+                    tc_st32(p_t + 32 * h, w);
+                    const float2 e = unpair(add2(sum[0], sum[1]));
+                    add += far ? 0.f : (e.x + e.y) * ex2_approx(-lf[h]);
+                    over = over || !(e.x + e.y <= kMost);   // NaN, too
+                }
+                again = turn == 0 && j > it.j0 && __any_sync(0xffffffffu, over);
+                if (!again)
+                    break;
+                tc_wait_st();   // before the weights are written over
             }
+            l += add;
             tc_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -1201,6 +1231,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         }
         mbar_init(bars + 8 * kReset, kConvertWarps);
         mbar_init(bars + 8 * kDrain, 1);
+        mbar_init(bars + 8 * (kDrain + 1), 1);
         fence_barrier_init();
     }
     if (warp == kMmaWarp)
@@ -1220,10 +1251,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
         if (warp == kMmaWarp)
-            mma_loop(base, base_s, tmem, p.status);
+            score_loop(base, base_s, tmem, p.status);
         else if (warp == kMmaWarp + 1)
+            value_loop(base, base_s, tmem, p.status);
+        else if (warp == kMmaWarp + 2)
             page_loop(p, base, base_s, tid & 31);
-        else if (tid == (kMmaWarp + 2) * 32)
+        else if (tid == (kMmaWarp + 3) * 32)
             key_loop(&map, base, base_s, p.status);
     }
     __syncwarp();
