@@ -14,7 +14,7 @@ constexpr int kTiles = 2;                         // tiles of an item
 constexpr int kKv = 128;                          // tokens of a step: two pages
 constexpr int kMaxB = 4096;
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr float kMost = 0x1p15f;                  // of the weights of a page, in f16: beyond it the row's maximum is taken anew
+constexpr float kMost = 0x1p15f;                  // of 32 weights, in f16: beyond it the row's reference is taken anew
 constexpr float kFarWeight = 60.f;                // log2 of the largest factor from a page's weights to O's
 constexpr int kItemCost = 320;                    // what an item costs beside its tokens, in tokens of one step
 constexpr int kMinWork = 1024;                    // the least share of a CTA, in the same units
@@ -26,9 +26,9 @@ constexpr int kConvertWarps = 4;
 constexpr int kConvertThreads = 32 * kConvertWarps;
 constexpr int kPieces = kKv * kD / 16 / kConvertThreads;   // 16-byte pieces of a step's values a thread
 constexpr int kMmaWarp = kConvertWarp + kConvertWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 4);     // scores, products with values, pages, keys
+constexpr int kThreads = 32 * (kMmaWarp + 4);     // products of either tile, pages, keys
 // Registers a thread of the four warpgroups; the block is launched with kRegs a thread.
-constexpr int kRegs = 128, kSoftmaxRegs = 184, kConvertRegs = 96, kMmaRegs = 48;
+constexpr int kRegs = 128, kSoftmaxRegs = 152, kConvertRegs = 112, kMmaRegs = 96;
 static_assert(kTiles * kSoftmaxRegs + kConvertRegs + kMmaRegs <= 4 * kRegs, "the split is what the block has");
 constexpr int kSub = kKv * 128;                   // 128 rows of 128 bytes: 128 e4m3 dims, or 64 f16 ones
 constexpr int kOperand = 2 * kSub;                // 128 x 128 f16, or both e4m3 terms
@@ -45,9 +45,8 @@ enum {
     kVEmpty = 10,    // [2] its products with the weights are done
     kQFull = 12,     // [tiles] queries of an item converted
     kSFull = 14,     // [tiles] scores of a step
-    kSFree = 16,     // [tiles] they are read
     kPFull = 18,     // [tiles] its weights
-    kOFull = 20,     // [tiles] the products of a step with its weights are done
+    kOFull = 20,     // [tiles] every product of an item is done
     kPages = 22,     // [2] a group of steps' pages are known
     kScales = 24,    // [2] and their scales
     kUsed = 26,      // [2] a group of steps is done
@@ -67,8 +66,7 @@ constexpr int kSmem = kOffLive + 2 * kMaxB + 1024;
 static_assert(kNumBars * 8 <= 320 && kOffRec % 16 == 0 && kOffStart % 8 == 0 && kOffScan % 8 == 0, "alignment");
 static_assert(kSmem <= 232448, "shared memory of a CTA");
 
-// Tensor memory: scores of one tile at a time, weights and outputs of each.
-constexpr int kColS = 0, kColP = 128, kColO = 256;
+constexpr int kColS = 0, kColO = kTiles * 128;    // tensor memory: scores (weights in their place), outputs
 
 // What the warps need to know of a step, sixteen written at a time.
 constexpr int kGroup = 16;
@@ -186,11 +184,11 @@ __device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[32])
         asm volatile("" : "+r"(r[i]));   // no use of a register moves before the wait
 }
 
-__device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t (&r)[32])
+__device__ __forceinline__ void tc_st16u(uint32_t taddr, const uint32_t (&r)[16])
 {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-                 "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-                 I8(r, 0), I8(r, 8), I8(r, 16), I8(r, 24)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+                 "%15, %16};" ::"r"(taddr),
+                 I8(r, 0), I8(r, 8)
                  : "memory");
 }
 
@@ -706,7 +704,7 @@ __device__ __forceinline__ void issue_pv(uint32_t base_s, uint32_t tmem, int t, 
     const uint32_t v_lo = desc_lo(base_s + kOffV + stage * kOperand, kSub);
 #pragma unroll
     for (int i = 0; i < kKv / 16; ++i)   // 16 tokens a product: two groups of eight rows
-        mma_ts(tmem + kColO + t * 128, tmem + kColP + t * 64 + i * 8, v_lo + i * (2048 >> 4), id, !first || i > 0);
+        mma_ts(tmem + kColO + t * 128, tmem + kColS + t * 128 + i * 8, v_lo + i * (2048 >> 4), id, !first || i > 0);
 }
 
 // S = Q K^T, Q in two e4m3 terms: 32 dims a product, the four of the second term last.
@@ -716,103 +714,68 @@ __device__ __forceinline__ void issue_qk(uint32_t base_s, uint32_t tmem, int t, 
     const uint32_t q_lo = desc_lo(base_s + kOffQ + t * kOperand, 16), k_lo = desc_lo(base_s + kOffK + stage * kSub, 16);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        mma_ss(tmem + kColS, q_lo + (((i >> 2) * kSub + (i & 3) * 32) >> 4), k_lo + (((i & 3) * 32) >> 4), id, i > 0);
+        mma_ss(tmem + kColS + t * 128, q_lo + (((i >> 2) * kSub + (i & 3) * 32) >> 4), k_lo + (((i & 3) * 32) >> 4), id, i > 0);
 }
 
-// The products are issued by two warps: issuing one takes until the one before has begun, so what a
-// warp waits for between them has to overlap with the other's.
-//
-// The first: scores of a step, tile by tile.  The softmax keeps scores in registers, so that the next ones go
-// to the same columns as soon as it has read them, before its weights are there.
-__device__ __forceinline__ void score_loop(uint8_t *base, uint32_t base_s, uint32_t tmem, int *status)
+// A warp a tile: its products of the step before with the weights, then its scores of a step, in their
+// place.  What one warp waits for overlaps with the other's products.
+__device__ __forceinline__ void mma_loop(uint8_t *base, uint32_t base_s, uint32_t tmem, int t, int *status)
 {
     const uint32_t bars = base_s + kOffBars;
-    uint32_t q_phase[kTiles] = {}, s_phase[kTiles] = {};
-    int reader = -1;   // the tile whose scores are in tensor memory
+    uint32_t q_phase = 0, p_phase = 0;
+    int before = 0;   // the flags of the step before
     bool ok = true;
 #pragma unroll 1
-    for (int f = 0; ok; ++f) {
+    for (int f = 0;; ++f) {
         ok = wait_step(bars, kPages, f) && wait_step(bars, kScales, f);   // the scales are read once the scores are there
-        const int flags = __shfl_sync(0xffffffffu, step_of(base, f)->flags, 0), stage = f % kKStages;
-        if (flags & kEnd)
-            break;
-        ok = ok && mbar_wait(bars + 8 * (kKFull + stage), (f / kKStages) & 1, kWaitNs);
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-            if (!(flags >> t & kActive))
-                continue;
-            if (flags & kBegins)
-                ok = ok && mbar_wait(bars + 8 * (kQFull + t), q_phase[t]++ & 1, kWaitNs);
-            if (reader == 0)
-                ok = ok && mbar_wait(bars + 8 * kSFree, s_phase[0]++ & 1, kWaitNs);
-            else if (reader == 1)
-                ok = ok && mbar_wait(bars + 8 * (kSFree + 1), s_phase[1]++ & 1, kWaitNs);
-            reader = t;
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok)
+        const int flags = __shfl_sync(0xffffffffu, step_of(base, f)->flags, 0), ks = f % kKStages, vs = (f - 1) & 1;
+        if (f > 0) {
+            // (a tile without rows that see the step waits all the same, so that it frees every stage once)
+            ok = ok && mbar_wait(bars + 8 * (kVFull + vs), ((f - 1) >> 1) & 1, kWaitNs);
+            const bool active = before >> t & kActive;
+            if (active)
+                ok = ok && mbar_wait(bars + 8 * (kPFull + t), p_phase++ & 1, kWaitNs);
+            if (!__all_sync(0xffffffffu, ok))
                 break;
             tc_fence_after();
             if (elect_one()) {
-                issue_qk(base_s, tmem, t, stage);
-                tc_commit(bars + 8 * (kSFull + t));
+                if (active)
+                    issue_pv(base_s, tmem, t, vs, (before & kBegins) != 0);
+                tc_commit(bars + 8 * (kVEmpty + vs));
+                if (before & kLast << t)
+                    tc_commit(bars + 8 * (kOFull + t));
+                // the weights of every step of the group before are there: its scales have been read
+                if (f % kGroup == 0)
+                    mbar_arrive(bars + 8 * (kUsed + ((f / kGroup - 1) & 1)));
             }
             __syncwarp();
         }
-        if (elect_one())
-            tc_commit(bars + 8 * (kKEmpty + stage));
+        if (flags & kEnd)
+            break;
+        ok = ok && mbar_wait(bars + 8 * (kKFull + ks), (f / kKStages) & 1, kWaitNs);
+        const bool active = flags >> t & kActive;
+        if (active && (flags & kBegins))
+            ok = ok && mbar_wait(bars + 8 * (kQFull + t), q_phase++ & 1, kWaitNs);
+        if (!__all_sync(0xffffffffu, ok))
+            break;
+        tc_fence_after();
+        if (elect_one()) {
+            if (active) {
+                issue_qk(base_s, tmem, t, ks);
+                tc_commit(bars + 8 * (kSFull + t));
+            }
+            tc_commit(bars + 8 * (kKEmpty + ks));
+        }
         __syncwarp();
+        before = flags;
     }
     if (!ok)
         report(status, SPARSE_ERR_TIMEOUT);
     // every product is done before the tensor memory is given back
     __syncwarp();
     if (elect_one())
-        tc_commit(bars + 8 * kDrain);
-    mbar_wait(bars + 8 * kDrain, 0, kWaitNs);
-}
-
-// The second: O += P V of a step, tile by tile.
-__device__ __forceinline__ void value_loop(uint8_t *base, uint32_t base_s, uint32_t tmem, int *status)
-{
-    const uint32_t bars = base_s + kOffBars;
-    uint32_t phase[kTiles] = {};
-    bool ok = true;
-#pragma unroll 1
-    for (int f = 0; ok; ++f) {
-        ok = wait_step(bars, kPages, f);
-        const int flags = __shfl_sync(0xffffffffu, step_of(base, f)->flags, 0), stage = f & 1;
-        if (flags & kEnd)
-            break;
-        ok = ok && mbar_wait(bars + 8 * (kVFull + stage), (f >> 1) & 1, kWaitNs);
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-            if (!(flags >> t & kActive))
-                continue;
-            ok = ok && mbar_wait(bars + 8 * (kPFull + t), phase[t]++ & 1, kWaitNs);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok)
-                break;
-            tc_fence_after();
-            if (elect_one()) {
-                issue_pv(base_s, tmem, t, stage, (flags & kBegins) != 0);
-                tc_commit(bars + 8 * (kOFull + t));
-            }
-            __syncwarp();
-        }
-        if (elect_one()) {
-            tc_commit(bars + 8 * (kVEmpty + stage));
-            // the weights of every step of the group are there: its scales have been read
-            if (f % kGroup == kGroup - 1)
-                mbar_arrive(bars + 8 * (kUsed + ((f / kGroup) & 1)));
-        }
-        __syncwarp();
-    }
-    if (!ok)
-        report(status, SPARSE_ERR_TIMEOUT);
-    __syncwarp();
-    if (elect_one())
-        tc_commit(bars + 8 * (kDrain + 1));
-    mbar_wait(bars + 8 * (kDrain + 1), 0, kWaitNs);
+        tc_commit(bars + 8 * (kDrain + t));
+    mbar_wait(bars + 8 * (kDrain + t), 0, kWaitNs);
 }
 
 // ---------------------------------------------------------------- softmax
@@ -962,13 +925,95 @@ __device__ __forceinline__ void rescale(uint32_t o_t, float alpha)
 }
 
 // One tile's softmax: a thread a row.
+// What a thread keeps of its row.  l is in units of 2^m; O in units of 2^mo, and so are the weights.
+struct Row {
+    float m, mo, l;
+};
+
+// Weights 2^(s sc + lf - m) of 32 columns, lf = log2 vs + m - mo, in f16 to tensor memory, and their part of l.  The
+// references m and mo are those of the item's first columns, and stay as long as no 32 weights add up to more than
+// kMost: no pass over the scores for their maximum.  Where they do (and where nothing was seen so far,
+// and in rows with NaN) m and mo become the maxima, and what is in their units is scaled: O, if the item has steps
+// behind it, and the `k` parts of this step's weights that are written.
+__device__ __forceinline__ void weigh(Row &r, uint32_t (&s)[32], uint32_t p_t, uint32_t o_t, int k, bool behind, float sc, float lv)
+{
+    bool over = r.m == -INFINITY || (r.mo == -INFINITY && lv > -INFINITY);
+#pragma unroll 1
+    for (int turn = 0;; ++turn) {
+        if (turn > 0) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                top = max3(top, __uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+            const float x = top == -INFINITY ? top : top * sc, y = top == -INFINITY ? top : x + lv;
+            float alpha = 1.f;
+            if (over && x > r.m) {
+                r.l *= ex2_approx(r.m - x);
+                r.m = x;
+            }
+            if (over && y > r.mo) {
+                alpha = ex2_approx(r.mo - y);
+                r.mo = y;
+            }
+            if (__any_sync(0xffffffffu, alpha != 1.f)) {
+                tc_wait_st();
+                if (behind)
+                    rescale(o_t, alpha);
+                for (int c = 0; c < k; ++c) {
+                    float w[16];
+                    tc_ld16(p_t + 16 * c, w);
+                    const __half2 a = __float2half2_rn(alpha);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const uint32_t u = __float_as_uint(w[i]);
+                        const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&u), a);
+                        w[i] = __uint_as_float(*reinterpret_cast<const uint32_t *>(&v));
+                    }
+                    tc_st16(p_t + 16 * c, w);
+                }
+            }
+        }
+        const float m_ref = r.m == -INFINITY ? 0.f : r.m;
+        // as long as no page counts for O its weights are in any units: they are scaled away with mo
+        const float lf = r.mo == -INFINITY ? 0.f : lv + (m_ref - r.mo), off = lf - m_ref;
+        const uint64_t sc2 = pair(sc, sc), off2 = pair(off, off);
+        uint64_t sum[2] = {0ull, 0ull};
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float2 e = unpair(fma2(pair(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sc2, off2));
+            e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+            sum[i & 1] = add2(sum[i & 1], pair(e.x, e.y));
+            w[i] = pack_f16x2(e.x, e.y);
+        }
+        const float2 e = unpair(add2(sum[0], sum[1]));
+        float add = e.x + e.y;
+        over = over || !(add <= kMost);
+        const bool far = !(fabsf(lf) <= kFarWeight);
+        if (__any_sync(0xffffffffu, far || (over && turn == 0))) {
+            if (turn == 0 && __any_sync(0xffffffffu, over))
+                continue;
+            if (__any_sync(0xffffffffu, far)) {   // l cannot be had from the weights of O
+                float p = 0.f;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    p += ex2_approx(fmaf(__uint_as_float(s[i]), sc, -m_ref));
+                r.l += far ? p : 0.f;
+                add = far ? 0.f : add;
+            }
+        }
+        tc_st16u(p_t + 16 * k, w);
+        r.l += far ? 0.f : add * ex2_approx(-lf);
+        break;
+    }
+}
+
 // One tile's softmax: a thread a row.
 __device__ __forceinline__ void softmax_loop(const ChunkParams &p, uint8_t *base, uint32_t base_s, uint32_t tmem, int t, int tid)
 {
     const uint32_t bars = base_s + kOffBars;
     const int warp = tid >> 5, lane = tid & 31;   // within the tile
-    const uint32_t s_t = tmem + kColS + (static_cast<uint32_t>(warp * 32) << 16);
-    const uint32_t p_t = tmem + kColP + t * 64 + (static_cast<uint32_t>(warp * 32) << 16);
+    const uint32_t s_t = tmem + kColS + t * 128 + (static_cast<uint32_t>(warp * 32) << 16);
     const uint32_t o_t = tmem + kColO + t * 128 + (static_cast<uint32_t>(warp * 32) << 16);
     const int tok_in = tid / p.G, g = tid - tok_in * p.G;
     Walk walk;
@@ -997,7 +1042,7 @@ __device__ __forceinline__ void softmax_loop(const ChunkParams &p, uint8_t *base
         const int end = min(it.j1, it.steps[t]);
         const int first_pos = it.pos + t * p.per_tile;
         const int pos = valid ? it.pos + tok : -1;
-        float m = -INFINITY, mo = -INFINITY, l = 0.f;
+        Row row = valid ? Row{-INFINITY, -INFINITY, 0.f} : Row{0.f, 0.f, 0.f};   // (rows past the tile's never wait for a first token)
         if (end > it.j0) {
             load_queries(p, it, t, base, base_s, warp, lane);
             fence_proxy_async_smem();
@@ -1012,110 +1057,35 @@ __device__ __forceinline__ void softmax_loop(const ChunkParams &p, uint8_t *base
             if (!ok)
                 break;
             tc_fence_after();
-            uint32_t s[4][32];   // the row's scores stay in registers
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                tc_ld32(s_t + 32 * k, s[k]);
+            // 32 columns at a time, the next ones on their way; O holds every step up to the one before, whose products
+            // were issued before these scores'
+            uint32_t x[32], y[32];
+            tc_ld32(s_t, x);
             const float4 rec = *reinterpret_cast<const float4 *>(step_of(base, f)->ks);   // there before the scores
             const bool masked = j * kKv + kKv - 1 > first_pos || rec.x < 0.f || rec.y < 0.f;
-            // a factor of zero (keys of zero) would make NaN of masked scores
-            const float sc[2] = {fmaxf(q_scale * rec.x, 0x1p-126f), fmaxf(q_scale * rec.y, 0x1p-126f)};
-            const float lv[2] = {rec.z, rec.w};
+            const int see = pos - j * kKv;   // columns up to this one
+            auto hide = [&](uint32_t(&v)[32], int k, float ks) {
+                const int lim = ks < 0.f ? -1 : see - 32 * k;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                tc_wait_ld(s[k]);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(bars + 8 * (kSFree + t));
-            if (masked) {
-                const int see = pos - j * kKv;   // columns up to this one
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int lim = (k < 2 ? rec.x : rec.y) < 0.f ? -1 : see - 32 * k;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        s[k][i] = i <= lim ? s[k][i] : 0xff800000u;   // -inf
-                }
+                for (int i = 0; i < 32; ++i)
+                    v[i] = i <= lim ? v[i] : 0xff800000u;   // -inf
+            };
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                const float ks = h ? rec.y : rec.x, lv = h ? rec.w : rec.z;
+                const float sc = fmaxf(q_scale * ks, 0x1p-126f);   // zero (keys of zero) would make NaN of masked scores
+                tc_wait_ld(x);
+                tc_ld32(s_t + 64 * h + 32, y);
+                if (masked)
+                    hide(x, 2 * h, ks);
+                weigh(row, x, s_t, o_t, 2 * h, j > it.j0, sc, lv);
+                tc_wait_ld(y);
+                if (h == 0)
+                    tc_ld32(s_t + 64, x);
+                if (masked)
+                    hide(y, 2 * h + 1, ks);
+                weigh(row, y, s_t, o_t, 2 * h + 1, j > it.j0, sc, lv);
             }
-            // The reference m is the maximum of the item's first step, and stays as long as no page's weights add up to
-            // more than kMost: only then (and in rows with NaN) is the maximum looked for and the step done again.
-            bool over = j == it.j0, again = over;
-            float add;
-            if (j > it.j0) {
-                // the products with the weights of the step before are done: O may be scaled, the weights written over
-                ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (kOFull + t), no++ & 1, kWaitNs));
-                if (!ok)
-                    break;
-                tc_fence_after();
-            }
-            for (int turn = 0;; ++turn) {
-                if (again) {
-                    float t_m = -INFINITY, t_o = -INFINITY;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            top[i & 3] = max3(top[i & 3], __uint_as_float(s[2 * h][i]), __uint_as_float(s[2 * h + 1][i]));
-                        const float x = fmaxf(max3(top[0], top[1], top[2]), top[3]) * sc[h];
-                        t_m = fmaxf(t_m, x);
-                        t_o = fmaxf(t_o, x == -INFINITY ? x : x + lv[h]);
-                    }
-                    if (over && t_m > m) {
-                        l *= ex2_approx(m - t_m);
-                        m = t_m;
-                    }
-                    const bool grow = over && t_o > mo;
-                    const float alpha = grow ? ex2_approx(mo - t_o) : 1.f;
-                    mo = grow ? t_o : mo;
-                    if (__any_sync(0xffffffffu, grow) && j > it.j0)
-                        rescale(o_t, alpha);
-                }
-                const float m_ref = m == -INFINITY ? 0.f : m;
-                float lf[2];
-                bool far = false;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    // as long as no page counts for O its weights are in any units: they are scaled away with mo
-                    lf[h] = mo == -INFINITY ? 0.f : lv[h] + (m_ref - mo);
-                    far = far || !(fabsf(lf[h]) <= kFarWeight);
-                }
-                far = __any_sync(0xffffffffu, far);
-                add = 0.f;
-                if (far) {   // l cannot be had from the weights of O
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            add += ex2_approx(fmaf(__uint_as_float(s[k][i]), sc[k >> 1], -m_ref));
-                }
-                over = far && !(add <= kMost);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float off = lf[h] - m_ref;
-                    const uint64_t sc2 = pair(sc[h], sc[h]), off2 = pair(off, off);
-                    uint64_t sum[2] = {0ull, 0ull};
-                    uint32_t w[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const uint32_t *x = &s[2 * h + (i >> 4)][2 * (i & 15)];
-                        float2 e = unpair(fma2(pair(__uint_as_float(x[0]), __uint_as_float(x[1])), sc2, off2));
-                        e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-                        sum[i & 1] = add2(sum[i & 1], pair(e.x, e.y));
-                        w[i] = pack_f16x2(e.x, e.y);
-                    }
-                    tc_st32(p_t + 32 * h, w);
-                    const float2 e = unpair(add2(sum[0], sum[1]));
-                    add += far ? 0.f : (e.x + e.y) * ex2_approx(-lf[h]);
-                    over = over || !(e.x + e.y <= kMost);   // NaN, too
-                }
-                again = turn == 0 && j > it.j0 && __any_sync(0xffffffffu, over);
-                if (!again)
-                    break;
-                tc_wait_st();   // before the weights are written over
-            }
-            l += add;
             tc_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -1132,6 +1102,7 @@ __device__ __forceinline__ void softmax_loop(const ChunkParams &p, uint8_t *base
         const bool whole = it.j0 == 0 && it.j1 == it.all;
         const int *first = reinterpret_cast<const int *>(base + kOffNan) + (items & 1) * kD;
         const bool nan = end > it.j0 && *(reinterpret_cast<const int *>(base + kOffNan) + 2 * kD + (items & 1)) != 0;
+        const float m = row.m, mo = row.mo, l = row.l;
         const Finish fin(m, l, mo);
         float *part = p.parts + static_cast<size_t>(2 * blockIdx.x + (it.j0 == 0 ? 1 : 0)) * kPartFloats;
         const int prow = t * kTileRows + tid;
@@ -1209,25 +1180,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(bars + 8 * (kVFull + i), kConvertWarps);
-            mbar_init(bars + 8 * (kVEmpty + i), 1);
+            mbar_init(bars + 8 * (kVEmpty + i), kTiles);
         }
         for (int t = 0; t < kTiles; ++t) {
             mbar_init(bars + 8 * (kQFull + t), 4);
             mbar_init(bars + 8 * (kSFull + t), 1);
             mbar_init(bars + 8 * (kPFull + t), 4);
             mbar_init(bars + 8 * (kOFull + t), 1);
-            mbar_init(bars + 8 * (kSFree + t), 4);
             mbar_init(bars + 8 * (kDone + 2 * t), 4);
             mbar_init(bars + 8 * (kDone + 2 * t + 1), 4);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bars + 8 * (kPages + i), 1);
             mbar_init(bars + 8 * (kScales + i), 1);
-            mbar_init(bars + 8 * (kUsed + i), 1);
+            mbar_init(bars + 8 * (kUsed + i), kTiles);
         }
         for (int i = 0; i < kKStages; ++i) {
             mbar_init(bars + 8 * (kKFull + i), 1);
-            mbar_init(bars + 8 * (kKEmpty + i), 1);
+            mbar_init(bars + 8 * (kKEmpty + i), kTiles);
         }
         mbar_init(bars + 8 * kReset, kConvertWarps);
         mbar_init(bars + 8 * kDrain, 1);
@@ -1250,10 +1220,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         convert_loop(p, base, base_s, tid - kConvertWarp * 32);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
-        if (warp == kMmaWarp)
-            score_loop(base, base_s, tmem, p.status);
-        else if (warp == kMmaWarp + 1)
-            value_loop(base, base_s, tmem, p.status);
+        if (warp < kMmaWarp + kTiles)
+            mma_loop(base, base_s, tmem, warp - kMmaWarp, p.status);
         else if (warp == kMmaWarp + 2)
             page_loop(p, base, base_s, tid & 31);
         else if (tid == (kMmaWarp + 3) * 32)
