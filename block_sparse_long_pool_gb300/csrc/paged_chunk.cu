@@ -44,16 +44,16 @@ enum {
     kVFull = 8,      // [2] values converted
     kVEmpty = 10,    // [2] its products with the weights are done
     kQFull = 12,     // [tiles] queries of an item converted
-    kSFull = 14,     // [tiles] scores of a step
-    kPFull = 18,     // [tiles] its weights
-    kOFull = 20,     // [tiles] every product of an item is done
-    kPages = 22,     // [2] a group of steps' pages are known
-    kScales = 24,    // [2] and their scales
-    kUsed = 26,      // [2] a group of steps is done
-    kDone = 28,      // [tiles][2] an item that the tile has steps of is finished; items in turn
-    kReset = 32,     // an item's words for NaN are reset
-    kDrain = 33,     // [2] every product is done
-    kNumBars = 35
+    kOFull = 14,     // [tiles][2] the products with the weights of a page are done
+    kSFull = 18,     // [tiles][2] scores of a page of a step
+    kPFull = 22,     // [tiles][2] its weights
+    kPages = 26,     // [2] a group of steps' pages are known
+    kScales = 28,    // [2] and their scales
+    kUsed = 30,      // [2] a group of steps is done
+    kDone = 32,      // [tiles][2] an item that the tile has steps of is finished; items in turn
+    kDrain = 36,     // [tiles] every product is done
+    kReset = 38,     // an item's words for NaN are reset
+    kNumBars = 39
 };
 constexpr int kOffRec = kOffBars + 320;           // Step [2][kGroup]
 constexpr int kOffCtrl = kOffRec + 2 * 16 * 32;   // int [16]
@@ -184,11 +184,11 @@ __device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[32])
         asm volatile("" : "+r"(r[i]));   // no use of a register moves before the wait
 }
 
-__device__ __forceinline__ void tc_st16u(uint32_t taddr, const uint32_t (&r)[16])
+__device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t (&r)[32])
 {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-                 "%15, %16};" ::"r"(taddr),
-                 I8(r, 0), I8(r, 8)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+                 "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+                 I8(r, 0), I8(r, 8), I8(r, 16), I8(r, 24)
                  : "memory");
 }
 
@@ -697,28 +697,29 @@ __device__ __forceinline__ void key_loop(const CUtensorMap *map, uint8_t *base, 
 
 // ---------------------------------------------------------------- products
 
-// O += P V of a step and a tile.
-__device__ __forceinline__ void issue_pv(uint32_t base_s, uint32_t tmem, int t, int stage, bool first)
+// O += P V of a page (h, of a step's two) and a tile.
+__device__ __forceinline__ void issue_pv(uint32_t base_s, uint32_t tmem, int t, int stage, int h, bool first)
 {
     constexpr uint32_t id = idesc(kTileRows, kD, 0, 1);   // weights; values as they are stored (dims contiguous)
-    const uint32_t v_lo = desc_lo(base_s + kOffV + stage * kOperand, kSub);
+    const uint32_t v_lo = desc_lo(base_s + kOffV + stage * kOperand + h * (kBlk * 128), kSub), p_t = tmem + kColS + t * 128 + h * kBlk;
 #pragma unroll
-    for (int i = 0; i < kKv / 16; ++i)   // 16 tokens a product: two groups of eight rows
-        mma_ts(tmem + kColO + t * 128, tmem + kColS + t * 128 + i * 8, v_lo + i * (2048 >> 4), id, !first || i > 0);
+    for (int i = 0; i < kBlk / 16; ++i)   // 16 tokens a product: two groups of eight rows
+        mma_ts(tmem + kColO + t * 128, p_t + i * 8, v_lo + i * (2048 >> 4), id, !first || i > 0);
 }
 
 // S = Q K^T, Q in two e4m3 terms: 32 dims a product, the four of the second term last.
-__device__ __forceinline__ void issue_qk(uint32_t base_s, uint32_t tmem, int t, int stage)
+__device__ __forceinline__ void issue_qk(uint32_t base_s, uint32_t tmem, int t, int stage, int h)
 {
-    constexpr uint32_t id = idesc(kTileRows, kKv, 0, 0);   // K-major queries and keys
-    const uint32_t q_lo = desc_lo(base_s + kOffQ + t * kOperand, 16), k_lo = desc_lo(base_s + kOffK + stage * kSub, 16);
+    constexpr uint32_t id = idesc(kTileRows, kBlk, 0, 0);   // K-major queries and keys
+    const uint32_t q_lo = desc_lo(base_s + kOffQ + t * kOperand, 16);
+    const uint32_t k_lo = desc_lo(base_s + kOffK + stage * kSub + h * (kBlk * 128), 16);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        mma_ss(tmem + kColS + t * 128, q_lo + (((i >> 2) * kSub + (i & 3) * 32) >> 4), k_lo + (((i & 3) * 32) >> 4), id, i > 0);
+        mma_ss(tmem + kColS + t * 128 + h * kBlk, q_lo + (((i >> 2) * kSub + (i & 3) * 32) >> 4), k_lo + (((i & 3) * 32) >> 4), id, i > 0);
 }
 
-// A warp a tile: its products of the step before with the weights, then its scores of a step, in their
-// place.  What one warp waits for overlaps with the other's products.
+// A warp a tile.  A tile's scores have room for two pages: after the products with a page's weights the scores
+// of the page after the next one go to their place, while the softmax works on the next one.
 __device__ __forceinline__ void mma_loop(uint8_t *base, uint32_t base_s, uint32_t tmem, int t, int *status)
 {
     const uint32_t bars = base_s + kOffBars;
@@ -729,45 +730,60 @@ __device__ __forceinline__ void mma_loop(uint8_t *base, uint32_t base_s, uint32_
     for (int f = 0;; ++f) {
         ok = wait_step(bars, kPages, f) && wait_step(bars, kScales, f);   // the scales are read once the scores are there
         const int flags = __shfl_sync(0xffffffffu, step_of(base, f)->flags, 0), ks = f % kKStages, vs = (f - 1) & 1;
-        if (f > 0) {
-            // (a tile without rows that see the step waits all the same, so that it frees every stage once)
+        // (a tile without rows that see a step waits all the same, so that it frees every stage once)
+        if (!(flags & kEnd))
+            ok = ok && mbar_wait(bars + 8 * (kKFull + ks), (f / kKStages) & 1, kWaitNs);
+        const bool now = flags >> t & kActive, begins = (flags & kBegins) != 0, was = before >> t & kActive;
+        if (f > 0)
             ok = ok && mbar_wait(bars + 8 * (kVFull + vs), ((f - 1) >> 1) & 1, kWaitNs);
-            const bool active = before >> t & kActive;
-            if (active)
-                ok = ok && mbar_wait(bars + 8 * (kPFull + t), p_phase++ & 1, kWaitNs);
-            if (!__all_sync(0xffffffffu, ok))
-                break;
-            tc_fence_after();
+        if (begins && !was && now)
+            ok = ok && mbar_wait(bars + 8 * (kQFull + t), q_phase++ & 1, kWaitNs);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            if (was) {
+                ok = ok && mbar_wait(bars + 8 * (kPFull + 2 * t + h), p_phase & 1, kWaitNs);
+                if (!__all_sync(0xffffffffu, ok))
+                    break;
+                tc_fence_after();
+            }
             if (elect_one()) {
-                if (active)
-                    issue_pv(base_s, tmem, t, vs, (before & kBegins) != 0);
-                tc_commit(bars + 8 * (kVEmpty + vs));
-                if (before & kLast << t)
-                    tc_commit(bars + 8 * (kOFull + t));
-                // the weights of every step of the group before are there: its scales have been read
-                if (f % kGroup == 0)
-                    mbar_arrive(bars + 8 * (kUsed + ((f / kGroup - 1) & 1)));
+                if (was) {
+                    issue_pv(base_s, tmem, t, vs, h, (before & kBegins) != 0 && h == 0);
+                    tc_commit(bars + 8 * (kOFull + 2 * t + h));
+                }
+                if (now && !begins) {
+                    issue_qk(base_s, tmem, t, ks, h);
+                    tc_commit(bars + 8 * (kSFull + 2 * t + h));
+                }
             }
             __syncwarp();
         }
-        if (flags & kEnd)
-            break;
-        ok = ok && mbar_wait(bars + 8 * (kKFull + ks), (f / kKStages) & 1, kWaitNs);
-        const bool active = flags >> t & kActive;
-        if (active && (flags & kBegins))
+        if (was)
+            ++p_phase;
+        if (begins && was && now)   // the next item's queries come after the last one's end
             ok = ok && mbar_wait(bars + 8 * (kQFull + t), q_phase++ & 1, kWaitNs);
         if (!__all_sync(0xffffffffu, ok))
             break;
         tc_fence_after();
         if (elect_one()) {
-            if (active) {
-                issue_qk(base_s, tmem, t, ks);
-                tc_commit(bars + 8 * (kSFull + t));
-            }
-            tc_commit(bars + 8 * (kKEmpty + ks));
+            if (now && begins)
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    issue_qk(base_s, tmem, t, ks, h);
+                    tc_commit(bars + 8 * (kSFull + 2 * t + h));
+                }
+            if (f > 0)
+                tc_commit(bars + 8 * (kVEmpty + vs));
+            if (!(flags & kEnd))
+                tc_commit(bars + 8 * (kKEmpty + ks));
+            // the weights of every step of the group before are there: its scales have been read
+            if (f > 0 && f % kGroup == 0)
+                mbar_arrive(bars + 8 * (kUsed + ((f / kGroup - 1) & 1)));
         }
         __syncwarp();
         before = flags;
+        if (flags & kEnd)
+            break;
     }
     if (!ok)
         report(status, SPARSE_ERR_TIMEOUT);
@@ -930,22 +946,24 @@ struct Row {
     float m, mo, l;
 };
 
-// Weights 2^(s sc + lf - m) of 32 columns, lf = log2 vs + m - mo, in f16 to tensor memory, and their part of l.  The
-// references m and mo are those of the item's first columns, and stay as long as no 32 weights add up to more than
-// kMost: no pass over the scores for their maximum.  Where they do (and where nothing was seen so far,
-// and in rows with NaN) m and mo become the maxima, and what is in their units is scaled: O, if the item has steps
-// behind it, and the `k` parts of this step's weights that are written.
-__device__ __forceinline__ void weigh(Row &r, uint32_t (&s)[32], uint32_t p_t, uint32_t o_t, int k, bool behind, float sc, float lv)
+// Weights 2^(s sc + lf - m) of a page's 64 columns, lf = log2 vs + m - mo, in f16 to tensor memory, and their part of l.
+// The references m and mo are those of the item's first page, and stay as long as no page's weights add up to more
+// than kMost: no pass over the scores for their maximum.  Where they do (and where nothing was seen so
+// far, and in rows with NaN) m and mo become the maxima, and what is in their units is scaled; `behind` waits
+// until the products with the weights before are done and says whether there were any.
+template <typename F>
+__device__ __forceinline__ void weigh(Row &r, uint32_t (&s)[2][32], uint32_t p_t, uint32_t o_t, float sc, float lv, F behind)
 {
     bool over = r.m == -INFINITY || (r.mo == -INFINITY && lv > -INFINITY);
 #pragma unroll 1
     for (int turn = 0;; ++turn) {
         if (turn > 0) {
-            float top = -INFINITY;
+            float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                top = max3(top, __uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
-            const float x = top == -INFINITY ? top : top * sc, y = top == -INFINITY ? top : x + lv;
+            for (int i = 0; i < 32; ++i)
+                top[i & 1] = max3(top[i & 1], __uint_as_float(s[0][i]), __uint_as_float(s[1][i]));
+            top[0] = fmaxf(top[0], top[1]);
+            const float x = top[0] == -INFINITY ? top[0] : top[0] * sc, y = top[0] == -INFINITY ? top[0] : x + lv;
             float alpha = 1.f;
             if (over && x > r.m) {
                 r.l *= ex2_approx(r.m - x);
@@ -955,38 +973,24 @@ __device__ __forceinline__ void weigh(Row &r, uint32_t (&s)[32], uint32_t p_t, u
                 alpha = ex2_approx(r.mo - y);
                 r.mo = y;
             }
-            if (__any_sync(0xffffffffu, alpha != 1.f)) {
-                tc_wait_st();
-                if (behind)
-                    rescale(o_t, alpha);
-                for (int c = 0; c < k; ++c) {
-                    float w[16];
-                    tc_ld16(p_t + 16 * c, w);
-                    const __half2 a = __float2half2_rn(alpha);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const uint32_t u = __float_as_uint(w[i]);
-                        const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&u), a);
-                        w[i] = __uint_as_float(*reinterpret_cast<const uint32_t *>(&v));
-                    }
-                    tc_st16(p_t + 16 * c, w);
-                }
-            }
+            if (__any_sync(0xffffffffu, alpha != 1.f) && behind())
+                rescale(o_t, alpha);
         }
         const float m_ref = r.m == -INFINITY ? 0.f : r.m;
         // as long as no page counts for O its weights are in any units: they are scaled away with mo
         const float lf = r.mo == -INFINITY ? 0.f : lv + (m_ref - r.mo), off = lf - m_ref;
         const uint64_t sc2 = pair(sc, sc), off2 = pair(off, off);
-        uint64_t sum[2] = {0ull, 0ull};
-        uint32_t w[16];
+        uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
+        uint32_t w[32];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float2 e = unpair(fma2(pair(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sc2, off2));
+        for (int i = 0; i < 32; ++i) {
+            const uint32_t *x = &s[i >> 4][2 * (i & 15)];
+            float2 e = unpair(fma2(pair(__uint_as_float(x[0]), __uint_as_float(x[1])), sc2, off2));
             e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-            sum[i & 1] = add2(sum[i & 1], pair(e.x, e.y));
+            sum[i & 3] = add2(sum[i & 3], pair(e.x, e.y));
             w[i] = pack_f16x2(e.x, e.y);
         }
-        const float2 e = unpair(add2(sum[0], sum[1]));
+        const float2 e = unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
         float add = e.x + e.y;
         over = over || !(add <= kMost);
         const bool far = !(fabsf(lf) <= kFarWeight);
@@ -996,13 +1000,13 @@ __device__ __forceinline__ void weigh(Row &r, uint32_t (&s)[32], uint32_t p_t, u
             if (__any_sync(0xffffffffu, far)) {   // l cannot be had from the weights of O
                 float p = 0.f;
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    p += ex2_approx(fmaf(__uint_as_float(s[i]), sc, -m_ref));
+                for (int i = 0; i < 64; ++i)
+                    p += ex2_approx(fmaf(__uint_as_float(s[i >> 5][i & 31]), sc, -m_ref));
                 r.l += far ? p : 0.f;
                 add = far ? 0.f : add;
             }
         }
-        tc_st16u(p_t + 16 * k, w);
+        tc_st32(p_t, w);
         r.l += far ? 0.f : add * ex2_approx(-lf);
         break;
     }
@@ -1019,7 +1023,7 @@ __device__ __forceinline__ void softmax_loop(const ChunkParams &p, uint8_t *base
     Walk walk;
     walk.open(p, reinterpret_cast<const Start *>(base + kOffStart), reinterpret_cast<const uint16_t *>(base + kOffLive));
     const float *qs = reinterpret_cast<const float *>(base + kOffQs) + t * kTileRows;
-    uint32_t ns = 0, no = 0;
+    uint32_t ns = 0;   // steps that the tile has had
     int fill = 0, items = 1;
     int4 tail = make_int4(-1, 0, 0, 0);
     int head = 0;
@@ -1053,47 +1057,50 @@ __device__ __forceinline__ void softmax_loop(const ChunkParams &p, uint8_t *base
         const float q_scale = qs[tid];   // written by this warp
         for (int j = it.j0; j < end && ok; ++j) {
             const int f = fill + j - it.j0;
-            ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (kSFull + t), ns++ & 1, kWaitNs));
-            if (!ok)
-                break;
-            tc_fence_after();
-            // 32 columns at a time, the next ones on their way; O holds every step up to the one before, whose products
-            // were issued before these scores'
-            uint32_t x[32], y[32];
-            tc_ld32(s_t, x);
-            const float4 rec = *reinterpret_cast<const float4 *>(step_of(base, f)->ks);   // there before the scores
-            const bool masked = j * kKv + kKv - 1 > first_pos || rec.x < 0.f || rec.y < 0.f;
-            const int see = pos - j * kKv;   // columns up to this one
-            auto hide = [&](uint32_t(&v)[32], int k, float ks) {
-                const int lim = ks < 0.f ? -1 : see - 32 * k;
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    v[i] = i <= lim ? v[i] : 0xff800000u;   // -inf
-            };
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
-                const float ks = h ? rec.y : rec.x, lv = h ? rec.w : rec.z;
+                ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (kSFull + 2 * t + h), ns & 1, kWaitNs));
+                if (!ok)
+                    break;
+                tc_fence_after();
+                uint32_t x[2][32];
+                tc_ld32(s_t + kBlk * h, x[0]);
+                tc_ld32(s_t + kBlk * h + 32, x[1]);
+                const Step *step = step_of(base, f);   // there before the scores
+                const float ks = step->ks[h], lv = step->log2_vs[h];
                 const float sc = fmaxf(q_scale * ks, 0x1p-126f);   // zero (keys of zero) would make NaN of masked scores
-                tc_wait_ld(x);
-                tc_ld32(s_t + 64 * h + 32, y);
-                if (masked)
-                    hide(x, 2 * h, ks);
-                weigh(row, x, s_t, o_t, 2 * h, j > it.j0, sc, lv);
-                tc_wait_ld(y);
-                if (h == 0)
-                    tc_ld32(s_t + 64, x);
-                if (masked)
-                    hide(y, 2 * h + 1, ks);
-                weigh(row, y, s_t, o_t, 2 * h + 1, j > it.j0, sc, lv);
+                const bool masked = j * kKv + h * kBlk + kBlk - 1 > first_pos || ks < 0.f;
+                tc_wait_ld(x[0]);
+                tc_wait_ld(x[1]);
+                if (masked) {
+                    const int lim = ks < 0.f ? -1 : pos - j * kKv - h * kBlk;   // columns up to this one
+#pragma unroll
+                    for (int i = 0; i < 64; ++i)
+                        x[i >> 5][i & 31] = i <= lim ? x[i >> 5][i & 31] : 0xff800000u;   // -inf
+                }
+                // the products with the weights of the page before may be left; those before are done, since these scores
+                // were issued after them
+                weigh(row, x, s_t + kBlk * h, o_t, sc, lv, [&]() {
+                    if (j == it.j0 && h == 0)
+                        return false;
+                    ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (kOFull + 2 * t + (h ^ 1)), (ns - (h ^ 1)) & 1, kWaitNs));
+                    tc_fence_after();
+                    return ok;
+                });
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bars + 8 * (kPFull + 2 * t + h));
+                if (!ok)
+                    break;
             }
-            tc_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(bars + 8 * (kPFull + t));
+            ++ns;
         }
         if (ok && end > it.j0) {
-            ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (kOFull + t), no++ & 1, kWaitNs));
+            ok = mbar_wait(bars + 8 * (kOFull + 2 * t), (ns - 1) & 1, kWaitNs) &&
+                 mbar_wait(bars + 8 * (kOFull + 2 * t + 1), (ns - 1) & 1, kWaitNs);
+            ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
         }
         if (!ok)
@@ -1184,9 +1191,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         }
         for (int t = 0; t < kTiles; ++t) {
             mbar_init(bars + 8 * (kQFull + t), 4);
-            mbar_init(bars + 8 * (kSFull + t), 1);
-            mbar_init(bars + 8 * (kPFull + t), 4);
-            mbar_init(bars + 8 * (kOFull + t), 1);
+            mbar_init(bars + 8 * (kSFull + 2 * t), 1);
+            mbar_init(bars + 8 * (kSFull + 2 * t + 1), 1);
+            mbar_init(bars + 8 * (kPFull + 2 * t), 4);
+            mbar_init(bars + 8 * (kPFull + 2 * t + 1), 4);
+            mbar_init(bars + 8 * (kOFull + 2 * t), 1);
+            mbar_init(bars + 8 * (kOFull + 2 * t + 1), 1);
             mbar_init(bars + 8 * (kDone + 2 * t), 4);
             mbar_init(bars + 8 * (kDone + 2 * t + 1), 4);
         }
