@@ -117,6 +117,7 @@ struct ChunkParams {
     int H_kv;
     int G;
     int per_tile;      // tokens of a tile
+    int recip;         // 2^16 / G, up: row * recip >> 16 = row / G for the rows of a tile
 };
 
 // One partial state: O [256][128], then m, l, mo [256].
@@ -197,10 +198,61 @@ __device__ __forceinline__ void tc_wait_st()
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// Two f16 values to e4m3, round to nearest even, beyond +-448 to +-448, NaN to NaN.
+__device__ __forceinline__ uint32_t f16x2_to_f8x2(uint32_t x)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+    return r;
+}
+
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
 {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Two fp32 values an instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ float2 unpair(uint64_t x)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 
@@ -498,6 +550,12 @@ __device__ __forceinline__ void page_loop(const ChunkParams &p, uint8_t *base, u
                 j = it.j0;
                 ++items;
                 f = kBegins;
+                // its queries on the way to L2, 256 bytes a row
+                for (int r = lane; r < it.n * p.G; r += 32) {
+                    const int tok = r / p.G, g = r - tok * p.G;
+                    const uint16_t *q = p.Q + (it.row + tok) * p.q_stride + static_cast<size_t>(it.head * p.G + g) * kD;
+                    asm volatile("prefetch.global.L2 [%0];\n\tprefetch.global.L2 [%0 + 128];" ::"l"(q));
+                }
             }
             if (lane >> 1 == s) {
                 const long long cap = static_cast<long long>(p.max_blocks) * kBlk;
@@ -800,64 +858,51 @@ __device__ __forceinline__ void mma_loop(uint8_t *base, uint32_t base_s, uint32_
 // leaves its largest element within 448.  bf16 has 8 bits and a term 4, so that the two hold elements
 // down to 2^-11 of the row's largest exactly and those below within 2^-19 of it (half of e4m3's
 // least step, 2^-10, of 2^8 and more; where the largest is past 1.75 times its power of two, of 2^7: 2^-10, 2^-18).
-// Two rows a warp at a time; rows past the tile's are zero, and those with an infinity are NaN.
+// (In f16 between: it holds bf16's 8 bits down to 2^-17, far below e4m3's least step.)  Two rows a warp at a time;
+// rows past the tile's are zero, and all of a row that is not finite is NaN.
 __device__ __forceinline__ void load_queries(const ChunkParams &p, const Item &it, int t, uint8_t *base, uint32_t base_s, int warp,
                                              int lane)
 {
     float *qs = reinterpret_cast<float *>(base + kOffQs) + t * kTileRows;
-    const int c = lane & 15;
+    const int c = lane & 15, row0 = warp * 32 + (lane >> 4);
     const int n = min(p.per_tile, it.n - t * p.per_tile) * p.G;
-#pragma unroll 1
-    for (int i0 = 0; i0 < 16; i0 += 8) {
-        uint4 x[8];
+    const uint16_t *first = p.Q + static_cast<size_t>(it.head * p.G) * kD + c * 8;
+    const long long tok0 = it.row + t * p.per_tile;
+    uint4 x[16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int row = warp * 32 + (i0 + i) * 2 + (lane >> 4);
-            x[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (row < n) {
-                const int tok = row / p.G, g = row - tok * p.G;
-                x[i] = *reinterpret_cast<const uint4 *>(p.Q + (it.row + t * p.per_tile + tok) * p.q_stride +
-                                                        static_cast<size_t>(it.head * p.G + g) * kD + c * 8);
-            }
+    for (int i = 0; i < 16; ++i) {
+        const int row = row0 + 2 * i, tok = row * p.recip >> 16, g = row - tok * p.G;
+        x[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (row < n)
+            x[i] = *reinterpret_cast<const uint4 *>(first + (tok0 + tok) * p.q_stride + g * kD);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int row = row0 + 2 * i;
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        // the largest element's bits: positive bf16 are in the order of their bits, infinities and NaN the largest
+        uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1)
+            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = max(top & 0xffffu, top >> 16);
+        const int e = static_cast<int>(top >> 7) - 127;   // the largest is 2^e times 1 to 2
+        const int up = top > 0u ? max(-120, min(126, ((top & 0x7fu) <= 0x60u ? 8 : 7) - e)) : 0;
+        const float f = top >= 0x7f80u ? NAN : __uint_as_float(static_cast<uint32_t>(up + 127) << 23 | p.q_sign);
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t v = pack_f16x2(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
+            hi[k] = f16x2_to_f8x2(v);
+            const uint32_t back = f8x2_to_f16x2(hi[k]);
+            const __half2 rest = __hsub2(*reinterpret_cast<const __half2 *>(&v), *reinterpret_cast<const __half2 *>(&back));
+            lo[k] = f16x2_to_f8x2(*reinterpret_cast<const uint32_t *>(&rest));
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int row = warp * 32 + (i0 + i) * 2 + (lane >> 4);
-            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-            float v[8];
-            float top = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                v[2 * k] = __uint_as_float(w[k] << 16);
-                v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const bool finite = fabsf(v[k]) <= 0x1.fep127f;
-                top = fmaxf(top, finite ? fabsf(v[k]) : 0.f);
-                v[k] = finite ? v[k] : NAN;
-            }
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1)
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const uint32_t bits = __float_as_uint(top);
-            const int e = static_cast<int>(bits >> 23) - 127;   // top = 2^e times 1 to 2
-            const int up = top > 0.f ? max(-120, min(126, ((bits & 0x7fffffu) <= 0x600000u ? 8 : 7) - e)) : 0;
-            const float f = __uint_as_float(static_cast<uint32_t>(up + 127) << 23 | p.q_sign);
-            uint32_t hi[2], lo[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float a = v[4 * k] * f, b = v[4 * k + 1] * f, d = v[4 * k + 2] * f, g = v[4 * k + 3] * f;
-                hi[k] = f8x4_pack(a, b, d, g);
-                const float2 ab = f8x2_to_float2(hi[k]), dg = f8x2_to_float2(hi[k] >> 16);
-                lo[k] = f8x4_pack(a - ab.x, b - ab.y, d - dg.x, g - dg.y);
-            }
-            const uint32_t at = base_s + kOffQ + t * kOperand + row * 128 + (((c >> 1) ^ (row & 7)) << 4) + (c & 1) * 8;
-            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0]), "r"(hi[1]) : "memory");
-            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + kSub), "r"(lo[0]), "r"(lo[1]) : "memory");
-            if (c == 0)
-                qs[row] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
-        }
+        const uint32_t at = base_s + kOffQ + t * kOperand + row * 128 + (((c >> 1) ^ (row & 7)) << 4) + (c & 1) * 8;
+        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0] | hi[1] << 16), "r"(hi[2] | hi[3] << 16) : "memory");
+        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + kSub), "r"(lo[0] | lo[1] << 16), "r"(lo[2] | lo[3] << 16) : "memory");
+        if (c == 0)
+            qs[row] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
     }
 }
 
@@ -883,47 +928,18 @@ struct Finish {
             half = rest = l;
     }
     __device__ __forceinline__ float operator()(float o) const { return o * half * rest; }
+    // Two values, in place: fp32 in `a` and `b`.
+    __device__ __forceinline__ void operator()(float &a, float &b) const
+    {
+        const float2 r = unpair(mul2(mul2(pair(a, b), pair(half, half)), pair(rest, rest)));
+        a = r.x;
+        b = r.y;
+    }
 };
 
 __device__ __forceinline__ float lse_of(float m, float l)
 {
     return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309417f;
-}
-
-// Two fp32 values an instruction.
-__device__ __forceinline__ uint64_t pair(float a, float b)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-
-__device__ __forceinline__ float2 unpair(uint64_t x)
-{
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-    return r;
-}
-
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c)
-{
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
 }
 
 // O of a row times alpha.
@@ -1136,8 +1152,8 @@ __device__ __forceinline__ void softmax_loop(const ChunkParams &p, uint8_t *base
             }
             if (valid && whole) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    v[i] = fin(v[i]);
+                for (int i = 0; i < 32; i += 2)
+                    fin(v[i], v[i + 1]);
                 store_bf16(p.O + out * kD + 32 * k, v);
             } else if (valid) {
 #pragma unroll
@@ -1398,6 +1414,7 @@ extern "C" SPARSE_API int sparse_paged_chunk_attn_f8(const uint16_t *Q, long lon
     p.H_kv = H_kv;
     p.G = H_q / H_kv;
     p.per_tile = per_tile;
+    p.recip = (65536 + p.G - 1) / p.G;
     rc = sp_host::cuda_status(launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), kThreads, kSmem, stream, map, p), name);
     if (rc != SPARSE_OK)
         return rc;
