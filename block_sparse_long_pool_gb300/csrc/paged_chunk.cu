@@ -16,9 +16,9 @@ constexpr int kMaxB = 4096;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kMost = 0x1p15f;                  // of 32 weights, in f16: beyond it the row's reference is taken anew
 constexpr float kFarWeight = 60.f;                // log2 of the largest factor from a page's weights to O's
-constexpr int kItemCost = 320;                    // what an item costs beside its tokens, in tokens of one step
-constexpr int kMinWork = 1024;                    // the least share of a CTA, in the same units
-constexpr int kMinCut = 2;                        // steps on either side of a cut through an item
+constexpr int kItemCost = 704;                    // what an item costs beside its tokens, in tokens of one step
+constexpr int kMinWork = 640;                     // the least share of a CTA, in the same units
+constexpr int kMinCut = 1;                        // steps on either side of a cut through an item
 
 constexpr int kSoftmaxWarps = 4 * kTiles;
 constexpr int kConvertWarp = kSoftmaxWarps;       // the first of them
@@ -868,41 +868,51 @@ __device__ __forceinline__ void load_queries(const ChunkParams &p, const Item &i
     const int n = min(p.per_tile, it.n - t * p.per_tile) * p.G;
     const uint16_t *first = p.Q + static_cast<size_t>(it.head * p.G) * kD + c * 8;
     const long long tok0 = it.row + t * p.per_tile;
-    uint4 x[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    auto load = [&](int i) {
         const int row = row0 + 2 * i, tok = row * p.recip >> 16, g = row - tok * p.G;
-        x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (row < n)
-            x[i] = *reinterpret_cast<const uint4 *>(first + (tok0 + tok) * p.q_stride + g * kD);
-    }
+        return row < n ? *reinterpret_cast<const uint4 *>(first + (tok0 + tok) * p.q_stride + g * kD) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    // four at a time, the next four on their way (all sixteen in one piece of code miss the instruction cache)
+    constexpr int kAtOnce = 4;
+    uint4 x[kAtOnce], y[kAtOnce];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int row = row0 + 2 * i;
-        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        // the largest element's bits: positive bf16 are in the order of their bits, infinities and NaN the largest
-        uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+    for (int i = 0; i < kAtOnce; ++i)
+        y[i] = load(i);
+#pragma unroll 1
+    for (int i0 = 0; i0 < 16; i0 += kAtOnce) {
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1)
-            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
-        top = max(top & 0xffffu, top >> 16);
-        const int e = static_cast<int>(top >> 7) - 127;   // the largest is 2^e times 1 to 2
-        const int up = top > 0u ? max(-120, min(126, ((top & 0x7fu) <= 0x60u ? 8 : 7) - e)) : 0;
-        const float f = top >= 0x7f80u ? NAN : __uint_as_float(static_cast<uint32_t>(up + 127) << 23 | p.q_sign);
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t v = pack_f16x2(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
-            hi[k] = f16x2_to_f8x2(v);
-            const uint32_t back = f8x2_to_f16x2(hi[k]);
-            const __half2 rest = __hsub2(*reinterpret_cast<const __half2 *>(&v), *reinterpret_cast<const __half2 *>(&back));
-            lo[k] = f16x2_to_f8x2(*reinterpret_cast<const uint32_t *>(&rest));
+        for (int i = 0; i < kAtOnce; ++i) {
+            x[i] = y[i];
+            y[i] = load(min(i0 + kAtOnce, 15) + i);
         }
-        const uint32_t at = base_s + kOffQ + t * kOperand + row * 128 + (((c >> 1) ^ (row & 7)) << 4) + (c & 1) * 8;
-        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0] | hi[1] << 16), "r"(hi[2] | hi[3] << 16) : "memory");
-        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + kSub), "r"(lo[0] | lo[1] << 16), "r"(lo[2] | lo[3] << 16) : "memory");
-        if (c == 0)
-            qs[row] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int row = row0 + 2 * (i0 + i);
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            // the largest element's bits: positive bf16 are in the order of their bits, infinities and NaN the largest
+            uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1)
+                top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+            top = max(top & 0xffffu, top >> 16);
+            const int e = static_cast<int>(top >> 7) - 127;   // the largest is 2^e times 1 to 2
+            const int up = top > 0u ? max(-120, min(126, ((top & 0x7fu) <= 0x60u ? 8 : 7) - e)) : 0;
+            const float f = top >= 0x7f80u ? NAN : __uint_as_float(static_cast<uint32_t>(up + 127) << 23 | p.q_sign);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t v = pack_f16x2(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
+                hi[k] = f16x2_to_f8x2(v);
+                const uint32_t back = f8x2_to_f16x2(hi[k]);
+                const __half2 rest = __hsub2(*reinterpret_cast<const __half2 *>(&v), *reinterpret_cast<const __half2 *>(&back));
+                lo[k] = f16x2_to_f8x2(*reinterpret_cast<const uint32_t *>(&rest));
+            }
+            const uint32_t at = base_s + kOffQ + t * kOperand + row * 128 + (((c >> 1) ^ (row & 7)) << 4) + (c & 1) * 8;
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0] | hi[1] << 16), "r"(hi[2] | hi[3] << 16) : "memory");
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + kSub), "r"(lo[0] | lo[1] << 16), "r"(lo[2] | lo[3] << 16) : "memory");
+            if (c == 0)
+                qs[row] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+        }
     }
 }
 

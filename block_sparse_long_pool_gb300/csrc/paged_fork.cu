@@ -1,14 +1,14 @@
 // paged_fork.cu -- requests that share pages: forks and ends, and the copies that a fork needs.
 //
-// Fork.  One cluster.  Pages stay at one block index in every request that holds them (a fork
-// takes its source's first blocks), so whether a page loses its last holder is found in one column of
-// the block table: its holders among the requests that end, counted and compared with the count
-// of holders beyond the first.  That needs no atomic whose order matters; the last holder in
-// request order puts the page onto the free list, so the list's order does not depend on timing.
-//   1. every warp takes an equal run of the ending requests' 32-block pieces, in order, decides which
-//      pages are freed and keeps that in a bit mask;
-//   2. (cluster barrier) freed pages to their places on the list by a prefix sum, counts lowered;
-//   3. (cluster barrier) forks: table entries, counts raised, fresh pages from the list's end.
+// Fork.  One cluster, each warp with an equal run of the ending requests' 32-block pieces, in order.
+//   1. A page without further holders is freed: its bit is set in a mask.
+//   2. Where there are others (in a step of their own, if the call meets any): every request that ends
+//      takes one off the count; where the count falls below zero all its holders end, and the last of them
+//      in request order, found by an atomic minimum of the count's place, frees the page.  So the list's
+//      order does not depend on timing.
+//   3. Freed pages go to their places on the list by a prefix sum.
+//   4. Forks: table entries, counts raised, fresh pages from the list's end.
+// Cluster barriers stand between the steps.
 // Copy.  Pieces of 16 KB of page pairs and of compressed keys, 4 loads of 16 bytes a thread
 // before the first store, over as many CTAs as the GPU holds.
 #include <limits.h>
@@ -24,6 +24,7 @@ constexpr int kForkThreads = 1024;
 constexpr int kForkWarps = kForkThreads / 32;
 constexpr int kForkCluster = 8;
 constexpr int kForkB = 4096;
+constexpr int kHolder = -(1 << 30);   // a count's place, less b: request b is its page's last holder, and ends
 
 // The unsound input is reported where a refusal has been, too.
 __device__ __forceinline__ void report_unsound(int *status)
@@ -35,8 +36,9 @@ __device__ __forceinline__ void report_unsound(int *status)
 struct ForkParams {
     const int *src, *fork_len;
     int *seq_len, *table, *extra, *free_pages, *n_free, *copy_src, *copy_dst;
-    int *warp_count;     // [kForkCluster * kForkWarps]
-    uint32_t *freed;     // [B * ceil(max_blocks / 32)]
+    int *warp_count;     // [2 * kForkCluster * kForkWarps]: pages that a warp frees, and those with other holders
+    uint32_t *freed;     // [B * ceil(max_blocks / 32)] masks: pages that a piece frees
+    uint32_t *shared;    // the same: pages with other holders
     int *status;
     int B, max_blocks, n_pages;
 };
@@ -91,7 +93,6 @@ __global__ void __launch_bounds__(kForkThreads, 1) page_fork_kernel(const __grid
     int *from = fork_smem;              // [B] the request that b becomes a copy of (b: it stays, -1: it ends)
     int *len = from + p.B;              // [B] tokens
     int *first = len + p.B;             // [B + 1] the first piece of b
-    int *ends = first + p.B + 1;        // [B] the requests that give up their pages
     __shared__ int warp_sums[kForkWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = p.B;
     const int rank = static_cast<int>(cluster_ctarank()), ctas = static_cast<int>(cluster_nctarank());
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(kForkThreads, 1) page_fork_kernel(const __grid
     griddep_launch_dependents();
     const int per = (B + kForkThreads - 1) / kForkThreads, b0 = min(B, tid * per), b1 = min(B, b0 + per);
 
-    int pieces = 0, n_ends = 0;
+    int pieces = 0;
     for (int b = b0; b < b1; ++b) {
         int s = p.src[b], n = p.seq_len[b];
         bool bad = n < 0 || static_cast<long long>(n) > static_cast<long long>(p.max_blocks) * kBlk;
@@ -118,58 +119,82 @@ __global__ void __launch_bounds__(kForkThreads, 1) page_fork_kernel(const __grid
         const int nb = s == b ? 0 : blocks_of(max(n, 0));
         first[b] = nb;   // blocks, for now
         pieces += (nb + 31) / 32;
-        n_ends += nb > 0;
     }
-    int at = pieces, at_end = n_ends;
+    int at = pieces;
     const int total = block_scan(at, warp_sums);
-    const int all_ends = block_scan(at_end, warp_sums);
     for (int b = b0; b < b1; ++b) {
         const int nb = first[b];
         first[b] = at;
         at += (nb + 31) / 32;
-        if (nb > 0)
-            ends[at_end++] = b;
     }
     if (tid == 0)
         first[B] = total;
     __syncthreads();
 
-    // 1. which pages are freed
+    // The pieces of this warp: `body` with the request, the block and the page of each lane (-1: none).
     const int run = (total + warps - 1) / warps, i0 = min(total, me * run), i1 = min(total, i0 + run);
-    int count = 0;
-    int b = i0 < i1 ? find(first, B, i0) : 0;
-    for (int i = i0; i < i1; ++i) {
-        while (first[b + 1] <= i)
-            ++b;
-        const int j = (i - first[b]) * 32 + lane;
-        const bool here = j < blocks_of(len[b]);
-        const int page = here ? p.table[static_cast<size_t>(b) * p.max_blocks + j] : -1;
-        const bool ok = page >= 0 && page < p.n_pages;
-        const int extra = ok ? max(0, p.extra[page]) : 0;
-        int holders = 1, last = b;
-        if (__any_sync(0xffffffffu, extra > 0)) {
-            holders = 0;
-            for (int e = 0; e < all_ends; ++e) {
-                const int o = ends[e];
-                if (j < blocks_of(len[o]) && p.table[static_cast<size_t>(o) * p.max_blocks + j] == page) {
-                    ++holders;
-                    last = o;
-                }
-            }
+    auto pages = [&](auto body) {
+        int b = i0 < i1 ? find(first, B, i0) : 0;
+        for (int i = i0; i < i1; ++i) {
+            while (first[b + 1] <= i)
+                ++b;
+            const int j = (i - first[b]) * 32 + lane;
+            body(i, b, j < blocks_of(len[b]) ? p.table[static_cast<size_t>(b) * p.max_blocks + j] : -1, j < blocks_of(len[b]));
         }
-        const bool freed = ok && (extra == 0 || (holders > extra && last == b));
-        if ((here && !ok) || (ok && extra > 0 && holders > extra + 1))
+    };
+    // 1. pages without other holders
+    int count = 0, others = 0;
+    pages([&](int i, int, int page, bool here) {
+        const bool ok = page >= 0 && page < p.n_pages;
+        if (here && !ok)
             report_unsound(p.status);
-        const uint32_t mask = __ballot_sync(0xffffffffu, freed);
-        if (lane == 0)
+        const bool more = ok && p.extra[page] > 0;
+        const uint32_t mask = __ballot_sync(0xffffffffu, ok && !more), shared = __ballot_sync(0xffffffffu, more);
+        if (lane == 0) {
             p.freed[i] = mask;
+            p.shared[i] = shared;
+        }
         count += __popc(mask);
-    }
-    if (lane == 0)
+        others += __popc(shared);
+    });
+    if (lane == 0) {
         p.warp_count[me] = count;
+        p.warp_count[warps + me] = others;
+    }
     cluster_sync();
 
-    // 2. onto the free list, and one holder less
+    // 2. those with others: the count's place takes the last holder where all of them end
+    int any = tid < warps ? __ldcg(p.warp_count + warps + tid) : 0;
+    if (block_scan(any, warp_sums) > 0) {
+        pages([&](int i, int, int page, bool) {
+            if (p.shared[i] >> lane & 1u)   // written by this warp
+                atomicSub(p.extra + page, 1);
+        });
+        cluster_sync();
+        pages([&](int i, int b, int page, bool) {
+            if (p.shared[i] >> lane & 1u) {
+                const int left = __ldcg(p.extra + page);
+                if (left < 0) {
+                    if (left < -1 && left > kHolder)
+                        report_unsound(p.status);   // more holders than counted
+                    atomicMin(p.extra + page, kHolder - b);
+                }
+            }
+        });
+        cluster_sync();
+        pages([&](int i, int b, int page, bool) {
+            const uint32_t shared = p.shared[i];
+            const uint32_t mask = __ballot_sync(0xffffffffu, (shared >> lane & 1u) && __ldcg(p.extra + page) == kHolder - b);
+            if (lane == 0)
+                p.freed[i] |= mask;
+            count += __popc(mask);
+        });
+        if (lane == 0)
+            p.warp_count[me] = count;
+        cluster_sync();
+    }
+
+    // 3. onto the free list
     int before = tid < warps ? __ldcg(p.warp_count + tid) : 0;
     const int back = block_scan(before, warp_sums);
     __shared__ int warp_first[kForkCluster * kForkWarps];
@@ -180,25 +205,20 @@ __global__ void __launch_bounds__(kForkThreads, 1) page_fork_kernel(const __grid
     if (rank == 0 && tid == 0 && (listed != held || static_cast<long long>(held) + back > p.n_pages))
         report_unsound(p.status);
     int place = min(held + min(warp_first[me], p.n_pages), p.n_pages);
-    b = i0 < i1 ? find(first, B, i0) : 0;
-    for (int i = i0; i < i1; ++i) {
-        while (first[b + 1] <= i)
-            ++b;
-        const int j = (i - first[b]) * 32 + lane;
-        const int page = j < blocks_of(len[b]) ? p.table[static_cast<size_t>(b) * p.max_blocks + j] : -1;
-        const uint32_t mask = p.freed[i];   // written by this warp
+    pages([&](int i, int, int page, bool) {
+        __syncwarp();   // lane 0's masks
+        const uint32_t mask = p.freed[i];
         const int mine = place + __popc(mask & ((1u << lane) - 1u));
-        if ((mask >> lane) & 1u) {
+        if (mask >> lane & 1u) {
             if (mine < p.n_pages)
                 p.free_pages[mine] = page;
-        } else if (page >= 0 && page < p.n_pages) {
-            atomicSub(p.extra + page, 1);
+            p.extra[page] = 0;
         }
         place = min(place + __popc(mask), p.n_pages);
-    }
+    });
     cluster_sync();
 
-    // 3. forks: those that need a page get one in request order, from the end of the list
+    // 4. forks: those that need a page get one in request order, from the end of the list
     const int have = min(held + min(back, p.n_pages), p.n_pages);
     int need = 0, share = 0;
     for (int x = b0; x < b1; ++x) {
@@ -255,7 +275,7 @@ __global__ void __launch_bounds__(kForkThreads, 1) page_fork_kernel(const __grid
         first[B] = all;
     __syncthreads();
     for (int i = me; i < all; i += warps) {
-        b = find(first, B, i);
+        int b = find(first, B, i);
         while (first[b + 1] <= i)
             ++b;
         const int j = (i - first[b]) * 32 + lane;
@@ -379,7 +399,7 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) paged_copy_kernel(con
 
 size_t fork_words(int B, int max_blocks)
 {
-    return kForkCluster * kForkWarps + static_cast<size_t>(B) * ((static_cast<size_t>(max_blocks) + 31) / 32);
+    return 2 * (kForkCluster * kForkWarps + static_cast<size_t>(B) * ((static_cast<size_t>(max_blocks) + 31) / 32));
 }
 
 }  // namespace
@@ -418,13 +438,14 @@ extern "C" SPARSE_API int sparse_page_fork(const int *src, const int *fork_len, 
     if (rc != SPARSE_OK)
         return rc;
     const void *kern = reinterpret_cast<const void *>(page_fork_kernel);
-    const int smem = (4 * B + 1) * static_cast<int>(sizeof(int));
+    const int smem = (3 * B + 1) * static_cast<int>(sizeof(int));
     static int configured[64];
-    rc = sp_host::configure_kernel(kern, (4 * kForkB + 1) * static_cast<int>(sizeof(int)), dev.device, configured);
+    rc = sp_host::configure_kernel(kern, (3 * kForkB + 1) * static_cast<int>(sizeof(int)), dev.device, configured);
     if (rc != SPARSE_OK)
         return rc;
+    uint32_t *masks = static_cast<uint32_t *>(workspace) + 2 * kForkCluster * kForkWarps;
     ForkParams p{src, fork_len, seq_len, block_table, page_extra, free_pages, n_free, copy_src, copy_dst, static_cast<int *>(workspace),
-                 static_cast<uint32_t *>(workspace) + kForkCluster * kForkWarps, status, B, max_blocks, n_pages};
+                 masks, masks + static_cast<size_t>(B) * ((static_cast<size_t>(max_blocks) + 31) / 32), status, B, max_blocks, n_pages};
     // a cluster's barriers cost more than a few thousand blocks do
     const unsigned ctas = static_cast<long long>(B) * max_blocks <= 32 * kForkThreads ? 1 : kForkCluster;
     cudaLaunchConfig_t cfg = {};
