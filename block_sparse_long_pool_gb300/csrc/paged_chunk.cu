@@ -60,8 +60,8 @@ constexpr int kOffCtrl = kOffRec + 2 * 16 * 32;   // int [16]
 constexpr int kOffStart = kOffCtrl + 64;          // Start
 constexpr int kOffQs = kOffStart + 64;            // float [tiles][128]
 constexpr int kOffNan = kOffQs + kTiles * kTileRows * 4;   // int [2][128], then int [2]
-constexpr int kOffScan = kOffNan + 2 * kD * 4 + 16;        // long long [32], int [32]
-constexpr int kOffLive = kOffScan + 32 * 12;               // uint16 [kMaxB]
+constexpr int kOffScan = kOffNan + 2 * kD * 4 + 16;        // long long [32], int [32], int [32]
+constexpr int kOffLive = kOffScan + 32 * 16;               // uint16 [kMaxB]
 constexpr int kSmem = kOffLive + 2 * kMaxB + 1024;
 static_assert(kNumBars * 8 <= 320 && kOffRec % 16 == 0 && kOffStart % 8 == 0 && kOffScan % 8 == 0, "alignment");
 static_assert(kSmem <= 232448, "shared memory of a CTA");
@@ -381,12 +381,13 @@ __device__ __forceinline__ void find_start(const ChunkParams &p, uint8_t *base, 
 {
     long long *warp_work = reinterpret_cast<long long *>(base + kOffScan);
     int *warp_live = reinterpret_cast<int *>(base + kOffScan + 32 * 8);
+    int *warp_items = warp_live + 32;
     uint16_t *list = reinterpret_cast<uint16_t *>(base + kOffLive);
     Start *s = reinterpret_cast<Start *>(base + kOffStart);
     constexpr int kWarps = kThreads / 32;
     const int warp = tid >> 5, lane = tid & 31;
     const int per = (p.B + kThreads - 1) / kThreads, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-    long long sum = 0;
+    long long sum = 0, items = 0;
     int count = 0;
     bool bad = false;
     for (int b = b0; b < b1; ++b) {
@@ -394,8 +395,10 @@ __device__ __forceinline__ void find_start(const ChunkParams &p, uint8_t *base, 
         if (r.n > 0) {
             sum += p.H_kv * work_upto(p, r, items_of(p, r.n));
             ++count;
+            items += static_cast<long long>(p.H_kv) * items_of(p, r.n);
         }
     }
+    const int few = __reduce_add_sync(0xffffffffu, static_cast<int>(min(items, 1LL << 20)));   // more than CTAs is all the same
     if (bad && blockIdx.x == 0)
         report(p.status, SPARSE_ERR_BAD_INDEX);
     long long up = sum;
@@ -412,12 +415,13 @@ __device__ __forceinline__ void find_start(const ChunkParams &p, uint8_t *base, 
     if (lane == 31) {
         warp_work[warp] = up;
         warp_live[warp] = cup;
+        warp_items[warp] = few;
     }
     if (tid == 0)
         s->n_live = 0;
     __syncthreads();
     long long before = up - sum, total = 0;
-    int cbefore = cup - count, ctotal = 0;
+    int cbefore = cup - count, ctotal = 0, all_items = 0;
     for (int w = 0; w < kWarps; ++w) {
         if (w < warp) {
             before += warp_work[w];
@@ -425,8 +429,13 @@ __device__ __forceinline__ void find_start(const ChunkParams &p, uint8_t *base, 
         }
         total += warp_work[w];
         ctotal += warp_live[w];
+        all_items += warp_items[w];
     }
-    const long long n = max(1LL, min(static_cast<long long>(gridDim.x), total / kMinWork));
+    // as many CTAs as there is work for; where they are more than items, the same number an item (of equal items no
+    // CTA then has parts of two: one request of 4K tokens, 2 KV heads 26 us, 32 with 15 CTAs)
+    long long n = max(1LL, min(static_cast<long long>(gridDim.x), total / kMinWork));
+    if (all_items > 0 && all_items < n)
+        n -= n % all_items;
     const long long c = blockIdx.x;
     const long long lo = c >= n ? total : total / n * c + total % n * c / n;
     const long long hi = c + 1 >= n ? total : total / n * (c + 1) + total % n * (c + 1) / n;
