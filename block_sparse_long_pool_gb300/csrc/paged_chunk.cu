@@ -1,4 +1,33 @@
 // paged_chunk.cu -- attention of a chunk of new tokens a request over the paged 8-bit cache.
+//
+// Work.  An item is two tiles of 128 query rows (a token's G heads side by side) of one KV head of one request, with
+// all the tokens they see, 128 at a time: a step.  A persistent grid, one CTA an SM, takes equal shares of the items'
+// work, which is known on the device only: every CTA sums up the requests itself and finds its own first item by
+// search.  So an item may be cut, at a step; its parts are states (O, m, l, mo) in the workspace, which a second
+// kernel adds up in CTA order.  An item counts as its tokens and kItemCost more.
+//
+// A CTA's warps:
+//   pages     one warp looks up block table and scales, 32 pages at a time, ahead of the others;
+//   keys      one thread: TMA of a step's keys, two pages, as they are (e4m3, 128-byte swizzle);
+//   values    four warps: a step's values to f16 in shared memory (exact: e4m3 has fewer bits and exponents);
+//   products  a warp a tile: S = Q K^T by tcgen05 kind::f8f6f4, with Q in two e4m3 terms (load_queries says what that
+//             rounds), and O += P V by kind::f16, with P from tensor memory and V as it is stored (dims contiguous);
+//   softmax   four warps a tile, a thread a row: scores from tensor memory to registers, weights back in f16.
+// e4m3 products cost twice as much for two terms and half for 8 bits, so K needs no conversion at no price; P would
+// need two terms too, and a range of 17 binades, in the instructions of the busiest warps.
+//   Tensor memory holds, a tile, scores of two pages (a page's weights take the place of its scores) and O: while the
+// softmax works on a page, the products of the page before and the scores of the next one run.
+//   Sums, maxima and O are fp32.  Weights are rounded to f16: 2^-11 of each, and 2^-25 of the reference for those
+// below 2^-14 of it.  Page scales: ks multiplies the scores, vs is in the weights' exponent (weigh).  Scores of masked
+// tokens are replaced by -infinity before they are used, whatever they are.
+//
+// What bounds it.  On GB300 a step of two tiles takes about 3300 cycles where its products take 2048: the softmax
+// warps' instructions (a thread has 128 weights a step at 3.5 instructions each, at 4 cycles an instruction) and the loops of all
+// warps, which have to share an instruction cache that loses what it holds past some 16 KB: loops
+// unrolled as far as registers allow missed 230 times a step (4300 cycles), these miss next to nothing.  2048 rows
+// behind 30720 tokens, 32 query heads over 8: 787 us, 0.74 of the bf16 matrix rate; a prompt of 16384: 1630 us, 0.70.  An
+// item's start and end (queries, first scores, O) cost 5 steps, which nothing overlaps: 64 requests, most with one
+// row, 347 us at a floor of 129.  The kernel's start takes 12 us (list, pages, queries: round trips one after another).
 #include <limits.h>
 #include <math.h>
 
@@ -16,8 +45,11 @@ constexpr int kMaxB = 4096;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kMost = 0x1p15f;                  // of 32 weights, in f16: beyond it the row's reference is taken anew
 constexpr float kFarWeight = 60.f;                // log2 of the largest factor from a page's weights to O's
-constexpr int kItemCost = 704;                    // what an item costs beside its tokens, in tokens of one step
-constexpr int kMinWork = 640;                     // the least share of a CTA, in the same units
+// What an item costs beside its tokens, in tokens of one step: ragged chunks of G = 5 216 us (320: 290, 576: 236, 832:
+// 216), a prompt of 16K 1620 us (1824, 1679, 1615), 64 requests 346 us (459, 344, 355).
+constexpr int kItemCost = 704;
+// The least share of a CTA, in the same units: one request of 4K tokens, 2 KV heads 25.8 us (1024: 28.7).
+constexpr int kMinWork = 640;
 constexpr int kMinCut = 1;                        // steps on either side of a cut through an item
 
 constexpr int kSoftmaxWarps = 4 * kTiles;
@@ -267,10 +299,10 @@ __device__ __forceinline__ Request request_of(const ChunkParams &p, int b, bool 
 {
     const int a = p.cu_new[b], z = p.cu_new[b + 1], s = p.start[b];
     const int c0 = max(0, min(a, p.n_tok)), c1 = max(c0, min(z, p.n_tok));
-    const long long cap = static_cast<long long>(p.max_blocks) * kBlk;
+    const int cap = p.max_blocks * kBlk;
     if (s >= 0 && (a != c0 || z != c1 || static_cast<long long>(s) + (c1 - c0) > cap))
         *bad = true;
-    return Request{c0, c1 - c0, s < 0 ? -1 : s};
+    return Request{c0, c1 - c0, s < 0 ? -1 : min(s, cap)};   // past the table every row sees all of it
 }
 
 // Work of the first `q` items of a head of a request: an item's is the position of its first
@@ -346,7 +378,7 @@ struct Walk {
             it.n = min(per, r.n - t0);
             it.head = head;
             it.b = b;
-            it.pos = r.start < 0 ? -1 : r.start + t0;
+            it.pos = r.start < 0 ? -1 : static_cast<int>(min(static_cast<long long>(r.start) + t0, static_cast<long long>(p.max_blocks) * kBlk));
             it.all = 0;
 #pragma unroll
             for (int t = 0; t < kTiles; ++t) {
@@ -864,10 +896,9 @@ __device__ __forceinline__ void mma_loop(uint8_t *base, uint32_t base_s, uint32_
 // ---------------------------------------------------------------- softmax
 
 // A tile's queries in two e4m3 terms, each row scaled by the largest power of two of its own that
-// leaves its largest element within 448.  bf16 has 8 bits and a term 4, so that the two hold elements
-// down to 2^-11 of the row's largest exactly and those below within 2^-19 of it (half of e4m3's
-// least step, 2^-10, of 2^8 and more; where the largest is past 1.75 times its power of two, of 2^7: 2^-10, 2^-18).
-// (In f16 between: it holds bf16's 8 bits down to 2^-17, far below e4m3's least step.)  Two rows a warp at a time;
+// leaves its largest element within 448, so above 224.  bf16 has 8 bits and a term 4: the two hold an
+// element of 1/4 and more exactly (2^-9 of the largest and more are), and those below within half of e4m3's least
+// step, 2^-10 (2^-17 of the largest).  (In f16 between: it holds bf16's 8 bits down to 2^-17, far below e4m3's least step.)  Two rows a warp at a time;
 // rows past the tile's are zero, and all of a row that is not finite is NaN.
 __device__ __forceinline__ void load_queries(const ChunkParams &p, const Item &it, int t, uint8_t *base, uint32_t base_s, int warp,
                                              int lane)
@@ -975,7 +1006,6 @@ __device__ __forceinline__ void rescale(uint32_t o_t, float alpha)
     }
 }
 
-// One tile's softmax: a thread a row.
 // What a thread keeps of its row.  l is in units of 2^m; O in units of 2^mo, and so are the weights.
 struct Row {
     float m, mo, l;
@@ -1369,7 +1399,7 @@ extern "C" SPARSE_API int sparse_paged_chunk_attn_f8(const uint16_t *Q, long lon
     const float scale_log2 = (scale == 0.f ? 1.f / sqrtf(static_cast<float>(kD)) : scale) * 1.44269504088896340736f;
     if (!isfinite(scale_log2))
         return fail(SPARSE_ERR_INVALID_ARG, "%s: scale * log2(e) is not finite", name);
-    if (!sizes_ok(B, H_q, H_kv) || n_pages > kMaxPages || max_blocks >= kMaxPages || n_tok > kMaxRows)
+    if (!sizes_ok(B, H_q, H_kv) || n_pages > kMaxPages || max_blocks > kMaxPages - 8 || n_tok > kMaxRows)
         return fail(SPARSE_ERR_UNSUPPORTED, "%s: G=%d > 16, B=%d > %d, H_kv=%d > 65535, n_pages or max_blocks too large, or n_tok > %d",
                     name, H_q / H_kv, B, kMaxB, H_kv, kMaxRows);
     // the list's work fits 62 bits

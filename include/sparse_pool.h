@@ -693,7 +693,10 @@ SPARSE_API size_t sparse_paged_decode_attn_f8_workspace_size(int B, int H_q, int
  * the table's tokens) are reported as SPARSE_ERR_BAD_INDEX; a call that gives up waiting as
  * SPARSE_ERR_TIMEOUT (O and lse are then not to be used).  The result does not depend on
  * timing.
- * G = H_q / H_kv <= 16, B <= 4096, n_tok <= 2^30, n_pages <= 2^25, max_blocks < 2^25.
+ * Scores take q in two e4m3 terms: elements below 2^-9 of a row's largest are off by up to 2^-17 of it.
+ * A row of Q that is not finite gives NaN.
+ * G = H_q / H_kv <= 16, B <= 4096, n_tok <= 2^30, n_pages <= 2^25, n_pages * H_kv < 2^30,
+ * max_blocks <= 2^25 - 8.
  */
 SPARSE_API int sparse_paged_chunk_attn_f8(const uint16_t *Q, long long q_stride, const uint8_t *kv_pages,
                                           const float *kv_scale, int n_pages, const int *block_table, int max_blocks,
