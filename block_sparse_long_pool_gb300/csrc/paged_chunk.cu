@@ -112,7 +112,6 @@ struct Step {
 static_assert(sizeof(Step) == 32 && kOffCtrl == kOffRec + 2 * kGroup * 32, "two 16-byte loads");
 enum {
     kActive = 1,       // << tile: the tile has rows that see a token of the step
-    kLast = 4,         // << tile: its last step of the item
     kBegins = 16,      // the first step of an item
     kOdd = 32,         // of an item with an odd number
     kEnd = 64,         // no step: the end
@@ -605,7 +604,6 @@ __device__ __forceinline__ void page_loop(const ChunkParams &p, uint8_t *base, u
                 for (int t = 0; t < kTiles; ++t) {
                     const int last = min(it.j1, it.steps[t]) - 1;
                     f |= j <= last ? kActive << t : 0;
-                    f |= j == last ? kLast << t : 0;
                 }
                 flags = f | (items & 1 ? kOdd : 0) | min(kKv, end - j * kKv) << kRowsShift;
                 tok = j * kKv;
@@ -759,8 +757,15 @@ __device__ __forceinline__ void convert_loop(const ChunkParams &p, uint8_t *base
         report(p.status, SPARSE_ERR_TIMEOUT);
 }
 
+__device__ __forceinline__ void prefetch_values(const uint8_t *pages, int at)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(pages + static_cast<size_t>(at) * (2 * kBlk * kD) + kBlk * kD),
+                 "r"(kBlk * kD)
+                 : "memory");
+}
+
 // One thread: a step's keys, two pages, to shared memory as they are.
-__device__ __forceinline__ void key_loop(const CUtensorMap *map, uint8_t *base, uint32_t base_s, int *status)
+__device__ __forceinline__ void key_loop(const CUtensorMap *map, const uint8_t *pages, uint8_t *base, uint32_t base_s, int *status)
 {
     const uint32_t bars = base_s + kOffBars;
     const uint64_t policy = policy_evict_last();   // other CTAs read them, too
@@ -786,6 +791,11 @@ __device__ __forceinline__ void key_loop(const CUtensorMap *map, uint8_t *base, 
             tma_load_3d(dst, map, bar, 0, 0, 2 * a, policy);
         if (z >= 0)
             tma_load_3d(dst + kBlk * kD, map, bar, 0, 0, 2 * z, policy);
+        // the step's values to L2 meanwhile: the converters ask for them only when those before are stored
+        if (a >= 0)
+            prefetch_values(pages, a);
+        if (z >= 0)
+            prefetch_values(pages, z);
     }
     if (!ok)
         report(status, SPARSE_ERR_TIMEOUT);
@@ -1300,7 +1310,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         else if (warp == kMmaWarp + 2)
             page_loop(p, base, base_s, tid & 31);
         else if (tid == (kMmaWarp + 3) * 32)
-            key_loop(&map, base, base_s, p.status);
+            key_loop(&map, p.kv_pages, base, base_s, p.status);
     }
     __syncwarp();
     tc_fence_before();
