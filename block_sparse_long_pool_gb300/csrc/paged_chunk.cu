@@ -122,6 +122,7 @@ enum {
 struct Start {
     long long at, lo, hi;
     int live, head, chunk, n_live;
+    int b, row, n, start;
 };
 
 struct ChunkParams {
@@ -346,7 +347,8 @@ struct Walk {
         chunk = s->chunk;
         n_live = s->n_live;
         list = live_list;
-        enter(p);
+        b = s->b;
+        r = Request{s->row, s->n, s->start};
     }
     __device__ __forceinline__ void enter(const ChunkParams &p)
     {
@@ -468,8 +470,8 @@ __device__ __forceinline__ void find_start(const ChunkParams &p, uint8_t *base, 
     if (all_items > 0 && all_items < n)
         n -= n % all_items;
     const long long c = blockIdx.x;
-    const long long lo = c >= n ? total : total / n * c + total % n * c / n;
-    const long long hi = c + 1 >= n ? total : total / n * (c + 1) + total % n * (c + 1) / n;
+    const long long each = total / n, rest = total - each * n;   // rest of them have one more
+    const long long lo = c >= n ? total : each * c + min(c, rest), hi = c >= n ? total : lo + each + (c < rest);
     if (tid == 0 && lo >= hi) {
         s->at = s->lo = s->hi = total;
         s->live = s->n_live = 0;
@@ -496,6 +498,10 @@ __device__ __forceinline__ void find_start(const ChunkParams &p, uint8_t *base, 
             s->lo = lo;
             s->hi = hi;
             s->live = cbefore;
+            s->b = b;
+            s->row = r.row;
+            s->n = r.n;
+            s->start = r.start;
             s->head = head;
             s->chunk = a;
             s->n_live = ctotal;
@@ -579,8 +585,9 @@ __device__ __forceinline__ void page_loop(const ChunkParams &p, uint8_t *base, u
             break;
         int flags = kEnd, tok = 0, at = -1, head = 0;
         const int *entry = nullptr;
-        for (int s = 0; s < kGroup && more; ++s) {
-            int f = 0;
+        int queries = 0;          // rows of the item that begins here, or of the last of them
+        for (int s = 0; s < kGroup;) {   // a run of steps of one item at a time
+            bool begins = false;
             if (j >= it.j1) {
                 do
                     more = walk.next(p, it);
@@ -589,29 +596,25 @@ __device__ __forceinline__ void page_loop(const ChunkParams &p, uint8_t *base, u
                     break;
                 j = it.j0;
                 ++items;
-                f = kBegins;
-                // its queries on the way to L2, 256 bytes a row
-                for (int r = lane; r < it.n * p.G; r += 32) {
-                    const int tok = r / p.G, g = r - tok * p.G;
-                    const uint16_t *q = p.Q + (it.row + tok) * p.q_stride + static_cast<size_t>(it.head * p.G + g) * kD;
-                    asm volatile("prefetch.global.L2 [%0];\n\tprefetch.global.L2 [%0 + 128];" ::"l"(q));
-                }
+                begins = true;
+                queries = it.n * p.G;
             }
-            if (lane >> 1 == s) {
+            const int run = min(kGroup - s, it.j1 - j), mine = (lane >> 1) - s;
+            if (mine >= 0 && mine < run) {
                 const long long cap = static_cast<long long>(p.max_blocks) * kBlk;
-                const int end = static_cast<int>(min(static_cast<long long>(it.pos) + it.n, cap));
+                const int end = static_cast<int>(min(static_cast<long long>(it.pos) + it.n, cap)), at_j = j + mine;
+                int f = begins && mine == 0 ? kBegins : 0;
 #pragma unroll
-                for (int t = 0; t < kTiles; ++t) {
-                    const int last = min(it.j1, it.steps[t]) - 1;
-                    f |= j <= last ? kActive << t : 0;
-                }
-                flags = f | (items & 1 ? kOdd : 0) | min(kKv, end - j * kKv) << kRowsShift;
-                tok = j * kKv;
+                for (int t = 0; t < kTiles; ++t)
+                    f |= at_j < min(it.j1, it.steps[t]) ? kActive << t : 0;
+                flags = f | (items & 1 ? kOdd : 0) | min(kKv, end - at_j * kKv) << kRowsShift;
+                tok = at_j * kKv;
                 head = it.head;
                 if (tok + (lane & 1) * kBlk < end)
-                    entry = p.block_table + static_cast<size_t>(it.b) * p.max_blocks + 2 * j + (lane & 1);
+                    entry = p.block_table + static_cast<size_t>(it.b) * p.max_blocks + 2 * at_j + (lane & 1);
             }
-            ++j;
+            s += run;
+            j += run;
         }
         if (entry != nullptr) {
             const int page = *entry;
@@ -637,6 +640,12 @@ __device__ __forceinline__ void page_loop(const ChunkParams &p, uint8_t *base, u
         __syncwarp();
         if (lane == 0)
             mbar_arrive(bars + 8 * (kScales + half));
+        // an item's queries on the way to L2, 256 bytes a row
+        for (int r = lane; r < queries; r += 32) {
+            const int in = r / p.G, g = r - in * p.G;
+            const uint16_t *q = p.Q + (it.row + in) * p.q_stride + static_cast<size_t>(it.head * p.G + g) * kD;
+            asm volatile("prefetch.global.L2 [%0];\n\tprefetch.global.L2 [%0 + 128];" ::"l"(q));
+        }
         // a full last group: the end is in the next one
         if (!more && __shfl_sync(0xffffffffu, flags, 31) != kEnd)
             more = true;
