@@ -48,8 +48,9 @@ constexpr float kFarWeight = 60.f;                // log2 of the largest factor 
 // What an item costs beside its tokens, in tokens of one step: ragged chunks of G = 5 216 us (320: 290, 576: 236, 832:
 // 216), a prompt of 16K 1620 us (1824, 1679, 1615), 64 requests 346 us (459, 344, 355).
 constexpr int kItemCost = 704;
-// The least share of a CTA, in the same units: one request of 4K tokens, 2 KV heads 25.8 us (1024: 28.7).
-constexpr int kMinWork = 640;
+// The least share of a CTA, in the same units: 500 rows of a prompt, 16 heads over 4, 27.6 us (400: 38.7, 200: 28.1), 16 rows
+// behind 4K tokens, 2 KV heads, 24.6 us (23.0, 25.9), eight ragged requests of one KV head 38.3 us (39.1, 40.5).
+constexpr int kMinWork = 300;
 constexpr int kMinCut = 1;                        // steps on either side of a cut through an item
 
 constexpr int kSoftmaxWarps = 4 * kTiles;
@@ -465,7 +466,7 @@ __device__ __forceinline__ void find_start(const ChunkParams &p, uint8_t *base, 
         all_items += warp_items[w];
     }
     // as many CTAs as there is work for; where they are more than items, the same number an item (of equal items no
-    // CTA then has parts of two: one request of 4K tokens, 2 KV heads 26 us, 32 with 15 CTAs)
+    // CTA then has parts of two: one request of 4K tokens, 2 KV heads 26 us with 14 CTAs, 32 with 15)
     long long n = max(1LL, min(static_cast<long long>(gridDim.x), total / kMinWork));
     if (all_items > 0 && all_items < n)
         n -= n % all_items;
@@ -1348,23 +1349,45 @@ __global__ void __launch_bounds__(32 * kMergeRows) paged_chunk_merge_kernel(cons
     constexpr int kAll = kTiles * kTileRows;
     float m = -INFINITY, mo = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0; c < n_ctas; ++c) {
-        const int kind = c == c0 ? 1 : p.heads[c];
-        if (kind == 0)
-            continue;
-        const float *part = p.parts + static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * kPartFloats;
-        const float *stat = part + kAll * kD;
-        const float pm = stat[prow], pl = stat[kAll + prow], pmo = stat[2 * kAll + prow];
-        const float4 x = *reinterpret_cast<const float4 *>(part + prow * kD + 4 * lane);
-        const float nm = fmaxf(m, pm), nmo = fmaxf(mo, pmo);
-        const float a = m == -INFINITY ? 0.f : exp2f(m - nm), b = pm == -INFINITY ? 0.f : exp2f(pm - nm);
-        l = l * a + pl * b;
-        m = nm;
-        const float ao = mo == -INFINITY ? 0.f : exp2f(mo - nmo), bo = pmo == -INFINITY ? 0.f : exp2f(pmo - nmo);
-        o = make_float4(o.x * ao + x.x * bo, o.y * ao + x.y * bo, o.z * ao + x.z * bo, o.w * ao + x.w * bo);
-        mo = nmo;
-        if (kind == 2)
-            break;
+    // the CTAs after this one, 32 at a time, to the one that ends the item; the states of four are asked for at once
+    constexpr int kAtOnce = 4;
+    bool last = false;
+    for (int c1 = c0; c1 < n_ctas && !last; c1 += 32) {
+        const int kind = c1 + lane == c0 ? 1 : c1 + lane < n_ctas ? p.heads[c1 + lane] : 0;
+        const uint32_t ends = __ballot_sync(0xffffffffu, kind == 2);
+        last = ends != 0u;
+        uint32_t parts = __ballot_sync(0xffffffffu, kind != 0) & (last ? (ends & (0u - ends)) * 2u - 1u : ~0u);
+        while (parts != 0u) {
+            float pm[kAtOnce], pl[kAtOnce], pmo[kAtOnce];
+            float4 x[kAtOnce];
+            int n = 0;
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                if (parts != 0u) {
+                    const int c = c1 + __ffs(parts) - 1;
+                    const float *part = p.parts + static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * kPartFloats;
+                    const float *stat = part + kAll * kD;
+                    pm[u] = stat[prow];
+                    pl[u] = stat[kAll + prow];
+                    pmo[u] = stat[2 * kAll + prow];
+                    x[u] = *reinterpret_cast<const float4 *>(part + prow * kD + 4 * lane);
+                    parts &= parts - 1u;
+                    ++n;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                if (u < n) {
+                    const float nm = fmaxf(m, pm[u]), nmo = fmaxf(mo, pmo[u]);
+                    const float a = m == -INFINITY ? 0.f : exp2f(m - nm), b = pm[u] == -INFINITY ? 0.f : exp2f(pm[u] - nm);
+                    l = l * a + pl[u] * b;
+                    m = nm;
+                    const float ao = mo == -INFINITY ? 0.f : exp2f(mo - nmo), bo = pmo[u] == -INFINITY ? 0.f : exp2f(pmo[u] - nmo);
+                    o = make_float4(o.x * ao + x[u].x * bo, o.y * ao + x[u].y * bo, o.z * ao + x[u].z * bo, o.w * ao + x[u].w * bo);
+                    mo = nmo;
+                }
+            }
+        }
     }
     const Finish fin(m, l, mo);
     const size_t out = static_cast<size_t>(tail.x + tok) * p.H_q + tail.y * p.G + g;
