@@ -21,13 +21,15 @@
 // below 2^-14 of it.  Page scales: ks multiplies the scores, vs is in the weights' exponent (weigh).  Scores of masked
 // tokens are replaced by -infinity before they are used, whatever they are.
 //
-// What bounds it.  On GB300 a step of two tiles takes about 3300 cycles where its products take 2048: the softmax
-// warps' instructions (a thread has 128 weights a step at 3.5 instructions each, at 4 cycles an instruction) and the loops of all
-// warps, which have to share an instruction cache that loses what it holds past some 16 KB: loops
-// unrolled as far as registers allow missed 230 times a step (4300 cycles), these miss next to nothing.  2048 rows
-// behind 30720 tokens, 32 query heads over 8: 787 us, 0.74 of the bf16 matrix rate; a prompt of 16384: 1630 us, 0.70.  An
-// item's start and end (queries, first scores, O) cost 5 steps, which nothing overlaps: 64 requests, most with one
-// row, 347 us at a floor of 129.  The kernel's start takes 12 us (list, pages, queries: round trips one after another).
+// What bounds it.  On GB300 a step of two tiles takes about 3300 cycles.  Its products take 2048 by the tensor pipe's
+// rate, 2560 by shared memory's: the scores of a page (N = 64) read 6 KB for 32 cycles of products, at 128 bytes a cycle.
+// (N = 128 would read 8 KB for 64, but then the next scores wait until both pages' weights are there: 4300 cycles.)
+// The softmax warps work 2600 of the 3300, 128 weights a thread and step at 3 instructions each.  All loops share an
+// instruction cache that loses what it holds past some 16 KB: unrolled as far as registers allow they missed 230 times
+// a step (4300 cycles), these miss next to nothing.  2048 rows behind 30720 tokens, 32 query heads over 8: 785 us, 0.74 of
+// the bf16 matrix rate (834 where no input is left in L2 and the clock is lower); a prompt of 16384: 1620 us, 0.70.  An item's
+// start and end (queries, first scores, O) cost 5 steps, which nothing overlaps: 64 requests, most with one row,
+// 345 us at a floor of 129.  First scores come 9 us after the kernel's start (list, pages, queries: round trips).
 #include <limits.h>
 #include <math.h>
 
@@ -43,7 +45,7 @@ constexpr int kTiles = 2;                         // tiles of an item
 constexpr int kKv = 128;                          // tokens of a step: two pages
 constexpr int kMaxB = 4096;
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr float kMost = 0x1p15f;                  // of 32 weights, in f16: beyond it the row's reference is taken anew
+constexpr float kMost = 0x1p15f;                  // of a page's weights together, in f16: beyond it the row's reference is taken anew
 constexpr float kFarWeight = 60.f;                // log2 of the largest factor from a page's weights to O's
 // What an item costs beside its tokens, in tokens of one step: ragged chunks of G = 5 216 us (320: 290, 576: 236, 832:
 // 216), a prompt of 16K 1620 us (1824, 1679, 1615), 64 requests 346 us (459, 344, 355).

@@ -547,8 +547,8 @@ SPARSE_API int sparse_gather_offloaded(const uint16_t *k_host, const uint16_t *v
                                        int *status, void *stream);
 
 /*
- * The paged 8-bit cache: three calls that serve requests of their own lengths from one
- * pool of pages.  The notes have no counterpart; block size, head dimension, compressed
+ * The paged 8-bit cache: calls that serve requests of their own lengths from one pool of
+ * pages.  The notes have no counterpart; block size, head dimension, compressed
  * keys and block lists are those of the calls above, so sparse_select_topk and the other
  * selectors run on it unchanged.
  *   page         64 tokens of every KV head: kv_pages [n_pages][H_kv][2][64][128] e4m3
@@ -558,9 +558,11 @@ SPARSE_API int sparse_gather_offloaded(const uint16_t *k_host, const uint16_t *v
  *   block table  [B][max_blocks] int32: the page that holds block j (tokens 64 j ..
  *                64 j + 63) of request b.
  *   slot         64 * page + row: the place of one token's rows.
- * A step is sparse_page_plan, then per layer sparse_paged_append_f8, a selector (or none),
- * and sparse_paged_decode_attn_f8.  All three are launched with programmatic stream
- * serialization and wait for the kernel before them on the stream before reading anything.
+ * A step is sparse_page_plan, then per layer sparse_rope, sparse_paged_append_f8 and
+ * sparse_paged_chunk_attn_f8, or, where every request has one new token, a selector (or none) and
+ * sparse_paged_decode_attn_f8.  Between steps sparse_page_fork, with sparse_paged_copy_f8 per layer,
+ * makes requests copies of others.  All are launched with programmatic stream serialization
+ * and wait for the kernel before them on the stream before reading anything.
  */
 
 /*
