@@ -26,10 +26,10 @@
 // (N = 128 would read 8 KB for 64, but then the next scores wait until both pages' weights are there: 4300 cycles.)
 // The softmax warps work 2600 of the 3300, 128 weights a thread and step at 3 instructions each.  All loops share an
 // instruction cache that loses what it holds past some 16 KB: unrolled as far as registers allow they missed 230 times
-// a step (4300 cycles), these miss next to nothing.  2048 rows behind 30720 tokens, 32 query heads over 8: 785 us, 0.74 of
-// the bf16 matrix rate (834 where no input is left in L2 and the clock is lower); a prompt of 16384: 1620 us, 0.70.  An item's
+// a step (4300 cycles), these miss next to nothing.  2048 rows behind 30720 tokens, 32 query heads over 8: 782 us, 0.75 of
+// the bf16 matrix rate (834 where no input is left in L2 and the clock is lower); a prompt of 16384: 1590 us, 0.71.  An item's
 // start and end (queries, first scores, O) cost 5 steps, which nothing overlaps: 64 requests, most with one row,
-// 345 us at a floor of 129.  First scores come 9 us after the kernel's start (list, pages, queries: round trips).
+// 341 us at a floor of 129.  First scores come 9 us after the kernel's start (list, pages, queries: round trips).
 #include <limits.h>
 #include <math.h>
 
@@ -920,58 +920,72 @@ __device__ __forceinline__ void mma_loop(uint8_t *base, uint32_t base_s, uint32_
 // A tile's queries in two e4m3 terms, each row scaled by the largest power of two of its own that
 // leaves its largest element within 448, so above 224.  bf16 has 8 bits and a term 4: the two hold an
 // element of 1/4 and more exactly (2^-9 of the largest and more are), and those below within half of e4m3's least
-// step, 2^-10 (2^-17 of the largest).  (In f16 between: it holds bf16's 8 bits down to 2^-17, far below e4m3's least step.)  Two rows a warp at a time;
+// step, 2^-10 (2^-17 of the largest).  (In f16 between: it holds bf16's 8 bits down to 2^-17, far below e4m3's least step.)  Four rows a warp at a time;
 // rows past the tile's are zero, and all of a row that is not finite is NaN.
 __device__ __forceinline__ void load_queries(const ChunkParams &p, const Item &it, int t, uint8_t *base, uint32_t base_s, int warp,
                                              int lane)
 {
     float *qs = reinterpret_cast<float *>(base + kOffQs) + t * kTileRows;
-    const int c = lane & 15, row0 = warp * 32 + (lane >> 4);
+    const int c = lane & 7, row0 = warp * 32 + (lane >> 3);   // eight lanes a row, 16 elements each
     const int n = min(p.per_tile, it.n - t * p.per_tile) * p.G;
-    const uint16_t *first = p.Q + static_cast<size_t>(it.head * p.G) * kD + c * 8;
+    const uint16_t *first = p.Q + static_cast<size_t>(it.head * p.G) * kD + c * 16;
     const long long tok0 = it.row + t * p.per_tile;
-    auto load = [&](int i) {
-        const int row = row0 + 2 * i, tok = row * p.recip >> 16, g = row - tok * p.G;
-        return row < n ? *reinterpret_cast<const uint4 *>(first + (tok0 + tok) * p.q_stride + g * kD) : make_uint4(0u, 0u, 0u, 0u);
+    struct Part {
+        uint4 a, b;
     };
-    // four at a time, the next four on their way (all sixteen in one piece of code miss the instruction cache)
-    constexpr int kAtOnce = 4;
-    uint4 x[kAtOnce], y[kAtOnce];
+    auto load = [&](int i) {
+        const int row = row0 + 4 * i, tok = row * p.recip >> 16, g = row - tok * p.G;
+        Part x{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+        if (row < n) {
+            const uint4 *q = reinterpret_cast<const uint4 *>(first + (tok0 + tok) * p.q_stride + g * kD);
+            x.a = q[0];
+            x.b = q[1];
+        }
+        return x;
+    };
+    // two at a time, the next two on their way (all of them in one piece of code miss the instruction cache)
+    constexpr int kAtOnce = 2;
+    Part x[kAtOnce], y[kAtOnce];
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i)
         y[i] = load(i);
 #pragma unroll 1
-    for (int i0 = 0; i0 < 16; i0 += kAtOnce) {
+    for (int i0 = 0; i0 < 8; i0 += kAtOnce) {
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
             x[i] = y[i];
-            y[i] = load(min(i0 + kAtOnce, 15) + i);
+            y[i] = load(min(i0 + kAtOnce, 7) + i);
         }
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
-            const int row = row0 + 2 * (i0 + i);
-            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            const int row = row0 + 4 * (i0 + i);
+            const uint32_t w[8] = {x[i].a.x, x[i].a.y, x[i].a.z, x[i].a.w, x[i].b.x, x[i].b.y, x[i].b.z, x[i].b.w};
             // the largest element's bits: positive bf16 are in the order of their bits, infinities and NaN the largest
-            uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+            uint32_t top = 0u;
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1)
+            for (int k = 0; k < 8; ++k)
+                top = __vmaxu2(top, w[k] & 0x7fff7fffu);
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1)
                 top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
             top = max(top & 0xffffu, top >> 16);
             const int e = static_cast<int>(top >> 7) - 127;   // the largest is 2^e times 1 to 2
             const int up = top > 0u ? max(-120, min(126, ((top & 0x7fu) <= 0x60u ? 8 : 7) - e)) : 0;
             const float f = top >= 0x7f80u ? NAN : __uint_as_float(static_cast<uint32_t>(up + 127) << 23 | p.q_sign);
+            const uint64_t f2 = pair(f, f);
             uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t v = pack_f16x2(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
-                hi[k] = f16x2_to_f8x2(v);
-                const uint32_t back = f8x2_to_f16x2(hi[k]);
+            for (int k = 0; k < 8; ++k) {
+                const float2 z = unpair(mul2(pair(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u)), f2));
+                const uint32_t v = pack_f16x2(z.x, z.y), h = f16x2_to_f8x2(v), back = f8x2_to_f16x2(h);
                 const __half2 rest = __hsub2(*reinterpret_cast<const __half2 *>(&v), *reinterpret_cast<const __half2 *>(&back));
-                lo[k] = f16x2_to_f8x2(*reinterpret_cast<const uint32_t *>(&rest));
+                const uint32_t l = f16x2_to_f8x2(*reinterpret_cast<const uint32_t *>(&rest));
+                hi[k >> 1] = k & 1 ? hi[k >> 1] | h << 16 : h;
+                lo[k >> 1] = k & 1 ? lo[k >> 1] | l << 16 : l;
             }
-            const uint32_t at = base_s + kOffQ + t * kOperand + row * 128 + (((c >> 1) ^ (row & 7)) << 4) + (c & 1) * 8;
-            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0] | hi[1] << 16), "r"(hi[2] | hi[3] << 16) : "memory");
-            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + kSub), "r"(lo[0] | lo[1] << 16), "r"(lo[2] | lo[3] << 16) : "memory");
+            const uint32_t at = base_s + kOffQ + t * kOperand + row * 128 + ((c ^ (row & 7)) << 4);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]) : "memory");
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + kSub), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
             if (c == 0)
                 qs[row] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
         }
