@@ -53,7 +53,6 @@ constexpr int kItemCost = 704;
 // The least share of a CTA, in the same units: 500 rows of a prompt, 16 heads over 4, 27.6 us (400: 38.7, 200: 28.1), 16 rows
 // behind 4K tokens, 2 KV heads, 24.6 us (23.0, 25.9), eight ragged requests of one KV head 38.3 us (39.1, 40.5).
 constexpr int kMinWork = 300;
-constexpr int kMinCut = 1;                        // steps on either side of a cut through an item
 
 constexpr int kSoftmaxWarps = 4 * kTiles;
 constexpr int kConvertWarp = kSoftmaxWarps;       // the first of them
@@ -368,8 +367,7 @@ struct Walk {
             return 0;
         if (x >= at + w)
             return all;
-        const int j = static_cast<int>((x - at) * all / w);
-        return j < kMinCut ? 0 : all - j < kMinCut ? all : j;
+        return static_cast<int>((x - at) * all / w);
     }
     // The next item that this CTA has steps of (or that it has to write, seeing nothing).
     __device__ __forceinline__ bool next(const ChunkParams &p, Item &it)
