@@ -33,6 +33,7 @@
 #include <limits.h>
 #include <math.h>
 
+#include "chunk_split.cuh"
 #include "common.cuh"
 #include "paged.cuh"
 
@@ -40,19 +41,10 @@ namespace {
 
 using namespace sp;
 
-constexpr int kTileRows = 128;                    // query rows of a tile: M of the products
-constexpr int kTiles = 2;                         // tiles of an item
-constexpr int kKv = 128;                          // tokens of a step: two pages
 constexpr int kMaxB = 4096;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kMost = 0x1p15f;                  // of a page's weights together, in f16: beyond it the row's reference is taken anew
 constexpr float kFarWeight = 60.f;                // log2 of the largest factor from a page's weights to O's
-// What an item costs beside its tokens, in tokens of one step: ragged chunks of G = 5 216 us (320: 290, 576: 236, 832:
-// 216), a prompt of 16K 1620 us (1824, 1679, 1615), 64 requests 346 us (459, 344, 355).
-constexpr int kItemCost = 704;
-// The least share of a CTA, in the same units: 500 rows of a prompt, 16 heads over 4, 27.6 us (400: 38.7, 200: 28.1), 16 rows
-// behind 4K tokens, 2 KV heads, 24.6 us (23.0, 25.9), eight ragged requests of one KV head 38.3 us (39.1, 40.5).
-constexpr int kMinWork = 300;
 
 constexpr int kSoftmaxWarps = 4 * kTiles;
 constexpr int kConvertWarp = kSoftmaxWarps;       // the first of them
@@ -103,7 +95,6 @@ static_assert(kSmem <= 232448, "shared memory of a CTA");
 constexpr int kColS = 0, kColO = kTiles * 128;    // tensor memory: scores (weights in their place), outputs
 
 // What the warps need to know of a step, sixteen written at a time.
-constexpr int kGroup = 16;
 struct Step {
     int page[2];       // page * H_kv + head, -1: none
     int flags;
@@ -120,20 +111,11 @@ enum {
     kRowsShift = 8     // tokens of the step that a row sees; those past them are zero
 };
 
-// A CTA's first item: where in the list of items it lies.
-struct Start {
-    long long at, lo, hi;
-    int live, head, chunk, n_live;
-    int b, row, n, start;
-};
-
-struct ChunkParams {
+struct ChunkParams : ChunkList {
     const uint16_t *Q;
     const uint8_t *kv_pages;
     const float *kv_scale;
     const int *block_table;
-    const int *cu_new;
-    const int *start;
     uint16_t *O;
     float *lse;
     float *parts;      // [2 * CTAs][part_floats]
@@ -144,13 +126,7 @@ struct ChunkParams {
     float scale_log2;  // not negative: the scale's sign is in the queries
     uint32_t q_sign;
     int n_pages;
-    int max_blocks;
-    int n_tok;
-    int B;
     int H_q;
-    int H_kv;
-    int G;
-    int per_tile;      // tokens of a tile
     int recip;         // 2^16 / G, up: row * recip >> 16 = row / G for the rows of a tile
 };
 
@@ -290,125 +266,7 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return r;
 }
 
-// ---------------------------------------------------------------- the list of items
-
-// A request's new tokens, held to the packed rows.
-struct Request {
-    int row, n, start;   // first row, rows, position of the first (-1: no pages, no token is seen)
-};
-
-__device__ __forceinline__ Request request_of(const ChunkParams &p, int b, bool *bad)
-{
-    const int a = p.cu_new[b], z = p.cu_new[b + 1], s = p.start[b];
-    const int c0 = max(0, min(a, p.n_tok)), c1 = max(c0, min(z, p.n_tok));
-    const int cap = p.max_blocks * kBlk;
-    if (s >= 0 && (a != c0 || z != c1 || static_cast<long long>(s) + (c1 - c0) > cap))
-        *bad = true;
-    return Request{c0, c1 - c0, s < 0 ? -1 : min(s, cap)};   // past the table every row sees all of it
-}
-
-// Work of the first `q` items of a head of a request: an item's is the position of its first
-// token and a constant, or the constant alone where no token is seen.
-__device__ __forceinline__ long long work_upto(const ChunkParams &p, const Request &r, long long q)
-{
-    if (r.start < 0)
-        return q * kItemCost;
-    return q * (static_cast<long long>(r.start) + kItemCost) + static_cast<long long>(kTiles * p.per_tile) * (q * (q - 1) / 2);
-}
-
-__device__ __forceinline__ int items_of(const ChunkParams &p, int n)
-{
-    const int t = kTiles * p.per_tile;
-    return n / t + (n % t != 0);
-}
-
-// An item: up to two tiles of one KV head's query rows, and the steps [j0, j1) of its tokens that
-// are this CTA's.
-struct Item {
-    int row, n;          // first row of the packed rows, tokens
-    int head, b;
-    int pos;             // position of the first token (-1: nothing is seen)
-    int steps[kTiles];   // steps that hold a token which a row of the tile sees
-    int all;             // steps of the item
-    int j0, j1;
-};
-
-struct Walk {
-    long long at, lo, hi;
-    int live, head, chunk, n_live, b;
-    Request r;
-    const uint16_t *list;
-
-    __device__ __forceinline__ void open(const ChunkParams &p, const Start *s, const uint16_t *live_list)
-    {
-        at = s->at;
-        lo = s->lo;
-        hi = s->hi;
-        live = s->live;
-        head = s->head;
-        chunk = s->chunk;
-        n_live = s->n_live;
-        list = live_list;
-        b = s->b;
-        r = Request{s->row, s->n, s->start};
-    }
-    __device__ __forceinline__ void enter(const ChunkParams &p)
-    {
-        bool bad = false;
-        if (live < n_live) {
-            b = list[live];
-            r = request_of(p, b, &bad);
-        }
-    }
-    // The step of the item at `at` with work w that the border x between two CTAs falls on.
-    static __device__ __forceinline__ int cut(long long x, long long at, long long w, int all)
-    {
-        if (x <= at)
-            return 0;
-        if (x >= at + w)
-            return all;
-        return static_cast<int>((x - at) * all / w);
-    }
-    // The next item that this CTA has steps of (or that it has to write, seeing nothing).
-    __device__ __forceinline__ bool next(const ChunkParams &p, Item &it)
-    {
-        while (live < n_live && at < hi) {
-            const int per = kTiles * p.per_tile;
-            const long long w = r.start < 0 ? kItemCost : static_cast<long long>(r.start) + kItemCost + static_cast<long long>(chunk) * per;
-            const int t0 = chunk * per;
-            it.row = r.row + t0;
-            it.n = min(per, r.n - t0);
-            it.head = head;
-            it.b = b;
-            it.pos = r.start < 0 ? -1 : static_cast<int>(min(static_cast<long long>(r.start) + t0, static_cast<long long>(p.max_blocks) * kBlk));
-            it.all = 0;
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-                it.steps[t] = 0;
-                if (r.start >= 0 && it.n > t * p.per_tile) {
-                    const long long last = static_cast<long long>(it.pos) + min(it.n, (t + 1) * p.per_tile);
-                    it.steps[t] = static_cast<int>((min(last, static_cast<long long>(p.max_blocks) * kBlk) + kKv - 1) / kKv);
-                }
-                it.all = max(it.all, it.steps[t]);
-            }
-            it.j0 = cut(lo, at, w, it.all);
-            it.j1 = cut(hi, at, w, it.all);
-            const bool mine = it.all > 0 ? it.j0 < it.j1 : at >= lo;
-            at += w;
-            if (++chunk == items_of(p, r.n)) {
-                chunk = 0;
-                if (++head == p.H_kv) {
-                    head = 0;
-                    ++live;
-                    enter(p);
-                }
-            }
-            if (mine)
-                return true;
-        }
-        return false;
-    }
-};
+// ---------------------------------------------------------------- this CTA's share
 
 // Every thread: the requests with rows, the work up to each, and this CTA's share of it.
 __device__ __forceinline__ void find_start(const ChunkParams &p, uint8_t *base, int tid)
@@ -465,14 +323,8 @@ __device__ __forceinline__ void find_start(const ChunkParams &p, uint8_t *base, 
         ctotal += warp_live[w];
         all_items += warp_items[w];
     }
-    // as many CTAs as there is work for; where they are more than items, the same number an item (of equal items no
-    // CTA then has parts of two: one request of 4K tokens, 2 KV heads 26 us with 14 CTAs, 32 with 15)
-    long long n = max(1LL, min(static_cast<long long>(gridDim.x), total / kMinWork));
-    if (all_items > 0 && all_items < n)
-        n -= n % all_items;
-    const long long c = blockIdx.x;
-    const long long each = total / n, rest = total - each * n;   // rest of them have one more
-    const long long lo = c >= n ? total : each * c + min(c, rest), hi = c >= n ? total : lo + each + (c < rest);
+    const Shares shares(total, all_items, gridDim.x);
+    const long long lo = shares.lo(blockIdx.x), hi = shares.hi(blockIdx.x);
     if (tid == 0 && lo >= hi) {
         s->at = s->lo = s->hi = total;
         s->live = s->n_live = 0;
@@ -482,31 +334,10 @@ __device__ __forceinline__ void find_start(const ChunkParams &p, uint8_t *base, 
         const Request r = request_of(p, b, &bad);
         if (r.n <= 0)
             continue;
-        const long long one = work_upto(p, r, items_of(p, r.n)), all = p.H_kv * one;
+        const long long all = p.H_kv * work_upto(p, r, items_of(p, r.n));
         list[cbefore] = static_cast<uint16_t>(b);
-        if (lo < hi && before <= lo && lo < before + all) {
-            const int head = static_cast<int>((lo - before) / one);
-            const long long in = lo - before - head * one;
-            int a = 0, z = items_of(p, r.n);   // work_upto(a) <= in < work_upto(z)
-            while (z - a > 1) {
-                const int mid = (a + z) / 2;
-                if (work_upto(p, r, mid) <= in)
-                    a = mid;
-                else
-                    z = mid;
-            }
-            s->at = before + head * one + work_upto(p, r, a);
-            s->lo = lo;
-            s->hi = hi;
-            s->live = cbefore;
-            s->b = b;
-            s->row = r.row;
-            s->n = r.n;
-            s->start = r.start;
-            s->head = head;
-            s->chunk = a;
-            s->n_live = ctotal;
-        }
+        if (lo < hi && before <= lo && lo < before + all)
+            locate(p, r, b, cbefore, ctotal, before, lo, hi, s);
         before += all;
         ++cbefore;
     }
@@ -572,13 +403,10 @@ __device__ __noinline__ uint4 take_nan(uint4 x, int tok, int c, int *first)
 __device__ __forceinline__ void page_loop(const ChunkParams &p, uint8_t *base, uint32_t base_s, int lane)
 {
     const uint32_t bars = base_s + kOffBars;
-    Walk walk;
-    walk.open(p, reinterpret_cast<const Start *>(base + kOffStart), reinterpret_cast<const uint16_t *>(base + kOffLive));
-    Item it;
-    int j = 0, items = 0;
-    it.j1 = 0;
-    bool more = true, ok = true, bad = false;
-    for (uint32_t group = 0; more; ++group) {
+    Steps steps;
+    steps.open(p, reinterpret_cast<const Start *>(base + kOffStart), reinterpret_cast<const uint16_t *>(base + kOffLive));
+    bool ok = true, bad = false;
+    for (uint32_t group = 0; steps.more; ++group) {
         const int half = group & 1;
         if (group >= 2)
             ok = ok && mbar_wait(bars + 8 * (kUsed + half), ((group >> 1) - 1) & 1, kWaitNs);
@@ -586,37 +414,23 @@ __device__ __forceinline__ void page_loop(const ChunkParams &p, uint8_t *base, u
             break;
         int flags = kEnd, tok = 0, at = -1, head = 0;
         const int *entry = nullptr;
-        int queries = 0;          // rows of the item that begins here, or of the last of them
-        for (int s = 0; s < kGroup;) {   // a run of steps of one item at a time
-            bool begins = false;
-            if (j >= it.j1) {
-                do
-                    more = walk.next(p, it);
-                while (more && it.all == 0);
-                if (!more)
-                    break;
-                j = it.j0;
-                ++items;
-                begins = true;
-                queries = it.n * p.G;
-            }
-            const int run = min(kGroup - s, it.j1 - j), mine = (lane >> 1) - s;
-            if (mine >= 0 && mine < run) {
-                const long long cap = static_cast<long long>(p.max_blocks) * kBlk;
-                const int end = static_cast<int>(min(static_cast<long long>(it.pos) + it.n, cap)), at_j = j + mine;
-                int f = begins && mine == 0 ? kBegins : 0;
+        steps.group(p, [&](int s, int run, int j, bool begins) {
+            const int mine = (lane >> 1) - s;
+            if (mine < 0 || mine >= run)
+                return;
+            const Item &it = steps.it;
+            const long long cap = static_cast<long long>(p.max_blocks) * kBlk;
+            const int end = static_cast<int>(min(static_cast<long long>(it.pos) + it.n, cap)), at_j = j + mine;
+            int f = begins && mine == 0 ? kBegins : 0;
 #pragma unroll
-                for (int t = 0; t < kTiles; ++t)
-                    f |= at_j < min(it.j1, it.steps[t]) ? kActive << t : 0;
-                flags = f | (items & 1 ? kOdd : 0) | min(kKv, end - at_j * kKv) << kRowsShift;
-                tok = at_j * kKv;
-                head = it.head;
-                if (tok + (lane & 1) * kBlk < end)
-                    entry = p.block_table + static_cast<size_t>(it.b) * p.max_blocks + 2 * at_j + (lane & 1);
-            }
-            s += run;
-            j += run;
-        }
+            for (int t = 0; t < kTiles; ++t)
+                f |= at_j < min(it.j1, it.steps[t]) ? kActive << t : 0;
+            flags = f | (steps.items & 1 ? kOdd : 0) | min(kKv, end - at_j * kKv) << kRowsShift;
+            tok = at_j * kKv;
+            head = it.head;
+            if (tok + (lane & 1) * kBlk < end)
+                entry = p.block_table + static_cast<size_t>(it.b) * p.max_blocks + 2 * at_j + (lane & 1);
+        });
         if (entry != nullptr) {
             const int page = *entry;
             if (page >= 0 && page < p.n_pages)
@@ -641,15 +455,12 @@ __device__ __forceinline__ void page_loop(const ChunkParams &p, uint8_t *base, u
         __syncwarp();
         if (lane == 0)
             mbar_arrive(bars + 8 * (kScales + half));
-        // an item's queries on the way to L2, 256 bytes a row
-        for (int r = lane; r < queries; r += 32) {
+        // the queries of the item that began on the way to L2, 256 bytes a row
+        for (int r = lane; r < steps.q_rows; r += 32) {
             const int in = r / p.G, g = r - in * p.G;
-            const uint16_t *q = p.Q + (it.row + in) * p.q_stride + static_cast<size_t>(it.head * p.G + g) * kD;
+            const uint16_t *q = p.Q + (steps.q_row + in) * p.q_stride + static_cast<size_t>(steps.q_head * p.G + g) * kD;
             asm volatile("prefetch.global.L2 [%0];\n\tprefetch.global.L2 [%0 + 128];" ::"l"(q));
         }
-        // a full last group: the end is in the next one
-        if (!more && __shfl_sync(0xffffffffu, flags, 31) != kEnd)
-            more = true;
     }
     if (bad)
         report(p.status, SPARSE_ERR_BAD_INDEX);
