@@ -18,7 +18,8 @@
 //   Tensor memory holds, a tile, scores of two pages (a page's weights take the place of its scores) and O: while the
 // softmax works on a page, the products of the page before and the scores of the next one run.
 //   Sums, maxima and O are fp32.  Weights are rounded to f16: 2^-11 of each, and 2^-25 of the reference for those
-// below 2^-14 of it.  Page scales: ks multiplies the scores, vs is in the weights' exponent (weigh).  Scores of masked
+// below 2^-14 of it, which is 2^-8 of a page's largest weight (weigh): a token far above all others costs them no bits
+// before it has 2^22 times their weight.  Page scales: ks multiplies the scores, vs is in the weights' exponent (weigh).  Scores of masked
 // tokens are replaced by -infinity before they are used, whatever they are.
 //
 // What bounds it.  On GB300 a step of two tiles takes about 3300 cycles.  Its products take 2048 by the tensor pipe's
@@ -43,7 +44,11 @@ using namespace sp;
 
 constexpr int kMaxB = 4096;
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr float kMost = 0x1p15f;                  // of a page's weights together, in f16: beyond it the row's reference is taken anew
+// log2 of a page's largest weight where its row's reference is taken; f16 holds 2^8 times that, and 2^22 times less in full.
+// (A reference at the maximum has all of f16's range above it and 2^14 below: as long either way, 2048 rows behind
+// 30720 tokens 824 us and 827, 64 requests 342 and 342; with weights of 2^15 together in place of f16's most 848 and 378.)
+constexpr float kAbove = 8.f;
+constexpr float kMost = 65504.f;                  // of a page's weights together, in f16: beyond it the row's reference is taken anew
 constexpr float kFarWeight = 60.f;                // log2 of the largest factor from a page's weights to O's
 
 constexpr int kSoftmaxWarps = 4 * kTiles;
@@ -857,9 +862,9 @@ struct Row {
 };
 
 // Weights 2^(s sc + lf - m) of a page's 64 columns, lf = log2 vs + m - mo, in f16 to tensor memory, and their part of l.
-// The references m and mo are those of the item's first page, and stay as long as no page's weights add up to more
+// The references m and mo, kAbove below the maxima of the item's first page, stay as long as no page's weights add up to more
 // than kMost: no pass over the scores for their maximum.  Where they do (and where nothing was seen so
-// far, and in rows with NaN) m and mo become the maxima, and what is in their units is scaled; `behind` waits
+// far, and in rows with NaN) they are taken from that page's maxima, and what is in their units is scaled; `behind` waits
 // until the products with the weights before are done and says whether there were any.
 template <typename F>
 __device__ __forceinline__ void weigh(Row &r, uint32_t (&s)[2][32], uint32_t p_t, uint32_t o_t, float sc, float lv, F behind)
@@ -873,7 +878,7 @@ __device__ __forceinline__ void weigh(Row &r, uint32_t (&s)[2][32], uint32_t p_t
             for (int i = 0; i < 32; ++i)
                 top[i & 1] = max3(top[i & 1], __uint_as_float(s[0][i]), __uint_as_float(s[1][i]));
             top[0] = fmaxf(top[0], top[1]);
-            const float x = top[0] == -INFINITY ? top[0] : top[0] * sc, y = top[0] == -INFINITY ? top[0] : x + lv;
+            const float x = top[0] == -INFINITY ? top[0] : fmaf(top[0], sc, -kAbove), y = top[0] == -INFINITY ? top[0] : x + lv;
             float alpha = 1.f;
             if (over && x > r.m) {
                 r.l *= ex2_approx(r.m - x);

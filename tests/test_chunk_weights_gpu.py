@@ -1,0 +1,45 @@
+"""Chunk attention's weights and row sums where scores and value scales are far apart."""
+import pytest
+import torch
+
+from block_sparse_long_pool_gb300 import binding
+from tests.chunk_utils import BLK, D, Chunk
+
+pytestmark = pytest.mark.gpu
+
+
+def ws(c):
+    return binding.paged_chunk_workspace(c.B, c.H_q, c.H_kv)
+
+
+@pytest.mark.parametrize("above", [11.5, 14.5])
+@pytest.mark.parametrize("at", [0, 70])
+def test_small_weights_behind_a_token_of_none(at, above):
+    # a token `above` nats over all others whose values are next to nothing: the others' weights carry the output.
+    # More items than a GPU has SMs, so that most of them are one CTA's
+    B, H, G = 40, 4, 2
+    c = Chunk([2000] * B, [3] * B, H, G, seed=31)
+    c.scale.fill_(1.0)
+    c.pages.copy_(c.pages.float().abs().to(torch.float8_e4m3fn))   # positive values: rounding of the weights does not average out
+    c.Q.zero_()
+    c.Q[..., 0] = 1.0
+    c.pages[:, :, 0] = 0.0
+    c.pages[:, :, 0, :, 0] = -0.5
+    for b in range(B):
+        p = int(c.table[b, at // BLK])
+        c.pages[p, :, 0, at % BLK, 0] = above - 0.5
+        c.pages[p, :, 1, at % BLK] = 2.0 ** -9
+    for b in range(B):   # (any bytes behind the last token)
+        c.pages[int(c.table[b, 2003 // BLK]), :, :, 2003 % BLK:] = float("nan")
+    c.call(ws(c), scale=1.0)
+    torch.cuda.synchronize()
+    assert c.status.item() == 0
+    O, _, _, _ = c.expected(1.0)
+    # Weights in f16 relative to 2^-8 of the largest of a page: 2^-11 of each where that is 2^-14 or more, so down to 2^-22 of
+    # the largest (14.5 nats are 2^20.9), and 2^-33 of the largest below.  Scores are exact but for the product with log2 e and
+    # the exponent's sum (2^-23 of 21 each, times ln 2), 2^x by 2^-22: 2^-17 together.  Values positive: a relative bound.
+    # O in bf16: 2^-8.
+    tol = O.abs() * (2.0 ** -8 + (2.0 ** -11 + 2.0 ** -16) * (1 + 2.0 ** -8))
+    tol = tol + 2.0 ** -33 * 448 * 2003
+    err = (c.O.double() - O).abs()
+    assert (err <= tol).all(), f"O off by {(err / O.abs()).max().item():.3g}"
