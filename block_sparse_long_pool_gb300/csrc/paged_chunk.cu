@@ -49,6 +49,7 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 // 30720 tokens 824 us and 827, 64 requests 342 and 342; with weights of 2^15 together in place of f16's most 848 and 378.)
 constexpr float kAbove = 8.f;
 constexpr float kMost = 65504.f;                  // of a page's weights together, in f16: beyond it the row's reference is taken anew
+constexpr float kMostFar = 0x1p64f;               // of a page's exponentials for l alone, where they are not O's weights
 constexpr float kFarWeight = 60.f;                // log2 of the largest factor from a page's weights to O's
 
 constexpr int kSoftmaxWarps = 4 * kTiles;
@@ -917,6 +918,10 @@ __device__ __forceinline__ void weigh(Row &r, uint32_t (&s)[2][32], uint32_t p_t
 #pragma unroll
                 for (int i = 0; i < 64; ++i)
                     p += ex2_approx(fmaf(__uint_as_float(s[i >> 5][i & 31]), sc, -m_ref));
+                // scores may have grown where the weights of O, for their small values, have not
+                over = over || (far && !(p <= kMostFar));
+                if (turn == 0 && __any_sync(0xffffffffu, over))
+                    continue;
                 r.l += far ? p : 0.f;
                 add = far ? 0.f : add;
             }

@@ -43,3 +43,24 @@ def test_small_weights_behind_a_token_of_none(at, above):
     tol = tol + 2.0 ** -33 * 448 * 2003
     err = (c.O.double() - O).abs()
     assert (err <= tol).all(), f"O off by {(err / O.abs()).max().item():.3g}"
+
+
+@pytest.mark.parametrize("high", [88.0, 200.0])
+@pytest.mark.parametrize("vs", [2.0 ** -120, 0.0])
+@pytest.mark.parametrize("last", ["high", "low"])
+def test_a_page_of_small_values_far_above(high, vs, last):
+    # scores 2^127 and more above the first page's, with values that add next to nothing; then a page that does
+    # (where it is as high), or one that is far below again
+    c = Chunk([170], [20], 1, 4, seed=32)
+    c.scale.fill_(1.0)
+    c.Q.zero_()
+    c.Q[..., 0] = 1.0
+    c.pages[:, :, 0] = 0.0
+    c.pages[int(c.table[0, 1]), :, 0, :, 0] = high
+    if last == "high":
+        c.pages[int(c.table[0, 2]), :, 0, :, 0] = high
+    c.pages[int(c.table[0, 2]), :, :, 62:] = float("nan")
+    c.scale[int(c.table[0, 1]), :, 1] = vs
+    c.call(ws(c), scale=1.0)
+    c.check(1.0)
+    assert c.lse.isfinite().all() and (c.lse > torch.tensor(high).to(torch.float8_e4m3fn).item()).all()
