@@ -89,14 +89,6 @@ __device__ __forceinline__ int saturate(long long v)
     return v > INT_MAX ? INT_MAX : static_cast<int>(v);
 }
 
-// An unsound input is reported in the place of a refusal too, so that a step with both reports the
-// same whichever thread is first.
-__device__ __forceinline__ void report_unsound(int *status)
-{
-    if (status != nullptr && atomicCAS(status, 0, SPARSE_ERR_BAD_INDEX) == SPARSE_ERR_NO_PAGES)
-        atomicCAS(status, SPARSE_ERR_NO_PAGES, SPARSE_ERR_BAD_INDEX);
-}
-
 // Pages that a granted request took.
 __device__ __forceinline__ int pages_taken(const int *cu, const int *first, int b)
 {

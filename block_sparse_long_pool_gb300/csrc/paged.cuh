@@ -46,6 +46,21 @@ __device__ __forceinline__ float2 f8x2_to_float2(uint32_t x)
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
+// An unsound input is reported in the place of a refusal too, so that a step with both reports the
+// same whichever thread is first.
+__device__ __forceinline__ void report_unsound(int *status)
+{
+    if (status != nullptr && atomicCAS(status, 0, SPARSE_ERR_BAD_INDEX) == SPARSE_ERR_NO_PAGES)
+        atomicCAS(status, SPARSE_ERR_NO_PAGES, SPARSE_ERR_BAD_INDEX);
+}
+
+// The results of a call that gave up are not to be used: nothing milder that the word holds may hide it.
+__device__ __forceinline__ void report_timeout(int *status)
+{
+    if (status != nullptr)
+        atomicExch(status, SPARSE_ERR_TIMEOUT);
+}
+
 __device__ __forceinline__ bool is_pow2(float x)
 {
     return (__float_as_uint(x) & 0x7fffffu) == 0;

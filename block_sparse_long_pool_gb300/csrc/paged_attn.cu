@@ -793,16 +793,8 @@ __device__ __forceinline__ bool finish_part(const PagedAttnParams &p, const Stat
     return true;
 }
 
-// A call that gave up leaves counts behind, with which later merges come too early: nothing milder
-// that the word holds may hide it.
-__device__ __forceinline__ void report_timeout(int *status)
-{
-    if (status != nullptr)
-        atomicExch(status, SPARSE_ERR_TIMEOUT);
-}
-
-// A wait ran out: report it, in the workspace too, for calls whose caller did not look; and stay for longer than any load in flight takes to land in
-// this CTA's shared memory.
+// A wait ran out: report it, in the workspace too, for calls whose caller did not look (the call leaves counts behind, with which
+// later merges come too early); and stay for longer than any load in flight takes to land in this CTA's shared memory.
 __device__ __forceinline__ void give_up(const PagedAttnParams &p, int lane)
 {
     if (lane == 0) {

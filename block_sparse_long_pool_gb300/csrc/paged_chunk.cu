@@ -298,7 +298,7 @@ __device__ __forceinline__ void find_start(const ChunkParams &p, uint8_t *base, 
     }
     const int few = __reduce_add_sync(0xffffffffu, static_cast<int>(min(items, 1LL << 20)));   // more than CTAs is all the same
     if (bad && blockIdx.x == 0)
-        report(p.status, SPARSE_ERR_BAD_INDEX);
+        report_unsound(p.status);
     long long up = sum;
     int cup = count;
 #pragma unroll
@@ -469,9 +469,9 @@ __device__ __forceinline__ void page_loop(const ChunkParams &p, uint8_t *base, u
         }
     }
     if (bad)
-        report(p.status, SPARSE_ERR_BAD_INDEX);
+        report_unsound(p.status);
     if (!ok)
-        report(p.status, SPARSE_ERR_TIMEOUT);
+        report_timeout(p.status);
 }
 
 __device__ __forceinline__ const Step *step_of(const uint8_t *base, int f)
@@ -581,7 +581,7 @@ __device__ __forceinline__ void convert_loop(const ChunkParams &p, uint8_t *base
             break;
     }
     if (!ok)
-        report(p.status, SPARSE_ERR_TIMEOUT);
+        report_timeout(p.status);
 }
 
 __device__ __forceinline__ void prefetch_values(const uint8_t *pages, int at)
@@ -625,7 +625,7 @@ __device__ __forceinline__ void key_loop(const CUtensorMap *map, const uint8_t *
             prefetch_values(pages, z);
     }
     if (!ok)
-        report(status, SPARSE_ERR_TIMEOUT);
+        report_timeout(status);
     // no copy is in flight when the block ends
     for (int i = f > kKStages ? f - kKStages : 0; i < f; ++i)
         mbar_wait(bars + 8 * (kKFull + i % kKStages), (i / kKStages) & 1, kWaitNs);
@@ -722,7 +722,7 @@ __device__ __forceinline__ void mma_loop(uint8_t *base, uint32_t base_s, uint32_
             break;
     }
     if (!ok)
-        report(status, SPARSE_ERR_TIMEOUT);
+        report_timeout(status);
     // every product is done before the tensor memory is given back
     __syncwarp();
     if (elect_one())
@@ -1088,7 +1088,7 @@ __device__ __forceinline__ void softmax_loop(const ChunkParams &p, uint8_t *base
         fill += it.j1 - it.j0;
     }
     if (!ok && lane == 0)
-        report(p.status, SPARSE_ERR_TIMEOUT);
+        report_timeout(p.status);
     if (t == 0 && tid == 0) {
         p.tails[blockIdx.x] = ok ? tail : make_int4(-1, 0, 0, 0);
         p.heads[blockIdx.x] = ok ? head : 0;

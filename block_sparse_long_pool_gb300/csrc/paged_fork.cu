@@ -26,13 +26,6 @@ constexpr int kForkCluster = 16;   // 240 samples of 32K tokens forked and ended
 constexpr int kForkB = 4096;
 constexpr int kHolder = -(1 << 30);   // a count's place, less b: request b is its page's last holder, and ends
 
-// The unsound input is reported where a refusal has been, too.
-__device__ __forceinline__ void report_unsound(int *status)
-{
-    if (status != nullptr && atomicCAS(status, 0, SPARSE_ERR_BAD_INDEX) == SPARSE_ERR_NO_PAGES)
-        atomicCAS(status, SPARSE_ERR_NO_PAGES, SPARSE_ERR_BAD_INDEX);
-}
-
 struct ForkParams {
     const int *src, *fork_len;
     int *seq_len, *table, *extra, *free_pages, *n_free, *copy_src, *copy_dst;

@@ -692,9 +692,9 @@ SPARSE_API size_t sparse_paged_decode_attn_f8_workspace_size(int B, int H_q, int
  * A token's values that no row sees are never used, whatever bytes they hold; NaN among the
  * values of a token reaches the rows that see it and no others.  A page outside [0, n_pages)
  * (left out), rows outside [0, n_tok) (left out) and positions past 64 max_blocks (they see
- * the table's tokens) are reported as SPARSE_ERR_BAD_INDEX; a call that gives up waiting as
- * SPARSE_ERR_TIMEOUT (O and lse are then not to be used).  The result does not depend on
- * timing.
+ * the table's tokens) are reported as SPARSE_ERR_BAD_INDEX, also where the word holds
+ * SPARSE_ERR_NO_PAGES; a call that gives up waiting as SPARSE_ERR_TIMEOUT, whatever the word
+ * held before (O and lse are then not to be used).  The result does not depend on timing.
  * Scores take q in two e4m3 terms: elements below 2^-9 of a row's largest are off by up to 2^-17 of it.
  * Weights times their pages' value scales are rounded to f16: each is off by 2^-11 of itself, or 2^-33 of the row's
  * largest where that is more.

@@ -1,0 +1,28 @@
+"""Chunk attention of inputs that are not as they should be: what is reported, and what stays as it was."""
+import pytest
+import torch
+
+from block_sparse_long_pool_gb300 import binding
+from tests.chunk_utils import Chunk
+
+pytestmark = pytest.mark.gpu
+
+
+def ws(c):
+    return binding.paged_chunk_workspace(c.B, c.H_q, c.H_kv)
+
+
+def test_a_bad_page_is_reported_where_the_plan_refused_a_request():
+    c = Chunk([300, 50], [40, 6], 1, 4, seed=42)
+    c.table[0, 2] = c.n_pages
+    c.status.fill_(binding.SPARSE_ERR_NO_PAGES)
+    c.call(ws(c))
+    c.check(status=binding.SPARSE_ERR_BAD_INDEX)
+    c.table[0, 2] = 0
+    c.status.fill_(binding.SPARSE_ERR_NO_PAGES)
+    c.call(ws(c))
+    c.check(status=binding.SPARSE_ERR_NO_PAGES)   # a sound call leaves the word as it is
+    c.table[0, 2] = c.n_pages
+    c.status.fill_(binding.SPARSE_ERR_TIMEOUT)
+    c.call(ws(c))
+    c.check(status=binding.SPARSE_ERR_TIMEOUT)
