@@ -3,7 +3,7 @@
 // Pair i of a row at position t turns by t f_i: y_a = s (x_a cos - x_b sin), y_b = s (x_b cos +
 // x_a sin), fp32, rounded once.  The angle in turns, t f_i / 2 pi mod 1, is taken in 64-bit fixed
 // point: F_i = (f_i / 2 pi mod 1) 2^64 once a CTA, then t F_i mod 2^64 by an integer product, off by
-// 2^-34 turns at most; its upper 32 bits, within half a turn of zero, go to sincospif.  (t f_i in fp32 is
+// 1.1 2^-33 turns at most; its upper 32 bits, within half a turn of zero, go to sincospif.  (t f_i in fp32 is
 // off by half a step of its own size: at position 10^6 by 1/32 radian.)  Sines and cosines are
 // worked out once a token and pair for all its heads.
 #include <math.h>
@@ -32,12 +32,14 @@ struct RopeParams {
     int heads_per_cta;
 };
 
-// f / 2 pi mod 1, in 2^-64.
+// f / 2 pi mod 1, in 2^-64, off by 1.1 of them at most for |f| <= 2^40.  Of |f|: a fraction taken of a negative number, so
+// with 1 added, would be rounded to 2^-53.  What is negative is so mod 2^64.
 __device__ __forceinline__ unsigned long long turns_of(double f)
 {
     constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;   // 1 / 2 pi, and what that leaves of it
-    const double hi = f * kHi, lo = fma(f, kHi, -hi) + f * kLo;
-    return __double2ull_rn((hi - floor(hi)) * 0x1p64) + static_cast<unsigned long long>(__double2ll_rn(lo * 0x1p64));
+    const double a = fabs(f), hi = a * kHi, lo = fma(a, kHi, -hi) + a * kLo;
+    const unsigned long long t = __double2ull_rn((hi - floor(hi)) * 0x1p64) + static_cast<unsigned long long>(__double2ll_rn(lo * 0x1p64));
+    return f < 0.0 ? 0ull - t : t;
 }
 
 // Eight elements of a row: bf16 in a 16-byte piece.

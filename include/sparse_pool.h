@@ -717,7 +717,8 @@ SPARSE_API size_t sparse_paged_chunk_attn_f8_workspace_size(int B, int H_q, int 
  *     factor * (a cos x - b sin x),  factor * (b cos x + a sin x),  x = t * inv_freq[i],
  * in fp32, rounded once; the elements from rot_dim on are copied.
  *   interleaved  0: pair i is elements i and i + rot_dim / 2; otherwise 2 i and 2 i + 1.
- *   inv_freq     [rot_dim / 2] fp64, finite: the angle is that of the exact product at any position.
+ *   inv_freq     [rot_dim / 2] fp64, of either sign, at most 2^40 in size: the angle is that of the exact
+ *                product at any position, within 2^-31 turns before its sine and cosine are taken in fp32.
  *   pos          [n_tok] int32; a row with a negative position is not written (padding, and
  *                the rows of requests without pages, as in sparse_page_plan's tok_pos).
  *   Q, K         [n_tok][H][128] bf16, tokens q_stride / k_stride elements apart (>= H * 128, a
