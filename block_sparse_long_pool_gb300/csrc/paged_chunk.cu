@@ -287,9 +287,10 @@ __device__ __forceinline__ void find_start(const ChunkParams &p, uint8_t *base, 
     const int per = (p.B + kThreads - 1) / kThreads, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
     long long sum = 0, items = 0;
     int count = 0;
-    bool bad = false;
+    bool bad = false, falls = false;   // cu_new falls: requests could have the same rows
     for (int b = b0; b < b1; ++b) {
         const Request r = request_of(p, b, &bad);
+        falls = falls || p.cu_new[b + 1] < p.cu_new[b];
         if (r.n > 0) {
             sum += p.H_kv * work_upto(p, r, items_of(p, r.n));
             ++count;
@@ -297,7 +298,8 @@ __device__ __forceinline__ void find_start(const ChunkParams &p, uint8_t *base, 
         }
     }
     const int few = __reduce_add_sync(0xffffffffu, static_cast<int>(min(items, 1LL << 20)));   // more than CTAs is all the same
-    if (bad && blockIdx.x == 0)
+    const bool warp_falls = __any_sync(0xffffffffu, falls);
+    if ((bad || falls) && blockIdx.x == 0)
         report_unsound(p.status);
     long long up = sum;
     int cup = count;
@@ -313,7 +315,7 @@ __device__ __forceinline__ void find_start(const ChunkParams &p, uint8_t *base, 
     if (lane == 31) {
         warp_work[warp] = up;
         warp_live[warp] = cup;
-        warp_items[warp] = few;
+        warp_items[warp] = warp_falls ? -1 : few;
     }
     if (tid == 0)
         s->n_live = 0;
@@ -328,7 +330,10 @@ __device__ __forceinline__ void find_start(const ChunkParams &p, uint8_t *base, 
         total += warp_work[w];
         ctotal += warp_live[w];
         all_items += warp_items[w];
+        falls = falls || warp_items[w] < 0;
     }
+    if (falls)
+        total = 0;   // nothing is done
     const Shares shares(total, all_items, gridDim.x);
     const long long lo = shares.lo(blockIdx.x), hi = shares.hi(blockIdx.x);
     if (tid == 0 && lo >= hi) {

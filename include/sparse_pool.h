@@ -684,7 +684,8 @@ SPARSE_API size_t sparse_paged_decode_attn_f8_workspace_size(int B, int H_q, int
  *                of one projection's rows.
  *   cu_new       [B + 1] int32, start [B] int32.  start[b] < 0 (a request that got no pages):
  *                its rows see nothing, O = 0 and lse = -inf.  Rows before cu_new[0] and from
- *                cu_new[B] on are left as they were.
+ *                cu_new[B] on are left as they were.  A cu_new that falls (two requests could
+ *                have the same rows) is reported as SPARSE_ERR_BAD_INDEX, and nothing is written.
  *   O, lse       [n_tok][H_q][128] bf16 and [n_tok][H_q] fp32 (or NULL), contiguous.
  *   scale        as for sparse_paged_decode_attn_f8.
  *   workspace    sparse_paged_chunk_attn_f8_workspace_size() bytes, 16-byte aligned, of any

@@ -12,6 +12,16 @@ def ws(c):
     return binding.paged_chunk_workspace(c.B, c.H_q, c.H_kv)
 
 
+@pytest.mark.parametrize("cu", [[0, 40, 10, 50], [30, 30, 0, 80], [0, 40, 80, 79]])
+def test_rows_of_two_requests_are_refused(cu):
+    c = Chunk([100, 100, 100], [40, 0, 40], 1, 4, seed=41)
+    c.cu.copy_(torch.tensor(cu, dtype=torch.int32))
+    c.call(ws(c))
+    torch.cuda.synchronize()
+    assert c.status.item() == binding.SPARSE_ERR_BAD_INDEX
+    assert (c.O == 7).all() and (c.lse == 7).all()
+
+
 def test_a_bad_page_is_reported_where_the_plan_refused_a_request():
     c = Chunk([300, 50], [40, 6], 1, 4, seed=42)
     c.table[0, 2] = c.n_pages
