@@ -36,3 +36,22 @@ def test_a_bad_page_is_reported_where_the_plan_refused_a_request():
     c.status.fill_(binding.SPARSE_ERR_TIMEOUT)
     c.call(ws(c))
     c.check(status=binding.SPARSE_ERR_TIMEOUT)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf")])
+@pytest.mark.parametrize("start,new,row", [([70], [60], 3), ([12000], [5], 3), ([70, 30] * 90, [3, 60] * 90, 61)])
+def test_infinite_queries(start, new, row, value):
+    # an item of one CTA, one that many share, one of many
+    c = Chunk(start, new, 1, 4, seed=43)
+    w = ws(c)
+    c.call(w)
+    c.check()
+    O, lse = c.O.clone(), c.lse.clone()
+    c.Q[row, 1, 5] = value
+    c.Q[row, 2, 127], c.Q[row, 2, 0] = value, -value
+    c.call(w)
+    torch.cuda.synchronize()
+    rest = torch.ones_like(lse, dtype=torch.bool)
+    rest[row, 1] = rest[row, 2] = False
+    assert c.O[~rest].isnan().all() and c.lse[~rest].isnan().all()
+    assert torch.equal(c.O[rest], O[rest]) and torch.equal(c.lse[rest], lse[rest])
