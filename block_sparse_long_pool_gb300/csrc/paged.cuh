@@ -11,6 +11,16 @@ namespace sp_host {
 // swizzle: the paged cache, a tile the keys or the values of a (page, head).
 int make_page_tensor_map(CUtensorMap *map, const void *base, long long tiles);
 
+// The largest cluster of most, most / 2, ... 2 CTAs that fits() finds room for, or 1: a part of a GPU may not have
+// the SMs side by side that the whole has.
+template <typename F>
+int largest_cluster(int most, F fits)
+{
+    while (most > 1 && !fits(most))
+        most /= 2;
+    return most;
+}
+
 }  // namespace sp_host
 
 namespace {

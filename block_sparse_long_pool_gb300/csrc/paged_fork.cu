@@ -11,6 +11,7 @@
 // Cluster barriers stand between the steps.
 // Copy.  Pieces of 16 KB of page pairs and of compressed keys, 4 loads of 16 bytes a thread
 // before the first store, over as many CTAs as the GPU holds.
+#include <atomic>
 #include <limits.h>
 
 #include "common.cuh"
@@ -22,7 +23,7 @@ using namespace sp;
 
 constexpr int kForkThreads = 1024;
 constexpr int kForkWarps = kForkThreads / 32;
-constexpr int kForkCluster = 16;   // 240 samples of 32K tokens forked and ended 45.6 us, 61.6 with 8
+constexpr int kForkCluster = 16;   // at most: 240 samples of 32K tokens forked and ended 45.6 us, 61.6 with 8
 constexpr int kForkB = 4096;
 constexpr int kHolder = -(1 << 30);   // a count's place, less b: request b is its page's last holder, and ends
 
@@ -396,6 +397,52 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) paged_copy_kernel(con
     }
 }
 
+// The launch of `ctas` CTAs as one cluster.
+cudaLaunchConfig_t fork_config(cudaLaunchAttribute *attr, int ctas, int smem, void *stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(kForkThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cfg;
+}
+
+// CTAs of a large fork's cluster on this device, found once: the result does not depend on their number.
+int fork_cluster(int device, int *ctas)
+{
+    static std::atomic<int> found[64];
+    int n = found[device].load();
+    if (n == 0) {
+        const void *kern = reinterpret_cast<const void *>(page_fork_kernel);
+        // clusters of more than eight have to be asked for
+        const int rc = sp_host::cuda_status(cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1), "sparse_page_fork");
+        if (rc != SPARSE_OK)
+            return rc;
+        n = sp_host::largest_cluster(kForkCluster, [&](int c) {
+            cudaLaunchAttribute attr[2];
+            cudaLaunchConfig_t cfg = fork_config(attr, c, (3 * kForkB + 1) * static_cast<int>(sizeof(int)), nullptr);
+            cfg.numAttrs = 1;   // the cluster alone
+            int placed = 0;
+            const cudaError_t e = cudaOccupancyMaxActiveClusters(&placed, kern, &cfg);
+            if (e != cudaSuccess)
+                (void)cudaGetLastError();   // a failed query leaves an error behind
+            return e == cudaSuccess && placed > 0;
+        });
+        found[device].store(n);
+    }
+    *ctas = n;
+    return SPARSE_OK;
+}
+
 size_t fork_words(int B, int max_blocks)
 {
     return 4 * kForkCluster * kForkWarps + 2 * static_cast<size_t>(B) * ((static_cast<size_t>(max_blocks) + 31) / 32);
@@ -438,33 +485,19 @@ extern "C" SPARSE_API int sparse_page_fork(const int *src, const int *fork_len, 
         return rc;
     const void *kern = reinterpret_cast<const void *>(page_fork_kernel);
     const int smem = (3 * B + 1) * static_cast<int>(sizeof(int));
-    static int configured[64], wide[64];
+    static int configured[64];
     rc = sp_host::configure_kernel(kern, (3 * kForkB + 1) * static_cast<int>(sizeof(int)), dev.device, configured);
-    if (rc == SPARSE_OK && wide[dev.device] == 0) {   // clusters of more than eight have to be asked for
-        rc = sp_host::cuda_status(cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1), name);
-        wide[dev.device] = rc == SPARSE_OK;
-    }
     if (rc != SPARSE_OK)
         return rc;
     uint32_t *masks = static_cast<uint32_t *>(workspace) + 4 * kForkCluster * kForkWarps;
     ForkParams p{src, fork_len, seq_len, block_table, page_extra, free_pages, n_free, copy_src, copy_dst, static_cast<int *>(workspace),
                  masks, masks + static_cast<size_t>(B) * ((static_cast<size_t>(max_blocks) + 31) / 32), status, B, max_blocks, n_pages};
     // a cluster's barriers cost more than a few thousand blocks do
-    const unsigned ctas = static_cast<long long>(B) * max_blocks <= 32 * kForkThreads ? 1 : kForkCluster;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kForkThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-    cfg.stream = static_cast<cudaStream_t>(stream);
+    int ctas = 1;
+    if (static_cast<long long>(B) * max_blocks > 32 * kForkThreads && (rc = fork_cluster(dev.device, &ctas)) != SPARSE_OK)
+        return rc;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ctas;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    const cudaLaunchConfig_t cfg = fork_config(attr, ctas, smem, stream);
     void *args[] = {&p};
     return sp_host::cuda_status(cudaLaunchKernelExC(&cfg, kern, args), name);
 }
