@@ -2,6 +2,8 @@
 // through them.  Integers only, the same on the host, where the tests replay them.
 #pragma once
 
+#include <limits.h>
+
 #include "common.cuh"
 
 namespace {
@@ -68,6 +70,13 @@ struct Start {
     int live, head, chunk, n_live;
     int b, row, n, start;
 };
+
+// The work of a request's largest item, within 32 bits.
+__host__ __device__ __forceinline__ int largest_of(const ChunkList &p, const Request &r)
+{
+    const int last = items_of(p, r.n) - 1;
+    return static_cast<int>(min(work_upto(p, r, last + 1) - work_upto(p, r, last), static_cast<long long>(INT_MAX)));
+}
 
 // An item: up to two tiles of one KV head's query rows, and the steps [j0, j1) of its tokens that
 // are this CTA's.
@@ -160,13 +169,28 @@ struct Walk {
 // Equal shares of the work for the CTAs of a grid: CTA c has [lo, hi), none where it is past n.
 struct Shares {
     long long total, n, each, rest;   // rest of them have one more
-    __host__ __device__ __forceinline__ Shares(long long work, int items, int grid) : total(work)
+    // `items` of them, the largest of work `largest`.
+    __host__ __device__ __forceinline__ Shares(long long work, int items, int largest, int grid) : total(work)
     {
-        // as many CTAs as there is work for; where they are more than items, the same number an item (of equal items no
-        // CTA then has parts of two: one request of 4K tokens, 2 KV heads 26 us with 14 CTAs, 32 with 15)
+        // As many CTAs as there is work for.  Where they are more than the items, a CTA may have parts of two, at the cost of
+        // another item; with the same number of CTAs an item it has of one, if items are equal.  (Unequal ones in several parts
+        // each still gain by borders that fall on those of heads, those of about a CTA each do not.)  That is done where
+        // the CTAs left over cost less (us, with and without; 32 query heads over 8 where nothing else is said):
+        //   equal items      144 of 1000 tokens 27.0 and 32.8, of 8000 106.7 and 109.0, 100 of 2000 38.6 and 36.9; 16 rows behind
+        //                    1000 tokens, 8 heads over 2, 17.9 and 18.4
+        //   several parts    500 rows of a prompt, 16 heads over 4, 26.5 and 36.7; 100 rows behind 1000 tokens, the same heads,
+        //                    26.1 and 33.4, 250 behind 4000 41.7 and 43.9
+        // and not for
+        //   long ones        behind 32K tokens 512 rows 251 and 218, 640 rows (80 items) 464 and 267, 768 467 and 312, 1024 472 and 408;
+        //                    700 behind 4000, 16 heads over 4, 57.1 and 54.6
+        //   unequal, a CTA each  18 rows of requests of 37 to 100 tokens 23.8 and 18.3, 200 rows of 12 requests 42.0 and 37.6
         n = max(1LL, min(static_cast<long long>(grid), total / kMinWork));
-        if (items > 0 && items < n)
-            n -= n % items;
+        if (items > 0 && items < n) {
+            const bool equal = static_cast<long long>(items) * largest == total;
+            const long long m = n - n % items, tokens = total - static_cast<long long>(items) * kItemCost;
+            if ((equal || 2 * items <= n) && tokens / m <= tokens / n + (equal ? kItemCost : kItemCost / 8))
+                n = m;
+        }
         each = total / n;
         rest = total - each * n;
     }

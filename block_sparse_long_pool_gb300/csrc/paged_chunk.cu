@@ -92,8 +92,8 @@ constexpr int kOffCtrl = kOffRec + 2 * 16 * 32;   // int [16]
 constexpr int kOffStart = kOffCtrl + 64;          // Start
 constexpr int kOffQs = kOffStart + 64;            // float [tiles][128]
 constexpr int kOffNan = kOffQs + kTiles * kTileRows * 4;   // int [2][128], then int [2]
-constexpr int kOffScan = kOffNan + 2 * kD * 4 + 16;        // long long [32], int [32], int [32]
-constexpr int kOffLive = kOffScan + 32 * 16;               // uint16 [kMaxB]
+constexpr int kOffScan = kOffNan + 2 * kD * 4 + 16;        // long long [32], int [32], int [32], int [32]
+constexpr int kOffLive = kOffScan + 32 * 20;               // uint16 [kMaxB]
 constexpr int kSmem = kOffLive + 2 * kMaxB + 1024;
 static_assert(kNumBars * 8 <= 320 && kOffRec % 16 == 0 && kOffStart % 8 == 0 && kOffScan % 8 == 0, "alignment");
 static_assert(kSmem <= 232448, "shared memory of a CTA");
@@ -279,14 +279,14 @@ __device__ __forceinline__ void find_start(const ChunkParams &p, uint8_t *base, 
 {
     long long *warp_work = reinterpret_cast<long long *>(base + kOffScan);
     int *warp_live = reinterpret_cast<int *>(base + kOffScan + 32 * 8);
-    int *warp_items = warp_live + 32;
+    int *warp_items = warp_live + 32, *warp_largest = warp_items + 32;
     uint16_t *list = reinterpret_cast<uint16_t *>(base + kOffLive);
     Start *s = reinterpret_cast<Start *>(base + kOffStart);
     constexpr int kWarps = kThreads / 32;
     const int warp = tid >> 5, lane = tid & 31;
     const int per = (p.B + kThreads - 1) / kThreads, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
     long long sum = 0, items = 0;
-    int count = 0;
+    int count = 0, largest = 0;
     bool bad = false, falls = false;   // cu_new falls: requests could have the same rows
     for (int b = b0; b < b1; ++b) {
         const Request r = request_of(p, b, &bad);
@@ -295,9 +295,11 @@ __device__ __forceinline__ void find_start(const ChunkParams &p, uint8_t *base, 
             sum += p.H_kv * work_upto(p, r, items_of(p, r.n));
             ++count;
             items += static_cast<long long>(p.H_kv) * items_of(p, r.n);
+            largest = max(largest, largest_of(p, r));
         }
     }
     const int few = __reduce_add_sync(0xffffffffu, static_cast<int>(min(items, 1LL << 20)));   // more than CTAs is all the same
+    largest = __reduce_max_sync(0xffffffffu, largest);
     const bool warp_falls = __any_sync(0xffffffffu, falls);
     if ((bad || falls) && blockIdx.x == 0)
         report_unsound(p.status);
@@ -316,6 +318,7 @@ __device__ __forceinline__ void find_start(const ChunkParams &p, uint8_t *base, 
         warp_work[warp] = up;
         warp_live[warp] = cup;
         warp_items[warp] = warp_falls ? -1 : few;
+        warp_largest[warp] = largest;
     }
     if (tid == 0)
         s->n_live = 0;
@@ -331,10 +334,11 @@ __device__ __forceinline__ void find_start(const ChunkParams &p, uint8_t *base, 
         ctotal += warp_live[w];
         all_items += warp_items[w];
         falls = falls || warp_items[w] < 0;
+        largest = max(largest, warp_largest[w]);
     }
     if (falls)
         total = 0;   // nothing is done
-    const Shares shares(total, all_items, gridDim.x);
+    const Shares shares(total, all_items, largest, gridDim.x);
     const long long lo = shares.lo(blockIdx.x), hi = shares.hi(blockIdx.x);
     if (tid == 0 && lo >= hi) {
         s->at = s->lo = s->hi = total;

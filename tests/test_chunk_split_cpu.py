@@ -13,6 +13,7 @@ CSRC = os.path.join(ROOT, "block_sparse_long_pool_gb300", "csrc")
 HARNESS = r"""
 #include <cstdio>
 #include <algorithm>
+#include <cstdlib>
 #include <vector>
 #include "chunk_split.cuh"
 
@@ -27,10 +28,11 @@ struct Lists {
             cu.push_back(cu.back() + x);
         p = ChunkList{cu.data(), start.data(), max_blocks, cu.back() + pad, static_cast<int>(n.size()), H_kv, G, kTileRows / G};
     }
-    // the list of requests with rows, the work and the number of items
-    long long sum(int *items)
+    // the list of requests with rows, the work, the number of items and the largest's work
+    long long sum(int *items, int *largest)
     {
         long long total = 0, all = 0;
+        *largest = 0;
         bool bad = false;
         live.clear();
         for (int b = 0; b < p.B; ++b) {
@@ -39,6 +41,7 @@ struct Lists {
                 live.push_back(static_cast<uint16_t>(b));
                 total += p.H_kv * work_upto(p, r, items_of(p, r.n));
                 all += static_cast<long long>(p.H_kv) * items_of(p, r.n);
+                *largest = std::max(*largest, largest_of(p, r));
             }
         }
         *items = static_cast<int>(all < (1 << 20) ? all : 1 << 20);
@@ -71,13 +74,14 @@ static bool fail(const char *what, int c)
     return false;
 }
 
-// Replays a call: `grid` CTAs. False where something is not as it has to be.
-static bool replay(Lists &l, int grid)
+// Replays a call: `grid` CTAs. False where something is not as it has to be. `longest`: the largest share, in tokens of its
+// steps and the cost of an item for every item that the CTA has steps of.
+static bool replay(Lists &l, int grid, long long *longest)
 {
     const ChunkList &p = l.p;
-    int items = 0;
-    const long long total = l.sum(&items);
-    const Shares sh(total, items, grid);
+    int items = 0, largest = 0;
+    const long long total = l.sum(&items, &largest);
+    const Shares sh(total, items, largest, grid);
     // what there is to do: an item a line, steps done so far
     struct Want { int row, n, head, all, done; };
     std::vector<Want> want;
@@ -94,6 +98,7 @@ static bool replay(Lists &l, int grid)
     }
     size_t at = 0;      // the first item that is not finished
     long long edge = 0;
+    *longest = 0;
     for (int c = 0; c < grid; ++c) {
         if (sh.lo(c) != edge || sh.hi(c) < sh.lo(c))
             return fail("shares do not follow one another", c);
@@ -105,6 +110,7 @@ static bool replay(Lists &l, int grid)
         walk.open(p, &s, l.live.data());
         Item it;
         std::vector<Item> mine;
+        long long share = 0;
         while (walk.next(p, it)) {
             if (at == want.size())
                 return fail("an item too many", c);
@@ -114,9 +120,11 @@ static bool replay(Lists &l, int grid)
             w.done = it.j1;
             if (it.j1 == it.all)
                 ++at;
+            share += static_cast<long long>(it.j1 - it.j0) * kKv + kItemCost;
             if (it.all > 0)
                 mine.push_back(it);
         }
+        *longest = std::max(*longest, share);
         // the page warp's groups: the same items' steps, and the queries of those that begin
         Steps steps;
         steps.open(p, &s, l.live.data());
@@ -163,8 +171,19 @@ static int spread(int most)   // about as many of every size
     return draw((1 << draw(32 - __builtin_clz(static_cast<unsigned>(most) | 1u))) + 1);
 }
 
-int main()
+int main(int argc, char **argv)
 {
+    if (argc > 1) {   // requests, their start, rows, H_kv, G: the longest share of 152 CTAs, and the work
+        const int B = atoi(argv[1]), at = atoi(argv[2]), n = atoi(argv[3]), H = atoi(argv[4]), G = atoi(argv[5]);
+        Lists l(std::vector<int>(B, n), std::vector<int>(B, at), 0, 0, (at + n) / kBlk + 4, H, G);
+        int items, largest;
+        const long long total = l.sum(&items, &largest);
+        long long longest = 0;
+        if (!replay(l, 152, &longest))
+            return 1;
+        printf("%lld %lld", longest, total);
+        return 0;
+    }
     for (int i = 0; i < 4000; ++i) {
         const int B = 1 + spread(100), H = 1 << draw(4), G = 1 + draw(16), most = 1 + spread(20000);
         std::vector<int> n, at;
@@ -175,7 +194,8 @@ int main()
             end = std::max(end, at.back() + n.back());
         }
         Lists l(n, at, draw(3) ? 0 : draw(50), draw(3) ? 0 : draw(50), std::max(1, end / kBlk + draw(5) - (i % 50 == 0)), H, G);
-        if (!replay(l, i % 4 ? 152 : 1 + draw(200))) {
+        long long longest;
+        if (!replay(l, i % 4 ? 152 : 1 + draw(200), &longest)) {
             printf("list %d: B=%d H=%d G=%d\n", i, B, H, G);
             return 1;
         }
@@ -202,3 +222,34 @@ def harness(tmp_path_factory):
 def test_shares_hand_out_every_step_and_fetch_their_own_queries(harness):
     r = subprocess.run([harness], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout
+
+
+def shares(harness, *what):
+    r = subprocess.run([harness, *map(str, what)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
+    return [int(x) for x in r.stdout.split()]
+
+
+ITEM, STEP = 704, 128   # an item's cost beside its tokens, a step's tokens
+
+
+@pytest.mark.parametrize("rows", [512, 576, 640, 700, 768, 900, 1024, 1216])
+@pytest.mark.parametrize("behind", [8000, 32768])
+def test_no_cta_is_left_over_where_items_are_long(harness, rows, behind):
+    # 64 to 152 items: of equal shares none is longer than an even part of the work, a second item's cost and a step
+    longest, total = shares(harness, 1, behind, rows, 8, 4)
+    assert longest <= total / 152 + 2 * ITEM + STEP
+
+
+@pytest.mark.parametrize("heads", [77, 100, 130, 144, 151])
+@pytest.mark.parametrize("tokens", [100, 400, 1000])
+def test_equal_short_items_are_a_cta_each(harness, heads, tokens):
+    longest, _ = shares(harness, 1, tokens - 1, 1, heads, 1)
+    assert longest == -(-tokens // STEP) * STEP + ITEM
+
+
+@pytest.mark.parametrize("rows,heads,behind", [(100, 4, 1000), (500, 4, 0), (16, 2, 1000), (16, 2, 4096)])
+def test_items_in_several_parts_are_not_mixed(harness, rows, heads, behind):
+    # a CTA has steps of one item: at most an even part of the largest, in whole steps, and one item's cost
+    longest, total = shares(harness, 1, behind, rows, heads, 4)
+    assert longest <= total / (heads * -(-rows // 64)) + ITEM
