@@ -1,7 +1,8 @@
 // paged_fork.cu -- requests that share pages: forks and ends, and the copies that a fork needs.
 //
 // Fork.  One cluster, each warp with an equal run of the ending requests' 32-block pieces, in order.
-//   1. A page without further holders is freed: its bit is set in a mask.
+//   1. A page without further holders is freed: its bit is set in a mask, and one taken off its count of zero (in
+//      step 3 the count is looked at: below -1 a second request has ended with the page).
 //   2. Where there are others (in a step of their own, if the call meets any): every request that ends
 //      takes one off the count; where the count falls below zero all its holders end, and the last of them
 //      in request order, found by an atomic minimum of the count's place, frees the page.  So the list's
@@ -143,6 +144,8 @@ __global__ void __launch_bounds__(kForkThreads, 1) page_fork_kernel(const __grid
         if (here && !ok)
             report_unsound(p.status);
         const bool more = ok && p.extra[page] > 0;
+        if (ok && !more)
+            atomicSub(p.extra + page, 1);
         const uint32_t mask = __ballot_sync(0xffffffffu, ok && !more), shared = __ballot_sync(0xffffffffu, more);
         if (lane == 0) {
             p.freed[i] = mask;
@@ -204,17 +207,23 @@ __global__ void __launch_bounds__(kForkThreads, 1) page_fork_kernel(const __grid
     if (rank == 0 && tid == 0 && (listed != held || static_cast<long long>(held) + back > p.n_pages))
         report_unsound(p.status);
     int place = min(held + min(warp_first[me], p.n_pages), p.n_pages);
-    pages([&](int i, int, int page, bool) {
+    bool wrong = false;         // a page freed twice
+    int left = -1, due = -1;
+    pages([&](int i, int b, int page, bool) {
         __syncwarp();   // lane 0's masks
         const uint32_t mask = p.freed[i];
         const int mine = place + __popc(mask & ((1u << lane) - 1u));
         if (mask >> lane & 1u) {
             if (mine < p.n_pages)
                 p.free_pages[mine] = page;
-            p.extra[page] = 0;
+            wrong = wrong || (left != -1 && left != due);   // of the piece before: nothing waits for its count here
+            left = atomicExch(p.extra + page, 0);
+            due = kHolder - b;
         }
         place = min(place + __popc(mask), p.n_pages);
     });
+    if (wrong || (left != -1 && left != due))
+        report_unsound(p.status);
     cluster_sync();
 
     // 4. forks: those that need a page get one in request order, from the end of the list

@@ -758,9 +758,10 @@ SPARSE_API int sparse_rope(const uint16_t *Q, long long q_stride, int H_q, const
  *   workspace    sparse_page_fork_workspace_size() bytes, 16-byte aligned, of any contents.
  *   status       a source outside [0, B) or that does not stay (the request stays as it is), a length
  *                outside [0, 64 max_blocks] (it gives up no pages, its copies end), a page outside
- *                [0, n_pages), an *n_free outside [0, n_pages] (clamped), a count that is too small or more
- *                pages returned than the list holds (dropped) is reported as SPARSE_ERR_BAD_INDEX, also
- *                where the word holds SPARSE_ERR_NO_PAGES.
+ *                [0, n_pages), an *n_free outside [0, n_pages] (clamped), a count that is too small for the
+ *                requests that end with the page (it may then be listed twice) or more pages returned than the
+ *                list holds (dropped) is reported as SPARSE_ERR_BAD_INDEX, also where the word holds
+ *                SPARSE_ERR_NO_PAGES.
  * B <= 4096; n_pages <= 2^25; max_blocks < 2^25; B * ceil(max_blocks / 32) < 2^30.
  */
 SPARSE_API int sparse_page_fork(const int *src, const int *fork_len, int B, int *seq_len, int *block_table,
