@@ -64,19 +64,19 @@ __host__ __device__ __forceinline__ int items_of(const ChunkList &p, int n)
     return n / t + (n % t != 0);
 }
 
+// The work of a request's largest item, its last, within 32 bits.
+__host__ __device__ __forceinline__ int largest_of(const ChunkList &p, const Request &r)
+{
+    const int t = kTiles * p.per_tile;
+    return r.start < 0 ? kItemCost : static_cast<int>(min(static_cast<long long>(r.start) + (r.n - 1) / t * t + kItemCost, static_cast<long long>(INT_MAX)));
+}
+
 // A CTA's first item: where in the list of items it lies.
 struct Start {
     long long at, lo, hi;
     int live, head, chunk, n_live;
     int b, row, n, start;
 };
-
-// The work of a request's largest item, within 32 bits.
-__host__ __device__ __forceinline__ int largest_of(const ChunkList &p, const Request &r)
-{
-    const int last = items_of(p, r.n) - 1;
-    return static_cast<int>(min(work_upto(p, r, last + 1) - work_upto(p, r, last), static_cast<long long>(INT_MAX)));
-}
 
 // An item: up to two tiles of one KV head's query rows, and the steps [j0, j1) of its tokens that
 // are this CTA's.
@@ -184,13 +184,17 @@ struct Shares {
         //   long ones        behind 32K tokens 512 rows 251 and 218, 640 rows (80 items) 464 and 267, 768 467 and 312, 1024 472 and 408;
         //                    700 behind 4000, 16 heads over 4, 57.1 and 54.6
         //   unequal, a CTA each  18 rows of requests of 37 to 100 tokens 23.8 and 18.3, 200 rows of 12 requests 42.0 and 37.6
-        n = max(1LL, min(static_cast<long long>(grid), total / kMinWork));
-        if (items > 0 && items < n) {
+        int ctas = static_cast<int>(max(1LL, min(static_cast<long long>(grid), total / kMinWork)));
+        const int over = items > 0 && items < ctas ? ctas % items : 0;
+        if (over > 0) {
             const bool equal = static_cast<long long>(items) * largest == total;
-            const long long m = n - n % items, tokens = total - static_cast<long long>(items) * kItemCost;
-            if ((equal || 2 * items <= n) && tokens / m <= tokens / n + (equal ? kItemCost : kItemCost / 8))
-                n = m;
+            const int m = ctas - over;
+            // tokens / m - tokens / ctas, without divisions (in fp32, alike in every CTA)
+            const float tokens = static_cast<float>(total - static_cast<long long>(items) * kItemCost);
+            if ((equal || 2 * items <= ctas) && tokens * over <= static_cast<float>(equal ? kItemCost : kItemCost / 8) * m * ctas)
+                ctas = m;
         }
+        n = ctas;
         each = total / n;
         rest = total - each * n;
     }
