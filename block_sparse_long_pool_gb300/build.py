@@ -3,7 +3,7 @@
 Each translation unit is compiled by nvcc in parallel, then linked into
 ``block_sparse_long_pool_gb300/libsparsepool.so``.  No cmake, no torch extension
 machinery: the product is a plain C-ABI shared library.  ``_marshal_<torch version>.so`` beside
-it, from csrc/marshal.cpp by g++, passes tensors from Python to three of its calls; it is left
+it, from csrc/marshal.cpp by g++, passes tensors from Python to the paged cache's calls; it is left
 out where there is no torch, which the library does not need.
 """
 from __future__ import annotations

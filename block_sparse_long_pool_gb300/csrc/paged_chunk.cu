@@ -3,7 +3,7 @@
 // Work.  An item is two tiles of 128 query rows (a token's G heads side by side) of one KV head of one request, with
 // all the tokens they see, 128 at a time: a step.  A persistent grid, one CTA an SM, takes equal shares of the items'
 // work, which is known on the device only: every CTA sums up the requests itself and finds its own first item by
-// search.  So an item may be cut, at a step; its parts are states (O, m, l, mo) in the workspace, which a second
+// search (chunk_split.cuh).  So an item may be cut, at a step; its parts are states (O, m, l, mo) in the workspace, which a second
 // kernel adds up in CTA order.  An item counts as its tokens and kItemCost more.
 //
 // A CTA's warps:
@@ -27,10 +27,10 @@
 // (N = 128 would read 8 KB for 64, but then the next scores wait until both pages' weights are there: 4300 cycles.)
 // The softmax warps work 2600 of the 3300, 128 weights a thread and step at 3 instructions each.  All loops share an
 // instruction cache that loses what it holds past some 16 KB: unrolled as far as registers allow they missed 230 times
-// a step (4300 cycles), these miss next to nothing.  2048 rows behind 30720 tokens, 32 query heads over 8: 782 us, 0.75 of
-// the bf16 matrix rate (834 where no input is left in L2 and the clock is lower); a prompt of 16384: 1590 us, 0.71.  An item's
+// a step (4300 cycles), these miss next to nothing.  2048 rows behind 32768 tokens, 32 query heads over 8: 806 us, 0.72 of
+// the bf16 matrix rate (823 where no input is left in L2); a prompt of 16384: 1642 us, 0.69.  An item's
 // start and end (queries, first scores, O) cost 5 steps, which nothing overlaps: 64 requests, most with one row,
-// 341 us at a floor of 129.  First scores come 9 us after the kernel's start (list, pages, queries: round trips).
+// 344 us at a floor of 129.  First scores come 9 us after the kernel's start (list, pages, queries: round trips).
 #include <limits.h>
 #include <math.h>
 
@@ -46,7 +46,7 @@ constexpr int kMaxB = 4096;
 constexpr uint64_t kWaitNs = 2000000000ull;
 // log2 of a page's largest weight where its row's reference is taken; f16 holds 2^8 times that, and 2^22 times less in full.
 // (A reference at the maximum has all of f16's range above it and 2^14 below: as long either way, 2048 rows behind
-// 30720 tokens 824 us and 827, 64 requests 342 and 342; with weights of 2^15 together in place of f16's most 848 and 378.)
+// 32768 tokens 824 us and 827, 64 requests 342 and 342; with weights of 2^15 together in place of f16's most 848 and 378.)
 constexpr float kAbove = 8.f;
 constexpr float kMost = 65504.f;                  // of a page's weights together, in f16: beyond it the row's reference is taken anew
 constexpr float kMostFar = 0x1p64f;               // of a page's exponentials for l alone, where they are not O's weights

@@ -24,7 +24,7 @@ using namespace sp;
 
 constexpr int kForkThreads = 1024;
 constexpr int kForkWarps = kForkThreads / 32;
-constexpr int kForkCluster = 16;   // at most: 240 samples of 32K tokens forked and ended 45.6 us, 61.6 with 8
+constexpr int kForkCluster = 16;   // at most: 240 samples of 32K tokens forked and ended 45.1 us, 61.6 with 8
 constexpr int kForkB = 4096;
 constexpr int kHolder = -(1 << 30);   // a count's place, less b: request b is its page's last holder, and ends
 
