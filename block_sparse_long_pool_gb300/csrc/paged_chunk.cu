@@ -3,7 +3,7 @@
 // Work.  An item is two tiles of 128 query rows (a token's G heads side by side) of one KV head of one request, with
 // all the tokens they see, 128 at a time: a step.  A persistent grid, one CTA an SM, takes equal shares of the items'
 // work, which is known on the device only: every CTA sums up the requests itself and finds its own first item by
-// search (chunk_split.cuh).  So an item may be cut, at a step; its parts are states (O, m, l, mo) in the workspace, which a second
+// search (chunk_split.cuh).  So an item may be cut, at a step; its parts are states (O, m, l, d) in the workspace, which a second
 // kernel adds up in CTA order.  An item counts as its tokens and kItemCost more.
 //
 // A CTA's warps:
@@ -27,10 +27,10 @@
 // (N = 128 would read 8 KB for 64, but then the next scores wait until both pages' weights are there: 4300 cycles.)
 // The softmax warps work 2600 of the 3300, 128 weights a thread and step at 3 instructions each.  All loops share an
 // instruction cache that loses what it holds past some 16 KB: unrolled as far as registers allow they missed 230 times
-// a step (4300 cycles), these miss next to nothing.  2048 rows behind 32768 tokens, 32 query heads over 8: 806 us, 0.72 of
-// the bf16 matrix rate (823 where no input is left in L2); a prompt of 16384: 1642 us, 0.69.  An item's
+// a step (4300 cycles), these miss next to nothing.  2048 rows behind 32768 tokens, 32 query heads over 8: 809 us, 0.72 of
+// the bf16 matrix rate (828 where no input is left in L2); a prompt of 16384: 1628 us, 0.70.  An item's
 // start and end (queries, first scores, O) cost 5 steps, which nothing overlaps: 64 requests, most with one row,
-// 344 us at a floor of 129.  First scores come 9 us after the kernel's start (list, pages, queries: round trips).
+// 346 us at a floor of 129.  First scores come 9 us after the kernel's start (list, pages, queries: round trips).
 #include <limits.h>
 #include <math.h>
 
@@ -49,7 +49,8 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 // 32768 tokens 824 us and 827, 64 requests 342 and 342; with weights of 2^15 together in place of f16's most 848 and 378.)
 constexpr float kAbove = 8.f;
 constexpr float kMost = 65504.f;                  // of a page's weights together, in f16: beyond it the row's reference is taken anew
-constexpr float kMostFar = 0x1p64f;               // of a page's exponentials for l alone, where they are not O's weights
+constexpr float kLarge = 0x1p22f;                 // of a row's reference: beyond it its scores are rounded before it is taken off
+constexpr float kGone = -512.f;                   // log2 of a unit of O, in the row sum's, below which O is zero
 constexpr float kFarWeight = 60.f;                // log2 of the largest factor from a page's weights to O's
 
 constexpr int kSoftmaxWarps = 4 * kTiles;
@@ -136,7 +137,7 @@ struct ChunkParams : ChunkList {
     int recip;         // 2^16 / G, up: row * recip >> 16 = row / G for the rows of a tile
 };
 
-// One partial state: O [256][128], then m, l, mo [256].
+// One partial state: O [256][128], then m, l, d [256].
 constexpr int kPartFloats = kTiles * kTileRows * (kD + 3);
 
 // Instruction descriptor with f16 (kind::f16) or e4m3 (kind::f8f6f4) operands and an f32 accumulator: both
@@ -209,6 +210,11 @@ __device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t (&r)[32])
                  : "memory");
 }
 
+__device__ __forceinline__ void tc_st8(uint32_t taddr, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), I8(r, 0) : "memory");
+}
+
 __device__ __forceinline__ void tc_wait_st()
 {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -262,13 +268,6 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
 {
     uint64_t r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c)
-{
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 
@@ -826,13 +825,13 @@ __device__ __forceinline__ void store_bf16(uint16_t *dst, const float (&o)[32])
                        pack_bf16x2(o[8 * k + 4], o[8 * k + 5]), pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
 }
 
-// O in the units of the weights, 2^mo, to O: times 2^(mo - m) / l, in two factors of 2^(half), since
+// O in the units of the weights, 2^(m + d), to O: times 2^d / l, in two factors of 2^(half), since
 // their product may be out of range where the result is not.
 struct Finish {
     float half, rest;
-    __device__ __forceinline__ Finish(float m, float l, float mo)
+    __device__ __forceinline__ Finish(float l, float d)
     {
-        half = l == 0.f || mo == -INFINITY ? 0.f : exp2f(0.5f * (mo - m));
+        half = l == 0.f ? 0.f : exp2f(0.5f * d);
         rest = l == 0.f ? 0.f : half / l;
         if (l != l)
             half = rest = l;
@@ -866,79 +865,109 @@ __device__ __forceinline__ void rescale(uint32_t o_t, float alpha)
     }
 }
 
-// What a thread keeps of its row.  l is in units of 2^m; O in units of 2^mo, and so are the weights.
+// What a thread keeps of its row.  l is in units of 2^m; O in units of 2^(m + d), and so are the weights.  (The sum
+// itself would lose the value scales where scores are large.)
 struct Row {
-    float m, mo, l;
+    float m, d, l;
 };
 
-// Weights 2^(s sc + lf - m) of a page's 64 columns, lf = log2 vs + m - mo, in f16 to tensor memory, and their part of l.
-// The references m and mo, kAbove below the maxima of the item's first page, stay as long as no page's weights add up to more
-// than kMost: no pass over the scores for their maximum.  Where they do (and where nothing was seen so
-// far, and in rows with NaN) they are taken from that page's maxima, and what is in their units is scaled; `behind` waits
-// until the products with the weights before are done and says whether there were any.
+// A page's weights where a row's references have to be taken anew (`anew`, others keep what they have and their part `add` of l):
+// two passes over its scores, which are still in tensor memory, columns up to `lim`.
 template <typename F>
-__device__ __forceinline__ void weigh(Row &r, uint32_t (&s)[2][32], uint32_t p_t, uint32_t o_t, float sc, float lv, F behind)
+__device__ __forceinline__ void weigh_anew(Row &r, bool anew, float add, uint32_t p_t, uint32_t o_t, float sc, float lv, int lim, F behind)
 {
-    bool over = r.m == -INFINITY || (r.mo == -INFINITY && lv > -INFINITY);
+    constexpr int kCols = 16;
+    float top = -INFINITY;
 #pragma unroll 1
-    for (int turn = 0;; ++turn) {
-        if (turn > 0) {
-            float top[2] = {-INFINITY, -INFINITY};
+    for (int k = 0; k < kBlk; k += kCols) {
+        float v[kCols];
+        tc_ld16(p_t + k, v);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                top[i & 1] = max3(top[i & 1], __uint_as_float(s[0][i]), __uint_as_float(s[1][i]));
-            top[0] = fmaxf(top[0], top[1]);
-            const float x = top[0] == -INFINITY ? top[0] : fmaf(top[0], sc, -kAbove), y = top[0] == -INFINITY ? top[0] : x + lv;
-            float alpha = 1.f;
-            if (over && x > r.m) {
-                r.l *= ex2_approx(r.m - x);
-                r.m = x;
-            }
-            if (over && y > r.mo) {
-                alpha = ex2_approx(r.mo - y);
-                r.mo = y;
-            }
-            if (__any_sync(0xffffffffu, alpha != 1.f) && behind())
-                rescale(o_t, alpha);
-        }
-        const float m_ref = r.m == -INFINITY ? 0.f : r.m;
-        // as long as no page counts for O its weights are in any units: they are scaled away with mo
-        const float lf = r.mo == -INFINITY ? 0.f : lv + (m_ref - r.mo), off = lf - m_ref;
-        const uint64_t sc2 = pair(sc, sc), off2 = pair(off, off);
-        uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
-        uint32_t w[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const uint32_t *x = &s[i >> 4][2 * (i & 15)];
-            float2 e = unpair(fma2(pair(__uint_as_float(x[0]), __uint_as_float(x[1])), sc2, off2));
-            e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-            sum[i & 3] = add2(sum[i & 3], pair(e.x, e.y));
-            w[i] = pack_f16x2(e.x, e.y);
-        }
-        const float2 e = unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
-        float add = e.x + e.y;
-        over = over || !(add <= kMost);
-        const bool far = !(fabsf(lf) <= kFarWeight);
-        if (__any_sync(0xffffffffu, far || (over && turn == 0))) {
-            if (turn == 0 && __any_sync(0xffffffffu, over))
-                continue;
-            if (__any_sync(0xffffffffu, far)) {   // l cannot be had from the weights of O
-                float p = 0.f;
-#pragma unroll
-                for (int i = 0; i < 64; ++i)
-                    p += ex2_approx(fmaf(__uint_as_float(s[i >> 5][i & 31]), sc, -m_ref));
-                // scores may have grown where the weights of O, for their small values, have not
-                over = over || (far && !(p <= kMostFar));
-                if (turn == 0 && __any_sync(0xffffffffu, over))
-                    continue;
-                r.l += far ? p : 0.f;
-                add = far ? 0.f : add;
-            }
-        }
-        tc_st32(p_t, w);
-        r.l += far ? 0.f : add * ex2_approx(-lf);
-        break;
+        for (int i = 0; i < kCols; ++i)
+            top = fmaxf(top, k + i <= lim ? v[i] : -INFINITY);
     }
+    float alpha = 1.f;
+    if (anew && top > -INFINITY) {
+        const float t = __fmul_rn(top, sc), x = fabsf(t) > kLarge ? t : fmaf(top, sc, -kAbove);
+        if (x > r.m) {
+            r.l *= ex2_approx(r.m - x);
+            r.d -= x - r.m;
+            r.m = x;
+        }
+        r.d = r.d < kGone ? -INFINITY : r.d;
+        const float y = x - r.m + lv;
+        if (y > r.d && y >= kGone) {
+            alpha = ex2_approx(r.d - y);
+            r.d = y;
+        }
+    }
+    if (__any_sync(0xffffffffu, alpha != 1.f) && behind())
+        rescale(o_t, alpha);
+    const float m_ref = r.m == -INFINITY ? 0.f : r.m;
+    // as long as no page counts for O its weights are in any units: they are scaled away with d
+    const float lf = r.d == -INFINITY ? 0.f : lv - r.d;
+    const bool large = fabsf(m_ref) > kLarge, far = !(fabsf(lf) <= kFarWeight);
+    const float f = large ? 1.f : sc, off = large ? 0.f : -m_ref;
+    float sum = 0.f, alone = 0.f;
+#pragma unroll 1
+    for (int k = 0; k < kBlk; k += kCols) {
+        float v[kCols];
+        uint32_t w[kCols / 2];
+        tc_ld16(p_t + k, v);
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) {
+            v[i] = k + i <= lim ? v[i] : -INFINITY;
+            v[i] = large ? __fadd_rn(__fmul_rn(v[i], sc), -m_ref) : v[i];
+        }
+        if (__any_sync(0xffffffffu, far)) {   // l cannot be had from the weights of O
+#pragma unroll
+            for (int i = 0; i < kCols; ++i)
+                alone += ex2_approx(fmaf(v[i], f, off));
+        }
+#pragma unroll
+        for (int i = 0; i < kCols; i += 2) {
+            const float a = ex2_approx(fmaf(v[i], f, lf + off)), b = ex2_approx(fmaf(v[i + 1], f, lf + off));
+            sum += a + b;
+            w[i / 2] = pack_f16x2(a, b);
+        }
+        tc_st8(p_t + k / 2, w);   // (over scores that have been read)
+    }
+    add = anew ? sum : add;
+    r.l += far ? alone : add * ex2_approx(-lf);
+}
+
+// Weights 2^(s sc - m + lf) of a page's 64 columns, lf = log2 vs - d, in f16 to tensor memory, and their part of l.
+// The references m and m + d, kAbove below the maxima of the item's first page, stay as long as no page's weights add up to more
+// than kMost: no pass over the scores for their maximum.  Where they do (and where nothing was seen so far, in rows with NaN, and
+// where l cannot be had from the weights of O) they are taken from that page's maxima, and what is in their units is scaled;
+// `behind` waits until the products with the weights before are done and says whether there were any.
+// Beyond kLarge, m is too coarse for s sc - m in one rounding to be near zero where it should be: there every page takes the
+// longer way, with scores that are rounded first, as m was.
+template <typename F>
+__device__ __forceinline__ void weigh(Row &r, const uint32_t (&s)[2][32], uint32_t p_t, uint32_t o_t, float sc, float lv, int lim, F behind)
+{
+    bool anew = !(fabsf(r.m) <= kLarge) || (r.d == -INFINITY && lv > -INFINITY);   // (nothing seen so far: m is -infinity)
+    const float lf = r.d == -INFINITY ? 0.f : lv - r.d, off = lf - r.m;
+    const uint64_t sc2 = pair(sc, sc), off2 = pair(off, off);
+    uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
+    uint32_t w[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const uint32_t *x = &s[i >> 4][2 * (i & 15)];
+        float2 e = unpair(fma2(pair(__uint_as_float(x[0]), __uint_as_float(x[1])), sc2, off2));
+        e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+        sum[i & 3] = add2(sum[i & 3], pair(e.x, e.y));
+        w[i] = pack_f16x2(e.x, e.y);
+    }
+    const float2 e = unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+    const float add = e.x + e.y;
+    anew = anew || !(add <= kMost) || !(fabsf(lf) <= kFarWeight);
+    if (__any_sync(0xffffffffu, anew)) {
+        weigh_anew(r, anew, add, p_t, o_t, sc, lv, lim, behind);
+        return;
+    }
+    tc_st32(p_t, w);
+    r.l += add * ex2_approx(-lf);
 }
 
 // One tile's softmax: a thread a row.
@@ -1001,15 +1030,15 @@ __device__ __forceinline__ void softmax_loop(const ChunkParams &p, uint8_t *base
                 const bool masked = j * kKv + h * kBlk + kBlk - 1 > first_pos || ks < 0.f;
                 tc_wait_ld(x[0]);
                 tc_wait_ld(x[1]);
+                const int lim = !masked ? kBlk : ks < 0.f ? -1 : pos - j * kKv - h * kBlk;   // columns up to this one
                 if (masked) {
-                    const int lim = ks < 0.f ? -1 : pos - j * kKv - h * kBlk;   // columns up to this one
 #pragma unroll
                     for (int i = 0; i < 64; ++i)
                         x[i >> 5][i & 31] = i <= lim ? x[i >> 5][i & 31] : 0xff800000u;   // -inf
                 }
                 // the products with the weights of the page before may be left; those before are done, since these scores
                 // were issued after them
-                weigh(row, x, s_t + kBlk * h, o_t, sc, lv, [&]() {
+                weigh(row, x, s_t + kBlk * h, o_t, sc, lv, lim, [&]() {
                     if (j == it.j0 && h == 0)
                         return false;
                     ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (kOFull + 2 * t + (h ^ 1)), (ns - (h ^ 1)) & 1, kWaitNs));
@@ -1038,8 +1067,8 @@ __device__ __forceinline__ void softmax_loop(const ChunkParams &p, uint8_t *base
         const bool whole = it.j0 == 0 && it.j1 == it.all;
         const int *first = reinterpret_cast<const int *>(base + kOffNan) + (items & 1) * kD;
         const bool nan = end > it.j0 && *(reinterpret_cast<const int *>(base + kOffNan) + 2 * kD + (items & 1)) != 0;
-        const float m = row.m, mo = row.mo, l = row.l;
-        const Finish fin(m, l, mo);
+        const float m = row.m, d = row.d, l = row.l;
+        const Finish fin(l, d);
         float *part = p.parts + static_cast<size_t>(2 * blockIdx.x + (it.j0 == 0 ? 1 : 0)) * kPartFloats;
         const int prow = t * kTileRows + tid;
 #pragma unroll 1
@@ -1082,7 +1111,7 @@ __device__ __forceinline__ void softmax_loop(const ChunkParams &p, uint8_t *base
                 float *stat = part + kTiles * kTileRows * kD;
                 stat[prow] = m;
                 stat[kTiles * kTileRows + prow] = l;
-                stat[2 * kTiles * kTileRows + prow] = mo;
+                stat[2 * kTiles * kTileRows + prow] = d;
             }
         }
         if (it.j0 > 0)
@@ -1191,7 +1220,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) paged_chunk_merge_kernel(cons
     if (tok_in >= p.per_tile || tok >= tail.z)
         return;
     constexpr int kAll = kTiles * kTileRows;
-    float m = -INFINITY, mo = -INFINITY, l = 0.f;
+    float m = -INFINITY, d = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     // the CTAs after this one, 32 at a time, to the one that ends the item; the states of four are asked for at once
     constexpr int kAtOnce = 4;
@@ -1202,7 +1231,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) paged_chunk_merge_kernel(cons
         last = ends != 0u;
         uint32_t parts = __ballot_sync(0xffffffffu, kind != 0) & (last ? (ends & (0u - ends)) * 2u - 1u : ~0u);
         while (parts != 0u) {
-            float pm[kAtOnce], pl[kAtOnce], pmo[kAtOnce];
+            float pm[kAtOnce], pl[kAtOnce], pd[kAtOnce];
             float4 x[kAtOnce];
             int n = 0;
 #pragma unroll
@@ -1213,7 +1242,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) paged_chunk_merge_kernel(cons
                     const float *stat = part + kAll * kD;
                     pm[u] = stat[prow];
                     pl[u] = stat[kAll + prow];
-                    pmo[u] = stat[2 * kAll + prow];
+                    pd[u] = stat[2 * kAll + prow];
                     x[u] = *reinterpret_cast<const float4 *>(part + prow * kD + 4 * lane);
                     parts &= parts - 1u;
                     ++n;
@@ -1222,18 +1251,21 @@ __global__ void __launch_bounds__(32 * kMergeRows) paged_chunk_merge_kernel(cons
 #pragma unroll
             for (int u = 0; u < kAtOnce; ++u) {
                 if (u < n) {
-                    const float nm = fmaxf(m, pm[u]), nmo = fmaxf(mo, pmo[u]);
-                    const float a = m == -INFINITY ? 0.f : exp2f(m - nm), b = pm[u] == -INFINITY ? 0.f : exp2f(pm[u] - nm);
-                    l = l * a + pl[u] * b;
+                    const float nm = fmaxf(m, pm[u]);
+                    const float up = m == -INFINITY ? m : m - nm, pup = pm[u] == -INFINITY ? pm[u] : pm[u] - nm;
+                    l = l * exp2f(up) + pl[u] * exp2f(pup);
                     m = nm;
-                    const float ao = mo == -INFINITY ? 0.f : exp2f(mo - nmo), bo = pmo[u] == -INFINITY ? 0.f : exp2f(pmo[u] - nmo);
+                    d += up;
+                    pd[u] += pup;
+                    const float nd = fmaxf(d, pd[u]);
+                    const float ao = d == -INFINITY ? 0.f : exp2f(d - nd), bo = pd[u] == -INFINITY ? 0.f : exp2f(pd[u] - nd);
                     o = make_float4(o.x * ao + x[u].x * bo, o.y * ao + x[u].y * bo, o.z * ao + x[u].z * bo, o.w * ao + x[u].w * bo);
-                    mo = nmo;
+                    d = nd;
                 }
             }
         }
     }
-    const Finish fin(m, l, mo);
+    const Finish fin(l, d);
     const size_t out = static_cast<size_t>(tail.x + tok) * p.H_q + tail.y * p.G + g;
     *reinterpret_cast<uint2 *>(p.O + out * kD + 4 * lane) =
         make_uint2(pack_bf16x2(fin(o.x), fin(o.y)), pack_bf16x2(fin(o.z), fin(o.w)));

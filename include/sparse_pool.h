@@ -699,6 +699,7 @@ SPARSE_API size_t sparse_paged_decode_attn_f8_workspace_size(int B, int H_q, int
  * Scores take q in two e4m3 terms: elements below 2^-9 of a row's largest are off by up to 2^-17 of it.
  * Weights times their pages' value scales are rounded to f16: each is off by 2^-11 of itself, or 2^-33 of the row's
  * largest where that is more.
+ * Scores are fp32, of any size within it: a row whose largest score times log2(e) is past its range is not to be used.
  * A row of Q that is not finite gives NaN.
  * G = H_q / H_kv <= 16, B <= 4096, n_tok <= 2^30, n_pages <= 2^25, n_pages * H_kv < 2^30,
  * max_blocks <= 2^25 - 8.

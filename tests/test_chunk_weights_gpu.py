@@ -64,3 +64,46 @@ def test_a_page_of_small_values_far_above(high, vs, last):
     c.call(ws(c), scale=1.0)
     c.check(1.0)
     assert c.lse.isfinite().all() and (c.lse > torch.tensor(high).to(torch.float8_e4m3fn).item()).all()
+
+
+@pytest.mark.parametrize("start,new", [([170], [20]), ([9000], [3]), ([150] * 90, [2] * 90)])
+@pytest.mark.parametrize("exp", [18, 21, 24, 27, 28, 30, 40, 90, 110])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("vs", [-6, 30])
+def test_scores_of_any_size(start, new, exp, sign, vs):
+    # scores of 2^exp and 9/8 of it, of either sign: the tokens with the largest share the row, all others are nothing.  Their
+    # number is two or three, in one page and in others, whose value scales differ
+    c = Chunk(start, new, 2, 4, seed=33)
+    n = start[0]
+    few = [3, 5, 100]
+    c.Q.zero_()
+    c.Q[..., 0] = 1.0
+    c.pages[:, :, 0] = 0.0
+    c.pages[:, :, 0, :, 0] = 8.0 if sign > 0 else -9.0
+    c.scale[..., 0] = 2.0 ** (exp - 3)
+    c.scale[..., 1] = 2.0 ** vs
+    want = torch.zeros((c.B, 2, D), dtype=torch.float64, device="cuda")
+    for b in range(c.B):
+        c.scale[int(c.table[b, 1]), :, 1] = 2.0 ** (vs - 3)
+        for t in few:
+            p = int(c.table[b, t // BLK])
+            c.pages[p, :, 0, t % BLK, 0] = 9.0 if sign > 0 else -8.0
+            want[b] += c.pages[p, :, 1, t % BLK].double() * c.scale[p, :, 1].double()[:, None] / len(few)
+        end = start[b] + new[b]
+        c.pages[int(c.table[b, end // BLK]), :, :, end % BLK:] = float("nan")   # (any bytes behind the last token)
+    c.call(ws(c), scale=1.0)
+    torch.cuda.synchronize()
+    assert c.status.item() == 0
+    top = (9.0 if sign > 0 else -8.0) * 2.0 ** (exp - 3)
+    row = 0
+    for b in range(c.B):
+        r = slice(row, row + new[b])
+        row += new[b]
+        w = want[b].repeat_interleave(4, 0)
+        # the largest scores have the same bits, so their weights are alike but for 2^x (2^-22) and f16 (2^-11), where a
+        # reference in fp32 leaves 2^0 to 2^-8 of them; the others' are below 2^(-2^14).  O in bf16: 2^-8
+        size = w.abs() + 448 * 2.0 ** vs
+        assert ((c.O[r].double() - w).abs() <= w.abs() * 2.0 ** -8 + size * (2.0 ** -11 + 2.0 ** -18) * (1 + 2.0 ** -8)).all()
+        # lse: base 2 and back, three roundings of the largest score, and ln 3
+        lse = top + torch.tensor(float(len(few)), dtype=torch.float64).log().item()
+        assert ((c.lse[r].double() - lse).abs() <= abs(lse) * 2.0 ** -21 + 2.0 ** -16).all()
